@@ -1,0 +1,483 @@
+// qs_fp8mm.cu -- e4m3 x e4m3 product with fp32 scales per 128 of the inner dimension, for one
+// matrix and for rows sorted by expert (sm_103a).
+//
+//   out[m, n] = sum_b sa[m, b] * sw[e, n/128, b] * (sum over k in block b of a[m, k] * w[e, n, k])
+//
+// The inner sums run on the tensor cores (tcgen05.mma kind::f8f6f4, fp32 accumulators in tensor
+// memory), one block of 128 at a time; since every block has its own scales, an accumulator holds one
+// block only and the sum over blocks is kept in registers.  Three roles work at their own pace:
+//   warp 0     TMA: a stage is 128 columns of the tile's rows of a and of its weight rows
+//   warp 1     MMA: four instructions a stage into the next of the accumulators, overwriting
+//   warps 2-9  read an accumulator (a thread a row, half of the columns each), add it, scaled, to
+//              their registers, and after the last block store the tile
+// A thread owns a row of the tile, so a block's scale is one number a thread (two where a tile spans
+// two weight blocks, one for each half of the warps) and a step costs one multiply-add an element.
+// Tiles are 128 rows by BN weight rows.  A CTA takes tiles blockIdx.x, + gridDim.x, ... and its
+// stages run on from one tile to the next.  With few rows the stage's row part is only as high as the
+// rows there are (the matrix instruction reads on into whatever follows: rows of the result that no
+// thread stores), so that nearly all of shared memory holds weights in flight.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "qs_internal.h"
+#include "qs_rows.cuh"
+#include "qs_tc.cuh"
+
+namespace qs {
+
+namespace {
+
+constexpr int kMaxStages = 32;
+constexpr int kThreads = 320;
+constexpr int kTileRows = 128;
+constexpr int kRowBox = 16;  // rows of the small TMA box of a
+
+struct alignas(64) MmParams {
+    CUtensorMap ta16;   // a, boxes of 16 rows x 128 bytes
+    CUtensorMap ta128;  // a, boxes of 128 rows
+    CUtensorMap tw;     // w [expert][row][k], boxes of BN rows
+    const float* sa;
+    const float* sw;
+    const int32_t* offsets;
+    void* out;
+    uint32_t* status;
+    int64_t sa_stride, out_stride;
+    int M, N, E, KB, NB;  // KB: blocks of K, NB: 128-row blocks of N
+    int out_dtype, out_vec;
+    int a_bytes, stages;  // bytes of a stage's row part
+};
+
+struct MmCtl {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t accfull[4], accempty[4];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __noinline__ void mm_timeout(uint32_t* status, uint32_t code) {
+    if (atomicCAS(status, 0u, (uint32_t)QS_ERR_TIMEOUT) == 0u) {
+        status[1] = code;
+        status[2] = blockIdx.x;
+        __threadfence();
+    }
+}
+
+// Bounded wait of the calling thread; false once the CTA gives up.
+__device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status,
+                                        uint32_t code) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
+        if (*abort) return false;
+        if (global_timer_ns() - t0 > kWaitNs) {
+            *abort = 1;
+            mm_timeout(status, code);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* m, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst)),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// D[tmem] = A[smem] * B[smem]^T (accumulate: added), e4m3, 32 of K
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(id), "r"(accumulate)
+        : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]);
+template <>
+__device__ __forceinline__ void tmem_load<32>(uint32_t addr, uint32_t (&r)[32]) { tc::ld32(addr, r); }
+template <>
+__device__ __forceinline__ void tmem_load<16>(uint32_t addr, uint32_t (&r)[16]) { tc::ld16(addr, r); }
+template <>
+__device__ __forceinline__ void tmem_load<8>(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr)
+                 : "memory");
+}
+
+struct Tile {
+    int e, row0, rows, n0;  // expert, first row of a, rows that are the tile's, first weight row
+};
+
+// Tiles of the call, by number: experts ascending, inside one the weight tiles, inside one the row
+// tiles, so that CTAs side by side share a weight tile.  prefix[e]: row tiles of the experts before e.
+__device__ __forceinline__ Tile tile_at(const MmParams& p, const int* prefix, int nt, int BN, int64_t tile) {
+    Tile t;
+    int lo = 0, first = 0, mt = prefix[p.E];
+    if (p.offsets) {
+        int hi = p.E;  // last e with prefix[e] * nt <= tile that has a tile
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((int64_t)prefix[mid] * nt <= tile) lo = mid;
+            else hi = mid;
+        }
+        first = min(max(p.offsets[lo], 0), p.M);
+        mt = prefix[lo + 1] - prefix[lo];
+    }
+    const int local = (int)(tile - (int64_t)prefix[lo] * nt);
+    const int last = p.offsets ? min(max(p.offsets[lo + 1], 0), p.M) : p.M;
+    const int n = local / mt, m = local - n * mt;
+    t.e = lo;
+    t.row0 = first + m * kTileRows;
+    t.rows = min(kTileRows, last - t.row0);
+    t.n0 = n * BN;
+    return t;
+}
+
+template <int BN>
+struct MmShape {
+    static constexpr int kAcc = BN == 256 ? 2 : 4;                      // accumulators in tensor memory
+    static constexpr int kTmemCols = BN * kAcc < 32 ? 32 : BN * kAcc;  // 64 .. 512
+    static constexpr int kCols = BN / 2;                                // columns of an epilogue thread
+    static constexpr int kLoad = kCols < 32 ? kCols : 32;               // columns of one tensor-memory load
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_constant__ MmParams p) {
+    using S = MmShape<BN>;
+    extern __shared__ uint8_t mm_smem[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~(uintptr_t)1023);
+    __shared__ MmCtl ctl;
+    __shared__ int prefix[1025];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort = &ctl.abort;
+    const int stages = p.stages;
+    // weight parts first: the row part of the last stage is followed by the tail that keeps the matrix
+    // instruction's 128 rows inside shared memory
+    uint8_t* wst = sm;
+    uint8_t* ast = sm + (size_t)stages * BN * 128;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; s++) {
+            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.empty[s], 1);
+        }
+        for (int s = 0; s < S::kAcc; s++) {
+            mbar_init(&ctl.accfull[s], 1);
+            mbar_init(&ctl.accempty[s], 8);
+        }
+        mbar_init(&ctl.drain, 1);
+        ctl.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&ctl.tmem, S::kTmemCols);
+        tc::tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_launch_next();
+    if (warp == 0) {
+        if (p.offsets) {
+            int carry = 0;
+            for (int b = 0; b < p.E; b += 32) {
+                const int e = b + lane;
+                int c = 0;
+                if (e < p.E) {
+                    const int r0 = min(max(p.offsets[e], 0), p.M), r1 = min(max(p.offsets[e + 1], 0), p.M);
+                    c = r1 > r0 ? (r1 - r0 + kTileRows - 1) / kTileRows : 0;
+                }
+                int s = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, s, o);
+                    if (lane >= o) s += v;
+                }
+                if (e < p.E) prefix[e] = carry + s - c;
+                carry += __shfl_sync(0xffffffffu, s, 31);
+            }
+            if (lane == 0) prefix[p.E] = carry;
+        } else if (lane == 0) {
+            prefix[0] = 0;
+            prefix[1] = (p.M + kTileRows - 1) / kTileRows;
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tbase = ctl.tmem;
+    const int nt = (p.N + BN - 1) / BN;
+    const int64_t n_tiles = (int64_t)prefix[p.E] * nt;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- TMA
+        if (lane == 0) {
+            int64_t c = 0;  // stages filled
+            bool ok = true;
+            for (int64_t u = blockIdx.x; u < n_tiles && ok; u += gridDim.x) {
+                const Tile t = tile_at(p, prefix, nt, BN, u);
+                const int boxes = t.rows <= 64 ? (t.rows + kRowBox - 1) / kRowBox : 0;  // 0: one of 128 rows
+                const uint32_t bytes = (boxes ? boxes * kRowBox : kTileRows) * 128 + BN * 128;
+                for (int kb = 0; kb < p.KB; kb++, c++) {
+                    const int s = (int)(c % stages);
+                    if (c >= stages && !mm_wait(&ctl.empty[s], (uint32_t)(c / stages - 1) & 1, abort, p.status, 1)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* as = ast + (size_t)s * p.a_bytes;
+                    mbar_arrive_expect_tx(&ctl.full[s], bytes);
+                    tma_3d(wst + (size_t)s * BN * 128, &p.tw, kb * 128, t.n0, t.e, &ctl.full[s]);
+                    if (boxes) {
+                        for (int b = 0; b < boxes; b++)
+                            tma_2d(as + b * kRowBox * 128, &p.ta16, kb * 128, t.row0 + b * kRowBox, &ctl.full[s]);
+                    } else {
+                        tma_2d(as, &p.ta128, kb * 128, t.row0, &ctl.full[s]);
+                    }
+                }
+            }
+            // copies in flight end before the CTA does
+            if (!ok || *abort)
+                for (int64_t i = max((int64_t)0, c - stages); i < c; i++)
+                    (void)mbar_wait(&ctl.full[i % stages], (uint32_t)(i / stages) & 1, 1000000ull);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- MMA
+        if (lane == 0) {
+            constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kTileRows, BN);
+            int64_t c = 0;
+            bool ok = true;
+            for (int64_t u = blockIdx.x; u < n_tiles && ok; u += gridDim.x) {
+                for (int kb = 0; kb < p.KB; kb++, c++) {
+                    const int s = (int)(c % stages), a = (int)(c % S::kAcc);
+                    if (!mm_wait(&ctl.full[s], (uint32_t)(c / stages) & 1, abort, p.status, 2) ||
+                        (c >= S::kAcc &&
+                         !mm_wait(&ctl.accempty[a], (uint32_t)(c / S::kAcc - 1) & 1, abort, p.status, 3))) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + (size_t)s * p.a_bytes));
+                    const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + (size_t)s * BN * 128));
+#pragma unroll
+                    for (int k = 0; k < 4; k++)  // 32 of K: 32 bytes, 2 units of the descriptors
+                        mma_f8(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
+                    tc::commit(&ctl.empty[s]);
+                    tc::commit(&ctl.accfull[a]);
+                }
+            }
+            tc::commit(&ctl.drain);
+            (void)mbar_wait(&ctl.drain, 0);
+        }
+    } else {
+        // ---------------------------------------------------------- sum over blocks, store
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const int r = quad * 32 + lane;
+        int64_t c = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; u < n_tiles && ok; u += gridDim.x) {
+            const Tile t = tile_at(p, prefix, nt, BN, u);
+            const int col0 = t.n0 + half * S::kCols;
+            const bool on = r < t.rows;
+            const float* sa = p.sa + (int64_t)(t.row0 + (on ? r : 0)) * p.sa_stride;
+            const float* sw = p.sw + ((int64_t)t.e * p.NB + min(col0 / kScaleCols, p.NB - 1)) * p.KB;
+            float acc[S::kCols];
+#pragma unroll
+            for (int i = 0; i < S::kCols; i++) acc[i] = 0.0f;
+            float scale = sa[0] * sw[0];
+            for (int kb = 0; kb < p.KB; kb++, c++) {
+                const int a = (int)(c % S::kAcc);
+                const int kn = min(kb + 1, p.KB - 1);
+                const float na = sa[kn], nw = sw[kn];  // the next block's, while this one is awaited
+                if (!mm_wait(&ctl.accfull[a], (uint32_t)(c / S::kAcc) & 1, abort, p.status, 4)) ok = false;
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const uint32_t src = tc::taddr(tbase, quad * 32, a * BN + half * S::kCols);
+#pragma unroll
+                for (int j = 0; j < S::kCols; j += S::kLoad) {
+                    uint32_t d[S::kLoad];
+                    tmem_load<S::kLoad>(src + j, d);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < S::kLoad; i++) acc[j + i] = fmaf(__uint_as_float(d[i]), scale, acc[j + i]);
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.accempty[a]);
+                scale = na * nw;
+            }
+            if (!ok || !on) continue;
+            const int n = min(S::kCols, p.N - col0);
+            uint8_t* o = static_cast<uint8_t*>(row_at(p.out, p.out_stride, type_size(p.out_dtype), t.row0 + r)) +
+                         (int64_t)col0 * type_size(p.out_dtype);
+            if (p.out_vec) {  // rows 16-byte aligned, N a multiple of 8
+#pragma unroll
+                for (int j = 0; j < S::kCols; j += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int q = 0; q < 8; q++) v[q] = acc[j + q];
+                    store8_row<true>(o, p.out_dtype, j, n, v);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < S::kCols; j++)
+                    if (j < n) {
+                        if (p.out_dtype == QS_BF16) reinterpret_cast<__nv_bfloat16*>(o)[j] = __float2bfloat16_rn(acc[j]);
+                        else reinterpret_cast<float*>(o)[j] = acc[j];
+                    }
+            }
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 1) tc::tmem_dealloc(tbase, S::kTmemCols);
+}
+
+// ================================================================== host side
+
+using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
+
+EncodeFn get_encode() {
+    static std::once_flag once;
+    static EncodeFn fn = nullptr;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(f);
+    });
+    return fn;
+}
+
+bool encode8(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides, uint32_t box_rows) {
+    EncodeFn fn = get_encode();
+    if (!fn) return false;
+    const cuuint32_t box[3] = {128, box_rows, 1}, es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base),
+              reinterpret_cast<const cuuint64_t*>(dims), reinterpret_cast<const cuuint64_t*>(strides), box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct MmFacts {
+    int n_sm = 0;
+    int smem = 0;  // dynamic shared memory a CTA may have beside the static part
+    bool set[5] = {};
+};
+
+cudaError_t mm_facts(MmFacts** out) {
+    static std::mutex mu;
+    static MmFacts facts[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    MmFacts& f = facts[dev];
+    if (f.n_sm == 0) {
+        int optin = 0, n_sm = 0;
+        if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+        f.smem = optin - (int)(sizeof(MmCtl) + 1025 * 4 + 64);
+        const void* fns[5] = {(const void*)fp8_mm_kernel<16>, (const void*)fp8_mm_kernel<32>, (const void*)fp8_mm_kernel<64>,
+                              (const void*)fp8_mm_kernel<128>, (const void*)fp8_mm_kernel<256>};
+        for (const void* fn : fns)
+            if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess) return e;
+        f.n_sm = n_sm;
+    }
+    *out = &f;
+    return cudaSuccess;
+}
+
+template <int BN>
+cudaError_t mm_run(const Fp8MmArgs& g, MmParams& p, const MmFacts& f, int64_t tiles, cudaStream_t st) {
+    const uint64_t dw[3] = {(uint64_t)g.n_inner, (uint64_t)g.n_cols, (uint64_t)g.n_experts};
+    const uint64_t sw[2] = {(uint64_t)g.w_stride, (uint64_t)g.w_expert_stride};
+    if (!encode8(&p.tw, 3, g.w, dw, sw, BN)) return cudaErrorInvalidValue;
+    p.a_bytes = g.n_rows <= 64 ? (g.n_rows + kRowBox - 1) / kRowBox * kRowBox * 128 : kTileRows * 128;
+    const int tail = kTileRows * 128 - p.a_bytes;  // the last stage's matrix instruction reads 128 rows
+    p.stages = std::min(kMaxStages, (f.smem - 1024 - tail) / (p.a_bytes + BN * 128));
+    const size_t smem = 1024 + (size_t)p.stages * (p.a_bytes + BN * 128) + tail;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, f.n_sm));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fp8_mm_kernel<BN>, p);
+}
+
+}  // namespace
+
+size_t fp8_matmul_workspace(int, int, int, int) { return kHeaderBytes; }
+
+cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t st) {
+    if (g.n_rows == 0) return cudaSuccess;
+    MmFacts* f;
+    cudaError_t e = mm_facts(&f);
+    if (e != cudaSuccess) return e;
+    MmParams p = {};
+    const uint64_t da[2] = {(uint64_t)g.n_inner, (uint64_t)g.n_rows}, sa[1] = {(uint64_t)g.a_stride};
+    if (!encode8(&p.ta16, 2, g.a, da, sa, kRowBox) || !encode8(&p.ta128, 2, g.a, da, sa, kTileRows)) return cudaErrorInvalidValue;
+    p.sa = g.a_scale;
+    p.sw = g.w_scale;
+    p.offsets = g.offsets;
+    p.out = g.out;
+    p.status = static_cast<uint32_t*>(workspace);
+    p.sa_stride = g.a_scale_stride;
+    p.out_stride = g.out_stride;
+    p.M = g.n_rows;
+    p.N = g.n_cols;
+    p.E = g.offsets ? g.n_experts : 1;
+    p.KB = scale_blocks(g.n_inner);
+    p.NB = scale_blocks(g.n_cols);
+    p.out_dtype = g.out_dtype;
+    p.out_vec = g.n_cols % 8 == 0 && ((uintptr_t)g.out & 15u) == 0 && (g.out_stride * type_size(g.out_dtype)) % 16 == 0;
+    // row tiles: those of one matrix, or for groups the most there can be if rows spread over the
+    // experts (each group's last tile may be short)
+    const int64_t mt = g.offsets ? (int64_t)g.n_rows / kTileRows + std::min(g.n_rows, g.n_experts)
+                                 : (g.n_rows + kTileRows - 1) / kTileRows;
+    // the width whose waves of tiles take least, a tile taking its columns and a fixed part
+    int best = 256;
+    int64_t best_cost = INT64_MAX;
+    for (int bn = 256; bn >= 16; bn /= 2) {
+        const int64_t tiles = mt * ((g.n_cols + bn - 1) / bn);
+        const int64_t cost = (tiles + f->n_sm - 1) / f->n_sm * (bn + 32);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = bn;
+        }
+    }
+    const int64_t tiles = mt * ((g.n_cols + best - 1) / best);
+    switch (best) {
+        case 256: return mm_run<256>(g, p, *f, tiles, st);
+        case 128: return mm_run<128>(g, p, *f, tiles, st);
+        case 64: return mm_run<64>(g, p, *f, tiles, st);
+        case 32: return mm_run<32>(g, p, *f, tiles, st);
+        default: return mm_run<16>(g, p, *f, tiles, st);
+    }
+}
+
+}  // namespace qs

@@ -117,4 +117,95 @@ cudaError_t launch_prefill(const qs_moe_shape& s, const void* x, const float* Wr
                            const uint16_t* sd, const uint16_t* ssig, int T, float* out, void* ws, const WsLayout& W,
                            cudaStream_t st);
 
+// Row operators (qs_norm.cu).  Strides in elements; a null pointer leaves its part out.
+struct NormArgs {
+    const void* x;
+    const void* residual;
+    const float* weight;
+    void* sum_out;
+    void* y;
+    uint8_t* q;
+    float* q_scale;
+    int64_t x_stride, residual_stride, sum_stride, y_stride, q_stride, q_scale_stride;
+    int x_dtype, residual_dtype, sum_dtype, y_dtype;
+    int n_rows, hidden;
+    float eps;
+};
+struct NormBwdArgs {
+    const void* sum;
+    const float* weight;
+    const void* dy;
+    const void* dsum;
+    void* dx;
+    float* partial;  // [n_parts x part_stride], or null without dweight
+    int64_t sum_stride, dy_stride, dsum_stride, dx_stride;
+    int sum_dtype, dy_dtype, dsum_dtype, dx_dtype;
+    int n_rows, hidden, part_stride, n_parts;
+    float eps;
+};
+struct SiluArgs {
+    const void* gate_up;
+    const int32_t* n_rows_dev;
+    uint8_t* q;
+    float* q_scale;
+    int64_t gate_up_stride, q_stride, q_scale_stride;
+    int dtype, n_rows, ffn;
+};
+constexpr int kNormParts = 1024;     // most partial rows of dweight
+constexpr int kNormMaxHidden = 16384;
+cudaError_t launch_rmsnorm(const NormArgs& p, cudaStream_t st);
+cudaError_t launch_rmsnorm_backward(const NormBwdArgs& p, float* dweight, cudaStream_t st);
+cudaError_t launch_silu_mul_quant(const SiluArgs& p, cudaStream_t st);
+
+// Token rows to experts and back (qs_tokens.cu).
+struct DispatchArgs {
+    const int32_t* ids;
+    int32_t *counts, *offsets, *perm, *pos;
+    const void* x;
+    void* xs;
+    const float* x_scale;
+    float* xs_scale;
+    int32_t* hist;  // workspace: [chunks x n_experts]
+    int64_t x_stride, xs_stride, x_scale_stride, xs_scale_stride;  // bytes of x and xs, floats of the scales
+    int n_tokens, top_k, n_experts;
+    int row_bytes, n_scales;
+};
+struct CombineArgs {
+    const void* y;
+    const int32_t* pos;
+    const float* w;
+    void* out;
+    int64_t y_stride, out_stride;
+    int y_dtype, out_dtype, n_tokens, top_k, hidden;
+};
+struct CombineBwdArgs {
+    const void* dout;
+    const void* y;
+    const int32_t* pos;
+    const float* w;
+    void* dy;
+    float* dw;
+    int64_t dout_stride, y_stride, dy_stride;
+    int dout_dtype, y_dtype, dy_dtype, n_tokens, top_k, hidden;
+};
+size_t dispatch_workspace(int n_tokens, int top_k, int n_experts);
+cudaError_t launch_dispatch(const DispatchArgs& p, cudaStream_t st);
+cudaError_t launch_combine(const CombineArgs& p, cudaStream_t st);
+cudaError_t launch_combine_backward(const CombineBwdArgs& p, cudaStream_t st);
+
+// e4m3 product with block scales (qs_fp8mm.cu).
+struct Fp8MmArgs {
+    const void* a;
+    const float* a_scale;
+    const void* w;
+    const float* w_scale;
+    const int32_t* offsets;
+    void* out;
+    uint32_t* status;
+    int64_t a_stride, a_scale_stride, w_stride, w_expert_stride, out_stride;
+    int n_experts, n_rows, n_cols, n_inner, out_dtype;
+};
+size_t fp8_matmul_workspace(int n_rows, int n_cols, int n_inner, int n_experts);
+cudaError_t launch_fp8_matmul(const Fp8MmArgs& p, void* workspace, cudaStream_t st);
+
 }  // namespace qs

@@ -1,0 +1,309 @@
+// qs_norm.cu -- root-mean-square norm with the residual's addition, its gradient, and the SwiGLU
+// activation, each with e4m3 output rows where asked (sm_103a).
+//
+// Norm.  s = x + residual, rho = 1 / sqrt(mean(s^2) + eps), v = s * rho * weight.  Bound: HBM (x
+// and residual in once, the sum, y and codes out once).  A row is held in the registers of a group
+// of G warps, eight consecutive elements a thread and step, so it is read once; the sum of squares
+// is a fixed-order tree over the group.  Sixteen neighbouring threads hold the 128 columns of a
+// scale, so a block's maximum is four shuffles and nothing is staged in shared memory.
+//
+// Gradient.  With g = weight * dy: dx = rho * g - s * rho^3 * mean(g * s) + dsum.  Both sums over a
+// row (s^2 and g * s) are formed in one pass; a group keeps its columns' share of dweight in
+// registers over all its rows and writes one partial row, and a second launch adds the partial
+// rows in ascending order (no atomics: the same bits every run).
+#include "qs_internal.h"
+#include "qs_rows.cuh"
+
+#include <algorithm>
+
+namespace qs {
+
+namespace {
+
+// Sum over a group of G warps, the same in every thread; red: G floats of the group's own, free
+// again after the next call's first barrier.  bar: the group's named barrier.
+template <int G, int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float* red, int wg, int lane, int bar) {
+#pragma unroll
+    for (int j = 0; j < N; j++) v[j] = warp_sum(v[j]);
+    if (G == 1) return;
+    if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j++) red[j * G + wg] = v[j];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * G) : "memory");
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < G; w++) t += red[j * G + w];
+        v[j] = t;
+    }
+}
+
+constexpr int cta_warps(int G) { return G < 8 ? 8 : G; }
+
+// G warps a row, NV steps of eight elements a thread: rows of up to 256 * G * NV elements.
+template <bool VEC, int G, int NV>
+__global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_kernel(const NormArgs p) {
+    constexpr int kGroups = cta_warps(G) / G;
+    __shared__ float red[kGroups][G];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = warp / G, wg = warp % G;
+    const int64_t t = (int64_t)blockIdx.x * kGroups + group;
+    pdl_wait();
+    pdl_launch_next();
+    if (t >= p.n_rows) return;
+    const void* xr = row_at(p.x, p.x_stride, type_size(p.x_dtype), t);
+    const void* rr = p.residual ? row_at(p.residual, p.residual_stride, type_size(p.residual_dtype), t) : nullptr;
+    float s[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; j++) load8_row<VEC>(xr, p.x_dtype, (j * 32 * G + wg * 32 + lane) * 8, p.hidden, s[j]);
+    if (rr) {
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            float r[8];
+            load8_row<VEC>(rr, p.residual_dtype, (j * 32 * G + wg * 32 + lane) * 8, p.hidden, r);
+#pragma unroll
+            for (int q = 0; q < 8; q++) s[j][q] += r[q];
+        }
+    }
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+        for (int q = 0; q < 8; q++) ss[0] = fmaf(s[j][q], s[j][q], ss[0]);
+    if (p.sum_out) {
+        void* o = row_at(p.sum_out, p.sum_stride, type_size(p.sum_dtype), t);
+#pragma unroll
+        for (int j = 0; j < NV; j++)
+            store8_row<VEC>(o, p.sum_dtype, (j * 32 * G + wg * 32 + lane) * 8, p.hidden, s[j]);
+    }
+    if (!p.y && !p.q) return;
+    group_sum<G, 1>(ss, red[group], wg, lane, 1 + group);
+    const float rho = rsqrtf(ss[0] / (float)p.hidden + p.eps);
+    void* yr = p.y ? row_at(p.y, p.y_stride, type_size(p.y_dtype), t) : nullptr;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+        const int i = (j * 32 * G + wg * 32 + lane) * 8;
+        float w[8];
+        load8_row<VEC>(p.weight, QS_F32, i, p.hidden, w);
+#pragma unroll
+        for (int q = 0; q < 8; q++) w[q] = s[j][q] * rho * w[q];
+        if (yr) store8_row<VEC>(yr, p.y_dtype, i, p.hidden, w);
+        if (p.q) quant8_row<VEC>(w, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, i, p.hidden);
+    }
+}
+
+// Rows r = group, group + (number of groups), ...; `partial` row `group` gets the group's dweight.
+template <bool VEC, int G, int NV>
+__global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_backward_kernel(const NormBwdArgs p) {
+    constexpr int kGroups = cta_warps(G) / G;
+    __shared__ float red[kGroups][2][2 * G];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = warp / G, wg = warp % G;
+    const int64_t first = (int64_t)blockIdx.x * kGroups + group, step = (int64_t)gridDim.x * kGroups;
+    pdl_wait();
+    pdl_launch_next();
+    float dw[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+        for (int q = 0; q < 8; q++) dw[j][q] = 0.0f;
+    int flip = 0;
+    for (int64_t t = first; t < p.n_rows; t += step, flip ^= 1) {
+        const void* sr = row_at(p.sum, p.sum_stride, type_size(p.sum_dtype), t);
+        const void* gr = row_at(p.dy, p.dy_stride, type_size(p.dy_dtype), t);
+        float s[NV][8], g[NV][8];
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            const int i = (j * 32 * G + wg * 32 + lane) * 8;
+            load8_row<VEC>(sr, p.sum_dtype, i, p.hidden, s[j]);
+            load8_row<VEC>(gr, p.dy_dtype, i, p.hidden, g[j]);
+        }
+        float a[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            float w[8];
+            load8_row<VEC>(p.weight, QS_F32, (j * 32 * G + wg * 32 + lane) * 8, p.hidden, w);
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                a[0] = fmaf(s[j][q], s[j][q], a[0]);
+                a[1] = fmaf(w[q] * g[j][q], s[j][q], a[1]);
+            }
+        }
+        group_sum<G, 2>(a, red[group][flip], wg, lane, 1 + group);
+        const float rho = rsqrtf(a[0] / (float)p.hidden + p.eps);
+        const float c = rho * rho * rho * (a[1] / (float)p.hidden);
+        void* o = row_at(p.dx, p.dx_stride, type_size(p.dx_dtype), t);
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            const int i = (j * 32 * G + wg * 32 + lane) * 8;
+            float w[8], d[8];
+            load8_row<VEC>(p.weight, QS_F32, i, p.hidden, w);
+            if (p.dsum) {
+                load8_row<VEC>(row_at(p.dsum, p.dsum_stride, type_size(p.dsum_dtype), t), p.dsum_dtype, i, p.hidden, d);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; q++) d[q] = 0.0f;
+            }
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                dw[j][q] = fmaf(g[j][q], s[j][q] * rho, dw[j][q]);
+                d[q] = fmaf(rho, w[q] * g[j][q], fmaf(-c, s[j][q], d[q]));
+            }
+            store8_row<VEC>(o, p.dx_dtype, i, p.hidden, d);
+        }
+    }
+    if (!p.partial || first >= p.n_parts) return;
+    float* part = p.partial + first * p.part_stride;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+        const int i = (j * 32 * G + wg * 32 + lane) * 8;
+        store8_row<true>(part, QS_F32, i, p.part_stride, dw[j]);  // part_stride: hidden rounded up to 8
+    }
+}
+
+// dweight[h] = sum of partial[r][h], r ascending within each of 32 slices of the rows, then the
+// slices ascending.  32 columns a CTA (lanes: neighbouring columns), 32 slices (warps).
+__global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* __restrict__ partial, int n_parts,
+                                                               int stride, int hidden, float* __restrict__ dweight) {
+    __shared__ float sm[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int h = blockIdx.x * 32 + lane;
+    pdl_wait();
+    pdl_launch_next();
+    float a = 0.0f;
+    if (h < hidden) {
+#pragma unroll 4
+        for (int r = warp; r < n_parts; r += 32) a += partial[(size_t)r * stride + h];
+    }
+    sm[warp][lane] = a;
+    __syncthreads();
+    const float v = warp_sum(sm[lane][warp]);  // column `warp` of this CTA
+    const int c = blockIdx.x * 32 + warp;
+    if (lane == 0 && c < hidden) dweight[c] = v;
+}
+
+// Sixteen lanes a (row, 128 columns): eight elements of gate and of up each.
+template <bool VEC>
+__global__ void __launch_bounds__(256) silu_mul_quant_kernel(const SiluArgs p) {
+    pdl_wait();
+    pdl_launch_next();
+    const int nb = scale_blocks(p.ffn);
+    const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
+    int64_t rows = p.n_rows;
+    if (p.n_rows_dev) rows = min(rows, (int64_t)max(*p.n_rows_dev, 0));
+    const int64_t work = rows * nb;
+    // a warp's two halves take neighbouring blocks; both run the shuffles as long as one has work
+    for (int64_t u0 = ((int64_t)blockIdx.x * 8 + (half >> 1)) * 2; u0 < work; u0 += (int64_t)gridDim.x * 16) {
+        const int64_t u = u0 + (half & 1);
+        const bool on = u < work;
+        const int64_t t = on ? u / nb : 0;
+        const int i = (int)(on ? u - t * nb : 0) * kScaleCols + l * 8;
+        const int n = on ? p.ffn : 0;
+        const uint8_t* row = static_cast<const uint8_t*>(row_at(p.gate_up, p.gate_up_stride, type_size(p.dtype), t));
+        float g[8], v[8];
+        load8_row<VEC>(row, p.dtype, i, n, g);
+        load8_row<VEC>(row + (size_t)p.ffn * type_size(p.dtype), p.dtype, i, n, v);
+#pragma unroll
+        for (int q = 0; q < 8; q++) v[q] *= silu(g[q]);
+        quant8_row<VEC>(v, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, i, n);
+    }
+}
+
+bool al16(const void* p, int64_t stride, int dtype) {
+    return ((uintptr_t)p & 15u) == 0 && (stride * type_size(dtype)) % 16 == 0;
+}
+
+template <class K, class... A>
+cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <bool VEC, int G, int NV>
+cudaError_t norm_run(const NormArgs& p, cudaStream_t st) {
+    constexpr int groups = cta_warps(G) / G;
+    return launch_pdl(rmsnorm_kernel<VEC, G, NV>, (unsigned)((p.n_rows + groups - 1) / groups), 32 * cta_warps(G), st, p);
+}
+
+template <bool VEC>
+cudaError_t norm_pick(const NormArgs& p, cudaStream_t st) {
+    // sixteen elements a thread keep four loads of 16 bytes in flight and full occupancy; more only
+    // for rows past 4096 (groups of more than 8 warps cost a wider barrier)
+    if (p.hidden <= 256) return norm_run<VEC, 1, 1>(p, st);
+    if (p.hidden <= 512) return norm_run<VEC, 1, 2>(p, st);
+    if (p.hidden <= 1024) return norm_run<VEC, 2, 2>(p, st);
+    if (p.hidden <= 2048) return norm_run<VEC, 4, 2>(p, st);
+    if (p.hidden <= 4096) return norm_run<VEC, 8, 2>(p, st);
+    if (p.hidden <= 8192) return norm_run<VEC, 16, 2>(p, st);
+    return norm_run<VEC, 16, 4>(p, st);
+}
+
+template <bool VEC, int G, int NV>
+cudaError_t norm_bwd_run(NormBwdArgs p, float* dweight, cudaStream_t st) {
+    constexpr int groups = cta_warps(G) / G;
+    static_assert(kNormParts % groups == 0, "partial rows fill whole CTAs");
+    const int64_t ctas = (p.n_rows + groups - 1) / groups;
+    // dweight: at most kNormParts groups, each with a partial row; without it one group a row
+    const unsigned grid = (unsigned)(dweight ? std::min<int64_t>(ctas, kNormParts / groups) : ctas);
+    p.n_parts = dweight ? (int)std::min<int64_t>(p.n_rows, (int64_t)grid * groups) : 0;
+    if (grid > 0) {
+        const cudaError_t e = launch_pdl(rmsnorm_backward_kernel<VEC, G, NV>, grid, 32 * cta_warps(G), st, p);
+        if (e != cudaSuccess || !dweight) return e;
+    }
+    if (!dweight) return cudaSuccess;
+    return launch_pdl(rmsnorm_dweight_kernel, (unsigned)((p.hidden + 31) / 32), 1024, st, (const float*)p.partial,
+                      p.n_parts, p.part_stride, p.hidden, dweight);
+}
+
+template <bool VEC>
+cudaError_t norm_bwd_pick(const NormBwdArgs& p, float* dweight, cudaStream_t st) {
+    if (p.hidden <= 256) return norm_bwd_run<VEC, 1, 1>(p, dweight, st);
+    if (p.hidden <= 512) return norm_bwd_run<VEC, 2, 1>(p, dweight, st);
+    if (p.hidden <= 1024) return norm_bwd_run<VEC, 4, 1>(p, dweight, st);
+    if (p.hidden <= 2048) return norm_bwd_run<VEC, 8, 1>(p, dweight, st);
+    if (p.hidden <= 4096) return norm_bwd_run<VEC, 16, 1>(p, dweight, st);
+    if (p.hidden <= 8192) return norm_bwd_run<VEC, 16, 2>(p, dweight, st);
+    return norm_bwd_run<VEC, 16, 4>(p, dweight, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm(const NormArgs& p, cudaStream_t st) {
+    if (p.n_rows == 0) return cudaSuccess;
+    const bool vec = p.hidden % 8 == 0 && al16(p.x, p.x_stride, p.x_dtype) &&
+                     (!p.residual || al16(p.residual, p.residual_stride, p.residual_dtype)) &&
+                     al16(p.weight, 0, QS_F32) && (!p.sum_out || al16(p.sum_out, p.sum_stride, p.sum_dtype)) &&
+                     (!p.y || al16(p.y, p.y_stride, p.y_dtype)) &&
+                     (!p.q || (((uintptr_t)p.q & 7u) == 0 && p.q_stride % 8 == 0));
+    return vec ? norm_pick<true>(p, st) : norm_pick<false>(p, st);
+}
+
+cudaError_t launch_rmsnorm_backward(const NormBwdArgs& p, float* dweight, cudaStream_t st) {
+    const bool vec = p.hidden % 8 == 0 && al16(p.sum, p.sum_stride, p.sum_dtype) &&
+                     al16(p.dy, p.dy_stride, p.dy_dtype) && al16(p.weight, 0, QS_F32) &&
+                     (!p.dsum || al16(p.dsum, p.dsum_stride, p.dsum_dtype)) && al16(p.dx, p.dx_stride, p.dx_dtype);
+    return vec ? norm_bwd_pick<true>(p, dweight, st) : norm_bwd_pick<false>(p, dweight, st);
+}
+
+cudaError_t launch_silu_mul_quant(const SiluArgs& p, cudaStream_t st) {
+    if (p.n_rows == 0) return cudaSuccess;
+    const bool vec = p.ffn % 8 == 0 && al16(p.gate_up, p.gate_up_stride, p.dtype) &&
+                     (p.ffn * type_size(p.dtype)) % 16 == 0 && ((uintptr_t)p.q & 7u) == 0 && p.q_stride % 8 == 0;
+    const int64_t work = (int64_t)p.n_rows * scale_blocks(p.ffn);
+    const unsigned grid = (unsigned)std::min<int64_t>((work + 15) / 16, 65536);
+    return vec ? launch_pdl(silu_mul_quant_kernel<true>, grid, 256, st, p)
+               : launch_pdl(silu_mul_quant_kernel<false>, grid, 256, st, p);
+}
+
+}  // namespace qs

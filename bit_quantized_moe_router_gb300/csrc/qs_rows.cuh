@@ -1,0 +1,118 @@
+// qs_rows.cuh -- device helpers of the row operators: eight consecutive elements of a row read
+// and written as fp32 / bf16 / e4m3, and the e4m3 encoding with one scale per 128 columns.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "qs_common.cuh"
+
+namespace qs {
+
+constexpr int kScaleCols = 128;                       // columns that share a scale
+constexpr float kE4m3Max = 448.0f;                    // largest e4m3 value
+constexpr float kMinAmax = 7.888609052210118e-31f;    // 2^-100: an all-zero block keeps a finite scale
+
+__host__ __device__ constexpr int scale_blocks(int cols) { return (cols + kScaleCols - 1) / kScaleCols; }
+
+// Wait for the kernels before this one in the stream (programmatic dependent launch); nothing is
+// read or written before it.  The launch of the kernel after this one may then begin: it waits in
+// the same way for this grid to end.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Elements i .. i+7 of a row as fp32; those at and past n are 0.  VEC: the row is 16-byte aligned,
+// i a multiple of 8 and n too, so the eight are there or not as one.
+template <bool VEC>
+__device__ __forceinline__ void load8_row(const void* row, int dtype, int i, int n, float (&v)[8]) {
+    if (VEC) {
+        if (i >= n) {
+#pragma unroll
+            for (int q = 0; q < 8; q++) v[q] = 0.0f;
+        } else if (dtype == QS_BF16) {
+            const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + i);
+            v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x);
+            v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+            v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z);
+            v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+        } else {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + i);
+            const float4 a = p[0], b = p[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; q++) v[q] = i + q < n ? load_x(row, dtype, (size_t)(i + q)) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The same eight elements written, rounded once to the row's type.
+template <bool VEC>
+__device__ __forceinline__ void store8_row(void* row, int dtype, int i, int n, const float (&v)[8]) {
+    if (VEC) {
+        if (i >= n) return;
+        if (dtype == QS_BF16) {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + i) =
+                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        } else {
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + i);
+            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; q++)
+            if (i + q < n) {
+                if (dtype == QS_BF16)
+                    static_cast<__nv_bfloat16*>(row)[i + q] = __float2bfloat16_rn(v[q]);
+                else
+                    static_cast<float*>(row)[i + q] = v[q];
+            }
+    }
+}
+
+// Address of row r: stride in elements of `size` bytes, offsets in 64 bits.
+__device__ __forceinline__ const void* row_at(const void* base, int64_t stride, int size, int64_t r) {
+    return static_cast<const uint8_t*>(base) + r * stride * size;
+}
+__device__ __forceinline__ void* row_at(void* base, int64_t stride, int size, int64_t r) {
+    return static_cast<uint8_t*>(base) + r * stride * size;
+}
+__host__ __device__ constexpr int type_size(int dtype) { return dtype == QS_F32 ? 4 : dtype == QS_BF16 ? 2 : 1; }
+
+// Sixteen lanes that hold the 128 columns of one scale block, eight each (columns i .. i+7; those
+// past n hold 0): the block's scale, and the lane's codes.  amax is the exact maximum, so the scale
+// is one fp32 division and each code one fp32 division and one rounding.  fmaxf drops a NaN: its own
+// code is a NaN and the others of its block keep their scale.
+template <bool VEC>
+__device__ __forceinline__ void quant8_row(const float (&v)[8], uint8_t* q_row, float* scale_row, int i, int n) {
+    float a = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(v[q]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    const float scale = fmaxf(a, kMinAmax) / kE4m3Max;
+    if (i >= n) return;
+    if (i % kScaleCols == 0) scale_row[i / kScaleCols] = scale;
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h] / scale, v[4 * h + 1] / scale), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2] / scale, v[4 * h + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+        w[h] = lo | (hi << 16);
+    }
+    if (VEC) {
+        *reinterpret_cast<uint2*>(q_row + i) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; q++)
+            if (i + q < n) q_row[i + q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
+    }
+}
+
+}  // namespace qs

@@ -70,7 +70,9 @@ typedef enum {
     QS_ERR_WORKSPACE = 5     /* workspace missing or smaller than required        */
 } qs_status;
 
-typedef enum { QS_F32 = 0, QS_BF16 = 1 } qs_dtype;
+/* QS_E4M3 (8-bit float: 4 exponent bits, 3 mantissa bits, largest value 448) is taken by the row
+ * operators below, never as a layer's x_dtype. */
+typedef enum { QS_F32 = 0, QS_BF16 = 1, QS_E4M3 = 2 } qs_dtype;
 
 /* Layer shape.  x_dtype is the storage type of x (fp32 or bf16). */
 typedef struct {
@@ -336,6 +338,126 @@ int qs_q2k_quantize(const float *w, int64_t n_rows, int64_t K, void *out, void *
  * word and returns.  Checks that a wait that runs out reports instead of
  * hanging. */
 int qs_test_wait_timeout(void *workspace, size_t workspace_bytes, int limit_us, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators around 8-bit rows.  The same conventions, and these:
+ *  - A matrix of rows is a pointer, a row stride in elements (any, >= its
+ *    columns) and a qs_dtype.  Columns are contiguous.  Every alignment of an
+ *    element is taken; 16-byte aligned rows run the vector forms.
+ *  - An e4m3 matrix [rows x cols] has its codes, one byte each, and fp32
+ *    scales: the value at (r, c) is code * scale[r * scale_stride + c / 128].
+ *    A row has ceil(cols / 128) scales; the last may cover fewer columns.
+ *  - Codes are made as: per row and 128 columns amax = max(max |v|, 2^-100),
+ *    scale = amax / 448, code = v / scale rounded to nearest, ties to even,
+ *    v in fp32.  A NaN becomes the code of a NaN; an infinity makes its block's
+ *    scale infinite, its own code a NaN and the block's finite values 0, so
+ *    every value the block stands for is a NaN.
+ *  - n_rows or n_tokens == 0 is QS_OK; outputs that have no row per row of input
+ *    (dweight, counts, offsets) are still written.
+ *  - Input and output buffers must not overlap unless an entry says so.
+ */
+
+/* Root-mean-square norm with the residual's addition.  Per row t:
+ *   s = x_t + residual_t (x_t if residual is NULL), in fp32
+ *   v = s * weight / sqrt(mean(s^2) + eps), in fp32
+ * sum_out (or NULL) gets s rounded to its type, y (or NULL) v rounded to its
+ * type, q with q_scale (or both NULL) v as codes with scales.  The norm is of s
+ * before its rounding to sum_out.  x, residual, sum_out and y are fp32 or bf16,
+ * each by its own type; weight is device fp32 [hidden].  sum_out may be x or
+ * residual itself (same address, stride and type).  1 <= hidden <= 16384,
+ * eps >= 0 and finite; at least one of y, q and sum_out.  One launch. */
+int qs_rmsnorm_residual(const void *x, int64_t x_stride, int x_dtype, const void *residual, int64_t residual_stride,
+                        int residual_dtype, const float *weight, float eps, int n_rows, int hidden, void *sum_out,
+                        int64_t sum_stride, int sum_dtype, void *y, int64_t y_stride, int y_dtype, void *q,
+                        int64_t q_stride, float *q_scale, int64_t q_scale_stride, void *stream);
+
+/* Gradient of qs_rmsnorm_residual's y and sum_out.  With s the rows of sum
+ * (what sum_out held), rho = 1 / sqrt(mean(s^2) + eps), per row
+ *   dx = rho * weight * dy - s * rho^3 * mean(weight * dy * s) + dsum
+ * (dsum: the gradient that reaches s by the residual stream, or NULL); it is the
+ * gradient of x and of residual alike.  dweight (fp32 [hidden], or NULL) is
+ * overwritten with the sum over rows of dy * s * rho; its rows are added in a
+ * fixed order (run-to-run identical).  workspace: at least
+ * qs_rmsnorm_backward_workspace_bytes(hidden), 256-byte aligned, needs no
+ * initialisation (NULL if dweight is NULL).  dx may be dy or dsum itself.  One
+ * launch, two with dweight. */
+size_t qs_rmsnorm_backward_workspace_bytes(int hidden);
+int qs_rmsnorm_residual_backward(const void *sum, int64_t sum_stride, int sum_dtype, const float *weight, float eps,
+                                 const void *dy, int64_t dy_stride, int dy_dtype, const void *dsum,
+                                 int64_t dsum_stride, int dsum_dtype, int n_rows, int hidden, void *dx,
+                                 int64_t dx_stride, int dx_dtype, float *dweight, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* SwiGLU of a gate/up product with an 8-bit output: per row of gate_up
+ * [n_rows x 2F] (gate columns first; fp32 or bf16) v = silu(gate) * up in fp32,
+ * stored as codes q [n_rows x F] with q_scale.  n_rows_dev (device int32, or
+ * NULL): rows at and beyond *n_rows_dev are left alone (the total of
+ * qs_dispatch_tokens is offsets[n_experts]).  One launch. */
+int qs_silu_mul_quant(const void *gate_up, int64_t gate_up_stride, int gate_up_dtype, int n_rows,
+                      const int32_t *n_rows_dev, int ffn, void *q, int64_t q_stride, float *q_scale,
+                      int64_t q_scale_stride, void *stream);
+
+/* Product of e4m3 rows with e4m3 weights, scales applied per 128 of the inner
+ * dimension, on the fifth-generation tensor cores:
+ *   out[m, n] = sum_b a_scale[m, b] * w_scale[e, n / 128, b]
+ *               * (sum over k in block b of a[m, k] * w[e, n, k])
+ * a      device codes [n_rows x K], 16-byte aligned, a_stride % 16 == 0
+ * a_scale device fp32, row stride a_scale_stride
+ * w      device codes [E x N x K]: row stride w_stride, expert stride
+ *        w_expert_stride (bytes, multiples of 16; 16-byte aligned)
+ * w_scale device fp32 [E x ceil(N / 128) x ceil(K / 128)], contiguous
+ * offsets device int32 [E + 1]: expert e takes rows offsets[e] .. offsets[e+1]
+ *        - 1 of a, ascending (as qs_dispatch_tokens writes it); NULL: one matrix
+ *        (E must be 1).  Rows outside every group are left alone; entries are
+ *        clipped to 0 .. n_rows.
+ * out    fp32 or bf16 [n_rows x N]
+ * Sums inside a block of 128 are formed by the tensor cores in fp32, the sum over
+ * blocks in fp32 in ascending order.  N, K >= 1, E <= 1024.  workspace: at least
+ * qs_fp8_matmul_workspace_bytes(n_rows, N, K, E), 256-byte aligned, initialised
+ * with qs_workspace_init (its header records a wait that ran out).  One launch. */
+size_t qs_fp8_matmul_workspace_bytes(int n_rows, int n_cols, int n_inner, int n_experts);
+int qs_fp8_matmul(const void *a, int64_t a_stride, const float *a_scale, int64_t a_scale_stride, const void *w,
+                  int64_t w_stride, int64_t w_expert_stride, const float *w_scale, const int32_t *offsets,
+                  int n_experts, int n_rows, int n_cols, int n_inner, void *out, int64_t out_stride, int out_dtype,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Token rows sorted by expert.  The plan of topk_ids (device int32
+ * [n_tokens x top_k]): counts [E], offsets [E + 1] and perm [n_tokens * top_k]
+ * as qs_group_tokens writes them, perm filled up with -1 where entries were
+ * dropped (ids outside [0, E)), and pos [n_tokens x top_k], the sorted position
+ * of each entry, -1 if dropped.  Then row p of xs is the row of token
+ * perm[p] / top_k of x, for p < offsets[E]; later rows are left alone.
+ * x [n_tokens x hidden] and xs [n_tokens * top_k x hidden] have the same type,
+ * fp32, bf16 or e4m3; with e4m3 x_scale's rows of ceil(hidden / 128) go along to
+ * xs_scale.  xs NULL makes the plan alone.  workspace: at least
+ * qs_dispatch_workspace_bytes(n_tokens, top_k, E), 256-byte aligned, needs no
+ * initialisation.  n_tokens * top_k <= 2^30, top_k <= 32, E <= 1024.  One
+ * launch for up to 2048 entries, else up to three. */
+size_t qs_dispatch_workspace_bytes(int n_tokens, int top_k, int n_experts);
+int qs_dispatch_tokens(const int32_t *topk_ids, int n_tokens, int top_k, int n_experts, int32_t *counts,
+                       int32_t *offsets, int32_t *perm, int32_t *pos, const void *x, int64_t x_stride, int x_dtype,
+                       const float *x_scale, int64_t x_scale_stride, int hidden, void *xs, int64_t xs_stride,
+                       float *xs_scale, int64_t xs_scale_stride, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* The experts' rows back to their tokens: out[t] = sum over slots j, ascending,
+ * of topk_w[t, j] * y[pos[t, j]], in fp32, rounded once to out's type; entries
+ * with pos outside [0, n_tokens * top_k) add nothing, and a token without any is
+ * a row of zeros.  topk_w NULL means weights of 1: the gradient of
+ * qs_dispatch_tokens's rows.  y [n_tokens * top_k x hidden] and out
+ * [n_tokens x hidden] fp32 or bf16.  One launch. */
+int qs_combine_tokens(const void *y, int64_t y_stride, int y_dtype, const int32_t *pos, const float *topk_w,
+                      int n_tokens, int top_k, int hidden, void *out, int64_t out_stride, int out_dtype,
+                      void *stream);
+
+/* Gradient of qs_combine_tokens: for each entry with a position
+ * dy[pos[t, j]] = topk_w[t, j] * dout[t] and dtopk_w[t, j] = dout[t] . y[pos[t, j]];
+ * dtopk_w of the other entries is 0, rows of dy that no entry has are left
+ * alone.  topk_w NULL means weights of 1; dtopk_w NULL leaves it out (y is then
+ * not read and may be NULL).  One launch. */
+int qs_combine_tokens_backward(const void *dout, int64_t dout_stride, int dout_dtype, const void *y, int64_t y_stride,
+                               int y_dtype, const int32_t *pos, const float *topk_w, int n_tokens, int top_k,
+                               int hidden, void *dy, int64_t dy_stride, int dy_dtype, float *dtopk_w, void *stream);
 
 #if defined(__GNUC__)
 #pragma GCC visibility pop

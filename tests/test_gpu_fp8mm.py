@@ -1,0 +1,155 @@
+"""The e4m3 product with block scales on the GPU against the sum in 64 bits.
+
+An output is a sum of n products with magnitudes |a||w|.  Products of e4m3 codes are exact in fp32; the sums inside a
+block take 128 additions, the sum over blocks ceil(K / 128), the scales two roundings a block; with 2^-23 for an addition
+(the tensor cores may cut where fp32 rounds) the error is at most (128 + blocks + 4) 2^-23 sum(|a||w|), and storing adds half
+a step of the output's type.
+"""
+import pytest
+import torch
+
+from bit_quantized_moe_router_gb300 import qs_moe as qm
+
+pytestmark = pytest.mark.gpu
+
+F8 = torch.float8_e4m3fn
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+def operand(shape, scale_shape, g, pad=0):
+    """Codes (rows 16 bytes apart at least, `pad` bytes more) and scales over several orders of magnitude."""
+    k = shape[-1]
+    buf = torch.randn(*shape[:-1], -(-k // 16) * 16 + pad, generator=g).mul_(8).to(F8).cuda()
+    return buf[..., :k], torch.exp2(torch.randint(-6, 3, scale_shape, generator=g).float() + torch.rand(scale_shape, generator=g)).cuda()
+
+
+def blocks(n):
+    return (n + 127) // 128
+
+
+def values(q, scale, weights):
+    v = q.cpu().float().double()
+    s = scale.cpu().double().repeat_interleave(128, -1)[..., : v.shape[-1]]
+    if weights:
+        s = s.repeat_interleave(128, -2)[..., : v.shape[-2], :]
+    return v * s
+
+
+def check(out, a, w, kind):
+    want, size = a @ w.T, a.abs() @ w.abs().T
+    got = out.cpu().double()
+    assert torch.all((got - want).abs() <= (128 + blocks(a.shape[1]) + 4) * 2.0 ** -23 * size + HALF[kind] * want.abs())
+
+
+@pytest.mark.parametrize("rows,cols,inner,kind", [
+    (1, 1, 1, torch.float32), (1, 16, 16, torch.bfloat16), (1, 4096, 2048, torch.bfloat16), (2, 100, 129, torch.float32),
+    (15, 256, 128, torch.bfloat16), (16, 17, 384, torch.float32), (17, 1000, 1000, torch.bfloat16), (64, 2049, 250, torch.float32),
+    (65, 128, 2048, torch.float32), (127, 300, 72, torch.bfloat16), (128, 256, 4096, torch.float32), (129, 257, 640, torch.bfloat16),
+    (333, 1000, 1200, torch.float32), (1024, 2048, 512, torch.bfloat16), (2500, 4104, 384, torch.bfloat16), (5000, 130, 90, torch.float32)])
+def test_matmul(rows, cols, inner, kind):
+    g = torch.Generator().manual_seed(rows + cols + inner)
+    a, sa = operand((rows, inner), (rows, blocks(inner)), g)
+    w, sw = operand((cols, inner), (blocks(cols), blocks(inner)), g)
+    out = torch.full((rows, cols), float("nan"), dtype=kind, device="cuda")
+    ws = qm.alloc_fp8_matmul_workspace(rows, cols, inner)
+    qm.qs_fp8_matmul(a, sa, w, sw, out, ws)
+    assert qm.qs_read_device_status(ws) == qm.QS_OK
+    check(out, values(a, sa, False), values(w, sw, True), kind)
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_matmul_strides(rows):
+    g = torch.Generator().manual_seed(5)
+    a, sa = operand((rows, 300), (rows, 8), g, pad=64)
+    sa = sa[:, :3]
+    w, sw = operand((70, 300), (1, 3), g, pad=16)
+    wide = torch.full((rows, 99), 7.0, device="cuda")
+    out = wide[:, 1:71]  # rows that start off every boundary
+    ws = qm.alloc_fp8_matmul_workspace(rows, 70, 300)
+    qm.qs_fp8_matmul(a, sa, w, sw, out, ws)
+    check(out, values(a, sa, False), values(w, sw, True), torch.float32)
+    assert torch.all(wide[:, 0] == 7) and torch.all(wide[:, 71:] == 7)
+
+
+COUNTS = {
+    "one row each": [1] * 12, "empty and full": [0, 0, 5, 0, 128, 1, 0, 129, 64, 65, 0, 300, 0], "all in one": [0, 0, 700, 0],
+    "none": [0, 0, 0], "many": [(7 * e) % 23 for e in range(256)], "last alone": [0] * 31 + [17], "sixty-four": [64] * 9, "one expert": [40]}
+
+
+@pytest.mark.parametrize("name", list(COUNTS))
+@pytest.mark.parametrize("cols,inner,kind", [(256, 256, torch.bfloat16), (100, 200, torch.float32), (1024, 512, torch.bfloat16)])
+def test_grouped(name, cols, inner, kind):
+    counts = COUNTS[name]
+    experts, total = len(counts), sum(counts)
+    rows = total + 9  # rows after the last group are left alone
+    g = torch.Generator().manual_seed(total + cols)
+    a, sa = operand((rows, inner), (rows, blocks(inner)), g)
+    w, sw = operand((experts, cols, inner), (experts, blocks(cols), blocks(inner)), g)
+    off = torch.tensor([0] + counts, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+    out = torch.full((rows, cols), 5.0, dtype=kind, device="cuda")
+    ws = qm.alloc_fp8_matmul_workspace(rows, cols, inner, experts)
+    qm.qs_fp8_matmul(a, sa, w, sw, out, ws, off)
+    assert qm.qs_read_device_status(ws) == qm.QS_OK
+    av, wv = values(a, sa, False), values(w, sw, True)
+    at = 0
+    for e, c in enumerate(counts):
+        if c:
+            check(out[at:at + c], av[at:at + c], wv[e], kind)
+        at += c
+    assert torch.all(out[total:] == 5.0)
+
+
+def test_grouped_offsets_are_clipped():
+    g = torch.Generator().manual_seed(3)
+    a, sa = operand((20, 128), (20, 1), g)
+    w, sw = operand((3, 64, 128), (3, 1, 1), g)
+    ws = qm.alloc_fp8_matmul_workspace(20, 64, 128, 3)
+    av, wv = values(a, sa, False), values(w, sw, True)
+    for off in ([-5, 10, 15, 1000], [4, 4, 2, 2 ** 31 - 1], [30, 40, 50, 60]):
+        out = torch.full((20, 64), 5.0, device="cuda")
+        qm.qs_fp8_matmul(a, sa, w, sw, out, ws, torch.tensor(off, dtype=torch.int32, device="cuda"))
+        cut = [min(max(o, 0), 20) for o in off]
+        untouched = torch.ones(20, dtype=torch.bool)
+        for e in range(3):
+            if cut[e + 1] > cut[e]:
+                check(out[cut[e]:cut[e + 1]], av[cut[e]:cut[e + 1]], wv[e], torch.float32)
+                untouched[cut[e]:cut[e + 1]] = False
+        assert torch.all(out.cpu()[untouched] == 5.0)
+    assert qm.qs_read_device_status(ws) == qm.QS_OK
+
+
+def test_nan_and_infinite_scales_stay_in_their_rows():
+    g = torch.Generator().manual_seed(9)
+    a, sa = operand((40, 256), (40, 2), g)
+    w, sw = operand((96, 256), (1, 2), g)
+    ref = torch.empty(40, 96, device="cuda")
+    ws = qm.alloc_fp8_matmul_workspace(40, 96, 256)
+    qm.qs_fp8_matmul(a, sa, w, sw, ref, ws)
+    a.view(torch.uint8)[3, 17] = 0x7F  # NaN code
+    sa[5, 1] = float("inf")
+    w.view(torch.uint8)[11, 200] = 0xFF
+    out = torch.empty_like(ref)
+    qm.qs_fp8_matmul(a, sa, w, sw, out, ws)
+    assert torch.all(torch.isnan(out[3])) and torch.all(torch.isnan(out[:, 11])) and not torch.any(torch.isfinite(out[5]))
+    rows = [r for r in range(40) if r not in (3, 5)]
+    cols = [c for c in range(96) if c != 11]
+    assert torch.equal(out[rows][:, cols], ref[rows][:, cols])
+
+
+def test_same_bits_alone_and_in_a_batch_and_in_a_graph():
+    """A row's result does not depend on the rows beside it, nor on the run."""
+    g = torch.Generator().manual_seed(11)
+    a, sa = operand((150, 1024), (150, 8), g)
+    w, sw = operand((512, 1024), (4, 8), g)
+    ws = qm.alloc_fp8_matmul_workspace(150, 512, 1024)
+    full, one = torch.empty(150, 512, device="cuda"), torch.empty(1, 512, device="cuda")
+    qm.qs_fp8_matmul(a, sa, w, sw, full, ws)
+    for r in (0, 77, 149):
+        qm.qs_fp8_matmul(a[r:r + 1], sa[r:r + 1], w, sw, one, ws)
+        assert torch.equal(one[0], full[r])
+    graph, again = torch.cuda.CUDAGraph(), torch.empty_like(full)
+    with torch.cuda.graph(graph):
+        qm.qs_fp8_matmul(a, sa, w, sw, again, ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, full)
