@@ -8,7 +8,7 @@
 // block only and the sum over blocks is kept in registers.  Three roles work at their own pace:
 //   warp 0     TMA: a stage is 128 columns of the tile's rows of a and of its weight rows
 //   warp 1     MMA: four instructions a stage into the next of the accumulators, overwriting
-//   warps 2-9  read an accumulator (a thread a row, half of the columns each), add it, scaled, to
+//   warps 4-11 read an accumulator (a thread a row, half of the columns each), add it, scaled, to
 //              their registers, and after the last block store the tile
 // A thread owns a row of the tile, so a block's scale is one number a thread (two where a tile spans
 // two weight blocks, one for each half of the warps) and a step costs one multiply-add an element.
@@ -31,11 +31,15 @@ namespace qs {
 namespace {
 
 constexpr int kMaxStages = 32;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+constexpr int kFirstSum = 4;  // first of the eight warps that sum (warps 2 and 3 fill their warpgroup)
+// Registers a thread of the widest tile: the launch's 168 x 384 are dealt out as 56 for warps 0-3 and
+// 224 for the others, (56 + 2 x 224) x 128 = 168 x 384.
+constexpr int kLaunchRegs = 168, kFewRegs = 56, kSumRegs = 224;
 constexpr int kTileRows = 128;
 constexpr int kRowBox = 16;  // rows of the small TMA box of a
 
-struct alignas(64) MmParams {
+struct MmParams {
     CUtensorMap ta16;   // a, boxes of 16 rows x 128 bytes
     CUtensorMap ta128;  // a, boxes of 128 rows
     CUtensorMap tw;     // w [expert][row][k], boxes of BN rows
@@ -154,8 +158,45 @@ struct MmShape {
     static constexpr int kAcc = BN == 256 ? 2 : 4;                      // accumulators in tensor memory
     static constexpr int kTmemCols = BN * kAcc < 32 ? 32 : BN * kAcc;  // 64 .. 512
     static constexpr int kCols = BN / 2;                                // columns of an epilogue thread
-    static constexpr int kLoad = kCols < 32 ? kCols : 32;               // columns of one tensor-memory load
+    static constexpr int kLoad = BN == 256 ? 16 : kCols < 32 ? kCols : 32;  // columns of one tensor-memory load (32 spill there)
 };
+
+// a + b * s in both halves
+__device__ __forceinline__ float2 fma2(uint32_t b0, uint32_t b1, float s, float2 a) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %6};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(b0), "r"(b1), "f"(s), "f"(a.x), "f"(a.y));
+    return d;
+}
+
+// acc += scale * the thread's columns of an accumulator.  The next 32 columns are read while these
+// are added; the accumulator is free once its last columns are in registers.
+template <int BN>
+__device__ __forceinline__ void add_block(float2 (&acc)[BN / 4], uint32_t src, float scale, uint64_t* empty, int lane) {
+    using S = MmShape<BN>;
+    constexpr int kSteps = S::kCols / S::kLoad;
+    uint32_t d[2][S::kLoad];
+    tc::fence_after();
+    tmem_load<S::kLoad>(src, d[0]);
+#pragma unroll
+    for (int j = 0; j < kSteps; j++) {
+        tc::wait_ld();
+        if (j + 1 < kSteps) {
+            tmem_load<S::kLoad>(src + (j + 1) * S::kLoad, d[(j + 1) & 1]);
+        } else {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty);
+        }
+#pragma unroll
+        for (int i = 0; i < S::kLoad / 2; i++) {
+            float2& v = acc[j * (S::kLoad / 2) + i];
+            v = fma2(d[j & 1][2 * i], d[j & 1][2 * i + 1], scale, v);
+        }
+    }
+}
 
 template <int BN>
 __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_constant__ MmParams p) {
@@ -223,7 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
     const int nt = (p.N + BN - 1) / BN;
     const int64_t n_tiles = (int64_t)prefix[p.E] * nt;
 
-    if (warp == 0) {
+    if (warp < kFirstSum) {
+      if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+      if (warp == 0) {
         // ---------------------------------------------------------- TMA
         if (lane == 0) {
             int64_t c = 0;  // stages filled
@@ -254,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                 for (int64_t i = max((int64_t)0, c - stages); i < c; i++)
                     (void)mbar_wait(&ctl.full[i % stages], (uint32_t)(i / stages) & 1, 1000000ull);
         }
-    } else if (warp == 1) {
+      } else if (warp == 1) {
         // ---------------------------------------------------------- MMA
         if (lane == 0) {
             constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kTileRows, BN);
@@ -282,9 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
             tc::commit(&ctl.drain);
             (void)mbar_wait(&ctl.drain, 0);
         }
+      }
     } else {
         // ---------------------------------------------------------- sum over blocks, store
-        const int quad = warp & 3, half = (warp - 2) >> 2;
+        if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        const int quad = warp & 3, half = (warp - kFirstSum) >> 2;
         const int r = quad * 32 + lane;
         int64_t c = 0;
         bool ok = true;
@@ -294,33 +339,36 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
             const bool on = r < t.rows;
             const float* sa = p.sa + (int64_t)(t.row0 + (on ? r : 0)) * p.sa_stride;
             const float* sw = p.sw + ((int64_t)t.e * p.NB + min(col0 / kScaleCols, p.NB - 1)) * p.KB;
-            float acc[S::kCols];
+            float2 acc[S::kCols / 2];
 #pragma unroll
-            for (int i = 0; i < S::kCols; i++) acc[i] = 0.0f;
-            float scale = sa[0] * sw[0];
-            for (int kb = 0; kb < p.KB; kb++, c++) {
-                const int a = (int)(c % S::kAcc);
-                const int kn = min(kb + 1, p.KB - 1);
-                const float na = sa[kn], nw = sw[kn];  // the next block's, while this one is awaited
-                if (!mm_wait(&ctl.accfull[a], (uint32_t)(c / S::kAcc) & 1, abort, p.status, 4)) ok = false;
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
+            for (int i = 0; i < S::kCols / 2; i++) acc[i] = make_float2(0.0f, 0.0f);
+            // scales of four blocks at a time, the next four read while these are used
+            float scale[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) scale[i] = sa[min(i, p.KB - 1)] * sw[min(i, p.KB - 1)];
+            for (int kb0 = 0; kb0 < p.KB && ok; kb0 += 4) {
+                float na[4], nw[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int kn = min(kb0 + 4 + i, p.KB - 1);
+                    na[i] = sa[kn];
+                    nw[i] = sw[kn];
                 }
-                tc::fence_after();
-                const uint32_t src = tc::taddr(tbase, quad * 32, a * BN + half * S::kCols);
 #pragma unroll
-                for (int j = 0; j < S::kCols; j += S::kLoad) {
-                    uint32_t d[S::kLoad];
-                    tmem_load<S::kLoad>(src + j, d);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int i = 0; i < S::kLoad; i++) acc[j + i] = fmaf(__uint_as_float(d[i]), scale, acc[j + i]);
+                for (int i = 0; i < 4; i++) {
+                    if (kb0 + i < p.KB && ok) {
+                        const int a = (int)(c % S::kAcc);
+                        ok = mm_wait(&ctl.accfull[a], (uint32_t)(c / S::kAcc) & 1, abort, p.status, 4);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (ok) {
+                            add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * BN + half * S::kCols), scale[i],
+                                          &ctl.accempty[a], lane);
+                            c++;
+                        }
+                    }
                 }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.accempty[a]);
-                scale = na * nw;
+#pragma unroll
+                for (int i = 0; i < 4; i++) scale[i] = na[i] * nw[i];
             }
             if (!ok || !on) continue;
             const int n = min(S::kCols, p.N - col0);
@@ -331,15 +379,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                 for (int j = 0; j < S::kCols; j += 8) {
                     float v[8];
 #pragma unroll
-                    for (int q = 0; q < 8; q++) v[q] = acc[j + q];
+                    for (int q = 0; q < 8; q += 2) {
+                        v[q] = acc[(j + q) / 2].x;
+                        v[q + 1] = acc[(j + q) / 2].y;
+                    }
                     store8_row<true>(o, p.out_dtype, j, n, v);
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < S::kCols; j++)
                     if (j < n) {
-                        if (p.out_dtype == QS_BF16) reinterpret_cast<__nv_bfloat16*>(o)[j] = __float2bfloat16_rn(acc[j]);
-                        else reinterpret_cast<float*>(o)[j] = acc[j];
+                        const float v = j % 2 ? acc[j / 2].y : acc[j / 2].x;
+                        if (p.out_dtype == QS_BF16) reinterpret_cast<__nv_bfloat16*>(o)[j] = __float2bfloat16_rn(v);
+                        else reinterpret_cast<float*>(o)[j] = v;
                     }
             }
         }
@@ -401,6 +453,10 @@ cudaError_t mm_facts(MmFacts** out) {
                               (const void*)fp8_mm_kernel<128>, (const void*)fp8_mm_kernel<256>};
         for (const void* fn : fns)
             if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess) return e;
+        // the register split would wait forever on a launch with fewer
+        cudaFuncAttributes wide;
+        if ((e = cudaFuncGetAttributes(&wide, fp8_mm_kernel<256>)) != cudaSuccess) return e;
+        if (wide.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
         f.n_sm = n_sm;
     }
     *out = &f;
