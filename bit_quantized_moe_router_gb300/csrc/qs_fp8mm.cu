@@ -265,73 +265,84 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
     const int64_t n_tiles = (int64_t)prefix[p.E] * nt;
 
     if (warp < kFirstSum) {
-      if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-      if (warp == 0) {
-        // ---------------------------------------------------------- TMA
-        if (lane == 0) {
-            int64_t c = 0;  // stages filled
+        if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------------ TMA
+            int s = 0;            // stage to fill
+            uint32_t phase = 1;   // parity of the phase of `empty` that frees it: the first round passes at once
+            int64_t filled = 0;
             bool ok = true;
             for (int64_t u = blockIdx.x; u < n_tiles && ok; u += gridDim.x) {
                 const Tile t = tile_at(p, prefix, nt, BN, u);
                 const int boxes = t.rows <= 64 ? (t.rows + kRowBox - 1) / kRowBox : 0;  // 0: one of 128 rows
                 const uint32_t bytes = (boxes ? boxes * kRowBox : kTileRows) * 128 + BN * 128;
-                for (int kb = 0; kb < p.KB; kb++, c++) {
-                    const int s = (int)(c % stages);
-                    if (c >= stages && !mm_wait(&ctl.empty[s], (uint32_t)(c / stages - 1) & 1, abort, p.status, 1)) {
+                for (int kb = 0; kb < p.KB; kb++) {
+                    if (!mm_wait(&ctl.empty[s], phase, abort, p.status, 1)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* as = ast + (size_t)s * p.a_bytes;
+                    uint8_t* as = ast + s * p.a_bytes;
                     mbar_arrive_expect_tx(&ctl.full[s], bytes);
-                    tma_3d(wst + (size_t)s * BN * 128, &p.tw, kb * 128, t.n0, t.e, &ctl.full[s]);
+                    tma_3d(wst + s * BN * 128, &p.tw, kb * 128, t.n0, t.e, &ctl.full[s]);
                     if (boxes) {
                         for (int b = 0; b < boxes; b++)
                             tma_2d(as + b * kRowBox * 128, &p.ta16, kb * 128, t.row0 + b * kRowBox, &ctl.full[s]);
                     } else {
                         tma_2d(as, &p.ta128, kb * 128, t.row0, &ctl.full[s]);
                     }
+                    filled++;
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             // copies in flight end before the CTA does
             if (!ok || *abort)
-                for (int64_t i = max((int64_t)0, c - stages); i < c; i++)
+                for (int64_t i = max((int64_t)0, filled - stages); i < filled; i++)
                     (void)mbar_wait(&ctl.full[i % stages], (uint32_t)(i / stages) & 1, 1000000ull);
-        }
-      } else if (warp == 1) {
-        // ---------------------------------------------------------- MMA
-        if (lane == 0) {
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------------------------------ MMA
             constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kTileRows, BN);
-            int64_t c = 0;
+            int s = 0, a = 0;
+            uint32_t phase = 0, aphase = 1;
             bool ok = true;
             for (int64_t u = blockIdx.x; u < n_tiles && ok; u += gridDim.x) {
-                for (int kb = 0; kb < p.KB; kb++, c++) {
-                    const int s = (int)(c % stages), a = (int)(c % S::kAcc);
-                    if (!mm_wait(&ctl.full[s], (uint32_t)(c / stages) & 1, abort, p.status, 2) ||
-                        (c >= S::kAcc &&
-                         !mm_wait(&ctl.accempty[a], (uint32_t)(c / S::kAcc - 1) & 1, abort, p.status, 3))) {
+                for (int kb = 0; kb < p.KB; kb++) {
+                    if (!mm_wait(&ctl.accempty[a], aphase, abort, p.status, 3) ||
+                        !mm_wait(&ctl.full[s], phase, abort, p.status, 2)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after();
-                    const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + (size_t)s * p.a_bytes));
-                    const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + (size_t)s * BN * 128));
+                    const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * p.a_bytes));
+                    const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * BN * 128));
 #pragma unroll
                     for (int k = 0; k < 4; k++)  // 32 of K: 32 bytes, 2 units of the descriptors
                         mma_f8(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
                     tc::commit(&ctl.empty[s]);
                     tc::commit(&ctl.accfull[a]);
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                    if (++a == S::kAcc) {
+                        a = 0;
+                        aphase ^= 1;
+                    }
                 }
             }
             tc::commit(&ctl.drain);
             (void)mbar_wait(&ctl.drain, 0);
         }
-      }
+        __syncwarp();
     } else {
         // ---------------------------------------------------------- sum over blocks, store
         if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         const int quad = warp & 3, half = (warp - kFirstSum) >> 2;
         const int r = quad * 32 + lane;
-        int64_t c = 0;
+        int a = 0;
+        uint32_t aphase = 0;
         bool ok = true;
         for (int64_t u = blockIdx.x; u < n_tiles && ok; u += gridDim.x) {
             const Tile t = tile_at(p, prefix, nt, BN, u);
@@ -357,13 +368,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     if (kb0 + i < p.KB && ok) {
-                        const int a = (int)(c % S::kAcc);
-                        ok = mm_wait(&ctl.accfull[a], (uint32_t)(c / S::kAcc) & 1, abort, p.status, 4);
+                        ok = mm_wait(&ctl.accfull[a], aphase, abort, p.status, 4);
                         ok = __all_sync(0xffffffffu, ok);
                         if (ok) {
                             add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * BN + half * S::kCols), scale[i],
                                           &ctl.accempty[a], lane);
-                            c++;
+                            if (++a == S::kAcc) {
+                                a = 0;
+                                aphase ^= 1;
+                            }
                         }
                     }
                 }
