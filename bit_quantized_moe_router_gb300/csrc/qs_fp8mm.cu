@@ -101,6 +101,58 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* m, int x, i
         : "memory");
 }
 
+// ---- two CTAs that share a tile (a cluster of 2; the even one leads)
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// shared::cluster address of the leader's copy of a shared variable
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
+// TMA into this CTA's shared memory, counted on the leader's barrier
+__device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(m), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_3d_pair(void* dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst)),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// D[tmem of both] = A[smem of both] * B[smem of both]^T: 256 rows, 128 and half of B's rows in each CTA
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(id), "r"(accumulate)
+        : "memory");
+}
+// arrive on the barrier of both CTAs when the MMAs issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// Arrive on a barrier of either CTA.  What it orders is tensor memory, by the tcgen05 fences: no release
+// at cluster scope, which costs a step of the sum more than the step.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // D[tmem] = A[smem] * B[smem]^T (accumulate: added), e4m3, 32 of K
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
     asm volatile(
@@ -130,6 +182,7 @@ struct Tile {
 
 // Tiles of the call, by number: experts ascending, inside one the weight tiles, inside one the row
 // tiles, so that CTAs side by side share a weight tile.  prefix[e]: row tiles of the experts before e.
+template <int ROWS>
 __device__ __forceinline__ Tile tile_at(const MmParams& p, const int* prefix, int nt, int BN, int64_t tile) {
     Tile t;
     int lo = 0, first = 0, mt = prefix[p.E];
@@ -147,8 +200,8 @@ __device__ __forceinline__ Tile tile_at(const MmParams& p, const int* prefix, in
     const int last = p.offsets ? min(max(p.offsets[lo + 1], 0), p.M) : p.M;
     const int n = local / mt, m = local - n * mt;
     t.e = lo;
-    t.row0 = first + m * kTileRows;
-    t.rows = min(kTileRows, last - t.row0);
+    t.row0 = first + m * ROWS;
+    t.rows = min(ROWS, last - t.row0);
     t.n0 = n * BN;
     return t;
 }
@@ -174,7 +227,7 @@ __device__ __forceinline__ float2 fma2(uint32_t b0, uint32_t b1, float s, float2
 // acc += scale * the thread's columns of an accumulator.  The next 32 columns are read while these
 // are added; the accumulator is free once its last columns are in registers.
 template <int BN>
-__device__ __forceinline__ void add_block(float2 (&acc)[BN / 4], uint32_t src, float scale, uint64_t* empty, int lane) {
+__device__ __forceinline__ void add_block(float2 (&acc)[BN / 4], uint32_t src, float scale, uint32_t empty, int lane) {
     using S = MmShape<BN>;
     constexpr int kSteps = S::kCols / S::kLoad;
     uint32_t d[2][S::kLoad];
@@ -188,7 +241,7 @@ __device__ __forceinline__ void add_block(float2 (&acc)[BN / 4], uint32_t src, f
         } else {
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty);
+            if (lane == 0) arrive_cluster(empty);
         }
 #pragma unroll
         for (int i = 0; i < S::kLoad / 2; i++) {
@@ -198,20 +251,26 @@ __device__ __forceinline__ void add_block(float2 (&acc)[BN / 4], uint32_t src, f
     }
 }
 
-template <int BN>
+// PAIR: two CTAs take a tile of 256 rows together, each 128 rows and half of the weight rows; the
+// leader issues the matrix instructions for both.
+template <int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_constant__ MmParams p) {
     using S = MmShape<BN>;
+    constexpr int kCtas = PAIR ? 2 : 1, kRows = kTileRows * kCtas;
+    constexpr int kWBytes = BN / kCtas * 128;  // a CTA's weight part of a stage
     extern __shared__ uint8_t mm_smem[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~(uintptr_t)1023);
     __shared__ MmCtl ctl;
     __shared__ int prefix[1025];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? (int)cluster_rank() : 0;
+    const unsigned first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
     volatile int* abort = &ctl.abort;
     const int stages = p.stages;
     // weight parts first: the row part of the last stage is followed by the tail that keeps the matrix
     // instruction's 128 rows inside shared memory
     uint8_t* wst = sm;
-    uint8_t* ast = sm + (size_t)stages * BN * 128;
+    uint8_t* ast = sm + (size_t)stages * kWBytes;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; s++) {
@@ -220,15 +279,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
         }
         for (int s = 0; s < S::kAcc; s++) {
             mbar_init(&ctl.accfull[s], 1);
-            mbar_init(&ctl.accempty[s], 8);
+            mbar_init(&ctl.accempty[s], 8 * kCtas);
         }
         mbar_init(&ctl.drain, 1);
         ctl.abort = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tc::tmem_alloc(&ctl.tmem, S::kTmemCols);
-        tc::tmem_relinquish();
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
+                         "r"(S::kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            tc::tmem_alloc(&ctl.tmem, S::kTmemCols);
+            tc::tmem_relinquish();
+        }
     }
     pdl_wait();
     pdl_launch_next();
@@ -240,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                 int c = 0;
                 if (e < p.E) {
                     const int r0 = min(max(p.offsets[e], 0), p.M), r1 = min(max(p.offsets[e + 1], 0), p.M);
-                    c = r1 > r0 ? (r1 - r0 + kTileRows - 1) / kTileRows : 0;
+                    c = r1 > r0 ? (r1 - r0 + kRows - 1) / kRows : 0;
                 }
                 int s = c;
 #pragma unroll
@@ -254,11 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
             if (lane == 0) prefix[p.E] = carry;
         } else if (lane == 0) {
             prefix[0] = 0;
-            prefix[1] = (p.M + kTileRows - 1) / kTileRows;
+            prefix[1] = (p.M + kRows - 1) / kRows;
         }
     }
     tc::fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // both CTAs' barriers are there
     tc::fence_after();
     const uint32_t tbase = ctl.tmem;
     const int nt = (p.N + BN - 1) / BN;
@@ -272,23 +339,29 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
             uint32_t phase = 1;   // parity of the phase of `empty` that frees it: the first round passes at once
             int64_t filled = 0;
             bool ok = true;
-            for (int64_t u = blockIdx.x; u < n_tiles && ok; u += gridDim.x) {
-                const Tile t = tile_at(p, prefix, nt, BN, u);
-                const int boxes = t.rows <= 64 ? (t.rows + kRowBox - 1) / kRowBox : 0;  // 0: one of 128 rows
-                const uint32_t bytes = (boxes ? boxes * kRowBox : kTileRows) * 128 + BN * 128;
+            for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
+                const Tile t = tile_at<kRows>(p, prefix, nt, BN, u);
+                const int boxes = !PAIR && t.rows <= 64 ? (t.rows + kRowBox - 1) / kRowBox : 0;  // 0: one of 128 rows
+                const uint32_t bytes = kCtas * ((boxes ? boxes * kRowBox : kTileRows) * 128 + kWBytes);
                 for (int kb = 0; kb < p.KB; kb++) {
                     if (!mm_wait(&ctl.empty[s], phase, abort, p.status, 1)) {
                         ok = false;
                         break;
                     }
                     uint8_t* as = ast + s * p.a_bytes;
-                    mbar_arrive_expect_tx(&ctl.full[s], bytes);
-                    tma_3d(wst + s * BN * 128, &p.tw, kb * 128, t.n0, t.e, &ctl.full[s]);
-                    if (boxes) {
-                        for (int b = 0; b < boxes; b++)
-                            tma_2d(as + b * kRowBox * 128, &p.ta16, kb * 128, t.row0 + b * kRowBox, &ctl.full[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
+                    if (PAIR) {  // the leader's barrier counts both CTAs' bytes
+                        const uint32_t bar = leader_addr(&ctl.full[s]);
+                        tma_3d_pair(wst + s * kWBytes, &p.tw, kb * 128, t.n0 + rank * (BN / 2), t.e, bar);
+                        tma_2d_pair(as, &p.ta128, kb * 128, t.row0 + rank * kTileRows, bar);
                     } else {
-                        tma_2d(as, &p.ta128, kb * 128, t.row0, &ctl.full[s]);
+                        tma_3d(wst + s * kWBytes, &p.tw, kb * 128, t.n0, t.e, &ctl.full[s]);
+                        if (boxes) {
+                            for (int b = 0; b < boxes; b++)
+                                tma_2d(as + b * kRowBox * 128, &p.ta16, kb * 128, t.row0 + b * kRowBox, &ctl.full[s]);
+                        } else {
+                            tma_2d(as, &p.ta128, kb * 128, t.row0, &ctl.full[s]);
+                        }
                     }
                     filled++;
                     if (++s == stages) {
@@ -297,17 +370,25 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                     }
                 }
             }
-            // copies in flight end before the CTA does
-            if (!ok || *abort)
+            if (PAIR && ok)  // every arrival that the leader sends to this CTA's `empty` lands while the CTA is there
+                for (int i = 0; i < stages; i++) {
+                    if (!mm_wait(&ctl.empty[s], phase, abort, p.status, 5)) break;
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            // copies in flight end before the CTAs do
+            if (rank == 0 && (!ok || *abort))
                 for (int64_t i = max((int64_t)0, filled - stages); i < filled; i++)
                     (void)mbar_wait(&ctl.full[i % stages], (uint32_t)(i / stages) & 1, 1000000ull);
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1 && lane == 0 && rank == 0) {
             // ------------------------------------------------------ MMA
-            constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kTileRows, BN);
+            constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kRows, BN);
             int s = 0, a = 0;
             uint32_t phase = 0, aphase = 1;
             bool ok = true;
-            for (int64_t u = blockIdx.x; u < n_tiles && ok; u += gridDim.x) {
+            for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
                 for (int kb = 0; kb < p.KB; kb++) {
                     if (!mm_wait(&ctl.accempty[a], aphase, abort, p.status, 3) ||
                         !mm_wait(&ctl.full[s], phase, abort, p.status, 2)) {
@@ -316,12 +397,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                     }
                     tc::fence_after();
                     const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * p.a_bytes));
-                    const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * BN * 128));
+                    const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * kWBytes));
 #pragma unroll
-                    for (int k = 0; k < 4; k++)  // 32 of K: 32 bytes, 2 units of the descriptors
-                        mma_f8(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
-                    tc::commit(&ctl.empty[s]);
-                    tc::commit(&ctl.accfull[a]);
+                    for (int k = 0; k < 4; k++) {  // 32 of K: 32 bytes, 2 units of the descriptors
+                        if (PAIR) mma_f8_pair(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
+                        else mma_f8(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
+                    }
+                    if (PAIR) {
+                        commit_pair(&ctl.empty[s]);
+                        commit_pair(&ctl.accfull[a]);
+                    } else {
+                        tc::commit(&ctl.empty[s]);
+                        tc::commit(&ctl.accfull[a]);
+                    }
                     if (++s == stages) {
                         s = 0;
                         phase ^= 1;
@@ -332,8 +420,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                     }
                 }
             }
-            tc::commit(&ctl.drain);
+            if (PAIR) commit_pair(&ctl.drain);
+            else tc::commit(&ctl.drain);
             (void)mbar_wait(&ctl.drain, 0);
+        } else if (PAIR && warp == 1 && lane == 0) {
+            // the leader's last arrival; a leader that gave up sends it too
+            (void)mbar_wait(&ctl.drain, 0, 4 * kWaitNs);
         }
         __syncwarp();
     } else {
@@ -341,14 +433,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
         if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         const int quad = warp & 3, half = (warp - kFirstSum) >> 2;
         const int r = quad * 32 + lane;
+        const uint32_t accempty = PAIR ? leader_addr(&ctl.accempty[0]) : smem_u32(&ctl.accempty[0]);
         int a = 0;
         uint32_t aphase = 0;
         bool ok = true;
-        for (int64_t u = blockIdx.x; u < n_tiles && ok; u += gridDim.x) {
-            const Tile t = tile_at(p, prefix, nt, BN, u);
+        for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
+            Tile t = tile_at<kRows>(p, prefix, nt, BN, u);
+            t.row0 += rank * kTileRows;
+            t.rows -= rank * kTileRows;
             const int col0 = t.n0 + half * S::kCols;
             const bool on = r < t.rows;
-            const float* sa = p.sa + (int64_t)(t.row0 + (on ? r : 0)) * p.sa_stride;
+            const float* sa = p.sa + (int64_t)(on ? t.row0 + r : 0) * p.sa_stride;
             const float* sw = p.sw + ((int64_t)t.e * p.NB + min(col0 / kScaleCols, p.NB - 1)) * p.KB;
             float2 acc[S::kCols / 2];
 #pragma unroll
@@ -372,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                         ok = __all_sync(0xffffffffu, ok);
                         if (ok) {
                             add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * BN + half * S::kCols), scale[i],
-                                          &ctl.accempty[a], lane);
+                                          accempty + a * 8, lane);
                             if (++a == S::kAcc) {
                                 a = 0;
                                 aphase ^= 1;
@@ -411,8 +506,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
     }
     tc::fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // neither CTA's shared memory or accumulators are in use any more
     tc::fence_after();
-    if (warp == 1) tc::tmem_dealloc(tbase, S::kTmemCols);
+    if (warp == 1) {
+        if (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(S::kTmemCols) : "memory");
+        else
+            tc::tmem_dealloc(tbase, S::kTmemCols);
+    }
 }
 
 // ================================================================== host side
@@ -445,7 +546,6 @@ bool encode8(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, c
 struct MmFacts {
     int n_sm = 0;
     int smem = 0;  // dynamic shared memory a CTA may have beside the static part
-    bool set[5] = {};
 };
 
 cudaError_t mm_facts(MmFacts** out) {
@@ -462,40 +562,49 @@ cudaError_t mm_facts(MmFacts** out) {
         if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
         f.smem = optin - (int)(sizeof(MmCtl) + 1025 * 4 + 64);
-        const void* fns[5] = {(const void*)fp8_mm_kernel<16>, (const void*)fp8_mm_kernel<32>, (const void*)fp8_mm_kernel<64>,
-                              (const void*)fp8_mm_kernel<128>, (const void*)fp8_mm_kernel<256>};
+        const void* fns[6] = {(const void*)fp8_mm_kernel<16, false>,  (const void*)fp8_mm_kernel<32, false>,
+                              (const void*)fp8_mm_kernel<64, false>,  (const void*)fp8_mm_kernel<128, false>,
+                              (const void*)fp8_mm_kernel<256, false>, (const void*)fp8_mm_kernel<256, true>};
         for (const void* fn : fns)
             if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess) return e;
         // the register split would wait forever on a launch with fewer
-        cudaFuncAttributes wide;
-        if ((e = cudaFuncGetAttributes(&wide, fp8_mm_kernel<256>)) != cudaSuccess) return e;
-        if (wide.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+        for (const void* fn : {fns[4], fns[5]}) {
+            cudaFuncAttributes wide;
+            if ((e = cudaFuncGetAttributes(&wide, fn)) != cudaSuccess) return e;
+            if (wide.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+        }
         f.n_sm = n_sm;
     }
     *out = &f;
     return cudaSuccess;
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 cudaError_t mm_run(const Fp8MmArgs& g, MmParams& p, const MmFacts& f, int64_t tiles, cudaStream_t st) {
+    constexpr int kCtas = PAIR ? 2 : 1;
     const uint64_t dw[3] = {(uint64_t)g.n_inner, (uint64_t)g.n_cols, (uint64_t)g.n_experts};
     const uint64_t sw[2] = {(uint64_t)g.w_stride, (uint64_t)g.w_expert_stride};
-    if (!encode8(&p.tw, 3, g.w, dw, sw, BN)) return cudaErrorInvalidValue;
+    if (!encode8(&p.tw, 3, g.w, dw, sw, BN / kCtas)) return cudaErrorInvalidValue;
     p.a_bytes = g.n_rows <= 64 ? (g.n_rows + kRowBox - 1) / kRowBox * kRowBox * 128 : kTileRows * 128;
+    const int stage = p.a_bytes + BN / kCtas * 128;
     const int tail = kTileRows * 128 - p.a_bytes;  // the last stage's matrix instruction reads 128 rows
-    p.stages = std::min(kMaxStages, (f.smem - 1024 - tail) / (p.a_bytes + BN * 128));
-    const size_t smem = 1024 + (size_t)p.stages * (p.a_bytes + BN * 128) + tail;
+    p.stages = std::min(kMaxStages, (f.smem - 1024 - tail) / stage);
+    const size_t smem = 1024 + (size_t)p.stages * stage + tail;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, f.n_sm));
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, f.n_sm / kCtas) * kCtas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fp8_mm_kernel<BN>, p);
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, fp8_mm_kernel<BN, PAIR>, p);
 }
 
 }  // namespace
@@ -524,6 +633,12 @@ cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t 
     p.NB = scale_blocks(g.n_cols);
     p.out_dtype = g.out_dtype;
     p.out_vec = g.n_cols % 8 == 0 && ((uintptr_t)g.out & 15u) == 0 && (g.out_stride * type_size(g.out_dtype)) % 16 == 0;
+    // Pairs of CTAs where tiles of 256 x 256 fill them: more than half of a tile's rows are there on
+    // average, and there is a tile for each pair.
+    const int64_t per = g.offsets ? g.n_rows / g.n_experts : g.n_rows;
+    const int64_t pair_tiles = (g.offsets ? (int64_t)g.n_rows / 256 + g.n_experts : ((int64_t)g.n_rows + 255) / 256) *
+                               ((g.n_cols + 255) / 256);
+    if (per > kTileRows && pair_tiles >= f->n_sm / 2) return mm_run<256, true>(g, p, *f, pair_tiles, st);
     // row tiles: those of one matrix, or for groups the most there can be if rows spread over the
     // experts (each group's last tile may be short)
     const int64_t mt = g.offsets ? (int64_t)g.n_rows / kTileRows + std::min(g.n_rows, g.n_experts)
@@ -541,11 +656,11 @@ cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t 
     }
     const int64_t tiles = mt * ((g.n_cols + best - 1) / best);
     switch (best) {
-        case 256: return mm_run<256>(g, p, *f, tiles, st);
-        case 128: return mm_run<128>(g, p, *f, tiles, st);
-        case 64: return mm_run<64>(g, p, *f, tiles, st);
-        case 32: return mm_run<32>(g, p, *f, tiles, st);
-        default: return mm_run<16>(g, p, *f, tiles, st);
+        case 256: return mm_run<256, false>(g, p, *f, tiles, st);
+        case 128: return mm_run<128, false>(g, p, *f, tiles, st);
+        case 64: return mm_run<64, false>(g, p, *f, tiles, st);
+        case 32: return mm_run<32, false>(g, p, *f, tiles, st);
+        default: return mm_run<16, false>(g, p, *f, tiles, st);
     }
 }
 

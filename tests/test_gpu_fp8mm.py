@@ -153,3 +153,20 @@ def test_same_bits_alone_and_in_a_batch_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(again, full)
+
+
+@pytest.mark.parametrize("rows,cols,inner,kind", [
+    (2304, 2560, 128, torch.float32), (2500, 2600, 700, torch.bfloat16), (5121, 1030, 200, torch.float32), (8192, 1024, 2048, torch.bfloat16),
+    (300, 9984, 130, torch.float32)])
+def test_matmul_with_tiles_of_two_ctas(rows, cols, inner, kind):
+    test_matmul(rows, cols, inner, kind)
+
+
+@pytest.mark.parametrize("counts", [[300, 0, 129, 700, 1, 256, 2, 512], [2000] + [0] * 4 + [1] * 3, [513] * 8])
+@pytest.mark.parametrize("cols,inner,kind", [(2560, 384, torch.bfloat16), (2100, 100, torch.float32)])
+def test_grouped_with_tiles_of_two_ctas(counts, cols, inner, kind):
+    COUNTS["wide"] = counts
+    try:
+        test_grouped("wide", cols, inner, kind)
+    finally:
+        del COUNTS["wide"]
