@@ -101,6 +101,15 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* m, int x, i
         : "memory");
 }
 
+// One lane of a converged warp, the same one each time.  Code under it is known to run in a single
+// thread, so descriptors stay in uniform registers: issuing a block takes a fraction of what it takes
+// under `lane == 0`.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ---- two CTAs that share a tile (a cluster of 2; the even one leads)
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
 
     if (warp < kFirstSum) {
         if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // ------------------------------------------------------ TMA
             int s = 0;            // stage to fill
             uint32_t phase = 1;   // parity of the phase of `empty` that frees it: the first round passes at once
@@ -344,25 +353,26 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                 const int boxes = !PAIR && t.rows <= 64 ? (t.rows + kRowBox - 1) / kRowBox : 0;  // 0: one of 128 rows
                 const uint32_t bytes = kCtas * ((boxes ? boxes * kRowBox : kTileRows) * 128 + kWBytes);
                 for (int kb = 0; kb < p.KB; kb++) {
-                    if (!mm_wait(&ctl.empty[s], phase, abort, p.status, 1)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(0xffffffffu, mm_wait(&ctl.empty[s], phase, abort, p.status, 1));
+                    if (!ok) break;
                     uint8_t* as = ast + s * p.a_bytes;
-                    if (rank == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
-                    if (PAIR) {  // the leader's barrier counts both CTAs' bytes
-                        const uint32_t bar = leader_addr(&ctl.full[s]);
-                        tma_3d_pair(wst + s * kWBytes, &p.tw, kb * 128, t.n0 + rank * (BN / 2), t.e, bar);
-                        tma_2d_pair(as, &p.ta128, kb * 128, t.row0 + rank * kTileRows, bar);
-                    } else {
-                        tma_3d(wst + s * kWBytes, &p.tw, kb * 128, t.n0, t.e, &ctl.full[s]);
-                        if (boxes) {
-                            for (int b = 0; b < boxes; b++)
-                                tma_2d(as + b * kRowBox * 128, &p.ta16, kb * 128, t.row0 + b * kRowBox, &ctl.full[s]);
+                    if (elect_one()) {
+                        if (rank == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
+                        if (PAIR) {  // the leader's barrier counts both CTAs' bytes
+                            const uint32_t bar = leader_addr(&ctl.full[s]);
+                            tma_3d_pair(wst + s * kWBytes, &p.tw, kb * 128, t.n0 + rank * (BN / 2), t.e, bar);
+                            tma_2d_pair(as, &p.ta128, kb * 128, t.row0 + rank * kTileRows, bar);
                         } else {
-                            tma_2d(as, &p.ta128, kb * 128, t.row0, &ctl.full[s]);
+                            tma_3d(wst + s * kWBytes, &p.tw, kb * 128, t.n0, t.e, &ctl.full[s]);
+                            if (boxes) {
+                                for (int b = 0; b < boxes; b++)
+                                    tma_2d(as + b * kRowBox * 128, &p.ta16, kb * 128, t.row0 + b * kRowBox, &ctl.full[s]);
+                            } else {
+                                tma_2d(as, &p.ta128, kb * 128, t.row0, &ctl.full[s]);
+                            }
                         }
                     }
+                    __syncwarp();
                     filled++;
                     if (++s == stages) {
                         s = 0;
@@ -382,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
             if (rank == 0 && (!ok || *abort))
                 for (int64_t i = max((int64_t)0, filled - stages); i < filled; i++)
                     (void)mbar_wait(&ctl.full[i % stages], (uint32_t)(i / stages) & 1, 1000000ull);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------------ MMA
             constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kRows, BN);
             int s = 0, a = 0;
@@ -390,26 +400,27 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
             bool ok = true;
             for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
                 for (int kb = 0; kb < p.KB; kb++) {
-                    if (!mm_wait(&ctl.accempty[a], aphase, abort, p.status, 3) ||
-                        !mm_wait(&ctl.full[s], phase, abort, p.status, 2)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = mm_wait(&ctl.accempty[a], aphase, abort, p.status, 3) && mm_wait(&ctl.full[s], phase, abort, p.status, 2);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                     tc::fence_after();
-                    const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * p.a_bytes));
-                    const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * kWBytes));
+                    if (elect_one()) {
+                        const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * p.a_bytes));
+                        const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * kWBytes));
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {  // 32 of K: 32 bytes, 2 units of the descriptors
-                        if (PAIR) mma_f8_pair(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
-                        else mma_f8(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
+                        for (int k = 0; k < 4; k++) {  // 32 of K: 32 bytes, 2 units of the descriptors
+                            if (PAIR) mma_f8_pair(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
+                            else mma_f8(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
+                        }
+                        if (PAIR) {
+                            commit_pair(&ctl.empty[s]);
+                            commit_pair(&ctl.accfull[a]);
+                        } else {
+                            tc::commit(&ctl.empty[s]);
+                            tc::commit(&ctl.accfull[a]);
+                        }
                     }
-                    if (PAIR) {
-                        commit_pair(&ctl.empty[s]);
-                        commit_pair(&ctl.accfull[a]);
-                    } else {
-                        tc::commit(&ctl.empty[s]);
-                        tc::commit(&ctl.accfull[a]);
-                    }
+                    __syncwarp();
                     if (++s == stages) {
                         s = 0;
                         phase ^= 1;
@@ -420,10 +431,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                     }
                 }
             }
-            if (PAIR) commit_pair(&ctl.drain);
-            else tc::commit(&ctl.drain);
+            if (elect_one()) {
+                if (PAIR) commit_pair(&ctl.drain);
+                else tc::commit(&ctl.drain);
+            }
+            __syncwarp();
             (void)mbar_wait(&ctl.drain, 0);
-        } else if (PAIR && warp == 1 && lane == 0) {
+        } else if (PAIR && warp == 1) {
             // the leader's last arrival; a leader that gave up sends it too
             (void)mbar_wait(&ctl.drain, 0, 4 * kWaitNs);
         }
