@@ -52,6 +52,7 @@ struct MmParams {
     int M, N, E, KB, NB;  // KB: blocks of K, NB: 128-row blocks of N
     int out_dtype, out_vec;
     int a_bytes, stages;  // bytes of a stage's row part
+    int out_at;           // where the summing warps' staging rows begin in shared memory
 };
 
 struct MmCtl {
@@ -68,6 +69,19 @@ __device__ __noinline__ void mm_timeout(uint32_t* status, uint32_t code) {
         status[2] = blockIdx.x;
         __threadfence();
     }
+}
+
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // Bounded wait of the calling thread; false once the CTA gives up.
@@ -233,8 +247,8 @@ __device__ __forceinline__ float2 fma2(uint32_t b0, uint32_t b1, float s, float2
     return d;
 }
 
-// acc += scale * the thread's columns of an accumulator.  The next 32 columns are read while these
-// are added; the accumulator is free once its last columns are in registers.
+// acc += scale * the thread's columns of an accumulator.  The next columns are read while these are
+// added; the accumulator is free once its last columns are in registers.
 template <int BN>
 __device__ __forceinline__ void add_block(float2 (&acc)[BN / 4], uint32_t src, float scale, uint32_t empty, int lane) {
     using S = MmShape<BN>;
@@ -257,6 +271,59 @@ __device__ __forceinline__ void add_block(float2 (&acc)[BN / 4], uint32_t src, f
             float2& v = acc[j * (S::kLoad / 2) + i];
             v = fma2(d[j & 1][2 * i], d[j & 1][2 * i + 1], scale, v);
         }
+    }
+}
+
+// A warp's 32 rows of the tile (a thread a row, COLS columns) to memory.  Pieces of up to 128 bytes a row
+// go through the warp's own shared memory, so that neighbouring lanes store neighbouring bytes: stored from
+// the registers as they lie, 32 rows at a time, a tile's end took 9000 cycles.
+constexpr int kOutRow = 144;                // bytes of a staged row: 128 and 16 against bank conflicts
+constexpr int kOutStage = 32 * kOutRow;     // of a warp
+
+template <int COLS, bool F32>
+__device__ __forceinline__ void store_rows(const MmParams& p, const float2 (&acc)[COLS / 2], uint8_t* stage, int64_t row0,
+                                           int rows, int col0, int lane) {
+    constexpr int kSize = F32 ? 4 : 2;
+    constexpr int kPiece = COLS * kSize < 128 ? COLS * kSize : 128;  // bytes of a row stored at a time
+    constexpr int kPieceCols = kPiece / kSize;
+    constexpr int kLanes = kPiece / 16;                              // lanes a row
+    constexpr int kStep = 32 / kLanes;                               // rows an instruction
+#pragma unroll
+    for (int c = 0; c < COLS; c += kPieceCols) {
+        uint4* mine = reinterpret_cast<uint4*>(stage + lane * kOutRow);
+#pragma unroll
+        for (int i = 0; i < kLanes; i++) {
+            uint4 w;
+            if (F32) {
+                const float2 a = acc[c / 2 + 2 * i], b = acc[c / 2 + 2 * i + 1];
+                w = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+            } else {
+                const float2* a = &acc[c / 2 + 4 * i];
+                w = make_uint4(pack_bf16(a[0].x, a[0].y), pack_bf16(a[1].x, a[1].y), pack_bf16(a[2].x, a[2].y),
+                               pack_bf16(a[3].x, a[3].y));
+            }
+            mine[i] = w;
+        }
+        __syncwarp();
+        const int n = min(kPieceCols, p.N - col0 - c);  // columns of this piece that are there
+        if (p.out_vec) {  // rows 16-byte aligned, N a multiple of 8: a lane's 16 bytes are there or not as one
+            const int l = lane % kLanes;
+            uint8_t* o = static_cast<uint8_t*>(p.out) + (row0 * p.out_stride + col0 + c) * kSize + 16 * l;
+#pragma unroll
+            for (int r = lane / kLanes; r < 32; r += kStep)
+                if (r < rows && l * (16 / kSize) < n)
+                    *reinterpret_cast<uint4*>(o + r * p.out_stride * kSize) =
+                        *reinterpret_cast<const uint4*>(stage + r * kOutRow + 16 * l);
+        } else {
+            const int last = min(32, rows);
+            for (int r = 0; r < last; r++)
+                for (int j = lane; j < n; j += 32) {
+                    const int64_t at = (row0 + r) * p.out_stride + col0 + c + j;
+                    if (F32) static_cast<float*>(p.out)[at] = reinterpret_cast<const float*>(stage + r * kOutRow)[j];
+                    else static_cast<uint16_t*>(p.out)[at] = reinterpret_cast<const uint16_t*>(stage + r * kOutRow)[j];
+                }
+        }
+        __syncwarp();
     }
 }
 
@@ -400,9 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
             bool ok = true;
             for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
                 for (int kb = 0; kb < p.KB; kb++) {
-                    ok = mm_wait(&ctl.accempty[a], aphase, abort, p.status, 3) && mm_wait(&ctl.full[s], phase, abort, p.status, 2);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    // both are looked at together: most often they are complete, and two waits cost twice one
+                    const bool e = mbar_done(&ctl.accempty[a], aphase), f = mbar_done(&ctl.full[s], phase);
+                    if (!__all_sync(0xffffffffu, e && f)) {
+                        ok = mm_wait(&ctl.accempty[a], aphase, abort, p.status, 3) &&
+                             mm_wait(&ctl.full[s], phase, abort, p.status, 2);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                    }
                     tc::fence_after();
                     if (elect_one()) {
                         const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * p.a_bytes));
@@ -451,26 +523,39 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
         int a = 0;
         uint32_t aphase = 0;
         bool ok = true;
-        for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
-            Tile t = tile_at<kRows>(p, prefix, nt, BN, u);
+        uint8_t* stage = sm + p.out_at + (warp - kFirstSum) * kOutStage;
+        // the thread's row of scales of a tile, and its half's weight block
+        auto place = [&](int64_t u, Tile& t, const float*& sa, const float*& sw) {
+            t = tile_at<kRows>(p, prefix, nt, BN, u);
             t.row0 += rank * kTileRows;
             t.rows -= rank * kTileRows;
-            const int col0 = t.n0 + half * S::kCols;
-            const bool on = r < t.rows;
-            const float* sa = p.sa + (int64_t)(on ? t.row0 + r : 0) * p.sa_stride;
-            const float* sw = p.sw + ((int64_t)t.e * p.NB + min(col0 / kScaleCols, p.NB - 1)) * p.KB;
+            t.n0 += half * S::kCols;
+            sa = p.sa + (int64_t)(r < t.rows ? t.row0 + r : 0) * p.sa_stride;
+            sw = p.sw + ((int64_t)t.e * p.NB + min(t.n0 / kScaleCols, p.NB - 1)) * p.KB;
+        };
+        Tile t;
+        const float *sa, *sw;
+        float scale[4];  // of four blocks at a time, the next four read while these are used
+        if (first_tile < n_tiles) {
+            place(first_tile, t, sa, sw);
+#pragma unroll
+            for (int i = 0; i < 4; i++) scale[i] = sa[min(i, p.KB - 1)] * sw[min(i, p.KB - 1)];
+        }
+        for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
+            const Tile now = t;
             float2 acc[S::kCols / 2];
 #pragma unroll
             for (int i = 0; i < S::kCols / 2; i++) acc[i] = make_float2(0.0f, 0.0f);
-            // scales of four blocks at a time, the next four read while these are used
-            float scale[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) scale[i] = sa[min(i, p.KB - 1)] * sw[min(i, p.KB - 1)];
             for (int kb0 = 0; kb0 < p.KB && ok; kb0 += 4) {
+                int next = kb0 + 4;
+                if (next >= p.KB) {  // the next tile's first four
+                    next = 0;
+                    if (u + tile_step < n_tiles) place(u + tile_step, t, sa, sw);
+                }
                 float na[4], nw[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const int kn = min(kb0 + 4 + i, p.KB - 1);
+                    const int kn = min(next + i, p.KB - 1);
                     na[i] = sa[kn];
                     nw[i] = sw[kn];
                 }
@@ -492,30 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 4; i++) scale[i] = na[i] * nw[i];
             }
-            if (!ok || !on) continue;
-            const int n = min(S::kCols, p.N - col0);
-            uint8_t* o = static_cast<uint8_t*>(row_at(p.out, p.out_stride, type_size(p.out_dtype), t.row0 + r)) +
-                         (int64_t)col0 * type_size(p.out_dtype);
-            if (p.out_vec) {  // rows 16-byte aligned, N a multiple of 8
-#pragma unroll
-                for (int j = 0; j < S::kCols; j += 8) {
-                    float v[8];
-#pragma unroll
-                    for (int q = 0; q < 8; q += 2) {
-                        v[q] = acc[(j + q) / 2].x;
-                        v[q + 1] = acc[(j + q) / 2].y;
-                    }
-                    store8_row<true>(o, p.out_dtype, j, n, v);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < S::kCols; j++)
-                    if (j < n) {
-                        const float v = j % 2 ? acc[j / 2].y : acc[j / 2].x;
-                        if (p.out_dtype == QS_BF16) reinterpret_cast<__nv_bfloat16*>(o)[j] = __float2bfloat16_rn(v);
-                        else reinterpret_cast<float*>(o)[j] = v;
-                    }
-            }
+            const int rows = now.rows - quad * 32;
+            if (!ok || rows <= 0) continue;
+            if (p.out_dtype == QS_F32) store_rows<S::kCols, true>(p, acc, stage, now.row0 + quad * 32, rows, now.n0, lane);
+            else store_rows<S::kCols, false>(p, acc, stage, now.row0 + quad * 32, rows, now.n0, lane);
         }
     }
     tc::fence_before();
@@ -602,8 +667,9 @@ cudaError_t mm_run(const Fp8MmArgs& g, MmParams& p, const MmFacts& f, int64_t ti
     p.a_bytes = g.n_rows <= 64 ? (g.n_rows + kRowBox - 1) / kRowBox * kRowBox * 128 : kTileRows * 128;
     const int stage = p.a_bytes + BN / kCtas * 128;
     const int tail = kTileRows * 128 - p.a_bytes;  // the last stage's matrix instruction reads 128 rows
-    p.stages = std::min(kMaxStages, (f.smem - 1024 - tail) / stage);
-    const size_t smem = 1024 + (size_t)p.stages * stage + tail;
+    p.stages = std::min(kMaxStages, (f.smem - 1024 - tail - 8 * kOutStage) / stage);
+    p.out_at = p.stages * stage + tail;
+    const size_t smem = 1024 + (size_t)p.out_at + 8 * kOutStage;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, f.n_sm / kCtas) * kCtas);
     cfg.blockDim = dim3(kThreads);
