@@ -8,6 +8,7 @@
 // block only and the sum over blocks is kept in registers.  Three roles work at their own pace:
 //   warp 0     TMA: a stage is 128 columns of the tile's rows of a and of its weight rows
 //   warp 1     MMA: four instructions a stage into the next of the accumulators, overwriting
+//   warps 2-3  bring the scales of eight blocks at a time to shared memory
 //   warps 4-11 read an accumulator (a thread a row, half of the columns each), add it, scaled, to
 //              their registers, and after the last block store the tile
 // A thread owns a row of the tile, so a block's scale is one number a thread (two where a tile spans
@@ -32,7 +33,7 @@ namespace {
 
 constexpr int kMaxStages = 32;
 constexpr int kThreads = 384;
-constexpr int kFirstSum = 4;  // first of the eight warps that sum (warps 2 and 3 fill their warpgroup)
+constexpr int kFirstSum = 4;  // first of the eight warps that sum
 // Registers a thread of the widest tile: the launch's 168 x 384 are dealt out as 56 for warps 0-3 and
 // 224 for the others, (56 + 2 x 224) x 128 = 168 x 384.
 constexpr int kLaunchRegs = 168, kFewRegs = 56, kSumRegs = 224;
@@ -55,7 +56,17 @@ struct MmParams {
     int out_at;           // where the summing warps' staging rows begin in shared memory
 };
 
+// Scales on their way to the summing warps: kScaleRing groups of kScaleGroup blocks.  Rows are 132 apart
+// so that the eight blocks of a row, read together, are stored to different banks.
+constexpr int kScaleGroup = 8, kScaleRing = 3;
+struct MmScales {
+    float a[kScaleGroup][kTileRows + 4];
+    float w[2][kScaleGroup];  // of the tile's two column halves
+};
+
 struct MmCtl {
+    MmScales scales[kScaleRing];
+    uint64_t scfull[kScaleRing], scempty[kScaleRing];
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t accfull[4], accempty[4];
     uint64_t drain;
@@ -357,6 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
             mbar_init(&ctl.accfull[s], 1);
             mbar_init(&ctl.accempty[s], 8 * kCtas);
         }
+        for (int s = 0; s < kScaleRing; s++) {
+            mbar_init(&ctl.scfull[s], 2);
+            mbar_init(&ctl.scempty[s], 8);
+        }
         mbar_init(&ctl.drain, 1);
         ctl.abort = 0;
         fence_barrier_init();
@@ -512,6 +527,46 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
         } else if (PAIR && warp == 1) {
             // the leader's last arrival; a leader that gave up sends it too
             (void)mbar_wait(&ctl.drain, 0, 4 * kWaitNs);
+        } else if (warp >= 2) {
+            // ------------------------------------------------------ scales
+            // A lane takes block lane % 8 of every eighth row: 32 bytes of a row are read together, whatever the
+            // rows' alignment, and the loads are far ahead of their use.  Read by the summing threads, each
+            // along its own row, they took 500 to 1800 cycles out of every four blocks.
+            const int b = lane & 7, r0 = (warp - 2) * 4 + (lane >> 3);
+            int slot = 0;
+            uint32_t phase = 1;
+            bool ok = true;
+            for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
+                const Tile t = tile_at<kRows>(p, prefix, nt, BN, u);
+                const int rows = min(kTileRows, t.rows - rank * kTileRows);
+                const float* sa = p.sa + (int64_t)(t.row0 + rank * kTileRows) * p.sa_stride;
+                for (int kb0 = 0; kb0 < p.KB; kb0 += kScaleGroup) {
+                    const int kb = kb0 + b;
+                    const bool on = kb < p.KB;
+                    float v[kTileRows / 8], w = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kTileRows / 8; i++) {
+                        const int r = r0 + 8 * i;
+                        v[i] = on && r < rows ? sa[(int64_t)r * p.sa_stride + kb] : 0.0f;
+                    }
+                    if (warp == 2 && lane < 16 && on) {
+                        const int nb = min((t.n0 + (lane >> 3) * S::kCols) / kScaleCols, p.NB - 1);
+                        w = p.sw[((int64_t)t.e * p.NB + nb) * p.KB + kb];
+                    }
+                    ok = __all_sync(0xffffffffu, mm_wait(&ctl.scempty[slot], phase, abort, p.status, 6));
+                    if (!ok) break;
+                    MmScales& sc = ctl.scales[slot];
+#pragma unroll
+                    for (int i = 0; i < kTileRows / 8; i++) sc.a[b][r0 + 8 * i] = v[i];
+                    if (warp == 2 && lane < 16) sc.w[lane >> 3][b] = w;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.scfull[slot]);
+                    if (++slot == kScaleRing) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
         }
         __syncwarp();
     } else {
@@ -524,63 +579,41 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
         uint32_t aphase = 0;
         bool ok = true;
         uint8_t* stage = sm + p.out_at + (warp - kFirstSum) * kOutStage;
-        // the thread's row of scales of a tile, and its half's weight block
-        auto place = [&](int64_t u, Tile& t, const float*& sa, const float*& sw) {
-            t = tile_at<kRows>(p, prefix, nt, BN, u);
-            t.row0 += rank * kTileRows;
-            t.rows -= rank * kTileRows;
-            t.n0 += half * S::kCols;
-            sa = p.sa + (int64_t)(r < t.rows ? t.row0 + r : 0) * p.sa_stride;
-            sw = p.sw + ((int64_t)t.e * p.NB + min(t.n0 / kScaleCols, p.NB - 1)) * p.KB;
-        };
-        Tile t;
-        const float *sa, *sw;
-        float scale[4];  // of four blocks at a time, the next four read while these are used
-        if (first_tile < n_tiles) {
-            place(first_tile, t, sa, sw);
-#pragma unroll
-            for (int i = 0; i < 4; i++) scale[i] = sa[min(i, p.KB - 1)] * sw[min(i, p.KB - 1)];
-        }
+        int slot = 0;
+        uint32_t scphase = 0;
         for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
-            const Tile now = t;
             float2 acc[S::kCols / 2];
 #pragma unroll
             for (int i = 0; i < S::kCols / 2; i++) acc[i] = make_float2(0.0f, 0.0f);
-            for (int kb0 = 0; kb0 < p.KB && ok; kb0 += 4) {
-                int next = kb0 + 4;
-                if (next >= p.KB) {  // the next tile's first four
-                    next = 0;
-                    if (u + tile_step < n_tiles) place(u + tile_step, t, sa, sw);
-                }
-                float na[4], nw[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int kn = min(next + i, p.KB - 1);
-                    na[i] = sa[kn];
-                    nw[i] = sw[kn];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    if (kb0 + i < p.KB && ok) {
-                        ok = mm_wait(&ctl.accfull[a], aphase, abort, p.status, 4);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (ok) {
-                            add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * BN + half * S::kCols), scale[i],
-                                          accempty + a * 8, lane);
-                            if (++a == S::kAcc) {
-                                a = 0;
-                                aphase ^= 1;
-                            }
-                        }
+            for (int kb0 = 0; kb0 < p.KB && ok; kb0 += kScaleGroup) {
+                ok = __all_sync(0xffffffffu, mm_wait(&ctl.scfull[slot], scphase, abort, p.status, 7));
+                if (!ok) break;
+                const MmScales& sc = ctl.scales[slot];
+                const int n = min(kScaleGroup, p.KB - kb0);
+                for (int i = 0; i < n; i++) {
+                    const float scale = sc.a[i][r] * sc.w[half][i];
+                    ok = __all_sync(0xffffffffu, mm_wait(&ctl.accfull[a], aphase, abort, p.status, 4));
+                    if (!ok) break;
+                    add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * BN + half * S::kCols), scale, accempty + a * 8, lane);
+                    if (++a == S::kAcc) {
+                        a = 0;
+                        aphase ^= 1;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; i++) scale[i] = na[i] * nw[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.scempty[slot]);
+                if (++slot == kScaleRing) {
+                    slot = 0;
+                    scphase ^= 1;
+                }
             }
-            const int rows = now.rows - quad * 32;
-            if (!ok || rows <= 0) continue;
-            if (p.out_dtype == QS_F32) store_rows<S::kCols, true>(p, acc, stage, now.row0 + quad * 32, rows, now.n0, lane);
-            else store_rows<S::kCols, false>(p, acc, stage, now.row0 + quad * 32, rows, now.n0, lane);
+            if (!ok) break;
+            const Tile now = tile_at<kRows>(p, prefix, nt, BN, u);
+            const int64_t row0 = now.row0 + rank * kTileRows + quad * 32;
+            const int rows = now.rows - rank * kTileRows - quad * 32, col0 = now.n0 + half * S::kCols;
+            if (rows <= 0) continue;
+            if (p.out_dtype == QS_F32) store_rows<S::kCols, true>(p, acc, stage, row0, rows, col0, lane);
+            else store_rows<S::kCols, false>(p, acc, stage, row0, rows, col0, lane);
         }
     }
     tc::fence_before();
