@@ -9,7 +9,8 @@
 //   warp 0     TMA: a stage is 128 columns of the tile's rows of a and of its weight rows
 //   warp 1     MMA: four instructions a stage into the next of the accumulators, overwriting
 //   warps 2-3  bring the scales of eight blocks at a time to shared memory
-//   warps 4-11 read an accumulator (a thread a row, half of the columns each), add it, scaled, to
+//   warps 4-   (eight, sixteen for the widest tile) read an accumulator, a thread 64 columns of a row
+//              at most, add it, scaled, to
 //              their registers, and after the last block store the tile
 // A thread owns a row of the tile, so a block's scale is one number a thread (two where a tile spans
 // two weight blocks, one for each half of the warps) and a step costs one multiply-add an element.
@@ -32,11 +33,7 @@ namespace qs {
 namespace {
 
 constexpr int kMaxStages = 32;
-constexpr int kThreads = 384;
-constexpr int kFirstSum = 4;  // first of the eight warps that sum
-// Registers a thread of the widest tile: the launch's 168 x 384 are dealt out as 56 for warps 0-3 and
-// 224 for the others, (56 + 2 x 224) x 128 = 168 x 384.
-constexpr int kLaunchRegs = 168, kFewRegs = 56, kSumRegs = 224;
+constexpr int kFirstSum = 4;  // first of the warps that sum
 constexpr int kTileRows = 128;
 constexpr int kRowBox = 16;  // rows of the small TMA box of a
 
@@ -44,6 +41,7 @@ struct MmParams {
     CUtensorMap ta16;   // a, boxes of 16 rows x 128 bytes
     CUtensorMap ta128;  // a, boxes of 128 rows
     CUtensorMap tw;     // w [expert][row][k], boxes of BN rows
+    CUtensorMap tout;   // out, boxes of 32 rows x 128 bytes
     const float* sa;
     const float* sw;
     const int32_t* offsets;
@@ -51,9 +49,9 @@ struct MmParams {
     uint32_t* status;
     int64_t sa_stride, out_stride;
     int M, N, E, KB, NB;  // KB: blocks of K, NB: 128-row blocks of N
-    int out_dtype, out_vec;
+    int out_dtype, out_vec, out_tma;
     int a_bytes, stages;  // bytes of a stage's row part
-    int out_at;           // where the summing warps' staging rows begin in shared memory
+    int out_at;           // where the summing warps' staging rows begin in shared memory, a multiple of 1024
 };
 
 // Scales on their way to the summing warps: kScaleRing groups of kScaleGroup blocks.  Rows are 132 apart
@@ -61,7 +59,7 @@ struct MmParams {
 constexpr int kScaleGroup = 8, kScaleRing = 3;
 struct MmScales {
     float a[kScaleGroup][kTileRows + 4];
-    float w[2][kScaleGroup];  // of the tile's two column halves
+    float w[2][kScaleGroup];  // of the tile's first and second 128 columns
 };
 
 struct MmCtl {
@@ -244,9 +242,20 @@ template <int BN>
 struct MmShape {
     static constexpr int kAcc = BN == 256 ? 2 : 4;                      // accumulators in tensor memory
     static constexpr int kTmemCols = BN * kAcc < 32 ? 32 : BN * kAcc;  // 64 .. 512
-    static constexpr int kCols = BN / 2;                                // columns of an epilogue thread
-    static constexpr int kLoad = BN == 256 ? 16 : kCols < 32 ? kCols : 32;  // columns of one tensor-memory load (32 spill there)
+    // Sixteen warps sum the widest tile: with eight (128 columns a thread) a block took 780 cycles, most of
+    // them waits that four warps a scheduler fill.
+    static constexpr int kSumWarps = BN == 256 ? 16 : 8;
+    static constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
+    static constexpr int kCols = BN * 4 / kSumWarps;                    // columns of a summing thread
+    static constexpr int kLoad = kCols < 32 ? kCols : BN == 256 ? 16 : 32;  // columns of one tensor-memory load
+    static constexpr int kBufs = BN == 256 ? 1 : 2;                     // loads in registers at a time
+    static constexpr int kSumBytes = kSumWarps * 4096;                  // their staging rows
 };
+
+// Registers a thread of the widest tile: the launch's 96 x 640 are dealt out as 56 for warps 0-3 and
+// 104 for the others, (56 + 4 x 104) x 128 <= 96 x 640.
+constexpr int kLaunchRegs = 96, kFewRegs = 56, kSumRegs = 104;
+static_assert((kFewRegs + 4 * kSumRegs) * 128 <= kLaunchRegs * MmShape<256>::kThreads, "more registers than launched");
 
 // a + b * s in both halves
 __device__ __forceinline__ float2 fma2(uint32_t b0, uint32_t b1, float s, float2 a) {
@@ -258,50 +267,55 @@ __device__ __forceinline__ float2 fma2(uint32_t b0, uint32_t b1, float s, float2
     return d;
 }
 
-// acc += scale * the thread's columns of an accumulator.  The next columns are read while these are
-// added; the accumulator is free once its last columns are in registers.
+// acc += scale * the thread's columns of an accumulator, which is free once its last columns are in
+// registers.  With two buffers the next columns are read while these are added.
 template <int BN>
-__device__ __forceinline__ void add_block(float2 (&acc)[BN / 4], uint32_t src, float scale, uint32_t empty, int lane) {
+__device__ __forceinline__ void add_block(float2 (&acc)[MmShape<BN>::kCols / 2], uint32_t src, float scale, uint32_t empty,
+                                          int lane) {
     using S = MmShape<BN>;
     constexpr int kSteps = S::kCols / S::kLoad;
-    uint32_t d[2][S::kLoad];
+    uint32_t d[S::kBufs][S::kLoad];
     tc::fence_after();
     tmem_load<S::kLoad>(src, d[0]);
 #pragma unroll
     for (int j = 0; j < kSteps; j++) {
         tc::wait_ld();
-        if (j + 1 < kSteps) {
-            tmem_load<S::kLoad>(src + (j + 1) * S::kLoad, d[(j + 1) & 1]);
-        } else {
+        if (j + 1 == kSteps) {
             tc::fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(empty);
+        } else if (S::kBufs == 2) {
+            tmem_load<S::kLoad>(src + (j + 1) * S::kLoad, d[(j + 1) % S::kBufs]);
         }
 #pragma unroll
         for (int i = 0; i < S::kLoad / 2; i++) {
             float2& v = acc[j * (S::kLoad / 2) + i];
-            v = fma2(d[j & 1][2 * i], d[j & 1][2 * i + 1], scale, v);
+            v = fma2(d[j % S::kBufs][2 * i], d[j % S::kBufs][2 * i + 1], scale, v);
         }
+        if (S::kBufs == 1 && j + 1 < kSteps) tmem_load<S::kLoad>(src + (j + 1) * S::kLoad, d[0]);
     }
 }
 
 // A warp's 32 rows of the tile (a thread a row, COLS columns) to memory.  Pieces of up to 128 bytes a row
-// go through the warp's own shared memory, so that neighbouring lanes store neighbouring bytes: stored from
-// the registers as they lie, 32 rows at a time, a tile's end took 9000 cycles.
-constexpr int kOutRow = 144;                // bytes of a staged row: 128 and 16 against bank conflicts
-constexpr int kOutStage = 32 * kOutRow;     // of a warp
-
+// go through the warp's 4096 bytes of shared memory, 16-byte parts swapped about as the 128-byte swizzle
+// does: whole pieces are then copied out by TMA while the warp goes on, or, where rows of the tile are
+// not the call's or the output is not aligned for that, stored by neighbouring lanes.  (Stored from the
+// registers as they lie, 32 rows at a time, a tile's end took 9000 cycles.)
 template <int COLS, bool F32>
-__device__ __forceinline__ void store_rows(const MmParams& p, const float2 (&acc)[COLS / 2], uint8_t* stage, int64_t row0,
+__device__ __forceinline__ void store_rows(const MmParams& p, const float2 (&acc)[COLS / 2], uint8_t* stage, int row0,
                                            int rows, int col0, int lane) {
     constexpr int kSize = F32 ? 4 : 2;
     constexpr int kPiece = COLS * kSize < 128 ? COLS * kSize : 128;  // bytes of a row stored at a time
     constexpr int kPieceCols = kPiece / kSize;
     constexpr int kLanes = kPiece / 16;                              // lanes a row
     constexpr int kStep = 32 / kLanes;                               // rows an instruction
+    const bool tma = kPiece == 128 && p.out_tma && (rows >= 32 || !p.offsets);
 #pragma unroll
     for (int c = 0; c < COLS; c += kPieceCols) {
-        uint4* mine = reinterpret_cast<uint4*>(stage + lane * kOutRow);
+        const int n = min(kPieceCols, p.N - col0 - c);  // columns of this piece that are there
+        if (n <= 0) break;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the piece before has left
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < kLanes; i++) {
             uint4 w;
@@ -313,25 +327,33 @@ __device__ __forceinline__ void store_rows(const MmParams& p, const float2 (&acc
                 w = make_uint4(pack_bf16(a[0].x, a[0].y), pack_bf16(a[1].x, a[1].y), pack_bf16(a[2].x, a[2].y),
                                pack_bf16(a[3].x, a[3].y));
             }
-            mine[i] = w;
+            *reinterpret_cast<uint4*>(stage + tc::sw128_offset(lane, 16 * i)) = w;
         }
+        if (tma) fence_proxy_async_smem();
         __syncwarp();
-        const int n = min(kPieceCols, p.N - col0 - c);  // columns of this piece that are there
-        if (p.out_vec) {  // rows 16-byte aligned, N a multiple of 8: a lane's 16 bytes are there or not as one
+        if (tma) {
+            if (lane == 0) {
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&p.tout),
+                             "r"(col0 + c), "r"(row0), "r"(smem_u32(stage))
+                             : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+        } else if (p.out_vec) {  // rows 16-byte aligned, N a multiple of 8: a lane's 16 bytes are there or not as one
             const int l = lane % kLanes;
             uint8_t* o = static_cast<uint8_t*>(p.out) + (row0 * p.out_stride + col0 + c) * kSize + 16 * l;
 #pragma unroll
             for (int r = lane / kLanes; r < 32; r += kStep)
                 if (r < rows && l * (16 / kSize) < n)
                     *reinterpret_cast<uint4*>(o + r * p.out_stride * kSize) =
-                        *reinterpret_cast<const uint4*>(stage + r * kOutRow + 16 * l);
+                        *reinterpret_cast<const uint4*>(stage + tc::sw128_offset(r, 16 * l));
         } else {
             const int last = min(32, rows);
             for (int r = 0; r < last; r++)
                 for (int j = lane; j < n; j += 32) {
                     const int64_t at = (row0 + r) * p.out_stride + col0 + c + j;
-                    if (F32) static_cast<float*>(p.out)[at] = reinterpret_cast<const float*>(stage + r * kOutRow)[j];
-                    else static_cast<uint16_t*>(p.out)[at] = reinterpret_cast<const uint16_t*>(stage + r * kOutRow)[j];
+                    const uint8_t* v = stage + tc::sw128_offset(r, kSize * j);
+                    if (F32) static_cast<float*>(p.out)[at] = *reinterpret_cast<const float*>(v);
+                    else static_cast<uint16_t*>(p.out)[at] = *reinterpret_cast<const uint16_t*>(v);
                 }
         }
         __syncwarp();
@@ -341,7 +363,7 @@ __device__ __forceinline__ void store_rows(const MmParams& p, const float2 (&acc
 // PAIR: two CTAs take a tile of 256 rows together, each 128 rows and half of the weight rows; the
 // leader issues the matrix instructions for both.
 template <int BN, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_constant__ MmParams p) {
+__global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const __grid_constant__ MmParams p) {
     using S = MmShape<BN>;
     constexpr int kCtas = PAIR ? 2 : 1, kRows = kTileRows * kCtas;
     constexpr int kWBytes = BN / kCtas * 128;  // a CTA's weight part of a stage
@@ -366,11 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
         }
         for (int s = 0; s < S::kAcc; s++) {
             mbar_init(&ctl.accfull[s], 1);
-            mbar_init(&ctl.accempty[s], 8 * kCtas);
+            mbar_init(&ctl.accempty[s], S::kSumWarps * kCtas);
         }
         for (int s = 0; s < kScaleRing; s++) {
             mbar_init(&ctl.scfull[s], 2);
-            mbar_init(&ctl.scempty[s], 8);
+            mbar_init(&ctl.scempty[s], S::kSumWarps);
         }
         mbar_init(&ctl.drain, 1);
         ctl.abort = 0;
@@ -550,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                         v[i] = on && r < rows ? sa[(int64_t)r * p.sa_stride + kb] : 0.0f;
                     }
                     if (warp == 2 && lane < 16 && on) {
-                        const int nb = min((t.n0 + (lane >> 3) * S::kCols) / kScaleCols, p.NB - 1);
+                        const int nb = min(t.n0 / kScaleCols + (BN == 256 ? lane >> 3 : 0), p.NB - 1);
                         w = p.sw[((int64_t)t.e * p.NB + nb) * p.KB + kb];
                     }
                     ok = __all_sync(0xffffffffu, mm_wait(&ctl.scempty[slot], phase, abort, p.status, 6));
@@ -572,13 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
     } else {
         // ---------------------------------------------------------- sum over blocks, store
         if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-        const int quad = warp & 3, half = (warp - kFirstSum) >> 2;
+        const int quad = warp & 3, part = (warp - kFirstSum) >> 2;  // rows, columns
+        constexpr int kParts = kScaleCols / S::kCols;                // of a weight block
         const int r = quad * 32 + lane;
         const uint32_t accempty = PAIR ? leader_addr(&ctl.accempty[0]) : smem_u32(&ctl.accempty[0]);
         int a = 0;
         uint32_t aphase = 0;
         bool ok = true;
-        uint8_t* stage = sm + p.out_at + (warp - kFirstSum) * kOutStage;
+        uint8_t* stage = sm + p.out_at + (warp - kFirstSum) * 4096;
         int slot = 0;
         uint32_t scphase = 0;
         for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
@@ -591,10 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
                 const MmScales& sc = ctl.scales[slot];
                 const int n = min(kScaleGroup, p.KB - kb0);
                 for (int i = 0; i < n; i++) {
-                    const float scale = sc.a[i][r] * sc.w[half][i];
+                    const float scale = sc.a[i][r] * sc.w[BN == 256 ? part / kParts : 0][i];
                     ok = __all_sync(0xffffffffu, mm_wait(&ctl.accfull[a], aphase, abort, p.status, 4));
                     if (!ok) break;
-                    add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * BN + half * S::kCols), scale, accempty + a * 8, lane);
+                    add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * BN + part * S::kCols), scale, accempty + a * 8, lane);
                     if (++a == S::kAcc) {
                         a = 0;
                         aphase ^= 1;
@@ -609,12 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mm_kernel(const __grid_consta
             }
             if (!ok) break;
             const Tile now = tile_at<kRows>(p, prefix, nt, BN, u);
-            const int64_t row0 = now.row0 + rank * kTileRows + quad * 32;
-            const int rows = now.rows - rank * kTileRows - quad * 32, col0 = now.n0 + half * S::kCols;
+            const int row0 = now.row0 + rank * kTileRows + quad * 32, rows = now.rows - rank * kTileRows - quad * 32;
+            const int col0 = now.n0 + part * S::kCols;
             if (rows <= 0) continue;
             if (p.out_dtype == QS_F32) store_rows<S::kCols, true>(p, acc, stage, row0, rows, col0, lane);
             else store_rows<S::kCols, false>(p, acc, stage, row0, rows, col0, lane);
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // copies out end before the CTA does
+        __syncwarp();
     }
     tc::fence_before();
     __syncthreads();
@@ -643,6 +668,16 @@ EncodeFn get_encode() {
             fn = reinterpret_cast<EncodeFn>(f);
     });
     return fn;
+}
+
+bool encode_out(CUtensorMap* m, void* base, int dtype, const uint64_t* dims, uint64_t stride) {
+    EncodeFn fn = get_encode();
+    if (!fn) return false;
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / type_size(dtype)), 32}, es[2] = {1, 1};
+    const cuuint64_t d[2] = {dims[0], dims[1]}, st[1] = {stride};
+    return fn(m, dtype == QS_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d, st, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode8(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides, uint32_t box_rows) {
@@ -700,12 +735,12 @@ cudaError_t mm_run(const Fp8MmArgs& g, MmParams& p, const MmFacts& f, int64_t ti
     p.a_bytes = g.n_rows <= 64 ? (g.n_rows + kRowBox - 1) / kRowBox * kRowBox * 128 : kTileRows * 128;
     const int stage = p.a_bytes + BN / kCtas * 128;
     const int tail = kTileRows * 128 - p.a_bytes;  // the last stage's matrix instruction reads 128 rows
-    p.stages = std::min(kMaxStages, (f.smem - 1024 - tail - 8 * kOutStage) / stage);
+    p.stages = std::min(kMaxStages, (f.smem - 1024 - tail - MmShape<BN>::kSumBytes) / stage);
     p.out_at = p.stages * stage + tail;
-    const size_t smem = 1024 + (size_t)p.out_at + 8 * kOutStage;
+    const size_t smem = 1024 + (size_t)p.out_at + MmShape<BN>::kSumBytes;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, f.n_sm / kCtas) * kCtas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(MmShape<BN>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
@@ -746,6 +781,12 @@ cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t 
     p.NB = scale_blocks(g.n_cols);
     p.out_dtype = g.out_dtype;
     p.out_vec = g.n_cols % 8 == 0 && ((uintptr_t)g.out & 15u) == 0 && (g.out_stride * type_size(g.out_dtype)) % 16 == 0;
+    // copied out by TMA: rows on 16-byte boundaries, at a stride that a tensor map holds
+    const int64_t out_bytes = g.out_stride * type_size(g.out_dtype);
+    p.out_tma = ((uintptr_t)g.out & 15u) == 0 && out_bytes % 16 == 0 && out_bytes >= g.n_cols * (int64_t)type_size(g.out_dtype) &&
+                out_bytes < (1ll << 40);
+    const uint64_t dout[2] = {(uint64_t)g.n_cols, (uint64_t)g.n_rows};
+    if (p.out_tma && !encode_out(&p.tout, g.out, g.out_dtype, dout, (uint64_t)out_bytes)) return cudaErrorInvalidValue;
     // Pairs of CTAs where tiles of 256 x 256 fill them: more than half of a tile's rows are there on
     // average, and there is a tile for each pair.
     const int64_t per = g.offsets ? g.n_rows / g.n_experts : g.n_rows;
