@@ -240,8 +240,12 @@ __device__ __forceinline__ Tile tile_at(const MmParams& p, const int* prefix, in
 
 template <int BN>
 struct MmShape {
-    static constexpr int kAcc = BN == 256 ? 2 : 4;                      // accumulators in tensor memory
-    static constexpr int kTmemCols = BN * kAcc < 32 ? 32 : BN * kAcc;  // 64 .. 512
+    // The widest tile is two accumulators of 128 columns, filled and read one after the other: with one of
+    // 256 the time from a read back to the next fill stood open, 700 cycles a block.
+    static constexpr int kHalves = BN == 256 ? 2 : 1;
+    static constexpr int kAccCols = BN / kHalves;
+    static constexpr int kAcc = 4;                                       // accumulators in tensor memory
+    static constexpr int kTmemCols = kAccCols * kAcc < 32 ? 32 : kAccCols * kAcc;  // 64 .. 512
     // Sixteen warps sum the widest tile: with eight (128 columns a thread) a block took 780 cycles, most of
     // them waits that four warps a scheduler fill.
     static constexpr int kSumWarps = BN == 256 ? 16 : 8;
@@ -371,7 +375,8 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~(uintptr_t)1023);
     __shared__ MmCtl ctl;
     __shared__ int prefix[1025];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // known to be the same in a warp, so that what follows from it may live in uniform registers
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_rank() : 0;
     const unsigned first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
     volatile int* abort = &ctl.abort;
@@ -388,7 +393,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
         }
         for (int s = 0; s < S::kAcc; s++) {
             mbar_init(&ctl.accfull[s], 1);
-            mbar_init(&ctl.accempty[s], S::kSumWarps * kCtas);
+            mbar_init(&ctl.accempty[s], S::kSumWarps / S::kHalves * kCtas);
         }
         for (int s = 0; s < kScaleRing; s++) {
             mbar_init(&ctl.scfull[s], 2);
@@ -498,45 +503,50 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                     (void)mbar_wait(&ctl.full[i % stages], (uint32_t)(i / stages) & 1, 1000000ull);
         } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------------ MMA
-            constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kRows, BN);
+            constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kRows, S::kAccCols);
             int s = 0, a = 0;
             uint32_t phase = 0, aphase = 1;
             bool ok = true;
             for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
                 for (int kb = 0; kb < p.KB; kb++) {
-                    // both are looked at together: most often they are complete, and two waits cost twice one
-                    const bool e = mbar_done(&ctl.accempty[a], aphase), f = mbar_done(&ctl.full[s], phase);
-                    if (!__all_sync(0xffffffffu, e && f)) {
-                        ok = mm_wait(&ctl.accempty[a], aphase, abort, p.status, 3) &&
-                             mm_wait(&ctl.full[s], phase, abort, p.status, 2);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                    }
-                    tc::fence_after();
-                    if (elect_one()) {
-                        const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * p.a_bytes));
-                        const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * kWBytes));
 #pragma unroll
-                        for (int k = 0; k < 4; k++) {  // 32 of K: 32 bytes, 2 units of the descriptors
-                            if (PAIR) mma_f8_pair(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
-                            else mma_f8(tbase + a * BN, ad + 2 * k, wd + 2 * k, id, k > 0);
+                    for (int h = 0; h < S::kHalves; h++) {
+                        // both are looked at together: most often they are complete, and two waits cost twice one
+                        const bool e = mbar_done(&ctl.accempty[a], aphase);
+                        const bool f = h > 0 || mbar_done(&ctl.full[s], phase);
+                        if (!__all_sync(0xffffffffu, e && f)) {
+                            ok = mm_wait(&ctl.accempty[a], aphase, abort, p.status, 3) &&
+                                 (h > 0 || mm_wait(&ctl.full[s], phase, abort, p.status, 2));
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
                         }
-                        if (PAIR) {
-                            commit_pair(&ctl.empty[s]);
-                            commit_pair(&ctl.accfull[a]);
-                        } else {
-                            tc::commit(&ctl.empty[s]);
-                            tc::commit(&ctl.accfull[a]);
+                        tc::fence_after();
+                        if (elect_one()) {
+                            const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * p.a_bytes));
+                            const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * kWBytes + h * (kWBytes / S::kHalves)));
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {  // 32 of K: 32 bytes, 2 units of the descriptors
+                                if (PAIR) mma_f8_pair(tbase + a * S::kAccCols, ad + 2 * k, wd + 2 * k, id, k > 0);
+                                else mma_f8(tbase + a * S::kAccCols, ad + 2 * k, wd + 2 * k, id, k > 0);
+                            }
+                            if (PAIR) {
+                                if (h + 1 == S::kHalves) commit_pair(&ctl.empty[s]);
+                                commit_pair(&ctl.accfull[a]);
+                            } else {
+                                if (h + 1 == S::kHalves) tc::commit(&ctl.empty[s]);
+                                tc::commit(&ctl.accfull[a]);
+                            }
+                        }
+                        __syncwarp();
+                        if (++a == S::kAcc) {
+                            a = 0;
+                            aphase ^= 1;
                         }
                     }
-                    __syncwarp();
+                    if (!ok) break;
                     if (++s == stages) {
                         s = 0;
                         phase ^= 1;
-                    }
-                    if (++a == S::kAcc) {
-                        a = 0;
-                        aphase ^= 1;
                     }
                 }
             }
@@ -594,11 +604,15 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
     } else {
         // ---------------------------------------------------------- sum over blocks, store
         if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-        const int quad = warp & 3, part = (warp - kFirstSum) >> 2;  // rows, columns
-        constexpr int kParts = kScaleCols / S::kCols;                // of a weight block
+        const int quad = warp & 3, part = (warp - kFirstSum) >> 2;  // the warp's rows and columns of the accumulators
+        constexpr int kParts = S::kAccCols / S::kCols;               // column parts of an accumulator
+        const int h = part / kParts, sub = part % kParts;
+        // First column of the tile that the warp's columns are.  An accumulator of a pair has half of its
+        // columns from each CTA's weight rows, and those are 128 apart.
+        const int col_at = PAIR ? h * (S::kAccCols / 2) + sub * (BN / 2) : h * S::kAccCols + sub * S::kCols;
         const int r = quad * 32 + lane;
         const uint32_t accempty = PAIR ? leader_addr(&ctl.accempty[0]) : smem_u32(&ctl.accempty[0]);
-        int a = 0;
+        int a = h;
         uint32_t aphase = 0;
         bool ok = true;
         uint8_t* stage = sm + p.out_at + (warp - kFirstSum) * 4096;
@@ -614,12 +628,12 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                 const MmScales& sc = ctl.scales[slot];
                 const int n = min(kScaleGroup, p.KB - kb0);
                 for (int i = 0; i < n; i++) {
-                    const float scale = sc.a[i][r] * sc.w[BN == 256 ? part / kParts : 0][i];
+                    const float scale = sc.a[i][r] * sc.w[col_at / kScaleCols][i];
                     ok = __all_sync(0xffffffffu, mm_wait(&ctl.accfull[a], aphase, abort, p.status, 4));
                     if (!ok) break;
-                    add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * BN + part * S::kCols), scale, accempty + a * 8, lane);
-                    if (++a == S::kAcc) {
-                        a = 0;
+                    add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * S::kAccCols + sub * S::kCols), scale, accempty + a * 8, lane);
+                    if ((a += S::kHalves) >= S::kAcc) {
+                        a = h;
                         aphase ^= 1;
                     }
                 }
@@ -633,7 +647,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             if (!ok) break;
             const Tile now = tile_at<kRows>(p, prefix, nt, BN, u);
             const int row0 = now.row0 + rank * kTileRows + quad * 32, rows = now.rows - rank * kTileRows - quad * 32;
-            const int col0 = now.n0 + part * S::kCols;
+            const int col0 = now.n0 + col_at;
             if (rows <= 0) continue;
             if (p.out_dtype == QS_F32) store_rows<S::kCols, true>(p, acc, stage, row0, rows, col0, lane);
             else store_rows<S::kCols, false>(p, acc, stage, row0, rows, col0, lane);
