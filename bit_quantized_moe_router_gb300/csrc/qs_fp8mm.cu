@@ -7,8 +7,8 @@
 // memory), one block of 128 at a time; since every block has its own scales, an accumulator holds one
 // block only and the sum over blocks is kept in registers.  Three roles work at their own pace:
 //   warp 0     TMA: a stage is 128 columns of the tile's rows of a and of its weight rows
-//   warp 1     MMA: four instructions a stage into the next of the accumulators, overwriting
-//   warps 2-3  bring the scales of eight blocks at a time to shared memory
+//   warps 1-2  MMA, taking accumulators in turn: four instructions a block and accumulator, overwriting
+//   warp 3     brings the scales of eight blocks at a time to shared memory
 //   warps 4-   (eight, sixteen for the widest tile) read an accumulator, a thread 64 columns of a row
 //              at most, add it, scaled, to
 //              their registers, and after the last block store the tile
@@ -246,20 +246,19 @@ struct MmShape {
     static constexpr int kAccCols = BN / kHalves;
     static constexpr int kAcc = 4;                                       // accumulators in tensor memory
     static constexpr int kTmemCols = kAccCols * kAcc < 32 ? 32 : kAccCols * kAcc;  // 64 .. 512
-    // Sixteen warps sum the widest tile: with eight (128 columns a thread) a block took 780 cycles, most of
-    // them waits that four warps a scheduler fill.
-    static constexpr int kSumWarps = BN == 256 ? 16 : 8;
+    static constexpr int kSumWarps = 8;
     static constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
-    static constexpr int kCols = BN * 4 / kSumWarps;                    // columns of a summing thread
-    static constexpr int kLoad = kCols < 32 ? kCols : BN == 256 ? 16 : 32;  // columns of one tensor-memory load
-    static constexpr int kBufs = BN == 256 ? 1 : 2;                     // loads in registers at a time
-    static constexpr int kSumBytes = kSumWarps * 4096;                  // their staging rows
+    static constexpr int kCols = BN * 4 / kSumWarps;            // columns of a summing thread, in runs of 64 at most:
+    static constexpr int kRun = kCols < 64 ? kCols : 64;        // what lies together in a pair's accumulator and in w
+    static constexpr int kRuns = kCols / kRun;
+    static constexpr int kLoad = BN == 256 ? 16 : kRun < 32 ? kRun : 32;  // columns of one tensor-memory load
+    static constexpr int kSumBytes = kSumWarps * 4096;          // staging rows of the summing warps
 };
 
-// Registers a thread of the widest tile: the launch's 96 x 640 are dealt out as 56 for warps 0-3 and
-// 104 for the others, (56 + 4 x 104) x 128 <= 96 x 640.
-constexpr int kLaunchRegs = 96, kFewRegs = 56, kSumRegs = 104;
-static_assert((kFewRegs + 4 * kSumRegs) * 128 <= kLaunchRegs * MmShape<256>::kThreads, "more registers than launched");
+// Registers a thread of the widest tile: the launch's 168 x 384 are dealt out as 56 for warps 0-3 and
+// 224 for the others, (56 + 2 x 224) x 128 <= 168 x 384.
+constexpr int kLaunchRegs = 168, kFewRegs = 56, kSumRegs = 224;
+static_assert((kFewRegs + 2 * kSumRegs) * 128 <= kLaunchRegs * MmShape<256>::kThreads, "more registers than launched");
 
 // a + b * s in both halves
 __device__ __forceinline__ float2 fma2(uint32_t b0, uint32_t b1, float s, float2 a) {
@@ -274,11 +273,11 @@ __device__ __forceinline__ float2 fma2(uint32_t b0, uint32_t b1, float s, float2
 // acc += scale * the thread's columns of an accumulator, which is free once its last columns are in
 // registers.  With two buffers the next columns are read while these are added.
 template <int BN>
-__device__ __forceinline__ void add_block(float2 (&acc)[MmShape<BN>::kCols / 2], uint32_t src, float scale, uint32_t empty,
-                                          int lane) {
+__device__ __forceinline__ void add_block(float2 (&acc)[MmShape<BN>::kRuns][MmShape<BN>::kRun / 2], uint32_t src,
+                                          const float (&scale)[MmShape<BN>::kRuns], uint32_t empty, int lane) {
     using S = MmShape<BN>;
     constexpr int kSteps = S::kCols / S::kLoad;
-    uint32_t d[S::kBufs][S::kLoad];
+    uint32_t d[2][S::kLoad];
     tc::fence_after();
     tmem_load<S::kLoad>(src, d[0]);
 #pragma unroll
@@ -288,15 +287,15 @@ __device__ __forceinline__ void add_block(float2 (&acc)[MmShape<BN>::kCols / 2],
             tc::fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(empty);
-        } else if (S::kBufs == 2) {
-            tmem_load<S::kLoad>(src + (j + 1) * S::kLoad, d[(j + 1) % S::kBufs]);
+        } else {
+            tmem_load<S::kLoad>(src + (j + 1) * S::kLoad, d[(j + 1) % 2]);
         }
+        constexpr int kPer = S::kRun / S::kLoad;  // loads of a run
 #pragma unroll
         for (int i = 0; i < S::kLoad / 2; i++) {
-            float2& v = acc[j * (S::kLoad / 2) + i];
-            v = fma2(d[j % S::kBufs][2 * i], d[j % S::kBufs][2 * i + 1], scale, v);
+            float2& v = acc[j / kPer][j % kPer * (S::kLoad / 2) + i];
+            v = fma2(d[j % 2][2 * i], d[j % 2][2 * i + 1], scale[j / kPer], v);
         }
-        if (S::kBufs == 1 && j + 1 < kSteps) tmem_load<S::kLoad>(src + (j + 1) * S::kLoad, d[0]);
     }
 }
 
@@ -389,17 +388,17 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; s++) {
             mbar_init(&ctl.full[s], 1);
-            mbar_init(&ctl.empty[s], 1);
+            mbar_init(&ctl.empty[s], S::kHalves);
         }
         for (int s = 0; s < S::kAcc; s++) {
             mbar_init(&ctl.accfull[s], 1);
             mbar_init(&ctl.accempty[s], S::kSumWarps / S::kHalves * kCtas);
         }
         for (int s = 0; s < kScaleRing; s++) {
-            mbar_init(&ctl.scfull[s], 2);
+            mbar_init(&ctl.scfull[s], 1);
             mbar_init(&ctl.scempty[s], S::kSumWarps);
         }
-        mbar_init(&ctl.drain, 1);
+        mbar_init(&ctl.drain, 2);
         ctl.abort = 0;
         fence_barrier_init();
     }
@@ -501,53 +500,55 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             if (rank == 0 && (!ok || *abort))
                 for (int64_t i = max((int64_t)0, filled - stages); i < filled; i++)
                     (void)mbar_wait(&ctl.full[i % stages], (uint32_t)(i / stages) & 1, 1000000ull);
-        } else if (warp == 1 && rank == 0) {
+        } else if (warp < 3 && rank == 0) {
             // ------------------------------------------------------ MMA
+            // Issuing a block's instructions and looking at its barriers takes one warp 400 to 500 cycles, as long
+            // as the tensor cores take for it: two warps take turns.  Warp w has accumulators w and w + 2: the
+            // widest tile's half w of every block, else every second block.
             constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kRows, S::kAccCols);
-            int s = 0, a = 0;
-            uint32_t phase = 0, aphase = 1;
+            constexpr int kTurn = 2 / S::kHalves;  // blocks from one of the warp's to the next
+            const int w = warp - 1, h = S::kHalves == 2 ? w : 0;
+            int64_t blocks = 0;  // of this CTA
+            for (int64_t u = first_tile; u < n_tiles; u += tile_step) blocks += p.KB;
+            int s = S::kHalves == 2 ? 0 : w % stages, a = w;
+            uint32_t phase = S::kHalves == 2 ? 0 : (w / stages) & 1, aphase = 1;
             bool ok = true;
-            for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
-                for (int kb = 0; kb < p.KB; kb++) {
-#pragma unroll
-                    for (int h = 0; h < S::kHalves; h++) {
-                        // both are looked at together: most often they are complete, and two waits cost twice one
-                        const bool e = mbar_done(&ctl.accempty[a], aphase);
-                        const bool f = h > 0 || mbar_done(&ctl.full[s], phase);
-                        if (!__all_sync(0xffffffffu, e && f)) {
-                            ok = mm_wait(&ctl.accempty[a], aphase, abort, p.status, 3) &&
-                                 (h > 0 || mm_wait(&ctl.full[s], phase, abort, p.status, 2));
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) break;
-                        }
-                        tc::fence_after();
-                        if (elect_one()) {
-                            const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * p.a_bytes));
-                            const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * kWBytes + h * (kWBytes / S::kHalves)));
-#pragma unroll
-                            for (int k = 0; k < 4; k++) {  // 32 of K: 32 bytes, 2 units of the descriptors
-                                if (PAIR) mma_f8_pair(tbase + a * S::kAccCols, ad + 2 * k, wd + 2 * k, id, k > 0);
-                                else mma_f8(tbase + a * S::kAccCols, ad + 2 * k, wd + 2 * k, id, k > 0);
-                            }
-                            if (PAIR) {
-                                if (h + 1 == S::kHalves) commit_pair(&ctl.empty[s]);
-                                commit_pair(&ctl.accfull[a]);
-                            } else {
-                                if (h + 1 == S::kHalves) tc::commit(&ctl.empty[s]);
-                                tc::commit(&ctl.accfull[a]);
-                            }
-                        }
-                        __syncwarp();
-                        if (++a == S::kAcc) {
-                            a = 0;
-                            aphase ^= 1;
-                        }
-                    }
+            for (int64_t c = S::kHalves == 2 ? 0 : w; c < blocks && ok; c += kTurn) {
+                // both are looked at together: most often they are complete, and two waits cost twice one
+                const bool e = mbar_done(&ctl.accempty[a], aphase), f = mbar_done(&ctl.full[s], phase);
+                if (!__all_sync(0xffffffffu, e && f)) {
+                    ok = mm_wait(&ctl.accempty[a], aphase, abort, p.status, 3) &&
+                         mm_wait(&ctl.full[s], phase, abort, p.status, 2);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    if (++s == stages) {
-                        s = 0;
-                        phase ^= 1;
+                }
+                tc::fence_after();
+                if (elect_one()) {
+                    const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * p.a_bytes));
+                    const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * kWBytes + h * (kWBytes / S::kHalves)));
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {  // 32 of K: 32 bytes, 2 units of the descriptors
+                        if (PAIR) mma_f8_pair(tbase + a * S::kAccCols, ad + 2 * k, wd + 2 * k, id, k > 0);
+                        else mma_f8(tbase + a * S::kAccCols, ad + 2 * k, wd + 2 * k, id, k > 0);
                     }
+                    if (PAIR) {
+                        commit_pair(&ctl.accfull[a]);
+                        commit_pair(&ctl.empty[s]);
+                    } else {
+                        tc::commit(&ctl.accfull[a]);
+                        tc::commit(&ctl.empty[s]);
+                    }
+                }
+                __syncwarp();
+                s += kTurn;
+                if (s >= stages) {
+                    s -= stages;
+                    phase ^= 1;
+                }
+                a += 2;
+                if (a >= S::kAcc) {
+                    a = w;
+                    aphase ^= 1;
                 }
             }
             if (elect_one()) {
@@ -557,14 +558,14 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             __syncwarp();
             (void)mbar_wait(&ctl.drain, 0);
         } else if (PAIR && warp == 1) {
-            // the leader's last arrival; a leader that gave up sends it too
+            // the leader's last arrivals; a leader that gave up sends them too
             (void)mbar_wait(&ctl.drain, 0, 4 * kWaitNs);
-        } else if (warp >= 2) {
+        } else if (warp == 3) {
             // ------------------------------------------------------ scales
-            // A lane takes block lane % 8 of every eighth row: 32 bytes of a row are read together, whatever the
+            // A lane takes block lane % 8 of every fourth row: 32 bytes of a row are read together, whatever the
             // rows' alignment, and the loads are far ahead of their use.  Read by the summing threads, each
             // along its own row, they took 500 to 1800 cycles out of every four blocks.
-            const int b = lane & 7, r0 = (warp - 2) * 4 + (lane >> 3);
+            const int b = lane & 7, r0 = lane >> 3;
             int slot = 0;
             uint32_t phase = 1;
             bool ok = true;
@@ -575,22 +576,28 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                 for (int kb0 = 0; kb0 < p.KB; kb0 += kScaleGroup) {
                     const int kb = kb0 + b;
                     const bool on = kb < p.KB;
-                    float v[kTileRows / 8], w = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < kTileRows / 8; i++) {
-                        const int r = r0 + 8 * i;
-                        v[i] = on && r < rows ? sa[(int64_t)r * p.sa_stride + kb] : 0.0f;
-                    }
-                    if (warp == 2 && lane < 16 && on) {
+                    MmScales& sc = ctl.scales[slot];
+                    float w = 0.0f;
+                    if (lane < 16 && on) {
                         const int nb = min(t.n0 / kScaleCols + (BN == 256 ? lane >> 3 : 0), p.NB - 1);
                         w = p.sw[((int64_t)t.e * p.NB + nb) * p.KB + kb];
                     }
-                    ok = __all_sync(0xffffffffu, mm_wait(&ctl.scempty[slot], phase, abort, p.status, 6));
-                    if (!ok) break;
-                    MmScales& sc = ctl.scales[slot];
+                    for (int r1 = 0; r1 < kTileRows; r1 += 64) {
+                        float v[16];
 #pragma unroll
-                    for (int i = 0; i < kTileRows / 8; i++) sc.a[b][r0 + 8 * i] = v[i];
-                    if (warp == 2 && lane < 16) sc.w[lane >> 3][b] = w;
+                        for (int i = 0; i < 16; i++) {
+                            const int r = r1 + r0 + 4 * i;
+                            v[i] = on && r < rows ? sa[(int64_t)r * p.sa_stride + kb] : 0.0f;
+                        }
+                        if (r1 == 0) {
+                            ok = __all_sync(0xffffffffu, mm_wait(&ctl.scempty[slot], phase, abort, p.status, 6));
+                            if (!ok) break;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; i++) sc.a[b][r1 + r0 + 4 * i] = v[i];
+                    }
+                    if (!ok) break;
+                    if (lane < 16) sc.w[lane >> 3][b] = w;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl.scfull[slot]);
                     if (++slot == kScaleRing) {
@@ -607,9 +614,11 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
         const int quad = warp & 3, part = (warp - kFirstSum) >> 2;  // the warp's rows and columns of the accumulators
         constexpr int kParts = S::kAccCols / S::kCols;               // column parts of an accumulator
         const int h = part / kParts, sub = part % kParts;
-        // First column of the tile that the warp's columns are.  An accumulator of a pair has half of its
-        // columns from each CTA's weight rows, and those are 128 apart.
-        const int col_at = PAIR ? h * (S::kAccCols / 2) + sub * (BN / 2) : h * S::kAccCols + sub * S::kCols;
+        // First column of the tile that a run of the warp's columns is.  An accumulator of a pair has half of
+        // its columns from each CTA's weight rows, and those are 128 apart.
+        auto col_at = [&](int q) {
+            return PAIR ? h * (S::kAccCols / 2) + q * (BN / 2) : h * S::kAccCols + sub * S::kCols + q * S::kRun;
+        };
         const int r = quad * 32 + lane;
         const uint32_t accempty = PAIR ? leader_addr(&ctl.accempty[0]) : smem_u32(&ctl.accempty[0]);
         int a = h;
@@ -619,16 +628,18 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
         int slot = 0;
         uint32_t scphase = 0;
         for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
-            float2 acc[S::kCols / 2];
+            float2 acc[S::kRuns][S::kRun / 2];
 #pragma unroll
-            for (int i = 0; i < S::kCols / 2; i++) acc[i] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < S::kCols / 2; i++) acc[i / (S::kRun / 2)][i % (S::kRun / 2)] = make_float2(0.0f, 0.0f);
             for (int kb0 = 0; kb0 < p.KB && ok; kb0 += kScaleGroup) {
                 ok = __all_sync(0xffffffffu, mm_wait(&ctl.scfull[slot], scphase, abort, p.status, 7));
                 if (!ok) break;
                 const MmScales& sc = ctl.scales[slot];
                 const int n = min(kScaleGroup, p.KB - kb0);
                 for (int i = 0; i < n; i++) {
-                    const float scale = sc.a[i][r] * sc.w[col_at / kScaleCols][i];
+                    float scale[S::kRuns];
+#pragma unroll
+                    for (int q = 0; q < S::kRuns; q++) scale[q] = sc.a[i][r] * sc.w[col_at(q) / kScaleCols][i];
                     ok = __all_sync(0xffffffffu, mm_wait(&ctl.accfull[a], aphase, abort, p.status, 4));
                     if (!ok) break;
                     add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * S::kAccCols + sub * S::kCols), scale, accempty + a * 8, lane);
@@ -647,10 +658,12 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             if (!ok) break;
             const Tile now = tile_at<kRows>(p, prefix, nt, BN, u);
             const int row0 = now.row0 + rank * kTileRows + quad * 32, rows = now.rows - rank * kTileRows - quad * 32;
-            const int col0 = now.n0 + col_at;
             if (rows <= 0) continue;
-            if (p.out_dtype == QS_F32) store_rows<S::kCols, true>(p, acc, stage, row0, rows, col0, lane);
-            else store_rows<S::kCols, false>(p, acc, stage, row0, rows, col0, lane);
+#pragma unroll
+            for (int q = 0; q < S::kRuns; q++) {
+                if (p.out_dtype == QS_F32) store_rows<S::kRun, true>(p, acc[q], stage, row0, rows, now.n0 + col_at(q), lane);
+                else store_rows<S::kRun, false>(p, acc[q], stage, row0, rows, now.n0 + col_at(q), lane);
+            }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // copies out end before the CTA does
         __syncwarp();
