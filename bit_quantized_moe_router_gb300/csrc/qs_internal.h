@@ -137,10 +137,10 @@ struct NormBwdArgs {
     const void* dy;
     const void* dsum;
     void* dx;
-    float* partial;  // [n_parts x part_stride], or null without dweight
+    float* partial;  // [a row a CTA x part_stride], or null without dweight
     int64_t sum_stride, dy_stride, dsum_stride, dx_stride;
     int sum_dtype, dy_dtype, dsum_dtype, dx_dtype;
-    int n_rows, hidden, part_stride, n_parts;
+    int n_rows, hidden, part_stride;
     float eps;
 };
 struct SiluArgs {
@@ -151,7 +151,7 @@ struct SiluArgs {
     int64_t gate_up_stride, q_stride, q_scale_stride;
     int dtype, n_rows, ffn;
 };
-constexpr int kNormParts = 1024;     // most partial rows of dweight
+constexpr int kNormParts = 456;      // most CTAs of the gradient, a partial row of dweight each: three an SM
 constexpr int kNormMaxHidden = 16384;
 cudaError_t launch_rmsnorm(const NormArgs& p, cudaStream_t st);
 cudaError_t launch_rmsnorm_backward(const NormBwdArgs& p, float* dweight, cudaStream_t st);

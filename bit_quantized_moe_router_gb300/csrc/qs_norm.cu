@@ -9,8 +9,8 @@
 //
 // Gradient.  With g = weight * dy: dx = rho * g - s * rho^3 * mean(g * s) + dsum.  Both sums over a
 // row (s^2 and g * s) are formed in one pass; a group keeps its columns' share of dweight in
-// registers over all its rows and writes one partial row, and a second launch adds the partial
-// rows in ascending order (no atomics: the same bits every run).
+// registers over all its rows, a CTA writes one partial row, and a second launch adds the partial
+// rows in a fixed order (no atomics: the same bits every run).
 #include "qs_internal.h"
 #include "qs_rows.cuh"
 
@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_kernel(const NormAr
     if (!p.y && !p.q) return;
     group_sum<G, 1>(ss, red[group], wg, lane, 1 + group);
     const float rho = rsqrtf(ss[0] / (float)p.hidden + p.eps);
+    // rho is left to the end, where it costs the codes no rounding; rows so small that it is large take it at once
+    const float factor = rho > 65536.0f ? 1.0f : rho, least = kMinAmax / factor;
     void* yr = p.y ? row_at(p.y, p.y_stride, type_size(p.y_dtype), t) : nullptr;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
@@ -89,47 +91,74 @@ __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_kernel(const NormAr
         float w[8];
         load8_row<VEC>(p.weight, QS_F32, i, p.hidden, w);
 #pragma unroll
-        for (int q = 0; q < 8; q++) w[q] = s[j][q] * rho * w[q];
-        if (yr) store8_row<VEC>(yr, p.y_dtype, i, p.hidden, w);
-        if (p.q) quant8_row<VEC>(w, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, i, p.hidden);
+        for (int q = 0; q < 8; q++) w[q] *= s[j][q];
+        if (rho != factor) {
+#pragma unroll
+            for (int q = 0; q < 8; q++) w[q] *= rho;
+        }
+        if (p.q) quant8_row<VEC>(w, factor, least, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, i, p.hidden);
+        if (yr) {
+#pragma unroll
+            for (int q = 0; q < 8; q++) w[q] *= factor;
+            store8_row<VEC>(yr, p.y_dtype, i, p.hidden, w);
+        }
     }
 }
 
-// Rows r = group, group + (number of groups), ...; `partial` row `group` gets the group's dweight.
-template <bool VEC, int G, int NV>
-__global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_backward_kernel(const NormBwdArgs p) {
-    constexpr int kGroups = cta_warps(G) / G;
+// Rows r = group, group + (number of groups), ...; row blockIdx.x of `partial` gets the CTA's dweight.  The
+// next row is on its way while a row's sums cross the group: without that a row cost its whole latency.
+template <bool VEC, bool B16, int G, int NV>
+__global__ void __launch_bounds__(32 * cta_warps(G), B16 && NV == 1 && G <= 8 ? 3 : 1) rmsnorm_backward_kernel(const NormBwdArgs p) {
+    constexpr int kGroups = cta_warps(G) / G, kCols = 256 * G * NV;
     __shared__ float red[kGroups][2][2 * G];
+    __shared__ float part[kGroups > 1 ? kGroups : 1][kGroups > 1 ? kCols : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / G, wg = warp % G;
     const int64_t first = (int64_t)blockIdx.x * kGroups + group, step = (int64_t)gridDim.x * kGroups;
+    auto col = [&](int j) { return (j * 32 * G + wg * 32 + lane) * 8; };
     pdl_wait();
     pdl_launch_next();
-    float dw[NV][8];
+    Held8<VEC, B16> sh[NV], gh[NV], dh[NV];
+    auto load_sg = [&](int64_t t) {
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            sh[j].load(row_at(p.sum, p.sum_stride, type_size(p.sum_dtype), t), p.sum_dtype, col(j), p.hidden);
+            gh[j].load(row_at(p.dy, p.dy_stride, type_size(p.dy_dtype), t), p.dy_dtype, col(j), p.hidden);
+        }
+    };
+    auto load_d = [&](int64_t t) {
+#pragma unroll
+        for (int j = 0; j < NV; j++)
+            dh[j].load(row_at(p.dsum, p.dsum_stride, type_size(p.dsum_dtype), t), p.dsum_dtype, col(j), p.hidden);
+    };
+    float dw[NV][8], w0[8];
 #pragma unroll
     for (int j = 0; j < NV; j++)
 #pragma unroll
         for (int q = 0; q < 8; q++) dw[j][q] = 0.0f;
+    if (NV == 1) load8_row<VEC>(p.weight, QS_F32, col(0), p.hidden, w0);
+    if (first < p.n_rows) {
+        load_sg(first);
+        if (p.dsum) load_d(first);
+    }
     int flip = 0;
     for (int64_t t = first; t < p.n_rows; t += step, flip ^= 1) {
-        const void* sr = row_at(p.sum, p.sum_stride, type_size(p.sum_dtype), t);
-        const void* gr = row_at(p.dy, p.dy_stride, type_size(p.dy_dtype), t);
         float s[NV][8], g[NV][8];
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            const int i = (j * 32 * G + wg * 32 + lane) * 8;
-            load8_row<VEC>(sr, p.sum_dtype, i, p.hidden, s[j]);
-            load8_row<VEC>(gr, p.dy_dtype, i, p.hidden, g[j]);
+            sh[j].get(p.sum_dtype, s[j]);
+            gh[j].get(p.dy_dtype, g[j]);
         }
+        if (t + step < p.n_rows) load_sg(t + step);
         float a[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < NV; j++) {
             float w[8];
-            load8_row<VEC>(p.weight, QS_F32, (j * 32 * G + wg * 32 + lane) * 8, p.hidden, w);
+            if (NV > 1) load8_row<VEC>(p.weight, QS_F32, col(j), p.hidden, w);
 #pragma unroll
             for (int q = 0; q < 8; q++) {
                 a[0] = fmaf(s[j][q], s[j][q], a[0]);
-                a[1] = fmaf(w[q] * g[j][q], s[j][q], a[1]);
+                a[1] = fmaf((NV > 1 ? w[q] : w0[q]) * g[j][q], s[j][q], a[1]);
             }
         }
         group_sum<G, 2>(a, red[group][flip], wg, lane, 1 + group);
@@ -138,11 +167,10 @@ __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_backward_kernel(con
         void* o = row_at(p.dx, p.dx_stride, type_size(p.dx_dtype), t);
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            const int i = (j * 32 * G + wg * 32 + lane) * 8;
             float w[8], d[8];
-            load8_row<VEC>(p.weight, QS_F32, i, p.hidden, w);
+            if (NV > 1) load8_row<VEC>(p.weight, QS_F32, col(j), p.hidden, w);
             if (p.dsum) {
-                load8_row<VEC>(row_at(p.dsum, p.dsum_stride, type_size(p.dsum_dtype), t), p.dsum_dtype, i, p.hidden, d);
+                dh[j].get(p.dsum_dtype, d);
             } else {
 #pragma unroll
                 for (int q = 0; q < 8; q++) d[q] = 0.0f;
@@ -150,17 +178,30 @@ __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_backward_kernel(con
 #pragma unroll
             for (int q = 0; q < 8; q++) {
                 dw[j][q] = fmaf(g[j][q], s[j][q] * rho, dw[j][q]);
-                d[q] = fmaf(rho, w[q] * g[j][q], fmaf(-c, s[j][q], d[q]));
+                d[q] = fmaf(rho, (NV > 1 ? w[q] : w0[q]) * g[j][q], fmaf(-c, s[j][q], d[q]));
             }
-            store8_row<VEC>(o, p.dx_dtype, i, p.hidden, d);
+            store8_row<VEC>(o, p.dx_dtype, col(j), p.hidden, d);
         }
+        if (p.dsum && t + step < p.n_rows) load_d(t + step);
     }
-    if (!p.partial || first >= p.n_parts) return;
-    float* part = p.partial + first * p.part_stride;
+    if (!p.partial) return;
+    // the CTA's groups in ascending order
+    float* row = p.partial + (int64_t)blockIdx.x * p.part_stride;
+    if (kGroups == 1) {
 #pragma unroll
-    for (int j = 0; j < NV; j++) {
-        const int i = (j * 32 * G + wg * 32 + lane) * 8;
-        store8_row<true>(part, QS_F32, i, p.part_stride, dw[j]);  // part_stride: hidden rounded up to 8
+        for (int j = 0; j < NV; j++) store8_row<true>(row, QS_F32, col(j), p.part_stride, dw[j]);  // hidden rounded up to 8
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; j++)
+#pragma unroll
+            for (int q = 0; q < 8; q++) part[group][col(j) + q] = dw[j][q];
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.part_stride; i += blockDim.x) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kGroups; k++) v += part[k][i];
+            row[i] = v;
+        }
     }
 }
 
@@ -175,7 +216,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* __re
     pdl_launch_next();
     float a = 0.0f;
     if (h < hidden) {
-#pragma unroll 4
+#pragma unroll 10
         for (int r = warp; r < n_parts; r += 32) a += partial[(size_t)r * stride + h];
     }
     sm[warp][lane] = a;
@@ -185,30 +226,43 @@ __global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* __re
     if (lane == 0 && c < hidden) dweight[c] = v;
 }
 
+// silu(g) * u.  The quotient's 2 units in the last place (__fdividef; expf has 1) are 2^-22 of the value,
+// far inside its code's 2^-4; a true division here and one a value for the codes made the kernel wait for
+// instructions, 69 us against 25 us of memory time at 65536 x 512.  Past g = -87 the quotient is 0.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
+
 // Sixteen lanes a (row, 128 columns): eight elements of gate and of up each.
 template <bool VEC>
 __global__ void __launch_bounds__(256) silu_mul_quant_kernel(const SiluArgs p) {
     pdl_wait();
     pdl_launch_next();
-    const int nb = scale_blocks(p.ffn);
-    const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
+    const unsigned nb = scale_blocks(p.ffn);
+    const unsigned half = threadIdx.x >> 4, l = threadIdx.x & 15;
     int64_t rows = p.n_rows;
     if (p.n_rows_dev) rows = min(rows, (int64_t)max(*p.n_rows_dev, 0));
-    const int64_t work = rows * nb;
-    // a warp's two halves take neighbouring blocks; both run the shuffles as long as one has work
-    for (int64_t u0 = ((int64_t)blockIdx.x * 8 + (half >> 1)) * 2; u0 < work; u0 += (int64_t)gridDim.x * 16) {
-        const int64_t u = u0 + (half & 1);
-        const bool on = u < work;
-        const int64_t t = on ? u / nb : 0;
-        const int i = (int)(on ? u - t * nb : 0) * kScaleCols + l * 8;
+    // (row, block) of this half warp, and the step to its next: the grid is small enough for 32 bits
+    const unsigned u0 = blockIdx.x * 16 + half, du = gridDim.x * 16;
+    int64_t t = u0 / nb;
+    unsigned b = u0 % nb;
+    const unsigned dt = du / nb, db = du % nb;
+    // both halves of a warp run the shuffles as long as one has work
+    while (__any_sync(0xffffffffu, t < rows)) {
+        const bool on = t < rows;
+        const int i = (int)(b * kScaleCols + l * 8);
         const int n = on ? p.ffn : 0;
         const uint8_t* row = static_cast<const uint8_t*>(row_at(p.gate_up, p.gate_up_stride, type_size(p.dtype), t));
         float g[8], v[8];
         load8_row<VEC>(row, p.dtype, i, n, g);
         load8_row<VEC>(row + (size_t)p.ffn * type_size(p.dtype), p.dtype, i, n, v);
 #pragma unroll
-        for (int q = 0; q < 8; q++) v[q] *= silu(g[q]);
-        quant8_row<VEC>(v, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, i, n);
+        for (int q = 0; q < 8; q++) v[q] = silu_mul(g[q], v[q]);
+        quant8_row<VEC>(v, 1.0f, kMinAmax, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, i, n);
+        t += dt;
+        b += db;
+        if (b >= nb) {
+            b -= nb;
+            t++;
+        }
     }
 }
 
@@ -249,32 +303,29 @@ cudaError_t norm_pick(const NormArgs& p, cudaStream_t st) {
     return norm_run<VEC, 16, 4>(p, st);
 }
 
-template <bool VEC, int G, int NV>
+template <bool VEC, bool B16, int G, int NV>
 cudaError_t norm_bwd_run(NormBwdArgs p, float* dweight, cudaStream_t st) {
     constexpr int groups = cta_warps(G) / G;
-    static_assert(kNormParts % groups == 0, "partial rows fill whole CTAs");
     const int64_t ctas = (p.n_rows + groups - 1) / groups;
-    // dweight: at most kNormParts groups, each with a partial row; without it one group a row
-    const unsigned grid = (unsigned)(dweight ? std::min<int64_t>(ctas, kNormParts / groups) : ctas);
-    p.n_parts = dweight ? (int)std::min<int64_t>(p.n_rows, (int64_t)grid * groups) : 0;
+    const unsigned grid = (unsigned)std::min<int64_t>(ctas, kNormParts);
     if (grid > 0) {
-        const cudaError_t e = launch_pdl(rmsnorm_backward_kernel<VEC, G, NV>, grid, 32 * cta_warps(G), st, p);
-        if (e != cudaSuccess || !dweight) return e;
+        const cudaError_t e = launch_pdl(rmsnorm_backward_kernel<VEC, B16, G, NV>, grid, 32 * cta_warps(G), st, p);
+        if (e != cudaSuccess) return e;
     }
     if (!dweight) return cudaSuccess;
     return launch_pdl(rmsnorm_dweight_kernel, (unsigned)((p.hidden + 31) / 32), 1024, st, (const float*)p.partial,
-                      p.n_parts, p.part_stride, p.hidden, dweight);
+                      (int)grid, p.part_stride, p.hidden, dweight);
 }
 
-template <bool VEC>
+template <bool VEC, bool B16>
 cudaError_t norm_bwd_pick(const NormBwdArgs& p, float* dweight, cudaStream_t st) {
-    if (p.hidden <= 256) return norm_bwd_run<VEC, 1, 1>(p, dweight, st);
-    if (p.hidden <= 512) return norm_bwd_run<VEC, 2, 1>(p, dweight, st);
-    if (p.hidden <= 1024) return norm_bwd_run<VEC, 4, 1>(p, dweight, st);
-    if (p.hidden <= 2048) return norm_bwd_run<VEC, 8, 1>(p, dweight, st);
-    if (p.hidden <= 4096) return norm_bwd_run<VEC, 16, 1>(p, dweight, st);
-    if (p.hidden <= 8192) return norm_bwd_run<VEC, 16, 2>(p, dweight, st);
-    return norm_bwd_run<VEC, 16, 4>(p, dweight, st);
+    if (p.hidden <= 256) return norm_bwd_run<VEC, B16, 1, 1>(p, dweight, st);
+    if (p.hidden <= 512) return norm_bwd_run<VEC, B16, 2, 1>(p, dweight, st);
+    if (p.hidden <= 1024) return norm_bwd_run<VEC, B16, 4, 1>(p, dweight, st);
+    if (p.hidden <= 2048) return norm_bwd_run<VEC, B16, 8, 1>(p, dweight, st);
+    if (p.hidden <= 4096) return norm_bwd_run<VEC, B16, 16, 1>(p, dweight, st);
+    if (p.hidden <= 8192) return norm_bwd_run<VEC, B16, 16, 2>(p, dweight, st);
+    return norm_bwd_run<VEC, B16, 16, 4>(p, dweight, st);
 }
 
 }  // namespace
@@ -293,7 +344,9 @@ cudaError_t launch_rmsnorm_backward(const NormBwdArgs& p, float* dweight, cudaSt
     const bool vec = p.hidden % 8 == 0 && al16(p.sum, p.sum_stride, p.sum_dtype) &&
                      al16(p.dy, p.dy_stride, p.dy_dtype) && al16(p.weight, 0, QS_F32) &&
                      (!p.dsum || al16(p.dsum, p.dsum_stride, p.dsum_dtype)) && al16(p.dx, p.dx_stride, p.dx_dtype);
-    return vec ? norm_bwd_pick<true>(p, dweight, st) : norm_bwd_pick<false>(p, dweight, st);
+    const bool b16 = p.sum_dtype == QS_BF16 && p.dy_dtype == QS_BF16 && (!p.dsum || p.dsum_dtype == QS_BF16);
+    if (!vec) return norm_bwd_pick<false, false>(p, dweight, st);
+    return b16 ? norm_bwd_pick<true, true>(p, dweight, st) : norm_bwd_pick<true, false>(p, dweight, st);
 }
 
 cudaError_t launch_silu_mul_quant(const SiluArgs& p, cudaStream_t st) {

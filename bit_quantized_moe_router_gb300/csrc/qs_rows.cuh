@@ -86,24 +86,29 @@ __device__ __forceinline__ void* row_at(void* base, int64_t stride, int size, in
 __host__ __device__ constexpr int type_size(int dtype) { return dtype == QS_F32 ? 4 : dtype == QS_BF16 ? 2 : 1; }
 
 // Sixteen lanes that hold the 128 columns of one scale block, eight each (columns i .. i+7; those
-// past n hold 0): the block's scale, and the lane's codes.  amax is the exact maximum, so the scale
-// is one fp32 division and each code one fp32 division and one rounding.  fmaxf drops a NaN: its own
-// code is a NaN and the others of its block keep their scale.
+// past n hold 0), of values v * factor with one factor for the row: the block's scale, and the lane's codes.
+// The factor drops out of a code, v * factor * (448 / (amax * factor)), so it is left out of it; 448 / amax is held
+// in two parts (its fp32 value and what that rounding left out), and a code's product has one rounding.
+// least: kMinAmax / factor.  fmaxf drops a NaN: its own code is a NaN and the others of its block keep their
+// scale.  An infinite amax leaves no remainder: all codes of the block are NaNs.
 template <bool VEC>
-__device__ __forceinline__ void quant8_row(const float (&v)[8], uint8_t* q_row, float* scale_row, int i, int n) {
+__device__ __forceinline__ void quant8_row(const float (&v)[8], float factor, float least, uint8_t* q_row, float* scale_row,
+                                           int i, int n) {
     float a = 0.0f;
 #pragma unroll
     for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(v[q]));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const float scale = fmaxf(a, kMinAmax) / kE4m3Max;
+    a = fmaxf(a, least);
+    const float amax = a * factor, part = __frcp_rn(a), inv = kE4m3Max * part, rest = fmaf(-inv, a, kE4m3Max) * part;
+    const auto scaled = [&](float x) { return fmaf(x, inv, x * rest); };
     if (i >= n) return;
-    if (i % kScaleCols == 0) scale_row[i / kScaleCols] = scale;
+    if (i % kScaleCols == 0) scale_row[i / kScaleCols] = amax * (1.0f / kE4m3Max);
     uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h] / scale, v[4 * h + 1] / scale), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2] / scale, v[4 * h + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(scaled(v[4 * h]), scaled(v[4 * h + 1])), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(scaled(v[4 * h + 2]), scaled(v[4 * h + 3])), __NV_SATFINITE, __NV_E4M3);
         w[h] = lo | (hi << 16);
     }
     if (VEC) {
@@ -114,5 +119,45 @@ __device__ __forceinline__ void quant8_row(const float (&v)[8], uint8_t* q_row, 
             if (i + q < n) q_row[i + q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
     }
 }
+
+// Eight elements of a row as they were loaded, to be widened later: loads of the next row or slot stay
+// in flight in half the registers (bf16).  B16: the row is known to be bf16.
+template <bool VEC, bool B16>
+struct Held8 {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void* row, int dtype, int i, int n) {
+        static_assert(VEC, "whole vectors");
+        if (i >= n) {
+            a = make_uint4(0, 0, 0, 0);
+            if (!B16) b = a;
+        } else if (B16 || dtype == QS_BF16) {
+            a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + i);
+        } else {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + i);
+            a = p[0];
+            b = p[1];
+        }
+    }
+    __device__ __forceinline__ void get(int dtype, float (&v)[8]) const {
+        if (B16 || dtype == QS_BF16) {
+            v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x);
+            v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
+            v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z);
+            v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+        } else {
+            v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+            v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+        }
+    }
+};
+template <>
+struct Held8<false, false> {  // any alignment: element by element
+    float f[8];
+    __device__ __forceinline__ void load(const void* row, int dtype, int i, int n) { load8_row<false>(row, dtype, i, n, f); }
+    __device__ __forceinline__ void get(int, float (&v)[8]) const {
+#pragma unroll
+        for (int q = 0; q < 8; q++) v[q] = f[q];
+    }
+};
 
 }  // namespace qs

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_place_kernel(const Disp
     // chunks before this one, and all of them
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int before = 0, all = 0;
-#pragma unroll 8
+#pragma unroll 16
         for (int c = 0; c < chunks; c++) {
             const int h = p.hist[(size_t)c * E + e];
             all += h;
@@ -220,19 +220,28 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(const DispatchArgs p
 
 constexpr int kBatch = 8;  // slots whose rows are in flight together
 
-template <bool VEC>
+// Rows in flight are held as they come (bf16: four registers each), half as many where they are fp32:
+// widened at once they took 86 registers, a quarter of the threads, and twice the time.
+template <bool VEC, bool B16>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs p) {
+    constexpr int kHeld = B16 ? kBatch : kBatch / 2;
     __shared__ int32_t at[32];
     __shared__ float w[32];
     const int64_t t = blockIdx.x;
     pdl_wait();
     pdl_launch_next();
-    if (threadIdx.x < p.top_k) {
-        const int64_t i = t * p.top_k + threadIdx.x;
-        const int a = p.pos[i];
-        // a position outside the rows is not read
-        at[threadIdx.x] = (unsigned)a < (unsigned)(p.n_tokens * p.top_k) ? a : -1;
-        w[threadIdx.x] = p.w ? p.w[i] : 1.0f;
+    if (threadIdx.x < 32) {
+        int a = -1;
+        float f = 0.0f;
+        if (threadIdx.x < p.top_k) {
+            const int64_t i = t * p.top_k + threadIdx.x;
+            a = p.pos[i];
+            // a position outside the rows is not read
+            if ((unsigned)a >= (unsigned)(p.n_tokens * p.top_k)) a = -1;
+            f = p.w ? p.w[i] : 1.0f;
+        }
+        at[threadIdx.x] = a;
+        w[threadIdx.x] = f;
     }
     __syncthreads();
     void* out = row_at(p.out, p.out_stride, type_size(p.out_dtype), t);
@@ -240,21 +249,21 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs p) {
         float acc[8];
 #pragma unroll
         for (int q = 0; q < 8; q++) acc[q] = 0.0f;
-        for (int j0 = 0; j0 < p.top_k; j0 += kBatch) {
-            float v[kBatch][8];
+        for (int j0 = 0; j0 < p.top_k; j0 += kHeld) {
+            Held8<VEC, B16> v[kHeld];
 #pragma unroll
-            for (int j = 0; j < kBatch; j++) {
-                const int a = j0 + j < p.top_k ? at[j0 + j] : -1;
-                load8_row<VEC>(row_at(p.y, p.y_stride, type_size(p.y_dtype), max(a, 0)), p.y_dtype, i,
-                               a >= 0 ? p.hidden : 0, v[j]);
+            for (int j = 0; j < kHeld; j++) {
+                const int a = at[j0 + j];
+                v[j].load(row_at(p.y, p.y_stride, type_size(p.y_dtype), max(a, 0)), p.y_dtype, i, a >= 0 ? p.hidden : 0);
             }
 #pragma unroll
-            for (int j = 0; j < kBatch; j++) {
-                const int a = j0 + j < p.top_k ? at[j0 + j] : -1;
-                if (a < 0) continue;  // a dropped entry adds nothing, whatever its weight is
+            for (int j = 0; j < kHeld; j++) {
+                if (at[j0 + j] < 0) continue;  // a dropped entry adds nothing, whatever its weight is
                 const float f = w[j0 + j];
+                float x[8];
+                v[j].get(p.y_dtype, x);
 #pragma unroll
-                for (int q = 0; q < 8; q++) acc[q] = fmaf(f, v[j][q], acc[q]);
+                for (int q = 0; q < 8; q++) acc[q] = fmaf(f, x[q], acc[q]);
             }
         }
         store8_row<VEC>(out, p.out_dtype, i, p.hidden, acc);
@@ -378,8 +387,10 @@ cudaError_t launch_combine(const CombineArgs& p, cudaStream_t st) {
     const int units = (p.hidden + 7) / 8;
     const unsigned block = p.n_tokens < 256 ? std::min(64u, row_threads(units)) : row_threads(units);
     const unsigned split = p.n_tokens < 256 ? (units + block - 1) / block : 1;
-    return vec ? launch_pdl(combine_kernel<true>, dim3(p.n_tokens, split), block, 0, st, p)
-               : launch_pdl(combine_kernel<false>, dim3(p.n_tokens, split), block, 0, st, p);
+    const dim3 grid(p.n_tokens, split);
+    if (!vec) return launch_pdl(combine_kernel<false, false>, grid, block, 0, st, p);
+    return p.y_dtype == QS_BF16 ? launch_pdl(combine_kernel<true, true>, grid, block, 0, st, p)
+                                : launch_pdl(combine_kernel<true, false>, grid, block, 0, st, p);
 }
 
 cudaError_t launch_combine_backward(const CombineBwdArgs& p, cudaStream_t st) {

@@ -349,9 +349,8 @@ int qs_test_wait_timeout(void *workspace, size_t workspace_bytes, int limit_us, 
  *    A row has ceil(cols / 128) scales; the last may cover fewer columns.
  *  - Codes are made as: per row and 128 columns amax = max(max |v|, 2^-100),
  *    scale = amax / 448, code = v / scale rounded to nearest, ties to even,
- *    v in fp32.  A NaN becomes the code of a NaN; an infinity makes its block's
- *    scale infinite, its own code a NaN and the block's finite values 0, so
- *    every value the block stands for is a NaN.
+ *    v in fp32.  A NaN becomes the code of a NaN and leaves its block's other
+ *    values alone; an infinity makes every value of its block a NaN.
  *  - n_rows or n_tokens == 0 is QS_OK; outputs that have no row per row of input
  *    (dweight, counts, offsets) are still written.
  *  - Input and output buffers must not overlap unless an entry says so.

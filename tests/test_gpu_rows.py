@@ -138,7 +138,7 @@ def test_norm_backward(hidden, rows, kind, with_dsum):
     want, size, dwant, dsize = bwd_ref(s, w, dy, dsum if with_dsum else None)
     # rho^3 carries three times rho's error, the mean over the row its own 48 U
     assert torch.all((dx.cpu().double() - want).abs() <= 160 * U * size + HALF[kind] * want.abs())
-    # a column's chain: rho, two products, the rows of a group (at most 2 here per group of 1024), 32 slices
+    # a column's chain: rho, two products, a group's rows (at most 3 here), the groups of a CTA, 32 slices of CTAs
     assert torch.all((dw.cpu().double() - dwant).abs() <= 160 * U * dsize)
     first = (dx.clone(), dw.clone())
     call()
@@ -409,3 +409,26 @@ def test_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, (total, xs.view(torch.uint8), ss, back, *out)))
+
+
+def test_infinities_and_nans_in_a_silu_block():
+    gu = torch.ones(3, 512, device="cuda")
+    gu[0, 300] = float("inf")   # up of column 44: block 0
+    gu[1, 5] = float("nan")
+    q, scale = codes(3, 256)
+    qm.qs_silu_mul_quant(gu, q, scale)
+    v = q.float() * scale.repeat_interleave(128, 1)
+    one = 1 / (1 + np.exp(-1.0))
+    assert torch.all(torch.isnan(v[0, :128])) and torch.all((v[0, 128:] - one).abs() <= one * 2.0 ** -4)
+    assert torch.isnan(v[1, 5]) and int(torch.isnan(v[1]).sum()) == 1 and torch.all((v[2] - one).abs() <= one * 2.0 ** -4)
+
+
+@pytest.mark.parametrize("size", [1e-37, 1e-30, 1e-20, 1e-8, 1e8, 1e15])
+@pytest.mark.parametrize("eps", [1e-12, 1e-5])
+def test_norm_codes_of_tiny_and_huge_rows(size, eps):
+    """The codes do not depend on how far the row's factor is from one."""
+    x, w = torch.randn(4, 640, generator=gen(3)) * size, torch.rand(640, generator=gen(4)) + 0.5
+    q, scale = codes(4, 640)
+    qm.qs_rmsnorm_residual(x.cuda(), None, w.cuda(), eps, q=q, q_scale=scale)
+    v = x.double() / torch.sqrt(x.double().pow(2).mean(1, keepdim=True) + float(np.float32(eps))) * w.double()
+    check_codes(q, scale, v, NORM_SLACK + U)
