@@ -51,56 +51,56 @@ __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_kernel(const NormAr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / G, wg = warp % G;
     const int64_t t = (int64_t)blockIdx.x * kGroups + group;
+    auto col = [&](int j) { return (j * 32 * G + wg * 32 + lane) * 8; };
     pdl_wait();
     pdl_launch_next();
     if (t >= p.n_rows) return;
     const void* xr = row_at(p.x, p.x_stride, type_size(p.x_dtype), t);
     const void* rr = p.residual ? row_at(p.residual, p.residual_stride, type_size(p.residual_dtype), t) : nullptr;
-    float s[NV][8];
+    float s[NV][1][8];
 #pragma unroll
-    for (int j = 0; j < NV; j++) load8_row<VEC>(xr, p.x_dtype, (j * 32 * G + wg * 32 + lane) * 8, p.hidden, s[j]);
+    for (int j = 0; j < NV; j++) load8_row<VEC>(xr, p.x_dtype, col(j), p.hidden, s[j][0]);
     if (rr) {
 #pragma unroll
         for (int j = 0; j < NV; j++) {
             float r[8];
-            load8_row<VEC>(rr, p.residual_dtype, (j * 32 * G + wg * 32 + lane) * 8, p.hidden, r);
+            load8_row<VEC>(rr, p.residual_dtype, col(j), p.hidden, r);
 #pragma unroll
-            for (int q = 0; q < 8; q++) s[j][q] += r[q];
+            for (int q = 0; q < 8; q++) s[j][0][q] += r[q];
         }
     }
     float ss[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; j++)
 #pragma unroll
-        for (int q = 0; q < 8; q++) ss[0] = fmaf(s[j][q], s[j][q], ss[0]);
+        for (int q = 0; q < 8; q++) ss[0] = fmaf(s[j][0][q], s[j][0][q], ss[0]);
     if (p.sum_out) {
         void* o = row_at(p.sum_out, p.sum_stride, type_size(p.sum_dtype), t);
 #pragma unroll
-        for (int j = 0; j < NV; j++)
-            store8_row<VEC>(o, p.sum_dtype, (j * 32 * G + wg * 32 + lane) * 8, p.hidden, s[j]);
+        for (int j = 0; j < NV; j++) store8_row<VEC>(o, p.sum_dtype, col(j), p.hidden, s[j][0]);
     }
     if (!p.y && !p.q) return;
     group_sum<G, 1>(ss, red[group], wg, lane, 1 + group);
     const float rho = rsqrtf(ss[0] / (float)p.hidden + p.eps);
+    void* yr = p.y ? row_at(p.y, p.y_stride, type_size(p.y_dtype), t) : nullptr;
     // rho is left to the end, where it costs the codes no rounding; rows so small that it is large take it at once
     const float factor = rho > 65536.0f ? 1.0f : rho, least = kMinAmax / factor;
-    void* yr = p.y ? row_at(p.y, p.y_stride, type_size(p.y_dtype), t) : nullptr;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
-        const int i = (j * 32 * G + wg * 32 + lane) * 8;
         float w[8];
-        load8_row<VEC>(p.weight, QS_F32, i, p.hidden, w);
+        load8_row<VEC>(p.weight, QS_F32, col(j), p.hidden, w);
 #pragma unroll
-        for (int q = 0; q < 8; q++) w[q] *= s[j][q];
+        for (int q = 0; q < 8; q++) s[j][0][q] *= w[q];
         if (rho != factor) {
 #pragma unroll
-            for (int q = 0; q < 8; q++) w[q] *= rho;
+            for (int q = 0; q < 8; q++) s[j][0][q] *= rho;
         }
-        if (p.q) quant8_row<VEC>(w, factor, least, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, i, p.hidden);
+        if (p.q)
+            quant_row<VEC, 1>(s[j], factor, least, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, col(j), p.hidden);
         if (yr) {
 #pragma unroll
-            for (int q = 0; q < 8; q++) w[q] *= factor;
-            store8_row<VEC>(yr, p.y_dtype, i, p.hidden, w);
+            for (int q = 0; q < 8; q++) s[j][0][q] *= factor;
+            store8_row<VEC>(yr, p.y_dtype, col(j), p.hidden, s[j][0]);
         }
     }
 }
@@ -118,18 +118,17 @@ __global__ void __launch_bounds__(32 * cta_warps(G), B16 && NV == 1 && G <= 8 ? 
     auto col = [&](int j) { return (j * 32 * G + wg * 32 + lane) * 8; };
     pdl_wait();
     pdl_launch_next();
-    Held8<VEC, B16> sh[NV], gh[NV], dh[NV];
-    auto load_sg = [&](int64_t t) {
+    struct Row {
+        Held8<VEC, B16> s[NV], g[NV], d[NV];
+    };
+    Row here, next;
+    auto load = [&](Row& r, int64_t t) {
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            sh[j].load(row_at(p.sum, p.sum_stride, type_size(p.sum_dtype), t), p.sum_dtype, col(j), p.hidden);
-            gh[j].load(row_at(p.dy, p.dy_stride, type_size(p.dy_dtype), t), p.dy_dtype, col(j), p.hidden);
+            r.s[j].load(row_at(p.sum, p.sum_stride, type_size(p.sum_dtype), t), p.sum_dtype, col(j), p.hidden);
+            r.g[j].load(row_at(p.dy, p.dy_stride, type_size(p.dy_dtype), t), p.dy_dtype, col(j), p.hidden);
+            if (p.dsum) r.d[j].load(row_at(p.dsum, p.dsum_stride, type_size(p.dsum_dtype), t), p.dsum_dtype, col(j), p.hidden);
         }
-    };
-    auto load_d = [&](int64_t t) {
-#pragma unroll
-        for (int j = 0; j < NV; j++)
-            dh[j].load(row_at(p.dsum, p.dsum_stride, type_size(p.dsum_dtype), t), p.dsum_dtype, col(j), p.hidden);
     };
     float dw[NV][8], w0[8];
 #pragma unroll
@@ -137,28 +136,22 @@ __global__ void __launch_bounds__(32 * cta_warps(G), B16 && NV == 1 && G <= 8 ? 
 #pragma unroll
         for (int q = 0; q < 8; q++) dw[j][q] = 0.0f;
     if (NV == 1) load8_row<VEC>(p.weight, QS_F32, col(0), p.hidden, w0);
-    if (first < p.n_rows) {
-        load_sg(first);
-        if (p.dsum) load_d(first);
-    }
+    if (first < p.n_rows) load(next, first);
     int flip = 0;
     for (int64_t t = first; t < p.n_rows; t += step, flip ^= 1) {
-        float s[NV][8], g[NV][8];
-#pragma unroll
-        for (int j = 0; j < NV; j++) {
-            sh[j].get(p.sum_dtype, s[j]);
-            gh[j].get(p.dy_dtype, g[j]);
-        }
-        if (t + step < p.n_rows) load_sg(t + step);
+        here = next;
+        if (t + step < p.n_rows) load(next, t + step);
         float a[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            float w[8];
+            float w[8], s[8], g[8];
             if (NV > 1) load8_row<VEC>(p.weight, QS_F32, col(j), p.hidden, w);
+            here.s[j].get(p.sum_dtype, s);
+            here.g[j].get(p.dy_dtype, g);
 #pragma unroll
             for (int q = 0; q < 8; q++) {
-                a[0] = fmaf(s[j][q], s[j][q], a[0]);
-                a[1] = fmaf((NV > 1 ? w[q] : w0[q]) * g[j][q], s[j][q], a[1]);
+                a[0] = fmaf(s[q], s[q], a[0]);
+                a[1] = fmaf((NV > 1 ? w[q] : w0[q]) * g[q], s[q], a[1]);
             }
         }
         group_sum<G, 2>(a, red[group][flip], wg, lane, 1 + group);
@@ -167,22 +160,23 @@ __global__ void __launch_bounds__(32 * cta_warps(G), B16 && NV == 1 && G <= 8 ? 
         void* o = row_at(p.dx, p.dx_stride, type_size(p.dx_dtype), t);
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            float w[8], d[8];
+            float w[8], s[8], g[8], d[8];
             if (NV > 1) load8_row<VEC>(p.weight, QS_F32, col(j), p.hidden, w);
+            here.s[j].get(p.sum_dtype, s);
+            here.g[j].get(p.dy_dtype, g);
             if (p.dsum) {
-                dh[j].get(p.dsum_dtype, d);
+                here.d[j].get(p.dsum_dtype, d);
             } else {
 #pragma unroll
                 for (int q = 0; q < 8; q++) d[q] = 0.0f;
             }
 #pragma unroll
             for (int q = 0; q < 8; q++) {
-                dw[j][q] = fmaf(g[j][q], s[j][q] * rho, dw[j][q]);
-                d[q] = fmaf(rho, (NV > 1 ? w[q] : w0[q]) * g[j][q], fmaf(-c, s[j][q], d[q]));
+                dw[j][q] = fmaf(g[q], s[q] * rho, dw[j][q]);
+                d[q] = fmaf(rho, (NV > 1 ? w[q] : w0[q]) * g[q], fmaf(-c, s[q], d[q]));
             }
             store8_row<VEC>(o, p.dx_dtype, col(j), p.hidden, d);
         }
-        if (p.dsum && t + step < p.n_rows) load_d(t + step);
     }
     if (!p.partial) return;
     // the CTA's groups in ascending order
@@ -226,37 +220,43 @@ __global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* __re
     if (lane == 0 && c < hidden) dweight[c] = v;
 }
 
-// silu(g) * u.  The quotient's 2 units in the last place (__fdividef; expf has 1) are 2^-22 of the value,
-// far inside its code's 2^-4; a true division here and one a value for the codes made the kernel wait for
-// instructions, 69 us against 25 us of memory time at 65536 x 512.  Past g = -87 the quotient is 0.
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
+// silu(g) * u.  __expf is off by at most 2 + 1.2 |g| units in the last place, which counts where g is negative and
+// exp(-g) large, and __fdividef by 2: under 2^-19 of the value for |g| <= 20, far inside its code's 2^-4.  With
+// expf and true divisions the kernel waited for instructions, 69 us against 25 us of memory time at 65536 x 512.
+// Past g = -87 the quotient is 0.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-// Sixteen lanes a (row, 128 columns): eight elements of gate and of up each.
+// Eight lanes a (row, 128 columns): sixteen elements of gate and of up each.
 template <bool VEC>
 __global__ void __launch_bounds__(256) silu_mul_quant_kernel(const SiluArgs p) {
     pdl_wait();
     pdl_launch_next();
     const unsigned nb = scale_blocks(p.ffn);
-    const unsigned half = threadIdx.x >> 4, l = threadIdx.x & 15;
+    const unsigned part = threadIdx.x >> 3, l = threadIdx.x & 7;
     int64_t rows = p.n_rows;
     if (p.n_rows_dev) rows = min(rows, (int64_t)max(*p.n_rows_dev, 0));
-    // (row, block) of this half warp, and the step to its next: the grid is small enough for 32 bits
-    const unsigned u0 = blockIdx.x * 16 + half, du = gridDim.x * 16;
+    // (row, block) of these eight lanes, and the step to their next: the grid is small enough for 32 bits
+    const unsigned u0 = blockIdx.x * 32 + part, du = gridDim.x * 32;
     int64_t t = u0 / nb;
     unsigned b = u0 % nb;
     const unsigned dt = du / nb, db = du % nb;
-    // both halves of a warp run the shuffles as long as one has work
+    // a warp's four parts all run the shuffles as long as one has work
     while (__any_sync(0xffffffffu, t < rows)) {
         const bool on = t < rows;
-        const int i = (int)(b * kScaleCols + l * 8);
+        const int i = (int)(b * kScaleCols + l * 16);
         const int n = on ? p.ffn : 0;
-        const uint8_t* row = static_cast<const uint8_t*>(row_at(p.gate_up, p.gate_up_stride, type_size(p.dtype), t));
-        float g[8], v[8];
-        load8_row<VEC>(row, p.dtype, i, n, g);
-        load8_row<VEC>(row + (size_t)p.ffn * type_size(p.dtype), p.dtype, i, n, v);
+        const uint8_t* row = static_cast<const uint8_t*>(row_at(p.gate_up, p.gate_up_stride, type_size(p.dtype), on ? t : 0));
+        float g[2][8], v[2][8];
 #pragma unroll
-        for (int q = 0; q < 8; q++) v[q] = silu_mul(g[q], v[q]);
-        quant8_row<VEC>(v, 1.0f, kMinAmax, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, i, n);
+        for (int k = 0; k < 2; k++) {
+            load8_row<VEC>(row, p.dtype, i + 8 * k, n, g[k]);
+            load8_row<VEC>(row + (size_t)p.ffn * type_size(p.dtype), p.dtype, i + 8 * k, n, v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+#pragma unroll
+            for (int q = 0; q < 8; q++) v[k][q] = silu_mul(g[k][q], v[k][q]);
+        quant_row<VEC, 2>(v, 1.0f, kMinAmax, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, i, n);
         t += dt;
         b += db;
         if (b >= nb) {
@@ -292,8 +292,8 @@ cudaError_t norm_run(const NormArgs& p, cudaStream_t st) {
 
 template <bool VEC>
 cudaError_t norm_pick(const NormArgs& p, cudaStream_t st) {
-    // sixteen elements a thread keep four loads of 16 bytes in flight and full occupancy; more only
-    // for rows past 4096 (groups of more than 8 warps cost a wider barrier)
+    // two steps a thread keep four loads of 16 bytes in flight; more only for rows past 8192.  (Sixteen
+    // neighbouring elements a thread, which share a block's maximum, took 90 us against 85 at 16384 x 4096.)
     if (p.hidden <= 256) return norm_run<VEC, 1, 1>(p, st);
     if (p.hidden <= 512) return norm_run<VEC, 1, 2>(p, st);
     if (p.hidden <= 1024) return norm_run<VEC, 2, 2>(p, st);
@@ -354,7 +354,7 @@ cudaError_t launch_silu_mul_quant(const SiluArgs& p, cudaStream_t st) {
     const bool vec = p.ffn % 8 == 0 && al16(p.gate_up, p.gate_up_stride, p.dtype) &&
                      (p.ffn * type_size(p.dtype)) % 16 == 0 && ((uintptr_t)p.q & 7u) == 0 && p.q_stride % 8 == 0;
     const int64_t work = (int64_t)p.n_rows * scale_blocks(p.ffn);
-    const unsigned grid = (unsigned)std::min<int64_t>((work + 15) / 16, 65536);
+    const unsigned grid = (unsigned)std::min<int64_t>((work + 31) / 32, 1216);  // eight CTAs an SM walk on: 37 us against 47 with one step each
     return vec ? launch_pdl(silu_mul_quant_kernel<true>, grid, 256, st, p)
                : launch_pdl(silu_mul_quant_kernel<false>, grid, 256, st, p);
 }

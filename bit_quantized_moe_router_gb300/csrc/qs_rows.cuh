@@ -85,38 +85,44 @@ __device__ __forceinline__ void* row_at(void* base, int64_t stride, int size, in
 }
 __host__ __device__ constexpr int type_size(int dtype) { return dtype == QS_F32 ? 4 : dtype == QS_BF16 ? 2 : 1; }
 
-// Sixteen lanes that hold the 128 columns of one scale block, eight each (columns i .. i+7; those
+// The 16 / N lanes that hold the 128 columns of one scale block, 8 N each (columns i .. i + 8 N - 1; those
 // past n hold 0), of values v * factor with one factor for the row: the block's scale, and the lane's codes.
 // The factor drops out of a code, v * factor * (448 / (amax * factor)), so it is left out of it; 448 / amax is held
 // in two parts (its fp32 value and what that rounding left out), and a code's product has one rounding.
 // least: kMinAmax / factor.  fmaxf drops a NaN: its own code is a NaN and the others of its block keep their
 // scale.  An infinite amax leaves no remainder: all codes of the block are NaNs.
-template <bool VEC>
-__device__ __forceinline__ void quant8_row(const float (&v)[8], float factor, float least, uint8_t* q_row, float* scale_row,
-                                           int i, int n) {
+template <bool VEC, int N>
+__device__ __forceinline__ void quant_row(const float (&v)[N][8], float factor, float least, uint8_t* q_row, float* scale_row,
+                                          int i, int n) {
     float a = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(v[q]));
+    for (int k = 0; k < N; k++)
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(v[k][q]));
+#pragma unroll
+    for (int o = kScaleCols / (16 * N); o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     a = fmaxf(a, least);
     const float amax = a * factor, part = __frcp_rn(a), inv = kE4m3Max * part, rest = fmaf(-inv, a, kE4m3Max) * part;
     const auto scaled = [&](float x) { return fmaf(x, inv, x * rest); };
     if (i >= n) return;
     if (i % kScaleCols == 0) scale_row[i / kScaleCols] = amax * (1.0f / kE4m3Max);
-    uint32_t w[2];
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(scaled(v[4 * h]), scaled(v[4 * h + 1])), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(scaled(v[4 * h + 2]), scaled(v[4 * h + 3])), __NV_SATFINITE, __NV_E4M3);
-        w[h] = lo | (hi << 16);
-    }
-    if (VEC) {
-        *reinterpret_cast<uint2*>(q_row + i) = make_uint2(w[0], w[1]);
-    } else {
+    for (int k = 0; k < N; k++) {
+        uint32_t w[2];
 #pragma unroll
-        for (int q = 0; q < 8; q++)
-            if (i + q < n) q_row[i + q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
+        for (int h = 0; h < 2; h++) {
+            const float* x = &v[k][4 * h];
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(scaled(x[0]), scaled(x[1])), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(scaled(x[2]), scaled(x[3])), __NV_SATFINITE, __NV_E4M3);
+            w[h] = lo | (hi << 16);
+        }
+        if (VEC) {
+            if (i + 8 * k < n) *reinterpret_cast<uint2*>(q_row + i + 8 * k) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; q++)
+                if (i + 8 * k + q < n) q_row[i + 8 * k + q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
+        }
     }
 }
 
