@@ -201,7 +201,6 @@ struct Fp8MmArgs {
     const float* w_scale;
     const int32_t* offsets;
     void* out;
-    uint32_t* status;
     int64_t a_stride, a_scale_stride, w_stride, w_expert_stride, out_stride;
     int n_experts, n_rows, n_cols, n_inner, out_dtype;
 };

@@ -10,13 +10,15 @@ bool wide_type(int dtype) { return dtype == QS_F32 || dtype == QS_BF16; }
 
 // A matrix of fp32 or bf16 rows: there, aligned to its elements, rows not longer than their stride
 // (one row may have any stride).  A matrix without rows may have no address.
-bool rows_ok(const void* p, int64_t stride, int dtype, int n_rows, int cols) {
-    return (p || n_rows == 0) && wide_type(dtype) && ((uintptr_t)p % type_size(dtype)) == 0 && (stride >= cols || (n_rows <= 1 && stride >= 0));
+bool rows_ok(const qs_rows& m, int n_rows, int cols) {
+    return (m.data || n_rows == 0) && wide_type(m.dtype) && ((uintptr_t)m.data % type_size(m.dtype)) == 0 &&
+           (m.stride >= cols || (n_rows <= 1 && m.stride >= 0));
 }
-bool codes_ok(const void* q, int64_t stride, const float* scale, int64_t scale_stride, int n_rows, int cols) {
+bool codes_ok(const qs_codes& m, int n_rows, int cols) {
     const bool one = n_rows <= 1;
-    return ((q && scale) || n_rows == 0) && ((uintptr_t)scale & 3u) == 0 && (stride >= cols || (one && stride >= 0)) &&
-           (scale_stride >= scale_blocks(cols) || (one && scale_stride >= 0));
+    return ((m.q && m.scale) || n_rows == 0) && ((uintptr_t)m.scale & 3u) == 0 &&
+           (m.stride >= cols || (one && m.stride >= 0)) &&
+           (m.scale_stride >= scale_blocks(cols) || (one && m.scale_stride >= 0));
 }
 bool eps_ok(float eps) { return eps >= 0.0f && eps <= 3.0e38f; }
 bool entries_ok(int n_tokens, int top_k) {
@@ -29,38 +31,38 @@ size_t norm_parts_bytes(int hidden) { return (size_t)kNormParts * ((hidden + 7) 
 
 extern "C" {
 
-int qs_rmsnorm_residual(const void* x, int64_t x_stride, int x_dtype, const void* residual, int64_t residual_stride,
-                        int residual_dtype, const float* weight, float eps, int n_rows, int hidden, void* sum_out,
-                        int64_t sum_stride, int sum_dtype, void* y, int64_t y_stride, int y_dtype, void* q,
-                        int64_t q_stride, float* q_scale, int64_t q_scale_stride, void* stream) {
-    if (n_rows < 0 || hidden < 1 || hidden > kNormMaxHidden || !eps_ok(eps)) return QS_ERR_INVALID;
-    if (!rows_ok(x, x_stride, x_dtype, n_rows, hidden) || !weight || ((uintptr_t)weight & 3u)) return QS_ERR_INVALID;
-    if (residual && !rows_ok(residual, residual_stride, residual_dtype, n_rows, hidden)) return QS_ERR_INVALID;
-    if (sum_out && !rows_ok(sum_out, sum_stride, sum_dtype, n_rows, hidden)) return QS_ERR_INVALID;
-    if (y && !rows_ok(y, y_stride, y_dtype, n_rows, hidden)) return QS_ERR_INVALID;
-    if ((q || q_scale) && !codes_ok(q, q_stride, q_scale, q_scale_stride, n_rows, hidden)) return QS_ERR_INVALID;
-    if (n_rows > 0 && !sum_out && !y && !q) return QS_ERR_INVALID;
+int qs_rmsnorm_residual(const qs_rmsnorm_args* args, void* stream) {
+    if (!args) return QS_ERR_INVALID;
+    const qs_rmsnorm_args& a = *args;
+    const int n = a.n_rows, h = a.hidden;
+    if (n < 0 || h < 1 || h > kNormMaxHidden || !eps_ok(a.eps)) return QS_ERR_INVALID;
+    if (!rows_ok(a.x, n, h) || !a.weight || ((uintptr_t)a.weight & 3u)) return QS_ERR_INVALID;
+    if (a.residual.data && !rows_ok(a.residual, n, h)) return QS_ERR_INVALID;
+    if (a.sum_out.data && !rows_ok(a.sum_out, n, h)) return QS_ERR_INVALID;
+    if (a.y.data && !rows_ok(a.y, n, h)) return QS_ERR_INVALID;
+    if ((a.q.q || a.q.scale) && !codes_ok(a.q, n, h)) return QS_ERR_INVALID;
+    if (n > 0 && !a.sum_out.data && !a.y.data && !a.q.q) return QS_ERR_INVALID;
     NormArgs p = {};
-    p.x = x;
-    p.residual = residual;
-    p.weight = weight;
-    p.sum_out = sum_out;
-    p.y = y;
-    p.q = static_cast<uint8_t*>(q);
-    p.q_scale = q_scale;
-    p.x_stride = x_stride;
-    p.residual_stride = residual_stride;
-    p.sum_stride = sum_stride;
-    p.y_stride = y_stride;
-    p.q_stride = q_stride;
-    p.q_scale_stride = q_scale_stride;
-    p.x_dtype = x_dtype;
-    p.residual_dtype = residual_dtype;
-    p.sum_dtype = sum_dtype;
-    p.y_dtype = y_dtype;
-    p.n_rows = n_rows;
-    p.hidden = hidden;
-    p.eps = eps;
+    p.x = a.x.data;
+    p.residual = a.residual.data;
+    p.weight = a.weight;
+    p.sum_out = a.sum_out.data;
+    p.y = a.y.data;
+    p.q = static_cast<uint8_t*>(a.q.q);
+    p.q_scale = a.q.scale;
+    p.x_stride = a.x.stride;
+    p.residual_stride = a.residual.stride;
+    p.sum_stride = a.sum_out.stride;
+    p.y_stride = a.y.stride;
+    p.q_stride = a.q.stride;
+    p.q_scale_stride = a.q.scale_stride;
+    p.x_dtype = a.x.dtype;
+    p.residual_dtype = a.residual.dtype;
+    p.sum_dtype = a.sum_out.dtype;
+    p.y_dtype = a.y.dtype;
+    p.n_rows = n;
+    p.hidden = h;
+    p.eps = a.eps;
     return done(launch_rmsnorm(p, (cudaStream_t)stream));
 }
 
@@ -68,57 +70,55 @@ size_t qs_rmsnorm_backward_workspace_bytes(int hidden) {
     return hidden < 1 || hidden > kNormMaxHidden ? 0 : norm_parts_bytes(hidden);
 }
 
-int qs_rmsnorm_residual_backward(const void* sum, int64_t sum_stride, int sum_dtype, const float* weight, float eps,
-                                 const void* dy, int64_t dy_stride, int dy_dtype, const void* dsum,
-                                 int64_t dsum_stride, int dsum_dtype, int n_rows, int hidden, void* dx,
-                                 int64_t dx_stride, int dx_dtype, float* dweight, void* workspace,
-                                 size_t workspace_bytes, void* stream) {
-    if (n_rows < 0 || hidden < 1 || hidden > kNormMaxHidden || !eps_ok(eps)) return QS_ERR_INVALID;
-    if (!rows_ok(sum, sum_stride, sum_dtype, n_rows, hidden) || !weight || ((uintptr_t)weight & 3u)) return QS_ERR_INVALID;
-    if (!rows_ok(dy, dy_stride, dy_dtype, n_rows, hidden)) return QS_ERR_INVALID;
-    if (dsum && !rows_ok(dsum, dsum_stride, dsum_dtype, n_rows, hidden)) return QS_ERR_INVALID;
-    if (!rows_ok(dx, dx_stride, dx_dtype, n_rows, hidden) || ((uintptr_t)dweight & 3u)) return QS_ERR_INVALID;
-    if (dweight && (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < norm_parts_bytes(hidden)))
+int qs_rmsnorm_residual_backward(const qs_rmsnorm_backward_args* args, void* stream) {
+    if (!args) return QS_ERR_INVALID;
+    const qs_rmsnorm_backward_args& a = *args;
+    const int n = a.n_rows, h = a.hidden;
+    if (n < 0 || h < 1 || h > kNormMaxHidden || !eps_ok(a.eps)) return QS_ERR_INVALID;
+    if (!rows_ok(a.sum, n, h) || !a.weight || ((uintptr_t)a.weight & 3u) || !rows_ok(a.dy, n, h)) return QS_ERR_INVALID;
+    if (a.dsum.data && !rows_ok(a.dsum, n, h)) return QS_ERR_INVALID;
+    if (!rows_ok(a.dx, n, h) || ((uintptr_t)a.dweight & 3u)) return QS_ERR_INVALID;
+    if (a.dweight && (!a.workspace || ((uintptr_t)a.workspace & 255u) || a.workspace_bytes < norm_parts_bytes(h)))
         return QS_ERR_WORKSPACE;
     NormBwdArgs p = {};
-    p.sum = sum;
-    p.weight = weight;
-    p.dy = dy;
-    p.dsum = dsum;
-    p.dx = dx;
-    p.partial = dweight ? static_cast<float*>(workspace) : nullptr;
-    p.sum_stride = sum_stride;
-    p.dy_stride = dy_stride;
-    p.dsum_stride = dsum_stride;
-    p.dx_stride = dx_stride;
-    p.sum_dtype = sum_dtype;
-    p.dy_dtype = dy_dtype;
-    p.dsum_dtype = dsum_dtype;
-    p.dx_dtype = dx_dtype;
-    p.n_rows = n_rows;
-    p.hidden = hidden;
-    p.part_stride = (hidden + 7) / 8 * 8;
-    p.eps = eps;
-    return done(launch_rmsnorm_backward(p, dweight, (cudaStream_t)stream));
+    p.sum = a.sum.data;
+    p.weight = a.weight;
+    p.dy = a.dy.data;
+    p.dsum = a.dsum.data;
+    p.dx = a.dx.data;
+    p.partial = a.dweight ? static_cast<float*>(a.workspace) : nullptr;
+    p.sum_stride = a.sum.stride;
+    p.dy_stride = a.dy.stride;
+    p.dsum_stride = a.dsum.stride;
+    p.dx_stride = a.dx.stride;
+    p.sum_dtype = a.sum.dtype;
+    p.dy_dtype = a.dy.dtype;
+    p.dsum_dtype = a.dsum.dtype;
+    p.dx_dtype = a.dx.dtype;
+    p.n_rows = n;
+    p.hidden = h;
+    p.part_stride = (h + 7) / 8 * 8;
+    p.eps = a.eps;
+    return done(launch_rmsnorm_backward(p, a.dweight, (cudaStream_t)stream));
 }
 
-int qs_silu_mul_quant(const void* gate_up, int64_t gate_up_stride, int gate_up_dtype, int n_rows,
-                      const int32_t* n_rows_dev, int ffn, void* q, int64_t q_stride, float* q_scale,
-                      int64_t q_scale_stride, void* stream) {
-    if (n_rows < 0 || ffn < 1 || ffn > (1 << 24)) return QS_ERR_INVALID;
-    if (!rows_ok(gate_up, gate_up_stride, gate_up_dtype, n_rows, 2 * ffn)) return QS_ERR_INVALID;
-    if (!codes_ok(q, q_stride, q_scale, q_scale_stride, n_rows, ffn) || ((uintptr_t)n_rows_dev & 3u)) return QS_ERR_INVALID;
+int qs_silu_mul_quant(const qs_silu_mul_args* args, void* stream) {
+    if (!args) return QS_ERR_INVALID;
+    const qs_silu_mul_args& a = *args;
+    if (a.n_rows < 0 || a.ffn < 1 || a.ffn > (1 << 24)) return QS_ERR_INVALID;
+    if (!rows_ok(a.gate_up, a.n_rows, 2 * a.ffn) || !codes_ok(a.q, a.n_rows, a.ffn)) return QS_ERR_INVALID;
+    if ((uintptr_t)a.n_rows_dev & 3u) return QS_ERR_INVALID;
     SiluArgs p = {};
-    p.gate_up = gate_up;
-    p.n_rows_dev = n_rows_dev;
-    p.q = static_cast<uint8_t*>(q);
-    p.q_scale = q_scale;
-    p.gate_up_stride = gate_up_stride;
-    p.q_stride = q_stride;
-    p.q_scale_stride = q_scale_stride;
-    p.dtype = gate_up_dtype;
-    p.n_rows = n_rows;
-    p.ffn = ffn;
+    p.gate_up = a.gate_up.data;
+    p.n_rows_dev = a.n_rows_dev;
+    p.q = static_cast<uint8_t*>(a.q.q);
+    p.q_scale = a.q.scale;
+    p.gate_up_stride = a.gate_up.stride;
+    p.q_stride = a.q.stride;
+    p.q_scale_stride = a.q.scale_stride;
+    p.dtype = a.gate_up.dtype;
+    p.n_rows = a.n_rows;
+    p.ffn = a.ffn;
     return done(launch_silu_mul_quant(p, (cudaStream_t)stream));
 }
 
@@ -131,43 +131,40 @@ size_t qs_fp8_matmul_workspace_bytes(int n_rows, int n_cols, int n_inner, int n_
     return matmul_shape_ok(n_rows, n_cols, n_inner, n_experts) ? fp8_matmul_workspace(n_rows, n_cols, n_inner, n_experts) : 0;
 }
 
-int qs_fp8_matmul(const void* a, int64_t a_stride, const float* a_scale, int64_t a_scale_stride, const void* w,
-                  int64_t w_stride, int64_t w_expert_stride, const float* w_scale, const int32_t* offsets,
-                  int n_experts, int n_rows, int n_cols, int n_inner, void* out, int64_t out_stride, int out_dtype,
-                  void* workspace, size_t workspace_bytes, void* stream) {
-    if (!matmul_shape_ok(n_rows, n_cols, n_inner, n_experts) || (!offsets && n_experts != 1)) return QS_ERR_INVALID;
+int qs_fp8_matmul(const qs_fp8_matmul_args* args, void* stream) {
+    if (!args) return QS_ERR_INVALID;
+    const qs_fp8_matmul_args& a = *args;
+    const int m = a.n_rows, n = a.n_cols, k = a.n_inner, e = a.n_experts;
+    if (!matmul_shape_ok(m, n, k, e) || (!a.offsets && e != 1)) return QS_ERR_INVALID;
     // the strides are a tensor map's: multiples of 16 bytes below 2^40, also where there is one row
     const int64_t top = 1ll << 40;
-    if (!codes_ok(a, a_stride, a_scale, a_scale_stride, n_rows, n_inner) || ((uintptr_t)a & 15u) || a_stride % 16 ||
-        a_stride < n_inner || a_stride >= top)
+    if (!codes_ok(a.a, m, k) || ((uintptr_t)a.a.q & 15u) || a.a.stride % 16 || a.a.stride < k || a.a.stride >= top)
         return QS_ERR_INVALID;
-    if (!w || !w_scale || ((uintptr_t)w & 15u) || ((uintptr_t)w_scale & 3u) || w_stride % 16 || w_stride < n_inner ||
-        w_stride >= top || w_expert_stride % 16 || w_expert_stride >= top ||
-        w_expert_stride < (n_experts > 1 ? w_stride * (n_cols - 1) + n_inner : 0) || ((uintptr_t)offsets & 3u))
+    if (!a.w || !a.w_scale || ((uintptr_t)a.w & 15u) || ((uintptr_t)a.w_scale & 3u) || a.w_stride % 16 ||
+        a.w_stride < k || a.w_stride >= top || a.w_expert_stride % 16 || a.w_expert_stride >= top ||
+        a.w_expert_stride < (e > 1 ? a.w_stride * (n - 1) + k : 0) || ((uintptr_t)a.offsets & 3u))
         return QS_ERR_INVALID;
-    if (!rows_ok(out, out_stride, out_dtype, n_rows, n_cols)) return QS_ERR_INVALID;
-    if (!workspace || ((uintptr_t)workspace & 255u) ||
-        workspace_bytes < fp8_matmul_workspace(n_rows, n_cols, n_inner, n_experts))
+    if (!rows_ok(a.out, m, n)) return QS_ERR_INVALID;
+    if (!a.workspace || ((uintptr_t)a.workspace & 255u) || a.workspace_bytes < fp8_matmul_workspace(m, n, k, e))
         return QS_ERR_WORKSPACE;
     Fp8MmArgs p = {};
-    p.a = a;
-    p.a_scale = a_scale;
-    p.w = w;
-    p.w_scale = w_scale;
-    p.offsets = offsets;
-    p.out = out;
-    p.status = static_cast<uint32_t*>(workspace);
-    p.a_stride = a_stride;
-    p.a_scale_stride = a_scale_stride;
-    p.w_stride = w_stride;
-    p.w_expert_stride = n_experts > 1 ? w_expert_stride : w_stride;
-    p.out_stride = out_stride;
-    p.n_experts = n_experts;
-    p.n_rows = n_rows;
-    p.n_cols = n_cols;
-    p.n_inner = n_inner;
-    p.out_dtype = out_dtype;
-    return done(launch_fp8_matmul(p, workspace, (cudaStream_t)stream));
+    p.a = a.a.q;
+    p.a_scale = a.a.scale;
+    p.w = a.w;
+    p.w_scale = a.w_scale;
+    p.offsets = a.offsets;
+    p.out = a.out.data;
+    p.a_stride = a.a.stride;
+    p.a_scale_stride = a.a.scale_stride;
+    p.w_stride = a.w_stride;
+    p.w_expert_stride = e > 1 ? a.w_expert_stride : a.w_stride;
+    p.out_stride = a.out.stride;
+    p.n_experts = e;
+    p.n_rows = m;
+    p.n_cols = n;
+    p.n_inner = k;
+    p.out_dtype = a.out.dtype;
+    return done(launch_fp8_matmul(p, a.workspace, (cudaStream_t)stream));
 }
 
 size_t qs_dispatch_workspace_bytes(int n_tokens, int top_k, int n_experts) {
@@ -176,98 +173,97 @@ size_t qs_dispatch_workspace_bytes(int n_tokens, int top_k, int n_experts) {
                : 0;
 }
 
-int qs_dispatch_tokens(const int32_t* topk_ids, int n_tokens, int top_k, int n_experts, int32_t* counts,
-                       int32_t* offsets, int32_t* perm, int32_t* pos, const void* x, int64_t x_stride, int x_dtype,
-                       const float* x_scale, int64_t x_scale_stride, int hidden, void* xs, int64_t xs_stride,
-                       float* xs_scale, int64_t xs_scale_stride, void* workspace, size_t workspace_bytes,
-                       void* stream) {
-    if (!entries_ok(n_tokens, top_k) || n_experts < 1 || n_experts > 1024) return QS_ERR_INVALID;
-    if (!counts || !offsets || (n_tokens > 0 && (!topk_ids || !perm || !pos))) return QS_ERR_INVALID;
-    if (((uintptr_t)topk_ids | (uintptr_t)counts | (uintptr_t)offsets | (uintptr_t)perm | (uintptr_t)pos) & 3u)
+int qs_dispatch_tokens(const qs_dispatch_args* args, void* stream) {
+    if (!args) return QS_ERR_INVALID;
+    const qs_dispatch_args& a = *args;
+    if (!entries_ok(a.n_tokens, a.top_k) || a.n_experts < 1 || a.n_experts > 1024) return QS_ERR_INVALID;
+    if (!a.counts || !a.offsets || (a.n_tokens > 0 && (!a.topk_ids || !a.perm || !a.pos))) return QS_ERR_INVALID;
+    if (((uintptr_t)a.topk_ids | (uintptr_t)a.counts | (uintptr_t)a.offsets | (uintptr_t)a.perm | (uintptr_t)a.pos) & 3u)
         return QS_ERR_INVALID;
     DispatchArgs p = {};
-    if (xs) {
-        const int n = n_tokens * top_k;
-        if (hidden < 1 || hidden > (1 << 24)) return QS_ERR_INVALID;
-        if (x_dtype == QS_E4M3) {
-            if (!codes_ok(x, x_stride, x_scale, x_scale_stride, n_tokens, hidden) ||
-                !codes_ok(xs, xs_stride, xs_scale, xs_scale_stride, n, hidden))
-                return QS_ERR_INVALID;
-            p.n_scales = scale_blocks(hidden);
-        } else if (!rows_ok(x, x_stride, x_dtype, n_tokens, hidden) || !rows_ok(xs, xs_stride, x_dtype, n, hidden)) {
+    if (a.xs.data) {
+        const int n = a.n_tokens * a.top_k;
+        if (a.hidden < 1 || a.hidden > (1 << 24) || a.x.dtype != a.xs.dtype) return QS_ERR_INVALID;
+        if (a.x.dtype == QS_E4M3) {
+            const qs_codes x = {a.x.data, a.x.stride, const_cast<float*>(a.x_scale), a.x_scale_stride};
+            const qs_codes xs = {a.xs.data, a.xs.stride, a.xs_scale, a.xs_scale_stride};
+            if (!codes_ok(x, a.n_tokens, a.hidden) || !codes_ok(xs, n, a.hidden)) return QS_ERR_INVALID;
+            p.n_scales = scale_blocks(a.hidden);
+        } else if (!rows_ok(a.x, a.n_tokens, a.hidden) || !rows_ok(a.xs, n, a.hidden)) {
             return QS_ERR_INVALID;
         }
-        p.row_bytes = hidden * type_size(x_dtype);
-        p.x_stride = x_stride * type_size(x_dtype);
-        p.xs_stride = xs_stride * type_size(x_dtype);
+        p.row_bytes = a.hidden * type_size(a.x.dtype);
+        p.x_stride = a.x.stride * type_size(a.x.dtype);
+        p.xs_stride = a.xs.stride * type_size(a.x.dtype);
     }
-    if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < dispatch_workspace(n_tokens, top_k, n_experts))
+    if (!a.workspace || ((uintptr_t)a.workspace & 255u) ||
+        a.workspace_bytes < dispatch_workspace(a.n_tokens, a.top_k, a.n_experts))
         return QS_ERR_WORKSPACE;
-    p.ids = topk_ids;
-    p.counts = counts;
-    p.offsets = offsets;
-    p.perm = perm;
-    p.pos = pos;
-    p.x = x;
-    p.xs = xs;
-    p.x_scale = x_scale;
-    p.xs_scale = xs_scale;
-    p.hist = static_cast<int32_t*>(workspace);
-    p.x_scale_stride = x_scale_stride;
-    p.xs_scale_stride = xs_scale_stride;
-    p.n_tokens = n_tokens;
-    p.top_k = top_k;
-    p.n_experts = n_experts;
+    p.ids = a.topk_ids;
+    p.counts = a.counts;
+    p.offsets = a.offsets;
+    p.perm = a.perm;
+    p.pos = a.pos;
+    p.x = a.x.data;
+    p.xs = a.xs.data;
+    p.x_scale = a.x_scale;
+    p.xs_scale = a.xs_scale;
+    p.hist = static_cast<int32_t*>(a.workspace);
+    p.x_scale_stride = a.x_scale_stride;
+    p.xs_scale_stride = a.xs_scale_stride;
+    p.n_tokens = a.n_tokens;
+    p.top_k = a.top_k;
+    p.n_experts = a.n_experts;
     return done(launch_dispatch(p, (cudaStream_t)stream));
 }
 
-int qs_combine_tokens(const void* y, int64_t y_stride, int y_dtype, const int32_t* pos, const float* topk_w,
-                      int n_tokens, int top_k, int hidden, void* out, int64_t out_stride, int out_dtype,
-                      void* stream) {
-    if (!entries_ok(n_tokens, top_k) || hidden < 1 || hidden > (1 << 24) || (!pos && n_tokens > 0)) return QS_ERR_INVALID;
-    if (((uintptr_t)pos | (uintptr_t)topk_w) & 3u) return QS_ERR_INVALID;
-    if (!rows_ok(y, y_stride, y_dtype, n_tokens * top_k, hidden) || !rows_ok(out, out_stride, out_dtype, n_tokens, hidden))
+int qs_combine_tokens(const qs_combine_args* args, void* stream) {
+    if (!args) return QS_ERR_INVALID;
+    const qs_combine_args& a = *args;
+    if (!entries_ok(a.n_tokens, a.top_k) || a.hidden < 1 || a.hidden > (1 << 24) || (!a.pos && a.n_tokens > 0))
         return QS_ERR_INVALID;
+    if (((uintptr_t)a.pos | (uintptr_t)a.topk_w) & 3u) return QS_ERR_INVALID;
+    if (!rows_ok(a.y, a.n_tokens * a.top_k, a.hidden) || !rows_ok(a.out, a.n_tokens, a.hidden)) return QS_ERR_INVALID;
     CombineArgs p = {};
-    p.y = y;
-    p.pos = pos;
-    p.w = topk_w;
-    p.out = out;
-    p.y_stride = y_stride;
-    p.out_stride = out_stride;
-    p.y_dtype = y_dtype;
-    p.out_dtype = out_dtype;
-    p.n_tokens = n_tokens;
-    p.top_k = top_k;
-    p.hidden = hidden;
+    p.y = a.y.data;
+    p.pos = a.pos;
+    p.w = a.topk_w;
+    p.out = a.out.data;
+    p.y_stride = a.y.stride;
+    p.out_stride = a.out.stride;
+    p.y_dtype = a.y.dtype;
+    p.out_dtype = a.out.dtype;
+    p.n_tokens = a.n_tokens;
+    p.top_k = a.top_k;
+    p.hidden = a.hidden;
     return done(launch_combine(p, (cudaStream_t)stream));
 }
 
-int qs_combine_tokens_backward(const void* dout, int64_t dout_stride, int dout_dtype, const void* y, int64_t y_stride,
-                               int y_dtype, const int32_t* pos, const float* topk_w, int n_tokens, int top_k,
-                               int hidden, void* dy, int64_t dy_stride, int dy_dtype, float* dtopk_w, void* stream) {
-    if (!entries_ok(n_tokens, top_k) || hidden < 1 || hidden > (1 << 24) || (!pos && n_tokens > 0)) return QS_ERR_INVALID;
-    if (((uintptr_t)pos | (uintptr_t)topk_w | (uintptr_t)dtopk_w) & 3u) return QS_ERR_INVALID;
-    const int n = n_tokens * top_k;
-    if (!rows_ok(dout, dout_stride, dout_dtype, n_tokens, hidden) || !rows_ok(dy, dy_stride, dy_dtype, n, hidden))
+int qs_combine_tokens_backward(const qs_combine_backward_args* args, void* stream) {
+    if (!args) return QS_ERR_INVALID;
+    const qs_combine_backward_args& a = *args;
+    if (!entries_ok(a.n_tokens, a.top_k) || a.hidden < 1 || a.hidden > (1 << 24) || (!a.pos && a.n_tokens > 0))
         return QS_ERR_INVALID;
-    if (dtopk_w && !rows_ok(y, y_stride, y_dtype, n, hidden)) return QS_ERR_INVALID;
+    if (((uintptr_t)a.pos | (uintptr_t)a.topk_w | (uintptr_t)a.dtopk_w) & 3u) return QS_ERR_INVALID;
+    const int n = a.n_tokens * a.top_k;
+    if (!rows_ok(a.dout, a.n_tokens, a.hidden) || !rows_ok(a.dy, n, a.hidden)) return QS_ERR_INVALID;
+    if (a.dtopk_w && !rows_ok(a.y, n, a.hidden)) return QS_ERR_INVALID;
     CombineBwdArgs p = {};
-    p.dout = dout;
-    p.y = y;
-    p.pos = pos;
-    p.w = topk_w;
-    p.dy = dy;
-    p.dw = dtopk_w;
-    p.dout_stride = dout_stride;
-    p.y_stride = y_stride;
-    p.dy_stride = dy_stride;
-    p.dout_dtype = dout_dtype;
-    p.y_dtype = y_dtype;
-    p.dy_dtype = dy_dtype;
-    p.n_tokens = n_tokens;
-    p.top_k = top_k;
-    p.hidden = hidden;
+    p.dout = a.dout.data;
+    p.y = a.y.data;
+    p.pos = a.pos;
+    p.w = a.topk_w;
+    p.dy = a.dy.data;
+    p.dw = a.dtopk_w;
+    p.dout_stride = a.dout.stride;
+    p.y_stride = a.y.stride;
+    p.dy_stride = a.dy.stride;
+    p.dout_dtype = a.dout.dtype;
+    p.y_dtype = a.y.dtype;
+    p.dy_dtype = a.dy.dtype;
+    p.n_tokens = a.n_tokens;
+    p.top_k = a.top_k;
+    p.hidden = a.hidden;
     return done(launch_combine_backward(p, (cudaStream_t)stream));
 }
 

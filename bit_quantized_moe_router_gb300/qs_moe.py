@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -106,17 +107,13 @@ def load(build_if_missing: bool = True):
     L.qs_moe_host_workspace_bytes.restype = sz
     L.qs_moe_host_workspace_bytes.argtypes = [SP, i32]
     L.qs_moe_ffn_host.argtypes = [SP, P, P, P, EP, HP, P, i32, P, sz, P]
-    rows, codes = [P, i64, i32], [P, i64, P, i64]  # (address, stride, type); (codes, stride, scales, stride)
-    L.qs_rmsnorm_residual.argtypes = [*rows, *rows, P, ctypes.c_float, i32, i32, *rows, *rows, *codes, P]
+    # the row operators take one packed struct each: a call of twenty ctypes arguments costs 1.3 us more than one
+    for name in ("qs_rmsnorm_residual", "qs_rmsnorm_residual_backward", "qs_silu_mul_quant", "qs_fp8_matmul",
+                 "qs_dispatch_tokens", "qs_combine_tokens", "qs_combine_tokens_backward"):
+        getattr(L, name).argtypes = [ctypes.c_char_p, P]
     L.qs_rmsnorm_backward_workspace_bytes.argtypes = [i32]
-    L.qs_rmsnorm_residual_backward.argtypes = [*rows, P, ctypes.c_float, *rows, *rows, i32, i32, *rows, P, P, sz, P]
-    L.qs_silu_mul_quant.argtypes = [*rows, i32, P, i32, *codes, P]
     L.qs_fp8_matmul_workspace_bytes.argtypes = [i32, i32, i32, i32]
-    L.qs_fp8_matmul.argtypes = [*codes, P, i64, i64, P, P, i32, i32, i32, i32, *rows, P, sz, P]
     L.qs_dispatch_workspace_bytes.argtypes = [i32, i32, i32]
-    L.qs_dispatch_tokens.argtypes = [P, i32, i32, i32, P, P, P, P, *rows, P, i64, i32, P, i64, P, i64, P, sz, P]
-    L.qs_combine_tokens.argtypes = [*rows, P, P, i32, i32, i32, *rows, P]
-    L.qs_combine_tokens_backward.argtypes = [*rows, *rows, P, P, i32, i32, i32, *rows, P, P]
     for name in ("qs_rmsnorm_backward_workspace_bytes", "qs_fp8_matmul_workspace_bytes", "qs_dispatch_workspace_bytes"):
         getattr(L, name).restype = sz
     for name in EXPORTS:
@@ -359,9 +356,23 @@ def qs_test_wait_timeout(workspace, limit_us, stream=None):
 # Matrices are 2-D tensors whose columns are contiguous; rows may be strided.  fp32 and bf16 tensors are
 # torch.float32 and torch.bfloat16, e4m3 codes torch.float8_e4m3fn.
 
-_TYPES = {torch.float32: QS_F32, torch.bfloat16: QS_BF16, torch.float8_e4m3fn: QS_E4M3}
-_NO_ROWS = (None, 0, 0)
-_NO_CODES = (None, 0, None, 0)
+_WIDE = {torch.float32: QS_F32, torch.bfloat16: QS_BF16}
+_E4M3 = {torch.float8_e4m3fn: QS_E4M3}
+_ANY = {**_WIDE, **_E4M3}
+
+# the argument structs of include/qs_moe.h, as they lie in memory
+_ROWS, _CODES = "Pqi4x", "PqPq"
+ARGS = {
+    "qs_rmsnorm_residual": struct.Struct("@" + 4 * _ROWS + _CODES + "Pfii4x"),
+    "qs_rmsnorm_residual_backward": struct.Struct("@" + 4 * _ROWS + "PPPNfii4x"),
+    "qs_silu_mul_quant": struct.Struct("@" + _ROWS + _CODES + "Pii"),
+    "qs_fp8_matmul": struct.Struct("@" + _CODES + "PqqPP" + _ROWS + "PNiiii"),
+    "qs_dispatch_tokens": struct.Struct("@PPPPP" + 2 * _ROWS + "PqPqPNiiii"),
+    "qs_combine_tokens": struct.Struct("@" + 2 * _ROWS + "PPiii4x"),
+    "qs_combine_tokens_backward": struct.Struct("@" + 3 * _ROWS + "PPPiii4x"),
+}
+_pack_norm, _pack_norm_bwd, _pack_silu, _pack_matmul, _pack_dispatch, _pack_combine, _pack_combine_bwd = (
+    a.pack for a in ARGS.values())
 
 
 def _refuse(t, what, shape, dtypes):
@@ -375,40 +386,39 @@ def _refuse(t, what, shape, dtypes):
     raise ValueError(f"{what}: expected contiguous {'columns' if t.dim() > 1 else 'elements'}")
 
 
-_WIDE = (torch.float32, torch.bfloat16)
-_E4M3 = (torch.float8_e4m3fn,)
-_F32 = (torch.float32,)
-_I32 = (torch.int32,)
-
-
-def _matrix(t, what, rows, cols, dtypes=_WIDE):
-    """(address, row stride, type) of a [rows, cols] matrix."""
-    if t.dim() != 2 or not t.is_cuda or t.dtype not in dtypes or t.shape != (rows, cols):
-        _refuse(t, what, (rows, cols), dtypes)
+def _matrix(t, what, shape, dtypes=_WIDE):
+    """(address, row stride, type) of a matrix of this shape."""
+    kind = dtypes.get(t.dtype)
+    if kind is None or t.shape != shape or not t.is_cuda:
+        _refuse(t, what, shape, dtypes)
     stride, col = t.stride()
-    if col != 1 and cols > 1 and rows > 0:
-        _refuse(t, what, (rows, cols), dtypes)
-    return t.data_ptr(), stride, _TYPES[t.dtype]
+    if col != 1 and shape[1] > 1 and shape[0] > 0:
+        _refuse(t, what, shape, dtypes)
+    return t.data_ptr(), stride, kind
 
 
-def _codes(q, scale, what, rows, cols):
+def _codes(q, scale, what, shape):
     """(codes, stride, scales, stride) of an e4m3 matrix."""
     if scale is None:
         raise ValueError(f"{what}: e4m3 codes come with scales")
-    a, s, _ = _matrix(q, what, rows, cols, _E4M3)
-    b, u, _ = _matrix(scale, what + " scale", rows, (cols + 127) // 128, _F32)
+    a, s, _ = _matrix(q, what, shape, _E4M3)
+    b, u, _ = _matrix(scale, what + " scale", (shape[0], (shape[1] + 127) // 128), _F32)
     return a, s, b, u
 
 
-def _flat(t, what, shape, dtypes):
+_F32 = {torch.float32: QS_F32}
+_I32 = {torch.int32: 0}
+
+
+def _flat(t, what, shape, dtypes=_F32):
     """Address of a contiguous tensor of this shape."""
-    if not t.is_cuda or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+    if t.dtype not in dtypes or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         _refuse(t, what, shape, dtypes)
     return t.data_ptr()
 
 
 def _two(t, what):
-    """The sizes of a matrix."""
+    """The shape of a matrix."""
     if t.dim() != 2:
         raise ValueError(f"{what}: expected a matrix, got {t.dim()} dimensions")
     return t.shape
@@ -418,17 +428,25 @@ def _ws(workspace):
     return _dptr(workspace), workspace.numel() * workspace.element_size()
 
 
+def _stream_of(t, stream):
+    """The given stream, or the current one of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
+
+
 def qs_rmsnorm_residual(x, residual, weight, eps, sum_out=None, y=None, q=None, q_scale=None, stream=None):
     """Per row: s = x + residual (residual may be None), v = s * weight / sqrt(mean(s^2) + eps); sum_out gets s,
     y gets v, q and q_scale get v as e4m3 codes with a scale per 128 columns (each may be None)."""
-    rows, hidden = _two(x, "x")
-    _check((_lib or load()).qs_rmsnorm_residual(
-        *_matrix(x, "x", rows, hidden), *(_NO_ROWS if residual is None else _matrix(residual, "residual", rows, hidden)),
-        _flat(weight, "weight", (hidden,), _F32), eps, rows, hidden,
-        *(_NO_ROWS if sum_out is None else _matrix(sum_out, "sum_out", rows, hidden)),
-        *(_NO_ROWS if y is None else _matrix(y, "y", rows, hidden)),
-        *(_NO_CODES if q is None and q_scale is None else _codes(q, q_scale, "q", rows, hidden)), _stream(stream)),
-        "qs_rmsnorm_residual")
+    shape = _two(x, "x")
+    xp, xs, xt = _matrix(x, "x", shape)
+    rp, rs, rt = (0, 0, 0) if residual is None else _matrix(residual, "residual", shape)
+    sp, ss, st = (0, 0, 0) if sum_out is None else _matrix(sum_out, "sum_out", shape)
+    yp, ys, yt = (0, 0, 0) if y is None else _matrix(y, "y", shape)
+    qp, qs, qsp, qss = (0, 0, 0, 0) if q is None and q_scale is None else _codes(q, q_scale, "q", shape)
+    rc = (_lib or load()).qs_rmsnorm_residual(
+        _pack_norm(xp, xs, xt, rp, rs, rt, sp, ss, st, yp, ys, yt, qp, qs, qsp, qss, _flat(weight, "weight", shape[1:]), eps,
+                   shape[0], shape[1]), _stream_of(x, stream))
+    if rc:
+        raise QsError(rc, "qs_rmsnorm_residual")
 
 
 def alloc_rmsnorm_backward_workspace(hidden, device="cuda"):
@@ -439,23 +457,29 @@ def alloc_rmsnorm_backward_workspace(hidden, device="cuda"):
 def qs_rmsnorm_residual_backward(sum, weight, eps, dy, dsum, dx, dweight=None, workspace=None, stream=None):
     """dx, the gradient of x and of residual alike, and dweight (None: left out) from dy and dsum (None: no gradient
     by the residual stream); sum is what qs_rmsnorm_residual stored in sum_out."""
-    rows, hidden = _two(sum, "sum")
+    shape = _two(sum, "sum")
     if dweight is not None and workspace is None:
         raise ValueError("dweight needs a workspace")
-    _check((_lib or load()).qs_rmsnorm_residual_backward(
-        *_matrix(sum, "sum", rows, hidden), _flat(weight, "weight", (hidden,), _F32), eps, *_matrix(dy, "dy", rows, hidden),
-        *(_NO_ROWS if dsum is None else _matrix(dsum, "dsum", rows, hidden)), rows, hidden, *_matrix(dx, "dx", rows, hidden),
-        None if dweight is None else _flat(dweight, "dweight", (hidden,), _F32), *((None, 0) if workspace is None else _ws(workspace)),
-        _stream(stream)), "qs_rmsnorm_residual_backward")
+    rc = (_lib or load()).qs_rmsnorm_residual_backward(
+        _pack_norm_bwd(*_matrix(sum, "sum", shape), *_matrix(dy, "dy", shape),
+                       *((0, 0, 0) if dsum is None else _matrix(dsum, "dsum", shape)), *_matrix(dx, "dx", shape),
+                       _flat(weight, "weight", shape[1:]), 0 if dweight is None else _flat(dweight, "dweight", shape[1:]),
+                       *((0, 0) if workspace is None else _ws(workspace)), eps, *shape), _stream_of(sum, stream))
+    _check(rc, "qs_rmsnorm_residual_backward")
 
 
 def qs_silu_mul_quant(gate_up, q, q_scale, n_rows=None, stream=None):
     """q, q_scale [rows, F]: silu(gate) * up of gate_up [rows, 2F] as e4m3 codes with scales; n_rows (an int32 tensor
     on the device, or None): rows at and beyond its value are left alone."""
-    rows, ffn = _two(q, "q")
-    _check((_lib or load()).qs_silu_mul_quant(
-        *_matrix(gate_up, "gate_up", rows, 2 * ffn), rows, None if n_rows is None else _flat(n_rows, "n_rows", n_rows.shape, _I32),
-        ffn, *_codes(q, q_scale, "q", rows, ffn), _stream(stream)), "qs_silu_mul_quant")
+    shape = _two(q, "q")
+    rows, ffn = shape
+    gp, gs, gt = _matrix(gate_up, "gate_up", (rows, 2 * ffn))
+    qp, qs, qsp, qss = _codes(q, q_scale, "q", shape)
+    rc = (_lib or load()).qs_silu_mul_quant(
+        _pack_silu(gp, gs, gt, qp, qs, qsp, qss, 0 if n_rows is None else _flat(n_rows, "n_rows", n_rows.shape, _I32), rows, ffn),
+        _stream_of(q, stream))
+    if rc:
+        raise QsError(rc, "qs_silu_mul_quant")
 
 
 def alloc_fp8_matmul_workspace(n_rows, n_cols, n_inner, n_experts=1, device="cuda"):
@@ -467,26 +491,30 @@ def qs_fp8_matmul(a, a_scale, w, w_scale, out, workspace, offsets=None, stream=N
     """out [rows, N] = a [rows, K] times w [N, K] (or, with offsets int32 [E + 1], w [E, N, K] of the expert whose
     rows offsets[e] .. offsets[e + 1] - 1 are) transposed; e4m3 codes with a scale per row and 128 columns of a and per
     128 x 128 block of w."""
-    rows, inner = _two(a, "a")
+    shape = _two(a, "a")
+    rows, inner = shape
     if offsets is None:
-        cols = _two(w, "w")[0]
-        experts, wp = 1, _matrix(w, "w", cols, inner, _E4M3)
-        strides = (wp[1], 0)
+        experts, cols, off, expert_stride = 1, _two(w, "w")[0], 0, 0
+        wp, w_stride, _ = _matrix(w, "w", (cols, inner), _E4M3)
         blocks = ((cols + 127) // 128, (inner + 127) // 128)
-        off = None
     else:
         if w.dim() != 3:
             raise ValueError(f"w: expected [experts, cols, inner], got {w.dim()} dimensions")
-        experts, cols, _ = w.shape
-        if not w.is_cuda or w.dtype not in _E4M3 or w.shape[2] != inner or (w.stride(2) != 1 and inner > 1):
+        experts, cols, k = w.shape
+        if w.dtype not in _E4M3 or k != inner or not w.is_cuda or (w.stride(2) != 1 and inner > 1):
             _refuse(w, "w", (experts, cols, inner), _E4M3)
-        wp = (w.data_ptr(),)
-        strides = (w.stride(1), w.stride(0))
+        wp = w.data_ptr()
+        expert_stride, w_stride, _ = w.stride()
         blocks = (experts, (cols + 127) // 128, (inner + 127) // 128)
         off = _flat(offsets, "offsets", (experts + 1,), _I32)
-    _check((_lib or load()).qs_fp8_matmul(
-        *_codes(a, a_scale, "a", rows, inner), wp[0], *strides, _flat(w_scale, "w scale", blocks, _F32), off, experts, rows,
-        cols, inner, *_matrix(out, "out", rows, cols), *_ws(workspace), _stream(stream)), "qs_fp8_matmul")
+    ap, as_, sp, ss = _codes(a, a_scale, "a", shape)
+    op, os_, ot = _matrix(out, "out", (rows, cols))
+    ws, ws_bytes = _ws(workspace)
+    rc = (_lib or load()).qs_fp8_matmul(
+        _pack_matmul(ap, as_, sp, ss, wp, w_stride, expert_stride, _flat(w_scale, "w scale", blocks), off, op, os_, ot, ws, ws_bytes,
+                     experts, rows, cols, inner), _stream_of(a, stream))
+    if rc:
+        raise QsError(rc, "qs_fp8_matmul")
 
 
 def alloc_dispatch_workspace(n_tokens, top_k, n_experts, device="cuda"):
@@ -498,46 +526,58 @@ def qs_dispatch_tokens(topk_ids, x, x_scale, counts, offsets, perm, pos, xs, xs_
     """The plan of topk_ids [tokens, k] (counts [E], offsets [E + 1], perm [tokens * k], pos [tokens, k], all int32)
     and xs [tokens * k, hidden], the rows of x sorted by expert; x e4m3 brings x_scale along to xs_scale.  x and xs
     None: the plan alone."""
-    tokens, k = _two(topk_ids, "topk_ids")
-    n, experts = tokens * k, counts.numel()
-    xp, sp, xq, sq, hidden = _NO_ROWS, (None, 0), (None, 0), (None, 0), 0
+    shape = _two(topk_ids, "topk_ids")
+    tokens, k = shape
+    n, experts, hidden = tokens * k, counts.numel(), 0
+    xp = xs_ = xt = yp = ys = sp = ss = tp = ts = 0
     if (x is None) != (xs is None):
         raise ValueError("x and xs come together")
     if x is not None:
         hidden = _two(x, "x")[1]
-        xp = _matrix(x, "x", tokens, hidden, tuple(_TYPES))
-        xq = _matrix(xs, "xs", n, hidden, (x.dtype,))[:2]
         if x.dtype is torch.float8_e4m3fn:
-            sp = _codes(x, x_scale, "x", tokens, hidden)[2:]
-            sq = _codes(xs, xs_scale, "xs", n, hidden)[2:]
-    _check((_lib or load()).qs_dispatch_tokens(
-        _flat(topk_ids, "topk_ids", (tokens, k), _I32), tokens, k, experts, _flat(counts, "counts", (experts,), _I32),
-        _flat(offsets, "offsets", (experts + 1,), _I32), _flat(perm, "perm", (n,), _I32), _flat(pos, "pos", (tokens, k), _I32),
-        *xp, *sp, hidden, *xq, *sq, *_ws(workspace), _stream(stream)), "qs_dispatch_tokens")
+            xp, xs_, sp, ss = _codes(x, x_scale, "x", (tokens, hidden))
+            yp, ys, tp, ts = _codes(xs, xs_scale, "xs", (n, hidden))
+            xt = QS_E4M3
+        else:
+            xp, xs_, xt = _matrix(x, "x", (tokens, hidden))
+            yp, ys, _ = _matrix(xs, "xs", (n, hidden), {x.dtype: xt})
+    ws, ws_bytes = _ws(workspace)
+    rc = (_lib or load()).qs_dispatch_tokens(
+        _pack_dispatch(_flat(topk_ids, "topk_ids", shape, _I32), _flat(counts, "counts", (experts,), _I32),
+                       _flat(offsets, "offsets", (experts + 1,), _I32), _flat(perm, "perm", (n,), _I32), _flat(pos, "pos", shape, _I32),
+                       xp, xs_, xt, yp, ys, xt, sp, ss, tp, ts, ws, ws_bytes, tokens, k, experts, hidden), _stream_of(topk_ids, stream))
+    if rc:
+        raise QsError(rc, "qs_dispatch_tokens")
 
 
 def qs_combine_tokens(y, pos, topk_w, out, stream=None):
     """out [tokens, hidden]: the sum over a token's slots of topk_w (None: 1) times its row of y [tokens * k, hidden]."""
-    tokens, k = _two(pos, "pos")
+    shape = _two(pos, "pos")
+    tokens, k = shape
     hidden = _two(out, "out")[1]
-    _check((_lib or load()).qs_combine_tokens(
-        *_matrix(y, "y", tokens * k, hidden), _flat(pos, "pos", (tokens, k), _I32),
-        None if topk_w is None else _flat(topk_w, "topk_w", (tokens, k), _F32), tokens, k, hidden,
-        *_matrix(out, "out", tokens, hidden), _stream(stream)), "qs_combine_tokens")
+    yp, ys, yt = _matrix(y, "y", (tokens * k, hidden))
+    op, os_, ot = _matrix(out, "out", (tokens, hidden))
+    rc = (_lib or load()).qs_combine_tokens(
+        _pack_combine(yp, ys, yt, op, os_, ot, _flat(pos, "pos", shape, _I32), 0 if topk_w is None else _flat(topk_w, "topk_w", shape),
+                      tokens, k, hidden), _stream_of(out, stream))
+    if rc:
+        raise QsError(rc, "qs_combine_tokens")
 
 
 def qs_combine_tokens_backward(dout, y, pos, topk_w, dy, dtopk_w=None, stream=None):
     """Gradient of qs_combine_tokens: dy [tokens * k, hidden] and dtopk_w [tokens, k] (None: left out; y may then be
     None)."""
-    tokens, k = _two(pos, "pos")
+    shape = _two(pos, "pos")
+    tokens, k = shape
     hidden = _two(dout, "dout")[1]
     if dtopk_w is not None and y is None:
         raise ValueError("dtopk_w needs y")
-    _check((_lib or load()).qs_combine_tokens_backward(
-        *_matrix(dout, "dout", tokens, hidden), *(_NO_ROWS if y is None else _matrix(y, "y", tokens * k, hidden)),
-        _flat(pos, "pos", (tokens, k), _I32), None if topk_w is None else _flat(topk_w, "topk_w", (tokens, k), _F32), tokens, k,
-        hidden, *_matrix(dy, "dy", tokens * k, hidden), None if dtopk_w is None else _flat(dtopk_w, "dtopk_w", (tokens, k), _F32),
-        _stream(stream)), "qs_combine_tokens_backward")
+    rc = (_lib or load()).qs_combine_tokens_backward(
+        _pack_combine_bwd(*_matrix(dout, "dout", (tokens, hidden)), *((0, 0, 0) if y is None else _matrix(y, "y", (tokens * k, hidden))),
+                          *_matrix(dy, "dy", (tokens * k, hidden)), _flat(pos, "pos", shape, _I32),
+                          0 if topk_w is None else _flat(topk_w, "topk_w", shape),
+                          0 if dtopk_w is None else _flat(dtopk_w, "dtopk_w", shape), tokens, k, hidden), _stream_of(dout, stream))
+    _check(rc, "qs_combine_tokens_backward")
 
 
 def _alloc(n, what, device):

@@ -341,9 +341,11 @@ int qs_test_wait_timeout(void *workspace, size_t workspace_bytes, int limit_us, 
 
 /* ---------------------------------------------------------------------------
  * Operators around 8-bit rows.  The same conventions, and these:
- *  - A matrix of rows is a pointer, a row stride in elements (any, >= its
- *    columns) and a qs_dtype.  Columns are contiguous.  Every alignment of an
- *    element is taken; 16-byte aligned rows run the vector forms.
+ *  - The arguments of a call are one struct, read before the call returns.
+ *  - A matrix of rows (qs_rows) is a pointer, a row stride in elements (any, >=
+ *    its columns) and a qs_dtype.  Columns are contiguous.  Every alignment of
+ *    an element is taken; 16-byte aligned rows run the vector forms.  data NULL
+ *    leaves an optional matrix out.
  *  - An e4m3 matrix [rows x cols] has its codes, one byte each, and fp32
  *    scales: the value at (r, c) is code * scale[r * scale_stride + c / 128].
  *    A row has ceil(cols / 128) scales; the last may cover fewer columns.
@@ -355,25 +357,52 @@ int qs_test_wait_timeout(void *workspace, size_t workspace_bytes, int limit_us, 
  *    (dweight, counts, offsets) are still written.
  *  - Input and output buffers must not overlap unless an entry says so.
  */
+typedef struct {
+    void *data;
+    int64_t stride;  /* elements between rows */
+    int32_t dtype;   /* qs_dtype */
+} qs_rows;
+
+typedef struct {
+    void *q;               /* e4m3 codes */
+    int64_t stride;        /* bytes between rows */
+    float *scale;
+    int64_t scale_stride;  /* floats between rows of scales */
+} qs_codes;
+
+typedef struct {
+    qs_rows x, residual, sum_out, y;
+    qs_codes q;
+    const float *weight;
+    float eps;
+    int32_t n_rows, hidden;
+} qs_rmsnorm_args;
 
 /* Root-mean-square norm with the residual's addition.  Per row t:
- *   s = x_t + residual_t (x_t if residual is NULL), in fp32
+ *   s = x_t + residual_t (x_t without a residual), in fp32
  *   v = s * weight / sqrt(mean(s^2) + eps), in fp32
- * sum_out (or NULL) gets s rounded to its type, y (or NULL) v rounded to its
- * type, q with q_scale (or both NULL) v as codes with scales.  The norm is of s
+ * sum_out (if there) gets s rounded to its type, y (if there) v rounded to its
+ * type, q (if there) v as codes with scales.  The norm is of s
  * before its rounding to sum_out.  x, residual, sum_out and y are fp32 or bf16,
  * each by its own type; weight is device fp32 [hidden].  sum_out may be x or
  * residual itself (same address, stride and type).  1 <= hidden <= 16384,
  * eps >= 0 and finite; at least one of y, q and sum_out.  One launch. */
-int qs_rmsnorm_residual(const void *x, int64_t x_stride, int x_dtype, const void *residual, int64_t residual_stride,
-                        int residual_dtype, const float *weight, float eps, int n_rows, int hidden, void *sum_out,
-                        int64_t sum_stride, int sum_dtype, void *y, int64_t y_stride, int y_dtype, void *q,
-                        int64_t q_stride, float *q_scale, int64_t q_scale_stride, void *stream);
+int qs_rmsnorm_residual(const qs_rmsnorm_args *args, void *stream);
+
+typedef struct {
+    qs_rows sum, dy, dsum, dx;
+    const float *weight;
+    float *dweight;
+    void *workspace;
+    size_t workspace_bytes;
+    float eps;
+    int32_t n_rows, hidden;
+} qs_rmsnorm_backward_args;
 
 /* Gradient of qs_rmsnorm_residual's y and sum_out.  With s the rows of sum
  * (what sum_out held), rho = 1 / sqrt(mean(s^2) + eps), per row
  *   dx = rho * weight * dy - s * rho^3 * mean(weight * dy * s) + dsum
- * (dsum: the gradient that reaches s by the residual stream, or NULL); it is the
+ * (dsum: the gradient that reaches s by the residual stream, if any); it is the
  * gradient of x and of residual alike.  dweight (fp32 [hidden], or NULL) is
  * overwritten with the sum over rows of dy * s * rho; its rows are added in a
  * fixed order (run-to-run identical).  workspace: at least
@@ -381,27 +410,39 @@ int qs_rmsnorm_residual(const void *x, int64_t x_stride, int x_dtype, const void
  * initialisation (NULL if dweight is NULL).  dx may be dy or dsum itself.  One
  * launch, two with dweight. */
 size_t qs_rmsnorm_backward_workspace_bytes(int hidden);
-int qs_rmsnorm_residual_backward(const void *sum, int64_t sum_stride, int sum_dtype, const float *weight, float eps,
-                                 const void *dy, int64_t dy_stride, int dy_dtype, const void *dsum,
-                                 int64_t dsum_stride, int dsum_dtype, int n_rows, int hidden, void *dx,
-                                 int64_t dx_stride, int dx_dtype, float *dweight, void *workspace,
-                                 size_t workspace_bytes, void *stream);
+int qs_rmsnorm_residual_backward(const qs_rmsnorm_backward_args *args, void *stream);
+
+typedef struct {
+    qs_rows gate_up;
+    qs_codes q;
+    const int32_t *n_rows_dev;
+    int32_t n_rows, ffn;
+} qs_silu_mul_args;
 
 /* SwiGLU of a gate/up product with an 8-bit output: per row of gate_up
  * [n_rows x 2F] (gate columns first; fp32 or bf16) v = silu(gate) * up in fp32,
- * stored as codes q [n_rows x F] with q_scale.  n_rows_dev (device int32, or
+ * stored as codes q [n_rows x F].  n_rows_dev (device int32, or
  * NULL): rows at and beyond *n_rows_dev are left alone (the total of
  * qs_dispatch_tokens is offsets[n_experts]).  One launch. */
-int qs_silu_mul_quant(const void *gate_up, int64_t gate_up_stride, int gate_up_dtype, int n_rows,
-                      const int32_t *n_rows_dev, int ffn, void *q, int64_t q_stride, float *q_scale,
-                      int64_t q_scale_stride, void *stream);
+int qs_silu_mul_quant(const qs_silu_mul_args *args, void *stream);
+
+typedef struct {
+    qs_codes a;
+    const void *w;
+    int64_t w_stride, w_expert_stride;
+    const float *w_scale;
+    const int32_t *offsets;
+    qs_rows out;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t n_experts, n_rows, n_cols, n_inner;
+} qs_fp8_matmul_args;
 
 /* Product of e4m3 rows with e4m3 weights, scales applied per 128 of the inner
  * dimension, on the fifth-generation tensor cores:
- *   out[m, n] = sum_b a_scale[m, b] * w_scale[e, n / 128, b]
+ *   out[m, n] = sum_b a.scale[m, b] * w_scale[e, n / 128, b]
  *               * (sum over k in block b of a[m, k] * w[e, n, k])
- * a      device codes [n_rows x K], 16-byte aligned, a_stride % 16 == 0
- * a_scale device fp32, row stride a_scale_stride
+ * a      device codes [n_rows x K], 16-byte aligned, a.stride % 16 == 0
  * w      device codes [E x N x K]: row stride w_stride, expert stride
  *        w_expert_stride (bytes, multiples of 16; 16-byte aligned)
  * w_scale device fp32 [E x ceil(N / 128) x ceil(K / 128)], contiguous
@@ -415,10 +456,20 @@ int qs_silu_mul_quant(const void *gate_up, int64_t gate_up_stride, int gate_up_d
  * qs_fp8_matmul_workspace_bytes(n_rows, N, K, E), 256-byte aligned, initialised
  * with qs_workspace_init (its header records a wait that ran out).  One launch. */
 size_t qs_fp8_matmul_workspace_bytes(int n_rows, int n_cols, int n_inner, int n_experts);
-int qs_fp8_matmul(const void *a, int64_t a_stride, const float *a_scale, int64_t a_scale_stride, const void *w,
-                  int64_t w_stride, int64_t w_expert_stride, const float *w_scale, const int32_t *offsets,
-                  int n_experts, int n_rows, int n_cols, int n_inner, void *out, int64_t out_stride, int out_dtype,
-                  void *workspace, size_t workspace_bytes, void *stream);
+int qs_fp8_matmul(const qs_fp8_matmul_args *args, void *stream);
+
+typedef struct {
+    const int32_t *topk_ids;
+    int32_t *counts, *offsets, *perm, *pos;
+    qs_rows x, xs;
+    const float *x_scale;
+    int64_t x_scale_stride;
+    float *xs_scale;
+    int64_t xs_scale_stride;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t n_tokens, top_k, n_experts, hidden;
+} qs_dispatch_args;
 
 /* Token rows sorted by expert.  The plan of topk_ids (device int32
  * [n_tokens x top_k]): counts [E], offsets [E + 1] and perm [n_tokens * top_k]
@@ -428,16 +479,19 @@ int qs_fp8_matmul(const void *a, int64_t a_stride, const float *a_scale, int64_t
  * perm[p] / top_k of x, for p < offsets[E]; later rows are left alone.
  * x [n_tokens x hidden] and xs [n_tokens * top_k x hidden] have the same type,
  * fp32, bf16 or e4m3; with e4m3 x_scale's rows of ceil(hidden / 128) go along to
- * xs_scale.  xs NULL makes the plan alone.  workspace: at least
+ * xs_scale.  Without xs the plan is made alone.  workspace: at least
  * qs_dispatch_workspace_bytes(n_tokens, top_k, E), 256-byte aligned, needs no
  * initialisation.  n_tokens * top_k <= 2^30, top_k <= 32, E <= 1024.  One
  * launch for up to 2048 entries, else up to three. */
 size_t qs_dispatch_workspace_bytes(int n_tokens, int top_k, int n_experts);
-int qs_dispatch_tokens(const int32_t *topk_ids, int n_tokens, int top_k, int n_experts, int32_t *counts,
-                       int32_t *offsets, int32_t *perm, int32_t *pos, const void *x, int64_t x_stride, int x_dtype,
-                       const float *x_scale, int64_t x_scale_stride, int hidden, void *xs, int64_t xs_stride,
-                       float *xs_scale, int64_t xs_scale_stride, void *workspace, size_t workspace_bytes,
-                       void *stream);
+int qs_dispatch_tokens(const qs_dispatch_args *args, void *stream);
+
+typedef struct {
+    qs_rows y, out;
+    const int32_t *pos;
+    const float *topk_w;
+    int32_t n_tokens, top_k, hidden;
+} qs_combine_args;
 
 /* The experts' rows back to their tokens: out[t] = sum over slots j, ascending,
  * of topk_w[t, j] * y[pos[t, j]], in fp32, rounded once to out's type; entries
@@ -445,18 +499,22 @@ int qs_dispatch_tokens(const int32_t *topk_ids, int n_tokens, int top_k, int n_e
  * a row of zeros.  topk_w NULL means weights of 1: the gradient of
  * qs_dispatch_tokens's rows.  y [n_tokens * top_k x hidden] and out
  * [n_tokens x hidden] fp32 or bf16.  One launch. */
-int qs_combine_tokens(const void *y, int64_t y_stride, int y_dtype, const int32_t *pos, const float *topk_w,
-                      int n_tokens, int top_k, int hidden, void *out, int64_t out_stride, int out_dtype,
-                      void *stream);
+int qs_combine_tokens(const qs_combine_args *args, void *stream);
+
+typedef struct {
+    qs_rows dout, y, dy;
+    const int32_t *pos;
+    const float *topk_w;
+    float *dtopk_w;
+    int32_t n_tokens, top_k, hidden;
+} qs_combine_backward_args;
 
 /* Gradient of qs_combine_tokens: for each entry with a position
  * dy[pos[t, j]] = topk_w[t, j] * dout[t] and dtopk_w[t, j] = dout[t] . y[pos[t, j]];
  * dtopk_w of the other entries is 0, rows of dy that no entry has are left
  * alone.  topk_w NULL means weights of 1; dtopk_w NULL leaves it out (y is then
- * not read and may be NULL).  One launch. */
-int qs_combine_tokens_backward(const void *dout, int64_t dout_stride, int dout_dtype, const void *y, int64_t y_stride,
-                               int y_dtype, const int32_t *pos, const float *topk_w, int n_tokens, int top_k,
-                               int hidden, void *dy, int64_t dy_stride, int dy_dtype, float *dtopk_w, void *stream);
+ * not read and may be left out).  One launch. */
+int qs_combine_tokens_backward(const qs_combine_backward_args *args, void *stream);
 
 #if defined(__GNUC__)
 #pragma GCC visibility pop

@@ -10,93 +10,103 @@ F32, BF16, E4M3 = qm.QS_F32, qm.QS_BF16, qm.QS_E4M3
 BIG = 1 << 40
 
 
-def change(base, **over):
-    d = dict(base)
-    assert set(over) <= set(d)
-    d.update(over)
-    return list(d.values())
+def call(name, base, over):
+    """The entry point on the packed struct of base's fields with some of them changed."""
+    assert set(over) <= set(base)
+    return getattr(qm.load(), name)(qm.ARGS[name].pack(*{**base, **over}.values()), None)
 
 
-NORM = dict(x=FAKE, x_stride=256, x_dtype=BF16, r=FAKE, r_stride=256, r_dtype=BF16, w=FAKE, eps=1e-6, n=4, h=256, s=FAKE,
-            s_stride=256, s_dtype=BF16, y=FAKE, y_stride=256, y_dtype=BF16, q=FAKE, q_stride=256, qs=FAKE, qs_stride=2, st=None)
+def rows(name, stride=256, dtype=BF16):
+    return {name: FAKE, name + "_stride": stride, name + "_dtype": dtype}
+
+
+def codes(name, stride=256):
+    return {name: FAKE, name + "_stride": stride, name + "_scale": FAKE, name + "_scale_stride": 2}
+
+
+NORM = {**rows("x"), **rows("r"), **rows("s"), **rows("y"), **codes("q"), "w": FAKE, "eps": 1e-6, "n": 4, "h": 256}
 
 
 @pytest.mark.parametrize("over", [
-    dict(x=None), dict(x_dtype=E4M3), dict(x_dtype=7), dict(x_stride=255), dict(x=FAKE + 1), dict(w=None), dict(w=FAKE + 2),
+    dict(x=0), dict(x_dtype=E4M3), dict(x_dtype=7), dict(x_stride=255), dict(x=FAKE + 1), dict(w=0), dict(w=FAKE + 2),
     dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(n=-1), dict(h=0), dict(h=16385), dict(r_stride=0),
-    dict(r_dtype=-1), dict(s_stride=10), dict(y_dtype=E4M3), dict(y=FAKE + 1), dict(q_stride=255), dict(qs=None), dict(q=None),
-    dict(qs_stride=1), dict(qs=FAKE + 2), dict(s=None, y=None, q=None, qs=None)], ids=str)
+    dict(r_dtype=-1), dict(s_stride=10), dict(y_dtype=E4M3), dict(y=FAKE + 1), dict(q_stride=255), dict(q_scale=0), dict(q=0),
+    dict(q_scale_stride=1), dict(q_scale=FAKE + 2), dict(s=0, y=0, q=0, q_scale=0)], ids=str)
 def test_norm_refusals(over):
-    assert qm.load().qs_rmsnorm_residual(*change(NORM, **over)) == INV
+    assert call("qs_rmsnorm_residual", NORM, over) == INV
 
 
-BWD = dict(s=FAKE, s_stride=256, s_dtype=F32, w=FAKE, eps=1e-6, dy=FAKE, dy_stride=256, dy_dtype=F32, ds=FAKE, ds_stride=256,
-           ds_dtype=F32, n=4, h=256, dx=FAKE, dx_stride=256, dx_dtype=F32, dw=FAKE, ws=FAKE, bytes=BIG, st=None)
+BWD = {**rows("s", 256, F32), **rows("dy", 256, F32), **rows("ds", 256, F32), **rows("dx", 256, F32), "w": FAKE, "dw": FAKE, "ws": FAKE,
+       "bytes": BIG, "eps": 1e-6, "n": 4, "h": 256}
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(s=None), INV), (dict(dy=None), INV), (dict(dx=None), INV), (dict(w=None), INV), (dict(h=20000), INV),
+    (dict(s=0), INV), (dict(dy=0), INV), (dict(dx=0), INV), (dict(w=0), INV), (dict(h=20000), INV),
     (dict(n=-2), INV), (dict(dy_stride=1), INV), (dict(ds_dtype=E4M3), INV), (dict(dx=FAKE + 2), INV), (dict(dw=FAKE + 1), INV),
-    (dict(ws=None), WS), (dict(ws=FAKE + 8), WS), (dict(bytes=1000), WS)], ids=str)
+    (dict(ws=0), WS), (dict(ws=FAKE + 8), WS), (dict(bytes=1000), WS)], ids=str)
 def test_norm_backward_refusals(over, code):
-    assert qm.load().qs_rmsnorm_residual_backward(*change(BWD, **over)) == code
+    assert call("qs_rmsnorm_residual_backward", BWD, over) == code
 
 
-SILU = dict(g=FAKE, g_stride=512, g_dtype=BF16, n=4, nd=None, f=256, q=FAKE, q_stride=256, qs=FAKE, qs_stride=2, st=None)
+SILU = {**rows("g", 512), **codes("q"), "nd": 0, "n": 4, "f": 256}
 
 
-@pytest.mark.parametrize("over", [dict(g=None), dict(g_stride=511), dict(g_dtype=E4M3), dict(n=-1), dict(f=0), dict(q=None),
-                                  dict(qs=None), dict(q_stride=1), dict(qs_stride=1), dict(nd=FAKE + 1)], ids=str)
+@pytest.mark.parametrize("over", [dict(g=0), dict(g_stride=511), dict(g_dtype=E4M3), dict(n=-1), dict(f=0), dict(q=0),
+                                  dict(q_scale=0), dict(q_stride=1), dict(q_scale_stride=1), dict(nd=FAKE + 1)], ids=str)
 def test_silu_refusals(over):
-    assert qm.load().qs_silu_mul_quant(*change(SILU, **over)) == INV
+    assert call("qs_silu_mul_quant", SILU, over) == INV
 
 
-MM = dict(a=FAKE, a_stride=256, sa=FAKE, sa_stride=2, w=FAKE, w_stride=256, we=256 * 64, sw=FAKE, off=FAKE, e=4, m=8, n=64, k=256,
-          out=FAKE, o_stride=64, o_dtype=BF16, ws=FAKE, bytes=BIG, st=None)
+MM = {**codes("a"), "w": FAKE, "w_stride": 256, "we": 256 * 64, "sw": FAKE, "off": FAKE, **rows("out", 64), "ws": FAKE, "bytes": BIG,
+      "e": 4, "m": 8, "n": 64, "k": 256}
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(a=None), INV), (dict(a=FAKE + 8), INV), (dict(a_stride=264), INV), (dict(a_stride=240), INV), (dict(sa=None), INV),
-    (dict(sa_stride=1), INV), (dict(w=None), INV), (dict(w=FAKE + 4), INV), (dict(w_stride=250), INV), (dict(w_stride=128), INV),
-    (dict(we=256 * 63), INV), (dict(we=256 * 64 + 8), INV), (dict(sw=None), INV), (dict(off=None), INV), (dict(off=FAKE + 2), INV),
-    (dict(e=0), INV), (dict(e=1025), INV), (dict(m=-1), INV), (dict(n=0), INV), (dict(k=0), INV), (dict(out=None), INV),
-    (dict(o_stride=63), INV), (dict(o_dtype=E4M3), INV), (dict(out=FAKE + 1), INV), (dict(ws=None), WS), (dict(ws=FAKE + 16), WS),
+    (dict(a=0), INV), (dict(a=FAKE + 8), INV), (dict(a_stride=264), INV), (dict(a_stride=240), INV), (dict(a_scale=0), INV),
+    (dict(a_scale_stride=1), INV), (dict(w=0), INV), (dict(w=FAKE + 4), INV), (dict(w_stride=250), INV), (dict(w_stride=128), INV),
+    (dict(we=256 * 63), INV), (dict(we=256 * 64 + 8), INV), (dict(sw=0), INV), (dict(off=0), INV), (dict(off=FAKE + 2), INV),
+    (dict(e=0), INV), (dict(e=1025), INV), (dict(m=-1), INV), (dict(n=0), INV), (dict(k=0), INV), (dict(out=0), INV),
+    (dict(out_stride=63), INV), (dict(out_dtype=E4M3), INV), (dict(out=FAKE + 1), INV), (dict(ws=0), WS), (dict(ws=FAKE + 16), WS),
     (dict(bytes=16), WS)], ids=str)
 def test_matmul_refusals(over, code):
-    assert qm.load().qs_fp8_matmul(*change(MM, **over)) == code
+    assert call("qs_fp8_matmul", MM, over) == code
 
 
-DISPATCH = dict(ids=FAKE, t=8, k=2, e=16, c=FAKE, o=FAKE, p=FAKE, pos=FAKE, x=FAKE, x_stride=256, x_dtype=E4M3, sx=FAKE, sx_stride=2,
-                h=256, xs=FAKE, xs_stride=256, sxs=FAKE, sxs_stride=2, ws=FAKE, bytes=BIG, st=None)
+DISPATCH = {"ids": FAKE, "c": FAKE, "o": FAKE, "p": FAKE, "pos": FAKE, **rows("x", 256, E4M3), **rows("xs", 256, E4M3), "sx": FAKE,
+            "sx_stride": 2, "sxs": FAKE, "sxs_stride": 2, "ws": FAKE, "bytes": BIG, "t": 8, "k": 2, "e": 16, "h": 256}
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(ids=None), INV), (dict(t=-1), INV), (dict(k=0), INV), (dict(k=33), INV), (dict(e=0), INV), (dict(e=1025), INV),
-    (dict(t=1 << 30), INV), (dict(c=None), INV), (dict(o=None), INV), (dict(p=None), INV), (dict(pos=None), INV),
-    (dict(pos=FAKE + 2), INV), (dict(x=None), INV), (dict(x_stride=1), INV), (dict(x_dtype=9), INV), (dict(sx=None), INV),
-    (dict(sxs=None), INV), (dict(sxs_stride=1), INV), (dict(xs_stride=255), INV), (dict(h=0), INV), (dict(ws=None), WS),
+    (dict(ids=0), INV), (dict(t=-1), INV), (dict(k=0), INV), (dict(k=33), INV), (dict(e=0), INV), (dict(e=1025), INV),
+    (dict(t=1 << 30), INV), (dict(c=0), INV), (dict(o=0), INV), (dict(p=0), INV), (dict(pos=0), INV),
+    (dict(pos=FAKE + 2), INV), (dict(x=0), INV), (dict(x_stride=1), INV), (dict(x_dtype=9, xs_dtype=9), INV), (dict(x_dtype=BF16), INV),
+    (dict(sx=0), INV), (dict(sxs=0), INV), (dict(sxs_stride=1), INV), (dict(xs_stride=255), INV), (dict(h=0), INV), (dict(ws=0), WS),
     (dict(ws=FAKE + 128), WS), (dict(bytes=8), WS)], ids=str)
 def test_dispatch_refusals(over, code):
-    assert qm.load().qs_dispatch_tokens(*change(DISPATCH, **over)) == code
+    assert call("qs_dispatch_tokens", DISPATCH, over) == code
 
 
-COMBINE = dict(y=FAKE, y_stride=256, y_dtype=BF16, pos=FAKE, w=FAKE, t=8, k=2, h=256, out=FAKE, o_stride=256, o_dtype=F32, st=None)
+COMBINE = {**rows("y"), **rows("out", 256, F32), "pos": FAKE, "w": FAKE, "t": 8, "k": 2, "h": 256}
 
 
-@pytest.mark.parametrize("over", [dict(y=None), dict(y_dtype=E4M3), dict(y_stride=0), dict(pos=None), dict(pos=FAKE + 1), dict(w=FAKE + 2),
-                                  dict(t=-1), dict(k=0), dict(k=40), dict(h=0), dict(out=None), dict(o_stride=255), dict(o_dtype=5)], ids=str)
+@pytest.mark.parametrize("over", [dict(y=0), dict(y_dtype=E4M3), dict(y_stride=0), dict(pos=0), dict(pos=FAKE + 1), dict(w=FAKE + 2),
+                                  dict(t=-1), dict(k=0), dict(k=40), dict(h=0), dict(out=0), dict(out_stride=255), dict(out_dtype=5)], ids=str)
 def test_combine_refusals(over):
-    assert qm.load().qs_combine_tokens(*change(COMBINE, **over)) == INV
+    assert call("qs_combine_tokens", COMBINE, over) == INV
 
 
-COMBINE_BWD = dict(d=FAKE, d_stride=256, d_dtype=BF16, y=FAKE, y_stride=256, y_dtype=BF16, pos=FAKE, w=FAKE, t=8, k=2, h=256, dy=FAKE,
-                   dy_stride=256, dy_dtype=BF16, dw=FAKE, st=None)
+COMBINE_BWD = {**rows("d"), **rows("y"), **rows("dy"), "pos": FAKE, "w": FAKE, "dw": FAKE, "t": 8, "k": 2, "h": 256}
 
 
-@pytest.mark.parametrize("over", [dict(d=None), dict(y=None), dict(y_stride=7), dict(pos=None), dict(dy=None), dict(dy_dtype=E4M3),
+@pytest.mark.parametrize("over", [dict(d=0), dict(y=0), dict(y_stride=7), dict(pos=0), dict(dy=0), dict(dy_dtype=E4M3),
                                   dict(dw=FAKE + 2), dict(k=0), dict(h=-5), dict(dy_stride=0)], ids=str)
 def test_combine_backward_refusals(over):
-    assert qm.load().qs_combine_tokens_backward(*change(COMBINE_BWD, **over)) == INV
+    assert call("qs_combine_tokens_backward", COMBINE_BWD, over) == INV
+
+
+@pytest.mark.parametrize("name", list(qm.ARGS))
+def test_missing_arguments_are_refused(name):
+    assert getattr(qm.load(), name)(None, None) == INV
 
 
 def test_workspace_sizes():
@@ -113,12 +123,11 @@ def test_workspace_sizes():
 
 
 def test_nothing_is_launched_for_no_rows():
-    L = qm.load()
-    assert L.qs_rmsnorm_residual(*change(NORM, n=0)) == qm.QS_OK
-    assert L.qs_silu_mul_quant(*change(SILU, n=0)) == qm.QS_OK
-    assert L.qs_fp8_matmul(*change(MM, m=0)) == qm.QS_OK
-    assert L.qs_combine_tokens(*change(COMBINE, t=0)) == qm.QS_OK
-    assert L.qs_combine_tokens_backward(*change(COMBINE_BWD, t=0)) == qm.QS_OK
+    assert call("qs_rmsnorm_residual", NORM, dict(n=0)) == qm.QS_OK
+    assert call("qs_silu_mul_quant", SILU, dict(n=0)) == qm.QS_OK
+    assert call("qs_fp8_matmul", MM, dict(m=0)) == qm.QS_OK
+    assert call("qs_combine_tokens", COMBINE, dict(t=0)) == qm.QS_OK
+    assert call("qs_combine_tokens_backward", COMBINE_BWD, dict(t=0)) == qm.QS_OK
 
 
 def test_binding_refuses_wrong_tensors():
