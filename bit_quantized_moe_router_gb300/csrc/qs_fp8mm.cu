@@ -35,12 +35,15 @@ namespace {
 constexpr int kMaxStages = 32;
 constexpr int kFirstSum = 4;  // first of the warps that sum
 constexpr int kTileRows = 128;
-constexpr int kRowBox = 16;  // rows of the small TMA box of a
+constexpr int kRowBox = 16;  // rows of the small TMA box of a are a multiple of this
+constexpr int kFewRows = 64; // most rows that are copied by small boxes
 
 struct MmParams {
-    CUtensorMap ta16;   // a, boxes of 16 rows x 128 bytes
+    // a as [block of K][row][128 columns] and w as [expert][block][row][128 columns], boxes of a group's blocks;
+    // where K is no multiple of 128, one block deep over whole rows, boxes of one block (columns past K read as 0)
+    CUtensorMap tfew;   // a, boxes of box_rows rows
     CUtensorMap ta128;  // a, boxes of 128 rows
-    CUtensorMap tw;     // w [expert][row][k], boxes of BN rows
+    CUtensorMap tw;     // w, boxes of BN rows
     CUtensorMap tout;   // out, boxes of 32 rows x 128 bytes
     const float* sa;
     const float* sw;
@@ -50,7 +53,8 @@ struct MmParams {
     int64_t sa_stride, out_stride;
     int M, N, E, KB, NB;  // KB: blocks of K, NB: 128-row blocks of N
     int out_dtype, out_vec, out_tma;
-    int a_bytes, stages;  // bytes of a stage's row part
+    int a_bytes, stages;  // bytes of a block's row part
+    int box_rows, blocked;
     int out_at;           // where the summing warps' staging rows begin in shared memory, a multiple of 1024
 };
 
@@ -109,18 +113,19 @@ __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, volatile
     }
 }
 
-__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* m, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+// Boxes of a (columns, row, block) and of w (columns, row, block, expert).
+__device__ __forceinline__ void tma_a(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
             smem_u32(dst)),
         "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_w(void* dst, const CUtensorMap* m, int x, int y, int z, int e, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            smem_u32(dst)),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(e), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -150,18 +155,18 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
     return a;
 }
 // TMA into this CTA's shared memory, counted on the leader's barrier
-__device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(m), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_3d_pair(void* dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_a_pair(void* dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
             smem_u32(dst)),
         "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_w_pair(void* dst, const CUtensorMap* m, int x, int y, int z, int e, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            smem_u32(dst)),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(e), "r"(bar)
         : "memory");
 }
 // D[tmem of both] = A[smem of both] * B[smem of both]^T: 256 rows, 128 and half of B's rows in each CTA
@@ -179,10 +184,16 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
         "h"((uint16_t)3)
         : "memory");
 }
-// Arrive on a barrier of either CTA.  What it orders is tensor memory, by the tcgen05 fences: no release
-// at cluster scope, which costs a step of the sum more than the step.
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrive on a barrier of this CTA, or (PAIR) of either.  What it orders is tensor memory, by the tcgen05
+// fences: no release at cluster scope, which costs a step of the sum more than the step.
+template <bool PAIR>
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    if (PAIR) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    else asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
 // D[tmem] = A[smem] * B[smem]^T (accumulate: added), e4m3, 32 of K
@@ -245,7 +256,12 @@ struct MmShape {
     static constexpr int kHalves = BN == 256 ? 2 : 1;
     static constexpr int kAccCols = BN / kHalves;
     static constexpr int kAcc = 4;                                       // accumulators in tensor memory
-    static constexpr int kTmemCols = kAccCols * kAcc < 32 ? 32 : kAccCols * kAcc;  // 64 .. 512
+    // Blocks of K that pass through the roles as one: a stage, an accumulator (side by side, each block with its
+    // own columns) and one round of barriers.  Waits, issue and release take 300 to 400 cycles whatever the
+    // width, which is all a narrow tile's time: one row by 4096 x 2048 took 6.0 us with one block at a time.
+    static constexpr int kGroup = BN >= 128 ? 1 : BN == 64 ? 2 : 4;
+    static constexpr int kAccStep = kAccCols * kGroup;                   // columns of an accumulator
+    static constexpr int kTmemCols = kAccStep * kAcc;                    // 256 or 512
     static constexpr int kSumWarps = 8;
     static constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
     static constexpr int kCols = BN * 4 / kSumWarps;            // columns of a summing thread, in runs of 64 at most:
@@ -272,7 +288,7 @@ __device__ __forceinline__ float2 fma2(uint32_t b0, uint32_t b1, float s, float2
 
 // acc += scale * the thread's columns of an accumulator, which is free once its last columns are in
 // registers.  With two buffers the next columns are read while these are added.
-template <int BN>
+template <int BN, bool PAIR>
 __device__ __forceinline__ void add_block(float2 (&acc)[MmShape<BN>::kRuns][MmShape<BN>::kRun / 2], uint32_t src,
                                           const float (&scale)[MmShape<BN>::kRuns], uint32_t empty, int lane) {
     using S = MmShape<BN>;
@@ -286,7 +302,7 @@ __device__ __forceinline__ void add_block(float2 (&acc)[MmShape<BN>::kRuns][MmSh
         if (j + 1 == kSteps) {
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(empty);
+            if (lane == 0) arrive_at<PAIR>(empty);
         } else {
             tmem_load<S::kLoad>(src + (j + 1) * S::kLoad, d[(j + 1) % 2]);
         }
@@ -295,6 +311,29 @@ __device__ __forceinline__ void add_block(float2 (&acc)[MmShape<BN>::kRuns][MmSh
         for (int i = 0; i < S::kLoad / 2; i++) {
             float2& v = acc[j / kPer][j % kPer * (S::kLoad / 2) + i];
             v = fma2(d[j % 2][2 * i], d[j % 2][2 * i + 1], scale[j / kPer], v);
+        }
+    }
+}
+
+// The same for the blocks of a narrow tile's accumulator (n of them are there), all read at once.
+template <int BN, bool PAIR>
+__device__ __forceinline__ void add_group(float2 (&acc)[MmShape<BN>::kRun / 2], uint32_t src,
+                                          const float (&scale)[MmShape<BN>::kGroup], int n, uint32_t empty, int lane) {
+    using S = MmShape<BN>;
+    static_assert(S::kRuns == 1 && S::kLoad == S::kCols, "one load a block");
+    uint32_t d[S::kGroup][S::kLoad];
+    tc::fence_after();
+#pragma unroll
+    for (int g = 0; g < S::kGroup; g++) tmem_load<S::kLoad>(src + g * S::kAccCols, d[g]);
+    tc::wait_ld();
+    tc::fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_at<PAIR>(empty);
+#pragma unroll
+    for (int g = 0; g < S::kGroup; g++) {
+        if (g < n) {
+#pragma unroll
+            for (int i = 0; i < S::kLoad / 2; i++) acc[i] = fma2(d[g][2 * i], d[g][2 * i + 1], scale[g], acc[i]);
         }
     }
 }
@@ -369,7 +408,8 @@ template <int BN, bool PAIR>
 __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const __grid_constant__ MmParams p) {
     using S = MmShape<BN>;
     constexpr int kCtas = PAIR ? 2 : 1, kRows = kTileRows * kCtas;
-    constexpr int kWBytes = BN / kCtas * 128;  // a CTA's weight part of a stage
+    constexpr int G = S::kGroup;
+    constexpr int kWBytes = BN / kCtas * 128;  // a CTA's weight part of a block; a stage has G blocks
     extern __shared__ uint8_t mm_smem[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~(uintptr_t)1023);
     __shared__ MmCtl ctl;
@@ -383,24 +423,33 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
     // weight parts first: the row part of the last stage is followed by the tail that keeps the matrix
     // instruction's 128 rows inside shared memory
     uint8_t* wst = sm;
-    uint8_t* ast = sm + (size_t)stages * kWBytes;
+    uint8_t* ast = sm + (size_t)stages * G * kWBytes;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; s++) {
-            mbar_init(&ctl.full[s], 1);
-            mbar_init(&ctl.empty[s], S::kHalves);
+    if (warp == 0) {  // the barriers of a stage a lane: in one thread they took a third of a microsecond
+        static_assert(kMaxStages <= 32, "a lane a stage");
+        if (lane < stages) {
+            mbar_init(&ctl.full[lane], 1);
+            mbar_init(&ctl.empty[lane], S::kHalves);
         }
-        for (int s = 0; s < S::kAcc; s++) {
-            mbar_init(&ctl.accfull[s], 1);
-            mbar_init(&ctl.accempty[s], S::kSumWarps / S::kHalves * kCtas);
+        if (lane < S::kAcc) {
+            mbar_init(&ctl.accfull[lane], 1);
+            mbar_init(&ctl.accempty[lane], S::kSumWarps / S::kHalves * kCtas);
         }
-        for (int s = 0; s < kScaleRing; s++) {
-            mbar_init(&ctl.scfull[s], 1);
-            mbar_init(&ctl.scempty[s], S::kSumWarps);
+        if (lane < kScaleRing) {
+            mbar_init(&ctl.scfull[lane], 1);
+            mbar_init(&ctl.scempty[lane], S::kSumWarps);
         }
-        mbar_init(&ctl.drain, 2);
-        ctl.abort = 0;
+        if (lane == 0) {
+            mbar_init(&ctl.drain, 2);
+            ctl.abort = 0;
+        }
         fence_barrier_init();
+        if (elect_one()) {
+            prefetch_map(&p.tw);
+            prefetch_map(&p.tfew);
+            prefetch_map(&p.ta128);
+        }
+        __syncwarp();
     }
     if (warp == 1) {
         if (PAIR) {
@@ -458,25 +507,37 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             bool ok = true;
             for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
                 const Tile t = tile_at<kRows>(p, prefix, nt, BN, u);
-                const int boxes = !PAIR && t.rows <= 64 ? (t.rows + kRowBox - 1) / kRowBox : 0;  // 0: one of 128 rows
-                const uint32_t bytes = kCtas * ((boxes ? boxes * kRowBox : kTileRows) * 128 + kWBytes);
-                for (int kb = 0; kb < p.KB; kb++) {
+                // rows by boxes of box_rows, or (0) by one of 128; boxes of several blocks lie as the blocks do
+                // only if one holds all rows
+                const int boxes = PAIR ? 0
+                                : p.M <= kFewRows ? 1
+                                : G == 1 && t.rows <= kFewRows ? (t.rows + p.box_rows - 1) / p.box_rows : 0;
+                const int abytes = (boxes ? boxes * p.box_rows : kTileRows) * 128;
+                for (int kb0 = 0; kb0 < p.KB; kb0 += G) {
                     ok = __all_sync(0xffffffffu, mm_wait(&ctl.empty[s], phase, abort, p.status, 1));
                     if (!ok) break;
-                    uint8_t* as = ast + s * p.a_bytes;
+                    const int n = p.blocked ? G : min(G, p.KB - kb0);  // blocks copied (past the last: zeros)
+                    uint8_t *as = ast + s * G * p.a_bytes, *ws = wst + s * G * kWBytes;
                     if (elect_one()) {
-                        if (rank == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
+                        if (rank == 0) mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)(kCtas * n * (abytes + kWBytes)));
                         if (PAIR) {  // the leader's barrier counts both CTAs' bytes
                             const uint32_t bar = leader_addr(&ctl.full[s]);
-                            tma_3d_pair(wst + s * kWBytes, &p.tw, kb * 128, t.n0 + rank * (BN / 2), t.e, bar);
-                            tma_2d_pair(as, &p.ta128, kb * 128, t.row0 + rank * kTileRows, bar);
+                            const int x = p.blocked ? 0 : kb0 * 128, z = p.blocked ? kb0 : 0;
+                            tma_w_pair(ws, &p.tw, x, t.n0 + rank * (BN / 2), z, t.e, bar);
+                            tma_a_pair(as, &p.ta128, x, t.row0 + rank * kTileRows, z, bar);
                         } else {
-                            tma_3d(wst + s * kWBytes, &p.tw, kb * 128, t.n0, t.e, &ctl.full[s]);
-                            if (boxes) {
-                                for (int b = 0; b < boxes; b++)
-                                    tma_2d(as + b * kRowBox * 128, &p.ta16, kb * 128, t.row0 + b * kRowBox, &ctl.full[s]);
-                            } else {
-                                tma_2d(as, &p.ta128, kb * 128, t.row0, &ctl.full[s]);
+                            // a copy takes the issuing thread 90 to 170 cycles: one for a group's blocks where there
+                            // can be
+                            for (int g = 0; g < (p.blocked ? 1 : n); g++) {
+                                const int x = p.blocked ? 0 : (kb0 + g) * 128, z = p.blocked ? kb0 : 0;
+                                tma_w(ws + g * kWBytes, &p.tw, x, t.n0, z, t.e, &ctl.full[s]);
+                                if (boxes) {
+                                    for (int b = 0; b < boxes; b++)
+                                        tma_a(as + g * p.a_bytes + b * p.box_rows * 128, &p.tfew, x, t.row0 + b * p.box_rows, z,
+                                              &ctl.full[s]);
+                                } else {
+                                    tma_a(as + g * p.a_bytes, &p.ta128, x, t.row0, z, &ctl.full[s]);
+                                }
                             }
                         }
                     }
@@ -502,18 +563,21 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                     (void)mbar_wait(&ctl.full[i % stages], (uint32_t)(i / stages) & 1, 1000000ull);
         } else if (warp < 3 && rank == 0) {
             // ------------------------------------------------------ MMA
-            // Issuing a block's instructions and looking at its barriers takes one warp 400 to 500 cycles, as long
-            // as the tensor cores take for it: two warps take turns.  Warp w has accumulators w and w + 2: the
-            // widest tile's half w of every block, else every second block.
+            // Issuing a group's instructions and looking at its barriers takes one warp 400 cycles and more, as long as
+            // the tensor cores take for it: two warps take turns.  Warp w has half w of every block of the widest
+            // tile, else every second group; its accumulators are w and w + 2, and, the number of stages being
+            // even, its stages every second one: it sees each phase of the barriers that it waits on.
             constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kRows, S::kAccCols);
-            constexpr int kTurn = 2 / S::kHalves;  // blocks from one of the warp's to the next
+            constexpr int kTurn = 2 / S::kHalves;  // groups of blocks from one of the warp's to the next
             const int w = warp - 1, h = S::kHalves == 2 ? w : 0;
-            int64_t blocks = 0;  // of this CTA
-            for (int64_t u = first_tile; u < n_tiles; u += tile_step) blocks += p.KB;
+            const int per = (p.KB + G - 1) / G;    // groups of a tile
+            int64_t groups = 0;                    // of this CTA
+            if (first_tile < n_tiles) groups = ((n_tiles - 1 - first_tile) / tile_step + 1) * per;
+            int at = S::kHalves == 2 ? 0 : w % per;  // the group's number in its tile
             int s = S::kHalves == 2 ? 0 : w % stages, a = w;
             uint32_t phase = S::kHalves == 2 ? 0 : (w / stages) & 1, aphase = 1;
             bool ok = true;
-            for (int64_t c = S::kHalves == 2 ? 0 : w; c < blocks && ok; c += kTurn) {
+            for (int64_t c = S::kHalves == 2 ? 0 : w; c < groups && ok; c += kTurn) {
                 // both are looked at together: most often they are complete, and two waits cost twice one
                 const bool e = mbar_done(&ctl.accempty[a], aphase), f = mbar_done(&ctl.full[s], phase);
                 if (!__all_sync(0xffffffffu, e && f)) {
@@ -524,12 +588,19 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                 }
                 tc::fence_after();
                 if (elect_one()) {
-                    const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * p.a_bytes));
-                    const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * kWBytes + h * (kWBytes / S::kHalves)));
+                    const uint64_t ad = tc::sdesc_sw128(smem_u32(ast + s * G * p.a_bytes));
+                    const uint64_t wd = tc::sdesc_sw128(smem_u32(wst + s * G * kWBytes + h * (kWBytes / S::kHalves)));
+                    const int n = min(G, p.KB - at * G);
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {  // 32 of K: 32 bytes, 2 units of the descriptors
-                        if (PAIR) mma_f8_pair(tbase + a * S::kAccCols, ad + 2 * k, wd + 2 * k, id, k > 0);
-                        else mma_f8(tbase + a * S::kAccCols, ad + 2 * k, wd + 2 * k, id, k > 0);
+                    for (int g = 0; g < G; g++) {
+                        if (g < n) {
+                            const uint64_t ag = ad + (uint64_t)(g * (p.a_bytes >> 4)), wg = wd + (uint64_t)(g * (kWBytes >> 4));
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {  // 32 of K: 32 bytes, 2 units of the descriptors
+                                if (PAIR) mma_f8_pair(tbase + a * S::kAccStep, ag + 2 * k, wg + 2 * k, id, k > 0);
+                                else mma_f8(tbase + a * S::kAccStep + g * S::kAccCols, ag + 2 * k, wg + 2 * k, id, k > 0);
+                            }
+                        }
                     }
                     if (PAIR) {
                         commit_pair(&ctl.accfull[a]);
@@ -540,8 +611,10 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                     }
                 }
                 __syncwarp();
+                at += kTurn;
+                while (at >= per) at -= per;
                 s += kTurn;
-                if (s >= stages) {
+                while (s >= stages) {
                     s -= stages;
                     phase ^= 1;
                 }
@@ -636,13 +709,24 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                 if (!ok) break;
                 const MmScales& sc = ctl.scales[slot];
                 const int n = min(kScaleGroup, p.KB - kb0);
-                for (int i = 0; i < n; i++) {
-                    float scale[S::kRuns];
+                for (int i = 0; i < n; i += G) {
+                    float scale[G][S::kRuns];
 #pragma unroll
-                    for (int q = 0; q < S::kRuns; q++) scale[q] = sc.a[i][r] * sc.w[col_at(q) / kScaleCols][i];
+                    for (int g = 0; g < G; g++)  // past the last block: a number that is not used
+#pragma unroll
+                        for (int q = 0; q < S::kRuns; q++)
+                            scale[g][q] = sc.a[i + g][r] * sc.w[col_at(q) / kScaleCols][i + g];
                     ok = __all_sync(0xffffffffu, mm_wait(&ctl.accfull[a], aphase, abort, p.status, 4));
                     if (!ok) break;
-                    add_block<BN>(acc, tc::taddr(tbase, quad * 32, a * S::kAccCols + sub * S::kCols), scale, accempty + a * 8, lane);
+                    const uint32_t src = tc::taddr(tbase, quad * 32, a * S::kAccStep + sub * S::kCols);
+                    if constexpr (G == 1) {
+                        add_block<BN, PAIR>(acc, src, scale[0], accempty + a * 8, lane);
+                    } else {
+                        float flat[G];
+#pragma unroll
+                        for (int g = 0; g < G; g++) flat[g] = scale[g][0];
+                        add_group<BN, PAIR>(acc[0], src, flat, n - i, accempty + a * 8, lane);
+                    }
                     if ((a += S::kHalves) >= S::kAcc) {
                         a = h;
                         aphase ^= 1;
@@ -707,12 +791,16 @@ bool encode_out(CUtensorMap* m, void* base, int dtype, const uint64_t* dims, uin
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode8(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides, uint32_t box_rows) {
+// rows x K codes (E of them, one after the other, if it is w) as the kernel's boxes take them.
+bool encode8(CUtensorMap* m, bool w, const void* base, int K, int64_t rows, int64_t stride, int E, int64_t expert_stride,
+             bool blocked, uint32_t box_rows, uint32_t box_blocks) {
     EncodeFn fn = get_encode();
     if (!fn) return false;
-    const cuuint32_t box[3] = {128, box_rows, 1}, es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base),
-              reinterpret_cast<const cuuint64_t*>(dims), reinterpret_cast<const cuuint64_t*>(strides), box, es,
+    const cuuint64_t dims[4] = {(cuuint64_t)(blocked ? 128 : K), (cuuint64_t)rows, (cuuint64_t)(blocked ? K / 128 : 1),
+                                (cuuint64_t)E};
+    const cuuint64_t strides[3] = {(cuuint64_t)stride, (cuuint64_t)(blocked ? 128 : stride), (cuuint64_t)expert_stride};
+    const cuuint32_t box[4] = {128, box_rows, blocked ? box_blocks : 1, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, w ? 4 : 3, const_cast<void*>(base), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -756,13 +844,22 @@ cudaError_t mm_facts(MmFacts** out) {
 template <int BN, bool PAIR>
 cudaError_t mm_run(const Fp8MmArgs& g, MmParams& p, const MmFacts& f, int64_t tiles, cudaStream_t st) {
     constexpr int kCtas = PAIR ? 2 : 1;
-    const uint64_t dw[3] = {(uint64_t)g.n_inner, (uint64_t)g.n_cols, (uint64_t)g.n_experts};
-    const uint64_t sw[2] = {(uint64_t)g.w_stride, (uint64_t)g.w_expert_stride};
-    if (!encode8(&p.tw, 3, g.w, dw, sw, BN / kCtas)) return cudaErrorInvalidValue;
-    p.a_bytes = g.n_rows <= 64 ? (g.n_rows + kRowBox - 1) / kRowBox * kRowBox * 128 : kTileRows * 128;
-    const int stage = p.a_bytes + BN / kCtas * 128;
+    constexpr int G = MmShape<BN>::kGroup;
+    const bool few = g.n_rows <= kFewRows;
+    p.blocked = g.n_inner % 128 == 0;
+    p.box_rows = few ? (g.n_rows + kRowBox - 1) / kRowBox * kRowBox : kRowBox;
+    p.a_bytes = few ? p.box_rows * 128 : kTileRows * 128;
+    if (!encode8(&p.tw, true, g.w, g.n_inner, g.n_cols, g.w_stride, g.n_experts, g.w_expert_stride, p.blocked, BN / kCtas, G) ||
+        !encode8(&p.tfew, false, g.a, g.n_inner, g.n_rows, g.a_stride, 1, 0, p.blocked, p.box_rows, G) ||
+        !encode8(&p.ta128, false, g.a, g.n_inner, g.n_rows, g.a_stride, 1, 0, p.blocked, kTileRows, G))
+        return cudaErrorInvalidValue;
+    const int stage = G * (p.a_bytes + BN / kCtas * 128);
     const int tail = kTileRows * 128 - p.a_bytes;  // the last stage's matrix instruction reads 128 rows
     p.stages = std::min(kMaxStages, (f.smem - 1024 - tail - MmShape<BN>::kSumBytes) / stage);
+    // Where the issuing warps take groups in turn, a stage is always the same warp's: it has to see every
+    // phase of the stage's barrier, or it takes the fill before last for the one it waits for.
+    if (MmShape<BN>::kHalves == 1) p.stages &= ~1;
+    if (p.stages < 2) return cudaErrorInvalidConfiguration;
     p.out_at = p.stages * stage + tail;
     const size_t smem = 1024 + (size_t)p.out_at + MmShape<BN>::kSumBytes;
     cudaLaunchConfig_t cfg = {};
@@ -792,8 +889,6 @@ cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t 
     cudaError_t e = mm_facts(&f);
     if (e != cudaSuccess) return e;
     MmParams p = {};
-    const uint64_t da[2] = {(uint64_t)g.n_inner, (uint64_t)g.n_rows}, sa[1] = {(uint64_t)g.a_stride};
-    if (!encode8(&p.ta16, 2, g.a, da, sa, kRowBox) || !encode8(&p.ta128, 2, g.a, da, sa, kTileRows)) return cudaErrorInvalidValue;
     p.sa = g.a_scale;
     p.sw = g.w_scale;
     p.offsets = g.offsets;
