@@ -44,7 +44,7 @@ struct MmParams {
     CUtensorMap tfew;   // a, boxes of box_rows rows
     CUtensorMap ta128;  // a, boxes of 128 rows
     CUtensorMap tw;     // w, boxes of BN rows
-    CUtensorMap tout;   // out, boxes of 32 rows x 128 bytes
+    CUtensorMap tout;   // out, boxes of 32 rows x 64 bytes
     const float* sa;
     const float* sw;
     const int32_t* offsets;
@@ -249,6 +249,8 @@ __device__ __forceinline__ Tile tile_at(const MmParams& p, const int* prefix, in
     return t;
 }
 
+constexpr int kStage = 2048;  // bytes of a summing warp's staging rows: 32 of 64 bytes
+
 template <int BN>
 struct MmShape {
     // The widest tile is two accumulators of 128 columns, filled and read one after the other: with one of
@@ -268,7 +270,7 @@ struct MmShape {
     static constexpr int kRun = kCols < 64 ? kCols : 64;        // what lies together in a pair's accumulator and in w
     static constexpr int kRuns = kCols / kRun;
     static constexpr int kLoad = BN == 256 ? 16 : kRun < 32 ? kRun : 32;  // columns of one tensor-memory load
-    static constexpr int kSumBytes = kSumWarps * 4096;          // staging rows of the summing warps
+    static constexpr int kSumBytes = kSumWarps * kStage;          // staging rows of the summing warps
 };
 
 // Registers a thread of the widest tile: the launch's 168 x 384 are dealt out as 56 for warps 0-3 and
@@ -338,20 +340,23 @@ __device__ __forceinline__ void add_group(float2 (&acc)[MmShape<BN>::kRun / 2], 
     }
 }
 
-// A warp's 32 rows of the tile (a thread a row, COLS columns) to memory.  Pieces of up to 128 bytes a row
-// go through the warp's 4096 bytes of shared memory, 16-byte parts swapped about as the 128-byte swizzle
-// does: whole pieces are then copied out by TMA while the warp goes on, or, where rows of the tile are
+// Where byte b of row r lies in the staging rows: as the 64-byte swizzle of a tensor map has it, which
+// spreads a column of 16-byte parts over all banks.
+__device__ __forceinline__ int stage_at(int r, int b) { return r * 64 + ((((b >> 4) ^ (r >> 1)) & 3) << 4) + (b & 15); }
+
+// A warp's 32 rows of the tile (a thread a row, COLS columns) to memory.  Pieces of up to 64 bytes a row
+// go through the warp's staging rows (pieces of 128 took a stage's room, and time): whole pieces are then copied out by TMA while the warp goes on, or, where rows of the tile are
 // not the call's or the output is not aligned for that, stored by neighbouring lanes.  (Stored from the
 // registers as they lie, 32 rows at a time, a tile's end took 9000 cycles.)
 template <int COLS, bool F32>
 __device__ __forceinline__ void store_rows(const MmParams& p, const float2 (&acc)[COLS / 2], uint8_t* stage, int row0,
                                            int rows, int col0, int lane) {
     constexpr int kSize = F32 ? 4 : 2;
-    constexpr int kPiece = COLS * kSize < 128 ? COLS * kSize : 128;  // bytes of a row stored at a time
+    constexpr int kPiece = COLS * kSize < 64 ? COLS * kSize : 64;  // bytes of a row stored at a time
     constexpr int kPieceCols = kPiece / kSize;
     constexpr int kLanes = kPiece / 16;                              // lanes a row
     constexpr int kStep = 32 / kLanes;                               // rows an instruction
-    const bool tma = kPiece == 128 && p.out_tma && (rows >= 32 || !p.offsets);
+    const bool tma = kPiece == 64 && p.out_tma && (rows >= 32 || !p.offsets);
 #pragma unroll
     for (int c = 0; c < COLS; c += kPieceCols) {
         const int n = min(kPieceCols, p.N - col0 - c);  // columns of this piece that are there
@@ -369,7 +374,7 @@ __device__ __forceinline__ void store_rows(const MmParams& p, const float2 (&acc
                 w = make_uint4(pack_bf16(a[0].x, a[0].y), pack_bf16(a[1].x, a[1].y), pack_bf16(a[2].x, a[2].y),
                                pack_bf16(a[3].x, a[3].y));
             }
-            *reinterpret_cast<uint4*>(stage + tc::sw128_offset(lane, 16 * i)) = w;
+            *reinterpret_cast<uint4*>(stage + stage_at(lane, 16 * i)) = w;
         }
         if (tma) fence_proxy_async_smem();
         __syncwarp();
@@ -387,13 +392,13 @@ __device__ __forceinline__ void store_rows(const MmParams& p, const float2 (&acc
             for (int r = lane / kLanes; r < 32; r += kStep)
                 if (r < rows && l * (16 / kSize) < n)
                     *reinterpret_cast<uint4*>(o + r * p.out_stride * kSize) =
-                        *reinterpret_cast<const uint4*>(stage + tc::sw128_offset(r, 16 * l));
+                        *reinterpret_cast<const uint4*>(stage + stage_at(r, 16 * l));
         } else {
             const int last = min(32, rows);
             for (int r = 0; r < last; r++)
                 for (int j = lane; j < n; j += 32) {
                     const int64_t at = (row0 + r) * p.out_stride + col0 + c + j;
-                    const uint8_t* v = stage + tc::sw128_offset(r, kSize * j);
+                    const uint8_t* v = stage + stage_at(r, kSize * j);
                     if (F32) static_cast<float*>(p.out)[at] = *reinterpret_cast<const float*>(v);
                     else static_cast<uint16_t*>(p.out)[at] = *reinterpret_cast<const uint16_t*>(v);
                 }
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
         int a = h;
         uint32_t aphase = 0;
         bool ok = true;
-        uint8_t* stage = sm + p.out_at + (warp - kFirstSum) * 4096;
+        uint8_t* stage = sm + p.out_at + (warp - kFirstSum) * kStage;
         int slot = 0;
         uint32_t scphase = 0;
         for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
@@ -784,10 +789,10 @@ EncodeFn get_encode() {
 bool encode_out(CUtensorMap* m, void* base, int dtype, const uint64_t* dims, uint64_t stride) {
     EncodeFn fn = get_encode();
     if (!fn) return false;
-    const cuuint32_t box[2] = {(cuuint32_t)(128 / type_size(dtype)), 32}, es[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)(64 / type_size(dtype)), 32}, es[2] = {1, 1};
     const cuuint64_t d[2] = {dims[0], dims[1]}, st[1] = {stride};
     return fn(m, dtype == QS_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d, st, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -170,3 +170,24 @@ def test_grouped_with_tiles_of_two_ctas(counts, cols, inner, kind):
         test_grouped("wide", cols, inner, kind)
     finally:
         del COUNTS["wide"]
+
+
+@pytest.mark.parametrize("rows,cols,inner", [(128, 8192, 4096), (300, 4104, 4096), (512, 8192, 1024), (1, 8192, 4096), (40, 2048, 4096), (100, 1000, 2000)])
+def test_same_bits_every_time(rows, cols, inner):
+    """Copies that land in another order, as they do when memory is busy, change nothing."""
+    g = torch.Generator().manual_seed(rows)
+    a, sa = operand((rows, inner), (rows, blocks(inner)), g)
+    w, sw = operand((cols, inner), (blocks(cols), blocks(inner)), g)
+    ws = qm.alloc_fp8_matmul_workspace(rows, cols, inner)
+    first = torch.empty(rows, cols, device="cuda")
+    qm.qs_fp8_matmul(a, sa, w, sw, first, ws)
+    check(first, values(a, sa, False), values(w, sw, True), torch.float32)
+    src = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    dst, side, out = torch.empty_like(src), torch.cuda.Stream(), torch.empty_like(first)
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            dst.copy_(src)
+        out.fill_(7)
+        qm.qs_fp8_matmul(a, sa, w, sw, out, ws)
+        assert torch.equal(out, first)
+    assert qm.qs_read_device_status(ws) == qm.QS_OK
