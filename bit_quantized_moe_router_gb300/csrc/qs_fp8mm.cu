@@ -60,7 +60,7 @@ struct MmParams {
 
 // Scales on their way to the summing warps: kScaleRing groups of kScaleGroup blocks.  Rows are 132 apart
 // so that the eight blocks of a row, read together, are stored to different banks.
-constexpr int kScaleGroup = 8, kScaleRing = 3;
+constexpr int kScaleGroup = 8, kScaleRing = 2;
 struct MmScales {
     float a[kScaleGroup][kTileRows + 4];
     float w[2][kScaleGroup];  // of the tile's first and second 128 columns
@@ -223,28 +223,29 @@ struct Tile {
     int e, row0, rows, n0;  // expert, first row of a, rows that are the tile's, first weight row
 };
 
+// The call's groups of rows: row tiles of the experts before e, and e's first row (entries of `offsets`
+// clipped to the rows there are; one group without them).  In shared memory: every role looks up every tile.
+struct Groups {
+    int prefix[1025], first[1025];
+};
+
 // Tiles of the call, by number: experts ascending, inside one the weight tiles, inside one the row
-// tiles, so that CTAs side by side share a weight tile.  prefix[e]: row tiles of the experts before e.
+// tiles, so that CTAs side by side share a weight tile.
 template <int ROWS>
-__device__ __forceinline__ Tile tile_at(const MmParams& p, const int* prefix, int nt, int BN, int64_t tile) {
+__device__ __forceinline__ Tile tile_at(const MmParams& p, const Groups& g, int nt, int BN, int64_t tile) {
     Tile t;
-    int lo = 0, first = 0, mt = prefix[p.E];
-    if (p.offsets) {
-        int hi = p.E;  // last e with prefix[e] * nt <= tile that has a tile
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if ((int64_t)prefix[mid] * nt <= tile) lo = mid;
-            else hi = mid;
-        }
-        first = min(max(p.offsets[lo], 0), p.M);
-        mt = prefix[lo + 1] - prefix[lo];
+    int lo = 0, hi = p.E;  // last e with prefix[e] * nt <= tile: it has a tile
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)g.prefix[mid] * nt <= tile) lo = mid;
+        else hi = mid;
     }
-    const int local = (int)(tile - (int64_t)prefix[lo] * nt);
-    const int last = p.offsets ? min(max(p.offsets[lo + 1], 0), p.M) : p.M;
+    const int mt = g.prefix[lo + 1] - g.prefix[lo];
+    const int local = (int)(tile - (int64_t)g.prefix[lo] * nt);
     const int n = local / mt, m = local - n * mt;
     t.e = lo;
-    t.row0 = first + m * ROWS;
-    t.rows = min(ROWS, last - t.row0);
+    t.row0 = g.first[lo] + m * ROWS;
+    t.rows = min(ROWS, g.first[lo + 1] - t.row0);
     t.n0 = n * BN;
     return t;
 }
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
     extern __shared__ uint8_t mm_smem[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~(uintptr_t)1023);
     __shared__ MmCtl ctl;
-    __shared__ int prefix[1025];
+    __shared__ Groups groups_of;
     // known to be the same in a warp, so that what follows from it may live in uniform registers
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_rank() : 0;
@@ -469,30 +470,37 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
     }
     pdl_wait();
     pdl_launch_next();
-    if (warp == 0) {
-        if (p.offsets) {
-            int carry = 0;
-            for (int b = 0; b < p.E; b += 32) {
-                const int e = b + lane;
-                int c = 0;
-                if (e < p.E) {
-                    const int r0 = min(max(p.offsets[e], 0), p.M), r1 = min(max(p.offsets[e + 1], 0), p.M);
-                    c = r1 > r0 ? (r1 - r0 + kRows - 1) / kRows : 0;
-                }
-                int s = c;
+    if (p.offsets) {
+        for (int e = threadIdx.x; e <= p.E; e += S::kThreads)
+            groups_of.first[e] = min(max(p.offsets[e], 0), p.M);
+        __syncthreads();
+        if (warp == 0) {
+            // a lane has the row tiles of `per` experts side by side: its sum, the sum of the lanes before, and again
+            const int per = (p.E + 31) / 32;
+            auto tiles_of = [&](int e) {
+                const int c = e < p.E ? groups_of.first[e + 1] - groups_of.first[e] : 0;
+                return c > 0 ? (c + kRows - 1) / kRows : 0;
+            };
+            int sum = 0;
+            for (int k = 0; k < per; k++) sum += tiles_of(lane * per + k);
+            int run = sum;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, s, o);
-                    if (lane >= o) s += v;
-                }
-                if (e < p.E) prefix[e] = carry + s - c;
-                carry += __shfl_sync(0xffffffffu, s, 31);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += v;
             }
-            if (lane == 0) prefix[p.E] = carry;
-        } else if (lane == 0) {
-            prefix[0] = 0;
-            prefix[1] = (p.M + kRows - 1) / kRows;
+            run -= sum;
+            for (int k = 0; k < per; k++) {
+                const int e = lane * per + k;
+                if (e <= p.E) groups_of.prefix[e] = run;
+                run += tiles_of(e);
+            }
+            if (lane == 31) groups_of.prefix[p.E] = run;
         }
+    } else if (threadIdx.x == 0) {
+        groups_of.first[0] = groups_of.prefix[0] = 0;
+        groups_of.first[1] = p.M;
+        groups_of.prefix[1] = (p.M + kRows - 1) / kRows;
     }
     tc::fence_before();
     __syncthreads();
@@ -500,7 +508,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
     tc::fence_after();
     const uint32_t tbase = ctl.tmem;
     const int nt = (p.N + BN - 1) / BN;
-    const int64_t n_tiles = (int64_t)prefix[p.E] * nt;
+    const int64_t n_tiles = (int64_t)groups_of.prefix[p.E] * nt;
 
     if (warp < kFirstSum) {
         if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             int64_t filled = 0;
             bool ok = true;
             for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
-                const Tile t = tile_at<kRows>(p, prefix, nt, BN, u);
+                const Tile t = tile_at<kRows>(p, groups_of, nt, BN, u);
                 // rows by boxes of box_rows, or (0) by one of 128; boxes of several blocks lie as the blocks do
                 // only if one holds all rows
                 const int boxes = PAIR ? 0
@@ -648,7 +656,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             uint32_t phase = 1;
             bool ok = true;
             for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
-                const Tile t = tile_at<kRows>(p, prefix, nt, BN, u);
+                const Tile t = tile_at<kRows>(p, groups_of, nt, BN, u);
                 const int rows = min(kTileRows, t.rows - rank * kTileRows);
                 const float* sa = p.sa + (int64_t)(t.row0 + rank * kTileRows) * p.sa_stride;
                 for (int kb0 = 0; kb0 < p.KB; kb0 += kScaleGroup) {
@@ -745,7 +753,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                 }
             }
             if (!ok) break;
-            const Tile now = tile_at<kRows>(p, prefix, nt, BN, u);
+            const Tile now = tile_at<kRows>(p, groups_of, nt, BN, u);
             const int row0 = now.row0 + rank * kTileRows + quad * 32, rows = now.rows - rank * kTileRows - quad * 32;
             if (rows <= 0) continue;
 #pragma unroll
@@ -828,7 +836,7 @@ cudaError_t mm_facts(MmFacts** out) {
         int optin = 0, n_sm = 0;
         if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
-        f.smem = optin - (int)(sizeof(MmCtl) + 1025 * 4 + 64);
+        f.smem = optin - (int)(sizeof(MmCtl) + sizeof(Groups) + 64);
         const void* fns[6] = {(const void*)fp8_mm_kernel<16, false>,  (const void*)fp8_mm_kernel<32, false>,
                               (const void*)fp8_mm_kernel<64, false>,  (const void*)fp8_mm_kernel<128, false>,
                               (const void*)fp8_mm_kernel<256, false>, (const void*)fp8_mm_kernel<256, true>};

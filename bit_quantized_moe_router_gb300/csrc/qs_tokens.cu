@@ -22,6 +22,7 @@ constexpr int kSmallN = 2048;   // entries of the one-launch form
 constexpr int kChunk = 1024;    // least entries of a chunk of the sort
 constexpr int kMaxChunks = 256; // most chunks
 constexpr int kSortThreads = 256;
+constexpr int kPlaceThreads = 1024;
 
 int chunk_entries(int64_t n) {
     const int64_t c = (n + kMaxChunks - 1) / kMaxChunks;
@@ -130,66 +131,62 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_hist_kernel(const int32
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(size_t)blockIdx.x * E + e] = sm[e];
 }
 
-// sm: total[E], off[E + 1], then the warps' running positions wrun[8][E].  Each warp owns an eighth
-// of the chunk, in order, so positions ascend with the entries within an expert.
-__global__ void __launch_bounds__(kSortThreads) dispatch_place_kernel(const DispatchArgs p, int n, int chunk, int chunks) {
+// A chunk a CTA, 1024 entries at a time.  An entry's position: its expert's offset, the entries of that expert in
+// earlier chunks and earlier in this one -- those of earlier warps from the warps' counts (a byte each: a warp
+// has 32 entries), those of its own warp from a match.  sm: total[E], off[E + 1], base[E], then cnt[32][E] bytes.
+__global__ void __launch_bounds__(kPlaceThreads) dispatch_place_kernel(const DispatchArgs p, int n, int chunk, int chunks) {
     extern __shared__ int32_t sm[];
     const int E = p.n_experts, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int32_t *total = sm, *off = sm + E, *wrun = sm + 2 * E + 1;
+    int32_t *total = sm, *off = sm + E, *base = off + E + 1;
+    uint8_t* cnt = reinterpret_cast<uint8_t*>(base + E);
     pdl_wait();
     pdl_launch_next();
-    for (int i = threadIdx.x; i < 8 * E; i += blockDim.x) wrun[i] = 0;
+    for (int e = threadIdx.x; e < E; e += kPlaceThreads) total[e] = base[e] = 0;
     __syncthreads();
-    const int64_t i0 = (int64_t)blockIdx.x * chunk, i1 = min((int64_t)n, i0 + chunk);
-    const int seg = chunk / 8;  // a chunk is a multiple of 32, so seg is one of 4
-    const int64_t s0 = min(i1, i0 + (int64_t)warp * seg), s1 = min(i1, s0 + seg);
-    for (int64_t i = s0 + lane; i < s1; i += 32) {
-        const int e = p.ids[i];
-        if ((unsigned)e < (unsigned)E) atomicAdd(&wrun[warp * E + e], 1);
-    }
-    // chunks before this one, and all of them
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    // all chunks, and those before this one: four threads an expert, each a quarter of the chunks, so that the
+    // loads of a thread are in flight together (one thread an expert took 9 us of 15)
+    const int per = (chunks + 3) / 4, c0 = threadIdx.x / (kPlaceThreads / 4) * per, c1 = min(chunks, c0 + per);
+    for (int e = threadIdx.x % (kPlaceThreads / 4); e < E; e += kPlaceThreads / 4) {
         int before = 0, all = 0;
 #pragma unroll 16
-        for (int c = 0; c < chunks; c++) {
+        for (int c = c0; c < c1; c++) {
             const int h = p.hist[(size_t)c * E + e];
             all += h;
             before += c < (int)blockIdx.x ? h : 0;
         }
-        total[e] = all;
-        off[e] = before;
-    }
-    __syncthreads();
-    // wrun[w][e]: entries of e before warp w's segment, in this chunk and earlier ones
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int run = off[e];
-        for (int w = 0; w < 8; w++) {
-            const int c = wrun[w * E + e];
-            wrun[w * E + e] = run;
-            run += c;
-        }
+        if (all) atomicAdd(&total[e], all);
+        if (before) atomicAdd(&base[e], before);
     }
     __syncthreads();
     if (warp == 0) scan_counts(total, off, E);
     __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kPlaceThreads) base[e] += off[e];
     if (blockIdx.x == 0) {
-        for (int e = threadIdx.x; e < E; e += blockDim.x) p.counts[e] = total[e];
-        for (int e = threadIdx.x; e <= E; e += blockDim.x) p.offsets[e] = off[e];
+        for (int e = threadIdx.x; e < E; e += kPlaceThreads) p.counts[e] = total[e];
+        for (int e = threadIdx.x; e <= E; e += kPlaceThreads) p.offsets[e] = off[e];
     }
+    const int64_t i0 = (int64_t)blockIdx.x * chunk, i1 = min((int64_t)n, i0 + chunk);
     // this chunk's share of perm's tail
-    for (int64_t i = max(i0, (int64_t)off[E]) + threadIdx.x; i < i1; i += blockDim.x) p.perm[i] = -1;
-    for (int64_t b = s0; b < s1; b += 32) {
-        const int64_t i = b + lane;
-        const int e = i < s1 ? p.ids[i] : -1;
+    for (int64_t i = max(i0, (int64_t)off[E]) + threadIdx.x; i < i1; i += kPlaceThreads) p.perm[i] = -1;
+    for (int64_t b = i0; b < i1; b += kPlaceThreads) {
+        const int64_t i = b + threadIdx.x;
+        const int e = i < i1 ? p.ids[i] : -1;
         const bool valid = (unsigned)e < (unsigned)E;
+        for (int k = threadIdx.x; k < 8 * E; k += kPlaceThreads) reinterpret_cast<uint32_t*>(cnt)[k] = 0;  // 32 E bytes
+        __syncthreads();
         const unsigned peers = __match_any_sync(0xffffffffu, valid ? e : -1);
+        const bool lead = valid && lane == __ffs(peers) - 1;
+        if (lead) cnt[warp * E + e] = (uint8_t)__popc(peers);
+        __syncthreads();
         int at = -1;
-        if (valid) at = off[e] + wrun[warp * E + e] + __popc(peers & ((1u << lane) - 1u));
-        if (i < s1) p.pos[i] = at;
-        if (valid) p.perm[at] = (int32_t)i;
-        __syncwarp();
-        if (valid && lane == __ffs(peers) - 1) wrun[warp * E + e] += __popc(peers);
-        __syncwarp();
+        if (valid) {
+            at = base[e] + __popc(peers & ((1u << lane) - 1u));
+            for (int w = 0; w < warp; w++) at += cnt[w * E + e];
+            p.perm[at] = (int32_t)i;
+        }
+        if (i < i1) p.pos[i] = at;
+        __syncthreads();
+        if (lead) atomicAdd(&base[e], __popc(peers));  // for the next 1024
     }
 }
 
@@ -357,8 +354,8 @@ cudaError_t dispatch_run(const DispatchArgs& p, cudaStream_t st) {
     cudaError_t e = launch_pdl(dispatch_hist_kernel, dim3(chunks), kSortThreads, p.n_experts * 4, st, p.ids, (int)n,
                                p.n_experts, chunk, p.hist);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(dispatch_place_kernel, dim3(chunks), kSortThreads, (10 * p.n_experts + 1) * 4, st, p, (int)n, chunk,
-                   chunks);
+    e = launch_pdl(dispatch_place_kernel, dim3(chunks), kPlaceThreads, (3 * p.n_experts + 1) * 4 + 32 * p.n_experts, st, p,
+                   (int)n, chunk, chunks);
     if (e != cudaSuccess || !p.xs) return e;
     return launch_pdl(dispatch_rows_kernel<W>, dim3(p.n_tokens), row_threads(p.row_bytes / W), 0, st, p);
 }
