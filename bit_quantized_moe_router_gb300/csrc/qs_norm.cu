@@ -95,8 +95,12 @@ __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_kernel(const NormAr
 #pragma unroll
             for (int q = 0; q < 8; q++) s[j][0][q] *= rho;
         }
-        if (p.q)
-            quant_row<VEC, 1>(s[j], factor, least, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, col(j), p.hidden);
+        if (p.q) {
+            uint8_t* q_row = p.q + t * p.q_stride;
+            float* scale_row = p.q_scale + t * p.q_scale_stride;
+            if (VEC) quant_vec<1>(s[j], factor, least, q_row, scale_row, col(j), p.hidden);
+            else quant_any(s[j][0], factor, least, q_row, scale_row, col(j), p.hidden);
+        }
         if (yr) {
 #pragma unroll
             for (int q = 0; q < 8; q++) s[j][0][q] *= factor;
@@ -136,11 +140,15 @@ __global__ void __launch_bounds__(32 * cta_warps(G), B16 && NV == 1 && G <= 8 ? 
 #pragma unroll
         for (int q = 0; q < 8; q++) dw[j][q] = 0.0f;
     if (NV == 1) load8_row<VEC>(p.weight, QS_F32, col(0), p.hidden, w0);
-    if (first < p.n_rows) load(next, first);
+    if (VEC && first < p.n_rows) load(next, first);
     int flip = 0;
     for (int64_t t = first; t < p.n_rows; t += step, flip ^= 1) {
-        here = next;
-        if (t + step < p.n_rows) load(next, t + step);
+        if (VEC) {
+            here = next;
+            if (t + step < p.n_rows) load(next, t + step);
+        } else {  // single elements are held widened: no room for two rows
+            load(here, t);
+        }
         float a[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < NV; j++) {
@@ -183,12 +191,12 @@ __global__ void __launch_bounds__(32 * cta_warps(G), B16 && NV == 1 && G <= 8 ? 
     float* row = p.partial + (int64_t)blockIdx.x * p.part_stride;
     if (kGroups == 1) {
 #pragma unroll
-        for (int j = 0; j < NV; j++) store8_row<true>(row, QS_F32, col(j), p.part_stride, dw[j]);  // hidden rounded up to 8
+        for (int j = 0; j < NV; j++) store8_row<VEC>(row, QS_F32, col(j), p.part_stride, dw[j]);  // hidden rounded up to 8
     } else {
 #pragma unroll
         for (int j = 0; j < NV; j++)
 #pragma unroll
-            for (int q = 0; q < 8; q++) part[group][col(j) + q] = dw[j][q];
+            for (int q = 0; q < 8; q++) part[group][col_of<VEC>(col(j), q)] = dw[j][q];
         __syncthreads();
         for (int i = threadIdx.x; i < p.part_stride; i += blockDim.x) {
             float v = 0.0f;
@@ -243,20 +251,39 @@ __global__ void __launch_bounds__(256) silu_mul_quant_kernel(const SiluArgs p) {
     // a warp's four parts all run the shuffles as long as one has work
     while (__any_sync(0xffffffffu, t < rows)) {
         const bool on = t < rows;
-        const int i = (int)(b * kScaleCols + l * 16);
-        const int n = on ? p.ffn : 0;
-        const uint8_t* row = static_cast<const uint8_t*>(row_at(p.gate_up, p.gate_up_stride, type_size(p.dtype), on ? t : 0));
-        float g[2][8], v[2][8];
+        const int64_t r = on ? t : 0;
+        const uint8_t* row = static_cast<const uint8_t*>(row_at(p.gate_up, p.gate_up_stride, type_size(p.dtype), r));
+        const uint8_t* up = row + (size_t)p.ffn * type_size(p.dtype);
+        uint8_t* q_row = p.q + r * p.q_stride;
+        float* scale_row = p.q_scale + r * p.q_scale_stride;
+        const int first = (int)(b * kScaleCols), n = on ? p.ffn : 0;
+        if (VEC) {  // sixteen neighbours a lane
+            const int i = first + l * 16;
+            float g[2][8], v[2][8];
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
-            load8_row<VEC>(row, p.dtype, i + 8 * k, n, g[k]);
-            load8_row<VEC>(row + (size_t)p.ffn * type_size(p.dtype), p.dtype, i + 8 * k, n, v[k]);
+            for (int k = 0; k < 2; k++) {
+                load8_row<true>(row, p.dtype, i + 8 * k, n, g[k]);
+                load8_row<true>(up, p.dtype, i + 8 * k, n, v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+#pragma unroll
+                for (int q = 0; q < 8; q++) v[k][q] = silu_mul(g[k][q], v[k][q]);
+            quant_vec<2>(v, 1.0f, kMinAmax, q_row, scale_row, i, n);
+        } else {  // every eighth
+            float v[16], a = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 16; q++) {
+                const int c = first + l + 8 * q;
+                v[q] = c < n ? silu_mul(load_x(row, p.dtype, (size_t)c), load_x(up, p.dtype, (size_t)c)) : 0.0f;
+                a = fmaxf(a, fabsf(v[q]));
+            }
+            const BlockCode code(lanes_max(a, 4), 1.0f, kMinAmax);
+            if (l == 0 && first < n) scale_row[b] = code.scale;
+#pragma unroll
+            for (int q = 0; q < 16; q++)
+                if (first + (int)l + 8 * q < n) q_row[first + l + 8 * q] = code.one(v[q]);
         }
-#pragma unroll
-        for (int k = 0; k < 2; k++)
-#pragma unroll
-            for (int q = 0; q < 8; q++) v[k][q] = silu_mul(g[k][q], v[k][q]);
-        quant_row<VEC, 2>(v, 1.0f, kMinAmax, p.q + t * p.q_stride, p.q_scale + t * p.q_scale_stride, i, n);
         t += dt;
         b += db;
         if (b >= nb) {

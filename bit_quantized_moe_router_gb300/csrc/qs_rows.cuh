@@ -20,8 +20,19 @@ __host__ __device__ constexpr int scale_blocks(int cols) { return (cols + kScale
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Elements i .. i+7 of a row as fp32; those at and past n are 0.  VEC: the row is 16-byte aligned,
-// i a multiple of 8 and n too, so the eight are there or not as one.
+// A warp takes 256 columns of a row at a time, a lane eight of them: i is the warp's first plus 8 * lane.
+// VEC (the row 16-byte aligned, its length a multiple of 8): columns i .. i+7, one or two vectors, there or not
+// as one.  Else every 32nd column from the warp's first plus lane, so that the lanes' single elements are neighbours.
+template <bool VEC>
+__device__ __forceinline__ int col_of(int i, int q) {
+    const int lane = threadIdx.x & 31;
+    return VEC ? i + q : i - 7 * lane + 32 * q;
+}
+// Whether a warp at i has a column below n.
+template <bool VEC>
+__device__ __forceinline__ bool cols_left(int i, int n) { return (VEC ? i : i - 8 * (int)(threadIdx.x & 31)) < n; }
+
+// A lane's eight elements as fp32; those at and past n are 0.
 template <bool VEC>
 __device__ __forceinline__ void load8_row(const void* row, int dtype, int i, int n, float (&v)[8]) {
     if (VEC) {
@@ -41,8 +52,19 @@ __device__ __forceinline__ void load8_row(const void* row, int dtype, int i, int
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         }
     } else {
+        if (dtype == QS_BF16) {
 #pragma unroll
-        for (int q = 0; q < 8; q++) v[q] = i + q < n ? load_x(row, dtype, (size_t)(i + q)) : 0.0f;
+            for (int q = 0; q < 8; q++) {
+                const int c = col_of<false>(i, q);
+                v[q] = c < n ? bf16_lo(static_cast<const uint16_t*>(row)[c]) : 0.0f;
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                const int c = col_of<false>(i, q);
+                v[q] = c < n ? static_cast<const float*>(row)[c] : 0.0f;
+            }
+        }
     }
 }
 
@@ -65,14 +87,19 @@ __device__ __forceinline__ void store8_row(void* row, int dtype, int i, int n, c
             p[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
     } else {
+        if (dtype == QS_BF16) {
 #pragma unroll
-        for (int q = 0; q < 8; q++)
-            if (i + q < n) {
-                if (dtype == QS_BF16)
-                    static_cast<__nv_bfloat16*>(row)[i + q] = __float2bfloat16_rn(v[q]);
-                else
-                    static_cast<float*>(row)[i + q] = v[q];
+            for (int q = 0; q < 8; q++) {
+                const int c = col_of<false>(i, q);
+                if (c < n) static_cast<__nv_bfloat16*>(row)[c] = __float2bfloat16_rn(v[q]);
             }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                const int c = col_of<false>(i, q);
+                if (c < n) static_cast<float*>(row)[c] = v[q];
+            }
+        }
     }
 }
 
@@ -85,43 +112,73 @@ __device__ __forceinline__ void* row_at(void* base, int64_t stride, int size, in
 }
 __host__ __device__ constexpr int type_size(int dtype) { return dtype == QS_F32 ? 4 : dtype == QS_BF16 ? 2 : 1; }
 
-// The 16 / N lanes that hold the 128 columns of one scale block, 8 N each (columns i .. i + 8 N - 1; those
-// past n hold 0), of values v * factor with one factor for the row: the block's scale, and the lane's codes.
-// The factor drops out of a code, v * factor * (448 / (amax * factor)), so it is left out of it; 448 / amax is held
-// in two parts (its fp32 value and what that rounding left out), and a code's product has one rounding.
-// least: kMinAmax / factor.  fmaxf drops a NaN: its own code is a NaN and the others of its block keep their
-// scale.  An infinite amax leaves no remainder: all codes of the block are NaNs.
-template <bool VEC, int N>
-__device__ __forceinline__ void quant_row(const float (&v)[N][8], float factor, float least, uint8_t* q_row, float* scale_row,
+// How a scale block's values v * factor (one factor for the row) become codes, from a, the largest |v|.  The factor
+// drops out of a code, v * factor * (448 / (a * factor)), so it is left out of it; 448 / a is held in two parts (its
+// fp32 value and what that rounding left out), and a code's product has one rounding.  least: kMinAmax / factor.
+// An infinite a leaves no remainder: all codes of the block are NaNs.
+struct BlockCode {
+    float inv, rest, scale;
+    __device__ __forceinline__ BlockCode(float a, float factor, float least) {
+        a = fmaxf(a, least);
+        const float part = __frcp_rn(a);
+        inv = kE4m3Max * part;
+        rest = fmaf(-inv, a, kE4m3Max) * part;
+        scale = a * factor * (1.0f / kE4m3Max);
+    }
+    __device__ __forceinline__ float scaled(float v) const { return fmaf(v, inv, v * rest); }
+    __device__ __forceinline__ uint32_t pair(float lo, float hi) const {
+        return __nv_cvt_float2_to_fp8x2(make_float2(scaled(lo), scaled(hi)), __NV_SATFINITE, __NV_E4M3);
+    }
+    __device__ __forceinline__ uint8_t one(float v) const { return __nv_cvt_float_to_fp8(scaled(v), __NV_SATFINITE, __NV_E4M3); }
+};
+
+// Largest |v| of the lanes that differ in the bits below 2 * first.  fmaxf drops a NaN: its own code is a NaN and
+// the others of its block keep their scale.
+__device__ __forceinline__ float lanes_max(float a, int first) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o <= first) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+}
+
+// The 16 / N lanes that hold the 128 columns of one scale block, 8 N neighbours each (columns i .. i + 8 N - 1;
+// those past n hold 0; n a multiple of 8): the block's scale, and the lane's codes.
+template <int N>
+__device__ __forceinline__ void quant_vec(const float (&v)[N][8], float factor, float least, uint8_t* q_row, float* scale_row,
                                           int i, int n) {
     float a = 0.0f;
 #pragma unroll
     for (int k = 0; k < N; k++)
 #pragma unroll
         for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(v[k][q]));
-#pragma unroll
-    for (int o = kScaleCols / (16 * N); o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    a = fmaxf(a, least);
-    const float amax = a * factor, part = __frcp_rn(a), inv = kE4m3Max * part, rest = fmaf(-inv, a, kE4m3Max) * part;
-    const auto scaled = [&](float x) { return fmaf(x, inv, x * rest); };
+    const BlockCode code(lanes_max(a, kScaleCols / (16 * N)), factor, least);
     if (i >= n) return;
-    if (i % kScaleCols == 0) scale_row[i / kScaleCols] = amax * (1.0f / kE4m3Max);
+    if (i % kScaleCols == 0) scale_row[i / kScaleCols] = code.scale;
 #pragma unroll
     for (int k = 0; k < N; k++) {
-        uint32_t w[2];
+        const float* x = v[k];
+        if (i + 8 * k < n)
+            *reinterpret_cast<uint2*>(q_row + i + 8 * k) =
+                make_uint2(code.pair(x[0], x[1]) | (code.pair(x[2], x[3]) << 16), code.pair(x[4], x[5]) | (code.pair(x[6], x[7]) << 16));
+    }
+}
+
+// The same for a warp's 256 columns as col_of<false> has them: two scale blocks, four elements a lane of each.
+__device__ __forceinline__ void quant_any(const float (&v)[8], float factor, float least, uint8_t* q_row, float* scale_row,
+                                          int i, int n) {
+    const int lane = threadIdx.x & 31, first = i - 8 * lane;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const float* x = &v[k][4 * h];
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(scaled(x[0]), scaled(x[1])), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(scaled(x[2]), scaled(x[3])), __NV_SATFINITE, __NV_E4M3);
-            w[h] = lo | (hi << 16);
-        }
-        if (VEC) {
-            if (i + 8 * k < n) *reinterpret_cast<uint2*>(q_row + i + 8 * k) = make_uint2(w[0], w[1]);
-        } else {
+    for (int h = 0; h < 2; h++) {
+        float a = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 8; q++)
-                if (i + 8 * k + q < n) q_row[i + 8 * k + q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
+        for (int q = 4 * h; q < 4 * h + 4; q++) a = fmaxf(a, fabsf(v[q]));
+        const BlockCode code(lanes_max(a, 16), factor, least);
+        const int block = first / kScaleCols + h;
+        if (lane == 0 && block * kScaleCols < n) scale_row[block] = code.scale;
+#pragma unroll
+        for (int q = 4 * h; q < 4 * h + 4; q++) {
+            const int c = col_of<false>(i, q);
+            if (c < n) q_row[c] = code.one(v[q]);
         }
     }
 }
@@ -157,7 +214,7 @@ struct Held8 {
     }
 };
 template <>
-struct Held8<false, false> {  // any alignment: element by element
+struct Held8<false, false> {  // any alignment: single elements, as load8_row has them
     float f[8];
     __device__ __forceinline__ void load(const void* row, int dtype, int i, int n) { load8_row<false>(row, dtype, i, n, f); }
     __device__ __forceinline__ void get(int, float (&v)[8]) const {

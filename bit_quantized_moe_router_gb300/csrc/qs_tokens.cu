@@ -30,11 +30,13 @@ int chunk_entries(int64_t n) {
 }
 int chunk_count(int64_t n) { return (int)((n + chunk_entries(n) - 1) / chunk_entries(n)); }
 
-// Copy one row of n bytes: by 16 where base addresses and strides allow, else by 4, else by 1.
+// Rows are copied by words of 16 bytes where base addresses and strides allow, else of 4, 2 or 1; what is left of a
+// row behind its last whole word, byte by byte.
 template <int W>
 struct Word;
 template <> struct Word<16> { using T = uint4; };
 template <> struct Word<4> { using T = uint32_t; };
+template <> struct Word<2> { using T = uint16_t; };
 template <> struct Word<1> { using T = uint8_t; };
 
 // Exclusive prefix sum of v over the first E threads' values in rounds of the CTA (all threads call).
@@ -107,6 +109,10 @@ __global__ void __launch_bounds__(256) dispatch_small_kernel(const DispatchArgs 
         T* dst = reinterpret_cast<T*>(static_cast<uint8_t*>(p.xs) + at * p.xs_stride);
 #pragma unroll 4
         for (int c = lane; c < p.row_bytes / W; c += 32) dst[c] = src[c];
+        if (W > 1 && lane < p.row_bytes % W) {
+            const int c = p.row_bytes / W * W + lane;
+            reinterpret_cast<uint8_t*>(dst)[c] = reinterpret_cast<const uint8_t*>(src)[c];
+        }
         for (int c = lane; c < p.n_scales; c += 32)
             p.xs_scale[at * p.xs_scale_stride + c] = p.x_scale[t * p.x_scale_stride + c];
     }
@@ -207,6 +213,12 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(const DispatchArgs p
         for (int j = 0; j < p.top_k; j++)
             if (at[j] >= 0) reinterpret_cast<T*>(xs + at[j] * p.xs_stride)[c] = v;
     }
+    if (W > 1 && threadIdx.x < p.row_bytes % W) {
+        const int c = p.row_bytes / W * W + threadIdx.x;
+        const uint8_t v = reinterpret_cast<const uint8_t*>(src)[c];
+        for (int j = 0; j < p.top_k; j++)
+            if (at[j] >= 0) xs[at[j] * p.xs_stride + c] = v;
+    }
     for (int c = threadIdx.x; c < p.n_scales * p.top_k; c += blockDim.x) {
         const int j = c / p.n_scales, b = c - j * p.n_scales;
         if (at[j] >= 0) p.xs_scale[at[j] * p.xs_scale_stride + b] = p.x_scale[t * p.x_scale_stride + b];
@@ -242,7 +254,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs p) {
     }
     __syncthreads();
     void* out = row_at(p.out, p.out_stride, type_size(p.out_dtype), t);
-    for (int i = (blockIdx.y * blockDim.x + threadIdx.x) * 8; i < p.hidden; i += gridDim.y * blockDim.x * 8) {
+    for (int i = (blockIdx.y * blockDim.x + threadIdx.x) * 8; cols_left<VEC>(i, p.hidden); i += gridDim.y * blockDim.x * 8) {
         float acc[8];
 #pragma unroll
         for (int q = 0; q < 8; q++) acc[q] = 0.0f;
@@ -288,7 +300,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineBwdA
         float dot[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; j++) dot[j] = 0.0f;
-        for (int i = threadIdx.x * 8; i < p.hidden; i += blockDim.x * 8) {
+        for (int i = threadIdx.x * 8; cols_left<VEC>(i, p.hidden); i += blockDim.x * 8) {
             float d[8];
             load8_row<VEC>(dr, p.dout_dtype, i, p.hidden, d);
 #pragma unroll
@@ -368,12 +380,12 @@ size_t dispatch_workspace(int n_tokens, int top_k, int n_experts) {
 }
 
 cudaError_t launch_dispatch(const DispatchArgs& p, cudaStream_t st) {
-    // bits that every address and byte count of the rows has in common
-    const uintptr_t all = p.xs ? ((uintptr_t)p.x | (uintptr_t)p.xs | (uintptr_t)p.x_stride | (uintptr_t)p.xs_stride |
-                                  (uintptr_t)p.row_bytes)
-                               : 0;
+    // bits that every row's address has in common
+    const uintptr_t all =
+        p.xs ? ((uintptr_t)p.x | (uintptr_t)p.xs | (uintptr_t)p.x_stride | (uintptr_t)p.xs_stride) : 0;
     if (all % 16 == 0) return dispatch_run<16>(p, st);
     if (all % 4 == 0) return dispatch_run<4>(p, st);
+    if (all % 2 == 0) return dispatch_run<2>(p, st);
     return dispatch_run<1>(p, st);
 }
 
