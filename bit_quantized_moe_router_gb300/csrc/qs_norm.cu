@@ -319,13 +319,15 @@ cudaError_t norm_run(const NormArgs& p, cudaStream_t st) {
 
 template <bool VEC>
 cudaError_t norm_pick(const NormArgs& p, cudaStream_t st) {
-    // two steps a thread keep four loads of 16 bytes in flight; more only for rows past 8192.  (Sixteen
-    // neighbouring elements a thread, which share a block's maximum, took 90 us against 85 at 16384 x 4096.)
+    // Few rows: as many threads a row as have a load, for the least latency (32 x 2048: 2.3 us, with two warps
+    // a row 4.0).  Many: a warp a row where its registers hold it, which needs no barrier (32768 x 1024: 47 us,
+    // with two warps 55, with four 67); 8 warps at 2048 (91 us; four 104, two 89) and at 4096 (85; sixteen 98, four 90).
+    const bool few = p.n_rows <= 304;  // two a SM
     if (p.hidden <= 256) return norm_run<VEC, 1, 1>(p, st);
     if (p.hidden <= 512) return norm_run<VEC, 1, 2>(p, st);
-    if (p.hidden <= 1024) return norm_run<VEC, 2, 2>(p, st);
-    if (p.hidden <= 2048) return norm_run<VEC, 4, 2>(p, st);
-    if (p.hidden <= 4096) return norm_run<VEC, 8, 2>(p, st);
+    if (p.hidden <= 1024) return few ? norm_run<VEC, 4, 1>(p, st) : norm_run<VEC, 1, 4>(p, st);
+    if (p.hidden <= 2048) return norm_run<VEC, 8, 1>(p, st);
+    if (p.hidden <= 4096) return few ? norm_run<VEC, 16, 1>(p, st) : norm_run<VEC, 8, 2>(p, st);
     if (p.hidden <= 8192) return norm_run<VEC, 16, 2>(p, st);
     return norm_run<VEC, 16, 4>(p, st);
 }

@@ -60,7 +60,8 @@ NORM_SLACK = (48 / 2 + 4 + 4) * U + 2 * U
 
 
 @pytest.mark.parametrize("hidden", [1, 7, 8, 100, 128, 129, 256, 264, 520, 1000, 1032, 2048, 2056, 4096, 5000, 8192, 8200, 16384])
-@pytest.mark.parametrize("rows,kind,res", [(1, torch.bfloat16, torch.bfloat16), (5, torch.float32, None), (77, torch.bfloat16, torch.float32)])
+@pytest.mark.parametrize("rows,kind,res", [(1, torch.bfloat16, torch.bfloat16), (5, torch.float32, None), (77, torch.bfloat16, torch.float32),
+                                           (311, torch.bfloat16, torch.bfloat16)])
 def test_norm(hidden, rows, kind, res):
     g = gen(hidden + rows)
     x = torch.randn(rows, hidden, generator=g).to(kind)
