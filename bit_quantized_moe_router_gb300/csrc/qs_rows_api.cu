@@ -123,7 +123,7 @@ int qs_silu_mul_quant(const qs_silu_mul_args* args, void* stream) {
 }
 
 static bool matmul_shape_ok(int n_rows, int n_cols, int n_inner, int n_experts) {
-    return n_rows >= 0 && n_cols >= 1 && n_inner >= 1 && n_inner <= (1 << 30) && n_cols <= (1 << 30) &&
+    return n_rows >= 0 && n_rows <= (1 << 30) && n_cols >= 1 && n_inner >= 1 && n_inner <= (1 << 30) && n_cols <= (1 << 30) &&
            n_experts >= 1 && n_experts <= 1024;
 }
 

@@ -8,7 +8,8 @@
 // own), and the rows, one token a CTA, so that a token's row is read once for its k copies.
 // Combine.  One token a CTA row: sum of w * y[pos] over the slots in ascending order, k loads in
 // flight a thread.  Its gradient reads dout once a token and y once, and writes dy once.
-// All of them move bytes once: the bound is HBM.
+// All of them move bytes once: the bound is HBM.  8192 tokens to 8 of 256 experts, bf16 rows of 2048: rows out 46 us
+// (302 MB), back 49 us (302 MB), the gradient of that 98 us (570 MB); the positions 12 us before.
 #include "qs_internal.h"
 #include "qs_rows.cuh"
 
@@ -18,7 +19,8 @@ namespace qs {
 
 namespace {
 
-constexpr int kSmallN = 2048;   // entries of the one-launch form
+constexpr int kSmallN = 4096;   // entries of the one-launch form: with 8 a token, 256 tokens 5.3 us against 8.8 in three
+                                // launches, 512 9.9 against 10.2, 1024 28.5 against 12.8 (bf16 rows of 2048)
 constexpr int kChunk = 1024;    // least entries of a chunk of the sort
 constexpr int kMaxChunks = 256; // most chunks
 constexpr int kSortThreads = 256;

@@ -452,7 +452,7 @@ typedef struct {
  *        clipped to 0 .. n_rows.
  * out    fp32 or bf16 [n_rows x N]
  * Sums inside a block of 128 are formed by the tensor cores in fp32, the sum over
- * blocks in fp32 in ascending order.  N, K >= 1, E <= 1024.  workspace: at least
+ * blocks in fp32 in ascending order.  n_rows, N, K <= 2^30, N, K >= 1, E <= 1024.  workspace: at least
  * qs_fp8_matmul_workspace_bytes(n_rows, N, K, E), 256-byte aligned, initialised
  * with qs_workspace_init (its header records a wait that ran out).  One launch. */
 size_t qs_fp8_matmul_workspace_bytes(int n_rows, int n_cols, int n_inner, int n_experts);
@@ -482,7 +482,7 @@ typedef struct {
  * xs_scale.  Without xs the plan is made alone.  workspace: at least
  * qs_dispatch_workspace_bytes(n_tokens, top_k, E), 256-byte aligned, needs no
  * initialisation.  n_tokens * top_k <= 2^30, top_k <= 32, E <= 1024.  One
- * launch for up to 2048 entries, else up to three. */
+ * launch for up to 4096 entries, else up to three. */
 size_t qs_dispatch_workspace_bytes(int n_tokens, int top_k, int n_experts);
 int qs_dispatch_tokens(const qs_dispatch_args *args, void *stream);
 

@@ -239,7 +239,8 @@ def routed(tokens, k, experts, g, how):
     (1, 1, 1, 16, torch.float32, "random"), (8, 8, 256, 2048, F8, "random"), (5, 3, 7, 100, F8, "drop"),
     (5, 2, 4, 1, F8, "random"), (33, 8, 64, 520, torch.bfloat16, "drop"), (7, 32, 1024, 24, torch.bfloat16, "random"),
     (256, 8, 16, 64, torch.bfloat16, "drop"), (257, 8, 16, 64, torch.bfloat16, "random"), (1000, 5, 100, 33, torch.bfloat16, "drop"),
-    (300, 8, 256, 128, torch.float32, "one"), (300, 8, 256, 129, torch.float32, "none"), (40, 2, 3, 7, torch.float32, "none"),
+    (512, 8, 16, 64, torch.bfloat16, "drop"), (513, 8, 300, 64, torch.bfloat16, "random"), (600, 8, 256, 128, torch.float32, "one"),
+    (600, 8, 256, 129, torch.float32, "none"), (300, 8, 256, 128, torch.float32, "one"), (300, 8, 256, 129, torch.float32, "none"), (40, 2, 3, 7, torch.float32, "none"),
     (4099, 32, 1024, 8, F8, "drop"), (0, 4, 16, 64, torch.bfloat16, "random")])
 def test_dispatch(tokens, k, experts, hidden, kind, how):
     g = gen(tokens + experts)
