@@ -914,9 +914,10 @@ cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t 
     p.NB = scale_blocks(g.n_cols);
     p.out_dtype = g.out_dtype;
     p.out_vec = g.n_cols % 8 == 0 && ((uintptr_t)g.out & 15u) == 0 && (g.out_stride * type_size(g.out_dtype)) % 16 == 0;
-    // copied out by TMA: rows on 16-byte boundaries, at a stride that a tensor map holds
-    const int64_t out_bytes = g.out_stride * type_size(g.out_dtype);
-    p.out_tma = ((uintptr_t)g.out & 15u) == 0 && out_bytes % 16 == 0 && out_bytes >= g.n_cols * (int64_t)type_size(g.out_dtype) &&
+    // copied out by TMA: rows on 16-byte boundaries, at a stride that a tensor map holds, and whole 16 bytes long
+    // (a copy is cut at the last column's 16 bytes, not at the column)
+    const int64_t out_bytes = g.out_stride * type_size(g.out_dtype), row_bytes = g.n_cols * (int64_t)type_size(g.out_dtype);
+    p.out_tma = ((uintptr_t)g.out & 15u) == 0 && out_bytes % 16 == 0 && row_bytes % 16 == 0 && out_bytes >= row_bytes &&
                 out_bytes < (1ll << 40);
     const uint64_t dout[2] = {(uint64_t)g.n_cols, (uint64_t)g.n_rows};
     if (p.out_tma && !encode_out(&p.tout, g.out, g.out_dtype, dout, (uint64_t)out_bytes)) return cudaErrorInvalidValue;

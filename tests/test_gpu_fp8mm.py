@@ -191,3 +191,56 @@ def test_same_bits_every_time(rows, cols, inner):
         qm.qs_fp8_matmul(a, sa, w, sw, out, ws)
         assert torch.equal(out, first)
     assert qm.qs_read_device_status(ws) == qm.QS_OK
+
+
+@pytest.mark.parametrize("rows,cols,kind", [(3, 70, torch.float32), (200, 70, torch.float32), (200, 131, torch.bfloat16), (2600, 2500, torch.bfloat16), (129, 257, torch.float32)])
+def test_columns_past_the_last_are_left_alone(rows, cols, kind):
+    """Aligned rows wider than the result: copies out are cut at its edge."""
+    g = torch.Generator().manual_seed(rows)
+    a, sa = operand((rows, 256), (rows, 2), g)
+    w, sw = operand((cols, 256), (blocks(cols), 2), g)
+    wide = torch.full((rows + 1, (cols + 63) // 16 * 16), 7.0, dtype=kind, device="cuda")
+    out = wide[:rows, :cols]
+    qm.qs_fp8_matmul(a, sa, w, sw, out, qm.alloc_fp8_matmul_workspace(rows, cols, 256))
+    check(out, values(a, sa, False), values(w, sw, True), kind)
+    assert torch.all(wide[:, cols:] == 7) and torch.all(wide[rows] == 7)
+
+
+def test_experts_and_scales_inside_wider_buffers():
+    g = torch.Generator().manual_seed(21)
+    counts, cols, inner = [5, 0, 70, 33], 200, 300
+    rows = sum(counts)
+    a, sa = operand((rows, inner), (rows, 5), g, pad=32)
+    big, sw = operand((4, cols + 9, inner), (4, blocks(cols), blocks(inner)), g, pad=48)
+    w = big[:, :cols]  # nine rows between experts that are another's
+    off = torch.tensor([0] + counts, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+    out = torch.empty(rows, cols, device="cuda")
+    qm.qs_fp8_matmul(a, sa[:, 1:4], w, sw, out, qm.alloc_fp8_matmul_workspace(rows, cols, inner, 4), off)
+    av, wv, at = values(a, sa[:, 1:4], False), values(w, sw, True), 0
+    for e, c in enumerate(counts):
+        if c:
+            check(out[at:at + c], av[at:at + c], wv[e], torch.float32)
+        at += c
+
+
+def test_first_call_of_a_process_may_be_captured():
+    import subprocess
+    import sys
+    code = """
+import torch
+from bit_quantized_moe_router_gb300 import qs_moe as qm
+F8 = torch.float8_e4m3fn
+a, w = torch.ones(5, 256, device="cuda").to(F8), torch.ones(64, 256, device="cuda").to(F8)
+sa, sw, out = torch.ones(5, 2, device="cuda"), torch.ones(1, 2, device="cuda"), torch.zeros(5, 64, device="cuda")
+ws = qm.alloc_fp8_matmul_workspace(5, 64, 256)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    qm.qs_fp8_matmul(a, sa, w, sw, out, ws)
+g.replay()
+torch.cuda.synchronize()
+assert torch.all(out == 256), out
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
