@@ -226,29 +226,45 @@ struct Tile {
     int e, row0, rows, n0;  // expert, first row of a, rows that are the tile's, first weight row
 };
 
-// The call's groups of rows: row tiles of the experts before e, and e's first row (entries of `offsets`
-// clipped to the rows there are; one group without them).  In shared memory: every role looks up every tile.
+// The call's groups of rows, in shared memory (every role looks up every tile): for each expert its first row
+// (entries of `offsets` clipped to the rows there are; one group without them) and the row tiles of the experts
+// before it among its 32, and for each 32 experts their row tiles.
 struct Groups {
-    int prefix[1025], first[1025];
+    int first[1025], before[1056], total[33];
 };
 
-// Tiles of the call, by number: experts ascending, inside one the weight tiles, inside one the row
-// tiles, so that CTAs side by side share a weight tile.
-template <int ROWS>
-__device__ __forceinline__ Tile tile_at(const MmParams& p, const Groups& g, int nt, int BN, int64_t tile) {
-    Tile t;
-    int lo = 0, hi = p.E;  // last e with prefix[e] * nt <= tile: it has a tile
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)g.prefix[mid] * nt <= tile) lo = mid;
-        else hi = mid;
+// A warp's view: lane c has the row tiles before the experts 32 c ..; `all` of them.
+struct Lookup {
+    int base, all;
+};
+__device__ __forceinline__ Lookup lookup_of(const Groups& g, int E) {
+    const int lane = threadIdx.x & 31, c = lane < (E + 31) / 32 ? g.total[lane] : 0;
+    int s = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += v;
     }
-    const int mt = g.prefix[lo + 1] - g.prefix[lo];
-    const int local = (int)(tile - (int64_t)g.prefix[lo] * nt);
-    const int n = local / mt, m = local - n * mt;
-    t.e = lo;
-    t.row0 = g.first[lo] + m * ROWS;
-    t.rows = min(ROWS, g.first[lo + 1] - t.row0);
+    return {s - c, __shfl_sync(0xffffffffu, s, 31)};
+}
+
+// Tiles of the call, by number: experts ascending, inside one the weight tiles, inside one the row
+// tiles, so that CTAs side by side share a weight tile.  A warp looks for the expert together: the last of the
+// 32 spans, and of its 32 experts, that begins at or before the tile (it has tiles: the next begins later).
+template <int ROWS>
+__device__ __forceinline__ Tile tile_at(const MmParams& p, const Groups& g, const Lookup& look, int nt, int BN, int64_t tile) {
+    Tile t;
+    const int lane = threadIdx.x & 31, spans = (p.E + 31) / 32;
+    const int span = 31 - __clz(__ballot_sync(0xffffffffu, lane < spans && (int64_t)look.base * nt <= tile));
+    const int from = __shfl_sync(0xffffffffu, look.base, span), e = span * 32 + lane;
+    const int mine = from + (e < p.E ? g.before[e] : 0);
+    const int at = 31 - __clz(__ballot_sync(0xffffffffu, e < p.E && (int64_t)mine * nt <= tile));
+    t.e = span * 32 + at;
+    const int first = g.first[t.e], last = g.first[t.e + 1], mt = (last - first + ROWS - 1) / ROWS;
+    const int local = (int)(tile - (int64_t)__shfl_sync(0xffffffffu, mine, at) * nt);
+    const int n = mt == 1 ? local : local / mt, m = local - n * mt;
+    t.row0 = first + m * ROWS;
+    t.rows = min(ROWS, last - t.row0);
     t.n0 = n * BN;
     return t;
 }
@@ -474,36 +490,26 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
     pdl_wait();
     pdl_launch_next();
     if (p.offsets) {
-        for (int e = threadIdx.x; e <= p.E; e += S::kThreads)
-            groups_of.first[e] = min(max(p.offsets[e], 0), p.M);
-        __syncthreads();
-        if (warp == 0) {
-            // a lane has the row tiles of `per` experts side by side: its sum, the sum of the lanes before, and again
-            const int per = (p.E + 31) / 32;
-            auto tiles_of = [&](int e) {
-                const int c = e < p.E ? groups_of.first[e + 1] - groups_of.first[e] : 0;
-                return c > 0 ? (c + kRows - 1) / kRows : 0;
-            };
-            int sum = 0;
-            for (int k = 0; k < per; k++) sum += tiles_of(lane * per + k);
-            int run = sum;
+        for (int c = warp; c * 32 <= p.E; c += S::kThreads / 32) {  // 32 experts a warp
+            const int e = c * 32 + lane;
+            const int r0 = min(max(p.offsets[min(e, p.E)], 0), p.M), r1 = min(max(p.offsets[min(e + 1, p.E)], 0), p.M);
+            const int mt = r1 > r0 ? (r1 - r0 + kRows - 1) / kRows : 0;
+            int s = mt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += v;
+                const int v = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += v;
             }
-            run -= sum;
-            for (int k = 0; k < per; k++) {
-                const int e = lane * per + k;
-                if (e <= p.E) groups_of.prefix[e] = run;
-                run += tiles_of(e);
+            if (e <= p.E) {
+                groups_of.first[e] = r0;
+                groups_of.before[e] = s - mt;
             }
-            if (lane == 31) groups_of.prefix[p.E] = run;
+            if (lane == 31) groups_of.total[c] = s;
         }
     } else if (threadIdx.x == 0) {
-        groups_of.first[0] = groups_of.prefix[0] = 0;
+        groups_of.first[0] = groups_of.before[0] = 0;
         groups_of.first[1] = p.M;
-        groups_of.prefix[1] = (p.M + kRows - 1) / kRows;
+        groups_of.total[0] = (p.M + kRows - 1) / kRows;
     }
     tc::fence_before();
     __syncthreads();
@@ -511,7 +517,8 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
     tc::fence_after();
     const uint32_t tbase = ctl.tmem;
     const int nt = (p.N + BN - 1) / BN;
-    const int64_t n_tiles = (int64_t)groups_of.prefix[p.E] * nt;
+    const Lookup look = lookup_of(groups_of, p.E);
+    const int64_t n_tiles = (int64_t)look.all * nt;
 
     if (warp < kFirstSum) {
         if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
@@ -522,7 +529,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             int64_t filled = 0;
             bool ok = true;
             for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
-                const Tile t = tile_at<kRows>(p, groups_of, nt, BN, u);
+                const Tile t = tile_at<kRows>(p, groups_of, look, nt, BN, u);
                 // rows by boxes of box_rows, or (0) by one of 128; boxes of several blocks lie as the blocks do
                 // only if one holds all rows
                 const int boxes = PAIR ? 0
@@ -654,7 +661,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             uint32_t phase = 1;
             bool ok = true;
             for (int64_t u = first_tile; u < n_tiles && ok; u += tile_step) {
-                const Tile t = tile_at<kRows>(p, groups_of, nt, BN, u);
+                const Tile t = tile_at<kRows>(p, groups_of, look, nt, BN, u);
                 const int rows = min(kTileRows, t.rows - rank * kTileRows);
                 const float* sa = p.sa + (int64_t)(t.row0 + rank * kTileRows) * p.sa_stride;
                 for (int kb0 = 0; kb0 < p.KB; kb0 += kScaleGroup) {
@@ -751,7 +758,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                 }
             }
             if (!ok) break;
-            const Tile now = tile_at<kRows>(p, groups_of, nt, BN, u);
+            const Tile now = tile_at<kRows>(p, groups_of, look, nt, BN, u);
             const int row0 = now.row0 + rank * kTileRows + quad * 32, rows = now.rows - rank * kTileRows - quad * 32;
             if (rows <= 0) continue;
 #pragma unroll

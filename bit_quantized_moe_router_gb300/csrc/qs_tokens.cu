@@ -9,7 +9,7 @@
 // Combine.  One token a CTA row: sum of w * y[pos] over the slots in ascending order, k loads in
 // flight a thread.  Its gradient reads dout once a token and y once, and writes dy once.
 // All of them move bytes once: the bound is HBM.  8192 tokens to 8 of 256 experts, bf16 rows of 2048: rows out 46 us
-// (302 MB), back 49 us (302 MB), the gradient of that 98 us (570 MB); the positions 12 us before.
+// (302 MB), back 49 us (302 MB), the gradient of that 94 us (570 MB); the positions 12 us before.
 #include "qs_internal.h"
 #include "qs_rows.cuh"
 
@@ -281,37 +281,54 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs p) {
     }
 }
 
-template <bool VEC>
+// The rows of y are read, held as they come, before rows of dy are written: the compiler may not move a read
+// across a write that could be to the same place (one row's read at a time: 98 us instead of 94 at the size above).
+template <bool VEC, bool B16>
 __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineBwdArgs p) {
+    constexpr int kHeld = B16 ? kBatch : kBatch / 2;
     __shared__ int32_t at[32];
     __shared__ float w[32];
-    __shared__ float red[8][kBatch];
+    __shared__ float red[8][kHeld];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     pdl_wait();
     pdl_launch_next();
-    if (threadIdx.x < p.top_k) {
-        const int64_t i = t * p.top_k + threadIdx.x;
-        const int a = p.pos[i];
-        at[threadIdx.x] = (unsigned)a < (unsigned)(p.n_tokens * p.top_k) ? a : -1;
-        w[threadIdx.x] = p.w ? p.w[i] : 1.0f;
+    if (threadIdx.x < 32) {
+        int a = -1;
+        float f = 0.0f;
+        if (threadIdx.x < p.top_k) {
+            const int64_t i = t * p.top_k + threadIdx.x;
+            a = p.pos[i];
+            if ((unsigned)a >= (unsigned)(p.n_tokens * p.top_k)) a = -1;
+            f = p.w ? p.w[i] : 1.0f;
+        }
+        at[threadIdx.x] = a;
+        w[threadIdx.x] = f;
     }
     __syncthreads();
     const void* dr = row_at(p.dout, p.dout_stride, type_size(p.dout_dtype), t);
-    for (int j0 = 0; j0 < p.top_k; j0 += kBatch) {
-        float dot[kBatch];
+    for (int j0 = 0; j0 < p.top_k; j0 += kHeld) {
+        float dot[kHeld];
 #pragma unroll
-        for (int j = 0; j < kBatch; j++) dot[j] = 0.0f;
+        for (int j = 0; j < kHeld; j++) dot[j] = 0.0f;
         for (int i = threadIdx.x * 8; cols_left<VEC>(i, p.hidden); i += blockDim.x * 8) {
             float d[8];
             load8_row<VEC>(dr, p.dout_dtype, i, p.hidden, d);
+            Held8<VEC, B16> y[kHeld];
+            if (p.dw) {
 #pragma unroll
-            for (int j = 0; j < kBatch; j++) {
-                const int a = j0 + j < p.top_k ? at[j0 + j] : -1;
+                for (int j = 0; j < kHeld; j++) {
+                    const int a = at[j0 + j];
+                    y[j].load(row_at(p.y, p.y_stride, type_size(p.y_dtype), max(a, 0)), p.y_dtype, i, a >= 0 ? p.hidden : 0);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kHeld; j++) {
+                const int a = at[j0 + j];
                 if (a < 0) continue;
                 float v[8];
                 if (p.dw) {
-                    load8_row<VEC>(row_at(p.y, p.y_stride, type_size(p.y_dtype), a), p.y_dtype, i, p.hidden, v);
+                    y[j].get(p.y_dtype, v);
 #pragma unroll
                     for (int q = 0; q < 8; q++) dot[j] = fmaf(d[q], v[q], dot[j]);
                 }
@@ -323,12 +340,12 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineBwdA
         }
         if (!p.dw) continue;
 #pragma unroll
-        for (int j = 0; j < kBatch; j++) {
+        for (int j = 0; j < kHeld; j++) {
             const float v = warp_sum(dot[j]);
             if (lane == 0) red[warp][j] = v;
         }
         __syncthreads();
-        if (threadIdx.x < kBatch && j0 + threadIdx.x < p.top_k) {
+        if (threadIdx.x < kHeld && j0 + threadIdx.x < p.top_k) {
             float v = 0.0f;
             for (int q = 0; q < nw; q++) v += red[q][threadIdx.x];
             p.dw[t * p.top_k + j0 + threadIdx.x] = v;
@@ -409,8 +426,9 @@ cudaError_t launch_combine_backward(const CombineBwdArgs& p, cudaStream_t st) {
     const bool vec = p.hidden % 8 == 0 && al16(p.dout, p.dout_stride, p.dout_dtype) &&
                      (!p.dw || al16(p.y, p.y_stride, p.y_dtype)) && al16(p.dy, p.dy_stride, p.dy_dtype);
     const unsigned block = row_threads((p.hidden + 7) / 8);
-    return vec ? launch_pdl(combine_backward_kernel<true>, dim3(p.n_tokens), block, 0, st, p)
-               : launch_pdl(combine_backward_kernel<false>, dim3(p.n_tokens), block, 0, st, p);
+    if (!vec) return launch_pdl(combine_backward_kernel<false, false>, dim3(p.n_tokens), block, 0, st, p);
+    return p.y_dtype == QS_BF16 || !p.dw ? launch_pdl(combine_backward_kernel<true, true>, dim3(p.n_tokens), block, 0, st, p)
+                                         : launch_pdl(combine_backward_kernel<true, false>, dim3(p.n_tokens), block, 0, st, p);
 }
 
 }  // namespace qs
