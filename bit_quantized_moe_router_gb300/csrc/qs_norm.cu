@@ -45,8 +45,9 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* red, int wg, int
 
 constexpr int cta_warps(int G) { return G < 8 ? 8 : G; }
 
-// G warps a row, NV steps of eight elements a thread: rows of up to 256 * G * NV elements.
-template <bool VEC, int G, int NV>
+// G warps a row, NV steps of eight elements a thread: rows of up to 256 * G * NV elements.  B16: every row that is
+// there is known to be bf16 (2 to 4 % less time than with the types looked up).
+template <bool VEC, bool B16, int G, int NV>
 __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_kernel(const NormArgs p) {
     constexpr int kGroups = cta_warps(G) / G;
     __shared__ float red[kGroups][G];
@@ -54,19 +55,21 @@ __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_kernel(const NormAr
     const int group = warp / G, wg = warp % G;
     const int64_t t = (int64_t)blockIdx.x * kGroups + group;
     auto col = [&](int j) { return (j * 32 * G + wg * 32 + lane) * 8; };
+    const int x_type = B16 ? QS_BF16 : p.x_dtype, r_type = B16 ? QS_BF16 : p.residual_dtype;
+    const int s_type = B16 ? QS_BF16 : p.sum_dtype, y_type = B16 ? QS_BF16 : p.y_dtype;
     pdl_wait();
     pdl_launch_next();
     if (t >= p.n_rows) return;
-    const void* xr = row_at(p.x, p.x_stride, type_size(p.x_dtype), t);
-    const void* rr = p.residual ? row_at(p.residual, p.residual_stride, type_size(p.residual_dtype), t) : nullptr;
+    const void* xr = row_at(p.x, p.x_stride, type_size(x_type), t);
+    const void* rr = p.residual ? row_at(p.residual, p.residual_stride, type_size(r_type), t) : nullptr;
     float s[NV][1][8];
 #pragma unroll
-    for (int j = 0; j < NV; j++) load8_row<VEC>(xr, p.x_dtype, col(j), p.hidden, s[j][0]);
+    for (int j = 0; j < NV; j++) load8_row<VEC>(xr, x_type, col(j), p.hidden, s[j][0]);
     if (rr) {
 #pragma unroll
         for (int j = 0; j < NV; j++) {
             float r[8];
-            load8_row<VEC>(rr, p.residual_dtype, col(j), p.hidden, r);
+            load8_row<VEC>(rr, r_type, col(j), p.hidden, r);
 #pragma unroll
             for (int q = 0; q < 8; q++) s[j][0][q] += r[q];
         }
@@ -77,19 +80,19 @@ __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_kernel(const NormAr
 #pragma unroll
         for (int q = 0; q < 8; q++) ss[0] = fmaf(s[j][0][q], s[j][0][q], ss[0]);
     if (p.sum_out) {
-        void* o = row_at(p.sum_out, p.sum_stride, type_size(p.sum_dtype), t);
+        void* o = row_at(p.sum_out, p.sum_stride, type_size(s_type), t);
 #pragma unroll
-        for (int j = 0; j < NV; j++) store8_row<VEC>(o, p.sum_dtype, col(j), p.hidden, s[j][0]);
+        for (int j = 0; j < NV; j++) store8_row<VEC>(o, s_type, col(j), p.hidden, s[j][0]);
     }
     if (!p.y && !p.q) return;
     group_sum<G, 1>(ss, red[group], wg, lane, 1 + group);
     const float rho = rsqrtf(ss[0] / (float)p.hidden + p.eps);
-    void* yr = p.y ? row_at(p.y, p.y_stride, type_size(p.y_dtype), t) : nullptr;
+    void* yr = p.y ? row_at(p.y, p.y_stride, type_size(y_type), t) : nullptr;
     // rho is left to the end, where it costs the codes no rounding; rows so small that it is large take it at once
     const float factor = rho > 65536.0f ? 1.0f : rho, least = kMinAmax / factor;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
-        float w[8];
+        float w[8];  // read here, not before the barrier: early, it took 10 % more at 8192 fp32 columns and gave decode 0.15 us
         load8_row<VEC>(p.weight, QS_F32, col(j), p.hidden, w);
 #pragma unroll
         for (int q = 0; q < 8; q++) s[j][0][q] *= w[q];
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_kernel(const NormAr
         if (yr) {
 #pragma unroll
             for (int q = 0; q < 8; q++) s[j][0][q] *= factor;
-            store8_row<VEC>(yr, p.y_dtype, col(j), p.hidden, s[j][0]);
+            store8_row<VEC>(yr, y_type, col(j), p.hidden, s[j][0]);
         }
     }
 }
@@ -295,43 +298,26 @@ __global__ void __launch_bounds__(256) silu_mul_quant_kernel(const SiluArgs p) {
     }
 }
 
-bool al16(const void* p, int64_t stride, int dtype) {
-    return ((uintptr_t)p & 15u) == 0 && (stride * type_size(dtype)) % 16 == 0;
-}
-
-template <class K, class... A>
-cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, cudaStream_t st, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <bool VEC, int G, int NV>
+template <bool VEC, bool B16, int G, int NV>
 cudaError_t norm_run(const NormArgs& p, cudaStream_t st) {
     constexpr int groups = cta_warps(G) / G;
-    return launch_pdl(rmsnorm_kernel<VEC, G, NV>, (unsigned)(((int64_t)p.n_rows + groups - 1) / groups), 32 * cta_warps(G), st, p);
+    return launch_pdl(rmsnorm_kernel<VEC, B16, G, NV>, dim3((unsigned)(((int64_t)p.n_rows + groups - 1) / groups)), 32 * cta_warps(G), 0, st, p);
 }
 
-template <bool VEC>
+template <bool VEC, bool B16>
 cudaError_t norm_pick(const NormArgs& p, cudaStream_t st) {
-    // Few rows: as many threads a row as have a load, for the least latency (32 x 2048: 2.3 us, with two warps
-    // a row 4.0).  Many: a warp a row where its registers hold it, which needs no barrier (32768 x 1024: 47 us,
-    // with two warps 55, with four 67); 8 warps at 2048 (91 us; four 104, two 89) and at 4096 (85; sixteen 98, four 90).
+    // Few rows: as many threads a row as have a load, for the least latency (32 x 2048: 2.1 us, with two warps
+    // a row 4.0).  Many: a warp a row where its registers hold it, which needs no barrier, else eight.  32768 rows of
+    // 1024: 44 us; compared with the types looked up, 47, with two warps 55, with four 67.  Of 2048: 86; so compared,
+    // 91, with four warps 104, with two 89.  16384 of 4096: 85, with sixteen warps 98, with four 90.
     const bool few = p.n_rows <= 304;  // two a SM
-    if (p.hidden <= 256) return norm_run<VEC, 1, 1>(p, st);
-    if (p.hidden <= 512) return norm_run<VEC, 1, 2>(p, st);
-    if (p.hidden <= 1024) return few ? norm_run<VEC, 4, 1>(p, st) : norm_run<VEC, 1, 4>(p, st);
-    if (p.hidden <= 2048) return norm_run<VEC, 8, 1>(p, st);
-    if (p.hidden <= 4096) return few ? norm_run<VEC, 16, 1>(p, st) : norm_run<VEC, 8, 2>(p, st);
-    if (p.hidden <= 8192) return norm_run<VEC, 16, 2>(p, st);
-    return norm_run<VEC, 16, 4>(p, st);
+    if (p.hidden <= 256) return norm_run<VEC, B16, 1, 1>(p, st);
+    if (p.hidden <= 512) return norm_run<VEC, B16, 1, 2>(p, st);
+    if (p.hidden <= 1024) return few ? norm_run<VEC, B16, 4, 1>(p, st) : norm_run<VEC, B16, 1, 4>(p, st);
+    if (p.hidden <= 2048) return norm_run<VEC, B16, 8, 1>(p, st);
+    if (p.hidden <= 4096) return few ? norm_run<VEC, B16, 16, 1>(p, st) : norm_run<VEC, B16, 8, 2>(p, st);
+    if (p.hidden <= 8192) return norm_run<VEC, false, 16, 2>(p, st);
+    return norm_run<VEC, false, 16, 4>(p, st);
 }
 
 template <bool VEC, bool B16, int G, int NV>
@@ -340,11 +326,11 @@ cudaError_t norm_bwd_run(NormBwdArgs p, float* dweight, cudaStream_t st) {
     const int64_t ctas = ((int64_t)p.n_rows + groups - 1) / groups;
     const unsigned grid = (unsigned)std::min<int64_t>(ctas, kNormParts);
     if (grid > 0) {
-        const cudaError_t e = launch_pdl(rmsnorm_backward_kernel<VEC, B16, G, NV>, grid, 32 * cta_warps(G), st, p);
+        const cudaError_t e = launch_pdl(rmsnorm_backward_kernel<VEC, B16, G, NV>, dim3(grid), 32 * cta_warps(G), 0, st, p);
         if (e != cudaSuccess) return e;
     }
     if (!dweight) return cudaSuccess;
-    return launch_pdl(rmsnorm_dweight_kernel, (unsigned)((p.hidden + 31) / 32), 1024, st, (const float*)p.partial,
+    return launch_pdl(rmsnorm_dweight_kernel, dim3((unsigned)((p.hidden + 31) / 32)), 1024, 0, st, (const float*)p.partial,
                       (int)grid, p.part_stride, p.hidden, dweight);
 }
 
@@ -368,7 +354,10 @@ cudaError_t launch_rmsnorm(const NormArgs& p, cudaStream_t st) {
                      al16(p.weight, 0, QS_F32) && (!p.sum_out || al16(p.sum_out, p.sum_stride, p.sum_dtype)) &&
                      (!p.y || al16(p.y, p.y_stride, p.y_dtype)) &&
                      (!p.q || (((uintptr_t)p.q & 7u) == 0 && p.q_stride % 8 == 0));
-    return vec ? norm_pick<true>(p, st) : norm_pick<false>(p, st);
+    const bool b16 = p.x_dtype == QS_BF16 && (!p.residual || p.residual_dtype == QS_BF16) &&
+                     (!p.sum_out || p.sum_dtype == QS_BF16) && (!p.y || p.y_dtype == QS_BF16);
+    if (!vec) return norm_pick<false, false>(p, st);
+    return b16 ? norm_pick<true, true>(p, st) : norm_pick<true, false>(p, st);
 }
 
 cudaError_t launch_rmsnorm_backward(const NormBwdArgs& p, float* dweight, cudaStream_t st) {
@@ -386,8 +375,8 @@ cudaError_t launch_silu_mul_quant(const SiluArgs& p, cudaStream_t st) {
                      (p.ffn * type_size(p.dtype)) % 16 == 0 && ((uintptr_t)p.q & 7u) == 0 && p.q_stride % 8 == 0;
     const int64_t work = (int64_t)p.n_rows * scale_blocks(p.ffn);
     const unsigned grid = (unsigned)std::min<int64_t>((work + 31) / 32, 1216);  // eight CTAs an SM walk on: 30.5 us at 65536 x 512 against 34.3 with one step each
-    return vec ? launch_pdl(silu_mul_quant_kernel<true>, grid, 256, st, p)
-               : launch_pdl(silu_mul_quant_kernel<false>, grid, 256, st, p);
+    return vec ? launch_pdl(silu_mul_quant_kernel<true>, dim3(grid), 256, 0, st, p)
+               : launch_pdl(silu_mul_quant_kernel<false>, dim3(grid), 256, 0, st, p);
 }
 
 }  // namespace qs

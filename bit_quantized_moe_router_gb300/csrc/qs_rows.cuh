@@ -223,4 +223,28 @@ struct Held8<false, false> {  // any alignment: single elements, as load8_row ha
     }
 };
 
+// ------------------------------------------------------------------ host side
+
+// Every row at 16-byte boundaries.
+inline bool al16(const void* p, int64_t stride, int dtype) {
+    return ((uintptr_t)p & 15u) == 0 && (stride * type_size(dtype)) % 16 == 0;
+}
+
+// A programmatic dependent launch: the kernel may start while the one before it in the stream ends, and waits for
+// it (pdl_wait) before it reads or writes anything.
+template <class K, class... A>
+cudaError_t launch_pdl(K kernel, dim3 grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace qs

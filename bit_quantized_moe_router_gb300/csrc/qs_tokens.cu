@@ -354,25 +354,6 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineBwdA
     }
 }
 
-bool al16(const void* p, int64_t stride, int dtype) {
-    return ((uintptr_t)p & 15u) == 0 && (stride * type_size(dtype)) % 16 == 0;
-}
-
-template <class K, class... A>
-cudaError_t launch_pdl(K kernel, dim3 grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Threads for a row of `units` units: whole warps, at most 256.
 unsigned row_threads(int units) { return (unsigned)std::min(256, (std::max(units, 1) + 31) / 32 * 32); }
 
