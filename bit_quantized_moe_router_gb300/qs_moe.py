@@ -489,8 +489,8 @@ def alloc_fp8_matmul_workspace(n_rows, n_cols, n_inner, n_experts=1, device="cud
 
 def qs_fp8_matmul(a, a_scale, w, w_scale, out, workspace, offsets=None, stream=None):
     """out [rows, N] = a [rows, K] times w [N, K] (or, with offsets int32 [E + 1], w [E, N, K] of the expert whose
-    rows offsets[e] .. offsets[e + 1] - 1 are) transposed; e4m3 codes with a scale per row and 128 columns of a and per
-    128 x 128 block of w."""
+    rows offsets[e] .. offsets[e + 1] - 1 are) transposed; e4m3 codes, rows of both at 16-byte boundaries, with a scale per
+    row and 128 columns of a and per 128 x 128 block of w."""
     shape = _two(a, "a")
     rows, inner = shape
     if offsets is None:

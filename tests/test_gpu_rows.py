@@ -434,3 +434,32 @@ def test_norm_codes_of_tiny_and_huge_rows(size, eps):
     qm.qs_rmsnorm_residual(x.cuda(), None, w.cuda(), eps, q=q, q_scale=scale)
     v = x.double() / torch.sqrt(x.double().pow(2).mean(1, keepdim=True) + float(np.float32(eps))) * w.double()
     check_codes(q, scale, v, NORM_SLACK + U)
+
+
+def test_binding_refuses_wrong_types_shapes_and_strides():
+    x, w = torch.zeros(4, 256, device="cuda"), torch.ones(256, device="cuda")
+    q, scale = codes(4, 256)
+    for call, text in [
+            (lambda: qm.qs_rmsnorm_residual(x.half(), None, w, EPS, y=x), "x: torch.float16"),
+            (lambda: qm.qs_rmsnorm_residual(x, x[:3], w, EPS, y=x), "residual: shape"),
+            (lambda: qm.qs_rmsnorm_residual(x, None, w[:255], EPS, y=x), "weight: shape"),
+            (lambda: qm.qs_rmsnorm_residual(x, None, w.double(), EPS, y=x), "weight: torch.float64"),
+            (lambda: qm.qs_rmsnorm_residual(x, None, w, EPS, y=torch.zeros(256, 4, device="cuda").t()), "y: expected contiguous columns"),
+            (lambda: qm.qs_rmsnorm_residual(x, None, w, EPS, q=q), "come with scales"),
+            (lambda: qm.qs_rmsnorm_residual(x, None, w, EPS, q=q, q_scale=scale[:, :1]), "q scale: shape"),
+            (lambda: qm.qs_silu_mul_quant(x, q, scale), "gate_up: shape"),
+            (lambda: qm.qs_fp8_matmul(q, scale, q, scale, torch.zeros(4, 4, device="cuda"), qm.alloc_fp8_matmul_workspace(4, 4, 256)), "w scale: shape"),
+            (lambda: qm.qs_combine_tokens(x, torch.zeros(2, 2, device="cuda"), None, x[:2]), "pos: torch.float32"),
+            (lambda: qm.qs_dispatch_tokens(torch.zeros(2, 2, dtype=torch.int32, device="cuda"), x[:2], None, *outputs(2, 2, 4)[:3], x, x, None,
+                                           qm.alloc_dispatch_workspace(2, 2, 4)), "pos: torch.float32")]:
+        with pytest.raises(ValueError, match=text):
+            call()
+    flat = torch.zeros(8 * 256 + 8, dtype=torch.uint8, device="cuda")
+    off = flat[8:8 + 4 * 256].view(4, 256).view(F8)  # not at 16 bytes
+    with pytest.raises(qm.QsError):
+        qm.qs_fp8_matmul(off, scale, q, torch.ones(1, 2, device="cuda"), torch.zeros(4, 4, device="cuda"), qm.alloc_fp8_matmul_workspace(4, 4, 256))
+    with pytest.raises(qm.QsError):  # a broadcast row
+        qm.qs_rmsnorm_residual(x[:1].expand(4, 256), None, w, EPS, y=x)
+    with pytest.raises(qm.QsError):
+        qm.qs_rmsnorm_residual(x, None, w, EPS)
+    torch.cuda.synchronize()
