@@ -9,11 +9,12 @@
 //   warp 0     TMA: a stage is a block (narrow tiles: two or four) of the tile's rows of a and of its weight rows
 //   warps 1-2  MMA, taking turns: four instructions a block and accumulator, overwriting
 //   warp 3     brings the scales of eight blocks at a time to shared memory
-//   warps 4-11 read an accumulator (a thread a row, BN / 2 of its columns), add it, scaled, to their registers,
+//   warps 4-11 read an accumulator (a thread a row, half of its columns), add it, scaled, to their registers,
 //              and after the last block send the tile out through shared memory
 // A thread owns a row of the tile, so a block's scale is one number a thread (two where its columns are of two
 // weight blocks) and a step costs one multiply-add an element.
-// Tiles are 128 rows by BN weight rows, or, where there is work for all SMs in them, 256 x 256 of two CTAs.  A CTA
+// Tiles are 128 rows by BN weight rows, or, where there is work for all SMs in them, 256 x 256 of two CTAs, or, for groups
+// of a call of few rows, 128 weight rows by all of them with the operands' parts changed about.  A CTA
 // takes tiles blockIdx.x, + gridDim.x, ... and its stages run on from one tile to the next.
 // Bound: weights from HBM where there are few rows a weight (2048 tokens to 8 of 256 experts, 2048 x 1024 each:
 // 93 us, 96 % of the copy rate), latency where a matrix is small (one row by 4096 x 2048: 4.6 us for 1.2 us of
@@ -64,7 +65,7 @@ struct MmParams {
 // Scales on their way to the summing warps: kScaleRing groups of kScaleGroup blocks.  Rows are 132 apart
 // so that the eight blocks of a row, read together, are stored to different banks.
 constexpr int kScaleGroup = 8, kScaleRing = 2;
-struct MmScales {
+struct alignas(16) MmScales {
     float a[kScaleGroup][kTileRows + 4];
     float w[2][kScaleGroup];  // of the tile's first and second 128 columns
 };
@@ -271,26 +272,29 @@ __device__ __forceinline__ Tile tile_at(const MmParams& p, const Groups& g, cons
 
 constexpr int kStage = 2048;  // bytes of a summing warp's staging rows: 32 of 64 bytes
 
-template <int BN>
+// FEW: all rows of the call fit one tile of FEW (16, 32 or 64) columns of an accumulator whose rows are 128 weight
+// rows: the matrix instruction's time goes with its columns, and those are then the call's rows.
+template <int BN, int FEW = 0>
 struct MmShape {
+    static_assert(FEW == 0 || BN == 128, "128 weight rows");
     // The widest tile is two accumulators of 128 columns, filled and read one after the other: with one of
     // 256 the time from a read back to the next fill stood open, 700 cycles a block.
     static constexpr int kHalves = BN == 256 ? 2 : 1;
-    static constexpr int kAccCols = BN / kHalves;
+    static constexpr int kAccCols = FEW ? FEW : BN / kHalves;
     static constexpr int kAcc = 4;                                       // accumulators in tensor memory
     // Blocks of K that pass through the roles as one: a stage, an accumulator (side by side, each block with its
     // own columns) and one round of barriers.  Waits, issue and release take 300 to 400 cycles whatever the
-    // width, which is all a narrow tile's time: one row by 4096 x 2048 took 6.0 us with one block at a time.
-    static constexpr int kGroup = BN >= 128 ? 1 : BN == 64 ? 2 : 4;
+    // width, which is all a narrow tile's time: one row by 4096 x 2048 took 6.0 us with one block at a time, 4.8 so.
+    static constexpr int kGroup = FEW ? 2 : BN >= 128 ? 1 : BN == 64 ? 2 : 4;
     static constexpr int kAccStep = kAccCols * kGroup;                   // columns of an accumulator
     static constexpr int kTmemCols = kAccStep * kAcc;                    // 256 or 512
     static constexpr int kSumWarps = 8;
     static constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
-    static constexpr int kCols = BN * 4 / kSumWarps;            // columns of a summing thread, in runs of 64 at most:
+    static constexpr int kCols = (FEW ? FEW : BN) * 4 / kSumWarps;            // columns of a summing thread, in runs of 64 at most:
     static constexpr int kRun = kCols < 64 ? kCols : 64;        // what lies together in a pair's accumulator and in w
     static constexpr int kRuns = kCols / kRun;
     static constexpr int kLoad = BN == 256 ? 16 : kRun < 32 ? kRun : 32;  // columns of one tensor-memory load
-    static constexpr int kSumBytes = kSumWarps * kStage;          // staging rows of the summing warps
+    static constexpr int kSumBytes = FEW ? 0 : kSumWarps * kStage;          // staging rows of the summing warps
 };
 
 // Registers a thread of the widest tile: the launch's 168 x 384 are dealt out as 56 for warps 0-3 and
@@ -356,6 +360,35 @@ __device__ __forceinline__ void add_group(float2 (&acc)[MmShape<BN>::kRun / 2], 
         if (g < n) {
 #pragma unroll
             for (int i = 0; i < S::kLoad / 2; i++) acc[i] = fma2(d[g][2 * i], d[g][2 * i + 1], scale[g], acc[i]);
+        }
+    }
+}
+
+// The same for a tile of few rows: a thread's columns are rows of the call, each with its own scale (of block g at
+// scale + g * step).
+template <int FEW>
+__device__ __forceinline__ void add_few(float2 (&acc)[MmShape<128, FEW>::kRun / 2], uint32_t src, const float* scale, int step,
+                                        int n, uint32_t empty, int lane) {
+    using S = MmShape<128, FEW>;
+    uint32_t d[S::kGroup][S::kLoad];
+    tc::fence_after();
+#pragma unroll
+    for (int g = 0; g < S::kGroup; g++) tmem_load<S::kLoad>(src + g * S::kAccCols, d[g]);
+    tc::wait_ld();
+    tc::fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_at<false>(empty);
+#pragma unroll
+    for (int g = 0; g < S::kGroup; g++) {
+        if (g < n) {
+#pragma unroll
+            for (int i = 0; i < S::kLoad; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(scale + g * step + i);
+                acc[i / 2].x = fmaf(__uint_as_float(d[g][i]), f.x, acc[i / 2].x);
+                acc[i / 2].y = fmaf(__uint_as_float(d[g][i + 1]), f.y, acc[i / 2].y);
+                acc[i / 2 + 1].x = fmaf(__uint_as_float(d[g][i + 2]), f.z, acc[i / 2 + 1].x);
+                acc[i / 2 + 1].y = fmaf(__uint_as_float(d[g][i + 3]), f.w, acc[i / 2 + 1].y);
+            }
         }
     }
 }
@@ -429,10 +462,10 @@ __device__ __forceinline__ void store_rows(const MmParams& p, const float2 (&acc
 
 // PAIR: two CTAs take a tile of 256 rows together, each 128 rows and half of the weight rows; the
 // leader issues the matrix instructions for both.
-template <int BN, bool PAIR>
-__global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const __grid_constant__ MmParams p) {
-    using S = MmShape<BN>;
-    constexpr int kCtas = PAIR ? 2 : 1, kRows = kTileRows * kCtas;
+template <int BN, bool PAIR, int FEW = 0>
+__global__ void __launch_bounds__(MmShape<BN, FEW>::kThreads, 1) fp8_mm_kernel(const __grid_constant__ MmParams p) {
+    using S = MmShape<BN, FEW>;
+    constexpr int kCtas = PAIR ? 2 : 1, kRows = FEW ? FEW : kTileRows * kCtas;
     constexpr int G = S::kGroup;
     constexpr int kWBytes = BN / kCtas * 128;  // a CTA's weight part of a block; a stage has G blocks
     extern __shared__ uint8_t mm_smem[];
@@ -585,7 +618,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             // the tensor cores take for it: two warps take turns.  Warp w has half w of every block of the widest
             // tile, else every second group; its accumulators are w and w + 2, and, the number of stages being
             // even, its stages every second one: it sees each phase of the barriers that it waits on.
-            constexpr uint32_t id = tc::idesc(0 /* e4m3 */, kRows, S::kAccCols);
+            constexpr uint32_t id = tc::idesc(0 /* e4m3 */, FEW ? 128 : kRows, S::kAccCols);
             constexpr int kTurn = 2 / S::kHalves;  // groups of blocks from one of the warp's to the next
             const int w = warp - 1, h = S::kHalves == 2 ? w : 0;
             const int per = (p.KB + G - 1) / G;    // groups of a tile
@@ -616,7 +649,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
 #pragma unroll
                             for (int k = 0; k < 4; k++) {  // 32 of K: 32 bytes, 2 units of the descriptors
                                 if (PAIR) mma_f8_pair(tbase + a * S::kAccStep, ag + 2 * k, wg + 2 * k, id, k > 0);
-                                else mma_f8(tbase + a * S::kAccStep + g * S::kAccCols, ag + 2 * k, wg + 2 * k, id, k > 0);
+                                else mma_f8(tbase + a * S::kAccStep + g * S::kAccCols, (FEW ? wg : ag) + 2 * k, (FEW ? ag : wg) + 2 * k, id, k > 0);
                             }
                         }
                     }
@@ -669,11 +702,11 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                     const bool on = kb < p.KB;
                     MmScales& sc = ctl.scales[slot];
                     float w = 0.0f;
-                    if (lane < 16 && on) {
+                    if ((FEW || lane < 16) && on) {
                         const int nb = min(t.n0 / kScaleCols + (BN == 256 ? lane >> 3 : 0), p.NB - 1);
                         w = p.sw[((int64_t)t.e * p.NB + nb) * p.KB + kb];
                     }
-                    for (int r1 = 0; r1 < kTileRows; r1 += 64) {
+                    for (int r1 = 0; r1 < (FEW ? 64 : kTileRows); r1 += 64) {
                         float v[16];
 #pragma unroll
                         for (int i = 0; i < 16; i++) {
@@ -685,7 +718,7 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                             if (!ok) break;
                         }
 #pragma unroll
-                        for (int i = 0; i < 16; i++) sc.a[b][r1 + r0 + 4 * i] = v[i];
+                        for (int i = 0; i < 16; i++) sc.a[b][r1 + r0 + 4 * i] = FEW ? v[i] * w : v[i];
                     }
                     if (!ok) break;
                     if (lane < 16) sc.w[lane >> 3][b] = w;
@@ -728,23 +761,20 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
                 const MmScales& sc = ctl.scales[slot];
                 const int n = min(kScaleGroup, p.KB - kb0);
                 for (int i = 0; i < n; i += G) {
-                    float scale[G][S::kRuns];
+                    // scales of the blocks (past the last: numbers that are not used), read before the accumulator is awaited
+                    float scale[S::kRuns], more[G];
+                    if constexpr (FEW == 0) {
 #pragma unroll
-                    for (int g = 0; g < G; g++)  // past the last block: a number that is not used
+                        for (int q = 0; q < S::kRuns; q++) scale[q] = sc.a[i][r] * sc.w[col_at(q) / kScaleCols][i];
 #pragma unroll
-                        for (int q = 0; q < S::kRuns; q++)
-                            scale[g][q] = sc.a[i + g][r] * sc.w[col_at(q) / kScaleCols][i + g];
+                        for (int g = 0; g < G; g++) more[g] = g == 0 ? scale[0] : sc.a[i + g][r] * sc.w[0][i + g];
+                    }
                     ok = __all_sync(0xffffffffu, mm_wait(&ctl.accfull[a], aphase, abort, p.status, 4));
                     if (!ok) break;
-                    const uint32_t src = tc::taddr(tbase, quad * 32, a * S::kAccStep + sub * S::kCols);
-                    if constexpr (G == 1) {
-                        add_block<BN, PAIR>(acc, src, scale[0], accempty + a * 8, lane);
-                    } else {
-                        float flat[G];
-#pragma unroll
-                        for (int g = 0; g < G; g++) flat[g] = scale[g][0];
-                        add_group<BN, PAIR>(acc[0], src, flat, n - i, accempty + a * 8, lane);
-                    }
+                    const uint32_t src = tc::taddr(tbase, quad * 32, a * S::kAccStep + sub * S::kCols), empty = accempty + a * 8;
+                    if constexpr (FEW != 0) add_few<FEW>(acc[0], src, &sc.a[i][sub * S::kCols], kTileRows + 4, n - i, empty, lane);
+                    else if constexpr (G > 1) add_group<BN, PAIR>(acc[0], src, more, n - i, empty, lane);
+                    else add_block<BN, PAIR>(acc, src, scale, empty, lane);
                     if ((a += S::kHalves) >= S::kAcc) {
                         a = h;
                         aphase ^= 1;
@@ -759,6 +789,20 @@ __global__ void __launch_bounds__(MmShape<BN>::kThreads, 1) fp8_mm_kernel(const 
             }
             if (!ok) break;
             const Tile now = tile_at<kRows>(p, groups_of, look, nt, BN, u);
+            if constexpr (FEW != 0) {  // a thread a weight row: a warp's lanes store neighbouring columns
+                const int col = now.n0 + r;
+#pragma unroll
+                for (int i = 0; i < S::kCols; i++) {
+                    const float v = i % 2 ? acc[0][i / 2].y : acc[0][i / 2].x;
+                    const int m = sub * S::kCols + i;
+                    if (m < now.rows && col < p.N) {
+                        const int64_t at = (int64_t)(now.row0 + m) * p.out_stride + col;
+                        if (p.out_dtype == QS_F32) static_cast<float*>(p.out)[at] = v;
+                        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+                    }
+                }
+                continue;
+            }
             const int row0 = now.row0 + rank * kTileRows + quad * 32, rows = now.rows - rank * kTileRows - quad * 32;
             if (rows <= 0) continue;
 #pragma unroll
@@ -842,9 +886,11 @@ cudaError_t mm_facts(MmFacts** out) {
         if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
         f.smem = optin - (int)(sizeof(MmCtl) + sizeof(Groups) + 64);
-        const void* fns[6] = {(const void*)fp8_mm_kernel<16, false>,  (const void*)fp8_mm_kernel<32, false>,
+        const void* fns[9] = {(const void*)fp8_mm_kernel<16, false>,  (const void*)fp8_mm_kernel<32, false>,
                               (const void*)fp8_mm_kernel<64, false>,  (const void*)fp8_mm_kernel<128, false>,
-                              (const void*)fp8_mm_kernel<256, false>, (const void*)fp8_mm_kernel<256, true>};
+                              (const void*)fp8_mm_kernel<256, false>, (const void*)fp8_mm_kernel<256, true>,
+                              (const void*)fp8_mm_kernel<128, false, 16>, (const void*)fp8_mm_kernel<128, false, 32>,
+                              (const void*)fp8_mm_kernel<128, false, 64>};
         for (const void* fn : fns)
             if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess) return e;
         // the register split would wait forever on a launch with fewer
@@ -859,30 +905,31 @@ cudaError_t mm_facts(MmFacts** out) {
     return cudaSuccess;
 }
 
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, int FEW = 0>
 cudaError_t mm_run(const Fp8MmArgs& g, MmParams& p, const MmFacts& f, int64_t tiles, cudaStream_t st) {
     constexpr int kCtas = PAIR ? 2 : 1;
-    constexpr int G = MmShape<BN>::kGroup;
+    using S = MmShape<BN, FEW>;
+    constexpr int G = S::kGroup;
     const bool few = g.n_rows <= kFewRows;
     p.blocked = g.n_inner % 128 == 0;
-    p.box_rows = few ? (g.n_rows + kRowBox - 1) / kRowBox * kRowBox : kRowBox;
+    p.box_rows = FEW ? FEW : few ? (g.n_rows + kRowBox - 1) / kRowBox * kRowBox : kRowBox;
     p.a_bytes = few ? p.box_rows * 128 : kTileRows * 128;
     if (!encode8(&p.tw, true, g.w, g.n_inner, g.n_cols, g.w_stride, g.n_experts, g.w_expert_stride, p.blocked, BN / kCtas, G) ||
         !encode8(&p.tfew, false, g.a, g.n_inner, g.n_rows, g.a_stride, 1, 0, p.blocked, p.box_rows, G) ||
         !encode8(&p.ta128, false, g.a, g.n_inner, g.n_rows, g.a_stride, 1, 0, p.blocked, kTileRows, G))
         return cudaErrorInvalidValue;
     const int stage = G * (p.a_bytes + BN / kCtas * 128);
-    const int tail = kTileRows * 128 - p.a_bytes;  // the last stage's matrix instruction reads 128 rows
-    p.stages = std::min(kMaxStages, (f.smem - 1024 - tail - MmShape<BN>::kSumBytes) / stage);
+    const int tail = FEW ? 0 : kTileRows * 128 - p.a_bytes;  // the last stage's matrix instruction reads 128 rows
+    p.stages = std::min(kMaxStages, (f.smem - 1024 - tail - S::kSumBytes) / stage);
     // Where the issuing warps take groups in turn, a stage is always the same warp's: it has to see every
     // phase of the stage's barrier, or it takes the fill before last for the one it waits for.
-    if (MmShape<BN>::kHalves == 1) p.stages &= ~1;
+    if (S::kHalves == 1) p.stages &= ~1;
     if (p.stages < 2) return cudaErrorInvalidConfiguration;
     p.out_at = p.stages * stage + tail;
-    const size_t smem = 1024 + (size_t)p.out_at + MmShape<BN>::kSumBytes;
+    const size_t smem = 1024 + (size_t)p.out_at + S::kSumBytes;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, f.n_sm / kCtas) * kCtas);
-    cfg.blockDim = dim3(MmShape<BN>::kThreads);
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
@@ -894,7 +941,7 @@ cudaError_t mm_run(const Fp8MmArgs& g, MmParams& p, const MmFacts& f, int64_t ti
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, fp8_mm_kernel<BN, PAIR>, p);
+    return cudaLaunchKernelEx(&cfg, fp8_mm_kernel<BN, PAIR, FEW>, p);
 }
 
 }  // namespace
@@ -934,6 +981,16 @@ cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t 
     const int64_t pair_tiles = (g.offsets ? (int64_t)g.n_rows / 256 + g.n_experts : ((int64_t)g.n_rows + 255) / 256) *
                                ((g.n_cols + 255) / 256);
     if (per > kTileRows && pair_tiles >= f->n_sm / 2) return mm_run<256, true>(g, p, *f, pair_tiles, st);
+    // Groups of a call of few rows: weight rows down the accumulator, the call's rows across.  Against the tiles
+    // below, 8 of 256 experts: one token at 2048 x 1024 (columns x inner) 4.6 us against 6.2, two 7.5 against 10.1,
+    // four at 1024 x 2048 13.6 against 15.1, eight 24.2 against 25.4; of 28 such shapes two lost, 3 and 7 % (eight
+    // tokens at 2048 x 1024 and 2048 x 512).
+    if (g.offsets && g.n_rows <= kFewRows) {
+        const int64_t tiles = (int64_t)std::min(g.n_rows, g.n_experts) * ((g.n_cols + 127) / 128);
+        if (g.n_rows <= 16) return mm_run<128, false, 16>(g, p, *f, tiles, st);
+        if (g.n_rows <= 32) return mm_run<128, false, 32>(g, p, *f, tiles, st);
+        return mm_run<128, false, 64>(g, p, *f, tiles, st);
+    }
     // row tiles: those of one matrix, or for groups the most there can be if rows spread over the
     // experts (each group's last tile may be short)
     const int64_t mt = g.offsets ? (int64_t)g.n_rows / kTileRows + std::min(g.n_rows, g.n_experts)
