@@ -17,8 +17,8 @@
 // of a call of few rows, 128 weight rows by all of them with the operands' parts changed about.  A CTA
 // takes tiles blockIdx.x, + gridDim.x, ... and its stages run on from one tile to the next.
 // Bound: weights from HBM where there are few rows a weight (2048 tokens to 8 of 256 experts, 2048 x 1024 each:
-// 93 us, 96 % of the copy rate), latency where a matrix is small (one row by 4096 x 2048: 4.6 us for 1.2 us of
-// weights), and for long prompts the tensor cores and the sums between them: 8192 x 8192 x 4096 takes 180 us, 3.05
+// 93 us, 96 % of the copy rate), latency where a matrix is small (one row by 4096 x 2048: 4.8 us for 1.2 us of
+// weights), and for long prompts the tensor cores and the sums between them: 8192 x 8192 x 4096 takes 184 us, 2.98
 // PFLOP/s; without the reads of accumulators 165, without the copies 169, without both 145.  With few rows the stage's row part is only as high as the
 // rows there are (the matrix instruction reads on into whatever follows: rows of the result that no
 // thread stores), so that nearly all of shared memory holds weights in flight.
@@ -290,11 +290,11 @@ struct MmShape {
     static constexpr int kTmemCols = kAccStep * kAcc;                    // 256 or 512
     static constexpr int kSumWarps = 8;
     static constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
-    static constexpr int kCols = (FEW ? FEW : BN) * 4 / kSumWarps;            // columns of a summing thread, in runs of 64 at most:
+    static constexpr int kCols = (FEW ? FEW : BN) * 4 / kSumWarps;  // columns of a summing thread, in runs of 64 at most:
     static constexpr int kRun = kCols < 64 ? kCols : 64;        // what lies together in a pair's accumulator and in w
     static constexpr int kRuns = kCols / kRun;
     static constexpr int kLoad = BN == 256 ? 16 : kRun < 32 ? kRun : 32;  // columns of one tensor-memory load
-    static constexpr int kSumBytes = FEW ? 0 : kSumWarps * kStage;          // staging rows of the summing warps
+    static constexpr int kSumBytes = FEW ? 0 : kSumWarps * kStage;  // staging rows of the summing warps
 };
 
 // Registers a thread of the widest tile: the launch's 168 x 384 are dealt out as 56 for warps 0-3 and

@@ -244,3 +244,23 @@ assert torch.all(out == 256), out
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("rows,cols,inner", [(13, 300, 384), (30, 130, 200), (60, 256, 640)])
+def test_groups_of_few_rows_have_the_bits_that_they_have_in_a_longer_call(rows, cols, inner):
+    g = torch.Generator().manual_seed(rows)
+    a, sa = operand((300, inner), (300, blocks(inner)), g)
+    w, sw = operand((5, cols, inner), (5, blocks(cols), blocks(inner)), g)
+    off = torch.tensor([0, 0, 3, 4, rows - 2, rows], dtype=torch.int32, device="cuda")
+    ws = qm.alloc_fp8_matmul_workspace(300, cols, inner, 5)
+    out = [torch.zeros(n, cols, device="cuda") for n in (300, rows, rows)]
+    qm.qs_fp8_matmul(a, sa, w, sw, out[0], ws, off)
+    qm.qs_fp8_matmul(a[:rows], sa[:rows], w, sw, out[1], ws, off)
+    assert torch.equal(out[1], out[0][:rows]) and out[1].abs().amax(1).min() > 0
+    # a row of NaN codes, and an expert with a NaN scale, stay where they are
+    a.view(torch.uint8)[3] = 0x7F
+    sw[4] = float("nan")
+    qm.qs_fp8_matmul(a[:rows], sa[:rows], w, sw, out[2], ws, off)
+    keep = [r for r in range(rows - 2) if r != 3]
+    assert torch.equal(out[2][keep], out[1][keep])
+    assert torch.isnan(out[2][3]).all() and torch.isnan(out[2][rows - 2:]).all()
