@@ -14,7 +14,7 @@
 // A thread owns a row of the tile, so a block's scale is one number a thread (two where its columns are of two
 // weight blocks) and a step costs one multiply-add an element.
 // Tiles are 128 rows by BN weight rows, or, where there is work for all SMs in them, 256 x 256 of two CTAs, or, for groups
-// of a call of few rows, 128 weight rows by all of them with the operands' parts changed about.  A CTA
+// of few rows, 128 weight rows by 16 rows with the operands' parts changed about.  A CTA
 // takes tiles blockIdx.x, + gridDim.x, ... and its stages run on from one tile to the next.
 // Bound: weights from HBM where there are few rows a weight (2048 tokens to 8 of 256 experts, 2048 x 1024 each:
 // 93 us, 96 % of the copy rate), latency where a matrix is small (one row by 4096 x 2048: 4.8 us for 1.2 us of
@@ -41,6 +41,7 @@ constexpr int kFirstSum = 4;  // first of the warps that sum
 constexpr int kTileRows = 128;
 constexpr int kRowBox = 16;  // rows of the small TMA box of a are a multiple of this
 constexpr int kFewRows = 64; // most rows that are copied by small boxes
+constexpr int kFewTile = 16, kFewAverage = 4;  // rows of a tile of groups of few, and of their average group at most
 
 struct MmParams {
     // a as [block of K][row][128 columns] and w as [expert][block][row][128 columns], boxes of a group's blocks;
@@ -272,8 +273,8 @@ __device__ __forceinline__ Tile tile_at(const MmParams& p, const Groups& g, cons
 
 constexpr int kStage = 2048;  // bytes of a summing warp's staging rows: 32 of 64 bytes
 
-// FEW: all rows of the call fit one tile of FEW (16, 32 or 64) columns of an accumulator whose rows are 128 weight
-// rows: the matrix instruction's time goes with its columns, and those are then the call's rows.
+// FEW (0 or 16): the accumulator's rows are 128 weight rows and its columns FEW rows of a, since the matrix
+// instruction's time goes with its columns.
 template <int BN, int FEW = 0>
 struct MmShape {
     static_assert(FEW == 0 || BN == 128, "128 weight rows");
@@ -364,7 +365,7 @@ __device__ __forceinline__ void add_group(float2 (&acc)[MmShape<BN>::kRun / 2], 
     }
 }
 
-// The same for a tile of few rows: a thread's columns are rows of the call, each with its own scale (of block g at
+// The same for a tile of few rows: a thread's columns are rows of a, each with its own scale (of block g at
 // scale + g * step).
 template <int FEW>
 __device__ __forceinline__ void add_few(float2 (&acc)[MmShape<128, FEW>::kRun / 2], uint32_t src, const float* scale, int step,
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(MmShape<BN, FEW>::kThreads, 1) fp8_mm_kernel(c
                 // rows by boxes of box_rows, or (0) by one of 128; boxes of several blocks lie as the blocks do
                 // only if one holds all rows
                 const int boxes = PAIR ? 0
-                                : p.M <= kFewRows ? 1
+                                : FEW || p.M <= kFewRows ? 1
                                 : G == 1 && t.rows <= kFewRows ? (t.rows + p.box_rows - 1) / p.box_rows : 0;
                 const int abytes = (boxes ? boxes * p.box_rows : kTileRows) * 128;
                 for (int kb0 = 0; kb0 < p.KB; kb0 += G) {
@@ -706,10 +707,11 @@ __global__ void __launch_bounds__(MmShape<BN, FEW>::kThreads, 1) fp8_mm_kernel(c
                         const int nb = min(t.n0 / kScaleCols + (BN == 256 ? lane >> 3 : 0), p.NB - 1);
                         w = p.sw[((int64_t)t.e * p.NB + nb) * p.KB + kb];
                     }
-                    for (int r1 = 0; r1 < (FEW ? 64 : kTileRows); r1 += 64) {
-                        float v[16];
+                    constexpr int kReads = FEW ? FEW / 4 : 16;  // rows of a lane at a time
+                    for (int r1 = 0; r1 < (FEW ? FEW : kTileRows); r1 += 4 * kReads) {
+                        float v[kReads];
 #pragma unroll
-                        for (int i = 0; i < 16; i++) {
+                        for (int i = 0; i < kReads; i++) {
                             const int r = r1 + r0 + 4 * i;
                             v[i] = on && r < rows ? sa[(int64_t)r * p.sa_stride + kb] : 0.0f;
                         }
@@ -718,7 +720,7 @@ __global__ void __launch_bounds__(MmShape<BN, FEW>::kThreads, 1) fp8_mm_kernel(c
                             if (!ok) break;
                         }
 #pragma unroll
-                        for (int i = 0; i < 16; i++) sc.a[b][r1 + r0 + 4 * i] = FEW ? v[i] * w : v[i];
+                        for (int i = 0; i < kReads; i++) sc.a[b][r1 + r0 + 4 * i] = FEW ? v[i] * w : v[i];
                     }
                     if (!ok) break;
                     if (lane < 16) sc.w[lane >> 3][b] = w;
@@ -886,11 +888,10 @@ cudaError_t mm_facts(MmFacts** out) {
         if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
         f.smem = optin - (int)(sizeof(MmCtl) + sizeof(Groups) + 64);
-        const void* fns[9] = {(const void*)fp8_mm_kernel<16, false>,  (const void*)fp8_mm_kernel<32, false>,
+        const void* fns[7] = {(const void*)fp8_mm_kernel<16, false>,  (const void*)fp8_mm_kernel<32, false>,
                               (const void*)fp8_mm_kernel<64, false>,  (const void*)fp8_mm_kernel<128, false>,
                               (const void*)fp8_mm_kernel<256, false>, (const void*)fp8_mm_kernel<256, true>,
-                              (const void*)fp8_mm_kernel<128, false, 16>, (const void*)fp8_mm_kernel<128, false, 32>,
-                              (const void*)fp8_mm_kernel<128, false, 64>};
+                              (const void*)fp8_mm_kernel<128, false, kFewTile>};
         for (const void* fn : fns)
             if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess) return e;
         // the register split would wait forever on a launch with fewer
@@ -913,7 +914,7 @@ cudaError_t mm_run(const Fp8MmArgs& g, MmParams& p, const MmFacts& f, int64_t ti
     const bool few = g.n_rows <= kFewRows;
     p.blocked = g.n_inner % 128 == 0;
     p.box_rows = FEW ? FEW : few ? (g.n_rows + kRowBox - 1) / kRowBox * kRowBox : kRowBox;
-    p.a_bytes = few ? p.box_rows * 128 : kTileRows * 128;
+    p.a_bytes = FEW || few ? p.box_rows * 128 : kTileRows * 128;
     if (!encode8(&p.tw, true, g.w, g.n_inner, g.n_cols, g.w_stride, g.n_experts, g.w_expert_stride, p.blocked, BN / kCtas, G) ||
         !encode8(&p.tfew, false, g.a, g.n_inner, g.n_rows, g.a_stride, 1, 0, p.blocked, p.box_rows, G) ||
         !encode8(&p.ta128, false, g.a, g.n_inner, g.n_rows, g.a_stride, 1, 0, p.blocked, kTileRows, G))
@@ -981,15 +982,15 @@ cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t 
     const int64_t pair_tiles = (g.offsets ? (int64_t)g.n_rows / 256 + g.n_experts : ((int64_t)g.n_rows + 255) / 256) *
                                ((g.n_cols + 255) / 256);
     if (per > kTileRows && pair_tiles >= f->n_sm / 2) return mm_run<256, true>(g, p, *f, pair_tiles, st);
-    // Groups of a call of few rows: weight rows down the accumulator, the call's rows across.  Against the tiles
-    // below, 8 of 256 experts: one token at 2048 x 1024 (columns x inner) 4.6 us against 6.2, two 7.5 against 10.1,
-    // four at 1024 x 2048 13.6 against 15.1, eight 24.2 against 25.4; of 28 such shapes two lost, 3 and 7 % (eight
-    // tokens at 2048 x 1024 and 2048 x 512).
-    if (g.offsets && g.n_rows <= kFewRows) {
-        const int64_t tiles = (int64_t)std::min(g.n_rows, g.n_experts) * ((g.n_cols + 127) / 128);
-        if (g.n_rows <= 16) return mm_run<128, false, 16>(g, p, *f, tiles, st);
-        if (g.n_rows <= 32) return mm_run<128, false, 32>(g, p, *f, tiles, st);
-        return mm_run<128, false, 64>(g, p, *f, tiles, st);
+    // Groups of few rows: weight rows down the accumulator, the group's across, 16 a tile.  Against the tiles below, 8 of
+    // 256 experts: one token at 2048 x 1024 (columns x inner) 4.8 us against 6.3, eight 21.6 against 24.8, 128 80.1
+    // against 84.7; sixty-four rows to two experts, 2048 x 2048, 5.3 against 5.6.  At eight rows an expert and more what is
+    // gained where they spread evenly (82.5 against 86.8) is lost where they do not (31.5 against 24.4 if popularity
+    // falls with rank^-1.5), since each 16 rows take an expert's weights again.  Tiles of 32 and 64 rows, and of 64 weight
+    // rows, were slower: eight tokens at 1024 x 2048 22.5, 24.3 and 22.6 against 22.2.
+    if (g.offsets && g.n_rows <= std::max(kFewRows, kFewAverage * g.n_experts)) {
+        const int64_t tiles = ((int64_t)g.n_rows / kFewTile + std::min(g.n_rows, g.n_experts)) * ((g.n_cols + 127) / 128);
+        return mm_run<128, false, kFewTile>(g, p, *f, tiles, st);
     }
     // row tiles: those of one matrix, or for groups the most there can be if rows spread over the
     // experts (each group's last tile may be short)

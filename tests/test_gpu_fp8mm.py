@@ -73,7 +73,8 @@ def test_matmul_strides(rows):
 
 COUNTS = {
     "one row each": [1] * 12, "empty and full": [0, 0, 5, 0, 128, 1, 0, 129, 64, 65, 0, 300, 0], "all in one": [0, 0, 700, 0],
-    "none": [0, 0, 0], "many": [(7 * e) % 23 for e in range(256)], "last alone": [0] * 31 + [17], "sixty-four": [64] * 9, "one expert": [40], "seven": [2, 0, 5, 0], "fifty-five": [20, 1, 0, 34]}
+    "none": [0, 0, 0], "many": [(7 * e) % 23 for e in range(256)], "last alone": [0] * 31 + [17], "sixty-four": [64] * 9, "one expert": [40], "seven": [2, 0, 5, 0], "fifty-five": [20, 1, 0, 34],
+    "few each": [(5 * e) % 7 for e in range(128)], "few but one": [1] * 60 + [100] + [0] * 67}
 
 
 @pytest.mark.parametrize("name", list(COUNTS))
