@@ -265,3 +265,16 @@ def test_groups_of_few_rows_have_the_bits_that_they_have_in_a_longer_call(rows, 
     keep = [r for r in range(rows - 2) if r != 3]
     assert torch.equal(out[2][keep], out[1][keep])
     assert torch.isnan(out[2][3]).all() and torch.isnan(out[2][rows - 2:]).all()
+
+
+@pytest.mark.parametrize("rows,cols,inner,kind", [(1, 20000, 256, torch.bfloat16), (7, 19999, 200, torch.float32), (16, 20001, 640, torch.bfloat16)])
+def test_few_rows_by_many_columns(rows, cols, inner, kind):
+    test_matmul(rows, cols, inner, kind)
+    g = torch.Generator().manual_seed(rows)
+    a, sa = operand((100, inner), (100, blocks(inner)), g)
+    w, sw = operand((cols, inner), (blocks(cols), blocks(inner)), g)
+    out = [torch.zeros(n, cols, dtype=kind, device="cuda") for n in (100, rows)]
+    ws = qm.alloc_fp8_matmul_workspace(100, cols, inner)
+    qm.qs_fp8_matmul(a, sa, w, sw, out[0], ws)
+    qm.qs_fp8_matmul(a[:rows], sa[:rows], w, sw, out[1], ws)
+    assert torch.equal(out[0][:rows], out[1])
