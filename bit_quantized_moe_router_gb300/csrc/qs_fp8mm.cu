@@ -13,11 +13,11 @@
 //              and after the last block send the tile out through shared memory
 // A thread owns a row of the tile, so a block's scale is one number a thread (two where its columns are of two
 // weight blocks) and a step costs one multiply-add an element.
-// Tiles are 128 rows by BN weight rows, or, where there is work for all SMs in them, 256 x 256 of two CTAs, or, for groups
-// of few rows, 128 weight rows by 16 rows with the operands' parts changed about.  A CTA
+// Tiles are 128 rows by BN weight rows, or, where there is work for all SMs in them, 256 x 256 of two CTAs, or, for few
+// rows, 64 or 128 weight rows by 16 rows with the operands' parts changed about.  A CTA
 // takes tiles blockIdx.x, + gridDim.x, ... and its stages run on from one tile to the next.
 // Bound: weights from HBM where there are few rows a weight (2048 tokens to 8 of 256 experts, 2048 x 1024 each:
-// 93 us, 96 % of the copy rate), latency where a matrix is small (one row by 4096 x 2048: 4.8 us for 1.2 us of
+// 93 us, 96 % of the copy rate), latency where a matrix is small (one row by 4096 x 2048: 4.2 us for 1.2 us of
 // weights), and for long prompts the tensor cores and the sums between them: 8192 x 8192 x 4096 takes 184 us, 2.98
 // PFLOP/s; without the reads of accumulators 165, without the copies 169, without both 145.  With few rows the stage's row part is only as high as the
 // rows there are (the matrix instruction reads on into whatever follows: rows of the result that no
@@ -273,11 +273,12 @@ __device__ __forceinline__ Tile tile_at(const MmParams& p, const Groups& g, cons
 
 constexpr int kStage = 2048;  // bytes of a summing warp's staging rows: 32 of 64 bytes
 
-// FEW (0 or 16): the accumulator's rows are 128 weight rows and its columns FEW rows of a, since the matrix
-// instruction's time goes with its columns.
+// FEW (0 or 16): the accumulator's rows are BN weight rows and its columns FEW rows of a.  The matrix instruction reads
+// all its rows from shared memory, 128 bytes a cycle: with few rows of a down the accumulator most of that is of rows that
+// nobody stores: by 4096 x 16384 a group of four blocks took 0.52 us with 32 weight rows a tile, so 0.42 with 64.
 template <int BN, int FEW = 0>
 struct MmShape {
-    static_assert(FEW == 0 || BN == 128, "128 weight rows");
+    static_assert(FEW == 0 || BN == 64 || BN == 128, "an accumulator's rows");
     // The widest tile is two accumulators of 128 columns, filled and read one after the other: with one of
     // 256 the time from a read back to the next fill stood open, 700 cycles a block.
     static constexpr int kHalves = BN == 256 ? 2 : 1;
@@ -285,8 +286,8 @@ struct MmShape {
     static constexpr int kAcc = 4;                                       // accumulators in tensor memory
     // Blocks of K that pass through the roles as one: a stage, an accumulator (side by side, each block with its
     // own columns) and one round of barriers.  Waits, issue and release take 300 to 400 cycles whatever the
-    // width, which is all a narrow tile's time: one row by 4096 x 2048 took 6.0 us with one block at a time, 4.8 so.
-    static constexpr int kGroup = FEW ? 2 : BN >= 128 ? 1 : BN == 64 ? 2 : 4;
+    // width, which is all a narrow tile's time: one row by 4096 x 2048 took 6.0 us with one block at a time, 4.8 so (then in tiles of 32).
+    static constexpr int kGroup = FEW ? (BN == 64 ? 4 : 2) : BN >= 128 ? 1 : BN == 64 ? 2 : 4;
     static constexpr int kAccStep = kAccCols * kGroup;                   // columns of an accumulator
     static constexpr int kTmemCols = kAccStep * kAcc;                    // 256 or 512
     static constexpr int kSumWarps = 8;
@@ -367,10 +368,10 @@ __device__ __forceinline__ void add_group(float2 (&acc)[MmShape<BN>::kRun / 2], 
 
 // The same for a tile of few rows: a thread's columns are rows of a, each with its own scale (of block g at
 // scale + g * step).
-template <int FEW>
-__device__ __forceinline__ void add_few(float2 (&acc)[MmShape<128, FEW>::kRun / 2], uint32_t src, const float* scale, int step,
+template <int BN, int FEW>
+__device__ __forceinline__ void add_few(float2 (&acc)[MmShape<BN, FEW>::kRun / 2], uint32_t src, const float* scale, int step,
                                         int n, uint32_t empty, int lane) {
-    using S = MmShape<128, FEW>;
+    using S = MmShape<BN, FEW>;
     uint32_t d[S::kGroup][S::kLoad];
     tc::fence_after();
 #pragma unroll
@@ -458,6 +459,19 @@ __device__ __forceinline__ void store_rows(const MmParams& p, const float2 (&acc
                 }
         }
         __syncwarp();
+    }
+}
+
+// A weight row's part of a tile of few rows: the first `left` of a thread's rows of column `col`.
+template <int ROWS, typename T>
+__device__ __forceinline__ void store_few(const MmParams& p, const float2 (&acc)[ROWS / 2], int row0, int left, int col) {
+    T* out = static_cast<T*>(p.out) + (int64_t)row0 * p.out_stride + col;
+#pragma unroll
+    for (int i = 0; i < ROWS; i++, out += p.out_stride) {
+        const float v = i % 2 ? acc[i / 2].y : acc[i / 2].x;
+        if (i >= left) break;
+        if constexpr (sizeof(T) == 4) *out = v;
+        else *out = __float2bfloat16_rn(v);
     }
 }
 
@@ -619,7 +633,7 @@ __global__ void __launch_bounds__(MmShape<BN, FEW>::kThreads, 1) fp8_mm_kernel(c
             // the tensor cores take for it: two warps take turns.  Warp w has half w of every block of the widest
             // tile, else every second group; its accumulators are w and w + 2, and, the number of stages being
             // even, its stages every second one: it sees each phase of the barriers that it waits on.
-            constexpr uint32_t id = tc::idesc(0 /* e4m3 */, FEW ? 128 : kRows, S::kAccCols);
+            constexpr uint32_t id = tc::idesc(0 /* e4m3 */, FEW ? BN : kRows, S::kAccCols);
             constexpr int kTurn = 2 / S::kHalves;  // groups of blocks from one of the warp's to the next
             const int w = warp - 1, h = S::kHalves == 2 ? w : 0;
             const int per = (p.KB + G - 1) / G;    // groups of a tile
@@ -774,7 +788,7 @@ __global__ void __launch_bounds__(MmShape<BN, FEW>::kThreads, 1) fp8_mm_kernel(c
                     ok = __all_sync(0xffffffffu, mm_wait(&ctl.accfull[a], aphase, abort, p.status, 4));
                     if (!ok) break;
                     const uint32_t src = tc::taddr(tbase, quad * 32, a * S::kAccStep + sub * S::kCols), empty = accempty + a * 8;
-                    if constexpr (FEW != 0) add_few<FEW>(acc[0], src, &sc.a[i][sub * S::kCols], kTileRows + 4, n - i, empty, lane);
+                    if constexpr (FEW != 0) add_few<BN, FEW>(acc[0], src, &sc.a[i][sub * S::kCols], kTileRows + 4, n - i, empty, lane);
                     else if constexpr (G > 1) add_group<BN, PAIR>(acc[0], src, more, n - i, empty, lane);
                     else add_block<BN, PAIR>(acc, src, scale, empty, lane);
                     if ((a += S::kHalves) >= S::kAcc) {
@@ -792,16 +806,11 @@ __global__ void __launch_bounds__(MmShape<BN, FEW>::kThreads, 1) fp8_mm_kernel(c
             if (!ok) break;
             const Tile now = tile_at<kRows>(p, groups_of, look, nt, BN, u);
             if constexpr (FEW != 0) {  // a thread a weight row: a warp's lanes store neighbouring columns
-                const int col = now.n0 + r;
-#pragma unroll
-                for (int i = 0; i < S::kCols; i++) {
-                    const float v = i % 2 ? acc[0][i / 2].y : acc[0][i / 2].x;
-                    const int m = sub * S::kCols + i;
-                    if (m < now.rows && col < p.N) {
-                        const int64_t at = (int64_t)(now.row0 + m) * p.out_stride + col;
-                        if (p.out_dtype == QS_F32) static_cast<float*>(p.out)[at] = v;
-                        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
-                    }
+                // 64 rows of an accumulator lie in the first 16 lanes of each 32
+                const int col = now.n0 + (BN == 64 ? quad * 16 + lane : r), m0 = sub * S::kCols, left = now.rows - m0;
+                if (left > 0 && col < p.N && (BN == 128 || lane < 16)) {
+                    if (p.out_dtype == QS_F32) store_few<S::kCols, float>(p, acc[0], now.row0 + m0, left, col);
+                    else store_few<S::kCols, __nv_bfloat16>(p, acc[0], now.row0 + m0, left, col);
                 }
                 continue;
             }
@@ -888,10 +897,10 @@ cudaError_t mm_facts(MmFacts** out) {
         if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
         f.smem = optin - (int)(sizeof(MmCtl) + sizeof(Groups) + 64);
-        const void* fns[7] = {(const void*)fp8_mm_kernel<16, false>,  (const void*)fp8_mm_kernel<32, false>,
+        const void* fns[8] = {(const void*)fp8_mm_kernel<16, false>,  (const void*)fp8_mm_kernel<32, false>,
                               (const void*)fp8_mm_kernel<64, false>,  (const void*)fp8_mm_kernel<128, false>,
                               (const void*)fp8_mm_kernel<256, false>, (const void*)fp8_mm_kernel<256, true>,
-                              (const void*)fp8_mm_kernel<128, false, kFewTile>};
+                              (const void*)fp8_mm_kernel<64, false, kFewTile>, (const void*)fp8_mm_kernel<128, false, kFewTile>};
         for (const void* fn : fns)
             if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess) return e;
         // the register split would wait forever on a launch with fewer
@@ -983,21 +992,29 @@ cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t 
                                ((g.n_cols + 255) / 256);
     if (per > kTileRows && pair_tiles >= f->n_sm / 2) return mm_run<256, true>(g, p, *f, pair_tiles, st);
     // Groups of few rows: weight rows down the accumulator, the group's across, 16 a tile.  Against the tiles below, 8 of
-    // 256 experts: one token at 2048 x 1024 (columns x inner) 4.8 us against 6.3, eight 21.6 against 24.8, 128 80.1
+    // 256 experts: one token at 2048 x 1024 (columns x inner) 4.6 us against 6.3, eight 21.3 against 24.8, 128 80.1
     // against 84.7; sixty-four rows to two experts, 2048 x 2048, 5.3 against 5.6.  At eight rows an expert and more what is
     // gained where they spread evenly (82.5 against 86.8) is lost where they do not (31.5 against 24.4 if popularity
-    // falls with rank^-1.5), since each 16 rows take an expert's weights again.  Tiles of 32 and 64 rows, and of 64 weight
-    // rows, were slower: eight tokens at 1024 x 2048 22.5, 24.3 and 22.6 against 22.2.
+    // falls with rank^-1.5), since each 16 rows take an expert's weights again.  Tiles of 32 and 64 rows were slower (eight
+    // tokens at 1024 x 2048 22.5 and 24.3 against 22.2).  64 weight rows a tile where those leave half of the SMs free
+    // (one token at 512 x 2048 4.5 against 5.0 with 128; with more tiles they lose as often, 5.1 against 4.8 for two
+    // tokens through 4 experts at 1024 x 2048).
+    const int64_t few64 = ((int64_t)g.n_cols + 63) / 64, few128 = ((int64_t)g.n_cols + 127) / 128;
     if (g.offsets && g.n_rows <= std::max(kFewRows, kFewAverage * g.n_experts)) {
-        const int64_t tiles = ((int64_t)g.n_rows / kFewTile + std::min(g.n_rows, g.n_experts)) * ((g.n_cols + 127) / 128);
-        return mm_run<128, false, kFewTile>(g, p, *f, tiles, st);
+        const int64_t mt = (int64_t)g.n_rows / kFewTile + std::min(g.n_rows, g.n_experts);
+        if (2 * mt * few64 <= f->n_sm) return mm_run<64, false, kFewTile>(g, p, *f, mt * few64, st);
+        return mm_run<128, false, kFewTile>(g, p, *f, mt * few128, st);
     }
-    // One matrix and few rows, if there are such tiles for three SMs in four: one row by 20000 x 2048 11.0 us against 12.3,
-    // by 32768 x 4096 22.9 against 25.0, 16 rows 23.9 against 25.2; with fewer tiles the SMs left out cost more (16 rows
-    // by 8192 x 4096 8.8 against 8.3), and 32 rows take the weights twice (29.3 against 25.4).
-    const int64_t few_tiles = ((int64_t)g.n_cols + 127) / 128;
-    if (!g.offsets && g.n_rows <= kFewTile && 4 * few_tiles >= 3 * f->n_sm)
-        return mm_run<128, false, kFewTile>(g, p, *f, few_tiles, st);
+    // One matrix: the tiles of 64 weight rows if all have an SM, since one fills its SM with the K of 64 weight rows
+    // faster than the tiles below with theirs: 1 x 4096 x 2048 4.2 us against 4.8, 16 x 9728 x 2048 4.5 against 5.5,
+    // 100 x 1024 x 4096 5.5 against 7.0, 1 x 4096 x 16384 16.8 against 19.7; at K of 1024 and less the same or better.
+    // Else those of 128 for 16 rows: 1 x 10000 x 2048 5.0 against 7.8, 1 x 32768 x 4096 22.9 against 25.0; 32 rows would
+    // take the weights twice (29.3 against 25.4).
+    if (!g.offsets) {
+        const int64_t mt = ((int64_t)g.n_rows + kFewTile - 1) / kFewTile;
+        if (mt * few64 <= f->n_sm) return mm_run<64, false, kFewTile>(g, p, *f, mt * few64, st);
+        if (mt == 1) return mm_run<128, false, kFewTile>(g, p, *f, few128, st);
+    }
     // row tiles: those of one matrix, or for groups the most there can be if rows spread over the
     // experts (each group's last tile may be short)
     const int64_t mt = g.offsets ? (int64_t)g.n_rows / kTileRows + std::min(g.n_rows, g.n_experts)

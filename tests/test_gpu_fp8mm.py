@@ -278,3 +278,16 @@ def test_few_rows_by_many_columns(rows, cols, inner, kind):
     qm.qs_fp8_matmul(a, sa, w, sw, out[0], ws)
     qm.qs_fp8_matmul(a[:rows], sa[:rows], w, sw, out[1], ws)
     assert torch.equal(out[0][:rows], out[1])
+
+
+@pytest.mark.parametrize("rows,cols,inner,kind", [
+    (1, 4096, 2048, torch.bfloat16), (9, 63, 129, torch.float32), (33, 65, 1000, torch.bfloat16), (100, 1000, 640, torch.float32),
+    (16, 9728, 130, torch.bfloat16), (17, 9728, 130, torch.bfloat16), (16, 9729, 256, torch.float32), (2000, 64, 300, torch.float32)])
+def test_tiles_of_few_rows(rows, cols, inner, kind):
+    test_matmul(rows, cols, inner, kind)
+
+
+@pytest.mark.parametrize("cols", [100, 512])
+def test_one_group_of_few_tiles(cols):
+    test_grouped("seven", cols, 520, torch.bfloat16)
+    test_grouped("one expert", cols, 1024, torch.float32)
