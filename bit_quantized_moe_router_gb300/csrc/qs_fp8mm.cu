@@ -273,9 +273,9 @@ __device__ __forceinline__ Tile tile_at(const MmParams& p, const Groups& g, cons
 
 constexpr int kStage = 2048;  // bytes of a summing warp's staging rows: 32 of 64 bytes
 
-// FEW (0 or 16): the accumulator's rows are BN weight rows and its columns FEW rows of a.  The matrix instruction reads
-// all its rows from shared memory, 128 bytes a cycle: with few rows of a down the accumulator most of that is of rows that
-// nobody stores: by 4096 x 16384 a group of four blocks took 0.52 us with 32 weight rows a tile, so 0.42 with 64.
+// FEW (0 or 16): the accumulator's rows are BN weight rows and its columns FEW rows of a.  A block's instructions cost
+// about the same whoever the 128 rows are: by 4096 x 16384 a group of four blocks took 0.52 us with 32 weight rows across
+// and one row of a among the 128 down, 0.42 us with 64 weight rows down.
 template <int BN, int FEW = 0>
 struct MmShape {
     static_assert(FEW == 0 || BN == 64 || BN == 128, "an accumulator's rows");
