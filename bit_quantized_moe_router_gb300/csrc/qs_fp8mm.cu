@@ -14,14 +14,14 @@
 // A thread owns a row of the tile, so a block's scale is one number a thread (two where its columns are of two
 // weight blocks) and a step costs one multiply-add an element.
 // Tiles are 128 rows by BN weight rows, or, where there is work for all SMs in them, 256 x 256 of two CTAs, or, for few
-// rows, 64 or 128 weight rows by 16 rows with the operands' parts changed about.  A CTA
-// takes tiles blockIdx.x, + gridDim.x, ... and its stages run on from one tile to the next.
+// rows, 64 or 128 weight rows by 16 or 32 rows with the operands' parts changed about.  A CTA takes tiles blockIdx.x,
+// + gridDim.x, ... and its stages run on from one tile to the next.
 // Bound: weights from HBM where there are few rows a weight (2048 tokens to 8 of 256 experts, 2048 x 1024 each:
 // 93 us, 96 % of the copy rate), latency where a matrix is small (one row by 4096 x 2048: 4.2 us for 1.2 us of
-// weights), and for long prompts the tensor cores and the sums between them: 8192 x 8192 x 4096 takes 184 us, 2.98
-// PFLOP/s; without the reads of accumulators 165, without the copies 169, without both 145.  With few rows the stage's row part is only as high as the
-// rows there are (the matrix instruction reads on into whatever follows: rows of the result that no
-// thread stores), so that nearly all of shared memory holds weights in flight.
+// weights), and for long prompts the tensor cores and the sums between them: 8192 x 8192 x 4096 takes 180 us, 3.05
+// PFLOP/s; without the reads of accumulators 165, without the copies 169, without both 145.  With 64 rows at most the
+// stage's row part is only as high as the rows there are (the matrix instruction reads on into whatever follows:
+// rows of the result that no thread stores), so that nearly all of shared memory holds weights in flight.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -273,7 +273,7 @@ __device__ __forceinline__ Tile tile_at(const MmParams& p, const Groups& g, cons
 
 constexpr int kStage = 2048;  // bytes of a summing warp's staging rows: 32 of 64 bytes
 
-// FEW (0 or 16): the accumulator's rows are BN weight rows and its columns FEW rows of a.  A block's instructions cost
+// FEW (0, 16 or 32): the accumulator's rows are BN weight rows and its columns FEW rows of a.  A block's instructions cost
 // about the same whoever the 128 rows are: by 4096 x 16384 a group of four blocks took 0.52 us with 32 weight rows across
 // and one row of a among the 128 down, 0.42 us with 64 weight rows down.
 template <int BN, int FEW = 0>
@@ -897,10 +897,11 @@ cudaError_t mm_facts(MmFacts** out) {
         if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
         f.smem = optin - (int)(sizeof(MmCtl) + sizeof(Groups) + 64);
-        const void* fns[8] = {(const void*)fp8_mm_kernel<16, false>,  (const void*)fp8_mm_kernel<32, false>,
+        const void* fns[9] = {(const void*)fp8_mm_kernel<16, false>,  (const void*)fp8_mm_kernel<32, false>,
                               (const void*)fp8_mm_kernel<64, false>,  (const void*)fp8_mm_kernel<128, false>,
                               (const void*)fp8_mm_kernel<256, false>, (const void*)fp8_mm_kernel<256, true>,
-                              (const void*)fp8_mm_kernel<64, false, kFewTile>, (const void*)fp8_mm_kernel<128, false, kFewTile>};
+                              (const void*)fp8_mm_kernel<64, false, kFewTile>, (const void*)fp8_mm_kernel<64, false, 2 * kFewTile>,
+                              (const void*)fp8_mm_kernel<128, false, kFewTile>};
         for (const void* fn : fns)
             if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess) return e;
         // the register split would wait forever on a launch with fewer
@@ -1008,11 +1009,15 @@ cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t 
     // One matrix: the tiles of 64 weight rows if all have an SM, since one fills its SM with the K of 64 weight rows
     // faster than the tiles below with theirs: 1 x 4096 x 2048 4.2 us against 4.8, 16 x 9728 x 2048 4.5 against 5.5,
     // 100 x 1024 x 4096 5.5 against 7.0, 1 x 4096 x 16384 16.8 against 19.7; at K of 1024 and less the same or better.
+    // Then the same with 32 rows: 64 x 4864 x 4096 6.4 against 7.9, 200 x 1024 x 2048 4.8 against 5.2, 512 x 512 x 1024
+    // 4.0 against 4.1 (with 64 rows 4.5: slower than what follows in 60 of 80 such shapes).
     // Else those of 128 for 16 rows: 1 x 10000 x 2048 5.0 against 7.8, 1 x 32768 x 4096 22.9 against 25.0; 32 rows would
     // take the weights twice (29.3 against 25.4).
     if (!g.offsets) {
         const int64_t mt = ((int64_t)g.n_rows + kFewTile - 1) / kFewTile;
         if (mt * few64 <= f->n_sm) return mm_run<64, false, kFewTile>(g, p, *f, mt * few64, st);
+        const int64_t mt32 = (mt + 1) / 2;
+        if (mt32 * few64 <= f->n_sm) return mm_run<64, false, 2 * kFewTile>(g, p, *f, mt32 * few64, st);
         if (mt == 1) return mm_run<128, false, kFewTile>(g, p, *f, few128, st);
     }
     // row tiles: those of one matrix, or for groups the most there can be if rows spread over the

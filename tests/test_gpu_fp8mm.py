@@ -282,7 +282,7 @@ def test_few_rows_by_many_columns(rows, cols, inner, kind):
 
 @pytest.mark.parametrize("rows,cols,inner,kind", [
     (1, 4096, 2048, torch.bfloat16), (9, 63, 129, torch.float32), (33, 65, 1000, torch.bfloat16), (100, 1000, 640, torch.float32),
-    (16, 9728, 130, torch.bfloat16), (17, 9728, 130, torch.bfloat16), (16, 9729, 256, torch.float32), (2000, 64, 300, torch.float32)])
+    (16, 9728, 130, torch.bfloat16), (17, 9728, 130, torch.bfloat16), (64, 4864, 200, torch.float32), (65, 3201, 1100, torch.bfloat16), (500, 511, 640, torch.bfloat16), (16, 9729, 256, torch.float32), (2000, 64, 300, torch.float32)])
 def test_tiles_of_few_rows(rows, cols, inner, kind):
     test_matmul(rows, cols, inner, kind)
 
@@ -291,3 +291,17 @@ def test_tiles_of_few_rows(rows, cols, inner, kind):
 def test_one_group_of_few_tiles(cols):
     test_grouped("seven", cols, 520, torch.bfloat16)
     test_grouped("one expert", cols, 1024, torch.float32)
+
+
+@pytest.mark.parametrize("cols,inner", [(4096, 512), (900, 1100)])
+def test_a_row_has_the_same_bits_in_calls_of_any_length(cols, inner):
+    g = torch.Generator().manual_seed(cols)
+    a, sa = operand((2600, inner), (2600, blocks(inner)), g)
+    w, sw = operand((cols, inner), (blocks(cols), blocks(inner)), g)
+    ws = qm.alloc_fp8_matmul_workspace(2600, cols, inner)
+    full = torch.empty(2600, cols, device="cuda")
+    qm.qs_fp8_matmul(a, sa, w, sw, full, ws)
+    for rows in (1, 16, 17, 33, 64, 65, 100, 129, 333, 1000):
+        out = torch.empty(rows, cols, device="cuda")
+        qm.qs_fp8_matmul(a[:rows], sa[:rows], w, sw, out, ws)
+        assert torch.equal(out, full[:rows])
