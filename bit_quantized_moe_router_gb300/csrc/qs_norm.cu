@@ -88,18 +88,19 @@ __global__ void __launch_bounds__(32 * cta_warps(G)) rmsnorm_kernel(const NormAr
     group_sum<G, 1>(ss, red[group], wg, lane, 1 + group);
     const float rho = rsqrtf(ss[0] / (float)p.hidden + p.eps);
     void* yr = p.y ? row_at(p.y, p.y_stride, type_size(y_type), t) : nullptr;
-    // rho is left to the end, where it costs the codes no rounding; rows so small that it is large take it at once
-    const float factor = rho > 65536.0f ? 1.0f : rho, least = kMinAmax / factor;
+    // rho is left to the end, where it costs the codes no rounding; rows so small that it is large take it at once, and
+    // so do those whose sum of squares is infinite, since kMinAmax over their rho of 0 made every block's scale a NaN
+    const float factor = rho > 65536.0f || rho == 0.0f ? 1.0f : rho, least = kMinAmax / factor;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
         float w[8];  // read here, not before the barrier: early, it took 10 % more at 8192 fp32 columns and gave decode 0.15 us
         load8_row<VEC>(p.weight, QS_F32, col(j), p.hidden, w);
-#pragma unroll
-        for (int q = 0; q < 8; q++) s[j][0][q] *= w[q];
         if (rho != factor) {
 #pragma unroll
             for (int q = 0; q < 8; q++) s[j][0][q] *= rho;
         }
+#pragma unroll
+        for (int q = 0; q < 8; q++) s[j][0][q] *= w[q];
         if (p.q) {
             uint8_t* q_row = p.q + t * p.q_stride;
             float* scale_row = p.q_scale + t * p.q_scale_stride;

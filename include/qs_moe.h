@@ -382,10 +382,11 @@ typedef struct {
  *   s = x_t + residual_t (x_t without a residual), in fp32
  *   v = s * weight / sqrt(mean(s^2) + eps), in fp32
  * sum_out (if there) gets s rounded to its type, y (if there) v rounded to its
- * type, q (if there) v as codes with scales.  The norm is of s
- * before its rounding to sum_out.  x, residual, sum_out and y are fp32 or bf16,
- * each by its own type; weight is device fp32 [hidden].  sum_out may be x or
- * residual itself (same address, stride and type).  1 <= hidden <= 16384,
+ * type, q (if there) v as codes with scales.  The norm is of s before its
+ * rounding to sum_out.  Where a row's sum of squares passes fp32's range its
+ * factor is 0: v is 0, or a NaN where s is infinite.  x, residual, sum_out and
+ * y are fp32 or bf16, each by its own type; weight is device fp32 [hidden].
+ * sum_out may be x or residual itself (same address, stride and type).  1 <= hidden <= 16384,
  * eps >= 0 and finite; at least one of y, q and sum_out.  One launch. */
 int qs_rmsnorm_residual(const qs_rmsnorm_args *args, void *stream);
 

@@ -1,0 +1,50 @@
+"""Row operators at the ends of fp32's range, on the GPU against 64-bit forms.
+
+Tolerances: 2^-24 (U) of the value a rounding, 2^-4 of the value or 2^-10 of the scale for a code, as the operators'
+other tests count them.
+"""
+import pytest
+import torch
+
+from bit_quantized_moe_router_gb300 import qs_moe as qm
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+F8 = torch.float8_e4m3fn
+LEAST = 2.0 ** -100 / 448  # the scale of a block of zeros
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def codes(rows, cols):
+    q = torch.full((rows, cols), 0x55, dtype=torch.uint8, device="cuda").view(F8)
+    return q, torch.full((rows, (cols + 127) // 128), -1.0, device="cuda")
+
+
+@pytest.mark.parametrize("hidden", [128, 640, 641, 2048, 4096, 8192, 16384])
+def test_codes_of_rows_whose_sum_of_squares_is_infinite(hidden):
+    """Codes are made of v: an infinity's own v is a NaN (infinity times the factor 0), all others are 0, as y has them."""
+    x = torch.randn(5, hidden, generator=gen(hidden))
+    x[1, 100] = float("inf")
+    x[2, 3] = -float("inf")
+    x[3, 7] = 1e25  # finite; its square is not
+    w = 0.5 + torch.rand(hidden, generator=gen(1))
+    q, scale = codes(5, hidden)
+    y = torch.empty(5, hidden, device="cuda")
+    qm.qs_rmsnorm_residual(x.cuda(), None, w.cuda(), 1e-5, y=y, q=q, q_scale=scale)
+    nan = torch.zeros(5, hidden, dtype=torch.bool)
+    nan[1, 100] = nan[2, 3] = True
+    got, y, scale = q.float().cpu(), y.cpu(), scale.cpu()
+    assert torch.equal(torch.isnan(y), nan) and torch.equal(torch.isnan(got), nan)
+    flat = torch.zeros(5, 1, dtype=torch.bool)
+    flat[1:4] = True
+    assert torch.all(y[(flat & ~nan)] == 0) and torch.all(got[(flat & ~nan)] == 0)
+    # 448 goes in as its rounded reciprocal: two roundings
+    assert torch.all((scale[1:4].double() - LEAST).abs() <= 2 * U * LEAST)
+    assert torch.all(torch.isfinite(scale[[0, 4]])) and torch.all(got[[0, 4]].abs().amax(1) == 448)
+    alone = codes(5, hidden)
+    qm.qs_rmsnorm_residual(x.cuda(), None, w.cuda(), 1e-5, q=alone[0], q_scale=alone[1])
+    assert torch.equal(alone[0].view(torch.uint8), q.view(torch.uint8)) and torch.equal(alone[1].cpu(), scale)
