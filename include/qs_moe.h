@@ -402,7 +402,7 @@ typedef struct {
 
 /* Gradient of qs_rmsnorm_residual's y and sum_out.  With s the rows of sum
  * (what sum_out held), rho = 1 / sqrt(mean(s^2) + eps), per row
- *   dx = rho * weight * dy - s * rho^3 * mean(weight * dy * s) + dsum
+ *   dx = rho * (weight * dy - s * rho * (rho * mean(weight * dy * s))) + dsum
  * (dsum: the gradient that reaches s by the residual stream, if any); it is the
  * gradient of x and of residual alike.  dweight (fp32 [hidden], or NULL) is
  * overwritten with the sum over rows of dy * s * rho; its rows are added in a

@@ -48,3 +48,25 @@ def test_codes_of_rows_whose_sum_of_squares_is_infinite(hidden):
     alone = codes(5, hidden)
     qm.qs_rmsnorm_residual(x.cuda(), None, w.cuda(), 1e-5, q=alone[0], q_scale=alone[1])
     assert torch.equal(alone[0].view(torch.uint8), q.view(torch.uint8)) and torch.equal(alone[1].cpu(), scale)
+
+
+@pytest.mark.parametrize("hidden", [264, 1001, 2048, 4096, 16384])
+@pytest.mark.parametrize("size,eps", [(1e-13, 0.0), (1e-17, 0.0), (1e-13, 1e-30), (1e-8, 1e-20), (1e8, 1e-5), (1e14, 1e-5), (1e15, 1e-5), (1e16, 1e-5)])
+def test_norm_gradient_of_tiny_and_huge_rows(hidden, size, eps):
+    """dx and dweight hold where 1 / rms cubed leaves fp32 (the sum of squares does not, at these sizes)."""
+    rows, g = 5, gen(hidden)
+    s, w = torch.randn(rows, hidden, generator=g) * size, 0.5 + torch.rand(hidden, generator=g)
+    dy = torch.randn(rows, hidden, generator=g) + 0.1 * s / size  # a part along s, so that the mean of dy * s counts
+    dsum = torch.randn(rows, hidden, generator=g) / size
+    dx, dw = torch.empty(rows, hidden, device="cuda"), torch.empty(hidden, device="cuda")
+    qm.qs_rmsnorm_residual_backward(s.cuda(), w.cuda(), eps, dy.cuda(), dsum.cuda(), dx, dw, qm.alloc_rmsnorm_backward_workspace(hidden))
+    eps = float(torch.tensor(eps, dtype=torch.float32))
+    s, w, dy, dsum = s.double(), w.double(), dy.double(), dsum.double()
+    rho = 1 / torch.sqrt(s.pow(2).mean(1, keepdim=True) + eps)
+    unit = s * rho
+    along = (w * dy * unit).mean(1, keepdim=True)
+    want = rho * (w * dy - unit * along) + dsum
+    terms = rho * ((w * dy).abs() + unit.abs() * (w * dy * unit).abs().mean(1, keepdim=True)) + dsum.abs()
+    # the row's two sums at most 48 U each, the first under a root; rho three times, a rounding a product
+    assert torch.all((dx.cpu().double() - want).abs() <= 160 * U * terms)
+    assert torch.all((dw.cpu().double() - (dy * unit).sum(0)).abs() <= 160 * U * (dy * unit).abs().sum(0))
