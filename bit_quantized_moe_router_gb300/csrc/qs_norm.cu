@@ -236,11 +236,20 @@ __global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* __re
     if (lane == 0 && c < hidden) dweight[c] = v;
 }
 
-// silu(g) * u.  __expf is off by at most 2 + 1.2 |g| units in the last place, which counts where g is negative and
-// exp(-g) large, and __fdividef by 2: under 2^-19 of the value for |g| <= 20, far inside its code's 2^-4.  The kernel
-// waits for instructions as much as for memory: 30.5 us at 65536 x 512, 34.8 with expf, 25 of memory time.
-// Past g = -87 the quotient is 0.
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// silu(g) * u = g u / (1 + exp(-g)).  exp(-g) = 2^h (1 + r) with h the fp32 value next to -g / ln 2 and r = -g - h ln 2,
+// what its rounding left out: without r the value is off by up to |g| 2^-24, which a block's scale shows where all its
+// gates are far below zero (65536 x 512: 30.0 us without r, 31.2 with it, 37.0 with expf and __fdividef).  ex2.approx is off
+// by 2^-22 at most, r by 2^-29 |h| (ln 2 in fp32), rcp.approx by 2^-23: with the other roundings under 2^-20 of the value.
+// Below g = -87.3, where 1 / (1 + exp(-g)) is no normal number, the value is 0.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    constexpr double kLn2 = 0.69314718055994531;
+    const float t = fminf(fmaxf(g, -88.0f), 88.0f), h = t * (float)(-1.0 / kLn2), r = fmaf(h, -(float)kLn2, -t);
+    float e, d;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(h));
+    e = fmaf(e, r, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(1.0f + e));
+    return g * d * u;
+}
 
 // Eight lanes a (row, 128 columns): sixteen elements of gate and of up each.
 template <bool VEC>
@@ -377,7 +386,7 @@ cudaError_t launch_silu_mul_quant(const SiluArgs& p, cudaStream_t st) {
     const bool vec = p.ffn % 8 == 0 && al16(p.gate_up, p.gate_up_stride, p.dtype) &&
                      (p.ffn * type_size(p.dtype)) % 16 == 0 && ((uintptr_t)p.q & 7u) == 0 && p.q_stride % 8 == 0;
     const int64_t work = (int64_t)p.n_rows * scale_blocks(p.ffn);
-    const unsigned grid = (unsigned)std::min<int64_t>((work + 31) / 32, 1216);  // eight CTAs an SM walk on: 30.5 us at 65536 x 512 against 34.3 with one step each
+    const unsigned grid = (unsigned)std::min<int64_t>((work + 31) / 32, 1216);  // eight CTAs an SM walk on: 31.2 us at 65536 x 512; with one step each 12 % more
     return vec ? launch_pdl(silu_mul_quant_kernel<true>, dim3(grid), 256, 0, st, p)
                : launch_pdl(silu_mul_quant_kernel<false>, dim3(grid), 256, 0, st, p);
 }

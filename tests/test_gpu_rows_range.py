@@ -70,3 +70,44 @@ def test_norm_gradient_of_tiny_and_huge_rows(hidden, size, eps):
     # the row's two sums at most 48 U each, the first under a root; rho three times, a rounding a product
     assert torch.all((dx.cpu().double() - want).abs() <= 160 * U * terms)
     assert torch.all((dw.cpu().double() - (dy * unit).sum(0)).abs() <= 160 * U * (dy * unit).abs().sum(0))
+
+
+@pytest.mark.parametrize("ffn", [5, 128, 512, 1001])
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("gate", [-1.0, -9.0, -20.0, -40.0, -80.0, -86.0])
+def test_silu_of_gates_far_below_zero(ffn, kind, gate):
+    """A block's scale and codes are as near where all gates are far below zero as elsewhere.
+
+    Units in the last place (2 U): the exponential 2 and its argument's remainder half of one; 1 + exp, product with the
+    gate and product with up half each; quotient 2: under 12 U together, and the scale's own two roundings.
+    """
+    rows = 40
+    g = gen(ffn)
+    gu = torch.empty(rows, 2 * ffn)
+    gu[:, :ffn] = gate + 0.5 * torch.rand(rows, ffn, generator=g)
+    gu[:, ffn:] = torch.randn(rows, ffn, generator=g) * 1e12  # so that no block's largest value is below 2^-100
+    gu = gu.to(kind)
+    q, scale = codes(rows, ffn)
+    qm.qs_silu_mul_quant(gu.cuda(), q, scale)
+    a, b = gu.double().chunk(2, 1)
+    v = a / (1 + torch.exp(-a)) * b
+    nb = scale.shape[1]
+    wide = torch.zeros(rows, nb * 128, dtype=torch.float64)
+    wide[:, :ffn] = v
+    amax = wide.abs().view(rows, nb, 128).amax(2)
+    got = scale.cpu().double()
+    assert float(amax.min()) > 2.0 ** -100
+    assert torch.all((got - amax / 448).abs() <= 14 * U * amax / 448)
+    per = got.repeat_interleave(128, 1)[:, :ffn]
+    assert torch.all((q.cpu().float().double() * per - v).abs() <= v.abs() * (2.0 ** -4 + 16 * U) + per * 2.0 ** -10)
+
+
+def test_silu_of_infinite_and_nan_gates():
+    inf, nan = float("inf"), float("nan")
+    gu = torch.zeros(5, 256)
+    gu[:, :128] = torch.tensor([200.0, inf, -inf, nan, -1e30])[:, None]
+    gu[:, 128:] = 2.0
+    q, scale = codes(5, 128)
+    qm.qs_silu_mul_quant(gu.cuda(), q, scale)
+    v = (q.float() * scale).cpu()
+    assert torch.all((v[0] - 400).abs() <= 400 * 4 * U) and torch.all(torch.isnan(v[1:4])) and torch.all(v[4] == 0)
