@@ -375,8 +375,10 @@ cudaError_t dispatch_run(const DispatchArgs& p, cudaStream_t st) {
 }  // namespace
 
 size_t dispatch_workspace(int n_tokens, int top_k, int n_experts) {
-    const int64_t n = (int64_t)n_tokens * top_k;
-    return n <= kSmallN ? 256 : ((size_t)chunk_count(n) * n_experts * 4 + 255) / 256 * 256;
+    // a histogram a chunk, for the most chunks that n entries or fewer have: past 262144 entries chunks grow by 32 at a
+    // time and their number falls, but a workspace is for calls of up to its size
+    const int64_t n = (int64_t)n_tokens * top_k, most = std::min<int64_t>((n + kChunk - 1) / kChunk, kMaxChunks);
+    return n <= kSmallN ? 256 : ((size_t)most * n_experts * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_dispatch(const DispatchArgs& p, cudaStream_t st) {

@@ -111,3 +111,20 @@ def test_silu_of_infinite_and_nan_gates():
     qm.qs_silu_mul_quant(gu.cuda(), q, scale)
     v = (q.float() * scale).cpu()
     assert torch.all((v[0] - 400).abs() <= 400 * 4 * U) and torch.all(torch.isnan(v[1:4])) and torch.all(v[4] == 0)
+
+
+def test_dispatch_with_a_workspace_made_for_more_tokens():
+    """Calls on both sides of the size from which chunks of the sort grow (262144 entries), in one workspace."""
+    k, experts = 8, 256
+    ws = qm.alloc_dispatch_workspace(33000, k, experts)
+    for tokens in (33000, 32769, 32768, 32700, 600, 512, 1):
+        ids = torch.randint(-1, experts, (tokens, k), generator=gen(tokens), dtype=torch.int32).cuda()
+        i32 = dict(dtype=torch.int32, device="cuda")
+        counts, offsets, perm, pos = torch.empty(experts, **i32), torch.empty(experts + 1, **i32), torch.empty(tokens * k, **i32), torch.empty(tokens, k, **i32)
+        qm.qs_dispatch_tokens(ids, None, None, counts, offsets, perm, pos, None, None, ws)
+        flat = torch.where(ids < 0, experts, ids).flatten().long()
+        order, total = torch.sort(flat, stable=True).indices, int((flat < experts).sum())
+        assert torch.equal(counts.long(), torch.bincount(flat, minlength=experts + 1)[:experts])
+        assert torch.equal(offsets[1:].long(), counts.long().cumsum(0)) and int(offsets[0]) == 0
+        assert torch.equal(perm[:total].long(), order[:total]) and torch.all(perm[total:] == -1)
+        assert torch.equal(pos.flatten()[order[:total]].long(), torch.arange(total, device="cuda")) and torch.all(pos[ids < 0] == -1)

@@ -146,3 +146,16 @@ def test_binding_refuses_wrong_tensors():
         qm.qs_combine_tokens_backward(host, None, torch.zeros(2, 2, dtype=torch.int32), None, host, dtopk_w=host)
     with pytest.raises(ValueError, match="experts, cols, inner"):
         qm.qs_fp8_matmul(host, host, host, host, host, host, offsets=host)
+
+
+@pytest.mark.parametrize("top_k", [1, 2, 3, 8, 32])
+@pytest.mark.parametrize("experts", [1, 7, 256, 1024])
+def test_a_dispatch_workspace_is_enough_for_every_smaller_call(top_k, experts):
+    size = qm.load().qs_dispatch_workspace_bytes
+    entries = [*range(1, 9000, 61), *range(260000, 273000, 32), *range(300000, 1200000, 7919), 1 << 24, (1 << 24) + 1, 1 << 30]
+    tokens = sorted({max(1, n // top_k + d) for n in entries for d in (-1, 0, 1)} - {(1 << 30) // top_k + 1})
+    sizes = [size(t, top_k, experts) for t in tokens]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    assert all(size(t, k, e) <= size(t, top_k, experts) for t in tokens[::50] for k, e in ((1, experts), (top_k, 1)))
+    # a chunk of at least 1024 entries has its histogram
+    assert all(s >= 4 * experts * min(256, t * top_k // 1024) for s, t in zip(sizes, tokens) if t * top_k > 4096)
