@@ -354,7 +354,7 @@ def qs_test_wait_timeout(workspace, limit_us, stream=None):
 # ------------------------------------------------------------------ row operators
 #
 # Matrices are 2-D tensors whose columns are contiguous; rows may be strided.  fp32 and bf16 tensors are
-# torch.float32 and torch.bfloat16, e4m3 codes torch.float8_e4m3fn.
+# torch.float32 and torch.bfloat16, e4m3 codes torch.float8_e4m3fn.  All of a call's tensors are on the current device.
 
 _WIDE = {torch.float32: QS_F32, torch.bfloat16: QS_BF16}
 _E4M3 = {torch.float8_e4m3fn: QS_E4M3}
@@ -375,10 +375,17 @@ _pack_norm, _pack_norm_bwd, _pack_silu, _pack_matmul, _pack_dispatch, _pack_comb
     a.pack for a in ARGS.values())
 
 
-def _refuse(t, what, shape, dtypes):
+_F32 = {torch.float32: QS_F32}
+_I32 = {torch.int32: 0}
+_current_device = torch._C._cuda_getDevice
+
+
+def _refuse(t, what, shape, dtypes, dev):
     """Say what is wrong with a tensor that _matrix or _flat does not take."""
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a tensor in device memory, got one on {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, the call's first operand on cuda:{dev}")
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: {t.dtype} is not one of {', '.join(str(d) for d in dtypes)}")
     if tuple(t.shape) != tuple(shape):
@@ -386,34 +393,40 @@ def _refuse(t, what, shape, dtypes):
     raise ValueError(f"{what}: expected contiguous {'columns' if t.dim() > 1 else 'elements'}")
 
 
-def _matrix(t, what, shape, dtypes=_WIDE):
-    """(address, row stride, type) of a matrix of this shape."""
+def _device(t, what):
+    """The device of a call's first operand.  The library launches on the current device, so it has to be that one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{what}: expected a tensor in device memory, got one on {t.device}")
+    if dev != _current_device():
+        raise ValueError(f"{what}: on cuda:{dev}, but cuda:{_current_device()} is the current device")
+    return dev
+
+
+def _matrix(t, what, shape, dev, dtypes=_WIDE):
+    """(address, row stride, type) of a matrix of this shape on device dev."""
     kind = dtypes.get(t.dtype)
-    if kind is None or t.shape != shape or not t.is_cuda:
-        _refuse(t, what, shape, dtypes)
+    if kind is None or t.shape != shape or t.get_device() != dev:
+        _refuse(t, what, shape, dtypes, dev)
     stride, col = t.stride()
     if col != 1 and shape[1] > 1 and shape[0] > 0:
-        _refuse(t, what, shape, dtypes)
+        _refuse(t, what, shape, dtypes, dev)
     return t.data_ptr(), stride, kind
 
 
-def _codes(q, scale, what, shape):
+def _codes(q, scale, what, shape, dev):
     """(codes, stride, scales, stride) of an e4m3 matrix."""
     if scale is None:
         raise ValueError(f"{what}: e4m3 codes come with scales")
-    a, s, _ = _matrix(q, what, shape, _E4M3)
-    b, u, _ = _matrix(scale, what + " scale", (shape[0], (shape[1] + 127) // 128), _F32)
+    a, s, _ = _matrix(q, what, shape, dev, _E4M3)
+    b, u, _ = _matrix(scale, what + " scale", (shape[0], (shape[1] + 127) // 128), dev, _F32)
     return a, s, b, u
 
 
-_F32 = {torch.float32: QS_F32}
-_I32 = {torch.int32: 0}
-
-
-def _flat(t, what, shape, dtypes=_F32):
-    """Address of a contiguous tensor of this shape."""
-    if t.dtype not in dtypes or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        _refuse(t, what, shape, dtypes)
+def _flat(t, what, shape, dev, dtypes=_F32):
+    """Address of a contiguous tensor of this shape on device dev."""
+    if t.dtype not in dtypes or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, what, shape, dtypes, dev)
     return t.data_ptr()
 
 
@@ -424,27 +437,31 @@ def _two(t, what):
     return t.shape
 
 
-def _ws(workspace):
-    return _dptr(workspace), workspace.numel() * workspace.element_size()
+def _ws(workspace, dev):
+    """(address, bytes) of a workspace on device dev."""
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(workspace, "workspace", workspace.shape, (workspace.dtype,), dev)
+    return workspace.data_ptr(), workspace.nbytes
 
 
-def _stream_of(t, stream):
-    """The given stream, or the current one of the tensor's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
+def _stream_of(dev, stream):
+    """The given stream, or the current one of the device."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def qs_rmsnorm_residual(x, residual, weight, eps, sum_out=None, y=None, q=None, q_scale=None, stream=None):
     """Per row: s = x + residual (residual may be None), v = s * weight / sqrt(mean(s^2) + eps); sum_out gets s,
     y gets v, q and q_scale get v as e4m3 codes with a scale per 128 columns (each may be None)."""
     shape = _two(x, "x")
-    xp, xs, xt = _matrix(x, "x", shape)
-    rp, rs, rt = (0, 0, 0) if residual is None else _matrix(residual, "residual", shape)
-    sp, ss, st = (0, 0, 0) if sum_out is None else _matrix(sum_out, "sum_out", shape)
-    yp, ys, yt = (0, 0, 0) if y is None else _matrix(y, "y", shape)
-    qp, qs, qsp, qss = (0, 0, 0, 0) if q is None and q_scale is None else _codes(q, q_scale, "q", shape)
+    dev = _device(x, "x")
+    xp, xs, xt = _matrix(x, "x", shape, dev)
+    rp, rs, rt = (0, 0, 0) if residual is None else _matrix(residual, "residual", shape, dev)
+    sp, ss, st = (0, 0, 0) if sum_out is None else _matrix(sum_out, "sum_out", shape, dev)
+    yp, ys, yt = (0, 0, 0) if y is None else _matrix(y, "y", shape, dev)
+    qp, qs, qsp, qss = (0, 0, 0, 0) if q is None and q_scale is None else _codes(q, q_scale, "q", shape, dev)
     rc = (_lib or load()).qs_rmsnorm_residual(
-        _pack_norm(xp, xs, xt, rp, rs, rt, sp, ss, st, yp, ys, yt, qp, qs, qsp, qss, _flat(weight, "weight", shape[1:]), eps,
-                   shape[0], shape[1]), _stream_of(x, stream))
+        _pack_norm(xp, xs, xt, rp, rs, rt, sp, ss, st, yp, ys, yt, qp, qs, qsp, qss, _flat(weight, "weight", shape[1:], dev), eps,
+                   shape[0], shape[1]), _stream_of(dev, stream))
     if rc:
         raise QsError(rc, "qs_rmsnorm_residual")
 
@@ -460,11 +477,12 @@ def qs_rmsnorm_residual_backward(sum, weight, eps, dy, dsum, dx, dweight=None, w
     shape = _two(sum, "sum")
     if dweight is not None and workspace is None:
         raise ValueError("dweight needs a workspace")
+    dev = _device(sum, "sum")
     rc = (_lib or load()).qs_rmsnorm_residual_backward(
-        _pack_norm_bwd(*_matrix(sum, "sum", shape), *_matrix(dy, "dy", shape),
-                       *((0, 0, 0) if dsum is None else _matrix(dsum, "dsum", shape)), *_matrix(dx, "dx", shape),
-                       _flat(weight, "weight", shape[1:]), 0 if dweight is None else _flat(dweight, "dweight", shape[1:]),
-                       *((0, 0) if workspace is None else _ws(workspace)), eps, *shape), _stream_of(sum, stream))
+        _pack_norm_bwd(*_matrix(sum, "sum", shape, dev), *_matrix(dy, "dy", shape, dev),
+                       *((0, 0, 0) if dsum is None else _matrix(dsum, "dsum", shape, dev)), *_matrix(dx, "dx", shape, dev),
+                       _flat(weight, "weight", shape[1:], dev), 0 if dweight is None else _flat(dweight, "dweight", shape[1:], dev),
+                       *((0, 0) if workspace is None else _ws(workspace, dev)), eps, *shape), _stream_of(dev, stream))
     _check(rc, "qs_rmsnorm_residual_backward")
 
 
@@ -473,11 +491,12 @@ def qs_silu_mul_quant(gate_up, q, q_scale, n_rows=None, stream=None):
     on the device, or None): rows at and beyond its value are left alone."""
     shape = _two(q, "q")
     rows, ffn = shape
-    gp, gs, gt = _matrix(gate_up, "gate_up", (rows, 2 * ffn))
-    qp, qs, qsp, qss = _codes(q, q_scale, "q", shape)
+    dev = _device(q, "q")
+    gp, gs, gt = _matrix(gate_up, "gate_up", (rows, 2 * ffn), dev)
+    qp, qs, qsp, qss = _codes(q, q_scale, "q", shape, dev)
     rc = (_lib or load()).qs_silu_mul_quant(
-        _pack_silu(gp, gs, gt, qp, qs, qsp, qss, 0 if n_rows is None else _flat(n_rows, "n_rows", n_rows.shape, _I32), rows, ffn),
-        _stream_of(q, stream))
+        _pack_silu(gp, gs, gt, qp, qs, qsp, qss, 0 if n_rows is None else _flat(n_rows, "n_rows", n_rows.shape, dev, _I32), rows, ffn),
+        _stream_of(dev, stream))
     if rc:
         raise QsError(rc, "qs_silu_mul_quant")
 
@@ -493,26 +512,27 @@ def qs_fp8_matmul(a, a_scale, w, w_scale, out, workspace, offsets=None, stream=N
     row and 128 columns of a and per 128 x 128 block of w."""
     shape = _two(a, "a")
     rows, inner = shape
+    if offsets is not None and w.dim() != 3:
+        raise ValueError(f"w: expected [experts, cols, inner], got {w.dim()} dimensions")
+    dev = _device(a, "a")
     if offsets is None:
         experts, cols, off, expert_stride = 1, _two(w, "w")[0], 0, 0
-        wp, w_stride, _ = _matrix(w, "w", (cols, inner), _E4M3)
+        wp, w_stride, _ = _matrix(w, "w", (cols, inner), dev, _E4M3)
         blocks = ((cols + 127) // 128, (inner + 127) // 128)
     else:
-        if w.dim() != 3:
-            raise ValueError(f"w: expected [experts, cols, inner], got {w.dim()} dimensions")
         experts, cols, k = w.shape
-        if w.dtype not in _E4M3 or k != inner or not w.is_cuda or (w.stride(2) != 1 and inner > 1):
-            _refuse(w, "w", (experts, cols, inner), _E4M3)
+        if w.dtype not in _E4M3 or k != inner or w.get_device() != dev or (w.stride(2) != 1 and inner > 1):
+            _refuse(w, "w", (experts, cols, inner), _E4M3, dev)
         wp = w.data_ptr()
         expert_stride, w_stride, _ = w.stride()
         blocks = (experts, (cols + 127) // 128, (inner + 127) // 128)
-        off = _flat(offsets, "offsets", (experts + 1,), _I32)
-    ap, as_, sp, ss = _codes(a, a_scale, "a", shape)
-    op, os_, ot = _matrix(out, "out", (rows, cols))
-    ws, ws_bytes = _ws(workspace)
+        off = _flat(offsets, "offsets", (experts + 1,), dev, _I32)
+    ap, as_, sp, ss = _codes(a, a_scale, "a", shape, dev)
+    op, os_, ot = _matrix(out, "out", (rows, cols), dev)
+    ws, ws_bytes = _ws(workspace, dev)
     rc = (_lib or load()).qs_fp8_matmul(
-        _pack_matmul(ap, as_, sp, ss, wp, w_stride, expert_stride, _flat(w_scale, "w scale", blocks), off, op, os_, ot, ws, ws_bytes,
-                     experts, rows, cols, inner), _stream_of(a, stream))
+        _pack_matmul(ap, as_, sp, ss, wp, w_stride, expert_stride, _flat(w_scale, "w scale", blocks, dev), off, op, os_, ot, ws, ws_bytes,
+                     experts, rows, cols, inner), _stream_of(dev, stream))
     if rc:
         raise QsError(rc, "qs_fp8_matmul")
 
@@ -532,20 +552,21 @@ def qs_dispatch_tokens(topk_ids, x, x_scale, counts, offsets, perm, pos, xs, xs_
     xp = xs_ = xt = yp = ys = sp = ss = tp = ts = 0
     if (x is None) != (xs is None):
         raise ValueError("x and xs come together")
+    dev = _device(topk_ids, "topk_ids")
     if x is not None:
         hidden = _two(x, "x")[1]
         if x.dtype is torch.float8_e4m3fn:
-            xp, xs_, sp, ss = _codes(x, x_scale, "x", (tokens, hidden))
-            yp, ys, tp, ts = _codes(xs, xs_scale, "xs", (n, hidden))
+            xp, xs_, sp, ss = _codes(x, x_scale, "x", (tokens, hidden), dev)
+            yp, ys, tp, ts = _codes(xs, xs_scale, "xs", (n, hidden), dev)
             xt = QS_E4M3
         else:
-            xp, xs_, xt = _matrix(x, "x", (tokens, hidden))
-            yp, ys, _ = _matrix(xs, "xs", (n, hidden), {x.dtype: xt})
-    ws, ws_bytes = _ws(workspace)
+            xp, xs_, xt = _matrix(x, "x", (tokens, hidden), dev)
+            yp, ys, _ = _matrix(xs, "xs", (n, hidden), dev, {x.dtype: xt})
+    ws, ws_bytes = _ws(workspace, dev)
     rc = (_lib or load()).qs_dispatch_tokens(
-        _pack_dispatch(_flat(topk_ids, "topk_ids", shape, _I32), _flat(counts, "counts", (experts,), _I32),
-                       _flat(offsets, "offsets", (experts + 1,), _I32), _flat(perm, "perm", (n,), _I32), _flat(pos, "pos", shape, _I32),
-                       xp, xs_, xt, yp, ys, xt, sp, ss, tp, ts, ws, ws_bytes, tokens, k, experts, hidden), _stream_of(topk_ids, stream))
+        _pack_dispatch(_flat(topk_ids, "topk_ids", shape, dev, _I32), _flat(counts, "counts", (experts,), dev, _I32),
+                       _flat(offsets, "offsets", (experts + 1,), dev, _I32), _flat(perm, "perm", (n,), dev, _I32), _flat(pos, "pos", shape, dev, _I32),
+                       xp, xs_, xt, yp, ys, xt, sp, ss, tp, ts, ws, ws_bytes, tokens, k, experts, hidden), _stream_of(dev, stream))
     if rc:
         raise QsError(rc, "qs_dispatch_tokens")
 
@@ -555,11 +576,12 @@ def qs_combine_tokens(y, pos, topk_w, out, stream=None):
     shape = _two(pos, "pos")
     tokens, k = shape
     hidden = _two(out, "out")[1]
-    yp, ys, yt = _matrix(y, "y", (tokens * k, hidden))
-    op, os_, ot = _matrix(out, "out", (tokens, hidden))
+    dev = _device(pos, "pos")
+    yp, ys, yt = _matrix(y, "y", (tokens * k, hidden), dev)
+    op, os_, ot = _matrix(out, "out", (tokens, hidden), dev)
     rc = (_lib or load()).qs_combine_tokens(
-        _pack_combine(yp, ys, yt, op, os_, ot, _flat(pos, "pos", shape, _I32), 0 if topk_w is None else _flat(topk_w, "topk_w", shape),
-                      tokens, k, hidden), _stream_of(out, stream))
+        _pack_combine(yp, ys, yt, op, os_, ot, _flat(pos, "pos", shape, dev, _I32), 0 if topk_w is None else _flat(topk_w, "topk_w", shape, dev),
+                      tokens, k, hidden), _stream_of(dev, stream))
     if rc:
         raise QsError(rc, "qs_combine_tokens")
 
@@ -572,11 +594,12 @@ def qs_combine_tokens_backward(dout, y, pos, topk_w, dy, dtopk_w=None, stream=No
     hidden = _two(dout, "dout")[1]
     if dtopk_w is not None and y is None:
         raise ValueError("dtopk_w needs y")
+    dev = _device(pos, "pos")
     rc = (_lib or load()).qs_combine_tokens_backward(
-        _pack_combine_bwd(*_matrix(dout, "dout", (tokens, hidden)), *((0, 0, 0) if y is None else _matrix(y, "y", (tokens * k, hidden))),
-                          *_matrix(dy, "dy", (tokens * k, hidden)), _flat(pos, "pos", shape, _I32),
-                          0 if topk_w is None else _flat(topk_w, "topk_w", shape),
-                          0 if dtopk_w is None else _flat(dtopk_w, "dtopk_w", shape), tokens, k, hidden), _stream_of(dout, stream))
+        _pack_combine_bwd(*_matrix(dout, "dout", (tokens, hidden), dev), *((0, 0, 0) if y is None else _matrix(y, "y", (tokens * k, hidden), dev)),
+                          *_matrix(dy, "dy", (tokens * k, hidden), dev), _flat(pos, "pos", shape, dev, _I32),
+                          0 if topk_w is None else _flat(topk_w, "topk_w", shape, dev),
+                          0 if dtopk_w is None else _flat(dtopk_w, "dtopk_w", shape, dev), tokens, k, hidden), _stream_of(dev, stream))
     _check(rc, "qs_combine_tokens_backward")
 
 

@@ -159,3 +159,89 @@ def test_a_dispatch_workspace_is_enough_for_every_smaller_call(top_k, experts):
     assert all(size(t, k, e) <= size(t, top_k, experts) for t in tokens[::50] for k, e in ((1, experts), (top_k, 1)))
     # a chunk of at least 1024 entries has its histogram
     assert all(s >= 4 * experts * min(256, t * top_k // 1024) for s, t in zip(sizes, tokens) if t * top_k > 4096)
+
+
+class OnDevice:
+    """What the binding reads of a CUDA tensor, for a device that need not be there."""
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self.device, self.is_cuda = torch.Size(shape), dtype, f"cuda:{device}", True
+        self._device = device
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, d=None):
+        strides = [1]
+        for n in self.shape[:0:-1]:
+            strides.insert(0, strides[0] * n)
+        return tuple(strides) if d is None else strides[d]
+
+    def numel(self):
+        return self.shape.numel()
+
+    @property
+    def nbytes(self):
+        return self.numel() * self.dtype.itemsize
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+    def get_device(self):
+        return self._device
+
+
+F8, I32, BF, FP = torch.float8_e4m3fn, torch.int32, torch.bfloat16, torch.float32
+OPERANDS = {  # entry point: its tensors by argument, the first operand first
+    "qs_rmsnorm_residual": dict(x=((4, 256), BF), residual=((4, 256), BF), weight=((256,), FP), sum_out=((4, 256), BF),
+                                y=((4, 256), BF), q=((4, 256), F8), q_scale=((4, 2), FP)),
+    "qs_rmsnorm_residual_backward": dict(sum=((4, 256), FP), weight=((256,), FP), dy=((4, 256), FP), dsum=((4, 256), FP),
+                                         dx=((4, 256), FP), dweight=((256,), FP), workspace=((1 << 22,), torch.uint8)),
+    "qs_silu_mul_quant": dict(q=((4, 256), F8), gate_up=((4, 512), BF), q_scale=((4, 2), FP), n_rows=((1,), I32)),
+    "qs_fp8_matmul": dict(a=((8, 256), F8), a_scale=((8, 2), FP), w=((3, 64, 256), F8), w_scale=((3, 1, 2), FP), out=((8, 64), FP),
+                          workspace=((4096,), torch.uint8), offsets=((4,), I32)),
+    "qs_dispatch_tokens": dict(topk_ids=((8, 2), I32), x=((8, 256), F8), x_scale=((8, 2), FP), counts=((16,), I32), offsets=((17,), I32),
+                               perm=((16,), I32), pos=((8, 2), I32), xs=((16, 256), F8), xs_scale=((16, 2), FP), workspace=((4096,), torch.uint8)),
+    "qs_combine_tokens": dict(pos=((8, 2), I32), y=((16, 256), BF), topk_w=((8, 2), FP), out=((8, 256), FP)),
+    "qs_combine_tokens_backward": dict(pos=((8, 2), I32), dout=((8, 256), BF), y=((16, 256), BF), topk_w=((8, 2), FP), dy=((16, 256), BF),
+                                       dtopk_w=((8, 2), FP)),
+}
+
+
+@pytest.fixture
+def no_launch(monkeypatch):
+    """Device 0 is current, and an entry point that is reached after all says so instead of running."""
+    monkeypatch.setattr(qm, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0)
+
+    class Library:
+        def __getattr__(self, name):
+            def entry(*args):
+                raise RuntimeError(f"{name} reached")
+            return entry
+
+    monkeypatch.setattr(qm, "_lib", Library())
+
+
+def on_devices(name, device, other=None):
+    """The entry point's call with its operands on `device`, those in `other` on theirs."""
+    at = other or {}
+    operands = {k: OnDevice(shape, dtype, at.get(k, device)) for k, (shape, dtype) in OPERANDS[name].items()}
+    return lambda: getattr(qm, name)(**operands, **({"eps": 1e-6} if "norm" in name else {}))
+
+
+@pytest.mark.parametrize("name,operand", [(n, k) for n in OPERANDS for k in OPERANDS[n]])
+def test_operands_of_two_devices_are_refused(no_launch, name, operand):
+    with pytest.raises(ValueError, match="cuda:1"):
+        on_devices(name, 0, {operand: 1})()
+
+
+@pytest.mark.parametrize("name", list(OPERANDS))
+def test_operands_on_a_device_that_is_not_current_are_refused(no_launch, name):
+    with pytest.raises(ValueError, match="on cuda:1, but cuda:0 is the current device"):
+        on_devices(name, 1)()
+    with pytest.raises(RuntimeError, match=f"{name} reached"):  # those on the current one are not
+        on_devices(name, 0)()
