@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "qs_fp8tiles.h"
 #include "qs_internal.h"
 #include "qs_rows.cuh"
 #include "qs_tc.cuh"
@@ -38,10 +39,7 @@ namespace {
 
 constexpr int kMaxStages = 32;
 constexpr int kFirstSum = 4;  // first of the warps that sum
-constexpr int kTileRows = 128;
 constexpr int kRowBox = 16;  // rows of the small TMA box of a are a multiple of this
-constexpr int kFewRows = 64; // most rows that are copied by small boxes
-constexpr int kFewTile = 16, kFewAverage = 4;  // rows of a tile of groups of few, and of their average group at most
 
 struct MmParams {
     // a as [block of K][row][128 columns] and w as [expert][block][row][128 columns], boxes of a group's blocks;
@@ -881,6 +879,7 @@ bool encode8(CUtensorMap* m, bool w, const void* base, int K, int64_t rows, int6
 struct MmFacts {
     int n_sm = 0;
     int smem = 0;  // dynamic shared memory a CTA may have beside the static part
+    bool wide = false;  // whether the tiles of 256 weight rows may run
 };
 
 cudaError_t mm_facts(MmFacts** out) {
@@ -904,11 +903,13 @@ cudaError_t mm_facts(MmFacts** out) {
                               (const void*)fp8_mm_kernel<128, false, kFewTile>};
         for (const void* fn : fns)
             if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess) return e;
-        // the register split would wait forever on a launch with fewer
+        // The register split would wait forever on a launch with fewer registers: where a compiler gives those kernels
+        // another number, the other tiles do their work.
+        f.wide = true;
         for (const void* fn : {fns[4], fns[5]}) {
             cudaFuncAttributes wide;
             if ((e = cudaFuncGetAttributes(&wide, fn)) != cudaSuccess) return e;
-            if (wide.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+            f.wide &= wide.numRegs == kLaunchRegs;
         }
         f.n_sm = n_sm;
     }
@@ -986,62 +987,17 @@ cudaError_t launch_fp8_matmul(const Fp8MmArgs& g, void* workspace, cudaStream_t 
                 out_bytes < (1ll << 40);
     const uint64_t dout[2] = {(uint64_t)g.n_cols, (uint64_t)g.n_rows};
     if (p.out_tma && !encode_out(&p.tout, g.out, g.out_dtype, dout, (uint64_t)out_bytes)) return cudaErrorInvalidValue;
-    // Pairs of CTAs where tiles of 256 x 256 fill them: more than half of a tile's rows are there on
-    // average, and there is a tile for each pair.
-    const int64_t per = g.offsets ? g.n_rows / g.n_experts : g.n_rows;
-    const int64_t pair_tiles = (g.offsets ? (int64_t)g.n_rows / 256 + g.n_experts : ((int64_t)g.n_rows + 255) / 256) *
-                               ((g.n_cols + 255) / 256);
-    if (per > kTileRows && pair_tiles >= f->n_sm / 2) return mm_run<256, true>(g, p, *f, pair_tiles, st);
-    // Groups of few rows: weight rows down the accumulator, the group's across, 16 a tile.  Against the tiles below, 8 of
-    // 256 experts: one token at 2048 x 1024 (columns x inner) 4.6 us against 6.3, eight 21.3 against 24.8, 128 80.1
-    // against 84.7; sixty-four rows to two experts, 2048 x 2048, 5.3 against 5.6.  At eight rows an expert and more what is
-    // gained where they spread evenly (82.5 against 86.8) is lost where they do not (31.5 against 24.4 if popularity
-    // falls with rank^-1.5), since each 16 rows take an expert's weights again.  Tiles of 32 and 64 rows were slower (eight
-    // tokens at 1024 x 2048 22.5 and 24.3 against 22.2).  64 weight rows a tile where those leave half of the SMs free
-    // (one token at 512 x 2048 4.5 against 5.0 with 128; with more tiles they lose as often, 5.1 against 4.8 for two
-    // tokens through 4 experts at 1024 x 2048).
-    const int64_t few64 = ((int64_t)g.n_cols + 63) / 64, few128 = ((int64_t)g.n_cols + 127) / 128;
-    if (g.offsets && g.n_rows <= std::max(kFewRows, kFewAverage * g.n_experts)) {
-        const int64_t mt = (int64_t)g.n_rows / kFewTile + std::min(g.n_rows, g.n_experts);
-        if (2 * mt * few64 <= f->n_sm) return mm_run<64, false, kFewTile>(g, p, *f, mt * few64, st);
-        return mm_run<128, false, kFewTile>(g, p, *f, mt * few128, st);
-    }
-    // One matrix: the tiles of 64 weight rows if all have an SM, since one fills its SM with the K of 64 weight rows
-    // faster than the tiles below with theirs: 1 x 4096 x 2048 4.2 us against 4.8, 16 x 9728 x 2048 4.5 against 5.5,
-    // 100 x 1024 x 4096 5.5 against 7.0, 1 x 4096 x 16384 16.8 against 19.7; at K of 1024 and less the same or better.
-    // Then the same with 32 rows: 64 x 4864 x 4096 6.4 against 7.9, 200 x 1024 x 2048 4.8 against 5.2, 512 x 512 x 1024
-    // 4.0 against 4.1 (with 64 rows 4.5: slower than what follows in 60 of 80 such shapes).
-    // Else those of 128 for 16 rows: 1 x 10000 x 2048 5.0 against 7.8, 1 x 32768 x 4096 22.9 against 25.0; 32 rows would
-    // take the weights twice (29.3 against 25.4).
-    if (!g.offsets) {
-        const int64_t mt = ((int64_t)g.n_rows + kFewTile - 1) / kFewTile;
-        if (mt * few64 <= f->n_sm) return mm_run<64, false, kFewTile>(g, p, *f, mt * few64, st);
-        const int64_t mt32 = (mt + 1) / 2;
-        if (mt32 * few64 <= f->n_sm) return mm_run<64, false, 2 * kFewTile>(g, p, *f, mt32 * few64, st);
-        if (mt == 1) return mm_run<128, false, kFewTile>(g, p, *f, few128, st);
-    }
-    // row tiles: those of one matrix, or for groups the most there can be if rows spread over the
-    // experts (each group's last tile may be short)
-    const int64_t mt = g.offsets ? (int64_t)g.n_rows / kTileRows + std::min(g.n_rows, g.n_experts)
-                                 : (g.n_rows + kTileRows - 1) / kTileRows;
-    // the width whose waves of tiles take least, a tile taking its columns and a fixed part
-    int best = 256;
-    int64_t best_cost = INT64_MAX;
-    for (int bn = 256; bn >= 16; bn /= 2) {
-        const int64_t tiles = mt * ((g.n_cols + bn - 1) / bn);
-        const int64_t cost = (tiles + f->n_sm - 1) / f->n_sm * (bn + 32);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = bn;
-        }
-    }
-    const int64_t tiles = mt * ((g.n_cols + best - 1) / best);
-    switch (best) {
-        case 256: return mm_run<256, false>(g, p, *f, tiles, st);
-        case 128: return mm_run<128, false>(g, p, *f, tiles, st);
-        case 64: return mm_run<64, false>(g, p, *f, tiles, st);
-        case 32: return mm_run<32, false>(g, p, *f, tiles, st);
-        default: return mm_run<16, false>(g, p, *f, tiles, st);
+    const MmTiles t = pick_tiles(g.n_rows, g.n_cols, g.n_experts, g.offsets != nullptr, f->n_sm, f->wide);
+    if (t.pair) return mm_run<256, true>(g, p, *f, t.count, st);
+    if (t.few == kFewTile)
+        return t.cols == 64 ? mm_run<64, false, kFewTile>(g, p, *f, t.count, st) : mm_run<128, false, kFewTile>(g, p, *f, t.count, st);
+    if (t.few) return mm_run<64, false, 2 * kFewTile>(g, p, *f, t.count, st);
+    switch (t.cols) {
+        case 256: return mm_run<256, false>(g, p, *f, t.count, st);
+        case 128: return mm_run<128, false>(g, p, *f, t.count, st);
+        case 64: return mm_run<64, false>(g, p, *f, t.count, st);
+        case 32: return mm_run<32, false>(g, p, *f, t.count, st);
+        default: return mm_run<16, false>(g, p, *f, t.count, st);
     }
 }
 
