@@ -488,12 +488,14 @@ def qs_rmsnorm_residual_backward(sum, weight, eps, dy, dsum, dx, dweight=None, w
 
 def qs_silu_mul_quant(gate_up, q, q_scale, n_rows=None, stream=None):
     """q, q_scale [rows, F]: silu(gate) * up of gate_up [rows, 2F] as e4m3 codes with scales; n_rows (an int32 tensor
-    on the device, or None): rows at and beyond its value are left alone."""
+    on the device, or None): rows at and beyond its first element are left alone."""
     shape = _two(q, "q")
     rows, ffn = shape
     dev = _device(q, "q")
     gp, gs, gt = _matrix(gate_up, "gate_up", (rows, 2 * ffn), dev)
     qp, qs, qsp, qss = _codes(q, q_scale, "q", shape, dev)
+    if n_rows is not None and n_rows.numel() == 0:  # its address is 0, which means no limit
+        raise ValueError("n_rows: expected an element")
     rc = (_lib or load()).qs_silu_mul_quant(
         _pack_silu(gp, gs, gt, qp, qs, qsp, qss, 0 if n_rows is None else _flat(n_rows, "n_rows", n_rows.shape, dev, _I32), rows, ffn),
         _stream_of(dev, stream))

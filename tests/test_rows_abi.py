@@ -245,3 +245,10 @@ def test_operands_on_a_device_that_is_not_current_are_refused(no_launch, name):
         on_devices(name, 1)()
     with pytest.raises(RuntimeError, match=f"{name} reached"):  # those on the current one are not
         on_devices(name, 0)()
+
+
+def test_a_row_limit_without_an_element_is_refused(no_launch, monkeypatch):
+    """It has no address, and none means no limit: rows past the limit that was meant would be overwritten."""
+    monkeypatch.setitem(OPERANDS["qs_silu_mul_quant"], "n_rows", ((0,), I32))
+    with pytest.raises(ValueError, match="n_rows: expected an element"):
+        on_devices("qs_silu_mul_quant", 0)()
