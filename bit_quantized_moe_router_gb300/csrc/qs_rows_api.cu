@@ -142,7 +142,10 @@ int qs_fp8_matmul(const qs_fp8_matmul_args* args, void* stream) {
         return QS_ERR_INVALID;
     if (!a.w || !a.w_scale || ((uintptr_t)a.w & 15u) || ((uintptr_t)a.w_scale & 3u) || a.w_stride % 16 ||
         a.w_stride < k || a.w_stride >= top || a.w_expert_stride % 16 || a.w_expert_stride >= top ||
-        a.w_expert_stride < (e > 1 ? a.w_stride * (n - 1) + k : 0) || ((uintptr_t)a.offsets & 3u))
+        ((uintptr_t)a.offsets & 3u))
+        return QS_ERR_INVALID;
+    // an expert's rows end before the next expert's begin; divided, since w_stride * (n - 1) may pass 64 bits
+    if (a.w_expert_stride < 0 || (e > 1 && (a.w_expert_stride < k || (a.w_expert_stride - k) / a.w_stride < n - 1)))
         return QS_ERR_INVALID;
     if (!rows_ok(a.out, m, n)) return QS_ERR_INVALID;
     if (!a.workspace || ((uintptr_t)a.workspace & 255u) || a.workspace_bytes < fp8_matmul_workspace(m, n, k, e))

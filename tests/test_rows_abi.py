@@ -252,3 +252,16 @@ def test_a_row_limit_without_an_element_is_refused(no_launch, monkeypatch):
     monkeypatch.setitem(OPERANDS["qs_silu_mul_quant"], "n_rows", ((0,), I32))
     with pytest.raises(ValueError, match="n_rows: expected an element"):
         on_devices("qs_silu_mul_quant", 0)()
+
+
+@pytest.mark.parametrize("stride,cols", [(1 << 39, (1 << 25) + 1), (1 << 39, 1 << 29), (1 << 36, (1 << 28) + 1), ((1 << 40) - 16, 1 << 30)])
+def test_strides_whose_product_passes_64_bits_are_refused(stride, cols):
+    """An expert's rows would reach past the next expert's, by more than 64 bits count."""
+    assert call("qs_fp8_matmul", MM, dict(w_stride=stride, n=cols, we=512, out_stride=cols)) == INV
+
+
+@pytest.mark.parametrize("expert_stride,code", [(256 * 64, INV), (256 * 63 + 272, INV), (256 * 63 + 256, INV), (240, INV), (0, INV), (-16, INV),
+                                                (272 * 63 + 240, INV), (272 * 63 + 256, WS)])
+def test_experts_that_overlap_are_refused(expert_stride, code):
+    """63 strides of 272 bytes and a last row of 256 is the least (without a workspace, so that nothing is launched)."""
+    assert call("qs_fp8_matmul", MM, dict(w_stride=272, we=expert_stride, ws=0)) == code
