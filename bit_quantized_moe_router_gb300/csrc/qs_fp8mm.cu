@@ -233,6 +233,14 @@ struct Groups {
     int first[1025], before[1056], total[33];
 };
 
+// Row tiles of 32 experts that count, at most.  Groups that do not overlap have fewer in all.  Offsets that are not
+// ascending may name a row 512 times; sums of these stay inside 32 bits all the same (one that wrapped numbered tiles outside
+// the rows), and a tile's number leads to rows of the tile's expert.
+constexpr int kSpanTiles = 1 << 25;
+static_assert(kMmMaxRows / kTileRows + kMmMaxExperts <= kSpanTiles, "all tiles of ascending groups count");
+static_assert(kFewAverage * kMmMaxExperts <= kSpanTiles, "and those of few rows");
+static_assert((int64_t)kMmMaxExperts / 32 * kSpanTiles + 32ll * (kMmMaxRows / kTileRows) <= INT32_MAX, "an expert's first tile");
+
 // A warp's view: lane c has the row tiles before the experts 32 c ..; `all` of them.
 struct Lookup {
     int base, all;
@@ -550,7 +558,7 @@ __global__ void __launch_bounds__(MmShape<BN, FEW>::kThreads, 1) fp8_mm_kernel(c
                 groups_of.first[e] = r0;
                 groups_of.before[e] = s - mt;
             }
-            if (lane == 31) groups_of.total[c] = s;
+            if (lane == 31) groups_of.total[c] = min(s, kSpanTiles);
         }
     } else if (threadIdx.x == 0) {
         groups_of.first[0] = groups_of.before[0] = 0;

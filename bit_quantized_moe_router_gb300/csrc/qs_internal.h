@@ -204,6 +204,7 @@ struct Fp8MmArgs {
     int64_t a_stride, a_scale_stride, w_stride, w_expert_stride, out_stride;
     int n_experts, n_rows, n_cols, n_inner, out_dtype;
 };
+constexpr int kMmMaxRows = 1 << 30, kMmMaxExperts = 1024;
 size_t fp8_matmul_workspace(int n_rows, int n_cols, int n_inner, int n_experts);
 cudaError_t launch_fp8_matmul(const Fp8MmArgs& p, void* workspace, cudaStream_t st);
 

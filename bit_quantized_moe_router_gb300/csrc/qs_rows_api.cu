@@ -123,8 +123,8 @@ int qs_silu_mul_quant(const qs_silu_mul_args* args, void* stream) {
 }
 
 static bool matmul_shape_ok(int n_rows, int n_cols, int n_inner, int n_experts) {
-    return n_rows >= 0 && n_rows <= (1 << 30) && n_cols >= 1 && n_inner >= 1 && n_inner <= (1 << 30) && n_cols <= (1 << 30) &&
-           n_experts >= 1 && n_experts <= 1024;
+    return n_rows >= 0 && n_rows <= kMmMaxRows && n_cols >= 1 && n_inner >= 1 && n_inner <= (1 << 30) && n_cols <= (1 << 30) &&
+           n_experts >= 1 && n_experts <= kMmMaxExperts;
 }
 
 size_t qs_fp8_matmul_workspace_bytes(int n_rows, int n_cols, int n_inner, int n_experts) {
