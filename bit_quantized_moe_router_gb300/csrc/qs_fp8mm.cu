@@ -17,9 +17,10 @@
 // rows, 64 or 128 weight rows by 16 or 32 rows with the operands' parts changed about.  A CTA takes tiles blockIdx.x,
 // + gridDim.x, ... and its stages run on from one tile to the next.
 // Bound: weights from HBM where there are few rows a weight (2048 tokens to 8 of 256 experts, 2048 x 1024 each:
-// 93 us, 96 % of the copy rate), latency where a matrix is small (one row by 4096 x 2048: 4.2 us for 1.2 us of
-// weights), and for long prompts the tensor cores and the sums between them: 8192 x 8192 x 4096 takes 180 us, 3.05
-// PFLOP/s; without the reads of accumulators 165, without the copies 169, without both 145.  With 64 rows at most the
+// 93 us, 96 % of the copy rate), latency where a matrix is small (one row by 4096 x 2048: 4.0 us with the weights in L2, 4.9 with them in HBM, for
+// 1.25 us of weights), and for long prompts the tensor cores and the sums between them: 8192 x 8192 x 4096 takes 180 us
+// in a burst of 20 ms, 3.05 PFLOP/s (without the reads of accumulators 165, without the copies 169, without both 145), and
+// 204 to 214 us for longer, at the card's power cap.  With 64 rows at most the
 // stage's row part is only as high as the rows there are (the matrix instruction reads on into whatever follows:
 // rows of the result that no thread stores), so that nearly all of shared memory holds weights in flight.
 #include <cuda.h>

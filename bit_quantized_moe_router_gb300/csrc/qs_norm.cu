@@ -6,13 +6,15 @@
 // of G warps, eight consecutive elements a thread and step, so it is read once; the sum of squares
 // is a fixed-order tree over the group.  Sixteen neighbouring threads hold the 128 columns of a
 // scale, so a block's maximum is four shuffles and nothing is staged in shared memory.  16384 x 4096 in bf16 with
-// the sum and the codes: 85 us, 5.5 TB/s, the same whatever the occupancy; in fp32 without them 78 us, 6.9 TB/s.
+// the sum and the codes: 77 us, 6.1 TB/s; in fp32 without them 78 us, 6.9 TB/s.
 //
 // Gradient.  With g = weight * dy: dx = rho * (g - s * rho * (rho * mean(g * s))) + dsum.  Both sums over a
 // row (s^2 and g * s) are formed in one pass; a group keeps its columns' share of dweight in
 // registers over all its rows, a CTA writes one partial row, and a second launch adds the partial
 // rows in a fixed order (no atomics: the same bits every run).  8192 x 2048 in bf16: 28 us, 4.8 TB/s; three CTAs an SM
-// with two rows each in registers (four with spills 32 us, two 31).
+// with two rows each in registers, 8 bytes a thread of them spilled (four CTAs with more spills 32 us, two 31).  In fp32
+// 52 us, 5.1 TB/s.  Rows of more than 4096 columns in fp32 or 8192 in bf16 hold more than there are registers: 2048 x 8192
+// in fp32 68 us, in bf16 35; 1024 x 16384 149 and 62.
 #include "qs_internal.h"
 #include "qs_rows.cuh"
 
@@ -320,8 +322,8 @@ template <bool VEC, bool B16>
 cudaError_t norm_pick(const NormArgs& p, cudaStream_t st) {
     // Few rows: as many threads a row as have a load, for the least latency (32 x 2048: 2.1 us, with two warps
     // a row 4.0).  Many: a warp a row where its registers hold it, which needs no barrier, else eight.  32768 rows of
-    // 1024: 44 us; compared with the types looked up, 47, with two warps 55, with four 67.  Of 2048: 86; so compared,
-    // 91, with four warps 104, with two 89.  16384 of 4096: 85, with sixteen warps 98, with four 90.
+    // 1024: 43 us; with the types looked up 46, with two warps 53, with four 64.  Of 2048: 85; with the types looked up
+    // 91, with four warps 90, with two 89.  16384 of 4096: 77; with the types looked up 85, with sixteen warps 94, with four 84.
     const bool few = p.n_rows <= 304;  // two a SM
     if (p.hidden <= 256) return norm_run<VEC, B16, 1, 1>(p, st);
     if (p.hidden <= 512) return norm_run<VEC, B16, 1, 2>(p, st);

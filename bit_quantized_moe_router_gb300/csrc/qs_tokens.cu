@@ -41,8 +41,8 @@ template <> struct Word<4> { using T = uint32_t; };
 template <> struct Word<2> { using T = uint16_t; };
 template <> struct Word<1> { using T = uint8_t; };
 
-// Exclusive prefix sum of v over the first E threads' values in rounds of the CTA (all threads call).
-__device__ void scan_counts(const int32_t* cnt, int32_t* off, int E) {  // one warp
+// off[e] = the sum of cnt[0 .. e - 1], off[E] the sum of all.  One warp calls it; the caller's barriers stand before and after.
+__device__ void scan_counts(const int32_t* cnt, int32_t* off, int E) {
     const int lane = threadIdx.x & 31;
     int carry = 0;
     for (int b = 0; b < E; b += 32) {

@@ -358,7 +358,6 @@ def qs_test_wait_timeout(workspace, limit_us, stream=None):
 
 _WIDE = {torch.float32: QS_F32, torch.bfloat16: QS_BF16}
 _E4M3 = {torch.float8_e4m3fn: QS_E4M3}
-_ANY = {**_WIDE, **_E4M3}
 
 # the argument structs of include/qs_moe.h, as they lie in memory
 _ROWS, _CODES = "Pqi4x", "PqPq"

@@ -421,10 +421,11 @@ typedef struct {
 } qs_silu_mul_args;
 
 /* SwiGLU of a gate/up product with an 8-bit output: per row of gate_up
- * [n_rows x 2F] (gate columns first; fp32 or bf16) v = silu(gate) * up in fp32,
- * stored as codes q [n_rows x F].  n_rows_dev (device int32, or
- * NULL): rows at and beyond *n_rows_dev are left alone (the total of
- * qs_dispatch_tokens is offsets[n_experts]).  One launch. */
+ * [n_rows x 2F] (gate columns first; fp32 or bf16) v = silu(gate) * up in fp32
+ * (within 2^-20 of the value; 0 for gates below -87.3), stored as codes
+ * q [n_rows x F].  n_rows_dev (device int32, or NULL): rows at and beyond
+ * *n_rows_dev are left alone (the total of qs_dispatch_tokens is
+ * offsets[n_experts]).  One launch. */
 int qs_silu_mul_quant(const qs_silu_mul_args *args, void *stream);
 
 typedef struct {
@@ -453,7 +454,8 @@ typedef struct {
  *        clipped to 0 .. n_rows.
  * out    fp32 or bf16 [n_rows x N]
  * Sums inside a block of 128 are formed by the tensor cores in fp32, the sum over
- * blocks in fp32 in ascending order.  n_rows, N, K <= 2^30, N, K >= 1, E <= 1024.  workspace: at least
+ * blocks in fp32 in ascending order.  A block's two scales are multiplied first,
+ * in fp32: a product of them below 2^-126 keeps fewer bits.  n_rows, N, K <= 2^30, N, K >= 1, E <= 1024.  workspace: at least
  * qs_fp8_matmul_workspace_bytes(n_rows, N, K, E), 256-byte aligned, initialised
  * with qs_workspace_init (its header records a wait that ran out).  One launch. */
 size_t qs_fp8_matmul_workspace_bytes(int n_rows, int n_cols, int n_inner, int n_experts);

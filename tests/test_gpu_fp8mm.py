@@ -305,3 +305,13 @@ def test_a_row_has_the_same_bits_in_calls_of_any_length(cols, inner):
         out = torch.empty(rows, cols, device="cuda")
         qm.qs_fp8_matmul(a[:rows], sa[:rows], w, sw, out, ws)
         assert torch.equal(out, full[:rows])
+
+
+@pytest.mark.parametrize("counts", [[0] * 5 + [990] + [1] * 24 + [0] * 226, [700, 0, 250] + [0] * 253])
+def test_long_groups_in_tiles_of_few_rows(counts):
+    """Four rows an expert on average, nearly all of them one expert's."""
+    COUNTS["long"] = counts
+    try:
+        test_grouped("long", 200, 384, torch.bfloat16)
+    finally:
+        del COUNTS["long"]
