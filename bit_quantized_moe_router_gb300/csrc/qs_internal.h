@@ -208,4 +208,57 @@ constexpr int kMmMaxRows = 1 << 30, kMmMaxExperts = 1024;
 size_t fp8_matmul_workspace(int n_rows, int n_cols, int n_inner, int n_experts);
 cudaError_t launch_fp8_matmul(const Fp8MmArgs& p, void* workspace, cudaStream_t st);
 
+// The paged key-value cache and its operators (qs_cache.cu, qs_attn.cuh).  Strides of the cache and of rows of heads in
+// bytes, of scales in floats.
+struct FastDiv {
+    uint32_t mul;
+    int shift;
+};
+struct CacheView {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t page_stride, slot_stride, head_stride;
+    int64_t scale_page_stride, scale_slot_stride, scale_head_stride;
+    FastDiv page_div;  // by page_size
+    int dtype, n_pages, page_size, n_kv, head_dim;
+};
+struct SeqsView {
+    const int32_t *table, *starts, *offsets;
+    int64_t table_stride;
+    int n_seqs, positions;  // positions: what a row of the table covers
+};
+struct HeadsView {
+    uint8_t* data;
+    int64_t token_stride, head_stride;
+    int dtype;
+};
+struct CacheRowsArgs {
+    CacheView cache;
+    SeqsView seqs;
+    HeadsView k, v;
+    int n_tokens;
+    bool aligned;      // every row of k and v at 16-byte boundaries
+    int lanes, units;  // set by the launch: lanes of a head row, warps of a token
+};
+cudaError_t launch_cache_write(const CacheRowsArgs& p, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheRowsArgs& p, cudaStream_t st);
+
+struct AttnArgs {
+    CacheView cache;
+    SeqsView seqs;
+    HeadsView q, out;  // out.data null: left out
+    uint8_t* codes;    // null: left out
+    float* codes_scale;
+    float* lse;        // null: left out
+    int64_t codes_stride, codes_scale_stride;
+    float scale;       // of the scores, times log2(e)
+    int n_tokens, n_heads, max_new, window;
+    bool q_aligned, out_aligned;
+    uint32_t* joined;  // workspace: a counter a CTA, and the parts of items that several CTAs share
+    float* parts;
+};
+constexpr int kAttnMaxCtas = 608;  // most CTAs of a call: four an SM
+size_t attn_workspace(int n_heads, int n_kv, int head_dim, int max_new);
+cudaError_t launch_cache_attention(const AttnArgs& p, void* workspace, cudaStream_t st);
+
 }  // namespace qs

@@ -30,6 +30,7 @@ EXPORTS = (
     "qs_rmsnorm_residual", "qs_rmsnorm_backward_workspace_bytes", "qs_rmsnorm_residual_backward", "qs_silu_mul_quant",
     "qs_fp8_matmul_workspace_bytes", "qs_fp8_matmul", "qs_dispatch_workspace_bytes", "qs_dispatch_tokens",
     "qs_combine_tokens", "qs_combine_tokens_backward",
+    "qs_cache_write", "qs_cache_read", "qs_cache_attention_workspace_bytes", "qs_cache_attention",
 )
 
 
@@ -109,17 +110,21 @@ def load(build_if_missing: bool = True):
     L.qs_moe_ffn_host.argtypes = [SP, P, P, P, EP, HP, P, i32, P, sz, P]
     # the row operators take one packed struct each: a call of twenty ctypes arguments costs 1.3 us more than one
     for name in ("qs_rmsnorm_residual", "qs_rmsnorm_residual_backward", "qs_silu_mul_quant", "qs_fp8_matmul",
-                 "qs_dispatch_tokens", "qs_combine_tokens", "qs_combine_tokens_backward"):
+                 "qs_dispatch_tokens", "qs_combine_tokens", "qs_combine_tokens_backward", "qs_cache_write", "qs_cache_read",
+                 "qs_cache_attention"):
         getattr(L, name).argtypes = [ctypes.c_char_p, P]
     L.qs_rmsnorm_backward_workspace_bytes.argtypes = [i32]
     L.qs_fp8_matmul_workspace_bytes.argtypes = [i32, i32, i32, i32]
     L.qs_dispatch_workspace_bytes.argtypes = [i32, i32, i32]
-    for name in ("qs_rmsnorm_backward_workspace_bytes", "qs_fp8_matmul_workspace_bytes", "qs_dispatch_workspace_bytes"):
+    L.qs_cache_attention_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    for name in ("qs_rmsnorm_backward_workspace_bytes", "qs_fp8_matmul_workspace_bytes", "qs_dispatch_workspace_bytes",
+                 "qs_cache_attention_workspace_bytes"):
         getattr(L, name).restype = sz
     for name in EXPORTS:
         if name not in ("qs_status_string", "qs_abi_version", "qs_last_cuda_error", "qs_moe_workspace_bytes",
                         "qs_moe_host_workspace_bytes", "qs_rmsnorm_backward_workspace_bytes",
-                        "qs_fp8_matmul_workspace_bytes", "qs_dispatch_workspace_bytes"):
+                        "qs_fp8_matmul_workspace_bytes", "qs_dispatch_workspace_bytes",
+                        "qs_cache_attention_workspace_bytes"):
             getattr(L, name).restype = i32
     _lib = L
     return L
@@ -361,6 +366,7 @@ _E4M3 = {torch.float8_e4m3fn: QS_E4M3}
 
 # the argument structs of include/qs_moe.h, as they lie in memory
 _ROWS, _CODES = "Pqi4x", "PqPq"
+_CACHE, _SEQS, _HEADS = "PPPPqqqqqqiiiii4x", "PqPPii", "Pqqi4x"
 ARGS = {
     "qs_rmsnorm_residual": struct.Struct("@" + 4 * _ROWS + _CODES + "Pfii4x"),
     "qs_rmsnorm_residual_backward": struct.Struct("@" + 4 * _ROWS + "PPPNfii4x"),
@@ -369,9 +375,15 @@ ARGS = {
     "qs_dispatch_tokens": struct.Struct("@PPPPP" + 2 * _ROWS + "PqPqPNiiii"),
     "qs_combine_tokens": struct.Struct("@" + 2 * _ROWS + "PPiii4x"),
     "qs_combine_tokens_backward": struct.Struct("@" + 3 * _ROWS + "PPPiii4x"),
+    "qs_cache_write": struct.Struct("@" + _CACHE + _SEQS + 2 * _HEADS + "i4x"),
+    "qs_cache_read": struct.Struct("@" + _CACHE + _SEQS + 2 * _HEADS + "i4x"),
+    "qs_cache_attention": struct.Struct("@" + _CACHE + _SEQS + 2 * _HEADS + _CODES + "PPNfiiii4x"),
 }
 _pack_norm, _pack_norm_bwd, _pack_silu, _pack_matmul, _pack_dispatch, _pack_combine, _pack_combine_bwd = (
-    a.pack for a in ARGS.values())
+    a.pack for a in list(ARGS.values())[:7])
+_pack_cache, _pack_seqs = struct.Struct("@" + _CACHE).pack, struct.Struct("@" + _SEQS).pack
+# what follows a call's cache and sequences, which are packed once
+_pack_rows_tail, _pack_attention_tail = struct.Struct("@" + 2 * _HEADS + "i4x").pack, struct.Struct("@" + 2 * _HEADS + _CODES + "PPNfiiii4x").pack
 
 
 _F32 = {torch.float32: QS_F32}
@@ -602,6 +614,153 @@ def qs_combine_tokens_backward(dout, y, pos, topk_w, dy, dtopk_w=None, stream=No
                           0 if topk_w is None else _flat(topk_w, "topk_w", shape, dev),
                           0 if dtopk_w is None else _flat(dtopk_w, "dtopk_w", shape, dev), tokens, k, hidden), _stream_of(dev, stream))
     _check(rc, "qs_combine_tokens_backward")
+
+
+# ------------------------------------------------------------------ the paged key-value cache
+
+class Cache:
+    """Keys and values of a paged cache, as make_cache found them: their layout, packed once for every call, and the
+    tensors themselves, which it keeps alive."""
+    __slots__ = ("tensors", "packed", "device", "n_kv_heads", "head_dim")
+
+
+class Seqs:
+    """The sequences of a call, as make_seqs found them: packed once, and the tensors, which it keeps alive.  Their
+    values are read by the kernels when they run, so a program changes them in place."""
+    __slots__ = ("tensors", "packed", "device", "n_seqs", "has_offsets")
+
+
+def make_cache(k, v, k_scale=None, v_scale=None):
+    """A paged cache of k and v [pages, page size, key-value heads, head size], bf16, or e4m3 with fp32 scales
+    [pages, page size, key-value heads].  Any strides (a view of another order of dimensions, or one half of a tensor that
+    holds both), the same for k and v."""
+    if k.dim() != 4:
+        raise ValueError(f"k: expected [pages, page size, heads, head size], got {k.dim()} dimensions")
+    dev = k.get_device()
+    if dev < 0:
+        raise ValueError(f"k: expected a tensor in device memory, got one on {k.device}")
+    kinds = {torch.bfloat16: QS_BF16, torch.float8_e4m3fn: QS_E4M3}
+    if k.dtype not in kinds:
+        _refuse(k, "k", k.shape, kinds, dev)
+    if v.dtype != k.dtype or v.shape != k.shape or v.get_device() != dev:
+        _refuse(v, "v", k.shape, (k.dtype,), dev)
+    pages, page, heads, d = k.shape
+    scales, scale_strides = (0, 0), (0, 0, 0)
+    for t, what in ((k, "k"), (v, "v")):
+        if t.stride(3) != 1 and d > 1 and t.numel():
+            _refuse(t, what, t.shape, kinds, dev)
+    if k.stride() != v.stride() and k.numel():
+        raise ValueError(f"v: strides {v.stride()}, k has {k.stride()}")
+    if k.dtype is torch.float8_e4m3fn:
+        if k_scale is None or v_scale is None:
+            raise ValueError("e4m3 codes come with scales")
+        for t, what in ((k_scale, "k scale"), (v_scale, "v scale")):
+            if t.dtype != torch.float32 or t.shape != k.shape[:3] or t.get_device() != dev:
+                _refuse(t, what, k.shape[:3], _F32, dev)
+        if k_scale.stride() != v_scale.stride() and k.numel():
+            raise ValueError(f"v scale: strides {v_scale.stride()}, k scale has {k_scale.stride()}")
+        scales, scale_strides = (k_scale.data_ptr(), v_scale.data_ptr()), k_scale.stride()
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("bf16 keys and values have no scales")
+    c = Cache()
+    c.tensors, c.device, c.n_kv_heads, c.head_dim = (k, v, k_scale, v_scale), dev, heads, d
+    c.packed = _pack_cache(k.data_ptr(), v.data_ptr(), *scales, *k.stride()[:3], *scale_strides, kinds[k.dtype], pages, page, heads, d)
+    return c
+
+
+def make_seqs(table, starts=None, offsets=None):
+    """Sequences: their pages, table int32 [sequences, pages], -1 for none; starts int32 [sequences], the position of
+    each one's first new token (None: 0); offsets int32 [sequences + 1], whose rows the tokens of a call are (None: one
+    token each)."""
+    n, pages = _two(table, "table")
+    dev = table.get_device()
+    if dev < 0:
+        raise ValueError(f"table: expected a tensor in device memory, got one on {table.device}")
+    tp, stride, _ = _matrix(table, "table", (n, pages), dev, _I32)
+    s = Seqs()
+    s.tensors, s.device, s.n_seqs, s.has_offsets = (table, starts, offsets), dev, n, offsets is not None
+    s.packed = _pack_seqs(tp, stride, 0 if starts is None else _flat(starts, "starts", (n,), dev, _I32),
+                          0 if offsets is None else _flat(offsets, "offsets", (n + 1,), dev, _I32), n, pages)
+    return s
+
+
+def _heads(t, what, shape, dev):
+    """(address, token stride, head stride, type) of rows of heads of this shape on device dev."""
+    kind = _WIDE.get(t.dtype)
+    if kind is None or t.shape != shape or t.get_device() != dev:
+        _refuse(t, what, shape, _WIDE, dev)
+    token, head, col = t.stride()
+    if col != 1 and shape[2] > 1:
+        _refuse(t, what, shape, _WIDE, dev)
+    return t.data_ptr(), token, head, kind
+
+
+def _cache_device(cache, seqs):
+    """The device of a cache and its sequences, which has to be the current one."""
+    dev = cache.device
+    if seqs.device != dev:
+        raise ValueError(f"sequences: on cuda:{seqs.device}, the cache on cuda:{dev}")
+    if dev != _current_device():
+        raise ValueError(f"cache: on cuda:{dev}, but cuda:{_current_device()} is the current device")
+    return dev
+
+
+def _token_rows(t, what, cache, seqs):
+    """The number of tokens of rows of heads."""
+    if t.dim() != 3:
+        raise ValueError(f"{what}: expected [tokens, heads, head size], got {t.dim()} dimensions")
+    n = t.shape[0]
+    if not seqs.has_offsets and n != seqs.n_seqs:
+        raise ValueError(f"{what}: {n} tokens for {seqs.n_seqs} sequences, and no offsets")
+    return n
+
+
+def qs_cache_write(cache, seqs, k, v, stream=None):
+    """The new tokens' keys and values [tokens, key-value heads, head size] (fp32 or bf16) to their places in the cache,
+    rounded to bf16 or as e4m3 codes with a scale per token and head; tokens without a place are dropped."""
+    n = _token_rows(k, "k", cache, seqs)
+    dev = _cache_device(cache, seqs)
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    rc = (_lib or load()).qs_cache_write(cache.packed + seqs.packed + _pack_rows_tail(*_heads(k, "k", shape, dev), *_heads(v, "v", shape, dev), n),
+                                         _stream_of(dev, stream))
+    if rc:
+        raise QsError(rc, "qs_cache_write")
+
+
+def qs_cache_read(cache, seqs, k, v, stream=None):
+    """k and v [tokens, key-value heads, head size] (fp32 or bf16) get the cached values of the sequences' positions from
+    starts on; zeros where there is no page."""
+    n = _token_rows(k, "k", cache, seqs)
+    dev = _cache_device(cache, seqs)
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    rc = (_lib or load()).qs_cache_read(cache.packed + seqs.packed + _pack_rows_tail(*_heads(k, "k", shape, dev), *_heads(v, "v", shape, dev), n),
+                                        _stream_of(dev, stream))
+    if rc:
+        raise QsError(rc, "qs_cache_read")
+
+
+def alloc_cache_attention_workspace(n_heads, n_kv_heads, head_dim, max_new=1, device="cuda"):
+    """A zero-initialised workspace for qs_cache_attention of up to max_new new tokens a sequence."""
+    return _alloc(load().qs_cache_attention_workspace_bytes(n_heads, n_kv_heads, head_dim, max_new), "qs_cache_attention_workspace_bytes", device)
+
+
+def qs_cache_attention(cache, seqs, q, scale, out, workspace, max_new=1, window=0, lse=None, codes=None, codes_scale=None, stream=None):
+    """out [tokens, heads, head size] (None: left out) = attention of the new tokens' queries q over their sequence's
+    positions in the cache up to their own, the last `window` of them (0: all); a sequence has up to max_new new tokens.
+    lse fp32 [tokens, heads] (None: left out) gets the logarithm of the softmax's sum; codes and codes_scale
+    [tokens, heads * head size] (None: left out) the output as e4m3 codes with a scale per 128 columns."""
+    n = _token_rows(q, "q", cache, seqs)
+    dev = _cache_device(cache, seqs)
+    heads, d = q.shape[1], cache.head_dim
+    shape = (n, heads, d)
+    cp, cs, sp, ss = (0, 0, 0, 0) if codes is None and codes_scale is None else _codes(codes, codes_scale, "codes", (n, heads * d), dev)
+    rc = (_lib or load()).qs_cache_attention(
+        cache.packed + seqs.packed + _pack_attention_tail(
+            *_heads(q, "q", shape, dev), *((0, 0, 0, 0) if out is None else _heads(out, "out", shape, dev)), cp, cs, sp, ss,
+            0 if lse is None else _flat(lse, "lse", (n, heads), dev), *_ws(workspace, dev), scale, n, heads, max_new, window),
+        _stream_of(dev, stream))
+    if rc:
+        raise QsError(rc, "qs_cache_attention")
 
 
 def _alloc(n, what, device):

@@ -519,6 +519,107 @@ typedef struct {
  * not read and may be left out).  One launch. */
 int qs_combine_tokens_backward(const qs_combine_backward_args *args, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The paged key-value cache of a decode step: rows of new keys and values into
+ * it, cached rows back, and the attention of the newest tokens over it.
+ * The conventions above, and these:
+ *  - k and v are two buffers of the same layout: the row of head_dim values of a
+ *    page, a slot in it and a key-value head begins at page * page_stride + slot *
+ *    slot_stride + head * head_stride elements; columns are contiguous.  Any
+ *    order and padding; k, v at 16-byte boundaries and the strides multiples of
+ *    16 bytes.  QS_BF16, or QS_E4M3 with one fp32 scale per page, slot and head
+ *    (k_scale, v_scale with strides of their own in floats): the value is code *
+ *    scale.  Scales are >= 0.  head_dim a multiple of 16 up to 256, n_kv_heads <= 256, any page size
+ *    up to 2^30.
+ *  - Sequence i's page of positions j * page_size .. is table[i * table_stride +
+ *    j], j < n_seq_pages (n_seq_pages * page_size <= 2^30).  An id outside 0 ..
+ *    n_pages - 1 (-1, say) is no page: a position without one is not there.
+ *  - Sequence i's new tokens are rows offsets[i] .. offsets[i + 1] - 1 of the call's
+ *    token rows (device int32 [n_seqs + 1], ascending, offsets of one sequence may be equal; NULL: token i is sequence i's only
+ *    one, n_tokens == n_seqs), at positions starts[i], starts[i] + 1, ... (device
+ *    int32 [n_seqs]; NULL: 0).  n_seqs <= 2^20, n_tokens <= 2^24.  Rows of no sequence, those
+ *    behind the last one among them, are left alone.  Lengths are read on the
+ *    device: a captured graph follows them.
+ *  - Sequences may share pages, but not one that a call writes to: two tokens
+ *    of a call at the same place leave either's values there.
+ */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;                                     /* QS_E4M3 */
+    int64_t page_stride, slot_stride, head_stride;                /* elements */
+    int64_t scale_page_stride, scale_slot_stride, scale_head_stride;
+    int32_t dtype, n_pages, page_size, n_kv_heads, head_dim;
+} qs_cache;
+
+typedef struct {
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *starts, *offsets;
+    int32_t n_seqs, n_seq_pages;
+} qs_seqs;
+
+/* Rows of heads [n_tokens x heads x head_dim], fp32 or bf16, columns contiguous, any strides and alignment of an element. */
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;  /* elements */
+    int32_t dtype;
+} qs_heads;
+
+typedef struct {
+    qs_cache cache;
+    qs_seqs seqs;
+    qs_heads k, v;  /* [n_tokens x n_kv_heads x head_dim] */
+    int32_t n_tokens;
+} qs_cache_rows_args;
+
+/* The new tokens' keys and values to their places.  A QS_BF16 cache gets them
+ * rounded, a QS_E4M3 one codes with one scale per token and head: amax =
+ * max(max |v|, 2^-100) of the row, scale = amax / 448, code = v / scale (NaN and
+ * infinity as in the codes above, the row being the block).  Tokens without a place are dropped.  Nothing else
+ * of the cache is written.  Places of the cache must differ (no stride of 0).  One launch. */
+int qs_cache_write(const qs_cache_rows_args *args, void *stream);
+
+/* The reverse: rows of k and v get the cached values of their tokens' positions,
+ * code * scale rounded to the rows' type; a token whose position is not there
+ * gets zeros.  The cache is not written.  One launch. */
+int qs_cache_read(const qs_cache_rows_args *args, void *stream);
+
+typedef struct {
+    qs_cache cache;
+    qs_seqs seqs;
+    qs_heads q, out;  /* [n_tokens x n_heads x head_dim] */
+    qs_codes codes;   /* [n_tokens x n_heads * head_dim] */
+    float *lse;       /* [n_tokens x n_heads] */
+    void *workspace;
+    size_t workspace_bytes;
+    float scale;
+    int32_t n_tokens, n_heads, max_new, window;
+} qs_cache_attention_args;
+
+/* Attention of the new tokens over the cache, which holds their own keys and
+ * values already (qs_cache_write before it, with the same qs_seqs).  The token at
+ * position p sees the positions 0 .. p that are there, with window > 0 of them
+ * the last `window`.  Per token and head h, with key-value head h / (n_heads / n_kv_heads):
+ *   s_i = scale * (q . k_i),  out = sum_i exp(s_i) v_i / sum_i exp(s_i),
+ *   lse = log(sum_i exp(s_i))
+ * in fp32; out rounded to its type; a token that sees no position (or whose every
+ * score is -infinity) has zeros, and an lse of -infinity.  Positions that a token
+ * does not see do not touch it, whatever they hold.  codes (if there): the same
+ * rows of n_heads * head_dim columns as e4m3 codes with a scale per 128, as
+ * qs_fp8_matmul takes them; head_dim must be a multiple of 128, codes and their
+ * stride at 16 bytes.  lse may be NULL, out may be left out where codes are there.
+ * n_heads a multiple of n_kv_heads, at most 256 times it.  A sequence has up to max_new new tokens (1 .. 256; the first
+ * max_new are attended, rows of the others left alone).  Few new tokens are what it is for: each
+ * key-value head's cache is read once per 64 rows of n_heads / n_kv_heads * max_new.
+ * Sums have a fixed order for given lengths (run-to-run identical); a row's bits
+ * depend on the other sequences' lengths, by which the work is split.
+ * Value scales below 2^-100 keep fewer bits.
+ * workspace: at least qs_cache_attention_workspace_bytes (0 for a bad shape),
+ * 256-byte aligned, initialised with qs_workspace_init and used by this entry
+ * alone.  One launch. */
+size_t qs_cache_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim, int max_new);
+int qs_cache_attention(const qs_cache_attention_args *args, void *stream);
+
 #if defined(__GNUC__)
 #pragma GCC visibility pop
 #endif
