@@ -6,15 +6,17 @@
 // a key the products are 8 to 16 operations a byte.
 //
 // Work.  An item is a sequence, a key-value head and a tile of RT rows (a row: a new token and one of the group's
-// heads).  Its positions are cut into tiles of TP.  All items' tiles in one line are dealt to the CTAs in equal runs,
-// wherever an item begins or ends: lengths are known on the device alone and may be uneven, and the line's share keeps
-// every SM busy to the end.  An item that several CTAs have parts of is joined by the last of them to finish (a counter
-// an item, no waits), in the order of the positions, so the result does not depend on who was last.
+// heads).  Its positions are cut into tiles of TP.  All items' tiles in one line are dealt to the teams of warps in equal
+// runs, wherever an item begins or ends: lengths are known on the device alone and may be uneven, and an even share of the
+// line keeps every SM busy to the end.  An item inside one team's run is written from its registers.  What a CTA's teams
+// have of the same item is added up in shared memory when their runs end; what several CTAs have of one is joined by the
+// last of them to finish (a counter an item, no waits), above kFan of them in two steps, always in the order of the
+// positions, so the result does not depend on who was last.
 //
-// A team of R warps goes through tiles of its own, with a ring of ST tiles in shared memory filled by 16-byte
-// asynchronous copies: pages of any size and order, one lookup a position a tile ahead of its copies; positions that are
-// not there are filled with zeros, never read.  The warps of a team share the tile and have 8 NT rows each; with R = 1
-// no barrier wider than a warp is met inside an item.
+// A team of R warps has a ring of ST tiles in shared memory filled by 16-byte asynchronous copies, which run ahead over the
+// ends of items: pages of any size and order, one lookup a position a tile ahead of its copies; positions that are not
+// there are filled with zeros, never read.  The warps of a team share the tile and have 8 NT rows each; with R = 1 no
+// barrier wider than a warp is met before the run's end.
 //
 // Products.  mma.sync m16n8k16 in the cache's own 16-bit values: bf16, or e4m3 widened to fp16 (exact) in registers.
 // tcgen05 would want 64 or 128 rows where there are 8, and the widened codes written back to shared memory first: here
@@ -42,33 +44,41 @@ namespace qs {
 
 namespace attn {
 
-constexpr int kWarps = 4;         // of a CTA
 constexpr float kSlack = 8.0f;    // a row's maximum may lag behind by this much (log2) before the sums are scaled
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kSmemMax = 227 * 1024;
+constexpr int kFan = 12;          // parts of an item that one CTA joins at a time
+constexpr int kMostTeams = 16;
+constexpr int kStatic = 7 * 1024;  // shared memory for tables
 
-// A kernel's sizes: cache type, columns (head_dim rounded up), 8 rows times NT a warp, R warps a team, and whether queries
-// and weights go into the products with all their parts.
-template <bool E4_, int DP_, int NT_, int R_, bool WIDE_>
+// A kernel's sizes: cache type, columns (head_dim rounded up), 8 rows times NT a warp, teams of R warps with rows of their
+// own times C with columns of their own, W warps a CTA, and whether queries and weights go into the products with all
+// their parts.
+template <bool E4_, int DP_, int NT_, int R_, int C_, int W_, bool WIDE_>
 struct Plan {
     static constexpr bool E4 = E4_, WIDE = WIDE_;
-    static constexpr int DP = DP_, NT = NT_, R = R_;
-    static constexpr int kTeams = kWarps / R, kRows = 8 * NT, RT = R * kRows;
+    static constexpr int DP = DP_, NT = NT_, R = R_, C = C_, kWarps = W_;
     static constexpr int kRowBytes = DP * (E4 ? 1 : 2), kChunks = kRowBytes / 16;
-    static constexpr int TP = kRowBytes >= 256 && (R == 1 || kRowBytes >= 512) ? 16 : 32;
+    static constexpr int kTeam = R * C, kTeams = kWarps / kTeam, kRows = 8 * NT, RT = R * kRows, kCols = DP / C;
+    static constexpr int TP = kRowBytes <= 64 || (R == 4 && kRowBytes <= 256) ? 32 : 16;
     static constexpr int kStage = 2 * TP * kRowBytes + (E4 ? 2 * TP * 4 : 0);  // keys, values, their scales
     static constexpr int QP = WIDE ? (E4 ? 2 : 3) : 1, PP = WIDE ? (E4 ? 2 : 3) : (E4 ? 1 : 2);
     static constexpr int kSteps = DP / 16;            // of the first product
-    static constexpr bool kQShared = WIDE || NT * DP > 256;  // query fragments: in shared memory, else in registers
-    static constexpr int kQBytes = kQShared ? kWarps * QP * kSteps * 32 * 8 * NT : 0;
-    static constexpr int kRed = kTeams * RT * (DP + 4) * 4 + kTeams * RT * 8;  // the teams' results, over the ring
-    static constexpr int kFit = (kSmemMax - 1024 - kQBytes) / (kTeams * kStage);
-    static constexpr int kGoal = 108 * 1024 / (kTeams * kStage);  // two CTAs an SM
-    static constexpr int ST = kGoal >= 3 ? (kGoal > 6 ? 6 : kGoal) : (kFit >= 3 ? 3 : kFit);
+    // The queries' fragments.  NT = 1: two parts share one, the second in the rows 8..15, which are empty.  In registers
+    // where they fit beside the sums and about 80 others, else in shared memory.
+    static constexpr int kQAll = NT == 1 ? (QP + 1) / 2 : QP;        // fragments of a step
+    static constexpr int kQEach = NT == 1 ? 2 * QP : 4 * QP;         // registers of a step
+    static constexpr bool kQInRegs = kQEach * kSteps <= 65536 / (32 * kWarps) - 80 - kCols * NT / 4;
+    static constexpr int kQBytes = kQInRegs ? 0 : kWarps * kQAll * kSteps * 32 * 16;
+    static constexpr int kRed = kTeams * RT * (DP + 4) * 4 + kTeams * RT * 8;  // the teams' results, over all of it
+    static constexpr int kFit = (kSmemMax - kStatic - kQBytes) / (kTeams * kStage);
+    static constexpr int ST = kFit > 6 ? 6 : kFit;
     static constexpr int kRing = kTeams * ST * kStage;
-    static constexpr int kSmem = kQBytes + (kRing > kRed ? kRing : kRed);
-    static_assert(ST >= 2 && kSmem + 1024 <= kSmemMax, "shared memory");
-    static_assert(kWarps % R == 0 && 32 * R % kChunks == 0 && TP * kChunks % (32 * R) == 0, "copies");
+    static constexpr int kSmem = kQBytes + kRing > kRed ? kQBytes + kRing : kRed;
+    static constexpr int kPart = RT * (DP + 2);       // floats of an item's part: sums, maxima and sums of weights
+    static_assert(ST >= 2 && kSmem + kStatic <= kSmemMax, "shared memory");
+    static_assert(kWarps % kTeam == 0 && 32 * kTeam % kChunks == 0 && TP * kChunks % (32 * kTeam) == 0, "copies");
+    static_assert(kTeams <= kMostTeams && kTeams <= 16 && kCols % 64 == 0, "teams");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
@@ -82,28 +92,10 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ float2 lds_f2(uint32_t a) {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ void sts_f2(uint32_t a, float x, float y) {
-    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
-}
-template <int R>
-__device__ __forceinline__ void team_sync(int team) {
-    if (R == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * R) : "memory");
+// Warps that wait for one another: `warps` of them at barrier `id` (1 .. 8).
+__device__ __forceinline__ void sync_warps(int id, int warps) {
+    if (warps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * warps) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -174,6 +166,11 @@ struct Seq {
     int tiles, row_tiles;     // of an item; row tiles of a head
     int64_t work;             // tiles of the whole sequence
 };
+// a / b and a % b, b > 0, a >= 0, in 32 bits where both fit.
+__device__ __forceinline__ int64_t div_of(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
 __device__ __forceinline__ int clip_pos(int64_t p, int n) { return (int)(p < 0 ? 0 : p > n ? n : p); }
 
 template <int TP, int RT>
@@ -226,26 +223,145 @@ __device__ __forceinline__ void finish(const AttnArgs& p, int token, int head, i
     if (p.lse && col == 0) p.lse[(int64_t)token * p.n_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// An item's rows from the registers of the warps that have all their positions.  most: the warps' largest values by row, for
+// the codes of 128 columns that two warps have.
 template <class P>
-__global__ void __launch_bounds__(32 * kWarps, 1) attn_kernel(const AttnArgs p) {
+__device__ __forceinline__ void finish_rows(const AttnArgs& p, const Seq& seq, int kv, int w0, int rows, int group, const float (&top)[P::NT], const float (&sum)[P::NT],
+                                            float (&acc)[P::kCols / 64][4][P::NT][4], float (*most)[8 * P::NT], int team) {
+    constexpr int NT = P::NT, kJ = P::kCols / 64;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, d = p.cache.head_dim;
+    const int col0 = warp % P::C * P::kCols;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+        const float inv = sum[nt] == 0.0f ? 0.0f : 1.0f / sum[nt];
+        const int own = w0 + nt * 8 + g;
+        if (p.lse && t == 0 && col0 == 0 && own < rows)
+            p.lse[(int64_t)(seq.first_token + own / group) * p.n_heads + kv * group + own % group] = sum[nt] == 0.0f ? -INFINITY : (top[nt] + log2f(sum[nt])) * kLn2;
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const float by = __shfl_sync(0xffffffffu, inv, 8 * t + 4 * e);
+#pragma unroll
+            for (int jj = 0; jj < kJ; jj++)
+#pragma unroll
+                for (int q = 0; q < 8; q++) {
+                    float& x = acc[jj][q / 2][nt][q % 2 * 2 + e];
+                    x = by == 0.0f ? 0.0f : x * by;
+                }
+        }
+    }
+    const bool shared_scale = P::kCols < kScaleCols && P::C > 1 && p.codes;
+    if (shared_scale) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                float a = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(acc[0][q / 2][nt][q % 2 * 2 + e]));
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                if (g == 0) most[warp][nt * 8 + 2 * t + e] = a;
+            }
+        sync_warps(1 + team, P::kTeam);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const int row = w0 + nt * 8 + 2 * t + e;
+            const bool real = row < rows;
+            const int64_t token = seq.first_token + row / group;
+            const int head = kv * group + row % group;
+            auto columns = [&](int jj, float (&v)[8]) {
+#pragma unroll
+                for (int q = 0; q < 8; q++) v[q] = acc[jj][q / 2][nt][q % 2 * 2 + e];
+            };
+            if (P::DP >= kScaleCols && p.codes) {  // a scale's columns are in the eight lanes of the same t, eight or twice eight each
+                constexpr int kEach = kJ >= 2 ? 2 : 1;
+#pragma unroll
+                for (int b = 0; b < kJ; b += kEach) {
+                    float a = 0.0f;
+                    if (shared_scale) {
+                        a = fmaxf(most[warp][nt * 8 + 2 * t + e], most[warp ^ 1][nt * 8 + 2 * t + e]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kEach; k++)
+#pragma unroll
+                            for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(acc[(b + k) % kJ][q / 2][nt][q % 2 * 2 + e]));
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                    }
+                    const BlockCode code(a, 1.0f, kMinAmax);
+                    if (!real || col0 + 64 * b >= d) continue;
+                    if (g == 0 && (col0 + 64 * b) % kScaleCols == 0) p.codes_scale[token * p.codes_scale_stride + (head * d + col0 + 64 * b) / kScaleCols] = code.scale;
+#pragma unroll
+                    for (int k = 0; k < kEach; k++) {
+                        float x[8];
+                        columns((b + k) % kJ, x);
+                        *reinterpret_cast<uint2*>(p.codes + token * p.codes_stride + head * d + col0 + 64 * (b + k) + 8 * g) =
+                            make_uint2(code.pair(x[0], x[1]) | (code.pair(x[2], x[3]) << 16), code.pair(x[4], x[5]) | (code.pair(x[6], x[7]) << 16));
+                    }
+                }
+            }
+            if (!real || !p.out.data) continue;
+            uint8_t* to = p.out.data + token * p.out.token_stride + head * p.out.head_stride;
+#pragma unroll
+            for (int jj = 0; jj < kJ; jj++) {
+                const int col = col0 + 64 * jj + 8 * g;
+                if (col >= d) continue;
+                float v[8];
+                columns(jj, v);
+                if (p.out_aligned) {
+                    store8_row<true>(to, p.out.dtype, col, d, v);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; q++) {
+                        if (p.out.dtype == QS_BF16) reinterpret_cast<__nv_bfloat16*>(to)[col + q] = __float2bfloat16_rn(v[q]);
+                        else reinterpret_cast<float*>(to)[col + q] = v[q];
+                    }
+                }
+            }
+        }
+}
+
+// What a team has of an item that is not whole in its run: the item's first tile in the line (-1: nothing), and which.
+struct Piece {
+    int64_t item0;
+    int seq, item;
+};
+// A tile in the ring: positions that are there, the first one, and where it lies in its item and the team's run.
+struct Tile {
+    unsigned there;
+    int pos0, first, last;  // first and last of a stretch: the item's or the run's
+    int seq, item, tile, tiles;
+};
+
+// What a part with maximum ml.x counts beside the maximum m; one of no positions (-infinity, 0) nothing.
+__device__ __forceinline__ float part_factor(float2 ml, float m) { return ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - m); }
+
+template <class P>
+__global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs p) {
     constexpr bool E4 = P::E4;
-    constexpr int DP = P::DP, NT = P::NT, R = P::R, RT = P::RT, TP = P::TP, ST = P::ST, NC = P::kChunks;
-    constexpr int kThreads = 32 * kWarps;
+    constexpr int DP = P::DP, NT = P::NT, RT = P::RT, TP = P::TP, ST = P::ST, NC = P::kChunks, kJ = P::kCols / 64;
+    constexpr int kWarps = P::kWarps, kThreads = 32 * kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t scan[kWarps];
-    __shared__ int64_t found_base;
-    __shared__ int found_seq;
-    __shared__ unsigned there_of[kWarps][ST];
-    __shared__ bool is_last;
+    __shared__ int64_t scan[kWarps], found_base[P::kTeams];
+    __shared__ int found_seq[P::kTeams];
+    __shared__ Tile tile_of[kWarps][ST];
+    __shared__ Piece piece_of[2 * P::kTeams];  // of each team: the stretch that begins inside an item and ends with it; the run's last
+    __shared__ float most_of[kWarps][8 * NT];
+    __shared__ bool last_of[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int team = warp / R, team_tid = tid % (32 * R);
+    const int team = warp / P::kTeam, team_tid = tid % (32 * P::kTeam), row_warp = warp % P::kTeam / P::C, col_warp = warp % P::C;
     const int group = p.n_heads / p.cache.n_kv, d = p.cache.head_dim;
-    uint8_t* ring_at = smem + P::kQBytes;
-    const uint32_t q_smem = smem_u32(smem) + warp * (P::kQBytes / kWarps), ring = smem_u32(ring_at) + team * ST * P::kStage, red = smem_u32(ring_at);
+    uint8_t* const q_shared = smem + warp * (P::kQBytes / kWarps) + lane * 16;
+    uint8_t* const ring = smem + P::kQBytes + team * ST * P::kStage;
+    float* const red = reinterpret_cast<float*>(smem);
+    float2* const red_ml = reinterpret_cast<float2*>(red + P::kTeams * RT * (DP + 4));
     pdl_wait();
     pdl_launch_next();
 
-    // ---- this CTA's run of tiles [a, b), and the sequence that it begins in
+    // ---- the CTA's run of tiles, the team's share of it [cur, end), and the sequence that this begins in
     const int per = (p.seqs.n_seqs + kThreads - 1) / kThreads;
     const int s0 = min(tid * per, p.seqs.n_seqs), s1 = min(s0 + per, p.seqs.n_seqs);
     int64_t mine = 0;
@@ -257,6 +373,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_kernel(const AttnArgs p) 
         if (lane >= o) upto += x;
     }
     if (lane == 31) scan[warp] = upto;
+    if (tid < 2 * P::kTeams) piece_of[tid].item0 = -1;
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
@@ -266,245 +383,323 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_kernel(const AttnArgs p) 
     }
     // as many CTAs as have a tile for each team
     const int64_t workers = min((int64_t)gridDim.x, (total + P::kTeams - 1) / P::kTeams);
-    const int64_t c = blockIdx.x;
+    const int c = blockIdx.x;
     if (c >= workers) return;
-    auto begin_of = [&](int64_t x) { return x * total / workers; };
-    auto cta_of = [&](int64_t tile) { return ((tile + 1) * workers - 1) / total; };  // the CTA whose run has it
-    int64_t cur = begin_of(c);
-    const int64_t end = begin_of(c + 1);
-    if (cur >= upto - mine && cur < upto) {
-        int64_t base = upto - mine;
-        int s = s0;
-        for (; s + 1 < s1; s++) {
-            const int64_t w = seq_of<TP, RT>(p, s, group).work;
-            if (cur < base + w) break;
-            base += w;
+    // equal runs, the first of them a tile longer
+    const int64_t each = div_of(total, workers), longer = total - each * workers;
+    const int64_t run0 = c * each + min((int64_t)c, longer), run1 = run0 + each + (c < longer);
+    auto cta_of = [&](int64_t tile) {  // the CTA whose run has it
+        const int64_t split = longer * (each + 1);
+        return (int)(tile < split ? div_of(tile, each + 1) : longer + div_of(tile - split, each));
+    };
+    auto begin_of = [&](int x) { return run0 + (run1 - run0) * x / P::kTeams; };
+    for (int w = 0; w < P::kTeams; w++) {
+        const int64_t from = begin_of(w);
+        if (from >= upto - mine && from < upto) {
+            int64_t base = upto - mine;
+            int s = s0;
+            for (; s + 1 < s1; s++) {
+                const int64_t x = seq_of<TP, RT>(p, s, group).work;
+                if (from < base + x) break;
+                base += x;
+            }
+            found_base[w] = base;
+            found_seq[w] = s;
         }
-        found_base = base;
-        found_seq = s;
     }
     __syncthreads();
-    int64_t base = found_base;
-    int s = found_seq;
-    Seq seq = seq_of<TP, RT>(p, s, group);
+    const int64_t cur = begin_of(team);
+    const int run = (int)(begin_of(team + 1) - cur);
 
-    while (cur < end) {
-        while (cur >= base + seq.work && s + 1 < p.seqs.n_seqs) {
-            base += seq.work;
-            seq = seq_of<TP, RT>(p, ++s, group);
-        }
-        const int item = (int)((cur - base) / seq.tiles), tile0 = (int)((cur - base) % seq.tiles);
-        const int tile1 = (int)min((int64_t)seq.tiles, tile0 + (end - cur));
-        const int kv = item / seq.row_tiles, row0 = item % seq.row_tiles * RT, rows = seq.tokens * group;
-        const int64_t item0 = cur - tile0;  // the item's first tile in the line
-        cur += tile1 - tile0;
-
-        // positions that the row tile sees, and that all this warp's rows see
-        auto hi_of = [&](int token) { return clip_pos(seq.start + token + 1, p.seqs.positions); };
-        auto lo_of = [&](int token) { return p.window ? clip_pos(seq.start + token + 1 - p.window, p.seqs.positions) : 0; };
-        const int tile_lo = lo_of(row0 / group), tile_hi = hi_of((min(row0 + RT, rows) - 1) / group);
-        const int w0 = row0 + (warp % R) * P::kRows, w1 = min(w0 + P::kRows, rows);
-        const bool active = w0 < rows;
-        const int token0 = w0 / group, token1 = max(w1 - 1, w0) / group;
-        const int all_lo = lo_of(token1), all_hi = hi_of(token0);
-
-        // ---- copies
-        const int n = max(0, (tile1 - tile0 - team + P::kTeams - 1) / P::kTeams);  // this team's tiles
-        const int first_pos = (seq.lo / TP + tile0 + team) * TP;
-        const uint8_t* k_base = p.cache.k + kv * p.cache.head_stride;
-        const uint8_t* v_base = p.cache.v + kv * p.cache.head_stride;
-        Place ahead = {-1, -1};
-        auto look = [&](int i) {
-            const int pos = first_pos + i * P::kTeams * TP + lane % TP;
-            ahead = i < n && pos >= tile_lo && pos < tile_hi ? place_of(p.cache, p.seqs, s, pos) : Place{-1, -1};
-        };
-        auto issue = [&](int i) {
-            if (i < n) {
-                const int stage = i % ST;
-                const uint32_t keys = ring + stage * P::kStage, values = keys + TP * P::kRowBytes;
-                const unsigned there = __ballot_sync(0xffffffffu, ahead.at >= 0);
-                if (lane == 0) there_of[warp][stage] = there;
-                const int chunk = team_tid % NC;
-                const bool in = chunk * 16 < d * (E4 ? 1 : 2);
+    // ---- copies: the next tile's place, kept for all warps of a team alike
+    struct {
+        int seq, item, items, tile, tiles, left, base_pos, lo, hi, kv;
+    } next = {};
+    Place ahead = {-1, -1};
+    auto hi_of = [&](const Seq& q, int token) { return clip_pos(q.start + token + 1, p.seqs.positions); };
+    auto lo_of = [&](const Seq& q, int token) { return p.window ? clip_pos(q.start + token + 1 - p.window, p.seqs.positions) : 0; };
+    auto enter = [&](const Seq& q) {
+        next.items = q.row_tiles * p.cache.n_kv;
+        next.tiles = q.tiles;
+        next.base_pos = q.lo / TP * TP;
+        next.kv = next.item / q.row_tiles;
+        const int row0 = next.item % q.row_tiles * RT, rows = q.tokens * group;
+        next.lo = lo_of(q, row0 / group);
+        next.hi = hi_of(q, (min(row0 + RT, rows) - 1) / group);
+    };
+    auto look = [&]() {
+        const int pos = next.base_pos + next.tile * TP + lane % TP;
+        ahead = Place{-1, -1};
+        if (next.left > 0 && pos >= next.lo && pos < next.hi) ahead = place_of(p.cache, p.seqs, next.seq, pos);
+    };
+    next.left = run;
+    if (run > 0) {
+        next.seq = found_seq[team];
+        Seq q = seq_of<TP, RT>(p, next.seq, group);
+        const int64_t in = cur - found_base[team];
+        next.item = (int)div_of(in, q.tiles);
+        next.tile = (int)(in - (int64_t)next.item * q.tiles);
+        enter(q);
+        look();
+    }
+    auto issue = [&](int i) {
+        if (next.left > 0) {
+            const int stage = i % ST;
+            uint8_t* const keys = ring + stage * P::kStage;
+            const unsigned there = __ballot_sync(0xffffffffu, ahead.at >= 0);
+            if (lane == 0)
+                tile_of[warp][stage] = Tile{there, next.base_pos + next.tile * TP, next.left == run || next.tile == 0, next.left == 1 || next.tile + 1 == next.tiles,
+                                            next.seq, next.item, next.tile, next.tiles};
+            const uint32_t to = smem_u32(keys);
+            const uint8_t* const nothing = reinterpret_cast<const uint8_t*>(p.joined);  // the source of a copy of 0 bytes
+            const uint8_t* const k_base = p.cache.k + next.kv * p.cache.head_stride;
+            const uint8_t* const v_base = p.cache.v + next.kv * p.cache.head_stride;
+            const int chunk = team_tid % NC;
+            const bool in = chunk * 16 < d * (E4 ? 1 : 2);
 #pragma unroll
-                for (int k = 0; k < TP * NC / (32 * R); k++) {
-                    const int row = team_tid / NC + k * (32 * R / NC);
-                    const int64_t at = __shfl_sync(0xffffffffu, ahead.at, row);
-                    const bool ok = at >= 0 && in;
-                    const int64_t from = ok ? at + chunk * 16 : 0;
-                    cp16(keys + row * P::kRowBytes + ((chunk ^ (NC >= 8 ? (row & 1) * 4 : 0)) * 16), ok ? k_base + from : p.cache.k, ok);
-                    cp16(values + row * P::kRowBytes + ((chunk ^ (((row >> 1) & 3) * 2 & (NC - 1))) * 16), ok ? v_base + from : p.cache.v, ok);
-                }
-                if (E4 && warp % R == 0 && lane < TP) {
-                    const bool ok = ahead.at >= 0;
-                    const int64_t from = ok ? ahead.scale_at + kv * p.cache.scale_head_stride : 0;
-                    cp4(values + TP * P::kRowBytes + lane * 4, p.cache.k_scale + from, ok);
-                    cp4(values + TP * P::kRowBytes + (TP + lane) * 4, p.cache.v_scale + from, ok);
+            for (int k = 0; k < TP * NC / (32 * P::kTeam); k++) {
+                const int row = team_tid / NC + k * (32 * P::kTeam / NC);
+                const int64_t at = __shfl_sync(0xffffffffu, ahead.at, row);
+                const bool ok = at >= 0 && in;
+                const int64_t from = at + chunk * 16;
+                cp16(to + row * P::kRowBytes + ((chunk ^ (NC >= 8 ? (row & 1) * 4 : 0)) * 16), ok ? k_base + from : nothing, ok);
+                cp16(to + (TP + row) * P::kRowBytes + ((chunk ^ (((row >> 1) & 3) * 2 & (NC - 1))) * 16), ok ? v_base + from : nothing, ok);
+            }
+            if (E4 && warp % P::kTeam == 0 && lane < TP) {
+                const bool ok = ahead.at >= 0;
+                const int64_t from = ahead.scale_at + next.kv * p.cache.scale_head_stride;
+                cp4(to + 2 * TP * P::kRowBytes + lane * 4, ok ? p.cache.k_scale + from : reinterpret_cast<const float*>(nothing), ok);
+                cp4(to + 2 * TP * P::kRowBytes + (TP + lane) * 4, ok ? p.cache.v_scale + from : reinterpret_cast<const float*>(nothing), ok);
+            }
+            next.left--;
+            if (++next.tile == next.tiles && next.left > 0) {
+                next.tile = 0;
+                if (++next.item == next.items) {
+                    next.item = 0;
+                    Seq q;
+                    do {
+                        next.seq = min(next.seq + 1, p.seqs.n_seqs - 1);
+                        q = seq_of<TP, RT>(p, next.seq, group);
+                    } while (q.work == 0 && next.seq + 1 < p.seqs.n_seqs);
+                    enter(q);
+                } else {
+                    enter(seq_of<TP, RT>(p, next.seq, group));
                 }
             }
-            cp_commit();
-            look(i + 1);
-        };
-        look(0);
-#pragma unroll
-        for (int i = 0; i < ST - 1; i++) issue(i);
+            look();
+        }
+        cp_commit();
+    };
+    // ---- the pass over the run's tiles
+    Seq seq = {};
+    int item = 0, kv = 0, w0 = 0, rows = 0, token0 = 0, token1 = 0, all_lo = 0, all_hi = 0, tile_lo = 0, tile_hi = 0, tile0 = 0;
+    bool active = false;
+    uint32_t qf[P::kQInRegs ? P::kSteps : 1][P::kQInRegs ? P::kQEach : 1];
+    float row_scale[NT];
+    float acc[kJ][4][NT][4];  // [64 columns][their pair][rows]: columns 64 jj + 8 g + 2 m (+ 1), rows 2 t, 2 t + 1
+    float top[NT], sum[NT];
 
-        // ---- queries: fragments in the order in which the keys' pieces lie
-        constexpr int kEach = NT == 1 ? 2 : 4;  // registers of a step: rows g, and g + 8 with NT = 2
-        uint32_t qf[P::kQShared ? 1 : P::kSteps][kEach];
-        float row_scale[NT];
+    // an item's rows: queries as fragments in the order in which the keys' pieces lie
+    auto begin = [&](const Tile& x) {
+        seq = seq_of<TP, RT>(p, x.seq, group);
+        item = x.item;
+        tile0 = x.tile;
+        kv = item / seq.row_tiles;
+        rows = seq.tokens * group;
+        const int row0 = item % seq.row_tiles * RT;
+        tile_lo = lo_of(seq, row0 / group);
+        tile_hi = hi_of(seq, (min(row0 + RT, rows) - 1) / group);
+        w0 = row0 + row_warp * P::kRows;
+        const int w1 = min(w0 + P::kRows, rows);
+        active = w0 < rows;
+        token0 = w0 / group;
+        token1 = max(w1 - 1, w0) / group;
+        all_lo = lo_of(seq, token1);
+        all_hi = hi_of(seq, token0);
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
+            top[nt] = -INFINITY;
+            sum[nt] = 0.0f;
             const int row = w0 + nt * 8 + g;
             const uint8_t* q = row < rows ? p.q.data + (seq.first_token + row / group) * p.q.token_stride + (kv * group + row % group) * p.q.head_stride : nullptr;
+            // bf16: piece i is columns 32 i + 8 t .. + 7, two steps of four; e4m3: 64 i + 16 t .. + 15, four steps
+            float v[DP / 32][8];
+#pragma unroll
+            for (int i = 0; i < DP / 32; i++) load_q8(p.q, p.q_aligned, q, E4 ? 64 * (i / 2) + 16 * t + 8 * (i % 2) : 32 * i + 8 * t, d, v[i]);
             float factor = 1.0f;
+            row_scale[nt] = p.scale;
             if (E4) {  // a power of two that brings the row's largest into fp16's upper range
                 float a = 0.0f;
 #pragma unroll
-                for (int i = 0; i < DP / 32; i++) {
-                    float v[8];
-                    load_q8(p.q, p.q_aligned, q, 32 * i + 8 * t, d, v);
+                for (int i = 0; i < DP / 32; i++)
 #pragma unroll
-                    for (int e = 0; e < 8; e++) a = fmaxf(a, fabsf(v[e]));
-                }
+                    for (int e = 0; e < 8; e++) a = fmaxf(a, fabsf(v[i][e]));
                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
                 const int e = min(max(14 - ((int)(__float_as_uint(a) >> 23) - 127), -100), 100);
                 factor = __uint_as_float((uint32_t)(127 + e) << 23);
                 row_scale[nt] = p.scale * __uint_as_float((uint32_t)(127 - e) << 23);
-            } else {
-                row_scale[nt] = p.scale;
             }
-            // bf16: piece i is columns 32 i + 8 t .. + 7, two steps of four; e4m3: 64 i + 16 t .. + 15, four steps
 #pragma unroll
-            for (int i = 0; i < DP / 32; i++) {
-                float v[8];
-                const int col = E4 ? 64 * (i / 2) + 16 * t + 8 * (i % 2) : 32 * i + 8 * t;
-                load_q8(p.q, p.q_aligned, q, col, d, v);
+            for (int i = 0; i < DP / 32; i++)
 #pragma unroll
-                for (int e = 0; e < 8; e++) v[e] *= factor;
+                for (int h = 0; h < 2; h++) {
+                    const int step = 2 * i + h;
+                    float* x = v[i] + 4 * h;
 #pragma unroll
-                for (int pl = 0; pl < P::QP; pl++) {
+                    for (int e = 0; e < 4; e++) x[e] *= factor;
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const int step = 2 * i + h;
-                        const uint32_t x = part<E4>(v[4 * h], v[4 * h + 1]), y = part<E4>(v[4 * h + 2], v[4 * h + 3]);
-                        if (P::kQShared) {
-                            const uint32_t at = q_smem + ((pl * P::kSteps + step) * 32 + lane) * (8 * NT) + 4 * nt;
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4 * NT), "r"(y) : "memory");
+                    for (int f = 0; f < P::kQAll; f++) {  // a fragment: rows g, g + 8, the same of the upper columns
+                        uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
+#pragma unroll
+                        for (int y = 0; y < (NT == 1 ? 2 : 1); y++)
+                            if (NT == 2 || 2 * f + y < P::QP) {
+                                lo[y] = part<E4>(x[0], x[1]);
+                                hi[y] = part<E4>(x[2], x[3]);
+                            }
+                        constexpr int kE = P::kQInRegs ? P::kQEach : 1;
+                        uint32_t(&to)[kE] = qf[step % (P::kQInRegs ? P::kSteps : 1)];
+                        uint32_t* shared = reinterpret_cast<uint32_t*>(q_shared + (f * P::kSteps + step) * 512);
+                        if (P::kQInRegs) {
+                            // NT = 1: a part's two; NT = 2: the four of a part for both rows
+                            if (NT == 1) {
+#pragma unroll
+                                for (int y = 0; y < 2; y++)
+                                    if (2 * f + y < P::QP) {
+                                        to[(4 * f + 2 * y) % kE] = lo[y];
+                                        to[(4 * f + 2 * y + 1) % kE] = hi[y];
+                                    }
+                            } else {
+                                to[(4 * f + nt) % kE] = lo[0];
+                                to[(4 * f + 2 + nt) % kE] = hi[0];
+                            }
+                        } else if (NT == 1) {
+                            *reinterpret_cast<uint4*>(shared) = make_uint4(lo[0], lo[1], hi[0], hi[1]);
                         } else {
-                            qf[step][nt] = x;
-                            qf[step][kEach / 2 + nt] = y;
+                            shared[nt] = lo[0];
+                            shared[2 + nt] = hi[0];
                         }
                     }
                 }
-            }
-        }
-        // one step of the first product: b of a key's piece with every part of the queries
-        auto score = [&](float (&c4)[4], int step, uint32_t b0, uint32_t b1) {
-#pragma unroll
-            for (int pl = 0; pl < P::QP; pl++) {
-                uint32_t a[4];
-                if (P::kQShared) {
-                    const uint32_t at = q_smem + ((pl * P::kSteps + step) * 32 + lane) * (8 * NT);
-                    if (NT == 1) {
-                        const uint2 x = lds8(at);
-                        a[0] = x.x; a[1] = 0; a[2] = x.y; a[3] = 0;
-                    } else {
-                        const uint4 x = lds16(at);
-                        a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
-                    }
-                } else {
-                    constexpr int kS = P::kQShared ? 0 : 1;
-                    a[0] = qf[step * kS][0];
-                    a[1] = NT == 1 ? 0u : qf[step * kS][1 % kEach];
-                    a[2] = qf[step * kS][kEach / 2];
-                    a[3] = NT == 1 ? 0u : qf[step * kS][kEach - 1];
-                }
-                mma<E4>(c4, a[0], a[1], a[2], a[3], b0, b1);
-            }
-        };
-
-        // ---- the pass over the positions
-        float acc[DP / 64][4][NT][4];  // [64 columns][their pair][rows]: columns 64 jj + 8 g + 2 m (+ 1), rows 2 t, 2 t + 1
-        float top[NT], sum[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-            top[nt] = -INFINITY;
-            sum[nt] = 0.0f;
         }
 #pragma unroll
-        for (int jj = 0; jj < DP / 64; jj++)
+        for (int jj = 0; jj < kJ; jj++)
 #pragma unroll
             for (int m = 0; m < 4; m++)
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int e = 0; e < 4; e++) acc[jj][m][nt][e] = 0.0f;
+    };
+    // one step of the first product: a key's piece with every part of the queries
+    auto score = [&](float (&c4)[4], int step, uint32_t b0, uint32_t b1) {
+#pragma unroll
+        for (int f = 0; f < P::kQAll; f++) {
+            if (P::kQInRegs) {
+                constexpr int kE = P::kQInRegs ? P::kQEach : 1;
+                const uint32_t(&q)[kE] = qf[step % (P::kQInRegs ? P::kSteps : 1)];
+                if (NT == 2) mma<E4>(c4, q[4 * f % kE], q[(4 * f + 1) % kE], q[(4 * f + 2) % kE], q[(4 * f + 3) % kE], b0, b1);
+                else if (2 * f + 1 < P::QP) mma<E4>(c4, q[4 * f % kE], q[(4 * f + 2) % kE], q[(4 * f + 1) % kE], q[(4 * f + 3) % kE], b0, b1);
+                else mma<E4>(c4, q[4 * f % kE], 0u, q[(4 * f + 1) % kE], 0u, b0, b1);
+            } else {
+                const uint4 x = *reinterpret_cast<const uint4*>(q_shared + (f * P::kSteps + step) * 512);
+                mma<E4>(c4, x.x, x.y, x.z, x.w, b0, b1);
+            }
+        }
+    };
+    // the rows' sums to where they are joined: [rows x stride], maxima and sums of weights at ml
+    auto put = [&](float* to, int stride, float2* ml) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            const int row = row_warp * P::kRows + nt * 8;
+            if (t == 0 && col_warp == 0) ml[row + g] = make_float2(top[nt], sum[nt]);
+#pragma unroll
+            for (int jj = 0; jj < kJ; jj++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float4* at = reinterpret_cast<float4*>(to + (row + 2 * t + e) * stride + col_warp * P::kCols + 64 * jj + 8 * g);
+                    at[0] = make_float4(acc[jj][0][nt][e], acc[jj][0][nt][e + 2], acc[jj][1][nt][e], acc[jj][1][nt][e + 2]);
+                    at[1] = make_float4(acc[jj][2][nt][e], acc[jj][2][nt][e + 2], acc[jj][3][nt][e], acc[jj][3][nt][e + 2]);
+                }
+        }
+    };
 
-        for (int i = 0; i < n; i++) {
+    for (int i = 1 - ST; i < run; i++) {
+        const int stage = i < 0 ? 0 : i % ST;
+        const Tile& x = tile_of[warp][stage];
+        if (i >= 0) {
+            __syncwarp();
+            if (x.first) begin(x);  // the queries are on their way with the tile
             cp_wait<ST - 2>();
-            team_sync<R>(team);
-            issue(i + ST - 1);
-            if (!active) continue;
-            const int stage = i % ST, pos0 = first_pos + i * P::kTeams * TP;
-            const uint32_t keys = ring + stage * P::kStage, values = keys + TP * P::kRowBytes, scales = values + TP * P::kRowBytes;
-            const unsigned there = there_of[warp][stage];
+            sync_warps(1 + team, P::kTeam);
+        }
+        issue(i + ST - 1);
+        if (i < 0) continue;
+        const unsigned there = x.there;
+        const int pos0 = x.pos0;
+        if (active) {
+            const uint8_t* const keys = ring + stage * P::kStage;
+            const uint8_t* const values = keys + TP * P::kRowBytes;
+            const float* const scales = reinterpret_cast<const float*>(values + TP * P::kRowBytes);
             const unsigned whole = TP == 32 ? 0xffffffffu : (1u << (TP & 31)) - 1u;
             const bool full = (there & whole) == whole && pos0 >= all_lo && pos0 + TP <= all_hi;
 
             float sc[TP / 8][4];
 #pragma unroll
-            for (int nt8 = 0; nt8 < TP / 8; nt8++) {
+            for (int n8 = 0; n8 < TP / 8; n8++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) sc[nt8][e] = 0.0f;
-                const int row = nt8 * 8 + g;
+                for (int e = 0; e < 4; e++) sc[n8][e] = 0.0f;
 #pragma unroll
-                for (int i4 = 0; i4 < NC / 4; i4++) {
-                    const uint4 w = lds16(keys + row * P::kRowBytes + (((4 * i4 + t) ^ (NC >= 8 ? (row & 1) * 4 : 0)) * 16));
+            for (int i4 = 0; i4 < NC / 4; i4++)
+#pragma unroll
+                for (int n8 = 0; n8 < TP / 8; n8++) {
+                    const int row = n8 * 8 + g;
+                    const uint4 w = *reinterpret_cast<const uint4*>(keys + row * P::kRowBytes + (((4 * i4 + t) ^ (NC >= 8 ? (row & 1) * 4 : 0)) * 16));
                     const uint32_t r4[4] = {w.x, w.y, w.z, w.w};
                     if (E4) {
 #pragma unroll
-                        for (int h = 0; h < 4; h++) score(sc[nt8], 4 * i4 + h, widen(r4[h]), widen(r4[h] >> 16));
+                        for (int h = 0; h < 4; h++) score(sc[n8], 4 * i4 + h, widen(r4[h]), widen(r4[h] >> 16));
                     } else {
-                        score(sc[nt8], 2 * i4, r4[0], r4[1]);
-                        score(sc[nt8], 2 * i4 + 1, r4[2], r4[3]);
+                        score(sc[n8], 2 * i4, r4[0], r4[1]);
+                        score(sc[n8], 2 * i4 + 1, r4[2], r4[3]);
                     }
                 }
-            }
             float2 vs[TP / 8];
 #pragma unroll
-            for (int nt8 = 0; nt8 < TP / 8; nt8++) {
+            for (int n8 = 0; n8 < TP / 8; n8++) {
+                if (NT == 1 && P::QP > 1) {  // the second part's rows
+                    sc[n8][0] += sc[n8][2];
+                    sc[n8][1] += sc[n8][3];
+                }
 #pragma unroll
-                for (int e = 0; e < 2 * NT; e++) sc[nt8][e] *= row_scale[e / 2];
+                for (int e = 0; e < 2 * NT; e++) sc[n8][e] *= row_scale[e / 2];
                 if (E4) {
-                    const float2 ks = lds_f2(scales + (nt8 * 8 + 2 * t) * 4);
-                    vs[nt8] = lds_f2(scales + (TP + nt8 * 8 + 2 * t) * 4);
+                    const float2 ks = *reinterpret_cast<const float2*>(scales + n8 * 8 + 2 * t);
+                    vs[n8] = *reinterpret_cast<const float2*>(scales + TP + n8 * 8 + 2 * t);
 #pragma unroll
-                    for (int e = 0; e < 2 * NT; e++) sc[nt8][e] *= e % 2 ? ks.y : ks.x;
+                    for (int e = 0; e < 2 * NT; e++) sc[n8][e] *= e % 2 ? ks.y : ks.x;
                 }
             }
             if (!full) {
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
                     const int token = (w0 + nt * 8 + g) / group;
-                    const int lo = lo_of(token), hi = hi_of(token);
+                    const int lo = lo_of(seq, token), hi = hi_of(seq, token);
 #pragma unroll
-                    for (int nt8 = 0; nt8 < TP / 8; nt8++)
+                    for (int n8 = 0; n8 < TP / 8; n8++)
 #pragma unroll
                         for (int e = 0; e < 2; e++) {
-                            const int at = nt8 * 8 + 2 * t + e;
-                            if (!((there >> at) & 1u) || pos0 + at < lo || pos0 + at >= hi) sc[nt8][2 * nt + e] = -INFINITY;
+                            const int at = n8 * 8 + 2 * t + e;
+                            if (!((there >> at) & 1u) || pos0 + at < lo || pos0 + at >= hi) sc[n8][2 * nt + e] = -INFINITY;
                         }
                 }
             }
             // the values' scales count for the maximum, as within 2^-100 .. 2^118: the weight's two factors stay in fp32's range
             float2 lv[TP / 8];
 #pragma unroll
-            for (int nt8 = 0; nt8 < TP / 8; nt8++) {
-                lv[nt8] = make_float2(0.0f, 0.0f);
-                if (E4) lv[nt8] = make_float2(fminf(fmaxf(lg2(vs[nt8].x), -100.0f), 118.0f), fminf(fmaxf(lg2(vs[nt8].y), -100.0f), 118.0f));
+            for (int n8 = 0; n8 < TP / 8; n8++) {
+                lv[n8] = make_float2(0.0f, 0.0f);
+                if (E4) lv[n8] = make_float2(fminf(fmaxf(lg2(vs[n8].x), -100.0f), 118.0f), fminf(fmaxf(lg2(vs[n8].y), -100.0f), 118.0f));
             }
             bool grown = false;
             float most[NT];
@@ -512,7 +707,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_kernel(const AttnArgs p) 
             for (int nt = 0; nt < NT; nt++) {
                 float a = -INFINITY;
 #pragma unroll
-                for (int nt8 = 0; nt8 < TP / 8; nt8++) a = fmaxf(a, fmaxf(sc[nt8][2 * nt] + lv[nt8].x, sc[nt8][2 * nt + 1] + lv[nt8].y));
+                for (int n8 = 0; n8 < TP / 8; n8++) a = fmaxf(a, fmaxf(sc[n8][2 * nt] + lv[n8].x, sc[n8][2 * nt + 1] + lv[n8].y));
                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
                 most[nt] = a;
@@ -527,7 +722,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_kernel(const AttnArgs p) 
                     sum[nt] *= by;
                     const float b0 = __shfl_sync(0xffffffffu, by, 8 * t), b1 = __shfl_sync(0xffffffffu, by, 8 * t + 4);
 #pragma unroll
-                    for (int jj = 0; jj < DP / 64; jj++)
+                    for (int jj = 0; jj < kJ; jj++)
 #pragma unroll
                         for (int m = 0; m < 4; m++) {
                             acc[jj][m][nt][0] *= b0;
@@ -542,191 +737,232 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_kernel(const AttnArgs p) 
             for (int nt = 0; nt < NT; nt++) {
                 const float ref = top[nt] == -INFINITY ? 0.0f : top[nt];
 #pragma unroll
-                for (int nt8 = 0; nt8 < TP / 8; nt8++) {
-                    float x = ex2(sc[nt8][2 * nt] - ref), y = ex2(sc[nt8][2 * nt + 1] - ref);
-                    sum[nt] += x + y;
+                for (int n8 = 0; n8 < TP / 8; n8++) {
+                    float a = ex2(sc[n8][2 * nt] - ref), b = ex2(sc[n8][2 * nt + 1] - ref);
+                    sum[nt] += a + b;
                     if (E4) {  // a weight of 0 stays 0 beside whatever scale a position has that is not seen
-                        x = sc[nt8][2 * nt] == -INFINITY ? 0.0f : x * vs[nt8].x;
-                        y = sc[nt8][2 * nt + 1] == -INFINITY ? 0.0f : y * vs[nt8].y;
+                        a = sc[n8][2 * nt] == -INFINITY ? 0.0f : a * vs[n8].x;
+                        b = sc[n8][2 * nt + 1] == -INFINITY ? 0.0f : b * vs[n8].y;
                     }
 #pragma unroll
-                    for (int pl = 0; pl < P::PP; pl++) pb[nt8 / 2][nt][pl][nt8 % 2] = part<E4>(x, y);
+                    for (int pl = 0; pl < P::PP; pl++) pb[n8 / 2][nt][pl][n8 % 2] = part<E4>(a, b);
                 }
             }
             // positions here that one of the warp's rows does not see and that were copied for another
             const bool mixed = !full && (min(pos0 + TP, tile_hi) > all_hi || max(pos0, tile_lo) < all_lo);
+            // four positions' eight columns, and a pair of these as the product's operand
+            constexpr int kW = E4 ? 2 : 4;
+            auto load_values = [&](int kk, int jj, uint32_t (&w)[4][kW]) {
 #pragma unroll
-            for (int kk = 0; kk < TP / 16; kk++) {
-#pragma unroll
-                for (int jj = 0; jj < DP / 64; jj++) {
-                    // four positions' eight columns
-                    uint32_t w[4][E4 ? 2 : 4];
-#pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        const int row = kk * 16 + 2 * t + (r & 1) + (r >> 1) * 8;
-                        if (E4) {
-                            const int chunk = 4 * jj + g / 2;
-                            const uint2 x = lds8(values + row * P::kRowBytes + ((chunk ^ (((row >> 1) & 3) * 2 & (NC - 1))) * 16) + (g & 1) * 8);
-                            w[r][0] = x.x;
-                            w[r][1] = x.y;
-                        } else {
-                            const int chunk = 8 * jj + g;
-                            const uint4 x = lds16(values + row * P::kRowBytes + ((chunk ^ (((row >> 1) & 3) * 2)) * 16));
-                            w[r][0] = x.x; w[r][1] = x.y; w[r][E4 ? 0 : 2] = x.z; w[r][E4 ? 0 : 3] = x.w;
-                        }
+                for (int r = 0; r < 4; r++) {
+                    const int row = kk * 16 + 2 * t + (r & 1) + (r >> 1) * 8;
+                    if (E4) {
+                        const uint2 y = *reinterpret_cast<const uint2*>(values + row * P::kRowBytes + (((4 * (jj + col_warp * kJ) + g / 2) ^ (((row >> 1) & 3) * 2 & (NC - 1))) * 16) + (g & 1) * 8);
+                        w[r][0] = y.x;
+                        w[r][1] = y.y;
+                    } else {
+                        const uint4 y = *reinterpret_cast<const uint4*>(values + row * P::kRowBytes + (((8 * (jj + col_warp * kJ) + g) ^ (((row >> 1) & 3) * 2)) * 16));
+                        w[r][0] = y.x;
+                        w[r][1] = y.y;
+                        w[r][2 % kW] = y.z;
+                        w[r][3 % kW] = y.w;
                     }
-                    auto values_of = [&](int m, uint32_t (&a)[4]) {
-                        if (E4) {
-                            const uint32_t x = __byte_perm(w[0][m / 2], w[1][m / 2], m % 2 ? 0x7362 : 0x5140);
-                            const uint32_t y = __byte_perm(w[2][m / 2], w[3][m / 2], m % 2 ? 0x7362 : 0x5140);
-                            a[0] = widen(x);
-                            a[1] = widen(x >> 16);
-                            a[2] = widen(y);
-                            a[3] = widen(y >> 16);
-                        } else {
-                            constexpr int kM = E4 ? 0 : 1;
-                            a[0] = __byte_perm(w[0][m * kM], w[1][m * kM], 0x5410);
-                            a[1] = __byte_perm(w[0][m * kM], w[1][m * kM], 0x7632);
-                            a[2] = __byte_perm(w[2][m * kM], w[3][m * kM], 0x5410);
-                            a[3] = __byte_perm(w[2][m * kM], w[3][m * kM], 0x7632);
-                        }
-                    };
-                    if (!mixed) {
+                }
+            };
+            auto pair_of = [&](const uint32_t (&w)[4][kW], int m, uint32_t (&a)[4]) {
+                if (E4) {
+                    const uint32_t y = __byte_perm(w[0][m / 2], w[1][m / 2], m % 2 ? 0x7362 : 0x5140);
+                    const uint32_t z = __byte_perm(w[2][m / 2], w[3][m / 2], m % 2 ? 0x7362 : 0x5140);
+                    a[0] = widen(y);
+                    a[1] = widen(y >> 16);
+                    a[2] = widen(z);
+                    a[3] = widen(z >> 16);
+                } else {
+                    a[0] = __byte_perm(w[0][m % kW], w[1][m % kW], 0x5410);
+                    a[1] = __byte_perm(w[0][m % kW], w[1][m % kW], 0x7632);
+                    a[2] = __byte_perm(w[2][m % kW], w[3][m % kW], 0x5410);
+                    a[3] = __byte_perm(w[2][m % kW], w[3][m % kW], 0x7632);
+                }
+            };
+            if (!mixed) {
+#pragma unroll
+                for (int kk = 0; kk < TP / 16; kk++)
+#pragma unroll
+                    for (int jj = 0; jj < kJ; jj++) {
+                        uint32_t w[4][kW];
+                        load_values(kk, jj, w);
 #pragma unroll
                         for (int m = 0; m < 4; m++) {
                             uint32_t a[4];
-                            values_of(m, a);
+                            pair_of(w, m, a);
 #pragma unroll
                             for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                                 for (int pl = 0; pl < P::PP; pl++) mma<E4>(acc[jj][m][nt], a[0], a[1], a[2], a[3], pb[kk][nt][pl][0], pb[kk][nt][pl][1]);
                         }
-                    } else {
-                        uint32_t all[4][E4 ? 2 : 4];
+                    }
+            } else {
+#pragma unroll 1
+                for (int token = token0; token <= token1; token++) {
+                    const int lo = lo_of(seq, token), hi = hi_of(seq, token);
 #pragma unroll
-                        for (int r = 0; r < 4; r++)
+                    for (int kk = 0; kk < TP / 16; kk++)
 #pragma unroll
-                            for (int x = 0; x < (E4 ? 2 : 4); x++) all[r][x] = w[r][x];
-                        for (int token = token0; token <= token1; token++) {
-                            const int lo = lo_of(token), hi = hi_of(token);
+                        for (int jj = 0; jj < kJ; jj++) {
+                            uint32_t w[4][kW];
+                            load_values(kk, jj, w);
 #pragma unroll
                             for (int r = 0; r < 4; r++) {
                                 const int at = pos0 + kk * 16 + 2 * t + (r & 1) + (r >> 1) * 8;
 #pragma unroll
-                                for (int x = 0; x < (E4 ? 2 : 4); x++) w[r][x] = at >= lo && at < hi ? all[r][x] : 0u;
+                                for (int y = 0; y < kW; y++)
+                                    if (at < lo || at >= hi) w[r][y] = 0u;
                             }
 #pragma unroll
                             for (int m = 0; m < 4; m++) {
                                 uint32_t a[4];
-                                values_of(m, a);
+                                pair_of(w, m, a);
 #pragma unroll
                                 for (int nt = 0; nt < NT; nt++) {
                                     float one[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                                     for (int pl = 0; pl < P::PP; pl++) mma<E4>(one, a[0], a[1], a[2], a[3], pb[kk][nt][pl][0], pb[kk][nt][pl][1]);
                                     const int row = w0 + nt * 8 + 2 * t;
-                                    const bool x0 = row / group == token, x1 = (row + 1) / group == token;
-                                    if (x0) {
+                                    if (row / group == token) {
                                         acc[jj][m][nt][0] += one[0];
                                         acc[jj][m][nt][2] += one[2];
                                     }
-                                    if (x1) {
+                                    if ((row + 1) / group == token) {
                                         acc[jj][m][nt][1] += one[1];
                                         acc[jj][m][nt][3] += one[3];
                                     }
                                 }
                             }
                         }
-                    }
                 }
             }
         }
-        cp_wait<0>();
-        __syncthreads();
+        if (!x.last) continue;
 
-        // ---- the teams' results, through shared memory
-        const uint32_t red_ml = red + P::kTeams * RT * (DP + 4) * 4;
+        // ---- the end of an item, or of the run inside one
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
             sum[nt] += __shfl_xor_sync(0xffffffffu, sum[nt], 1);
             sum[nt] += __shfl_xor_sync(0xffffffffu, sum[nt], 2);
-            const int row = team * RT + (warp % R) * P::kRows + nt * 8;
-            if (t == 0) sts_f2(red_ml + (row + g) * 8, top[nt], sum[nt]);
-#pragma unroll
-            for (int jj = 0; jj < DP / 64; jj++)
-#pragma unroll
-                for (int m = 0; m < 4; m++) {
-                    const uint32_t at = red + ((row + 2 * t) * (DP + 4) + 64 * jj + 8 * g + 2 * m) * 4;
-                    sts_f2(at, acc[jj][m][nt][0], acc[jj][m][nt][2]);
-                    sts_f2(at + (DP + 4) * 4, acc[jj][m][nt][1], acc[jj][m][nt][3]);
-                }
         }
-        __syncthreads();
-        const int64_t c0 = cta_of(item0), c1 = cta_of(item0 + seq.tiles - 1);
-        // 8 columns of a row a thread; whole warps, as the codes' maxima are found by shuffles
-        constexpr int kPieces = RT * DP / 8;
-        for (int x = tid; x < (kPieces + 31) / 32 * 32; x += kThreads) {
-            const int row = x / (DP / 8), col = x % (DP / 8) * 8;
-            float m = -INFINITY, l = 0.0f, v[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++) v[e] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < P::kTeams; w++) m = fmaxf(m, lds_f2(red_ml + (w * RT + row) * 8).x);
-#pragma unroll
-            for (int w = 0; w < P::kTeams; w++) {
-                const float2 ml = lds_f2(red_ml + (w * RT + row) * 8);
-                const float by = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - m);
-                const uint32_t at = red + ((w * RT + row) * (DP + 4) + col) * 4;
-                l += by * ml.y;
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float2 o = lds_f2(at + 4 * e);
-                    v[e] += by * o.x;
-                    v[e + 1] += by * o.y;
-                }
-            }
-            if (c0 == c1) {
-                const int r = row0 + row;
-                finish<DP>(p, seq.first_token + r / group, kv * group + r % group, col, v, m, l, r < rows);
-            } else {
-                float* to = p.parts + (c * 2 + (c == c0)) * (RT * (DP + 2));
-                float4* o = reinterpret_cast<float4*>(to + row * DP + col);
-                __stcg(o, make_float4(v[0], v[1], v[2], v[3]));
-                __stcg(o + 1, make_float4(v[4], v[5], v[6], v[7]));
-                if (col == 0) __stcg(reinterpret_cast<float2*>(to + RT * DP) + row, make_float2(m, l));
-            }
+        const bool ends = x.tile + 1 == x.tiles;
+        if (tile0 == 0 && ends) {
+            finish_rows<P>(p, seq, kv, w0, rows, group, top, sum, acc, most_of, team);
+            continue;
         }
-        if (c0 != c1) {
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) is_last = atom_acq_rel_add(p.joined + c0, 1u) == (uint32_t)(c1 - c0);
-            __syncthreads();
-            if (is_last) {
-                __threadfence();
-                for (int x = tid; x < (kPieces + 31) / 32 * 32; x += kThreads) {
-                    const int row = x / (DP / 8), col = x % (DP / 8) * 8;
-                    auto part_at = [&](int64_t w) { return p.parts + (w * 2 + (w == c0)) * (RT * (DP + 2)); };
-                    float m = -INFINITY, l = 0.0f, v[8];
+        if (team_tid == 0) piece_of[2 * team + !ends] = Piece{cur + i - x.tile, x.seq, item};
+        if (ends) {
+            float* to = p.heads + (c * P::kTeams + team) * P::kPart;
+            put(to, DP, reinterpret_cast<float2*>(to + RT * DP));
+        }
+    }
+    cp_wait<0>();
+    __syncthreads();  // the ring is free
+    if (piece_of[2 * team + 1].item0 >= 0) put(red + team * RT * (DP + 4), DP + 4, red_ml + team * RT);
+    __syncthreads();
+
+    // ---- what the teams have of the same item, and then the CTAs: the warps are dealt to the items
+    const int64_t my_item0 = lane < 2 * P::kTeams ? piece_of[lane].item0 : -1;
+    const unsigned pieces = __ballot_sync(0xffffffffu, my_item0 >= 0);
+    const unsigned before = pieces & ((1u << lane) - 1u);
+    const int64_t item_before = __shfl_sync(0xffffffffu, my_item0, before ? 31 - __clz(before) : 0);
+    unsigned starts = __ballot_sync(0xffffffffu, my_item0 >= 0 && (!before || item_before != my_item0));
+    const int items = __popc(starts);
+    if (items == 0) return;
+    const int crews = min(items, kWarps), size = kWarps / crews, crew = warp / size, crew_tid = tid - crew * size * 32;
+    if (crew >= crews) return;
+    for (int n = 0; n < items; n++, starts &= starts - 1u) {
+        if (n % crews != crew) continue;
+        const int i0 = __ffs(starts) - 1, i1 = starts & (starts - 1u) ? __ffs(starts & (starts - 1u)) - 1 : 2 * P::kTeams;
+        const int64_t item0 = piece_of[i0].item0;
+        const Seq q = seq_of<TP, RT>(p, piece_of[i0].seq, group);
+        const int head = piece_of[i0].item / q.row_tiles * group, row0 = piece_of[i0].item % q.row_tiles * RT, n_rows = q.tokens * group;
+        const bool whole = item0 >= run0 && item0 + q.tiles <= run1;
+        const int c0 = whole ? c : cta_of(item0), c1 = whole ? c : cta_of(item0 + q.tiles - 1);
+        // CTAs c0 .. c1 have the item; the first kFan of them, the next kFan and so on are joined first
+        const int sub = (c - c0) / kFan, first = c0 + sub * kFan, many = min(kFan, c1 - first + 1), subs = (c1 - c0) / kFan + 1;
+        for (int level = 0;; level++) {
+            // part i of this level: of the teams, of CTAs, of kFan CTAs
+            const int lo = level == 0 ? i0 : 0, hi = level == 0 ? i1 : level == 1 ? many : subs;
+            auto part_at = [&](int i) -> const float* {
+                if (level == 0) return p.heads + (c * P::kTeams + i / 2) * P::kPart;
+                if (level == 1) return p.parts + ((first + i) * 2 + (first + i == c0)) * P::kPart;
+                return p.merged + ((c0 + i * kFan) * 2 + (i == 0)) * P::kPart;
+            };
+            const bool done = whole || level == 2 || (level == 1 && subs == 1);
+            for (int x = crew_tid; x < (RT * DP / 8 + 31) / 32 * 32; x += size * 32) {  // eight columns of a row a thread
+                const int row = x / (DP / 8), col = x % (DP / 8) * 8;
+                float m = -INFINITY, l = 0.0f, v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; e++) v[e] = 0.0f;
-                    for (int64_t w = c0; w <= c1; w++) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(part_at(w) + RT * DP) + row).x);
-                    for (int64_t w = c0; w <= c1; w++) {
-                        const float* from = part_at(w);
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + RT * DP) + row);
-                        const float by = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - m);
-                        l += by * ml.y;
-                        const float4 a = __ldcg(reinterpret_cast<const float4*>(from + row * DP + col));
-                        const float4 b = __ldcg(reinterpret_cast<const float4*>(from + row * DP + col) + 1);
-                        v[0] += by * a.x; v[1] += by * a.y; v[2] += by * a.z; v[3] += by * a.w;
-                        v[4] += by * b.x; v[5] += by * b.y; v[6] += by * b.z; v[7] += by * b.w;
+                for (int e = 0; e < 8; e++) v[e] = 0.0f;
+                for (int at = lo; at < hi; at += 4) {
+                    float2 ml[4];
+                    float4 a[4], b[4];
+#pragma unroll
+                    for (int y = 0; y < 4; y++) {
+                        const int i = at + y;
+                        ml[y] = make_float2(-INFINITY, 0.0f);
+                        a[y] = b[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (i >= hi || (level == 0 && !((pieces >> i) & 1u))) continue;
+                        if (level == 0 && i % 2) {
+                            ml[y] = red_ml[i / 2 * RT + row];
+                            const float4* from = reinterpret_cast<const float4*>(red + (i / 2 * RT + row) * (DP + 4) + col);
+                            a[y] = from[0];
+                            b[y] = from[1];
+                        } else {
+                            const float* part = part_at(i);
+                            ml[y] = __ldcg(reinterpret_cast<const float2*>(part + RT * DP) + row);
+                            const float4* from = reinterpret_cast<const float4*>(part + row * DP + col);
+                            a[y] = __ldcg(from);
+                            b[y] = __ldcg(from + 1);
+                        }
                     }
-                    const int r = row0 + row;
-                    finish<DP>(p, seq.first_token + r / group, kv * group + r % group, col, v, m, l, r < rows);
+                    const float now = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+                    const float by = part_factor(make_float2(m, l), now);
+                    m = now;
+                    l *= by;
+#pragma unroll
+                    for (int e = 0; e < 8; e++) v[e] *= by;
+#pragma unroll
+                    for (int y = 0; y < 4; y++) {
+                        const float f = part_factor(ml[y], m);
+                        l += f * ml[y].y;
+                        v[0] += f * a[y].x; v[1] += f * a[y].y; v[2] += f * a[y].z; v[3] += f * a[y].w;
+                        v[4] += f * b[y].x; v[5] += f * b[y].y; v[6] += f * b[y].z; v[7] += f * b[y].w;
+                    }
                 }
-                if (tid == 0) p.joined[c0] = 0u;
+                if (done) {
+                    const int r = row0 + row;
+                    finish<DP>(p, q.first_token + r / group, head + r % group, col, v, m, l, r < n_rows);
+                } else {
+                    float* to = level == 0 ? p.parts + (c * 2 + (c == c0)) * P::kPart : p.merged + (first * 2 + (first == c0)) * P::kPart;
+                    float4* o = reinterpret_cast<float4*>(to + row * DP + col);
+                    __stcg(o, make_float4(v[0], v[1], v[2], v[3]));
+                    __stcg(o + 1, make_float4(v[4], v[5], v[6], v[7]));
+                    if (col == 0) __stcg(reinterpret_cast<float2*>(to + RT * DP) + row, make_float2(m, l));
+                }
             }
+            if (done) break;
+            // the last of those that have parts goes on; it leaves the counter at zero
+            __threadfence();
+            sync_warps(1 + crew, size);
+            if (crew_tid == 0) {
+                uint32_t* counter = p.joined + (level == 1 ? 2 * kAttnMaxCtas + c0 : sub == 0 ? c0 : kAttnMaxCtas + first);
+                const bool last = atom_acq_rel_add(counter, 1u) == (uint32_t)((level == 0 ? many : subs) - 1);
+                if (last) *counter = 0u;
+                last_of[crew] = last;
+            }
+            sync_warps(1 + crew, size);
+            const bool last = last_of[crew];
+            sync_warps(1 + crew, size);
+            if (!last) break;
+            __threadfence();
         }
-        __syncthreads();  // the ring is free for the next item
     }
 }
 
@@ -742,24 +978,35 @@ cudaError_t launch(AttnArgs p, cudaStream_t st) {
         int sms = 0, each = 0;
         if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if ((e = cudaFuncSetAttribute(attn_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem)) != cudaSuccess) return e;
-        if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, attn_kernel<P>, 32 * kWarps, P::kSmem)) != cudaSuccess) return e;
+        if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, attn_kernel<P>, 32 * P::kWarps, P::kSmem)) != cudaSuccess) return e;
         if (each < 1) return cudaErrorLaunchOutOfResources;
         ctas = std::min(kAttnMaxCtas, sms * each);
         if (dev < 64) ctas_of[dev] = ctas;
     }
-    return launch_pdl(attn_kernel<P>, dim3((unsigned)ctas), 32 * kWarps, P::kSmem, st, p);
+    return launch_pdl(attn_kernel<P>, dim3((unsigned)ctas), 32 * P::kWarps, P::kSmem, st, p);
 }
 
-// Rows of an item: 8 of one warp, 16 of one (two with 256 columns, whose sums fill the registers), else 64 of four.
+// Rows of an item: 8, 16 or 64, each with the plan that was fastest of those that fit the registers and three tiles a team.
 constexpr int padded_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 constexpr int item_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 64; }
+constexpr int most_teams(int rows) { return rows <= 16 ? 16 : 4; }
 
 template <bool E4, int DP, bool WIDE>
 cudaError_t launch_rows(const AttnArgs& p, cudaStream_t st) {
     const int rows = item_rows(p.n_heads / p.cache.n_kv * p.max_new);
-    if (rows == 8) return launch<Plan<E4, DP, 1, 1, WIDE>>(p, st);
-    if (rows == 16) return launch<Plan<E4, DP, DP == 256 ? 1 : 2, DP == 256 ? 2 : 1, WIDE>>(p, st);
-    return launch<Plan<E4, DP, 2, 4, WIDE>>(p, st);
+    // columns of a team's warps and warps a CTA
+    if (rows == 8) {
+        constexpr int C = DP == 64 ? 1 : DP == 128 ? (E4 || WIDE ? 1 : 2) : E4 ? (WIDE ? 1 : 2) : WIDE ? 2 : 4;
+        constexpr int W = DP == 64 ? 16 : DP == 128 ? (E4 ? 12 : WIDE ? 8 : 16) : WIDE ? 8 : E4 ? 12 : 16;
+        return launch<Plan<E4, DP, 1, 1, C, W, WIDE>>(p, st);
+    }
+    if (rows == 16) {
+        constexpr int C = DP == 64 || (DP == 128 && WIDE) ? 1 : 2;
+        return launch<Plan<E4, DP, DP == 256 ? 1 : 2, DP == 256 ? 2 : 1, C, (DP > 64 && WIDE ? 8 : 12), WIDE>>(p, st);
+    }
+    constexpr int C = DP == 256 && (E4 || !WIDE) ? 2 : 1;
+    constexpr int W = DP == 64 ? 12 : DP == 128 ? (WIDE && !E4 ? 8 : 12) : WIDE && !E4 ? 4 : 8;
+    return launch<Plan<E4, DP, 2, 4, C, W, WIDE>>(p, st);
 }
 
 }  // namespace attn

@@ -254,10 +254,10 @@ struct AttnArgs {
     float scale;       // of the scores, times log2(e)
     int n_tokens, n_heads, max_new, window;
     bool q_aligned, out_aligned;
-    uint32_t* joined;  // workspace: a counter a CTA, and the parts of items that several CTAs share
-    float* parts;
+    uint32_t* joined;  // workspace: three counters a CTA, and the parts of items that several teams or CTAs share
+    float *parts, *merged, *heads;
 };
-constexpr int kAttnMaxCtas = 608;  // most CTAs of a call: four an SM
+constexpr int kAttnMaxCtas = 160;  // most CTAs of a call, one an SM
 size_t attn_workspace(int n_heads, int n_kv, int head_dim, int max_new);
 cudaError_t launch_cache_attention(const AttnArgs& p, void* workspace, cudaStream_t st);
 
