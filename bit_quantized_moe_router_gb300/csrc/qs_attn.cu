@@ -19,6 +19,11 @@ cudaError_t launch_cache_attention(const AttnArgs& args, void* workspace, cudaSt
     AttnArgs p = args;
     if (p.n_tokens == 0 || p.seqs.n_seqs == 0) return cudaSuccess;
     p.scale *= attn::kLog2e;
+    if (p.cache.n_pages == 0) {  // copies of no bytes are still given an address
+        p.cache.k = p.cache.v = static_cast<uint8_t*>(workspace);
+        p.cache.k_scale = p.cache.v_scale = static_cast<float*>(workspace);
+        p.cache.head_stride = p.cache.scale_head_stride = 0;
+    }
     p.joined = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
     const size_t part = part_floats(attn::item_rows(p.n_heads / p.cache.n_kv * p.max_new), p.cache.head_dim);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPartsAt);

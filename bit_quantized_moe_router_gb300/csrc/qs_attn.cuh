@@ -75,6 +75,7 @@ struct Plan {
     static constexpr int ST = kFit > 6 ? 6 : kFit;
     static constexpr int kRing = kTeams * ST * kStage;
     static constexpr int kSmem = kQBytes + kRing > kRed ? kQBytes + kRing : kRed;
+    static constexpr int kEnter = 2;
     static constexpr int kPart = RT * (DP + 2);       // floats of an item's part: sums, maxima and sums of weights
     static_assert(ST >= 2 && kSmem + kStatic <= kSmemMax, "shared memory");
     static_assert(kWarps % kTeam == 0 && 32 * kTeam % kChunks == 0 && TP * kChunks % (32 * kTeam) == 0, "copies");
@@ -158,75 +159,81 @@ __device__ __forceinline__ void load_q8(const HeadsView& x, bool aligned, const 
     }
 }
 
-// What a sequence has to do.
+// What a sequence has to do.  Positions are 32-bit numbers near enough to the table's (0 .. positions): a start far outside
+// it is brought so near that its tokens see the same.
 struct Seq {
     int first_token, tokens;  // the new tokens that are attended (max_new at most)
-    int64_t start;            // the first one's position
-    int lo, hi;               // positions that any of them sees
+    int lo_base, hi_base;     // token j sees lo_base + j .. hi_base + j - 1, clipped to the table
+    int lo;                   // the first position that any of them sees
     int tiles, row_tiles;     // of an item; row tiles of a head
-    int64_t work;             // tiles of the whole sequence
 };
-// a / b and a % b, b > 0, a >= 0, in 32 bits where both fit.
+// a / b, b > 0, a >= 0, in 32 bits where both fit.
 __device__ __forceinline__ int64_t div_of(int64_t a, int64_t b) {
     if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
     return a / b;
 }
-__device__ __forceinline__ int clip_pos(int64_t p, int n) { return (int)(p < 0 ? 0 : p > n ? n : p); }
+__device__ __forceinline__ int near_pos(int64_t p, int n) { return (int)(p < -1024 ? -1024 : p > n ? n : p); }
+__device__ __forceinline__ int clip_pos(int p, int n) { return min(max(p, 0), n); }
 
 template <int TP, int RT>
-__device__ __forceinline__ Seq seq_of(const AttnArgs& p, int s, int group) {
+__device__ __forceinline__ Seq seq_of(const AttnArgs& p, int s) {
     Seq q;
     q.first_token = s;
-    int end = s + 1;
+    q.tokens = 1;
     if (p.seqs.offsets) {
         q.first_token = min(max(p.seqs.offsets[s], 0), p.n_tokens);
-        end = min(max(p.seqs.offsets[s + 1], 0), p.n_tokens);
+        q.tokens = min(max(min(p.seqs.offsets[s + 1], p.n_tokens) - q.first_token, 0), p.max_new);
     }
-    q.tokens = min(max(end - q.first_token, 0), p.max_new);
-    q.start = p.seqs.starts ? p.seqs.starts[s] : 0;
-    q.lo = p.window ? clip_pos(q.start - p.window + 1, p.seqs.positions) : 0;
-    q.hi = clip_pos(q.start + q.tokens, p.seqs.positions);
-    q.tiles = max(1, (q.hi + TP - 1) / TP - q.lo / TP);  // one where nothing is seen: its rows are still written
-    q.row_tiles = (q.tokens * group + RT - 1) / RT;
-    q.work = (int64_t)q.tiles * q.row_tiles * p.cache.n_kv;
+    const int64_t start = p.seqs.starts ? p.seqs.starts[s] : 0;
+    const int n = p.seqs.positions;
+    q.lo_base = p.window ? near_pos(start - p.window + 1, n) : -1024;
+    q.hi_base = near_pos(start + 1, n);
+    q.lo = clip_pos(q.lo_base, n);
+    q.tiles = max(1, (clip_pos(q.hi_base + q.tokens - 1, n) + TP - 1) / TP - q.lo / TP);  // one where nothing is seen: its rows are still written
+    q.row_tiles = (q.tokens * p.group + RT - 1) / RT;
     return q;
 }
 
-// An output row's eight columns from col: v is the sum of weighted values, l the sum of weights, m the maximum
-// they are relative to.
-template <int DP>
-__device__ __forceinline__ void finish(const AttnArgs& p, int token, int head, int col, float (&v)[8], float m, float l, bool real) {
+// Four of an output row's columns from col: v is the sum of weighted values, l the sum of weights, m the maximum they are
+// relative to.
+__device__ __forceinline__ void finish(const AttnArgs& p, int token, int head, int col, float (&v)[4], float m, float l, bool real) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int q = 0; q < 8; q++) v[q] = l == 0.0f ? 0.0f : v[q] * inv;
+    for (int q = 0; q < 4; q++) v[q] = l == 0.0f ? 0.0f : v[q] * inv;
     const int d = p.cache.head_dim;
-    if (p.codes) {  // head_dim a multiple of 128: the 16 lanes of a scale's columns are all here
-        float w[1][8];
-#pragma unroll
-        for (int q = 0; q < 8; q++) w[0][q] = v[q];
-        const int i = head * d + col;
-        quant_vec<1>(w, 1.0f, kMinAmax, p.codes + token * p.codes_stride, p.codes_scale + token * p.codes_scale_stride, i, real ? p.n_heads * d : 0);
+    if (p.codes) {  // head_dim a multiple of 128: a warp has a scale's columns
+        const BlockCode code(lanes_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))), 16), 1.0f, kMinAmax);
+        if (real) {
+            const int i = head * d + col;
+            *reinterpret_cast<uint32_t*>(p.codes + token * p.codes_stride + i) = code.pair(v[0], v[1]) | (code.pair(v[2], v[3]) << 16);
+            if (i % kScaleCols == 0) p.codes_scale[token * p.codes_scale_stride + i / kScaleCols] = code.scale;
+        }
     }
     if (!real || col >= d) return;
     if (p.out.data) {
         uint8_t* row = p.out.data + token * p.out.token_stride + head * p.out.head_stride;
-        if (p.out_aligned) {
-            store8_row<true>(row, p.out.dtype, col, d, v);
-        } else {
+        if (!p.out_aligned) {
 #pragma unroll
-            for (int q = 0; q < 8; q++) {
+            for (int q = 0; q < 4; q++) {
                 if (p.out.dtype == QS_BF16) reinterpret_cast<__nv_bfloat16*>(row)[col + q] = __float2bfloat16_rn(v[q]);
                 else reinterpret_cast<float*>(row)[col + q] = v[q];
             }
+        } else if (p.out.dtype == QS_BF16) {
+            *reinterpret_cast<uint2*>(row + 2 * col) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        } else {
+            *reinterpret_cast<float4*>(row + 4 * col) = make_float4(v[0], v[1], v[2], v[3]);
         }
     }
     if (p.lse && col == 0) p.lse[(int64_t)token * p.n_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// The token of an item's row.
+__device__ __forceinline__ int token_of(const AttnArgs& p, int row) { return fast_div(row, p.group_div); }
+
 // An item's rows from the registers of the warps that have all their positions.  most: the warps' largest values by row, for
 // the codes of 128 columns that two warps have.
 template <class P>
-__device__ __forceinline__ void finish_rows(const AttnArgs& p, const Seq& seq, int kv, int w0, int rows, int group, const float (&top)[P::NT], const float (&sum)[P::NT],
+__device__ __forceinline__ void finish_rows(const AttnArgs& p, const Seq& seq, int kv, int w0, int rows, const float (&top)[P::NT], const float (&sum)[P::NT],
                                             float (&acc)[P::kCols / 64][4][P::NT][4], float (*most)[8 * P::NT], int team) {
     constexpr int NT = P::NT, kJ = P::kCols / 64;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, d = p.cache.head_dim;
@@ -236,7 +243,7 @@ __device__ __forceinline__ void finish_rows(const AttnArgs& p, const Seq& seq, i
         const float inv = sum[nt] == 0.0f ? 0.0f : 1.0f / sum[nt];
         const int own = w0 + nt * 8 + g;
         if (p.lse && t == 0 && col0 == 0 && own < rows)
-            p.lse[(int64_t)(seq.first_token + own / group) * p.n_heads + kv * group + own % group] = sum[nt] == 0.0f ? -INFINITY : (top[nt] + log2f(sum[nt])) * kLn2;
+            p.lse[(int64_t)(seq.first_token + token_of(p, own)) * p.n_heads + kv * p.group + (own - token_of(p, own) * p.group)] = sum[nt] == 0.0f ? -INFINITY : (top[nt] + log2f(sum[nt])) * kLn2;
 #pragma unroll
         for (int e = 0; e < 2; e++) {
             const float by = __shfl_sync(0xffffffffu, inv, 8 * t + 4 * e);
@@ -270,8 +277,8 @@ __device__ __forceinline__ void finish_rows(const AttnArgs& p, const Seq& seq, i
         for (int e = 0; e < 2; e++) {
             const int row = w0 + nt * 8 + 2 * t + e;
             const bool real = row < rows;
-            const int64_t token = seq.first_token + row / group;
-            const int head = kv * group + row % group;
+            const int at = token_of(p, row), head = kv * p.group + row - at * p.group;
+            const int64_t token = seq.first_token + at;
             auto columns = [&](int jj, float (&v)[8]) {
 #pragma unroll
                 for (int q = 0; q < 8; q++) v[q] = acc[jj][q / 2][nt][q % 2 * 2 + e];
@@ -324,16 +331,17 @@ __device__ __forceinline__ void finish_rows(const AttnArgs& p, const Seq& seq, i
         }
 }
 
-// What a team has of an item that is not whole in its run: the item's first tile in the line (-1: nothing), and which.
+// What a team has of an item that is not whole in its run: where the item begins in the line (-1: nothing), and which.
 struct Piece {
-    int64_t item0;
+    int64_t at;
     int seq, item;
 };
-// A tile in the ring: positions that are there, the first one, and where it lies in its item and the team's run.
+// A tile in the ring: positions that are there, the first one, and whether it is the first or last of a stretch (the item's
+// or the run's); the item, the tile's number in it, and where it begins in the line, from the run's start.
 struct Tile {
     unsigned there;
-    int pos0, first, last;  // first and last of a stretch: the item's or the run's
-    int seq, item, tile, tiles;
+    int pos0, first, last;
+    int seq, item, tile, at;
 };
 
 // What a part with maximum ml.x counts beside the maximum m; one of no positions (-infinity, 0) nothing.
@@ -353,7 +361,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     __shared__ bool last_of[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int team = warp / P::kTeam, team_tid = tid % (32 * P::kTeam), row_warp = warp % P::kTeam / P::C, col_warp = warp % P::C;
-    const int group = p.n_heads / p.cache.n_kv, d = p.cache.head_dim;
+    const int d = p.cache.head_dim;
     uint8_t* const q_shared = smem + warp * (P::kQBytes / kWarps) + lane * 16;
     uint8_t* const ring = smem + P::kQBytes + team * ST * P::kStage;
     float* const red = reinterpret_cast<float*>(smem);
@@ -361,11 +369,13 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     pdl_wait();
     pdl_launch_next();
 
-    // ---- the CTA's run of tiles, the team's share of it [cur, end), and the sequence that this begins in
+    // ---- the CTA's run of the line [run0, run1), the team's share of it, and the sequence that this begins in.  An item
+    // takes kEnter places before its tiles', about what entering and leaving it costs.
     const int per = (p.seqs.n_seqs + kThreads - 1) / kThreads;
     const int s0 = min(tid * per, p.seqs.n_seqs), s1 = min(s0 + per, p.seqs.n_seqs);
+    auto places_of = [&](const Seq& q) { return (int64_t)(q.tiles + P::kEnter) * (q.row_tiles * p.cache.n_kv); };
     int64_t mine = 0;
-    for (int s = s0; s < s1; s++) mine += seq_of<TP, RT>(p, s, group).work;
+    for (int s = s0; s < s1; s++) mine += places_of(seq_of<TP, RT>(p, s));
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -373,7 +383,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
         if (lane >= o) upto += x;
     }
     if (lane == 31) scan[warp] = upto;
-    if (tid < 2 * P::kTeams) piece_of[tid].item0 = -1;
+    if (tid < 2 * P::kTeams) piece_of[tid].at = -1;
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
@@ -381,25 +391,28 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
         if (w < warp) upto += scan[w];
         total += scan[w];
     }
-    // as many CTAs as have a tile for each team
-    const int64_t workers = min((int64_t)gridDim.x, (total + P::kTeams - 1) / P::kTeams);
+    // as many CTAs as have an item's first tile for each team
+    const int64_t workers = min((int64_t)gridDim.x, div_of(total - 1, P::kTeams * (P::kEnter + 1)) + 1);
     const int c = blockIdx.x;
-    if (c >= workers) return;
-    // equal runs, the first of them a tile longer
+    if (total == 0 || c >= workers) return;
+    // equal runs, the first of them a place longer
     const int64_t each = div_of(total, workers), longer = total - each * workers;
     const int64_t run0 = c * each + min((int64_t)c, longer), run1 = run0 + each + (c < longer);
-    auto cta_of = [&](int64_t tile) {  // the CTA whose run has it
+    auto cta_of = [&](int64_t place) {  // the CTA whose run has it
         const int64_t split = longer * (each + 1);
-        return (int)(tile < split ? div_of(tile, each + 1) : longer + div_of(tile - split, each));
+        return (int)(place < split ? div_of(place, each + 1) : longer + div_of(place - split, each));
     };
-    auto begin_of = [&](int x) { return run0 + (run1 - run0) * x / P::kTeams; };
-    for (int w = 0; w < P::kTeams; w++) {
-        const int64_t from = begin_of(w);
-        if (from >= upto - mine && from < upto) {
+    const unsigned length = (unsigned)(run1 - run0);
+    auto begin_of = [&](unsigned x) { return length / P::kTeams * x + length % P::kTeams * x / P::kTeams; };
+    // the threads whose sequences the teams begin in say so
+    if (upto > run0 && upto - mine < run1) {
+        for (unsigned w = 0; w < P::kTeams; w++) {
+            const int64_t from = run0 + begin_of(w);
+            if (from < upto - mine || from >= upto) continue;
             int64_t base = upto - mine;
             int s = s0;
             for (; s + 1 < s1; s++) {
-                const int64_t x = seq_of<TP, RT>(p, s, group).work;
+                const int64_t x = places_of(seq_of<TP, RT>(p, s));
                 if (from < base + x) break;
                 base += x;
             }
@@ -408,91 +421,111 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
         }
     }
     __syncthreads();
-    const int64_t cur = begin_of(team);
-    const int run = (int)(begin_of(team + 1) - cur);
+    const int64_t from = run0 + begin_of(team);
 
-    // ---- copies: the next tile's place, kept for all warps of a team alike
+    // ---- copies: the next tile's place, kept by all warps of a team alike
     struct {
-        int seq, item, items, tile, tiles, left, base_pos, lo, hi, kv;
+        int seq, item, items, kv, tile, tiles, left, base_pos, lo, hi, at;
+        bool first;
+        const uint8_t *k, *v;
     } next = {};
+    int issued = 0;
     Place ahead = {-1, -1};
-    auto hi_of = [&](const Seq& q, int token) { return clip_pos(q.start + token + 1, p.seqs.positions); };
-    auto lo_of = [&](const Seq& q, int token) { return p.window ? clip_pos(q.start + token + 1 - p.window, p.seqs.positions) : 0; };
+    auto hi_of = [&](const Seq& q, int token) { return clip_pos(q.hi_base + token, p.seqs.positions); };
+    auto lo_of = [&](const Seq& q, int token) { return clip_pos(q.lo_base + token, p.seqs.positions); };
+    // an item's key-value head and first row
+    auto rows_of = [&](const Seq& q, int item, int& kv, int& row0) {
+        kv = item;
+        row0 = 0;
+        if (q.row_tiles != 1) {
+            kv = item / q.row_tiles;
+            row0 = (item - kv * q.row_tiles) * RT;
+        }
+    };
+    const int chunk = team_tid % NC, chunk_row = team_tid / NC;
+    const bool chunk_in = chunk * 16 < d * (E4 ? 1 : 2);
     auto enter = [&](const Seq& q) {
+        int row0;
+        rows_of(q, next.item, next.kv, row0);
         next.items = q.row_tiles * p.cache.n_kv;
         next.tiles = q.tiles;
         next.base_pos = q.lo / TP * TP;
-        next.kv = next.item / q.row_tiles;
-        const int row0 = next.item % q.row_tiles * RT, rows = q.tokens * group;
-        next.lo = lo_of(q, row0 / group);
-        next.hi = hi_of(q, (min(row0 + RT, rows) - 1) / group);
+        next.lo = lo_of(q, token_of(p, row0));
+        next.hi = hi_of(q, token_of(p, min(row0 + RT, q.tokens * p.group) - 1));
+        next.k = p.cache.k + next.kv * p.cache.head_stride + (chunk_in ? chunk * 16 : 0);
+        next.v = p.cache.v + next.kv * p.cache.head_stride + (chunk_in ? chunk * 16 : 0);
     };
     auto look = [&]() {
         const int pos = next.base_pos + next.tile * TP + lane % TP;
         ahead = Place{-1, -1};
         if (next.left > 0 && pos >= next.lo && pos < next.hi) ahead = place_of(p.cache, p.seqs, next.seq, pos);
     };
-    next.left = run;
+    const int run = (int)(begin_of(team + 1) - begin_of(team));
     if (run > 0) {
         next.seq = found_seq[team];
-        Seq q = seq_of<TP, RT>(p, next.seq, group);
-        const int64_t in = cur - found_base[team];
-        next.item = (int)div_of(in, q.tiles);
-        next.tile = (int)(in - (int64_t)next.item * q.tiles);
+        const Seq q = seq_of<TP, RT>(p, next.seq);
+        const int64_t in = from - found_base[team];
+        next.item = (int)div_of(in, q.tiles + P::kEnter);
+        const int place = (int)(in - (int64_t)next.item * (q.tiles + P::kEnter));
+        next.tile = max(0, place - P::kEnter);
+        next.left = run - max(0, P::kEnter - place);
+        next.at = -place;
+        next.first = true;
         enter(q);
         look();
     }
     auto issue = [&](int i) {
         if (next.left > 0) {
             const int stage = i % ST;
-            uint8_t* const keys = ring + stage * P::kStage;
             const unsigned there = __ballot_sync(0xffffffffu, ahead.at >= 0);
-            if (lane == 0)
-                tile_of[warp][stage] = Tile{there, next.base_pos + next.tile * TP, next.left == run || next.tile == 0, next.left == 1 || next.tile + 1 == next.tiles,
-                                            next.seq, next.item, next.tile, next.tiles};
-            const uint32_t to = smem_u32(keys);
-            const uint8_t* const nothing = reinterpret_cast<const uint8_t*>(p.joined);  // the source of a copy of 0 bytes
-            const uint8_t* const k_base = p.cache.k + next.kv * p.cache.head_stride;
-            const uint8_t* const v_base = p.cache.v + next.kv * p.cache.head_stride;
-            const int chunk = team_tid % NC;
-            const bool in = chunk * 16 < d * (E4 ? 1 : 2);
+            const bool ends = next.tile + 1 == next.tiles;
+            if (lane == 0) tile_of[warp][stage] = Tile{there, next.base_pos + next.tile * TP, next.first, ends || next.left == 1, next.seq, next.item, ends ? -1 - next.tile : next.tile, next.at};
+            const uint32_t to = smem_u32(ring + stage * P::kStage);
 #pragma unroll
             for (int k = 0; k < TP * NC / (32 * P::kTeam); k++) {
-                const int row = team_tid / NC + k * (32 * P::kTeam / NC);
+                const int row = chunk_row + k * (32 * P::kTeam / NC);
                 const int64_t at = __shfl_sync(0xffffffffu, ahead.at, row);
-                const bool ok = at >= 0 && in;
-                const int64_t from = at + chunk * 16;
-                cp16(to + row * P::kRowBytes + ((chunk ^ (NC >= 8 ? (row & 1) * 4 : 0)) * 16), ok ? k_base + from : nothing, ok);
-                cp16(to + (TP + row) * P::kRowBytes + ((chunk ^ (((row >> 1) & 3) * 2 & (NC - 1))) * 16), ok ? v_base + from : nothing, ok);
+                const bool ok = at >= 0 && chunk_in;
+                const int64_t from_base = ok ? at : 0;
+                cp16(to + row * P::kRowBytes + ((chunk ^ (NC >= 8 ? (row & 1) * 4 : 0)) * 16), next.k + from_base, ok);
+                cp16(to + (TP + row) * P::kRowBytes + ((chunk ^ (((row >> 1) & 3) * 2 & (NC - 1))) * 16), next.v + from_base, ok);
             }
             if (E4 && warp % P::kTeam == 0 && lane < TP) {
                 const bool ok = ahead.at >= 0;
-                const int64_t from = ahead.scale_at + next.kv * p.cache.scale_head_stride;
-                cp4(to + 2 * TP * P::kRowBytes + lane * 4, ok ? p.cache.k_scale + from : reinterpret_cast<const float*>(nothing), ok);
-                cp4(to + 2 * TP * P::kRowBytes + (TP + lane) * 4, ok ? p.cache.v_scale + from : reinterpret_cast<const float*>(nothing), ok);
+                const int64_t from_base = ok ? ahead.scale_at + next.kv * p.cache.scale_head_stride : 0;
+                cp4(to + 2 * TP * P::kRowBytes + lane * 4, p.cache.k_scale + from_base, ok);
+                cp4(to + 2 * TP * P::kRowBytes + (TP + lane) * 4, p.cache.v_scale + from_base, ok);
             }
+            issued++;
             next.left--;
-            if (++next.tile == next.tiles && next.left > 0) {
-                next.tile = 0;
-                if (++next.item == next.items) {
-                    next.item = 0;
+            next.tile++;
+            next.first = ends;
+            if (ends) {
+                next.left -= P::kEnter;
+                if (next.left > 0) {
+                    next.at += next.tiles + P::kEnter;
+                    next.tile = 0;
                     Seq q;
-                    do {
-                        next.seq = min(next.seq + 1, p.seqs.n_seqs - 1);
-                        q = seq_of<TP, RT>(p, next.seq, group);
-                    } while (q.work == 0 && next.seq + 1 < p.seqs.n_seqs);
+                    if (++next.item == next.items) {
+                        next.item = 0;
+                        do {
+                            next.seq = min(next.seq + 1, p.seqs.n_seqs - 1);
+                            q = seq_of<TP, RT>(p, next.seq);
+                        } while (q.tokens == 0 && next.seq + 1 < p.seqs.n_seqs);
+                    } else {
+                        q = seq_of<TP, RT>(p, next.seq);
+                    }
                     enter(q);
-                } else {
-                    enter(seq_of<TP, RT>(p, next.seq, group));
                 }
             }
             look();
         }
         cp_commit();
     };
+
     // ---- the pass over the run's tiles
     Seq seq = {};
-    int item = 0, kv = 0, w0 = 0, rows = 0, token0 = 0, token1 = 0, all_lo = 0, all_hi = 0, tile_lo = 0, tile_hi = 0, tile0 = 0;
+    int kv = 0, w0 = 0, rows = 0, token0 = 0, token1 = 0, all_lo = 0, all_hi = 0, tile_lo = 0, tile_hi = 0, tile0 = 0;
     bool active = false;
     uint32_t qf[P::kQInRegs ? P::kSteps : 1][P::kQInRegs ? P::kQEach : 1];
     float row_scale[NT];
@@ -501,19 +534,17 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
 
     // an item's rows: queries as fragments in the order in which the keys' pieces lie
     auto begin = [&](const Tile& x) {
-        seq = seq_of<TP, RT>(p, x.seq, group);
-        item = x.item;
-        tile0 = x.tile;
-        kv = item / seq.row_tiles;
-        rows = seq.tokens * group;
-        const int row0 = item % seq.row_tiles * RT;
-        tile_lo = lo_of(seq, row0 / group);
-        tile_hi = hi_of(seq, (min(row0 + RT, rows) - 1) / group);
+        seq = seq_of<TP, RT>(p, x.seq);
+        tile0 = x.tile < 0 ? -1 - x.tile : x.tile;
+        int row0;
+        rows_of(seq, x.item, kv, row0);
+        rows = seq.tokens * p.group;
+        tile_lo = lo_of(seq, token_of(p, row0));
+        tile_hi = hi_of(seq, token_of(p, min(row0 + RT, rows) - 1));
         w0 = row0 + row_warp * P::kRows;
-        const int w1 = min(w0 + P::kRows, rows);
         active = w0 < rows;
-        token0 = w0 / group;
-        token1 = max(w1 - 1, w0) / group;
+        token0 = token_of(p, w0);
+        token1 = max(token_of(p, max(min(w0 + P::kRows, rows) - 1, 0)), token0);
         all_lo = lo_of(seq, token1);
         all_hi = hi_of(seq, token0);
 #pragma unroll
@@ -521,13 +552,49 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             top[nt] = -INFINITY;
             sum[nt] = 0.0f;
             const int row = w0 + nt * 8 + g;
-            const uint8_t* q = row < rows ? p.q.data + (seq.first_token + row / group) * p.q.token_stride + (kv * group + row % group) * p.q.head_stride : nullptr;
+            const int at = token_of(p, row);
+            const uint8_t* q = row < rows ? p.q.data + (seq.first_token + at) * p.q.token_stride + (kv * p.group + row - at * p.group) * p.q.head_stride : nullptr;
+            row_scale[nt] = p.scale;
+            if constexpr (!E4 && !P::WIDE) {  // bf16 as it lies, by the rule below
+                uint4 raw[DP / 32];
+#pragma unroll
+                for (int i = 0; i < DP / 32; i++) {
+                    const int col = 32 * i + 8 * t;
+                    raw[i] = make_uint4(0, 0, 0, 0);
+                    if (!q || col >= d) continue;
+                    if (p.q_aligned) {
+                        raw[i] = *reinterpret_cast<const uint4*>(q + 2 * col);
+                    } else {
+                        const uint16_t* e = reinterpret_cast<const uint16_t*>(q) + col;
+                        raw[i] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < DP / 32; i++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t x0 = h ? raw[i].z : raw[i].x, x1 = h ? raw[i].w : raw[i].y;
+                        constexpr int kE = P::kQInRegs ? P::kQEach : 1;
+                        if (P::kQInRegs) {
+                            uint32_t(&to)[kE] = qf[(2 * i + h) % (P::kQInRegs ? P::kSteps : 1)];
+                            to[nt % kE] = x0;
+                            to[(NT + nt) % kE] = x1;
+                        } else {
+                            uint32_t* shared = reinterpret_cast<uint32_t*>(q_shared + (2 * i + h) * 512);
+                            if (NT == 1) {
+                                *reinterpret_cast<uint4*>(shared) = make_uint4(x0, 0u, x1, 0u);
+                            } else {
+                                shared[nt] = x0;
+                                shared[2 + nt] = x1;
+                            }
+                        }
+                    }
+            } else {
             // bf16: piece i is columns 32 i + 8 t .. + 7, two steps of four; e4m3: 64 i + 16 t .. + 15, four steps
             float v[DP / 32][8];
 #pragma unroll
             for (int i = 0; i < DP / 32; i++) load_q8(p.q, p.q_aligned, q, E4 ? 64 * (i / 2) + 16 * t + 8 * (i % 2) : 32 * i + 8 * t, d, v[i]);
             float factor = 1.0f;
-            row_scale[nt] = p.scale;
             if (E4) {  // a power of two that brings the row's largest into fp16's upper range
                 float a = 0.0f;
 #pragma unroll
@@ -581,6 +648,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                         }
                     }
                 }
+            }
         }
 #pragma unroll
         for (int jj = 0; jj < kJ; jj++)
@@ -624,7 +692,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
         }
     };
 
-    for (int i = 1 - ST; i < run; i++) {
+    for (int i = 1 - ST; i < 0 || i < issued; i++) {  // tile i is consumed, tile i + ST - 1 copied
         const int stage = i < 0 ? 0 : i % ST;
         const Tile& x = tile_of[warp][stage];
         if (i >= 0) {
@@ -683,7 +751,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             if (!full) {
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
-                    const int token = (w0 + nt * 8 + g) / group;
+                    const int token = token_of(p, w0 + nt * 8 + g);
                     const int lo = lo_of(seq, token), hi = hi_of(seq, token);
 #pragma unroll
                     for (int n8 = 0; n8 < TP / 8; n8++)
@@ -828,11 +896,11 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
 #pragma unroll
                                     for (int pl = 0; pl < P::PP; pl++) mma<E4>(one, a[0], a[1], a[2], a[3], pb[kk][nt][pl][0], pb[kk][nt][pl][1]);
                                     const int row = w0 + nt * 8 + 2 * t;
-                                    if (row / group == token) {
+                                    if (token_of(p, row) == token) {
                                         acc[jj][m][nt][0] += one[0];
                                         acc[jj][m][nt][2] += one[2];
                                     }
-                                    if ((row + 1) / group == token) {
+                                    if (token_of(p, row + 1) == token) {
                                         acc[jj][m][nt][1] += one[1];
                                         acc[jj][m][nt][3] += one[3];
                                     }
@@ -850,12 +918,12 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             sum[nt] += __shfl_xor_sync(0xffffffffu, sum[nt], 1);
             sum[nt] += __shfl_xor_sync(0xffffffffu, sum[nt], 2);
         }
-        const bool ends = x.tile + 1 == x.tiles;
+        const bool ends = x.tile < 0;
         if (tile0 == 0 && ends) {
-            finish_rows<P>(p, seq, kv, w0, rows, group, top, sum, acc, most_of, team);
+            finish_rows<P>(p, seq, kv, w0, rows, top, sum, acc, most_of, team);
             continue;
         }
-        if (team_tid == 0) piece_of[2 * team + !ends] = Piece{cur + i - x.tile, x.seq, item};
+        if (team_tid == 0) piece_of[2 * team + !ends] = Piece{from + x.at, x.seq, x.item};
         if (ends) {
             float* to = p.heads + (c * P::kTeams + team) * P::kPart;
             put(to, DP, reinterpret_cast<float2*>(to + RT * DP));
@@ -863,87 +931,85 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     }
     cp_wait<0>();
     __syncthreads();  // the ring is free
-    if (piece_of[2 * team + 1].item0 >= 0) put(red + team * RT * (DP + 4), DP + 4, red_ml + team * RT);
+    if (piece_of[2 * team + 1].at >= 0) put(red + team * RT * (DP + 4), DP + 4, red_ml + team * RT);
     __syncthreads();
 
     // ---- what the teams have of the same item, and then the CTAs: the warps are dealt to the items
-    const int64_t my_item0 = lane < 2 * P::kTeams ? piece_of[lane].item0 : -1;
-    const unsigned pieces = __ballot_sync(0xffffffffu, my_item0 >= 0);
+    const int64_t my_at = lane < 2 * P::kTeams ? piece_of[lane].at : -1;
+    const unsigned pieces = __ballot_sync(0xffffffffu, my_at >= 0);
     const unsigned before = pieces & ((1u << lane) - 1u);
-    const int64_t item_before = __shfl_sync(0xffffffffu, my_item0, before ? 31 - __clz(before) : 0);
-    unsigned starts = __ballot_sync(0xffffffffu, my_item0 >= 0 && (!before || item_before != my_item0));
+    const int64_t at_before = __shfl_sync(0xffffffffu, my_at, before ? 31 - __clz(before) : 0);
+    unsigned starts = __ballot_sync(0xffffffffu, my_at >= 0 && (!before || at_before != my_at));
     const int items = __popc(starts);
     if (items == 0) return;
     const int crews = min(items, kWarps), size = kWarps / crews, crew = warp / size, crew_tid = tid - crew * size * 32;
     if (crew >= crews) return;
     for (int n = 0; n < items; n++, starts &= starts - 1u) {
         if (n % crews != crew) continue;
-        const int i0 = __ffs(starts) - 1, i1 = starts & (starts - 1u) ? __ffs(starts & (starts - 1u)) - 1 : 2 * P::kTeams;
-        const int64_t item0 = piece_of[i0].item0;
-        const Seq q = seq_of<TP, RT>(p, piece_of[i0].seq, group);
-        const int head = piece_of[i0].item / q.row_tiles * group, row0 = piece_of[i0].item % q.row_tiles * RT, n_rows = q.tokens * group;
-        const bool whole = item0 >= run0 && item0 + q.tiles <= run1;
-        const int c0 = whole ? c : cta_of(item0), c1 = whole ? c : cta_of(item0 + q.tiles - 1);
+        const int i0 = __ffs(starts) - 1;
+        const unsigned later = starts & (starts - 1u), of_item = pieces & ~((1u << i0) - 1u) & (later ? (later & (0u - later)) - 1u : 0xffffffffu);
+        const Seq q = seq_of<TP, RT>(p, piece_of[i0].seq);
+        int kv, row0;
+        rows_of(q, piece_of[i0].item, kv, row0);
+        const int n_rows = q.tokens * p.group;
+        const int64_t tiles0 = piece_of[i0].at + P::kEnter, tiles1 = tiles0 + q.tiles;
+        const bool whole = tiles0 >= run0 && tiles1 <= run1;
+        const int c0 = whole ? c : cta_of(tiles0), c1 = whole ? c : cta_of(tiles1 - 1);
         // CTAs c0 .. c1 have the item; the first kFan of them, the next kFan and so on are joined first
         const int sub = (c - c0) / kFan, first = c0 + sub * kFan, many = min(kFan, c1 - first + 1), subs = (c1 - c0) / kFan + 1;
         for (int level = 0;; level++) {
-            // part i of this level: of the teams, of CTAs, of kFan CTAs
-            const int lo = level == 0 ? i0 : 0, hi = level == 0 ? i1 : level == 1 ? many : subs;
-            auto part_at = [&](int i) -> const float* {
-                if (level == 0) return p.heads + (c * P::kTeams + i / 2) * P::kPart;
-                if (level == 1) return p.parts + ((first + i) * 2 + (first + i == c0)) * P::kPart;
-                return p.merged + ((c0 + i * kFan) * 2 + (i == 0)) * P::kPart;
-            };
+            // the parts: of the teams, of CTAs, of kFan CTAs
             const bool done = whole || level == 2 || (level == 1 && subs == 1);
-            for (int x = crew_tid; x < (RT * DP / 8 + 31) / 32 * 32; x += size * 32) {  // eight columns of a row a thread
-                const int row = x / (DP / 8), col = x % (DP / 8) * 8;
-                float m = -INFINITY, l = 0.0f, v[8];
+            for (int x = crew_tid; x < RT * DP / 4; x += size * 32) {  // four columns of a row a thread
+                const int row = x / (DP / 4), col = x % (DP / 4) * 4;
+                unsigned rest = level == 0 ? of_item : (1u << (level == 1 ? many : subs)) - 1u;
+                float m = -INFINITY, l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                constexpr int kBatch = 6;  // parts on their way at once
+                while (rest) {
+                    float2 ml[kBatch];
+                    float4 a[kBatch];
 #pragma unroll
-                for (int e = 0; e < 8; e++) v[e] = 0.0f;
-                for (int at = lo; at < hi; at += 4) {
-                    float2 ml[4];
-                    float4 a[4], b[4];
-#pragma unroll
-                    for (int y = 0; y < 4; y++) {
-                        const int i = at + y;
+                    for (int y = 0; y < kBatch; y++) {
+                        const int i = __ffs(rest) - 1;
+                        rest &= rest - 1u;
                         ml[y] = make_float2(-INFINITY, 0.0f);
-                        a[y] = b[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (i >= hi || (level == 0 && !((pieces >> i) & 1u))) continue;
+                        a[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (i < 0) continue;
                         if (level == 0 && i % 2) {
                             ml[y] = red_ml[i / 2 * RT + row];
-                            const float4* from = reinterpret_cast<const float4*>(red + (i / 2 * RT + row) * (DP + 4) + col);
-                            a[y] = from[0];
-                            b[y] = from[1];
+                            a[y] = *reinterpret_cast<const float4*>(red + (i / 2 * RT + row) * (DP + 4) + col);
                         } else {
-                            const float* part = part_at(i);
+                            const float* part = level == 0   ? p.heads + (c * P::kTeams + i / 2) * P::kPart
+                                                : level == 1 ? p.parts + ((first + i) * 2 + (first + i == c0)) * P::kPart
+                                                             : p.merged + ((c0 + i * kFan) * 2 + (i == 0)) * P::kPart;
                             ml[y] = __ldcg(reinterpret_cast<const float2*>(part + RT * DP) + row);
-                            const float4* from = reinterpret_cast<const float4*>(part + row * DP + col);
-                            a[y] = __ldcg(from);
-                            b[y] = __ldcg(from + 1);
+                            a[y] = __ldcg(reinterpret_cast<const float4*>(part + row * DP + col));
                         }
                     }
-                    const float now = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+                    float now = m;
+#pragma unroll
+                    for (int y = 0; y < kBatch; y++) now = fmaxf(now, ml[y].x);
                     const float by = part_factor(make_float2(m, l), now);
                     m = now;
                     l *= by;
 #pragma unroll
-                    for (int e = 0; e < 8; e++) v[e] *= by;
+                    for (int e = 0; e < 4; e++) v[e] *= by;
 #pragma unroll
-                    for (int y = 0; y < 4; y++) {
+                    for (int y = 0; y < kBatch; y++) {
                         const float f = part_factor(ml[y], m);
                         l += f * ml[y].y;
-                        v[0] += f * a[y].x; v[1] += f * a[y].y; v[2] += f * a[y].z; v[3] += f * a[y].w;
-                        v[4] += f * b[y].x; v[5] += f * b[y].y; v[6] += f * b[y].z; v[7] += f * b[y].w;
+                        v[0] += f * a[y].x;
+                        v[1] += f * a[y].y;
+                        v[2] += f * a[y].z;
+                        v[3] += f * a[y].w;
                     }
                 }
                 if (done) {
-                    const int r = row0 + row;
-                    finish<DP>(p, q.first_token + r / group, head + r % group, col, v, m, l, r < n_rows);
+                    const int r = row0 + row, token = token_of(p, r);
+                    finish(p, q.first_token + token, kv * p.group + r - token * p.group, col, v, m, l, r < n_rows);
                 } else {
                     float* to = level == 0 ? p.parts + (c * 2 + (c == c0)) * P::kPart : p.merged + (first * 2 + (first == c0)) * P::kPart;
-                    float4* o = reinterpret_cast<float4*>(to + row * DP + col);
-                    __stcg(o, make_float4(v[0], v[1], v[2], v[3]));
-                    __stcg(o + 1, make_float4(v[4], v[5], v[6], v[7]));
+                    __stcg(reinterpret_cast<float4*>(to + row * DP + col), make_float4(v[0], v[1], v[2], v[3]));
                     if (col == 0) __stcg(reinterpret_cast<float2*>(to + RT * DP) + row, make_float2(m, l));
                 }
             }

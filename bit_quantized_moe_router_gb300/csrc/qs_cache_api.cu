@@ -76,6 +76,13 @@ HeadsView view(const qs_heads& x) {
     return {static_cast<uint8_t*>(x.data), x.token_stride * z, x.head_stride * z, x.dtype};
 }
 
+FastDiv fast_div_by(int d) {
+    FastDiv f = {0, 31};
+    while ((1ll << (f.shift - 31)) < d) f.shift++;
+    f.mul = (uint32_t)(((1ull << f.shift) + d - 1) / d);
+    return f;
+}
+
 CacheView view(const qs_cache& c) {
     const int64_t z = type_size(c.dtype);
     CacheView v = {};
@@ -89,9 +96,7 @@ CacheView view(const qs_cache& c) {
     v.scale_page_stride = c.scale_page_stride;
     v.scale_slot_stride = c.scale_slot_stride;
     v.scale_head_stride = c.scale_head_stride;
-    v.page_div.shift = 31;
-    while ((1ll << (v.page_div.shift - 31)) < c.page_size) v.page_div.shift++;
-    v.page_div.mul = (uint32_t)(((1ull << v.page_div.shift) + c.page_size - 1) / c.page_size);
+    v.page_div = fast_div_by(c.page_size);
     v.dtype = c.dtype;
     v.n_pages = c.n_pages;
     v.page_size = c.page_size;
@@ -178,6 +183,8 @@ int qs_cache_attention(const qs_cache_attention_args* args, void* stream) {
     p.n_tokens = n;
     p.n_heads = h;
     p.max_new = a.max_new;
+    p.group = h / kv;
+    p.group_div = fast_div_by(p.group);
     p.window = a.window;
     return done(launch_cache_attention(p, a.workspace, (cudaStream_t)stream));
 }

@@ -253,6 +253,8 @@ struct AttnArgs {
     int64_t codes_stride, codes_scale_stride;
     float scale;       // of the scores, times log2(e)
     int n_tokens, n_heads, max_new, window;
+    FastDiv group_div;  // by group, the query heads of a key-value head
+    int group;
     bool q_aligned, out_aligned;
     uint32_t* joined;  // workspace: three counters a CTA, and the parts of items that several teams or CTAs share
     float *parts, *merged, *heads;
