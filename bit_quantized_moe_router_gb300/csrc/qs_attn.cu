@@ -8,7 +8,7 @@ namespace qs {
 // CTAs' are joined first, and one a team (of the item that its run begins inside).
 static constexpr size_t kPartsAt = kHeaderBytes + (3 * kAttnMaxCtas * 4 + 255) / 256 * 256;
 
-static size_t part_floats(const int rows, int head_dim) { return (size_t)rows * (attn::padded_dim(head_dim) + 2); }
+static size_t part_floats(const int rows, int head_dim) { return (size_t)rows * (attn::padded_dim(head_dim) + 6); }
 
 size_t attn_workspace(int n_heads, int n_kv, int head_dim, int max_new) {
     const int rows = attn::item_rows(n_heads / n_kv * max_new);

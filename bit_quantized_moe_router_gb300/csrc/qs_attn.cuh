@@ -54,32 +54,32 @@ constexpr int kStatic = 7 * 1024;  // shared memory for tables
 // A kernel's sizes: cache type, columns (head_dim rounded up), 8 rows times NT a warp, teams of R warps with rows of their
 // own times C with columns of their own, W warps a CTA, and whether queries and weights go into the products with all
 // their parts.
-template <bool E4_, int DP_, int NT_, int R_, int C_, int W_, bool WIDE_>
+template <bool E4_, int DP_, int NT_, int R_, int C_, int W_, int TP_, bool WIDE_>
 struct Plan {
     static constexpr bool E4 = E4_, WIDE = WIDE_;
     static constexpr int DP = DP_, NT = NT_, R = R_, C = C_, kWarps = W_;
     static constexpr int kRowBytes = DP * (E4 ? 1 : 2), kChunks = kRowBytes / 16;
     static constexpr int kTeam = R * C, kTeams = kWarps / kTeam, kRows = 8 * NT, RT = R * kRows, kCols = DP / C;
-    static constexpr int TP = kRowBytes <= 64 || (R == 4 && kRowBytes <= 256) ? 32 : 16;
+    static constexpr int TP = TP_;
     static constexpr int kStage = 2 * TP * kRowBytes + (E4 ? 2 * TP * 4 : 0);  // keys, values, their scales
     static constexpr int QP = WIDE ? (E4 ? 2 : 3) : 1, PP = WIDE ? (E4 ? 2 : 3) : (E4 ? 1 : 2);
     static constexpr int kSteps = DP / 16;            // of the first product
-    // The queries' fragments.  NT = 1: two parts share one, the second in the rows 8..15, which are empty.  In registers
-    // where they fit beside the sums and about 80 others, else in shared memory.
-    static constexpr int kQAll = NT == 1 ? (QP + 1) / 2 : QP;        // fragments of a step
-    static constexpr int kQEach = NT == 1 ? 2 * QP : 4 * QP;         // registers of a step
+    // The queries' fragments: in registers where they fit beside the sums and about 80 others, else in shared memory.
+    static constexpr int kQEach = 2 * NT * QP;         // registers of a step
     static constexpr bool kQInRegs = kQEach * kSteps <= 65536 / (32 * kWarps) - 80 - kCols * NT / 4;
-    static constexpr int kQBytes = kQInRegs ? 0 : kWarps * kQAll * kSteps * 32 * 16;
-    static constexpr int kRed = kTeams * RT * (DP + 4) * 4 + kTeams * RT * 8;  // the teams' results, over all of it
+    static constexpr int kQBytes = kQInRegs ? 0 : kWarps * QP * NT * kSteps * 32 * 8;
+    static constexpr int kPieces = kCols / 16;         // of the output: 16 columns of a warp's rows
+    static constexpr int kRow = DP + 4, kPart = RT * (kRow + 2);  // floats of an item's part: rows of sums, maxima and sums of weights
+    static constexpr int kRed = kTeams * kPart * 4;  // the teams' parts, over all of it
     static constexpr int kFit = (kSmemMax - kStatic - kQBytes) / (kTeams * kStage);
     static constexpr int ST = kFit > 6 ? 6 : kFit;
     static constexpr int kRing = kTeams * ST * kStage;
     static constexpr int kSmem = kQBytes + kRing > kRed ? kQBytes + kRing : kRed;
     static constexpr int kEnter = 2;
-    static constexpr int kPart = RT * (DP + 2);       // floats of an item's part: sums, maxima and sums of weights
     static_assert(ST >= 2 && kSmem + kStatic <= kSmemMax, "shared memory");
     static_assert(kWarps % kTeam == 0 && 32 * kTeam % kChunks == 0 && TP * kChunks % (32 * kTeam) == 0, "copies");
-    static_assert(kTeams <= kMostTeams && kTeams <= 16 && kCols % 64 == 0, "teams");
+    static_assert(kTeams <= kMostTeams && kTeams <= 16 && kCols % 64 == 0 && (kTeam == 1 || kTeams <= 15), "teams");
+    static_assert(!WIDE || DP < kScaleCols || kCols >= kScaleCols, "a scale's columns are one warp's");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
@@ -93,7 +93,7 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Warps that wait for one another: `warps` of them at barrier `id` (1 .. 8).
+// Warps that wait for one another: `warps` of them at barrier `id` (1 .. 15).
 __device__ __forceinline__ void sync_warps(int id, int warps) {
     if (warps == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * warps) : "memory");
@@ -122,6 +122,19 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Four 8 x 8 matrices of 16-bit values from shared memory, a row's address from each lane; as they lie or transposed.
+template <bool TRANS>
+__device__ __forceinline__ void load_matrices(uint32_t (&a)[4], uint32_t at) {
+    if (TRANS) asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(at) : "memory");
+    else asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(at) : "memory");
+}
+// An 8 x 8 matrix of 16-bit values, two of a row in a lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // Two e4m3 codes as fp16.
 __device__ __forceinline__ uint32_t widen(uint32_t two) {
     uint32_t r;
@@ -143,20 +156,6 @@ __device__ __forceinline__ uint32_t part(float& lo, float& hi) {
     lo -= bf16_lo(w);
     hi -= bf16_hi(w);
     return w;
-}
-
-// One of a row's eight-element pieces as fp32; zeros past n.
-__device__ __forceinline__ void load_q8(const HeadsView& x, bool aligned, const uint8_t* row, int i, int n, float (&v)[8]) {
-    if (!row || i >= n) {
-#pragma unroll
-        for (int q = 0; q < 8; q++) v[q] = 0.0f;
-    } else if (aligned) {
-        load8_row<true>(row, x.dtype, i, n, v);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 8; q++)
-            v[q] = x.dtype == QS_BF16 ? bf16_lo(reinterpret_cast<const uint16_t*>(row)[i + q]) : reinterpret_cast<const float*>(row)[i + q];
-    }
 }
 
 // What a sequence has to do.  Positions are 32-bit numbers near enough to the table's (0 .. positions): a start far outside
@@ -194,155 +193,140 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& p, int s) {
     return q;
 }
 
-// Four of an output row's columns from col: v is the sum of weighted values, l the sum of weights, m the maximum they are
-// relative to.
-__device__ __forceinline__ void finish(const AttnArgs& p, int token, int head, int col, float (&v)[4], float m, float l, bool real) {
+// The token of an item's row.
+__device__ __forceinline__ int token_of(const AttnArgs& p, int row) { return fast_div(row, p.group_div); }
+
+// What an item's rows are and see, and what of it a team's run has: `count` tiles from the one at position pos0, a stretch.
+struct Item {
+    int first_token, rows, kv, row0;
+    int lo_base, hi_base, tiles, marks;
+    int count, pos0, at, unused;  // at: where the item begins in the line, from the run's start
+};
+enum { kOpens = 1, kEnds = 2 };  // the stretch has the item's first tile, its last
+// What a team has of an item that is not whole in its run: where the item begins in the line (-1: nothing), and which.
+struct Piece {
+    int64_t at;
+    int first_token, rows, kv, row0, tiles, unused;
+};
+
+// An output row: where it goes.
+struct Row {
+    int64_t token;
+    int head;
+    bool real;
+};
+template <class X>
+__device__ __forceinline__ Row row_of(const AttnArgs& p, const X& x, int row) {
+    const int at = token_of(p, row);
+    return {x.first_token + at, x.kv * p.group + row - at * p.group, row < x.rows};
+}
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
+
+// Four columns of a row from col, of a warp that has 128 of it side by side: v is the sum of weighted values, l the sum of
+// weights, m the maximum that they are relative to.
+template <bool WIDE>
+__device__ __forceinline__ void finish(const AttnArgs& p, const Row& r, int col, float (&v)[4], float m, float l) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int q = 0; q < 4; q++) v[q] = l == 0.0f ? 0.0f : v[q] * inv;
     const int d = p.cache.head_dim;
-    if (p.codes) {  // head_dim a multiple of 128: a warp has a scale's columns
+    if (WIDE && p.codes) {
         const BlockCode code(lanes_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))), 16), 1.0f, kMinAmax);
-        if (real) {
-            const int i = head * d + col;
-            *reinterpret_cast<uint32_t*>(p.codes + token * p.codes_stride + i) = code.pair(v[0], v[1]) | (code.pair(v[2], v[3]) << 16);
-            if (i % kScaleCols == 0) p.codes_scale[token * p.codes_scale_stride + i / kScaleCols] = code.scale;
+        if (r.real) {
+            const int i = r.head * d + col;
+            *reinterpret_cast<uint32_t*>(p.codes + r.token * p.codes_stride + i) = code.pair(v[0], v[1]) | (code.pair(v[2], v[3]) << 16);
+            if (i % kScaleCols == 0) p.codes_scale[r.token * p.codes_scale_stride + i / kScaleCols] = code.scale;
         }
     }
-    if (!real || col >= d) return;
+    if (!r.real || col >= d) return;
     if (p.out.data) {
-        uint8_t* row = p.out.data + token * p.out.token_stride + head * p.out.head_stride;
-        if (!p.out_aligned) {
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                if (p.out.dtype == QS_BF16) reinterpret_cast<__nv_bfloat16*>(row)[col + q] = __float2bfloat16_rn(v[q]);
-                else reinterpret_cast<float*>(row)[col + q] = v[q];
-            }
-        } else if (p.out.dtype == QS_BF16) {
-            *reinterpret_cast<uint2*>(row + 2 * col) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-        } else {
-            *reinterpret_cast<float4*>(row + 4 * col) = make_float4(v[0], v[1], v[2], v[3]);
-        }
+        uint8_t* to = p.out.data + r.token * p.out.token_stride + r.head * p.out.head_stride;
+        if (WIDE && p.out.dtype == QS_F32) *reinterpret_cast<float4*>(to + 4 * col) = make_float4(v[0], v[1], v[2], v[3]);
+        else *reinterpret_cast<uint2*>(to + 2 * col) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     }
-    if (p.lse && col == 0) p.lse[(int64_t)token * p.n_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (p.lse && col == 0) p.lse[r.token * p.n_heads + r.head] = lse_of(m, l);
 }
 
-// The token of an item's row.
-__device__ __forceinline__ int token_of(const AttnArgs& p, int row) { return fast_div(row, p.group_div); }
+// A warp's output, acc[j][nt][2 h + e]: of piece j the column col_of_value(j, h) from the warp's first, of rows nt * 8 + 2 t + e.
+// bf16: piece j is columns 16 j ..; e4m3: four pieces are 64 columns, of which a lane has eight neighbours.
+template <bool E4>
+__device__ __forceinline__ int col_of_value(int j, int h) {
+    const int g = (threadIdx.x & 31) >> 2;
+    return E4 ? 64 * (j / 4) + 8 * g + 2 * (j % 4) + h : 16 * j + 8 * h + g;
+}
 
-// An item's rows from the registers of the warps that have all their positions.  most: the warps' largest values by row, for
-// the codes of 128 columns that two warps have.
-template <class P>
-__device__ __forceinline__ void finish_rows(const AttnArgs& p, const Seq& seq, int kv, int w0, int rows, const float (&top)[P::NT], const float (&sum)[P::NT],
-                                            float (&acc)[P::kCols / 64][4][P::NT][4], float (*most)[8 * P::NT], int team) {
-    constexpr int NT = P::NT, kJ = P::kCols / 64;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, d = p.cache.head_dim;
-    const int col0 = warp % P::C * P::kCols;
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++) {
-        const float inv = sum[nt] == 0.0f ? 0.0f : 1.0f / sum[nt];
-        const int own = w0 + nt * 8 + g;
-        if (p.lse && t == 0 && col0 == 0 && own < rows)
-            p.lse[(int64_t)(seq.first_token + token_of(p, own)) * p.n_heads + kv * p.group + (own - token_of(p, own) * p.group)] = sum[nt] == 0.0f ? -INFINITY : (top[nt] + log2f(sum[nt])) * kLn2;
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-            const float by = __shfl_sync(0xffffffffu, inv, 8 * t + 4 * e);
-#pragma unroll
-            for (int jj = 0; jj < kJ; jj++)
-#pragma unroll
-                for (int q = 0; q < 8; q++) {
-                    float& x = acc[jj][q / 2][nt][q % 2 * 2 + e];
-                    x = by == 0.0f ? 0.0f : x * by;
-                }
-        }
-    }
-    const bool shared_scale = P::kCols < kScaleCols && P::C > 1 && p.codes;
-    if (shared_scale) {
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                float a = 0.0f;
-#pragma unroll
-                for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(acc[0][q / 2][nt][q % 2 * 2 + e]));
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                if (g == 0) most[warp][nt * 8 + 2 * t + e] = a;
-            }
-        sync_warps(1 + team, P::kTeam);
-    }
+// An item's rows from the registers of the warps that have all their positions: columns col0 .. of rows w0 ...
+template <class P, class X>
+__device__ __forceinline__ void finish_rows(const AttnArgs& p, const X& x, int w0, int col0, const float (&top)[P::NT][2], const float (&sum)[P::NT][2],
+                                            const float (&acc)[P::kPieces][P::NT][4]) {
+    constexpr int NT = P::NT, kJ = P::kPieces;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, d = p.cache.head_dim;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-            const int row = w0 + nt * 8 + 2 * t + e;
-            const bool real = row < rows;
-            const int at = token_of(p, row), head = kv * p.group + row - at * p.group;
-            const int64_t token = seq.first_token + at;
-            auto columns = [&](int jj, float (&v)[8]) {
+            const float l = sum[nt][e], by = l == 0.0f ? 0.0f : 1.0f / l;
+            const Row r = row_of(p, x, w0 + nt * 8 + 2 * t + e);
+            if (p.lse && g == 0 && col0 == 0 && r.real) p.lse[r.token * p.n_heads + r.head] = lse_of(top[nt][e], l);
+            float v[kJ][2];
 #pragma unroll
-                for (int q = 0; q < 8; q++) v[q] = acc[jj][q / 2][nt][q % 2 * 2 + e];
-            };
-            if (P::DP >= kScaleCols && p.codes) {  // a scale's columns are in the eight lanes of the same t, eight or twice eight each
-                constexpr int kEach = kJ >= 2 ? 2 : 1;
+            for (int j = 0; j < kJ; j++)
 #pragma unroll
-                for (int b = 0; b < kJ; b += kEach) {
-                    float a = 0.0f;
-                    if (shared_scale) {
-                        a = fmaxf(most[warp][nt * 8 + 2 * t + e], most[warp ^ 1][nt * 8 + 2 * t + e]);
-                    } else {
+                for (int h = 0; h < 2; h++) v[j][h] = by == 0.0f ? 0.0f : acc[j][nt][2 * h + e] * by;
+            if constexpr (P::WIDE && kJ >= 8) {  // a scale's 128 columns are in the eight lanes of the same t
+                if (p.codes) {
 #pragma unroll
-                        for (int k = 0; k < kEach; k++)
+                    for (int b = 0; b < kJ; b += 8) {
+                        float a = 0.0f;
 #pragma unroll
-                            for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(acc[(b + k) % kJ][q / 2][nt][q % 2 * 2 + e]));
+                        for (int j = b; j < b + 8; j++) a = fmaxf(a, fmaxf(fabsf(v[j][0]), fabsf(v[j][1])));
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                    }
-                    const BlockCode code(a, 1.0f, kMinAmax);
-                    if (!real || col0 + 64 * b >= d) continue;
-                    if (g == 0 && (col0 + 64 * b) % kScaleCols == 0) p.codes_scale[token * p.codes_scale_stride + (head * d + col0 + 64 * b) / kScaleCols] = code.scale;
+                        const BlockCode code(a, 1.0f, kMinAmax);
+                        if (!r.real) continue;
+                        const int i = r.head * d + col0 + 16 * b;
+                        if (g == 0) p.codes_scale[r.token * p.codes_scale_stride + i / kScaleCols] = code.scale;
+                        uint8_t* to = p.codes + r.token * p.codes_stride + r.head * d + col0;
 #pragma unroll
-                    for (int k = 0; k < kEach; k++) {
-                        float x[8];
-                        columns((b + k) % kJ, x);
-                        *reinterpret_cast<uint2*>(p.codes + token * p.codes_stride + head * d + col0 + 64 * (b + k) + 8 * g) =
-                            make_uint2(code.pair(x[0], x[1]) | (code.pair(x[2], x[3]) << 16), code.pair(x[4], x[5]) | (code.pair(x[6], x[7]) << 16));
+                        for (int j = b; j < b + 8; j++) {
+                            if (P::E4) *reinterpret_cast<uint16_t*>(to + col_of_value<P::E4>(j, 0)) = (uint16_t)code.pair(v[j][0], v[j][1]);
+                            else
+#pragma unroll
+                                for (int h = 0; h < 2; h++) to[col_of_value<P::E4>(j, h)] = code.one(v[j][h]);
+                        }
                     }
                 }
             }
-            if (!real || !p.out.data) continue;
-            uint8_t* to = p.out.data + token * p.out.token_stride + head * p.out.head_stride;
+            if (!r.real || !p.out.data) continue;
+            uint8_t* to = p.out.data + r.token * p.out.token_stride + r.head * p.out.head_stride;
+            const bool f32 = P::WIDE && p.out.dtype == QS_F32;
+            if (P::E4) {  // eight neighbours
 #pragma unroll
-            for (int jj = 0; jj < kJ; jj++) {
-                const int col = col0 + 64 * jj + 8 * g;
-                if (col >= d) continue;
-                float v[8];
-                columns(jj, v);
-                if (p.out_aligned) {
-                    store8_row<true>(to, p.out.dtype, col, d, v);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; q++) {
-                        if (p.out.dtype == QS_BF16) reinterpret_cast<__nv_bfloat16*>(to)[col + q] = __float2bfloat16_rn(v[q]);
-                        else reinterpret_cast<float*>(to)[col + q] = v[q];
-                    }
+                for (int j = 0; j < kJ; j += 4) {
+                    const int col = col0 + col_of_value<true>(j, 0);
+                    const float y[8] = {v[j][0], v[j][1], v[j + 1][0], v[j + 1][1], v[j + 2][0], v[j + 2][1], v[j + 3][0], v[j + 3][1]};
+                    if (col < d) store8_row<true>(to, f32 ? QS_F32 : QS_BF16, col, d, y);
                 }
+            } else {  // the lanes of eight neighbouring columns store one each
+#pragma unroll
+                for (int j = 0; j < kJ; j++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int col = col0 + col_of_value<false>(j, h);
+                        if (col >= d) continue;
+                        if (f32) reinterpret_cast<float*>(to)[col] = v[j][h];
+                        else reinterpret_cast<__nv_bfloat16*>(to)[col] = __float2bfloat16_rn(v[j][h]);
+                    }
             }
         }
 }
 
-// What a team has of an item that is not whole in its run: where the item begins in the line (-1: nothing), and which.
-struct Piece {
-    int64_t at;
-    int seq, item;
-};
-// A tile in the ring: positions that are there, the first one, and whether it is the first or last of a stretch (the item's
-// or the run's); the item, the tile's number in it, and where it begins in the line, from the run's start.
-struct Tile {
-    unsigned there;
-    int pos0, first, last;
-    int seq, item, tile, at;
-};
+// Where a row's 16-byte pieces lie in shared memory: piece c of row r at c ^ swap(r), so that the eight that are read at
+// once have banks of their own.  bf16: a matrix's eight rows; e4m3 keys: two rows' four; e4m3 values: four rows' two.
+template <bool E4, int NC>
+__device__ __forceinline__ int key_swap(int row) { return E4 ? (NC >= 8 ? (row & 1) * 4 : 0) : row & 7; }
+template <bool E4, int NC>
+__device__ __forceinline__ int value_swap(int row) { return E4 ? ((row >> 1) & 3) * 2 & (NC - 1) : row & 7; }
 
 // What a part with maximum ml.x counts beside the maximum m; one of no positions (-infinity, 0) nothing.
 __device__ __forceinline__ float part_factor(float2 ml, float m) { return ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - m); }
@@ -350,22 +334,21 @@ __device__ __forceinline__ float part_factor(float2 ml, float m) { return ml.x =
 template <class P>
 __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs p) {
     constexpr bool E4 = P::E4;
-    constexpr int DP = P::DP, NT = P::NT, RT = P::RT, TP = P::TP, ST = P::ST, NC = P::kChunks, kJ = P::kCols / 64;
+    constexpr int DP = P::DP, NT = P::NT, RT = P::RT, TP = P::TP, ST = P::ST, NC = P::kChunks, kJ = P::kPieces;
     constexpr int kWarps = P::kWarps, kThreads = 32 * kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t scan[kWarps], found_base[P::kTeams];
     __shared__ int found_seq[P::kTeams];
-    __shared__ Tile tile_of[kWarps][ST];
-    __shared__ Piece piece_of[2 * P::kTeams];  // of each team: the stretch that begins inside an item and ends with it; the run's last
-    __shared__ float most_of[kWarps][8 * NT];
+    __shared__ unsigned there_of[kWarps][ST];           // a tile's positions that are there
+    __shared__ __align__(16) Item item_of[kWarps][ST];  // of the tiles that are a stretch's first
+    __shared__ __align__(16) Piece piece_of[2 * P::kTeams];  // of each team: the stretch that begins inside an item and ends with it; the run's last
     __shared__ bool last_of[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int team = warp / P::kTeam, team_tid = tid % (32 * P::kTeam), row_warp = warp % P::kTeam / P::C, col_warp = warp % P::C;
-    const int d = p.cache.head_dim;
-    uint8_t* const q_shared = smem + warp * (P::kQBytes / kWarps) + lane * 16;
+    const int n_pos = p.seqs.positions;
+    uint8_t* const q_shared = smem + warp * (P::kQBytes / kWarps) + lane * 8;
     uint8_t* const ring = smem + P::kQBytes + team * ST * P::kStage;
-    float* const red = reinterpret_cast<float*>(smem);
-    float2* const red_ml = reinterpret_cast<float2*>(red + P::kTeams * RT * (DP + 4));
+    float* const red = reinterpret_cast<float*>(smem);  // a part a team, over all of it
     pdl_wait();
     pdl_launch_next();
 
@@ -373,9 +356,12 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     // takes kEnter places before its tiles', about what entering and leaving it costs.
     const int per = (p.seqs.n_seqs + kThreads - 1) / kThreads;
     const int s0 = min(tid * per, p.seqs.n_seqs), s1 = min(s0 + per, p.seqs.n_seqs);
-    auto places_of = [&](const Seq& q) { return (int64_t)(q.tiles + P::kEnter) * (q.row_tiles * p.cache.n_kv); };
+    auto places_of = [&](int s) {
+        const Seq q = seq_of<TP, RT>(p, s);
+        return (int64_t)(q.tiles + P::kEnter) * (q.row_tiles * p.cache.n_kv);
+    };
     int64_t mine = 0;
-    for (int s = s0; s < s1; s++) mine += places_of(seq_of<TP, RT>(p, s));
+    for (int s = s0; s < s1; s++) mine += places_of(s);
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -398,540 +384,556 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     // equal runs, the first of them a place longer
     const int64_t each = div_of(total, workers), longer = total - each * workers;
     const int64_t run0 = c * each + min((int64_t)c, longer), run1 = run0 + each + (c < longer);
-    auto cta_of = [&](int64_t place) {  // the CTA whose run has it
-        const int64_t split = longer * (each + 1);
-        return (int)(place < split ? div_of(place, each + 1) : longer + div_of(place - split, each));
-    };
     const unsigned length = (unsigned)(run1 - run0);
     auto begin_of = [&](unsigned x) { return length / P::kTeams * x + length % P::kTeams * x / P::kTeams; };
     // the threads whose sequences the teams begin in say so
     if (upto > run0 && upto - mine < run1) {
-        for (unsigned w = 0; w < P::kTeams; w++) {
-            const int64_t from = run0 + begin_of(w);
-            if (from < upto - mine || from >= upto) continue;
-            int64_t base = upto - mine;
-            int s = s0;
-            for (; s + 1 < s1; s++) {
-                const int64_t x = places_of(seq_of<TP, RT>(p, s));
-                if (from < base + x) break;
-                base += x;
+        int64_t base = upto - mine;
+        for (int s = s0; s < s1; s++) {
+            const int64_t next = s + 1 < s1 ? base + places_of(s) : upto;
+#pragma unroll 1
+            for (unsigned w = 0; w < P::kTeams; w++) {
+                const int64_t from = run0 + begin_of(w);
+                if (from >= base && from < next) {
+                    found_base[w] = base;
+                    found_seq[w] = s;
+                }
             }
-            found_base[w] = base;
-            found_seq[w] = s;
+            base = next;
         }
     }
     __syncthreads();
     const int64_t from = run0 + begin_of(team);
-
-    // ---- copies: the next tile's place, kept by all warps of a team alike
-    struct {
-        int seq, item, items, kv, tile, tiles, left, base_pos, lo, hi, at;
-        bool first;
-        const uint8_t *k, *v;
-    } next = {};
-    int issued = 0;
-    Place ahead = {-1, -1};
-    auto hi_of = [&](const Seq& q, int token) { return clip_pos(q.hi_base + token, p.seqs.positions); };
-    auto lo_of = [&](const Seq& q, int token) { return clip_pos(q.lo_base + token, p.seqs.positions); };
-    // an item's key-value head and first row
-    auto rows_of = [&](const Seq& q, int item, int& kv, int& row0) {
-        kv = item;
-        row0 = 0;
-        if (q.row_tiles != 1) {
-            kv = item / q.row_tiles;
-            row0 = (item - kv * q.row_tiles) * RT;
-        }
-    };
-    const int chunk = team_tid % NC, chunk_row = team_tid / NC;
-    const bool chunk_in = chunk * 16 < d * (E4 ? 1 : 2);
-    auto enter = [&](const Seq& q) {
-        int row0;
-        rows_of(q, next.item, next.kv, row0);
-        next.items = q.row_tiles * p.cache.n_kv;
-        next.tiles = q.tiles;
-        next.base_pos = q.lo / TP * TP;
-        next.lo = lo_of(q, token_of(p, row0));
-        next.hi = hi_of(q, token_of(p, min(row0 + RT, q.tokens * p.group) - 1));
-        next.k = p.cache.k + next.kv * p.cache.head_stride + (chunk_in ? chunk * 16 : 0);
-        next.v = p.cache.v + next.kv * p.cache.head_stride + (chunk_in ? chunk * 16 : 0);
-    };
-    auto look = [&]() {
-        const int pos = next.base_pos + next.tile * TP + lane % TP;
-        ahead = Place{-1, -1};
-        if (next.left > 0 && pos >= next.lo && pos < next.hi) ahead = place_of(p.cache, p.seqs, next.seq, pos);
-    };
     const int run = (int)(begin_of(team + 1) - begin_of(team));
-    if (run > 0) {
-        next.seq = found_seq[team];
-        const Seq q = seq_of<TP, RT>(p, next.seq);
-        const int64_t in = from - found_base[team];
-        next.item = (int)div_of(in, q.tiles + P::kEnter);
-        const int place = (int)(in - (int64_t)next.item * (q.tiles + P::kEnter));
-        next.tile = max(0, place - P::kEnter);
-        next.left = run - max(0, P::kEnter - place);
-        next.at = -place;
-        next.first = true;
-        enter(q);
-        look();
-    }
-    auto issue = [&](int i) {
-        if (next.left > 0) {
-            const int stage = i % ST;
-            const unsigned there = __ballot_sync(0xffffffffu, ahead.at >= 0);
-            const bool ends = next.tile + 1 == next.tiles;
-            if (lane == 0) tile_of[warp][stage] = Tile{there, next.base_pos + next.tile * TP, next.first, ends || next.left == 1, next.seq, next.item, ends ? -1 - next.tile : next.tile, next.at};
-            const uint32_t to = smem_u32(ring + stage * P::kStage);
-#pragma unroll
-            for (int k = 0; k < TP * NC / (32 * P::kTeam); k++) {
-                const int row = chunk_row + k * (32 * P::kTeam / NC);
-                const int64_t at = __shfl_sync(0xffffffffu, ahead.at, row);
-                const bool ok = at >= 0 && chunk_in;
-                const int64_t from_base = ok ? at : 0;
-                cp16(to + row * P::kRowBytes + ((chunk ^ (NC >= 8 ? (row & 1) * 4 : 0)) * 16), next.k + from_base, ok);
-                cp16(to + (TP + row) * P::kRowBytes + ((chunk ^ (((row >> 1) & 3) * 2 & (NC - 1))) * 16), next.v + from_base, ok);
-            }
-            if (E4 && warp % P::kTeam == 0 && lane < TP) {
-                const bool ok = ahead.at >= 0;
-                const int64_t from_base = ok ? ahead.scale_at + next.kv * p.cache.scale_head_stride : 0;
-                cp4(to + 2 * TP * P::kRowBytes + lane * 4, p.cache.k_scale + from_base, ok);
-                cp4(to + 2 * TP * P::kRowBytes + (TP + lane) * 4, p.cache.v_scale + from_base, ok);
-            }
-            issued++;
-            next.left--;
-            next.tile++;
-            next.first = ends;
-            if (ends) {
-                next.left -= P::kEnter;
-                if (next.left > 0) {
-                    next.at += next.tiles + P::kEnter;
-                    next.tile = 0;
-                    Seq q;
-                    if (++next.item == next.items) {
-                        next.item = 0;
-                        do {
-                            next.seq = min(next.seq + 1, p.seqs.n_seqs - 1);
-                            q = seq_of<TP, RT>(p, next.seq);
-                        } while (q.tokens == 0 && next.seq + 1 < p.seqs.n_seqs);
-                    } else {
-                        q = seq_of<TP, RT>(p, next.seq);
-                    }
-                    enter(q);
-                }
-            }
-            look();
-        }
-        cp_commit();
-    };
 
-    // ---- the pass over the run's tiles
-    Seq seq = {};
-    int kv = 0, w0 = 0, rows = 0, token0 = 0, token1 = 0, all_lo = 0, all_hi = 0, tile_lo = 0, tile_hi = 0, tile0 = 0;
+    // ---- the next tile to copy, kept by all warps of a team alike
+    struct {
+        int seq, item, items, left, count, pos, lo, hi;
+        const uint8_t *k, *v;
+        const int32_t* table;
+        const float *k_scale, *v_scale;
+    } next = {};
+    Item entered = {};
+    bool first = false;
+    int ahead = -1;          // a lane's position's place, in units; -1: not there
+    int64_t ahead_scale = 0;
+    next.seq = run > 0 ? found_seq[team] : 0;
+    next.left = run;
+    // a thread copies the 16 bytes `chunk` of the rows chunk_row, chunk_row + kStep, ...; a row's bits above chunk_row's are
+    // the pass's, and swap() is of bits
+    constexpr int kStep = 32 * P::kTeam / NC, kPasses = TP / kStep;
+    const int chunk = team_tid % NC, chunk_row = team_tid / NC;
+    const bool chunk_in = chunk * 16 < p.cache.head_dim * (E4 ? 1 : 2), all_in = p.cache.head_dim == DP;
+    const uint32_t key_to = smem_u32(ring) + chunk_row * P::kRowBytes, key_piece = (chunk ^ key_swap<E4, NC>(chunk_row)) * 16, value_piece = (chunk ^ value_swap<E4, NC>(chunk_row)) * 16;
+    constexpr unsigned kAll = TP == 32 ? 0xffffffffu : (1u << (TP & 31)) - 1u;
+
+    // ---- the rows of the item under way
+    struct {
+        int first_token, rows, kv, row0, lo_base, hi_base, tiles, marks, at;
+    } item = {};
+    int remain = 0, pos0 = 0, w0 = 0, all_lo = 0, all_hi = 0, tile_lo = 0, tile_hi = 0;
     bool active = false;
     uint32_t qf[P::kQInRegs ? P::kSteps : 1][P::kQInRegs ? P::kQEach : 1];
-    float row_scale[NT];
-    float acc[kJ][4][NT][4];  // [64 columns][their pair][rows]: columns 64 jj + 8 g + 2 m (+ 1), rows 2 t, 2 t + 1
-    float top[NT], sum[NT];
+    float row_scale[NT][2];
+    float acc[kJ][NT][4];
+    float top[NT][2], sum[NT][2];  // of rows 2 t, 2 t + 1: the maximum, and the sum of weights of this lane's positions
+    auto lo_of = [&](int base, int row) { return clip_pos(base + token_of(p, row), n_pos); };  // of lo_base or hi_base, and a row
 
-    // an item's rows: queries as fragments in the order in which the keys' pieces lie
-    auto begin = [&](const Tile& x) {
-        seq = seq_of<TP, RT>(p, x.seq);
-        tile0 = x.tile < 0 ? -1 - x.tile : x.tile;
-        int row0;
-        rows_of(seq, x.item, kv, row0);
-        rows = seq.tokens * p.group;
-        tile_lo = lo_of(seq, token_of(p, row0));
-        tile_hi = hi_of(seq, token_of(p, min(row0 + RT, rows) - 1));
-        w0 = row0 + row_warp * P::kRows;
-        active = w0 < rows;
-        token0 = token_of(p, w0);
-        token1 = max(token_of(p, max(min(w0 + P::kRows, rows) - 1, 0)), token0);
-        all_lo = lo_of(seq, token1);
-        all_hi = hi_of(seq, token0);
+    // queries as fragments in the order in which the keys' pieces lie
+    auto begin = [&](const Item& x) {
+        item = {x.first_token, x.rows, x.kv, x.row0, x.lo_base, x.hi_base, x.tiles, x.marks, x.at};
+        remain = x.count;
+        pos0 = x.pos0;
+        w0 = x.row0 + row_warp * P::kRows;
+        active = w0 < x.rows;
+        const int last = min(x.row0 + RT, x.rows) - 1;
+        tile_lo = lo_of(x.lo_base, x.row0);
+        tile_hi = lo_of(x.hi_base, last);
+        all_lo = lo_of(x.lo_base, last);
+        all_hi = lo_of(x.hi_base, x.row0);
+        constexpr int kE = P::kQInRegs ? P::kQEach : 1, kS = P::kQInRegs ? P::kSteps : 1;
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
-            top[nt] = -INFINITY;
-            sum[nt] = 0.0f;
-            const int row = w0 + nt * 8 + g;
-            const int at = token_of(p, row);
-            const uint8_t* q = row < rows ? p.q.data + (seq.first_token + at) * p.q.token_stride + (kv * p.group + row - at * p.group) * p.q.head_stride : nullptr;
-            row_scale[nt] = p.scale;
-            if constexpr (!E4 && !P::WIDE) {  // bf16 as it lies, by the rule below
-                uint4 raw[DP / 32];
-#pragma unroll
-                for (int i = 0; i < DP / 32; i++) {
-                    const int col = 32 * i + 8 * t;
-                    raw[i] = make_uint4(0, 0, 0, 0);
-                    if (!q || col >= d) continue;
-                    if (p.q_aligned) {
-                        raw[i] = *reinterpret_cast<const uint4*>(q + 2 * col);
-                    } else {
-                        const uint16_t* e = reinterpret_cast<const uint16_t*>(q) + col;
-                        raw[i] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
-                    }
+            const Row r = row_of(p, x, w0 + nt * 8 + g);
+            const uint8_t* q = p.q.data + r.token * p.q.token_stride + r.head * p.q.head_stride;
+            const int n_cols = r.real ? p.cache.head_dim : 0;
+            // a step's columns: two neighbours for the lower half of the step, two for the upper
+            auto cols_of = [&](int step, int half) { return E4 ? 64 * (step / 4) + 16 * t + 4 * (step % 4) + 2 * half : 16 * step + 8 * half + 2 * t; };
+            auto store = [&](int step, int pl, uint32_t lo, uint32_t hi) {
+                if (P::kQInRegs) {
+                    qf[step % kS][(2 * (pl * NT + nt)) % kE] = lo;
+                    qf[step % kS][(2 * (pl * NT + nt) + 1) % kE] = hi;
+                } else {
+                    *reinterpret_cast<uint2*>(q_shared + ((pl * NT + nt) * P::kSteps + step) * 256) = make_uint2(lo, hi);
                 }
-#pragma unroll
-                for (int i = 0; i < DP / 32; i++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const uint32_t x0 = h ? raw[i].z : raw[i].x, x1 = h ? raw[i].w : raw[i].y;
-                        constexpr int kE = P::kQInRegs ? P::kQEach : 1;
-                        if (P::kQInRegs) {
-                            uint32_t(&to)[kE] = qf[(2 * i + h) % (P::kQInRegs ? P::kSteps : 1)];
-                            to[nt % kE] = x0;
-                            to[(NT + nt) % kE] = x1;
-                        } else {
-                            uint32_t* shared = reinterpret_cast<uint32_t*>(q_shared + (2 * i + h) * 512);
-                            if (NT == 1) {
-                                *reinterpret_cast<uint4*>(shared) = make_uint4(x0, 0u, x1, 0u);
-                            } else {
-                                shared[nt] = x0;
-                                shared[2 + nt] = x1;
-                            }
-                        }
-                    }
-            } else {
-            // bf16: piece i is columns 32 i + 8 t .. + 7, two steps of four; e4m3: 64 i + 16 t .. + 15, four steps
-            float v[DP / 32][8];
-#pragma unroll
-            for (int i = 0; i < DP / 32; i++) load_q8(p.q, p.q_aligned, q, E4 ? 64 * (i / 2) + 16 * t + 8 * (i % 2) : 32 * i + 8 * t, d, v[i]);
+            };
             float factor = 1.0f;
-            if (E4) {  // a power of two that brings the row's largest into fp16's upper range
-                float a = 0.0f;
+            if constexpr (!E4 && !P::WIDE) {  // bf16 as it lies
+                uint32_t raw[P::kSteps][2];
 #pragma unroll
-                for (int i = 0; i < DP / 32; i++)
+                for (int step = 0; step < P::kSteps; step++)
 #pragma unroll
-                    for (int e = 0; e < 8; e++) a = fmaxf(a, fabsf(v[i][e]));
-                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-                const int e = min(max(14 - ((int)(__float_as_uint(a) >> 23) - 127), -100), 100);
-                factor = __uint_as_float((uint32_t)(127 + e) << 23);
-                row_scale[nt] = p.scale * __uint_as_float((uint32_t)(127 - e) << 23);
-            }
+                    for (int half = 0; half < 2; half++) {
+                        raw[step][half] = 0u;
+                        if (cols_of(step, half) < n_cols) raw[step][half] = *reinterpret_cast<const uint32_t*>(q + 2 * cols_of(step, half));
+                    }
 #pragma unroll
-            for (int i = 0; i < DP / 32; i++)
+                for (int step = 0; step < P::kSteps; step++) store(step, 0, raw[step][0], raw[step][1]);
+            } else {
+                float2 v[P::kSteps][2];
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const int step = 2 * i + h;
-                    float* x = v[i] + 4 * h;
+                for (int step = 0; step < P::kSteps; step++)
 #pragma unroll
-                    for (int e = 0; e < 4; e++) x[e] *= factor;
-#pragma unroll
-                    for (int f = 0; f < P::kQAll; f++) {  // a fragment: rows g, g + 8, the same of the upper columns
-                        uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
-#pragma unroll
-                        for (int y = 0; y < (NT == 1 ? 2 : 1); y++)
-                            if (NT == 2 || 2 * f + y < P::QP) {
-                                lo[y] = part<E4>(x[0], x[1]);
-                                hi[y] = part<E4>(x[2], x[3]);
-                            }
-                        constexpr int kE = P::kQInRegs ? P::kQEach : 1;
-                        uint32_t(&to)[kE] = qf[step % (P::kQInRegs ? P::kSteps : 1)];
-                        uint32_t* shared = reinterpret_cast<uint32_t*>(q_shared + (f * P::kSteps + step) * 512);
-                        if (P::kQInRegs) {
-                            // NT = 1: a part's two; NT = 2: the four of a part for both rows
-                            if (NT == 1) {
-#pragma unroll
-                                for (int y = 0; y < 2; y++)
-                                    if (2 * f + y < P::QP) {
-                                        to[(4 * f + 2 * y) % kE] = lo[y];
-                                        to[(4 * f + 2 * y + 1) % kE] = hi[y];
-                                    }
-                            } else {
-                                to[(4 * f + nt) % kE] = lo[0];
-                                to[(4 * f + 2 + nt) % kE] = hi[0];
-                            }
-                        } else if (NT == 1) {
-                            *reinterpret_cast<uint4*>(shared) = make_uint4(lo[0], lo[1], hi[0], hi[1]);
+                    for (int half = 0; half < 2; half++) {
+                        const int col = cols_of(step, half);
+                        v[step][half] = make_float2(0.0f, 0.0f);
+                        if (col >= n_cols) continue;
+                        if (P::WIDE && p.q.dtype == QS_F32) {
+                            v[step][half] = *reinterpret_cast<const float2*>(q + 4 * col);
                         } else {
-                            shared[nt] = lo[0];
-                            shared[2 + nt] = hi[0];
+                            const uint32_t w = *reinterpret_cast<const uint32_t*>(q + 2 * col);
+                            v[step][half] = make_float2(bf16_lo(w), bf16_hi(w));
                         }
+                    }
+                if (E4) {  // a power of two that brings the row's largest into fp16's upper range
+                    float a = 0.0f;
+#pragma unroll
+                    for (int step = 0; step < P::kSteps; step++)
+#pragma unroll
+                        for (int half = 0; half < 2; half++) a = fmaxf(a, fmaxf(fabsf(v[step][half].x), fabsf(v[step][half].y)));
+                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                    const int e = min(max(14 - ((int)(__float_as_uint(a) >> 23) - 127), -100), 100);
+                    factor = __uint_as_float((uint32_t)(127 + e) << 23);
+                }
+#pragma unroll
+                for (int step = 0; step < P::kSteps; step++) {
+                    float2 y = v[step][0], z = v[step][1];
+                    y.x *= factor;
+                    y.y *= factor;
+                    z.x *= factor;
+                    z.y *= factor;
+#pragma unroll
+                    for (int pl = 0; pl < P::QP; pl++) {
+                        const uint32_t lo = part<E4>(y.x, y.y);
+                        store(step, pl, lo, part<E4>(z.x, z.y));
                     }
                 }
             }
-        }
 #pragma unroll
-        for (int jj = 0; jj < kJ; jj++)
-#pragma unroll
-            for (int m = 0; m < 4; m++)
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++) acc[jj][m][nt][e] = 0.0f;
-    };
-    // one step of the first product: a key's piece with every part of the queries
-    auto score = [&](float (&c4)[4], int step, uint32_t b0, uint32_t b1) {
-#pragma unroll
-        for (int f = 0; f < P::kQAll; f++) {
-            if (P::kQInRegs) {
-                constexpr int kE = P::kQInRegs ? P::kQEach : 1;
-                const uint32_t(&q)[kE] = qf[step % (P::kQInRegs ? P::kSteps : 1)];
-                if (NT == 2) mma<E4>(c4, q[4 * f % kE], q[(4 * f + 1) % kE], q[(4 * f + 2) % kE], q[(4 * f + 3) % kE], b0, b1);
-                else if (2 * f + 1 < P::QP) mma<E4>(c4, q[4 * f % kE], q[(4 * f + 2) % kE], q[(4 * f + 1) % kE], q[(4 * f + 3) % kE], b0, b1);
-                else mma<E4>(c4, q[4 * f % kE], 0u, q[(4 * f + 1) % kE], 0u, b0, b1);
-            } else {
-                const uint4 x = *reinterpret_cast<const uint4*>(q_shared + (f * P::kSteps + step) * 512);
-                mma<E4>(c4, x.x, x.y, x.z, x.w, b0, b1);
+            for (int e = 0; e < 2; e++) {
+                top[nt][e] = -INFINITY;
+                sum[nt][e] = 0.0f;
+                row_scale[nt][e] = E4 ? p.scale * (1.0f / __shfl_sync(0xffffffffu, factor, 8 * t + 4 * e)) : p.scale;
             }
         }
+#pragma unroll
+        for (int j = 0; j < kJ; j++)
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[j][nt][e] = 0.0f;
     };
-    // the rows' sums to where they are joined: [rows x stride], maxima and sums of weights at ml
-    auto put = [&](float* to, int stride, float2* ml) {
+    // one step of the first product: 16 positions' keys with every part of the queries
+    auto score = [&](float (&c)[NT][4], int step, const uint32_t (&a)[4]) {
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-            const int row = row_warp * P::kRows + nt * 8;
-            if (t == 0 && col_warp == 0) ml[row + g] = make_float2(top[nt], sum[nt]);
+        for (int pl = 0; pl < P::QP; pl++)
 #pragma unroll
-            for (int jj = 0; jj < kJ; jj++)
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    float4* at = reinterpret_cast<float4*>(to + (row + 2 * t + e) * stride + col_warp * P::kCols + 64 * jj + 8 * g);
-                    at[0] = make_float4(acc[jj][0][nt][e], acc[jj][0][nt][e + 2], acc[jj][1][nt][e], acc[jj][1][nt][e + 2]);
-                    at[1] = make_float4(acc[jj][2][nt][e], acc[jj][2][nt][e + 2], acc[jj][3][nt][e], acc[jj][3][nt][e + 2]);
+            for (int nt = 0; nt < NT; nt++) {
+                constexpr int kE = P::kQInRegs ? P::kQEach : 1, kS = P::kQInRegs ? P::kSteps : 1;
+                if (P::kQInRegs) {
+                    mma<E4>(c[nt], a[0], a[1], a[2], a[3], qf[step % kS][2 * (pl * NT + nt) % kE], qf[step % kS][(2 * (pl * NT + nt) + 1) % kE]);
+                } else {
+                    const uint2 b = *reinterpret_cast<const uint2*>(q_shared + ((pl * NT + nt) * P::kSteps + step) * 256);
+                    mma<E4>(c[nt], a[0], a[1], a[2], a[3], b.x, b.y);
                 }
-        }
+            }
+    };
+    // the rows' sums as a part: rows of kRow floats, then a maximum and a sum of weights a row
+    auto put = [&](float* to) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int row = row_warp * P::kRows + nt * 8 + 2 * t + e;
+                if (g == 0 && col_warp == 0) reinterpret_cast<float2*>(to + RT * P::kRow)[row] = make_float2(top[nt][e], sum[nt][e]);
+                float* at = to + row * P::kRow + col_warp * P::kCols;
+                if (E4) {
+#pragma unroll
+                    for (int j = 0; j < kJ; j += 2)
+                        *reinterpret_cast<float4*>(at + col_of_value<E4>(j, 0)) = make_float4(acc[j][nt][e], acc[j][nt][2 + e], acc[j + 1][nt][e], acc[j + 1][nt][2 + e]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kJ; j++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++) at[col_of_value<E4>(j, h)] = acc[j][nt][2 * h + e];
+                }
+            }
     };
 
-    for (int i = 1 - ST; i < 0 || i < issued; i++) {  // tile i is consumed, tile i + ST - 1 copied
-        const int stage = i < 0 ? 0 : i % ST;
-        const Tile& x = tile_of[warp][stage];
+    // ---- the pass over the run's tiles: tile i is consumed, tile i + ST - 1 copied, the one after it looked up
+    int issued = 0, use = 0, fill = 0;
+    for (int i = -ST; i < 0 || i < issued; i++) {
+        const int stage = use;
+        unsigned there = 0;
         if (i >= 0) {
+            if (++use == ST) use = 0;
             __syncwarp();
-            if (x.first) begin(x);  // the queries are on their way with the tile
+            there = there_of[warp][stage];
+            pos0 += TP;
+            if (remain == 0) begin(item_of[warp][stage]);  // the queries are on their way with the tile
+            remain--;
             cp_wait<ST - 2>();
             sync_warps(1 + team, P::kTeam);
         }
-        issue(i + ST - 1);
-        if (i < 0) continue;
-        const unsigned there = x.there;
-        const int pos0 = x.pos0;
-        if (active) {
-            const uint8_t* const keys = ring + stage * P::kStage;
-            const uint8_t* const values = keys + TP * P::kRowBytes;
-            const float* const scales = reinterpret_cast<const float*>(values + TP * P::kRowBytes);
-            const unsigned whole = TP == 32 ? 0xffffffffu : (1u << (TP & 31)) - 1u;
-            const bool full = (there & whole) == whole && pos0 >= all_lo && pos0 + TP <= all_hi;
-
-            float sc[TP / 8][4];
+        if (i > -ST) {
+            if (next.left > 0) {
+                const unsigned found = __ballot_sync(0xffffffffu, ahead >= 0) & kAll;
+                if (lane == 0) {
+                    there_of[warp][fill] = found;
+                    if (first) item_of[warp][fill] = entered;
+                }
+                first = false;
+                const uint32_t to = key_to + fill * P::kStage;
+                if (found == kAll && all_in) {
 #pragma unroll
-            for (int n8 = 0; n8 < TP / 8; n8++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) sc[n8][e] = 0.0f;
-#pragma unroll
-            for (int i4 = 0; i4 < NC / 4; i4++)
-#pragma unroll
-                for (int n8 = 0; n8 < TP / 8; n8++) {
-                    const int row = n8 * 8 + g;
-                    const uint4 w = *reinterpret_cast<const uint4*>(keys + row * P::kRowBytes + (((4 * i4 + t) ^ (NC >= 8 ? (row & 1) * 4 : 0)) * 16));
-                    const uint32_t r4[4] = {w.x, w.y, w.z, w.w};
-                    if (E4) {
-#pragma unroll
-                        for (int h = 0; h < 4; h++) score(sc[n8], 4 * i4 + h, widen(r4[h]), widen(r4[h] >> 16));
-                    } else {
-                        score(sc[n8], 2 * i4, r4[0], r4[1]);
-                        score(sc[n8], 2 * i4 + 1, r4[2], r4[3]);
+                    for (int k = 0; k < kPasses; k++) {
+                        const int64_t offset = (int64_t)__shfl_sync(0xffffffffu, ahead, chunk_row + k * kStep) * p.places.unit;
+                        cp16(to + k * kStep * P::kRowBytes + (key_piece ^ key_swap<E4, NC>(k * kStep) * 16), next.k + offset, true);
+                        cp16(to + (TP + k * kStep) * P::kRowBytes + (value_piece ^ value_swap<E4, NC>(k * kStep) * 16), next.v + offset, true);
                     }
-                }
-            float2 vs[TP / 8];
-#pragma unroll
-            for (int n8 = 0; n8 < TP / 8; n8++) {
-                if (NT == 1 && P::QP > 1) {  // the second part's rows
-                    sc[n8][0] += sc[n8][2];
-                    sc[n8][1] += sc[n8][3];
-                }
-#pragma unroll
-                for (int e = 0; e < 2 * NT; e++) sc[n8][e] *= row_scale[e / 2];
-                if (E4) {
-                    const float2 ks = *reinterpret_cast<const float2*>(scales + n8 * 8 + 2 * t);
-                    vs[n8] = *reinterpret_cast<const float2*>(scales + TP + n8 * 8 + 2 * t);
-#pragma unroll
-                    for (int e = 0; e < 2 * NT; e++) sc[n8][e] *= e % 2 ? ks.y : ks.x;
-                }
-            }
-            if (!full) {
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                    const int token = token_of(p, w0 + nt * 8 + g);
-                    const int lo = lo_of(seq, token), hi = hi_of(seq, token);
-#pragma unroll
-                    for (int n8 = 0; n8 < TP / 8; n8++)
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            const int at = n8 * 8 + 2 * t + e;
-                            if (!((there >> at) & 1u) || pos0 + at < lo || pos0 + at >= hi) sc[n8][2 * nt + e] = -INFINITY;
-                        }
-                }
-            }
-            // the values' scales count for the maximum, as within 2^-100 .. 2^118: the weight's two factors stay in fp32's range
-            float2 lv[TP / 8];
-#pragma unroll
-            for (int n8 = 0; n8 < TP / 8; n8++) {
-                lv[n8] = make_float2(0.0f, 0.0f);
-                if (E4) lv[n8] = make_float2(fminf(fmaxf(lg2(vs[n8].x), -100.0f), 118.0f), fminf(fmaxf(lg2(vs[n8].y), -100.0f), 118.0f));
-            }
-            bool grown = false;
-            float most[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++) {
-                float a = -INFINITY;
-#pragma unroll
-                for (int n8 = 0; n8 < TP / 8; n8++) a = fmaxf(a, fmaxf(sc[n8][2 * nt] + lv[n8].x, sc[n8][2 * nt + 1] + lv[n8].y));
-                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-                most[nt] = a;
-                grown |= a > top[nt] + kSlack;
-            }
-            if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                    const float now = fmaxf(top[nt], most[nt]);
-                    const float by = now == top[nt] ? 1.0f : ex2(top[nt] - now);
-                    top[nt] = now;
-                    sum[nt] *= by;
-                    const float b0 = __shfl_sync(0xffffffffu, by, 8 * t), b1 = __shfl_sync(0xffffffffu, by, 8 * t + 4);
-#pragma unroll
-                    for (int jj = 0; jj < kJ; jj++)
-#pragma unroll
-                        for (int m = 0; m < 4; m++) {
-                            acc[jj][m][nt][0] *= b0;
-                            acc[jj][m][nt][1] *= b1;
-                            acc[jj][m][nt][2] *= b0;
-                            acc[jj][m][nt][3] *= b1;
-                        }
-                }
-            }
-            uint32_t pb[TP / 16][NT][P::PP][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++) {
-                const float ref = top[nt] == -INFINITY ? 0.0f : top[nt];
-#pragma unroll
-                for (int n8 = 0; n8 < TP / 8; n8++) {
-                    float a = ex2(sc[n8][2 * nt] - ref), b = ex2(sc[n8][2 * nt + 1] - ref);
-                    sum[nt] += a + b;
-                    if (E4) {  // a weight of 0 stays 0 beside whatever scale a position has that is not seen
-                        a = sc[n8][2 * nt] == -INFINITY ? 0.0f : a * vs[n8].x;
-                        b = sc[n8][2 * nt + 1] == -INFINITY ? 0.0f : b * vs[n8].y;
-                    }
-#pragma unroll
-                    for (int pl = 0; pl < P::PP; pl++) pb[n8 / 2][nt][pl][n8 % 2] = part<E4>(a, b);
-                }
-            }
-            // positions here that one of the warp's rows does not see and that were copied for another
-            const bool mixed = !full && (min(pos0 + TP, tile_hi) > all_hi || max(pos0, tile_lo) < all_lo);
-            // four positions' eight columns, and a pair of these as the product's operand
-            constexpr int kW = E4 ? 2 : 4;
-            auto load_values = [&](int kk, int jj, uint32_t (&w)[4][kW]) {
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const int row = kk * 16 + 2 * t + (r & 1) + (r >> 1) * 8;
-                    if (E4) {
-                        const uint2 y = *reinterpret_cast<const uint2*>(values + row * P::kRowBytes + (((4 * (jj + col_warp * kJ) + g / 2) ^ (((row >> 1) & 3) * 2 & (NC - 1))) * 16) + (g & 1) * 8);
-                        w[r][0] = y.x;
-                        w[r][1] = y.y;
-                    } else {
-                        const uint4 y = *reinterpret_cast<const uint4*>(values + row * P::kRowBytes + (((8 * (jj + col_warp * kJ) + g) ^ (((row >> 1) & 3) * 2)) * 16));
-                        w[r][0] = y.x;
-                        w[r][1] = y.y;
-                        w[r][2 % kW] = y.z;
-                        w[r][3 % kW] = y.w;
-                    }
-                }
-            };
-            auto pair_of = [&](const uint32_t (&w)[4][kW], int m, uint32_t (&a)[4]) {
-                if (E4) {
-                    const uint32_t y = __byte_perm(w[0][m / 2], w[1][m / 2], m % 2 ? 0x7362 : 0x5140);
-                    const uint32_t z = __byte_perm(w[2][m / 2], w[3][m / 2], m % 2 ? 0x7362 : 0x5140);
-                    a[0] = widen(y);
-                    a[1] = widen(y >> 16);
-                    a[2] = widen(z);
-                    a[3] = widen(z >> 16);
                 } else {
-                    a[0] = __byte_perm(w[0][m % kW], w[1][m % kW], 0x5410);
-                    a[1] = __byte_perm(w[0][m % kW], w[1][m % kW], 0x7632);
-                    a[2] = __byte_perm(w[2][m % kW], w[3][m % kW], 0x5410);
-                    a[3] = __byte_perm(w[2][m % kW], w[3][m % kW], 0x7632);
+#pragma unroll
+                    for (int k = 0; k < kPasses; k++) {
+                        const int at = __shfl_sync(0xffffffffu, ahead, chunk_row + k * kStep);
+                        const bool ok = at >= 0 && chunk_in;
+                        const int64_t offset = (int64_t)max(at, 0) * p.places.unit;
+                        cp16(to + k * kStep * P::kRowBytes + (key_piece ^ key_swap<E4, NC>(k * kStep) * 16), next.k + offset, ok);
+                        cp16(to + (TP + k * kStep) * P::kRowBytes + (value_piece ^ value_swap<E4, NC>(k * kStep) * 16), next.v + offset, ok);
+                    }
                 }
-            };
-            if (!mixed) {
+                if (E4 && warp % P::kTeam == 0 && lane < TP) {
+                    const bool ok = ahead >= 0;
+                    const int64_t offset = ok ? ahead_scale : 0;
+                    const uint32_t scale_to = smem_u32(ring) + fill * P::kStage + 2 * TP * P::kRowBytes + lane * 4;
+                    cp4(scale_to, next.k_scale + offset, ok);
+                    cp4(scale_to + TP * 4, next.v_scale + offset, ok);
+                }
+                if (++fill == ST) fill = 0;
+                issued++;
+                next.left--;
+                next.count--;
+                next.pos += TP;
+            }
+            cp_commit();
+        }
+        if (next.count == 0 && next.left > 0) {  // an item is entered
+            int at = entered.at + entered.tiles + P::kEnter, tile = 0;
+            if (i > -ST) {
+                next.left -= P::kEnter;
+                if (++next.item == next.items) {
+                    next.item = 0;
+                    next.seq++;
+                }
+            }
+            Seq q;
+            for (;; next.seq++) {
+                next.seq = min(next.seq, p.seqs.n_seqs - 1);
+                q = seq_of<TP, RT>(p, next.seq);
+                if (q.tokens > 0 || next.seq + 1 >= p.seqs.n_seqs) break;
+            }
+            next.items = q.row_tiles * p.cache.n_kv;
+            if (i == -ST) {  // the run's first, at any of its places
+                const int64_t in = from - found_base[team];
+                next.item = (int)div_of(in, q.tiles + P::kEnter);
+                const int place = (int)(in - (int64_t)next.item * (q.tiles + P::kEnter));
+                tile = max(0, place - P::kEnter);
+                next.left -= max(0, P::kEnter - place);
+                at = -place;
+            }
+            int kv = next.item, row0 = 0;
+            if (q.row_tiles != 1) {
+                kv = next.item / q.row_tiles;
+                row0 = (next.item - kv * q.row_tiles) * RT;
+            }
+            next.count = min(q.tiles - tile, next.left);
+            next.pos = q.lo / TP * TP + tile * TP + lane % TP;
+            entered = Item{q.first_token, q.tokens * p.group, kv, row0, q.lo_base, q.hi_base, q.tiles, (tile == 0 ? kOpens : 0) | (tile + next.count == q.tiles ? kEnds : 0),
+                           next.count, next.pos - lane % TP, at, 0};
+            first = true;
+            next.lo = lo_of(q.lo_base, row0);
+            next.hi = lo_of(q.hi_base, min(row0 + RT, entered.rows) - 1);
+            const int64_t head = kv * p.cache.head_stride + (chunk_in ? chunk * 16 : 0);
+            next.k = p.cache.k + head;
+            next.v = p.cache.v + head;
+            next.table = p.seqs.table + next.seq * p.seqs.table_stride;
+            if (E4) {
+                next.k_scale = p.cache.k_scale + kv * p.cache.scale_head_stride;
+                next.v_scale = p.cache.v_scale + kv * p.cache.scale_head_stride;
+            }
+        }
+        ahead = -1;
+        if (next.left > 0 && next.pos >= next.lo && next.pos < next.hi) {
+            const int page_of = fast_div(next.pos, p.cache.page_div), slot = next.pos - page_of * p.cache.page_size, page = next.table[page_of];
+            if ((unsigned)page < (unsigned)p.cache.n_pages) ahead = page * p.places.page + slot * p.places.slot;
+            if (E4) ahead_scale = page * p.cache.scale_page_stride + slot * p.cache.scale_slot_stride;
+        }
+        if (i < 0) continue;
+
+        uint8_t* const keys = ring + stage * P::kStage;
+        uint8_t* const values = keys + TP * P::kRowBytes;
+        const bool full = there == kAll && pos0 >= all_lo && pos0 + TP <= all_hi;
+        // positions here that some of the item's rows see and others do not
+        const bool mixed = !full && (min(pos0 + TP, tile_hi) > all_hi || max(pos0, tile_lo) < all_lo);
+        // their values become zeros, once every row that sees one has added it by itself
+        auto clear_mixed = [&]() {
+            sync_warps(1 + team, P::kTeam);
+#pragma unroll 1
+            for (int y = team_tid; y < TP * NC; y += 32 * P::kTeam) {
+                const int at = pos0 + y / NC;
+                if (at < all_lo || at >= all_hi) reinterpret_cast<uint4*>(values)[y] = make_uint4(0, 0, 0, 0);
+            }
+            sync_warps(1 + team, P::kTeam);
+        };
+        if (!active) {
+            if (mixed) clear_mixed();
+        } else {
+            const float* const scales = reinterpret_cast<const float*>(values + TP * P::kRowBytes);
+            // S^T = K Q^T: 16 positions down, a warp's rows across.  With one block of positions two sums, of every second step: a
+            // product waits three times its own length for the one before.
+            constexpr int kB = TP / 16, kSums = kB == 1 ? 2 : 1;
+            float sc[kSums * kB][NT][4];
 #pragma unroll
-                for (int kk = 0; kk < TP / 16; kk++)
+            for (int b = 0; b < kSums * kB; b++)
 #pragma unroll
-                    for (int jj = 0; jj < kJ; jj++) {
-                        uint32_t w[4][kW];
-                        load_values(kk, jj, w);
+                for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                        for (int m = 0; m < 4; m++) {
-                            uint32_t a[4];
-                            pair_of(w, m, a);
+                    for (int e = 0; e < 4; e++) sc[b][nt][e] = 0.0f;
+            if constexpr (E4) {
 #pragma unroll
-                            for (int nt = 0; nt < NT; nt++)
+                for (int i4 = 0; i4 < NC / 4; i4++)
 #pragma unroll
-                                for (int pl = 0; pl < P::PP; pl++) mma<E4>(acc[jj][m][nt], a[0], a[1], a[2], a[3], pb[kk][nt][pl][0], pb[kk][nt][pl][1]);
+                    for (int b = 0; b < kB; b++) {
+                        uint4 w[2];
+#pragma unroll
+                        for (int y = 0; y < 2; y++) {
+                            const int row = 16 * b + 8 * y + g;
+                            w[y] = *reinterpret_cast<const uint4*>(keys + row * P::kRowBytes + (((4 * i4 + t) ^ key_swap<E4, NC>(row)) * 16));
+                        }
+                        const uint32_t lo[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, hi[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+                        for (int h = 0; h < 4; h++) {
+                            const uint32_t a[4] = {widen(lo[h]), widen(hi[h]), widen(lo[h] >> 16), widen(hi[h] >> 16)};
+                            score(sc[b + h % kSums * kB], 4 * i4 + h, a);
                         }
                     }
             } else {
-#pragma unroll 1
-                for (int token = token0; token <= token1; token++) {
-                    const int lo = lo_of(seq, token), hi = hi_of(seq, token);
+                const int row = lane & 15;
+                const uint32_t at = smem_u32(keys) + row * P::kRowBytes;
 #pragma unroll
-                    for (int kk = 0; kk < TP / 16; kk++)
+                for (int step = 0; step < P::kSteps; step++)
 #pragma unroll
-                        for (int jj = 0; jj < kJ; jj++) {
-                            uint32_t w[4][kW];
-                            load_values(kk, jj, w);
-#pragma unroll
-                            for (int r = 0; r < 4; r++) {
-                                const int at = pos0 + kk * 16 + 2 * t + (r & 1) + (r >> 1) * 8;
-#pragma unroll
-                                for (int y = 0; y < kW; y++)
-                                    if (at < lo || at >= hi) w[r][y] = 0u;
-                            }
-#pragma unroll
-                            for (int m = 0; m < 4; m++) {
-                                uint32_t a[4];
-                                pair_of(w, m, a);
-#pragma unroll
-                                for (int nt = 0; nt < NT; nt++) {
-                                    float one[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                                    for (int pl = 0; pl < P::PP; pl++) mma<E4>(one, a[0], a[1], a[2], a[3], pb[kk][nt][pl][0], pb[kk][nt][pl][1]);
-                                    const int row = w0 + nt * 8 + 2 * t;
-                                    if (token_of(p, row) == token) {
-                                        acc[jj][m][nt][0] += one[0];
-                                        acc[jj][m][nt][2] += one[2];
-                                    }
-                                    if (token_of(p, row + 1) == token) {
-                                        acc[jj][m][nt][1] += one[1];
-                                        acc[jj][m][nt][3] += one[3];
-                                    }
-                                }
-                            }
-                        }
-                }
+                    for (int b = 0; b < kB; b++) {
+                        uint32_t a[4];
+                        load_matrices<false>(a, at + 16 * b * P::kRowBytes + (((2 * step + (lane >> 4)) ^ key_swap<E4, NC>(row)) * 16));
+                        score(sc[b + step % kSums * kB], step, a);
+                    }
             }
+            // scores to weights.  A lane's are of rows 2 t + e at positions 16 b + 8 y + g, sc[b][nt][2 y + e].
+            float by_key[kB][2], vs[kB][2], lv[kB][2];
+#pragma unroll
+            for (int b = 0; b < kB; b++)
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                    by_key[b][y] = 1.0f;
+                    vs[b][y] = 1.0f;
+                    lv[b][y] = 0.0f;
+                    if (E4) {  // the values' scales count for the maximum, 2^-100 at least: the weight's two factors stay in fp32's range
+                        by_key[b][y] = scales[16 * b + 8 * y + g];
+                        vs[b][y] = scales[TP + 16 * b + 8 * y + g];
+                        // a position that some rows do not see has weights of 0 for them, which its scale must not make NaNs: it is left to
+                        // its own sums below, with the scale as it is
+                        if (mixed && (pos0 + 16 * b + 8 * y + g < all_lo || pos0 + 16 * b + 8 * y + g >= all_hi)) vs[b][y] = 1.0f;
+                        lv[b][y] = fmaxf(lg2(vs[b][y]), -100.0f);
+                    }
+                }
+#pragma unroll
+            for (int b = 0; b < kB; b++)
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        if (kSums == 2) sc[b][nt][e] += sc[(b + kB) % (kSums * kB)][nt][e];
+                        sc[b][nt][e] *= E4 ? row_scale[nt][e % 2] * by_key[b][e / 2] : row_scale[nt][e % 2];
+                    }
+            if (!full) {
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const int row = w0 + nt * 8 + 2 * t + e;
+                        const int lo = lo_of(item.lo_base, row) - pos0 - g, hi = lo_of(item.hi_base, row) - pos0 - g;
+#pragma unroll
+                        for (int y = 0; y < 2 * kB; y++)
+                            if (!((there >> (8 * y + g)) & 1u) || 8 * y < lo || 8 * y >= hi) sc[y / 2][nt][y % 2 * 2 + e] = -INFINITY;
+                    }
+            }
+            bool grown = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int b = 0; b < kB; b++) most = fmaxf(most, fmaxf(sc[b][nt][e] + lv[b][0], sc[b][nt][2 + e] + lv[b][1]));
+                    grown |= most > top[nt][e] + kSlack;
+                }
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        float now = top[nt][e];
+#pragma unroll
+                        for (int b = 0; b < kB; b++) now = fmaxf(now, fmaxf(sc[b][nt][e] + lv[b][0], sc[b][nt][2 + e] + lv[b][1]));
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+                        const float by = now == top[nt][e] ? 1.0f : ex2(top[nt][e] - now);
+                        top[nt][e] = now;
+                        sum[nt][e] *= by;
+#pragma unroll
+                        for (int j = 0; j < kJ; j++) {
+                            acc[j][nt][e] *= by;
+                            acc[j][nt][2 + e] *= by;
+                        }
+                    }
+            }
+            // weights, left in sc, and their parts, transposed to the second product's operand
+            uint32_t pb[kB][NT][P::PP][2];
+#pragma unroll
+            for (int b = 0; b < kB; b++)
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int y = 0; y < 2; y++) {
+                        float two[2];
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const float z = sc[b][nt][2 * y + e], ref = top[nt][e] == -INFINITY ? 0.0f : top[nt][e];
+                            two[e] = ex2(z - ref);
+                            sum[nt][e] += two[e];
+                            if (E4) two[e] *= vs[b][y];
+                            sc[b][nt][2 * y + e] = two[e];
+                        }
+#pragma unroll
+                        for (int pl = 0; pl < P::PP; pl++) pb[b][nt][pl][y] = transposed(part<E4>(two[0], two[1]));
+                    }
+            if (mixed) {
+                // positions that some of the rows see: one at a time, for those rows alone
+#pragma unroll 1
+                for (int at = max(pos0, tile_lo); at < min(pos0 + TP, tile_hi); at++) {
+                    if (at >= all_lo && at < all_hi) {
+                        at = all_hi - 1;
+                        continue;
+                    }
+                    const int o = at - pos0;
+                    if (!((there >> o) & 1u)) continue;
+                    float by[NT][2];
+                    bool sees[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            float mine = 0.0f;
+#pragma unroll
+                            for (int y = 0; y < 2 * kB; y++)
+                                if (o / 8 == y) mine = sc[y / 2][nt][y % 2 * 2 + e];
+                            by[nt][e] = __shfl_sync(0xffffffffu, mine, o % 8 * 4 + t) * (E4 ? scales[TP + o] : 1.0f);
+                            const int row = w0 + nt * 8 + 2 * t + e;
+                            sees[nt][e] = at >= lo_of(item.lo_base, row) && at < lo_of(item.hi_base, row);
+                        }
+                    const uint8_t* const value = values + o * P::kRowBytes;
+                    const int swap = value_swap<E4, NC>(o);
+#pragma unroll
+                    for (int j = 0; j < kJ; j++) {
+                        float2 v;
+                        const int col = col_warp * P::kCols + col_of_value<E4>(j, 0);
+                        if (E4) {
+                            const uint32_t two = widen(*reinterpret_cast<const uint16_t*>(value + ((col / 16) ^ swap) * 16 + col % 16));
+                            v = __half22float2(*reinterpret_cast<const __half2*>(&two));
+                        } else {
+                            v.x = bf16_lo(*reinterpret_cast<const uint16_t*>(value + ((col / 8) ^ swap) * 16 + g * 2));
+                            v.y = bf16_lo(*reinterpret_cast<const uint16_t*>(value + ((col / 8 + 1) ^ swap) * 16 + g * 2));
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                            for (int e = 0; e < 2; e++)
+                                if (sees[nt][e]) {
+                                    acc[j][nt][e] = fmaf(by[nt][e], v.x, acc[j][nt][e]);
+                                    acc[j][nt][2 + e] = fmaf(by[nt][e], v.y, acc[j][nt][2 + e]);
+                                }
+                    }
+                }
+                clear_mixed();
+            }
+            // O^T += V^T P^T: 16 columns down, a warp's rows across
+#pragma unroll
+            for (int b = 0; b < kB; b++)
+#pragma unroll
+                for (int j4 = 0; j4 < kJ; j4 += 4) {
+                    uint32_t w[4][2];  // e4m3: four positions' eight columns
+                    if (E4) {
+#pragma unroll
+                        for (int r = 0; r < 4; r++) {
+                            const int row = b * 16 + 2 * t + (r & 1) + (r >> 1) * 8;
+                            const uint2 y = *reinterpret_cast<const uint2*>(values + row * P::kRowBytes + (((j4 + col_warp * kJ + g / 2) ^ value_swap<E4, NC>(row)) * 16) + (g & 1) * 8);
+                            w[r][0] = y.x;
+                            w[r][1] = y.y;
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < 4; m++) {
+                        uint32_t a[4];
+                        if (E4) {
+                            const uint32_t y = __byte_perm(w[0][m / 2], w[1][m / 2], m % 2 ? 0x7362 : 0x5140);
+                            const uint32_t z = __byte_perm(w[2][m / 2], w[3][m / 2], m % 2 ? 0x7362 : 0x5140);
+                            a[0] = widen(y);
+                            a[1] = widen(y >> 16);
+                            a[2] = widen(z);
+                            a[3] = widen(z >> 16);
+                        } else {
+                            const int row = (lane & 7) + (lane >> 4) * 8;
+                            load_matrices<true>(a, smem_u32(values) + (b * 16 + row) * P::kRowBytes + (((2 * (j4 + m + col_warp * kJ) + (lane >> 3 & 1)) ^ value_swap<E4, NC>(row)) * 16));
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                            for (int pl = 0; pl < P::PP; pl++) mma<E4>(acc[j4 + m][nt], a[0], a[1], a[2], a[3], pb[b][nt][pl][0], pb[b][nt][pl][1]);
+                    }
+                }
         }
-        if (!x.last) continue;
+        if (remain > 0) continue;
 
         // ---- the end of an item, or of the run inside one
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-            sum[nt] += __shfl_xor_sync(0xffffffffu, sum[nt], 1);
-            sum[nt] += __shfl_xor_sync(0xffffffffu, sum[nt], 2);
-        }
-        const bool ends = x.tile < 0;
-        if (tile0 == 0 && ends) {
-            finish_rows<P>(p, seq, kv, w0, rows, top, sum, acc, most_of, team);
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], o);
+        const bool ends = item.marks & kEnds;
+        if (item.marks == (kOpens | kEnds)) {
+            if (active) finish_rows<P>(p, item, w0, col_warp * P::kCols, top, sum, acc);
             continue;
         }
-        if (team_tid == 0) piece_of[2 * team + !ends] = Piece{from + x.at, x.seq, x.item};
-        if (ends) {
-            float* to = p.heads + (c * P::kTeams + team) * P::kPart;
-            put(to, DP, reinterpret_cast<float2*>(to + RT * DP));
-        }
+        if (team_tid == 0) piece_of[2 * team + !ends] = Piece{from + item.at, item.first_token, item.rows, item.kv, item.row0, item.tiles, 0};
+        if (!ends) break;  // the run's last; its sums wait for the ring to be free
+        put(p.heads + (c * P::kTeams + team) * P::kPart);
     }
     cp_wait<0>();
     __syncthreads();  // the ring is free
-    if (piece_of[2 * team + 1].at >= 0) put(red + team * RT * (DP + 4), DP + 4, red_ml + team * RT);
+    if (piece_of[2 * team + 1].at >= 0) put(red + team * P::kPart);
     __syncthreads();
 
     // ---- what the teams have of the same item, and then the CTAs: the warps are dealt to the items
@@ -944,25 +946,38 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     if (items == 0) return;
     const int crews = min(items, kWarps), size = kWarps / crews, crew = warp / size, crew_tid = tid - crew * size * 32;
     if (crew >= crews) return;
+    auto cta_of = [&](int64_t place) {  // the CTA whose run has it
+        const int64_t split = longer * (each + 1);
+        const bool low = place < split;
+        return (int)((low ? 0 : longer) + div_of(low ? place : place - split, low ? each + 1 : each));
+    };
+#pragma unroll 1
     for (int n = 0; n < items; n++, starts &= starts - 1u) {
         if (n % crews != crew) continue;
         const int i0 = __ffs(starts) - 1;
         const unsigned later = starts & (starts - 1u), of_item = pieces & ~((1u << i0) - 1u) & (later ? (later & (0u - later)) - 1u : 0xffffffffu);
-        const Seq q = seq_of<TP, RT>(p, piece_of[i0].seq);
-        int kv, row0;
-        rows_of(q, piece_of[i0].item, kv, row0);
-        const int n_rows = q.tokens * p.group;
-        const int64_t tiles0 = piece_of[i0].at + P::kEnter, tiles1 = tiles0 + q.tiles;
+        const Piece q = piece_of[i0];
+        const int64_t tiles0 = q.at + P::kEnter, tiles1 = tiles0 + q.tiles;
         const bool whole = tiles0 >= run0 && tiles1 <= run1;
-        const int c0 = whole ? c : cta_of(tiles0), c1 = whole ? c : cta_of(tiles1 - 1);
+        int c0 = c, c1 = c;
+        if (!whole) {
+            c0 = cta_of(tiles0);
+            c1 = cta_of(tiles1 - 1);
+        }
         // CTAs c0 .. c1 have the item; the first kFan of them, the next kFan and so on are joined first
         const int sub = (c - c0) / kFan, first = c0 + sub * kFan, many = min(kFan, c1 - first + 1), subs = (c1 - c0) / kFan + 1;
+#pragma unroll 1
         for (int level = 0;; level++) {
-            // the parts: of the teams, of CTAs, of kFan CTAs
+            // the parts: of the teams, of CTAs, of kFan CTAs; part i in global memory at base + i * step (+ shift, the first)
             const bool done = whole || level == 2 || (level == 1 && subs == 1);
+            const float* const base = level == 0 ? p.heads + c * P::kTeams * P::kPart : level == 1 ? p.parts + first * 2 * P::kPart : p.merged + c0 * 2 * P::kPart;
+            const int step = level == 0 ? P::kPart : level == 1 ? 2 * P::kPart : 2 * kFan * P::kPart, shift = level > 0 && (level == 2 || first == c0) ? P::kPart : 0;
+            float* const result = (level == 0 ? p.parts + (c * 2 + (c == c0)) * P::kPart : p.merged + (first * 2 + (first == c0)) * P::kPart);
+            const unsigned all = level == 0 ? of_item : (1u << (level == 1 ? many : subs)) - 1u;
+#pragma unroll 1
             for (int x = crew_tid; x < RT * DP / 4; x += size * 32) {  // four columns of a row a thread
                 const int row = x / (DP / 4), col = x % (DP / 4) * 4;
-                unsigned rest = level == 0 ? of_item : (1u << (level == 1 ? many : subs)) - 1u;
+                unsigned rest = all;
                 float m = -INFINITY, l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 constexpr int kBatch = 6;  // parts on their way at once
                 while (rest) {
@@ -970,20 +985,20 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     float4 a[kBatch];
 #pragma unroll
                     for (int y = 0; y < kBatch; y++) {
-                        const int i = __ffs(rest) - 1;
-                        rest &= rest - 1u;
                         ml[y] = make_float2(-INFINITY, 0.0f);
                         a[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (i < 0) continue;
+                        if (!rest) continue;
+                        const int i = __ffs(rest) - 1;
+                        rest &= rest - 1u;
+                        const int j = level == 0 ? i / 2 : i;
                         if (level == 0 && i % 2) {
-                            ml[y] = red_ml[i / 2 * RT + row];
-                            a[y] = *reinterpret_cast<const float4*>(red + (i / 2 * RT + row) * (DP + 4) + col);
+                            const float* from_team = red + j * P::kPart;
+                            ml[y] = reinterpret_cast<const float2*>(from_team + RT * P::kRow)[row];
+                            a[y] = *reinterpret_cast<const float4*>(from_team + row * P::kRow + col);
                         } else {
-                            const float* part = level == 0   ? p.heads + (c * P::kTeams + i / 2) * P::kPart
-                                                : level == 1 ? p.parts + ((first + i) * 2 + (first + i == c0)) * P::kPart
-                                                             : p.merged + ((c0 + i * kFan) * 2 + (i == 0)) * P::kPart;
-                            ml[y] = __ldcg(reinterpret_cast<const float2*>(part + RT * DP) + row);
-                            a[y] = __ldcg(reinterpret_cast<const float4*>(part + row * DP + col));
+                            const float* from_part = base + (int64_t)j * step + (j == 0 ? shift : 0);
+                            ml[y] = __ldcg(reinterpret_cast<const float2*>(from_part + RT * P::kRow) + row);
+                            a[y] = __ldcg(reinterpret_cast<const float4*>(from_part + row * P::kRow + col));
                         }
                     }
                     float now = m;
@@ -1005,12 +1020,10 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     }
                 }
                 if (done) {
-                    const int r = row0 + row, token = token_of(p, r);
-                    finish(p, q.first_token + token, kv * p.group + r - token * p.group, col, v, m, l, r < n_rows);
+                    finish<P::WIDE>(p, row_of(p, q, q.row0 + row), col, v, m, l);
                 } else {
-                    float* to = level == 0 ? p.parts + (c * 2 + (c == c0)) * P::kPart : p.merged + (first * 2 + (first == c0)) * P::kPart;
-                    __stcg(reinterpret_cast<float4*>(to + row * DP + col), make_float4(v[0], v[1], v[2], v[3]));
-                    if (col == 0) __stcg(reinterpret_cast<float2*>(to + RT * DP) + row, make_float2(m, l));
+                    __stcg(reinterpret_cast<float4*>(result + row * P::kRow + col), make_float4(v[0], v[1], v[2], v[3]));
+                    if (col == 0) __stcg(reinterpret_cast<float2*>(result + RT * P::kRow) + row, make_float2(m, l));
                 }
             }
             if (done) break;
@@ -1059,20 +1072,21 @@ constexpr int most_teams(int rows) { return rows <= 16 ? 16 : 4; }
 
 template <bool E4, int DP, bool WIDE>
 cudaError_t launch_rows(const AttnArgs& p, cudaStream_t st) {
+    constexpr int kBytes = DP * (E4 ? 1 : 2);
     const int rows = item_rows(p.n_heads / p.cache.n_kv * p.max_new);
-    // columns of a team's warps and warps a CTA
+    // a team's warps by columns, warps a CTA, positions a tile
     if (rows == 8) {
-        constexpr int C = DP == 64 ? 1 : DP == 128 ? (E4 || WIDE ? 1 : 2) : E4 ? (WIDE ? 1 : 2) : WIDE ? 2 : 4;
-        constexpr int W = DP == 64 ? 16 : DP == 128 ? (E4 ? 12 : WIDE ? 8 : 16) : WIDE ? 8 : E4 ? 12 : 16;
-        return launch<Plan<E4, DP, 1, 1, C, W, WIDE>>(p, st);
+        constexpr int C = DP == 64 || E4 || (DP == 128 && WIDE) ? 1 : DP == 128 || WIDE ? 2 : 4;
+        constexpr int W = DP == 64 ? 16 : DP == 128 ? (E4 ? 12 : WIDE ? 8 : 16) : WIDE || E4 ? 8 : 16;
+        return launch<Plan<E4, DP, 1, 1, C, W, kBytes <= 64 ? 32 : 16, WIDE>>(p, st);
     }
     if (rows == 16) {
         constexpr int C = DP == 64 || (DP == 128 && WIDE) ? 1 : 2;
-        return launch<Plan<E4, DP, DP == 256 ? 1 : 2, DP == 256 ? 2 : 1, C, (DP > 64 && WIDE ? 8 : 12), WIDE>>(p, st);
+        return launch<Plan<E4, DP, DP == 256 ? 1 : 2, DP == 256 ? 2 : 1, C, (DP > 64 && WIDE ? 8 : 12), kBytes <= 64 ? 32 : 16, WIDE>>(p, st);
     }
     constexpr int C = DP == 256 && (E4 || !WIDE) ? 2 : 1;
     constexpr int W = DP == 64 ? 12 : DP == 128 ? (WIDE && !E4 ? 8 : 12) : WIDE && !E4 ? 4 : 8;
-    return launch<Plan<E4, DP, 2, 4, C, W, WIDE>>(p, st);
+    return launch<Plan<E4, DP, 2, 4, C, W, kBytes <= 256 ? 32 : 16, WIDE>>(p, st);
 }
 
 }  // namespace attn

@@ -8,9 +8,9 @@
 
 namespace qs {
 
-// x / d for 0 <= x < 2^31 by a product: with 2^shift >= 2^31 * d and mul = ceil(2^shift / d), the product's error is
-// below 1 / d for every such x.  mul < 2^32.
-__device__ __forceinline__ int fast_div(int x, const FastDiv& d) { return (int)(((uint64_t)(uint32_t)x * d.mul) >> d.shift); }
+// x / d for 0 <= x < 2^31 by a product: with 2^(31 + shift) >= 2^31 * d and mul = ceil(2^(31 + shift) / d), the product's
+// error is below 1 / d for every such x.  mul < 2^32; the upper word of 2 x mul is x mul / 2^31.
+__device__ __forceinline__ int fast_div(int x, const FastDiv& d) { return (int)(__umulhi(2u * (uint32_t)x, d.mul) >> d.shift); }
 
 // The place of position pos of a sequence, in bytes of k and v (and floats of the scales, if asked for): -1 where the
 // sequence has no such position or its page id names no page.  pos in 64 bits, as it was computed.

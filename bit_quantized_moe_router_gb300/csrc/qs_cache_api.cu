@@ -69,7 +69,10 @@ bool heads_ok(const qs_heads& x, int n_tokens, int n_heads, int head_dim, bool w
     return !written || distinct({x.token_stride, n_tokens}, {x.head_stride, n_heads}, {0, 1}, head_dim);
 }
 
-bool heads_aligned(const qs_heads& x) { return al16(x.data, x.token_stride, x.dtype) && al16(x.data, x.head_stride, x.dtype); }
+// Every row at 16-byte boundaries; the stride of a dimension of one is never used.
+bool heads_aligned(const qs_heads& x, int n_tokens, int n_heads) {
+    return al16(x.data, n_tokens > 1 ? x.token_stride : 0, x.dtype) && al16(x.data, n_heads > 1 ? x.head_stride : 0, x.dtype);
+}
 
 HeadsView view(const qs_heads& x) {
     const int64_t z = type_size(x.dtype);
@@ -77,9 +80,9 @@ HeadsView view(const qs_heads& x) {
 }
 
 FastDiv fast_div_by(int d) {
-    FastDiv f = {0, 31};
-    while ((1ll << (f.shift - 31)) < d) f.shift++;
-    f.mul = (uint32_t)(((1ull << f.shift) + d - 1) / d);
+    FastDiv f = {0, 0};
+    while ((1ll << f.shift) < d) f.shift++;
+    f.mul = (uint32_t)(((1ull << (31 + f.shift)) + d - 1) / d);
     return f;
 }
 
@@ -116,7 +119,7 @@ bool rows_args(const qs_cache_rows_args& a, bool write, CacheRowsArgs& p) {
     p.k = view(a.k);
     p.v = view(a.v);
     p.n_tokens = a.n_tokens;
-    p.aligned = heads_aligned(a.k) && heads_aligned(a.v);
+    p.aligned = heads_aligned(a.k, a.n_tokens, a.cache.n_kv_heads) && heads_aligned(a.v, a.n_tokens, a.cache.n_kv_heads);
     return true;
 }
 
@@ -153,9 +156,9 @@ int qs_cache_attention(const qs_cache_attention_args* args, void* stream) {
     const int h = a.n_heads, kv = a.cache.n_kv_heads, d = a.cache.head_dim, n = a.n_tokens;
     if (!cache_ok(a.cache, false) || !seqs_ok(a.seqs, a.cache, n) || !attention_shape_ok(h, kv, d, a.max_new)) return QS_ERR_INVALID;
     if (!(a.scale >= -3.0e38f && a.scale <= 3.0e38f) || a.window < 0) return QS_ERR_INVALID;
-    if (!heads_ok(a.q, n, h, d, false)) return QS_ERR_INVALID;
+    if (!heads_ok(a.q, n, h, d, false) || !heads_aligned(a.q, n, h)) return QS_ERR_INVALID;
     if (n > 0 && !a.out.data && !a.codes.q) return QS_ERR_INVALID;
-    if (a.out.data && !heads_ok(a.out, n, h, d, true)) return QS_ERR_INVALID;
+    if (a.out.data && (!heads_ok(a.out, n, h, d, true) || !heads_aligned(a.out, n, h))) return QS_ERR_INVALID;
     if (a.codes.q || a.codes.scale) {
         if (d % kScaleCols || !a.codes.q || !a.codes.scale || ((uintptr_t)a.codes.q & 15u) || a.codes.stride % 16 || ((uintptr_t)a.codes.scale & 3u)) return QS_ERR_INVALID;
         if (!stride_ok(a.codes.stride) || !stride_ok(a.codes.scale_stride)) return QS_ERR_INVALID;
@@ -167,13 +170,10 @@ int qs_cache_attention(const qs_cache_attention_args* args, void* stream) {
     if (!a.workspace || ((uintptr_t)a.workspace & 255u) || a.workspace_bytes < attn_workspace(h, kv, d, a.max_new)) return QS_ERR_WORKSPACE;
     AttnArgs p = {};
     p.cache = view(a.cache);
+    if (!p.places.set(p.cache)) return QS_ERR_UNSUPPORTED;
     p.seqs = view(a.seqs, a.cache);
     p.q = view(a.q);
-    p.q_aligned = heads_aligned(a.q);
-    if (a.out.data) {
-        p.out = view(a.out);
-        p.out_aligned = heads_aligned(a.out);
-    }
+    if (a.out.data) p.out = view(a.out);
     p.codes = static_cast<uint8_t*>(a.codes.q);
     p.codes_scale = a.codes.scale;
     p.codes_stride = a.codes.stride;

@@ -243,8 +243,24 @@ struct CacheRowsArgs {
 cudaError_t launch_cache_write(const CacheRowsArgs& p, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheRowsArgs& p, cudaStream_t st);
 
+// Places of pages and slots as 32-bit numbers of `unit` bytes, the largest power of two that divides their strides.
+struct Units {
+    int page, slot, unit;
+    bool set(const CacheView& c) {
+        const int64_t page_stride = c.n_pages > 1 ? c.page_stride : 0, slot_stride = c.page_size > 1 ? c.slot_stride : 0;
+        unit = 16;
+        while (unit < (1 << 30) && (page_stride | slot_stride) % (2 * unit) == 0) unit *= 2;
+        const int64_t most = 0x7fffffff;
+        if (page_stride / unit > most || slot_stride / unit > most) return false;
+        page = (int)(page_stride / unit);
+        slot = (int)(slot_stride / unit);
+        const double last = (double)page * (c.n_pages > 0 ? c.n_pages - 1 : 0) + (double)slot * (c.page_size - 1);
+        return last <= (double)most;
+    }
+};
 struct AttnArgs {
     CacheView cache;
+    Units places;
     SeqsView seqs;
     HeadsView q, out;  // out.data null: left out
     uint8_t* codes;    // null: left out
@@ -255,7 +271,6 @@ struct AttnArgs {
     int n_tokens, n_heads, max_new, window;
     FastDiv group_div;  // by group, the query heads of a key-value head
     int group;
-    bool q_aligned, out_aligned;
     uint32_t* joined;  // workspace: three counters a CTA, and the parts of items that several teams or CTAs share
     float *parts, *merged, *heads;
 };

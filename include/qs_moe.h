@@ -587,7 +587,7 @@ int qs_cache_read(const qs_cache_rows_args *args, void *stream);
 typedef struct {
     qs_cache cache;
     qs_seqs seqs;
-    qs_heads q, out;  /* [n_tokens x n_heads x head_dim] */
+    qs_heads q, out;  /* [n_tokens x n_heads x head_dim], rows at 16-byte boundaries */
     qs_codes codes;   /* [n_tokens x n_heads * head_dim] */
     float *lse;       /* [n_tokens x n_heads] */
     void *workspace;

@@ -58,7 +58,7 @@ def test_read_refuses_rows_that_coincide(over):
 
 
 @pytest.mark.parametrize("over,code", [(o, INV) for o in BAD_CACHE + BAD_SEQS] + [
-    (dict(q=0), INV), (dict(q=FAKE + 1), INV), (dict(q_dtype=E4M3), INV), (dict(out=0, codes=0, codes_scale=0), INV), (dict(out=FAKE + 1), INV), (dict(out_dtype=E4M3), INV),
+    (dict(q=0), INV), (dict(q=FAKE + 1), INV), (dict(q=FAKE + 2), INV), (dict(q_head=132), INV), (dict(q_token=1028), INV), (dict(out=FAKE + 8), INV), (dict(out_head=132, out_token=1100), INV), (dict(q_dtype=E4M3), INV), (dict(out=0, codes=0, codes_scale=0), INV), (dict(out=FAKE + 1), INV), (dict(out_dtype=E4M3), INV),
     (dict(out_head=0), INV), (dict(out_token=1000), INV), (dict(codes=0), INV), (dict(codes_scale=0), INV), (dict(codes=FAKE + 8), INV),
     (dict(codes_stride=1032), INV), (dict(codes_stride=1008), INV), (dict(codes_scale_stride=7), INV), (dict(codes_scale=FAKE + 1), INV),
     (dict(d=64, head=64, slot=256, page=4096), INV),                     # codes of rows whose heads share a scale

@@ -341,20 +341,25 @@ def test_attention_codes(kind, d, heads, out):
 
 @pytest.mark.parametrize("q_type,out_type", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
 def test_attention_strides_and_alignment(q_type, out_type):
-    """Queries and output as slices of wider rows, at any alignment of an element, and other heads left as they are."""
+    """Queries and output as slices of wider rows at 16-byte boundaries, other heads left as they are; others are refused."""
     c = Paged([70, 33], [2, 1], BF16, kv=2, d=64, page=16)
-    for pad in (0, 1, 3):
+    ws = qm.alloc_cache_attention_workspace(8, 2, 64, 2)
+    for pad in (0, 8, 24):
         q_all = torch.randn(3, 9, 64 + 8 + pad, device="cuda").to(q_type)
         q = q_all[:, 1:9, pad:pad + 64]
         o_all = torch.full((3, 9, 64 + 8 + pad), 3.0, dtype=out_type, device="cuda")
         o = o_all[:, :8, pad:pad + 64]
-        ws = qm.alloc_cache_attention_workspace(8, 2, 64, 2)
         qm.qs_cache_attention(c.cache, c.seqs, q, 0.2, o, ws, max_new=2)
         want = torch.empty(3, 8, 64, dtype=out_type, device="cuda")
         qm.qs_cache_attention(c.cache, c.seqs, q.contiguous(), 0.2, want, ws, max_new=2)
         assert torch.equal(o, want)
         o.fill_(3.0)
         assert (o_all == 3.0).all()
+        for odd in (q_all[:, 1:9, pad + 1:pad + 65], torch.randn(3, 8, 65, device="cuda").to(q_type)[:, :, :64]):
+            with pytest.raises(qm.QsError):
+                qm.qs_cache_attention(c.cache, c.seqs, odd, 0.2, o, ws, max_new=2)
+        with pytest.raises(qm.QsError):
+            qm.qs_cache_attention(c.cache, c.seqs, q, 0.2, o_all[:, :8, pad + 1:pad + 65], ws, max_new=2)
 
 
 def test_attention_one_token_each_without_offsets_or_starts():
