@@ -49,7 +49,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kFan = 12;          // parts of an item that one CTA joins at a time
 constexpr int kMostTeams = 16;
-constexpr int kStatic = 7 * 1024;  // shared memory for tables
+constexpr int kAhead = 64 * 1024;
+constexpr int kStatic = 8 * 1024;  // shared memory for tables
 
 // A kernel's sizes: cache type, columns (head_dim rounded up), 8 rows times NT a warp, teams of R warps with rows of their
 // own times C with columns of their own, W warps a CTA, and whether queries and weights go into the products with all
@@ -72,7 +73,9 @@ struct Plan {
     static constexpr int kRow = DP + 4, kPart = RT * (kRow + 2);  // floats of an item's part: rows of sums, maxima and sums of weights
     static constexpr int kRed = kTeams * kPart * 4;  // the teams' parts, over all of it
     static constexpr int kFit = (kSmemMax - kStatic - kQBytes) / (kTeams * kStage);
-    static constexpr int ST = kFit > 6 ? 6 : kFit;
+    // about 64 KB of copies on their way: with more, SMs get uneven shares of the memory and the last is late
+    static constexpr int kGoal = 1 + (kAhead + kTeams * kStage / 2) / (kTeams * kStage);
+    static constexpr int ST = kGoal < 2 ? (kFit < 2 ? kFit : 2) : kGoal > kFit ? kFit : kGoal;
     static constexpr int kRing = kTeams * ST * kStage;
     static constexpr int kSmem = kQBytes + kRing > kRed ? kQBytes + kRing : kRed;
     static constexpr int kEnter = 2;
@@ -328,6 +331,11 @@ __device__ __forceinline__ int key_swap(int row) { return E4 ? (NC >= 8 ? (row &
 template <bool E4, int NC>
 __device__ __forceinline__ int value_swap(int row) { return E4 ? ((row >> 1) & 3) * 2 & (NC - 1) : row & 7; }
 
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
+
 // What a part with maximum ml.x counts beside the maximum m; one of no positions (-infinity, 0) nothing.
 __device__ __forceinline__ float part_factor(float2 ml, float m) { return ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - m); }
 
@@ -337,8 +345,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     constexpr int DP = P::DP, NT = P::NT, RT = P::RT, TP = P::TP, ST = P::ST, NC = P::kChunks, kJ = P::kPieces;
     constexpr int kWarps = P::kWarps, kThreads = 32 * kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t scan[kWarps], found_base[P::kTeams];
-    __shared__ int found_seq[P::kTeams];
+    __shared__ int64_t scan[kWarps], before_of[kThreads];
     __shared__ unsigned there_of[kWarps][ST];           // a tile's positions that are there
     __shared__ __align__(16) Item item_of[kWarps][ST];  // of the tiles that are a stretch's first
     __shared__ __align__(16) Piece piece_of[2 * P::kTeams];  // of each team: the stretch that begins inside an item and ends with it; the run's last
@@ -368,15 +375,13 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
         const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
     }
+    before_of[tid] = upto - mine;  // within the warp
     if (lane == 31) scan[warp] = upto;
     if (tid < 2 * P::kTeams) piece_of[tid].at = -1;
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-        if (w < warp) upto += scan[w];
-        total += scan[w];
-    }
+    for (int w = 0; w < kWarps; w++) total += scan[w];
     // as many CTAs as have an item's first tile for each team
     const int64_t workers = min((int64_t)gridDim.x, div_of(total - 1, P::kTeams * (P::kEnter + 1)) + 1);
     const int c = blockIdx.x;
@@ -386,25 +391,33 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     const int64_t run0 = c * each + min((int64_t)c, longer), run1 = run0 + each + (c < longer);
     const unsigned length = (unsigned)(run1 - run0);
     auto begin_of = [&](unsigned x) { return length / P::kTeams * x + length % P::kTeams * x / P::kTeams; };
-    // the threads whose sequences the teams begin in say so
-    if (upto > run0 && upto - mine < run1) {
-        int64_t base = upto - mine;
-        for (int s = s0; s < s1; s++) {
-            const int64_t next = s + 1 < s1 ? base + places_of(s) : upto;
-#pragma unroll 1
-            for (unsigned w = 0; w < P::kTeams; w++) {
-                const int64_t from = run0 + begin_of(w);
-                if (from >= base && from < next) {
-                    found_base[w] = base;
-                    found_seq[w] = s;
-                }
-            }
-            base = next;
-        }
-    }
-    __syncthreads();
     const int64_t from = run0 + begin_of(team);
     const int run = (int)(begin_of(team + 1) - begin_of(team));
+    // the last thread whose sequences begin at or before it
+    int64_t base = 0;
+    int seq0 = 0;
+    if (p.seqs.n_seqs > 1 && run > 0) {
+        int of_warp = 0;
+        int64_t sums = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            if (sums <= from) {
+                of_warp = w;
+                base = sums;
+            }
+            sums += scan[w];
+        }
+        const int64_t mine_before = before_of[of_warp * 32 + lane];
+        const unsigned at_or_before = __ballot_sync(0xffffffffu, base + mine_before <= from && (of_warp * 32 + lane) * per < p.seqs.n_seqs);
+        const int of_lane = 31 - __clz(at_or_before);
+        base += __shfl_sync(0xffffffffu, mine_before, of_lane);
+        seq0 = (of_warp * 32 + of_lane) * per;
+        for (int n = 1; n < per && seq0 + 1 < p.seqs.n_seqs; n++, seq0++) {
+            const int64_t x = places_of(seq0);
+            if (from < base + x) break;
+            base += x;
+        }
+    }
 
     // ---- the next tile to copy, kept by all warps of a team alike
     struct {
@@ -417,7 +430,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     bool first = false;
     int ahead = -1;          // a lane's position's place, in units; -1: not there
     int64_t ahead_scale = 0;
-    next.seq = run > 0 ? found_seq[team] : 0;
+    next.seq = seq0;
     next.left = run;
     // a thread copies the 16 bytes `chunk` of the rows chunk_row, chunk_row + kStep, ...; a row's bits above chunk_row's are
     // the pass's, and swap() is of bits
@@ -481,8 +494,19 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                 for (int step = 0; step < P::kSteps; step++) store(step, 0, raw[step][0], raw[step][1]);
             } else {
                 float2 v[P::kSteps][2];
+                if (E4) {  // two steps' columns of a lane are neighbours
 #pragma unroll
-                for (int step = 0; step < P::kSteps; step++)
+                    for (int step = 0; step < P::kSteps; step += 2) {
+                        float y[8];
+                        load8_row<true>(q, P::WIDE ? p.q.dtype : QS_BF16, cols_of(step, 0), n_cols, y);
+                        v[step][0] = make_float2(y[0], y[1]);
+                        v[step][1] = make_float2(y[2], y[3]);
+                        v[step + 1][0] = make_float2(y[4], y[5]);
+                        v[step + 1][1] = make_float2(y[6], y[7]);
+                    }
+                }
+#pragma unroll
+                for (int step = 0; step < (E4 ? 0 : P::kSteps); step++)
 #pragma unroll
                     for (int half = 0; half < 2; half++) {
                         const int col = cols_of(step, half);
@@ -644,7 +668,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             }
             next.items = q.row_tiles * p.cache.n_kv;
             if (i == -ST) {  // the run's first, at any of its places
-                const int64_t in = from - found_base[team];
+                const int64_t in = from - base;
                 next.item = (int)div_of(in, q.tiles + P::kEnter);
                 const int place = (int)(in - (int64_t)next.item * (q.tiles + P::kEnter));
                 tile = max(0, place - P::kEnter);
@@ -968,49 +992,27 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
         const int sub = (c - c0) / kFan, first = c0 + sub * kFan, many = min(kFan, c1 - first + 1), subs = (c1 - c0) / kFan + 1;
 #pragma unroll 1
         for (int level = 0;; level++) {
-            // the parts: of the teams, of CTAs, of kFan CTAs; part i in global memory at base + i * step (+ shift, the first)
+            // the parts: of the teams; of CTAs, of kFan CTAs, part i at base + i * step (+ shift, the first)
             const bool done = whole || level == 2 || (level == 1 && subs == 1);
-            const float* const base = level == 0 ? p.heads + c * P::kTeams * P::kPart : level == 1 ? p.parts + first * 2 * P::kPart : p.merged + c0 * 2 * P::kPart;
-            const int step = level == 0 ? P::kPart : level == 1 ? 2 * P::kPart : 2 * kFan * P::kPart, shift = level > 0 && (level == 2 || first == c0) ? P::kPart : 0;
+            const float* const base = level == 1 ? p.parts + first * 2 * P::kPart : p.merged + c0 * 2 * P::kPart;
+            const int step = level == 1 ? 2 * P::kPart : 2 * kFan * P::kPart, shift = level == 2 || first == c0 ? P::kPart : 0;
             float* const result = (level == 0 ? p.parts + (c * 2 + (c == c0)) * P::kPart : p.merged + (first * 2 + (first == c0)) * P::kPart);
-            const unsigned all = level == 0 ? of_item : (1u << (level == 1 ? many : subs)) - 1u;
+            const int parts = level == 1 ? many : subs;
 #pragma unroll 1
             for (int x = crew_tid; x < RT * DP / 4; x += size * 32) {  // four columns of a row a thread
                 const int row = x / (DP / 4), col = x % (DP / 4) * 4;
-                unsigned rest = all;
                 float m = -INFINITY, l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                constexpr int kBatch = 6;  // parts on their way at once
-                while (rest) {
-                    float2 ml[kBatch];
-                    float4 a[kBatch];
-#pragma unroll
-                    for (int y = 0; y < kBatch; y++) {
-                        ml[y] = make_float2(-INFINITY, 0.0f);
-                        a[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (!rest) continue;
-                        const int i = __ffs(rest) - 1;
-                        rest &= rest - 1u;
-                        const int j = level == 0 ? i / 2 : i;
-                        if (level == 0 && i % 2) {
-                            const float* from_team = red + j * P::kPart;
-                            ml[y] = reinterpret_cast<const float2*>(from_team + RT * P::kRow)[row];
-                            a[y] = *reinterpret_cast<const float4*>(from_team + row * P::kRow + col);
-                        } else {
-                            const float* from_part = base + (int64_t)j * step + (j == 0 ? shift : 0);
-                            ml[y] = __ldcg(reinterpret_cast<const float2*>(from_part + RT * P::kRow) + row);
-                            a[y] = __ldcg(reinterpret_cast<const float4*>(from_part + row * P::kRow + col));
-                        }
-                    }
+                auto add = [&](const float2* ml, const float4* a, auto count) {
                     float now = m;
 #pragma unroll
-                    for (int y = 0; y < kBatch; y++) now = fmaxf(now, ml[y].x);
+                    for (int y = 0; y < count.value; y++) now = fmaxf(now, ml[y].x);
                     const float by = part_factor(make_float2(m, l), now);
                     m = now;
                     l *= by;
 #pragma unroll
                     for (int e = 0; e < 4; e++) v[e] *= by;
 #pragma unroll
-                    for (int y = 0; y < kBatch; y++) {
+                    for (int y = 0; y < count.value; y++) {
                         const float f = part_factor(ml[y], m);
                         l += f * ml[y].y;
                         v[0] += f * a[y].x;
@@ -1018,6 +1020,42 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                         v[2] += f * a[y].z;
                         v[3] += f * a[y].w;
                     }
+                };
+                if (level == 0) {
+#pragma unroll 1
+                    for (unsigned rest = of_item; rest; rest &= rest - 1u) {
+                        const int k = __ffs(rest) - 1;
+                        float2 ml[1];
+                        float4 a[1];
+                        if (k % 2) {
+                            const float* from_team = red + k / 2 * P::kPart;
+                            ml[0] = reinterpret_cast<const float2*>(from_team + RT * P::kRow)[row];
+                            a[0] = *reinterpret_cast<const float4*>(from_team + row * P::kRow + col);
+                        } else {
+                            const float* from_part = p.heads + (c * P::kTeams + k / 2) * P::kPart;
+                            ml[0] = __ldcg(reinterpret_cast<const float2*>(from_part + RT * P::kRow) + row);
+                            a[0] = __ldcg(reinterpret_cast<const float4*>(from_part + row * P::kRow + col));
+                        }
+                        add(ml, a, Count<1>());
+                    }
+                } else {  // all loads on their way before the first is used
+                    const float* at = base + row * P::kRow + col;
+                    const float2* ml_at = reinterpret_cast<const float2*>(base + RT * P::kRow) + row;
+                    constexpr int kMost = 14;
+                    static_assert(kFan <= kMost && (kAttnMaxCtas + kFan - 1) / kFan <= kMost, "parts");
+                    float2 ml[kMost];
+                    float4 a[kMost];
+#pragma unroll
+                    for (int y = 0; y < kMost; y++) {
+                        ml[y] = make_float2(-INFINITY, 0.0f);
+                        a[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (y < parts) {
+                            const int64_t off = (int64_t)y * step + (y == 0 ? shift : 0);
+                            ml[y] = __ldcg(ml_at + off / 2);
+                            a[y] = __ldcg(reinterpret_cast<const float4*>(at + off));
+                        }
+                    }
+                    add(ml, a, Count<kMost>());
                 }
                 if (done) {
                     finish<P::WIDE>(p, row_of(p, q, q.row0 + row), col, v, m, l);
@@ -1027,8 +1065,8 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                 }
             }
             if (done) break;
-            // the last of those that have parts goes on; it leaves the counter at zero
-            __threadfence();
+            // the last of those that have parts goes on; it leaves the counter at zero.  One thread releases and acquires, the
+            // barriers before and after it carry that from and to the others: fences in all threads cost 2 us.
             sync_warps(1 + crew, size);
             if (crew_tid == 0) {
                 uint32_t* counter = p.joined + (level == 1 ? 2 * kAttnMaxCtas + c0 : sub == 0 ? c0 : kAttnMaxCtas + first);
@@ -1040,7 +1078,6 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             const bool last = last_of[crew];
             sync_warps(1 + crew, size);
             if (!last) break;
-            __threadfence();
         }
     }
 }
@@ -1077,8 +1114,8 @@ cudaError_t launch_rows(const AttnArgs& p, cudaStream_t st) {
     // a team's warps by columns, warps a CTA, positions a tile
     if (rows == 8) {
         constexpr int C = DP == 64 || E4 || (DP == 128 && WIDE) ? 1 : DP == 128 || WIDE ? 2 : 4;
-        constexpr int W = DP == 64 ? 16 : DP == 128 ? (E4 ? 12 : WIDE ? 8 : 16) : WIDE || E4 ? 8 : 16;
-        return launch<Plan<E4, DP, 1, 1, C, W, kBytes <= 64 ? 32 : 16, WIDE>>(p, st);
+        constexpr int W = DP == 64 ? 16 : DP == 128 ? (E4 ? 12 : 8) : WIDE || E4 ? 8 : 16;
+        return launch<Plan<E4, DP, 1, 1, C, W, kBytes <= 64 || (!E4 && !WIDE && DP == 128) ? 32 : 16, WIDE>>(p, st);
     }
     if (rows == 16) {
         constexpr int C = DP == 64 || (DP == 128 && WIDE) ? 1 : 2;
