@@ -78,7 +78,7 @@ struct Plan {
     static constexpr int ST = kGoal < 2 ? (kFit < 2 ? kFit : 2) : kGoal > kFit ? kFit : kGoal;
     static constexpr int kRing = kTeams * ST * kStage;
     static constexpr int kSmem = kQBytes + kRing > kRed ? kQBytes + kRing : kRed;
-    static constexpr int kEnter = 2;
+    static constexpr int kTileBase = 12, kEnter = R == 1 ? 4 : 4 * (kTileBase + R), kLeast = kEnter + (R == 1 ? 1 : kTileBase);  // places: of a tile, and of entering an item
     static_assert(ST >= 2 && kSmem + kStatic <= kSmemMax, "shared memory");
     static_assert(kWarps % kTeam == 0 && 32 * kTeam % kChunks == 0 && TP * kChunks % (32 * kTeam) == 0, "copies");
     static_assert(kTeams <= kMostTeams && kTeams <= 16 && kCols % 64 == 0 && (kTeam == 1 || kTeams <= 15), "teams");
@@ -168,6 +168,7 @@ struct Seq {
     int lo_base, hi_base;     // token j sees lo_base + j .. hi_base + j - 1, clipped to the table
     int lo;                   // the first position that any of them sees
     int tiles, row_tiles;     // of an item; row tiles of a head
+    int weight;               // places in the line that a tile takes
 };
 // a / b, b > 0, a >= 0, in 32 bits where both fit.
 __device__ __forceinline__ int64_t div_of(int64_t a, int64_t b) {
@@ -177,8 +178,9 @@ __device__ __forceinline__ int64_t div_of(int64_t a, int64_t b) {
 __device__ __forceinline__ int near_pos(int64_t p, int n) { return (int)(p < -1024 ? -1024 : p > n ? n : p); }
 __device__ __forceinline__ int clip_pos(int p, int n) { return min(max(p, 0), n); }
 
-template <int TP, int RT>
+template <class P>
 __device__ __forceinline__ Seq seq_of(const AttnArgs& p, int s) {
+    constexpr int TP = P::TP, RT = P::RT;
     Seq q;
     q.first_token = s;
     q.tokens = 1;
@@ -193,6 +195,8 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& p, int s) {
     q.lo = clip_pos(q.lo_base, n);
     q.tiles = max(1, (clip_pos(q.hi_base + q.tokens - 1, n) + TP - 1) / TP - q.lo / TP);  // one where nothing is seen: its rows are still written
     q.row_tiles = (q.tokens * p.group + RT - 1) / RT;
+    // where warps share a tile, its time grows with those that have rows
+    q.weight = P::R == 1 ? 1 : P::kTileBase + (min(q.tokens * p.group, RT) + P::kRows - 1) / P::kRows;
     return q;
 }
 
@@ -203,13 +207,13 @@ __device__ __forceinline__ int token_of(const AttnArgs& p, int row) { return fas
 struct Item {
     int first_token, rows, kv, row0;
     int lo_base, hi_base, tiles, marks;
-    int count, pos0, at, unused;  // at: where the item begins in the line, from the run's start
+    int count, pos0, at, weight;  // at: where the item begins in the line, from the run's start
 };
 enum { kOpens = 1, kEnds = 2 };  // the stretch has the item's first tile, its last
 // What a team has of an item that is not whole in its run: where the item begins in the line (-1: nothing), and which.
 struct Piece {
     int64_t at;
-    int first_token, rows, kv, row0, tiles, unused;
+    int first_token, rows, kv, row0, tiles, weight;
 };
 
 // An output row: where it goes.
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     __shared__ __align__(16) Piece piece_of[2 * P::kTeams];  // of each team: the stretch that begins inside an item and ends with it; the run's last
     __shared__ bool last_of[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int team = warp / P::kTeam, team_tid = tid % (32 * P::kTeam), row_warp = warp % P::kTeam / P::C, col_warp = warp % P::C;
+    const int team = warp / P::kTeam, team_tid = tid % (32 * P::kTeam), row_warp = (warp % P::kTeam / P::C + team) % P::R /* dealt to the SM's quarters in turn: the last ones may have no rows */, col_warp = warp % P::C;
     const int n_pos = p.seqs.positions;
     uint8_t* const q_shared = smem + warp * (P::kQBytes / kWarps) + lane * 8;
     uint8_t* const ring = smem + P::kQBytes + team * ST * P::kStage;
@@ -364,8 +368,8 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     const int per = (p.seqs.n_seqs + kThreads - 1) / kThreads;
     const int s0 = min(tid * per, p.seqs.n_seqs), s1 = min(s0 + per, p.seqs.n_seqs);
     auto places_of = [&](int s) {
-        const Seq q = seq_of<TP, RT>(p, s);
-        return (int64_t)(q.tiles + P::kEnter) * (q.row_tiles * p.cache.n_kv);
+        const Seq q = seq_of<P>(p, s);
+        return (int64_t)(q.tiles * q.weight + P::kEnter) * (q.row_tiles * p.cache.n_kv);
     };
     int64_t mine = 0;
     for (int s = s0; s < s1; s++) mine += places_of(s);
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
 #pragma unroll
     for (int w = 0; w < kWarps; w++) total += scan[w];
     // as many CTAs as have an item's first tile for each team
-    const int64_t workers = min((int64_t)gridDim.x, div_of(total - 1, P::kTeams * (P::kEnter + 1)) + 1);
+    const int64_t workers = min((int64_t)gridDim.x, div_of(total - 1, P::kTeams * P::kLeast) + 1);
     const int c = blockIdx.x;
     if (total == 0 || c >= workers) return;
     // equal runs, the first of them a place longer
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
         const float *k_scale, *v_scale;
     } next = {};
     Item entered = {};
-    bool first = false;
+    bool first = false, entered_one = false;
     int ahead = -1;          // a lane's position's place, in units; -1: not there
     int64_t ahead_scale = 0;
     next.seq = seq0;
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
 
     // ---- the rows of the item under way
     struct {
-        int first_token, rows, kv, row0, lo_base, hi_base, tiles, marks, at;
+        int first_token, rows, kv, row0, lo_base, hi_base, tiles, marks, at, weight;
     } item = {};
     int remain = 0, pos0 = 0, w0 = 0, all_lo = 0, all_hi = 0, tile_lo = 0, tile_hi = 0;
     bool active = false;
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
 
     // queries as fragments in the order in which the keys' pieces lie
     auto begin = [&](const Item& x) {
-        item = {x.first_token, x.rows, x.kv, x.row0, x.lo_base, x.hi_base, x.tiles, x.marks, x.at};
+        item = {x.first_token, x.rows, x.kv, x.row0, x.lo_base, x.hi_base, x.tiles, x.marks, x.at, x.weight};
         remain = x.count;
         pos0 = x.pos0;
         w0 = x.row0 + row_warp * P::kRows;
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             sync_warps(1 + team, P::kTeam);
         }
         if (i > -ST) {
-            if (next.left > 0) {
+            if (next.count > 0) {
                 const unsigned found = __ballot_sync(0xffffffffu, ahead >= 0) & kAll;
                 if (lane == 0) {
                     there_of[warp][fill] = found;
@@ -645,15 +649,15 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                 }
                 if (++fill == ST) fill = 0;
                 issued++;
-                next.left--;
+                next.left -= entered.weight;
                 next.count--;
                 next.pos += TP;
             }
             cp_commit();
         }
-        if (next.count == 0 && next.left > 0) {  // an item is entered
-            int at = entered.at + entered.tiles + P::kEnter, tile = 0;
-            if (i > -ST) {
+        while (next.count == 0 && next.left > 0) {  // an item is entered
+            int at = entered.at + entered.tiles * entered.weight + P::kEnter, tile = 0;
+            if (entered_one) {
                 next.left -= P::kEnter;
                 if (++next.item == next.items) {
                     next.item = 0;
@@ -663,16 +667,17 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             Seq q;
             for (;; next.seq++) {
                 next.seq = min(next.seq, p.seqs.n_seqs - 1);
-                q = seq_of<TP, RT>(p, next.seq);
+                q = seq_of<P>(p, next.seq);
                 if (q.tokens > 0 || next.seq + 1 >= p.seqs.n_seqs) break;
             }
             next.items = q.row_tiles * p.cache.n_kv;
-            if (i == -ST) {  // the run's first, at any of its places
+            if (!entered_one) {  // the run's first, at any of its places
                 const int64_t in = from - base;
-                next.item = (int)div_of(in, q.tiles + P::kEnter);
-                const int place = (int)(in - (int64_t)next.item * (q.tiles + P::kEnter));
-                tile = max(0, place - P::kEnter);
-                next.left -= max(0, P::kEnter - place);
+                const int span = q.tiles * q.weight + P::kEnter;
+                next.item = (int)div_of(in, span);
+                const int place = (int)(in - (int64_t)next.item * span);
+                tile = max(0, place - P::kEnter + q.weight - 1) / q.weight;  // the first that begins at or after it
+                next.left -= tile * q.weight + P::kEnter - place;
                 at = -place;
             }
             int kv = next.item, row0 = 0;
@@ -680,10 +685,11 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                 kv = next.item / q.row_tiles;
                 row0 = (next.item - kv * q.row_tiles) * RT;
             }
-            next.count = min(q.tiles - tile, next.left);
+            next.count = max(0, min(q.tiles - tile, (next.left + q.weight - 1) / q.weight));
             next.pos = q.lo / TP * TP + tile * TP + lane % TP;
+            entered_one = true;
             entered = Item{q.first_token, q.tokens * p.group, kv, row0, q.lo_base, q.hi_base, q.tiles, (tile == 0 ? kOpens : 0) | (tile + next.count == q.tiles ? kEnds : 0),
-                           next.count, next.pos - lane % TP, at, 0};
+                           next.count, next.pos - lane % TP, at, q.weight};
             first = true;
             next.lo = lo_of(q.lo_base, row0);
             next.hi = lo_of(q.hi_base, min(row0 + RT, entered.rows) - 1);
@@ -697,7 +703,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             }
         }
         ahead = -1;
-        if (next.left > 0 && next.pos >= next.lo && next.pos < next.hi) {
+        if (next.count > 0 && next.pos >= next.lo && next.pos < next.hi) {
             const int page_of = fast_div(next.pos, p.cache.page_div), slot = next.pos - page_of * p.cache.page_size, page = next.table[page_of];
             if ((unsigned)page < (unsigned)p.cache.n_pages) ahead = page * p.places.page + slot * p.places.slot;
             if (E4) ahead_scale = page * p.cache.scale_page_stride + slot * p.cache.scale_slot_stride;
@@ -951,7 +957,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             if (active) finish_rows<P>(p, item, w0, col_warp * P::kCols, top, sum, acc);
             continue;
         }
-        if (team_tid == 0) piece_of[2 * team + !ends] = Piece{from + item.at, item.first_token, item.rows, item.kv, item.row0, item.tiles, 0};
+        if (team_tid == 0) piece_of[2 * team + !ends] = Piece{from + item.at, item.first_token, item.rows, item.kv, item.row0, item.tiles, item.weight};
         if (!ends) break;  // the run's last; its sums wait for the ring to be free
         put(p.heads + (c * P::kTeams + team) * P::kPart);
     }
@@ -981,12 +987,12 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
         const int i0 = __ffs(starts) - 1;
         const unsigned later = starts & (starts - 1u), of_item = pieces & ~((1u << i0) - 1u) & (later ? (later & (0u - later)) - 1u : 0xffffffffu);
         const Piece q = piece_of[i0];
-        const int64_t tiles0 = q.at + P::kEnter, tiles1 = tiles0 + q.tiles;
-        const bool whole = tiles0 >= run0 && tiles1 <= run1;
+        const int64_t tiles0 = q.at + P::kEnter, last0 = tiles0 + (int64_t)(q.tiles - 1) * q.weight;
+        const bool whole = tiles0 >= run0 && last0 < run1;
         int c0 = c, c1 = c;
         if (!whole) {
             c0 = cta_of(tiles0);
-            c1 = cta_of(tiles1 - 1);
+            c1 = cta_of(last0);
         }
         // CTAs c0 .. c1 have the item; the first kFan of them, the next kFan and so on are joined first
         const int sub = (c - c0) / kFan, first = c0 + sub * kFan, many = min(kFan, c1 - first + 1), subs = (c1 - c0) / kFan + 1;
@@ -1023,20 +1029,27 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                 };
                 if (level == 0) {
 #pragma unroll 1
-                    for (unsigned rest = of_item; rest; rest &= rest - 1u) {
-                        const int k = __ffs(rest) - 1;
-                        float2 ml[1];
-                        float4 a[1];
-                        if (k % 2) {
-                            const float* from_team = red + k / 2 * P::kPart;
-                            ml[0] = reinterpret_cast<const float2*>(from_team + RT * P::kRow)[row];
-                            a[0] = *reinterpret_cast<const float4*>(from_team + row * P::kRow + col);
-                        } else {
-                            const float* from_part = p.heads + (c * P::kTeams + k / 2) * P::kPart;
-                            ml[0] = __ldcg(reinterpret_cast<const float2*>(from_part + RT * P::kRow) + row);
-                            a[0] = __ldcg(reinterpret_cast<const float4*>(from_part + row * P::kRow + col));
+                    for (unsigned rest = of_item; rest;) {
+                        float2 ml[4];
+                        float4 a[4];
+#pragma unroll
+                        for (int y = 0; y < 4; y++) {
+                            ml[y] = make_float2(-INFINITY, 0.0f);
+                            a[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (!rest) continue;
+                            const int k = __ffs(rest) - 1;
+                            rest &= rest - 1u;
+                            if (k % 2) {
+                                const float* from_team = red + k / 2 * P::kPart;
+                                ml[y] = reinterpret_cast<const float2*>(from_team + RT * P::kRow)[row];
+                                a[y] = *reinterpret_cast<const float4*>(from_team + row * P::kRow + col);
+                            } else {
+                                const float* from_part = p.heads + (c * P::kTeams + k / 2) * P::kPart;
+                                ml[y] = __ldcg(reinterpret_cast<const float2*>(from_part + RT * P::kRow) + row);
+                                a[y] = __ldcg(reinterpret_cast<const float4*>(from_part + row * P::kRow + col));
+                            }
                         }
-                        add(ml, a, Count<1>());
+                        add(ml, a, Count<4>());
                     }
                 } else {  // all loads on their way before the first is used
                     const float* at = base + row * P::kRow + col;
@@ -1114,14 +1127,15 @@ cudaError_t launch_rows(const AttnArgs& p, cudaStream_t st) {
     // a team's warps by columns, warps a CTA, positions a tile
     if (rows == 8) {
         constexpr int C = DP == 64 || E4 || (DP == 128 && WIDE) ? 1 : DP == 128 || WIDE ? 2 : 4;
-        constexpr int W = DP == 64 ? 16 : DP == 128 ? (E4 ? 12 : 8) : WIDE || E4 ? 8 : 16;
-        return launch<Plan<E4, DP, 1, 1, C, W, kBytes <= 64 || (!E4 && !WIDE && DP == 128) ? 32 : 16, WIDE>>(p, st);
+        constexpr int W = DP == 64 ? 16 : DP == 128 || WIDE || E4 ? 8 : 16;
+        return launch<Plan<E4, DP, 1, 1, C, W, kBytes <= 64 || (DP == 128 && (E4 || !WIDE)) ? 32 : 16, WIDE>>(p, st);
     }
     if (rows == 16) {
-        constexpr int C = DP == 64 || (DP == 128 && WIDE) ? 1 : 2;
-        return launch<Plan<E4, DP, DP == 256 ? 1 : 2, DP == 256 ? 2 : 1, C, (DP > 64 && WIDE ? 8 : 12), kBytes <= 64 ? 32 : 16, WIDE>>(p, st);
+        constexpr int C = DP == 64 || (DP == 128 && (E4 || WIDE)) ? 1 : 2;
+        constexpr int W = DP == 64 ? 12 : WIDE || (E4 && DP == 128) ? 8 : 12;
+        return launch<Plan<E4, DP, DP == 256 ? 1 : 2, DP == 256 ? 2 : 1, C, W, kBytes <= 64 || (E4 && WIDE && DP == 128) ? 32 : 16, WIDE>>(p, st);
     }
-    constexpr int C = DP == 256 && (E4 || !WIDE) ? 2 : 1;
+    constexpr int C = DP == 256 && !E4 && !WIDE ? 2 : 1;
     constexpr int W = DP == 64 ? 12 : DP == 128 ? (WIDE && !E4 ? 8 : 12) : WIDE && !E4 ? 4 : 8;
     return launch<Plan<E4, DP, 2, 4, C, W, kBytes <= 256 ? 32 : 16, WIDE>>(p, st);
 }

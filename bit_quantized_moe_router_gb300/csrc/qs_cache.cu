@@ -6,15 +6,16 @@
 //
 // Bound: HBM, each row in once and out once.  A head row is held by the lanes that take eight elements each (2 to 32 of
 // them, a power of two), so a warp has one to 16 rows side by side and a row's maximum is at most five shuffles.  A
-// warp takes kPasses such steps of one token, all their loads before the first use: at one row a warp in flight the
-// copy was bound by latency.  The sequence of a token is looked up once a warp.
+// warp takes kPasses such steps of one token, all their loads before the first use and held as they came, since the
+// copies are bound by the bytes on their way: eight steps of bf16 rows (4 KB a warp).  The place of a token is looked
+// up once a warp, while its rows are on their way.
 #include "qs_cache.cuh"
 
 namespace qs {
 
 namespace {
 
-constexpr int kPasses = 4;   // steps of a warp
+constexpr int kPasses = 8;   // steps of a warp
 constexpr int kWarps = 4;    // of a CTA
 
 // One of a token's 2 * n_kv head rows, keys first.
@@ -30,17 +31,40 @@ __device__ __forceinline__ HeadRow head_row(int r, int n_kv) {
     return h;
 }
 
-// Eight elements of a row from column i; VEC: 16-byte aligned rows.
-template <bool VEC>
-__device__ __forceinline__ void load8_at(const void* row, int dtype, int i, float (&v)[8]) {
-    if (VEC) {
-        load8_row<true>(row, dtype, i, i + 8, v);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 8; q++)
-            v[q] = dtype == QS_BF16 ? bf16_lo(static_cast<const uint16_t*>(row)[i + q]) : static_cast<const float*>(row)[i + q];
+// Eight elements of a row from column i, as they are and widened.  VEC: 16-byte aligned rows; B16: bf16, else fp32.
+template <bool VEC, bool B16>
+struct Eight {
+    uint4 a, b;
+    __device__ __forceinline__ void clear() {
+        a = make_uint4(0, 0, 0, 0);
+        if (!B16) b = a;
     }
-}
+    __device__ __forceinline__ void load(const void* row, int i) {
+        if (VEC) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + i * (B16 ? 2 : 4));
+            a = p[0];
+            if (!B16) b = p[1];
+        } else if (B16) {
+            const uint16_t* p = static_cast<const uint16_t*>(row) + i;
+            a = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+        } else {
+            const uint32_t* p = static_cast<const uint32_t*>(row) + i;
+            a = make_uint4(p[0], p[1], p[2], p[3]);
+            b = make_uint4(p[4], p[5], p[6], p[7]);
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if (B16) {
+            v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x);
+            v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
+            v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z);
+            v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+        } else {
+            v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+            v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+        }
+    }
+};
 template <bool VEC>
 __device__ __forceinline__ void store8_at(void* row, int dtype, int i, const float (&v)[8]) {
     if (VEC) {
@@ -54,7 +78,7 @@ __device__ __forceinline__ void store8_at(void* row, int dtype, int i, const flo
     }
 }
 
-template <bool E4, bool VEC>
+template <bool E4, bool VEC, bool B16>
 __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheRowsArgs p) {
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -64,15 +88,14 @@ __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheRow
     if (t >= p.n_tokens) return;
     const int rows = 32 / p.lanes, col = (lane % p.lanes) * 8, first = (unit * kPasses) * rows + lane / p.lanes;
     const bool in = col < p.cache.head_dim;
-    float v[kPasses][8];
+    Eight<VEC, B16> x[kPasses];
 #pragma unroll
     for (int k = 0; k < kPasses; k++) {
         const HeadRow h = head_row(first + k * rows, p.cache.n_kv);
-#pragma unroll
-        for (int q = 0; q < 8; q++) v[k][q] = 0.0f;
+        x[k].clear();
         if (h.there && in) {
-            const HeadsView& x = h.which ? p.v : p.k;
-            load8_at<VEC>(x.data + t * x.token_stride + h.head * x.head_stride, x.dtype, col, v[k]);
+            const HeadsView& from = h.which ? p.v : p.k;
+            x[k].load(from.data + t * from.token_stride + h.head * from.head_stride, col);
         }
     }
     int seq;
@@ -84,18 +107,19 @@ __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheRow
     for (int k = 0; k < kPasses; k++) {
         const HeadRow h = head_row(first + k * rows, p.cache.n_kv);
         uint8_t* row = (h.which ? p.cache.v : p.cache.k) + at.at + h.head * p.cache.head_stride;
+        float v[8];
+        x[k].get(v);
         if (E4) {
             float a = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(v[k][q]));
+            for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(v[q]));
             const BlockCode code(lanes_max(a, p.lanes / 2), 1.0f, kMinAmax);
             if (!h.there || !in) continue;
-            const float* x = v[k];
             *reinterpret_cast<uint2*>(row + col) =
-                make_uint2(code.pair(x[0], x[1]) | (code.pair(x[2], x[3]) << 16), code.pair(x[4], x[5]) | (code.pair(x[6], x[7]) << 16));
+                make_uint2(code.pair(v[0], v[1]) | (code.pair(v[2], v[3]) << 16), code.pair(v[4], v[5]) | (code.pair(v[6], v[7]) << 16));
             if (col == 0) (h.which ? p.cache.v_scale : p.cache.k_scale)[at.scale_at + h.head * p.cache.scale_head_stride] = code.scale;
         } else if (h.there && in) {
-            store8_row<true>(row, QS_BF16, col, col + 8, v[k]);
+            store8_row<true>(row, QS_BF16, col, col + 8, v);
         }
     }
 }
@@ -171,9 +195,14 @@ cudaError_t launch_rows(K kernel, CacheRowsArgs p, cudaStream_t st) {
 
 }  // namespace
 
+template <bool E4>
+static cudaError_t launch_write(const CacheRowsArgs& p, cudaStream_t st) {
+    const bool b16 = p.k.dtype == QS_BF16;  // v's type too
+    if (p.aligned) return b16 ? launch_rows(cache_write_kernel<E4, true, true>, p, st) : launch_rows(cache_write_kernel<E4, true, false>, p, st);
+    return b16 ? launch_rows(cache_write_kernel<E4, false, true>, p, st) : launch_rows(cache_write_kernel<E4, false, false>, p, st);
+}
 cudaError_t launch_cache_write(const CacheRowsArgs& p, cudaStream_t st) {
-    if (p.cache.dtype == QS_E4M3) return p.aligned ? launch_rows(cache_write_kernel<true, true>, p, st) : launch_rows(cache_write_kernel<true, false>, p, st);
-    return p.aligned ? launch_rows(cache_write_kernel<false, true>, p, st) : launch_rows(cache_write_kernel<false, false>, p, st);
+    return p.cache.dtype == QS_E4M3 ? launch_write<true>(p, st) : launch_write<false>(p, st);
 }
 
 cudaError_t launch_cache_read(const CacheRowsArgs& p, cudaStream_t st) {

@@ -114,6 +114,7 @@ bool rows_args(const qs_cache_rows_args& a, bool write, CacheRowsArgs& p) {
     if (!cache_ok(a.cache, write) || !seqs_ok(a.seqs, a.cache, a.n_tokens)) return false;
     for (const qs_heads* x : {&a.k, &a.v})
         if (!heads_ok(*x, a.n_tokens, a.cache.n_kv_heads, a.cache.head_dim, !write)) return false;
+    if (a.k.dtype != a.v.dtype) return false;
     p.cache = view(a.cache);
     p.seqs = view(a.seqs, a.cache);
     p.k = view(a.k);

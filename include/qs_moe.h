@@ -568,7 +568,7 @@ typedef struct {
 typedef struct {
     qs_cache cache;
     qs_seqs seqs;
-    qs_heads k, v;  /* [n_tokens x n_kv_heads x head_dim] */
+    qs_heads k, v;  /* [n_tokens x n_kv_heads x head_dim], of one type */
     int32_t n_tokens;
 } qs_cache_rows_args;
 

@@ -39,7 +39,7 @@ BAD_SEQS = [
 
 @pytest.mark.parametrize("name", ["qs_cache_write", "qs_cache_read"])
 @pytest.mark.parametrize("over", BAD_CACHE + BAD_SEQS + [
-    dict(k=0), dict(v=0), dict(k=FAKE + 1), dict(k_dtype=E4M3), dict(v_dtype=5), dict(k_token=-1), dict(v_head=-128), dict(k_token=1 << 41)], ids=str)
+    dict(k=0), dict(v=0), dict(k=FAKE + 1), dict(k_dtype=E4M3), dict(v_dtype=5), dict(v_dtype=F32), dict(k_token=-1), dict(v_head=-128), dict(k_token=1 << 41)], ids=str)
 def test_rows_refusals(name, over):
     assert call(name, ROWS, over) == INV
     assert getattr(qm.load(), name)(None, None) == INV
