@@ -78,7 +78,7 @@ struct Plan {
     static constexpr int ST = kGoal < 2 ? (kFit < 2 ? kFit : 2) : kGoal > kFit ? kFit : kGoal;
     static constexpr int kRing = kTeams * ST * kStage;
     static constexpr int kSmem = kQBytes + kRing > kRed ? kQBytes + kRing : kRed;
-    static constexpr int kTileBase = 12, kEnter = R == 1 ? 4 : 4 * (kTileBase + R), kLeast = kEnter + (R == 1 ? 1 : kTileBase);  // places: of a tile, and of entering an item
+    static constexpr int kTileBase = 12, kEnter = R == 1 ? 4 : 4 * (kTileBase + R), kLeast = kEnter + (R == 1 ? 1 : kTileBase), kUnsplit = 2 * kEnter * kTeams;  // places: of a tile, and of entering an item
     static_assert(ST >= 2 && kSmem + kStatic <= kSmemMax, "shared memory");
     static_assert(kWarps % kTeam == 0 && 32 * kTeam % kChunks == 0 && TP * kChunks % (32 * kTeam) == 0, "copies");
     static_assert(kTeams <= kMostTeams && kTeams <= 16 && kCols % 64 == 0 && (kTeam == 1 || kTeams <= 15), "teams");
@@ -392,36 +392,52 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     if (total == 0 || c >= workers) return;
     // equal runs, the first of them a place longer
     const int64_t each = div_of(total, workers), longer = total - each * workers;
-    const int64_t run0 = c * each + min((int64_t)c, longer), run1 = run0 + each + (c < longer);
-    const unsigned length = (unsigned)(run1 - run0);
-    auto begin_of = [&](unsigned x) { return length / P::kTeams * x + length % P::kTeams * x / P::kTeams; };
-    const int64_t from = run0 + begin_of(team);
-    const int run = (int)(begin_of(team + 1) - begin_of(team));
-    // the last thread whose sequences begin at or before it
-    int64_t base = 0;
-    int seq0 = 0;
-    if (p.seqs.n_seqs > 1 && run > 0) {
+    auto begin_of_cta = [&](int x) { return x * each + min((int64_t)x, longer); };
+    // where a place lies: its sequence, and where that begins
+    auto find = [&](int64_t place, int64_t& base) {
+        base = 0;
+        if (p.seqs.n_seqs <= 1) return 0;
         int of_warp = 0;
         int64_t sums = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; w++) {
-            if (sums <= from) {
+            if (sums <= place) {
                 of_warp = w;
                 base = sums;
             }
             sums += scan[w];
         }
+        // of that warp's threads the last whose sequences begin at or before it
         const int64_t mine_before = before_of[of_warp * 32 + lane];
-        const unsigned at_or_before = __ballot_sync(0xffffffffu, base + mine_before <= from && (of_warp * 32 + lane) * per < p.seqs.n_seqs);
+        const unsigned at_or_before = __ballot_sync(0xffffffffu, base + mine_before <= place && (of_warp * 32 + lane) * per < p.seqs.n_seqs);
         const int of_lane = 31 - __clz(at_or_before);
         base += __shfl_sync(0xffffffffu, mine_before, of_lane);
-        seq0 = (of_warp * 32 + of_lane) * per;
-        for (int n = 1; n < per && seq0 + 1 < p.seqs.n_seqs; n++, seq0++) {
-            const int64_t x = places_of(seq0);
-            if (from < base + x) break;
+        int s = (of_warp * 32 + of_lane) * per;
+        for (int n = 1; n < per && s + 1 < p.seqs.n_seqs; n++, s++) {
+            const int64_t x = places_of(s);
+            if (place < base + x) break;
             base += x;
         }
-    }
+        return s;
+    };
+    // Runs begin where they fall, but for items of few places, which one CTA has: what sharing such a one over two saves is
+    // less than what joining it costs.
+    auto whole_items = [&](int64_t place) {
+        if (place <= 0 || place >= total) return place;
+        int64_t base;
+        const Seq q = seq_of<P>(p, find(place, base));
+        const int span = q.tiles * q.weight + P::kEnter;
+        if (span > P::kUnsplit) return place;
+        const int in = (int)((place - base) - div_of(place - base, span) * span);
+        return place - in + (2 * in < span ? 0 : span);
+    };
+    const int64_t run0 = whole_items(begin_of_cta(c)), run1 = whole_items(begin_of_cta(c + 1));
+    const unsigned length = (unsigned)(run1 - run0);
+    auto begin_of = [&](unsigned x) { return length / P::kTeams * x + length % P::kTeams * x / P::kTeams; };
+    const int64_t from = run0 + begin_of(team);
+    const int run = (int)(begin_of(team + 1) - begin_of(team));
+    int64_t base;
+    const int seq0 = find(min(from, total - 1), base);
 
     // ---- the next tile to copy, kept by all warps of a team alike
     struct {
@@ -1003,9 +1019,9 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             const float* const base = level == 1 ? p.parts + first * 2 * P::kPart : p.merged + c0 * 2 * P::kPart;
             const int step = level == 1 ? 2 * P::kPart : 2 * kFan * P::kPart, shift = level == 2 || first == c0 ? P::kPart : 0;
             float* const result = (level == 0 ? p.parts + (c * 2 + (c == c0)) * P::kPart : p.merged + (first * 2 + (first == c0)) * P::kPart);
-            const int parts = level == 1 ? many : subs;
+            const int parts = level == 1 ? many : subs, n_real = min(RT, q.rows - q.row0);
 #pragma unroll 1
-            for (int x = crew_tid; x < RT * DP / 4; x += size * 32) {  // four columns of a row a thread
+            for (int x = crew_tid; x < (n_real * (DP / 4) + 31) / 32 * 32; x += size * 32) {  // four columns of a row a thread
                 const int row = x / (DP / 4), col = x % (DP / 4) * 4;
                 float m = -INFINITY, l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 auto add = [&](const float2* ml, const float4* a, auto count) {
@@ -1051,24 +1067,26 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                         }
                         add(ml, a, Count<4>());
                     }
-                } else {  // all loads on their way before the first is used
+                } else {  // seven parts on their way at once
                     const float* at = base + row * P::kRow + col;
                     const float2* ml_at = reinterpret_cast<const float2*>(base + RT * P::kRow) + row;
-                    constexpr int kMost = 14;
-                    static_assert(kFan <= kMost && (kAttnMaxCtas + kFan - 1) / kFan <= kMost, "parts");
-                    float2 ml[kMost];
-                    float4 a[kMost];
+                    constexpr int kBatch = 7;
+#pragma unroll 1
+                    for (int y0 = 0; y0 < parts; y0 += kBatch) {
+                        float2 ml[kBatch];
+                        float4 a[kBatch];
 #pragma unroll
-                    for (int y = 0; y < kMost; y++) {
-                        ml[y] = make_float2(-INFINITY, 0.0f);
-                        a[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (y < parts) {
-                            const int64_t off = (int64_t)y * step + (y == 0 ? shift : 0);
-                            ml[y] = __ldcg(ml_at + off / 2);
-                            a[y] = __ldcg(reinterpret_cast<const float4*>(at + off));
+                        for (int y = 0; y < kBatch; y++) {
+                            ml[y] = make_float2(-INFINITY, 0.0f);
+                            a[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (y0 + y < parts) {
+                                const int64_t off = (int64_t)(y0 + y) * step + (y0 + y == 0 ? shift : 0);
+                                ml[y] = __ldcg(ml_at + off / 2);
+                                a[y] = __ldcg(reinterpret_cast<const float4*>(at + off));
+                            }
                         }
+                        add(ml, a, Count<kBatch>());
                     }
-                    add(ml, a, Count<kMost>());
                 }
                 if (done) {
                     finish<P::WIDE>(p, row_of(p, q, q.row0 + row), col, v, m, l);
