@@ -78,7 +78,7 @@ struct Plan {
     static constexpr int ST = kGoal < 2 ? (kFit < 2 ? kFit : 2) : kGoal > kFit ? kFit : kGoal;
     static constexpr int kRing = kTeams * ST * kStage;
     static constexpr int kSmem = kQBytes + kRing > kRed ? kQBytes + kRing : kRed;
-    static constexpr int kTileBase = 12, kEnter = R == 1 ? 4 : 4 * (kTileBase + R), kLeast = kEnter + (R == 1 ? 1 : kTileBase), kUnsplit = 2 * kEnter * kTeams;  // places: of a tile, and of entering an item
+    static constexpr int kTileBase = 12, kEnter = R == 1 ? 4 : 4 * (kTileBase + R), kLeast = R == 1 ? 2 : kEnter + kTileBase, kUnsplit = 2 * kEnter * kTeams;  // places: of a tile, and of entering an item
     static_assert(ST >= 2 && kSmem + kStatic <= kSmemMax, "shared memory");
     static_assert(kWarps % kTeam == 0 && 32 * kTeam % kChunks == 0 && TP * kChunks % (32 * kTeam) == 0, "copies");
     static_assert(kTeams <= kMostTeams && kTeams <= 16 && kCols % 64 == 0 && (kTeam == 1 || kTeams <= 15), "teams");
@@ -578,8 +578,15 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
 #pragma unroll
                 for (int e = 0; e < 4; e++) acc[j][nt][e] = 0.0f;
     };
-    // one step of the first product: 16 positions' keys with every part of the queries
-    auto score = [&](float (&c)[NT][4], int step, const uint32_t (&a)[4]) {
+    // one step of the first product: 16 positions' keys with every part of the queries.  The tensor cores cut what a sum
+    // drops, always toward zero, so that a long chain of them is off by half a unit a step (2e-6 after 30): with all parts a
+    // step begins at zero and is added with a rounding.
+    auto score = [&](float (&sums)[NT][4], int step, const uint32_t (&a)[4]) {
+        float c[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) c[nt][e] = P::WIDE ? 0.0f : sums[nt][e];
 #pragma unroll
         for (int pl = 0; pl < P::QP; pl++)
 #pragma unroll
@@ -592,6 +599,10 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     mma<E4>(c[nt], a[0], a[1], a[2], a[3], b.x, b.y);
                 }
             }
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) sums[nt][e] = P::WIDE ? sums[nt][e] + c[nt][e] : c[nt][e];
     };
     // the rows' sums as a part: rows of kRow floats, then a maximum and a sum of weights a row
     auto put = [&](float* to) {
@@ -747,7 +758,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             const float* const scales = reinterpret_cast<const float*>(values + TP * P::kRowBytes);
             // S^T = K Q^T: 16 positions down, a warp's rows across.  With one block of positions two sums, of every second step: a
             // product waits three times its own length for the one before.
-            constexpr int kB = TP / 16, kSums = kB == 1 ? 2 : 1;
+            constexpr int kB = TP / 16, kSums = kB == 1 && !P::WIDE ? 2 : 1;
             float sc[kSums * kB][NT][4];
 #pragma unroll
             for (int b = 0; b < kSums * kB; b++)
@@ -953,9 +964,19 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                             load_matrices<true>(a, smem_u32(values) + (b * 16 + row) * P::kRowBytes + (((2 * (j4 + m + col_warp * kJ) + (lane >> 3 & 1)) ^ value_swap<E4, NC>(row)) * 16));
                         }
 #pragma unroll
-                        for (int nt = 0; nt < NT; nt++)
+                        for (int nt = 0; nt < NT; nt++) {
+                            float(&sums)[4] = acc[j4 + m][nt];
+                            if (P::WIDE) {
+                                float one[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                            for (int pl = 0; pl < P::PP; pl++) mma<E4>(acc[j4 + m][nt], a[0], a[1], a[2], a[3], pb[b][nt][pl][0], pb[b][nt][pl][1]);
+                                for (int pl = 0; pl < P::PP; pl++) mma<E4>(one, a[0], a[1], a[2], a[3], pb[b][nt][pl][0], pb[b][nt][pl][1]);
+#pragma unroll
+                                for (int e = 0; e < 4; e++) sums[e] += one[e];
+                            } else {
+#pragma unroll
+                                for (int pl = 0; pl < P::PP; pl++) mma<E4>(sums, a[0], a[1], a[2], a[3], pb[b][nt][pl][0], pb[b][nt][pl][1]);
+                            }
+                        }
                     }
                 }
         }
