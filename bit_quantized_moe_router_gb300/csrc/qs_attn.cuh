@@ -45,6 +45,7 @@ namespace qs {
 namespace attn {
 
 constexpr float kSlack = 8.0f;    // a row's maximum may lag behind by this much (log2) before the sums are scaled
+constexpr float kLift = 7.0f;     // fp16 weights are 2^(score - maximum + kLift), at most 2^15: small ones keep 7 more bits
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kFan = 12;          // parts of an item that one CTA joins at a time
@@ -63,6 +64,7 @@ struct Plan {
     static constexpr int kTeam = R * C, kTeams = kWarps / kTeam, kRows = 8 * NT, RT = R * kRows, kCols = DP / C;
     static constexpr int TP = TP_;
     static constexpr int kStage = 2 * TP * kRowBytes + (E4 ? 2 * TP * 4 : 0);  // keys, values, their scales
+    static constexpr float kUp = E4 ? kLift : 0.0f;
     static constexpr int QP = WIDE ? (E4 ? 2 : 3) : 1, PP = WIDE ? (E4 ? 2 : 3) : (E4 ? 1 : 2);
     static constexpr int kSteps = DP / 16;            // of the first product
     // The queries' fragments: in registers where they fit beside the sums and about 80 others, else in shared memory.
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     uint32_t qf[P::kQInRegs ? P::kSteps : 1][P::kQInRegs ? P::kQEach : 1];
     float row_scale[NT][2];
     float acc[kJ][NT][4];
-    float top[NT][2], sum[NT][2];  // of rows 2 t, 2 t + 1: the maximum, and the sum of weights of this lane's positions
+    float top[NT][2], sum[NT][2];  // of rows 2 t, 2 t + 1: what weights are relative to (the maximum less kUp), and the sum of this lane's
     auto lo_of = [&](int base, int row) { return clip_pos(base + token_of(p, row), n_pos); };  // of lo_base or hi_base, and a row
 
     // queries as fragments in the order in which the keys' pieces lie
@@ -579,14 +581,16 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                 for (int e = 0; e < 4; e++) acc[j][nt][e] = 0.0f;
     };
     // one step of the first product: 16 positions' keys with every part of the queries.  The tensor cores cut what a sum
-    // drops, always toward zero, so that a long chain of them is off by half a unit a step (2e-6 after 30): with all parts a
-    // step begins at zero and is added with a rounding.
-    auto score = [&](float (&sums)[NT][4], int step, const uint32_t (&a)[4]) {
-        float c[NT][4];
+    // drops, always toward zero, so that a long chain of them is off by half a unit a step (2e-6 after 30): with all parts two
+    // steps begin at zero, in `two`, and are added with a rounding.
+    auto score = [&](float (&sums)[NT][4], float (&two)[NT][4], int step, const uint32_t (&a)[4]) {
+        float(&c)[NT][4] = P::WIDE ? two : sums;
+        if (P::WIDE && step % 2 == 0) {
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
+            for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) c[nt][e] = P::WIDE ? 0.0f : sums[nt][e];
+                for (int e = 0; e < 4; e++) c[nt][e] = 0.0f;
+        }
 #pragma unroll
         for (int pl = 0; pl < P::QP; pl++)
 #pragma unroll
@@ -599,10 +603,12 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     mma<E4>(c[nt], a[0], a[1], a[2], a[3], b.x, b.y);
                 }
             }
+        if (P::WIDE && step % 2 == 1) {
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
+            for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) sums[nt][e] = P::WIDE ? sums[nt][e] + c[nt][e] : c[nt][e];
+                for (int e = 0; e < 4; e++) sums[nt][e] += c[nt][e];
+        }
     };
     // the rows' sums as a part: rows of kRow floats, then a maximum and a sum of weights a row
     auto put = [&](float* to) {
@@ -766,6 +772,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int e = 0; e < 4; e++) sc[b][nt][e] = 0.0f;
+            float two[P::WIDE ? kB : 1][NT][4];
             if constexpr (E4) {
 #pragma unroll
                 for (int i4 = 0; i4 < NC / 4; i4++)
@@ -781,7 +788,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
 #pragma unroll
                         for (int h = 0; h < 4; h++) {
                             const uint32_t a[4] = {widen(lo[h]), widen(hi[h]), widen(lo[h] >> 16), widen(hi[h] >> 16)};
-                            score(sc[b + h % kSums * kB], 4 * i4 + h, a);
+                            score(sc[b + h % kSums * kB], two[P::WIDE ? b : 0], 4 * i4 + h, a);
                         }
                     }
             } else {
@@ -793,7 +800,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     for (int b = 0; b < kB; b++) {
                         uint32_t a[4];
                         load_matrices<false>(a, at + 16 * b * P::kRowBytes + (((2 * step + (lane >> 4)) ^ key_swap<E4, NC>(row)) * 16));
-                        score(sc[b + step % kSums * kB], step, a);
+                        score(sc[b + step % kSums * kB], two[P::WIDE ? b : 0], step, a);
                     }
             }
             // scores to weights.  A lane's are of rows 2 t + e at positions 16 b + 8 y + g, sc[b][nt][2 y + e].
@@ -843,18 +850,19 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     float most = -INFINITY;
 #pragma unroll
                     for (int b = 0; b < kB; b++) most = fmaxf(most, fmaxf(sc[b][nt][e] + lv[b][0], sc[b][nt][2 + e] + lv[b][1]));
-                    grown |= most > top[nt][e] + kSlack;
+                    grown |= most > top[nt][e] + (P::kUp + kSlack);
                 }
             if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
-                        float now = top[nt][e];
+                        float now = -INFINITY;
 #pragma unroll
                         for (int b = 0; b < kB; b++) now = fmaxf(now, fmaxf(sc[b][nt][e] + lv[b][0], sc[b][nt][2 + e] + lv[b][1]));
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+                        now = fmaxf(top[nt][e], now - P::kUp);
                         const float by = now == top[nt][e] ? 1.0f : ex2(top[nt][e] - now);
                         top[nt][e] = now;
                         sum[nt][e] *= by;
@@ -935,10 +943,12 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                 clear_mixed();
             }
             // O^T += V^T P^T: 16 columns down, a warp's rows across
+            float tile[P::WIDE ? 4 : 1][NT][4];
 #pragma unroll
-            for (int b = 0; b < kB; b++)
-#pragma unroll
-                for (int j4 = 0; j4 < kJ; j4 += 4) {
+            for (int bj = 0; bj < kB * kJ / 4; bj++) {
+                // with all parts a tile's products begin at zero too: all of its positions for 64 columns, then the next
+                const int b = P::WIDE ? bj % kB : bj / (kJ / 4), j4 = 4 * (P::WIDE ? bj / kB : bj % (kJ / 4));
+                {
                     uint32_t w[4][2];  // e4m3: four positions' eight columns
                     if (E4) {
 #pragma unroll
@@ -965,20 +975,19 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; nt++) {
-                            float(&sums)[4] = acc[j4 + m][nt];
-                            if (P::WIDE) {
-                                float one[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            float(&sums)[4] = P::WIDE ? tile[P::WIDE ? m : 0][nt] : acc[j4 + m][nt];
 #pragma unroll
-                                for (int pl = 0; pl < P::PP; pl++) mma<E4>(one, a[0], a[1], a[2], a[3], pb[b][nt][pl][0], pb[b][nt][pl][1]);
+                            for (int e = 0; e < 4; e++)
+                                if (P::WIDE && b == 0) sums[e] = 0.0f;
 #pragma unroll
-                                for (int e = 0; e < 4; e++) sums[e] += one[e];
-                            } else {
+                            for (int pl = 0; pl < P::PP; pl++) mma<E4>(sums, a[0], a[1], a[2], a[3], pb[b][nt][pl][0], pb[b][nt][pl][1]);
 #pragma unroll
-                                for (int pl = 0; pl < P::PP; pl++) mma<E4>(sums, a[0], a[1], a[2], a[3], pb[b][nt][pl][0], pb[b][nt][pl][1]);
-                            }
+                            for (int e = 0; e < 4; e++)
+                                if (P::WIDE && b == kB - 1) acc[j4 + m][nt][e] += sums[e];
                         }
                     }
                 }
+            }
         }
         if (remain > 0) continue;
 
