@@ -8,32 +8,44 @@
 // Work.  An item is a sequence, a key-value head and a tile of RT rows (a row: a new token and one of the group's
 // heads).  Its positions are cut into tiles of TP.  All items' tiles in one line are dealt to the teams of warps in equal
 // runs, wherever an item begins or ends: lengths are known on the device alone and may be uneven, and an even share of the
-// line keeps every SM busy to the end.  An item inside one team's run is written from its registers.  What a CTA's teams
+// line keeps every SM busy to the end.  Entering an item counts as kEnter places of the line (many short sequences 70 -> 44
+// us), and an item of few places is not split over CTAs (many short windows 65 -> 48 us).  An item inside one team's run is written from its registers.  What a CTA's teams
 // have of the same item is added up in shared memory when their runs end; what several CTAs have of one is joined by the
 // last of them to finish (a counter an item, no waits), above kFan of them in two steps, always in the order of the
-// positions, so the result does not depend on who was last.
+// positions, so the result does not depend on who was last.  (One CTA that read all 76 parts of a long sequence took 100 us.)
 //
-// A team of R warps has a ring of ST tiles in shared memory filled by 16-byte asynchronous copies, which run ahead over the
-// ends of items: pages of any size and order, one lookup a position a tile ahead of its copies; positions that are not
-// there are filled with zeros, never read.  The warps of a team share the tile and have 8 NT rows each; with R = 1 no
-// barrier wider than a warp is met before the run's end.
+// A team of R x C warps has a ring of ST tiles in shared memory filled by 16-byte asynchronous copies, which run ahead over
+// the ends of items: pages of any size and order, one lookup a position a tile ahead of its copies; positions that are not
+// there are filled with zeros, never read.  The warps of a team share the tile; R of them have 8 NT rows each, C of them a
+// share of the output's columns (where a tile is so large that one a warp would not fit).  With R = C = 1 no barrier wider
+// than a warp is met before the run's end.  About 64 KB an SM are on their way: with 128 KB the SMs' shares of the memory
+// became uneven and the last ones late (64 sequences of bf16 218 -> 179 us).
 //
 // Products.  mma.sync m16n8k16 in the cache's own 16-bit values: bf16, or e4m3 widened to fp16 (exact) in registers.
-// tcgen05 would want 64 or 128 rows where there are 8, and the widened codes written back to shared memory first: here
-// the codes pass from shared memory to registers once, and a lane's fragments are whole 16-byte pieces, since the order
-// of the inner dimension is free as long as both operands have the same.  S = Q K^T has the queries down (rows 8..15
-// are empty with NT = 1); its accumulator is, as it lies, the second operand of O^T = V^T P^T, whose first operand is
-// made by interleaving the bytes of a lane's four positions.
+// tcgen05 takes 64 or 128 rows where there are mostly 8, its results have to be fetched for the softmax, and widened
+// codes would go back to shared memory first; at 8 rows mma.sync's 1024 multiply-adds a cycle and SM are 2.5 times what HBM
+// can feed.  At 64 rows (eight heads, eight drafted tokens) they are not, and the kernel reads 2 TB/s there.
+// S^T = K Q^T: 16 positions down, rows across, so that 8 rows leave nothing empty (queries down: twice the products).  bf16 keys
+// and values come by ldmatrix, values transposed; e4m3's are widened from 16- and 8-byte loads, values interleaved by
+// position first.  A lane's weights are transposed by movmatrix into the second operand of O^T = V^T P^T.
 //
 // Roundings.  Scores, maxima, sums and O are fp32.  e4m3 scales stay out of the 16-bit operands: the key's multiplies
-// the score, the value's the weight, and the running maximum is of s' + log2(value scale), so that weights stay below
-// 2^kSlack whatever the scales are.  A weight goes into the product as PP 16-bit parts, each the rounding of what the
+// the score, the value's the weight, and the running maximum is of s' + log2(value scale), so that fp16 weights stay below
+// 2^(kLift + kSlack) whatever the scales are.  A weight goes into the product as PP 16-bit parts, each the rounding of what the
 // ones before leave out: two of bf16 or one of fp16 for bf16 output (off by 2^-16, 2^-11 of the weight), three or two with fp32
 // rows or codes (2^-24, 2^-22).  fp32 queries are QP such parts; for an fp16 product a row is scaled by a power of two.
 //
-// A position that a row does not see never touches it, NaN and infinity included: scores are replaced, and where a
-// tile has positions that some rows see and others do not, the second product is formed for one token's rows at a time
-// with the values that it does not see set to zero.
+// A position that a row does not see never touches it, NaN and infinity included: scores are replaced, and positions that
+// some of an item's rows see and others do not (the drafted tokens' own, the first ones of a window) are added for those rows
+// alone in fp32, their values then cleared before the product.
+//
+// Code that runs once an SM and call costs 3 to 6 cycles an instruction beyond 32 KB, so there is one copy of each part.
+//
+// Measured on one GB300, in a replayed graph, cold (HBM): 64 sequences of up to 8192 positions, 32 heads on 8 of 128
+// columns, bf16 174 us (6.2 TB/s), e4m3 to codes 116 us (4.8 TB/s; 4-byte scales of one head are 32-byte sectors); one
+// token over 131072 positions of 2 e4m3 heads of 256 43 us (3.2 TB/s: 23 us of it enter, add up and join); 1000 positions
+// of 2 bf16 heads of 256 15 us; 16 sequences of up to eight drafted tokens over 16384 positions 105 us; 200 windows of 301
+// positions 50 us.
 #pragma once
 
 #include <algorithm>
@@ -50,12 +62,12 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kFan = 12;          // parts of an item that one CTA joins at a time
 constexpr int kMostTeams = 16;
-constexpr int kAhead = 64 * 1024;
+constexpr int kAhead = 64 * 1024;  // bytes of copies on their way
 constexpr int kStatic = 8 * 1024;  // shared memory for tables
 
 // A kernel's sizes: cache type, columns (head_dim rounded up), 8 rows times NT a warp, teams of R warps with rows of their
-// own times C with columns of their own, W warps a CTA, and whether queries and weights go into the products with all
-// their parts.
+// own times C with columns of their own, W warps a CTA, TP positions a tile, and whether queries and weights go into the
+// products with all their parts.
 template <bool E4_, int DP_, int NT_, int R_, int C_, int W_, int TP_, bool WIDE_>
 struct Plan {
     static constexpr bool E4 = E4_, WIDE = WIDE_;
@@ -75,15 +87,18 @@ struct Plan {
     static constexpr int kRow = DP + 4, kPart = RT * (kRow + 2);  // floats of an item's part: rows of sums, maxima and sums of weights
     static constexpr int kRed = kTeams * kPart * 4;  // the teams' parts, over all of it
     static constexpr int kFit = (kSmemMax - kStatic - kQBytes) / (kTeams * kStage);
-    // about 64 KB of copies on their way: with more, SMs get uneven shares of the memory and the last is late
     static constexpr int kGoal = 1 + (kAhead + kTeams * kStage / 2) / (kTeams * kStage);
     static constexpr int ST = kGoal < 2 ? (kFit < 2 ? kFit : 2) : kGoal > kFit ? kFit : kGoal;
     static constexpr int kRing = kTeams * ST * kStage;
     static constexpr int kSmem = kQBytes + kRing > kRed ? kQBytes + kRing : kRed;
-    static constexpr int kTileBase = 12, kEnter = R == 1 ? 4 : 4 * (kTileBase + R), kLeast = R == 1 ? 2 : kEnter + kTileBase, kUnsplit = 2 * kEnter * kTeams;  // places: of a tile, and of entering an item
+    // Places in the line.  A tile's: one, or where warps share it kTileBase and one more for each warp with rows (a tile takes
+    // nearly as long for 8 rows as for 64).  Entering an item; the least share of a team (one token over 1000 positions: 15.2
+    // us with two places, 17.1 with four); the largest item that is not split over CTAs.
+    static constexpr int kTileBase = 12, kEnter = R == 1 ? 4 : 4 * (kTileBase + R);
+    static constexpr int kLeast = R == 1 ? 2 : kEnter + kTileBase, kUnsplit = 2 * kEnter * kTeams;
     static_assert(ST >= 2 && kSmem + kStatic <= kSmemMax, "shared memory");
     static_assert(kWarps % kTeam == 0 && 32 * kTeam % kChunks == 0 && TP * kChunks % (32 * kTeam) == 0, "copies");
-    static_assert(kTeams <= kMostTeams && kTeams <= 16 && kCols % 64 == 0 && (kTeam == 1 || kTeams <= 15), "teams");
+    static_assert(kTeams <= (RT <= 16 ? kMostTeams : 3) && kTeams <= 16 && kCols % 64 == 0 && (kTeam == 1 || kTeams <= 15), "teams");
     static_assert(!WIDE || DP < kScaleCols || kCols >= kScaleCols, "a scale's columns are one warp's");
 };
 
@@ -357,7 +372,8 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     __shared__ __align__(16) Piece piece_of[2 * P::kTeams];  // of each team: the stretch that begins inside an item and ends with it; the run's last
     __shared__ bool last_of[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int team = warp / P::kTeam, team_tid = tid % (32 * P::kTeam), row_warp = (warp % P::kTeam / P::C + team) % P::R /* dealt to the SM's quarters in turn: the last ones may have no rows */, col_warp = warp % P::C;
+    const int team = warp / P::kTeam, team_tid = tid % (32 * P::kTeam), row_warp = (warp % P::kTeam / P::C + team) % P::R , col_warp = warp % P::C;
+    // (rows dealt to the SM's quarters in turn: an item's last warps may have none)
     const int n_pos = p.seqs.positions;
     uint8_t* const q_shared = smem + warp * (P::kQBytes / kWarps) + lane * 8;
     uint8_t* const ring = smem + P::kQBytes + team * ST * P::kStage;
@@ -388,7 +404,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     int64_t total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; w++) total += scan[w];
-    // as many CTAs as have an item's first tile for each team
+    // as many CTAs as have kLeast places for each team
     const int64_t workers = min((int64_t)gridDim.x, div_of(total - 1, P::kTeams * P::kLeast) + 1);
     const int c = blockIdx.x;
     if (total == 0 || c >= workers) return;
@@ -1163,10 +1179,14 @@ cudaError_t launch(AttnArgs p, cudaStream_t st) {
     return launch_pdl(attn_kernel<P>, dim3((unsigned)ctas), 32 * P::kWarps, P::kSmem, st, p);
 }
 
-// Rows of an item: 8, 16 or 64, each with the plan that was fastest of those that fit the registers and three tiles a team.
+// Rows of an item: 8, 16 or 64, each with the plan that was fastest of those that fit.  Some of the others, us: 64 sequences
+// of bf16, 8 rows a head: two column warps of 8, tiles of 32 178, one of 12, tiles of 16 179 (short sequences 43 and 49), one of 8
+// 184, two of 16 196.  The same in e4m3: one of 8, tiles of 32 125, one of 12, tiles of 16 147, of 16 178.  131072 positions of
+// e4m3, 256 columns: one of 8 46, two of 12 48, two of 16 60.  e4m3, 16 rows: one of 8 68, two of 12 109.  64 rows of bf16: 12
+// warps 104, 8 113, 16 149, 8 of 32 rows each 139.
 constexpr int padded_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 constexpr int item_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 64; }
-constexpr int most_teams(int rows) { return rows <= 16 ? 16 : 4; }
+constexpr int most_teams(int rows) { return rows <= 16 ? 16 : 3; }
 
 template <bool E4, int DP, bool WIDE>
 cudaError_t launch_rows(const AttnArgs& p, cudaStream_t st) {

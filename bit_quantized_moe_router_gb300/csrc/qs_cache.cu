@@ -7,15 +7,15 @@
 // Bound: HBM, each row in once and out once.  A head row is held by the lanes that take eight elements each (2 to 32 of
 // them, a power of two), so a warp has one to 16 rows side by side and a row's maximum is at most five shuffles.  A
 // warp takes kPasses such steps of one token, all their loads before the first use and held as they came, since the
-// copies are bound by the bytes on their way: eight steps of bf16 rows (4 KB a warp).  The place of a token is looked
-// up once a warp, while its rows are on their way.
+// copies are bound by the bytes on their way: eight steps where there are many rows (16384 tokens of 8 heads of 128 into
+// e4m3: 25.1 us with eight, 26.4 with four, 31.7 with two), two where all warps have a place at once (one token of 2 heads of
+// 256: 2.5 us, 3.8 with eight).  The place of a token is looked up once a warp, while its rows are on their way.
 #include "qs_cache.cuh"
 
 namespace qs {
 
 namespace {
 
-constexpr int kPasses = 8;   // steps of a warp
 constexpr int kWarps = 4;    // of a CTA
 
 // One of a token's 2 * n_kv head rows, keys first.
@@ -78,15 +78,14 @@ __device__ __forceinline__ void store8_at(void* row, int dtype, int i, const flo
     }
 }
 
-template <bool E4, bool VEC, bool B16>
+template <int kPasses, bool E4, bool VEC, bool B16>
 __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheRowsArgs p) {
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_launch_next();
-    const int t = (int)(item / p.units), unit = (int)(item % p.units);
     if (t >= p.n_tokens) return;
-    const int rows = 32 / p.lanes, col = (lane % p.lanes) * 8, first = (unit * kPasses) * rows + lane / p.lanes;
+    const int lanes = 1 << p.lane_bits, rows = 32 >> p.lane_bits, col = (lane & (lanes - 1)) * 8, first = blockIdx.y * kPasses * rows + (lane >> p.lane_bits);
     const bool in = col < p.cache.head_dim;
     Eight<VEC, B16> x[kPasses];
 #pragma unroll
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheRow
             float a = 0.0f;
 #pragma unroll
             for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(v[q]));
-            const BlockCode code(lanes_max(a, p.lanes / 2), 1.0f, kMinAmax);
+            const BlockCode code(lanes_max(a, lanes / 2), 1.0f, kMinAmax);
             if (!h.there || !in) continue;
             *reinterpret_cast<uint2*>(row + col) =
                 make_uint2(code.pair(v[0], v[1]) | (code.pair(v[2], v[3]) << 16), code.pair(v[4], v[5]) | (code.pair(v[6], v[7]) << 16));
@@ -124,19 +123,18 @@ __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheRow
     }
 }
 
-template <bool E4, bool VEC>
+template <int kPasses, bool E4, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheRowsArgs p) {
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_launch_next();
-    const int t = (int)(item / p.units), unit = (int)(item % p.units);
     if (t >= p.n_tokens) return;
     int seq;
     int64_t pos;
     if (!token_at(p.seqs, t, seq, pos)) return;
     const Place at = place_of(p.cache, p.seqs, seq, pos);
-    const int rows = 32 / p.lanes, col = (lane % p.lanes) * 8, first = (unit * kPasses) * rows + lane / p.lanes;
+    const int lanes = 1 << p.lane_bits, rows = 32 >> p.lane_bits, col = (lane & (lanes - 1)) * 8, first = blockIdx.y * kPasses * rows + (lane >> p.lane_bits);
     if (col >= p.cache.head_dim) return;
     uint4 raw[kPasses];
     float scale[kPasses];
@@ -182,32 +180,43 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheRows
     }
 }
 
+// few and many: the kernel with two and with eight steps a warp.
 template <class K>
-cudaError_t launch_rows(K kernel, CacheRowsArgs p, cudaStream_t st) {
+cudaError_t launch_rows(K few, K many, CacheRowsArgs p, cudaStream_t st) {
     if (p.n_tokens == 0 || p.seqs.n_seqs == 0) return cudaSuccess;
-    p.lanes = 2;
-    while (p.lanes * 8 < p.cache.head_dim) p.lanes *= 2;
-    const int rows = 32 / p.lanes * kPasses;  // of a unit
-    p.units = (2 * p.cache.n_kv + rows - 1) / rows;
-    const int64_t ctas = ((int64_t)p.n_tokens * p.units + kWarps - 1) / kWarps;
-    return launch_pdl(kernel, dim3((unsigned)ctas), 32 * kWarps, 0, st, p);
+    p.lane_bits = 1;
+    while ((8 << p.lane_bits) < p.cache.head_dim) p.lane_bits++;
+    const int head_rows = 2 * p.cache.n_kv, rows = 32 >> p.lane_bits;  // of a token, of a step
+    const int units = (head_rows + 2 * rows - 1) / (2 * rows);
+    const bool small = (int64_t)p.n_tokens * units <= 152 * 32;        // warps that run at once
+    const dim3 grid((p.n_tokens + kWarps - 1) / kWarps, small ? units : (head_rows + 8 * rows - 1) / (8 * rows));
+    return launch_pdl(small ? few : many, grid, 32 * kWarps, 0, st, p);
+}
+
+template <bool E4, bool VEC, bool B16>
+cudaError_t launch_write(const CacheRowsArgs& p, cudaStream_t st) {
+    return launch_rows(cache_write_kernel<2, E4, VEC, B16>, cache_write_kernel<8, E4, VEC, B16>, p, st);
+}
+template <bool E4, bool VEC>
+cudaError_t launch_read(const CacheRowsArgs& p, cudaStream_t st) {
+    return launch_rows(cache_read_kernel<2, E4, VEC>, cache_read_kernel<8, E4, VEC>, p, st);
 }
 
 }  // namespace
 
-template <bool E4>
-static cudaError_t launch_write(const CacheRowsArgs& p, cudaStream_t st) {
-    const bool b16 = p.k.dtype == QS_BF16;  // v's type too
-    if (p.aligned) return b16 ? launch_rows(cache_write_kernel<E4, true, true>, p, st) : launch_rows(cache_write_kernel<E4, true, false>, p, st);
-    return b16 ? launch_rows(cache_write_kernel<E4, false, true>, p, st) : launch_rows(cache_write_kernel<E4, false, false>, p, st);
-}
 cudaError_t launch_cache_write(const CacheRowsArgs& p, cudaStream_t st) {
-    return p.cache.dtype == QS_E4M3 ? launch_write<true>(p, st) : launch_write<false>(p, st);
+    const bool e4 = p.cache.dtype == QS_E4M3, b16 = p.k.dtype == QS_BF16;  // v's type too
+    if (p.aligned) {
+        if (e4) return b16 ? launch_write<true, true, true>(p, st) : launch_write<true, true, false>(p, st);
+        return b16 ? launch_write<false, true, true>(p, st) : launch_write<false, true, false>(p, st);
+    }
+    if (e4) return b16 ? launch_write<true, false, true>(p, st) : launch_write<true, false, false>(p, st);
+    return b16 ? launch_write<false, false, true>(p, st) : launch_write<false, false, false>(p, st);
 }
 
 cudaError_t launch_cache_read(const CacheRowsArgs& p, cudaStream_t st) {
-    if (p.cache.dtype == QS_E4M3) return p.aligned ? launch_rows(cache_read_kernel<true, true>, p, st) : launch_rows(cache_read_kernel<true, false>, p, st);
-    return p.aligned ? launch_rows(cache_read_kernel<false, true>, p, st) : launch_rows(cache_read_kernel<false, false>, p, st);
+    if (p.cache.dtype == QS_E4M3) return p.aligned ? launch_read<true, true>(p, st) : launch_read<true, false>(p, st);
+    return p.aligned ? launch_read<false, true>(p, st) : launch_read<false, false>(p, st);
 }
 
 }  // namespace qs

@@ -8,7 +8,7 @@ using namespace qs;
 
 namespace {
 
-constexpr int kMaxTokens = 1 << 24, kMaxSeqs = 1 << 20, kMaxHeads = 256, kMaxPositions = 1 << 30, kMaxNew = 256;
+constexpr int kMaxTokens = 1 << 24, kMaxSeqs = 1 << 16, kMaxHeads = 256, kMaxPositions = 1 << 30, kMaxNew = 256;
 
 int done(cudaError_t e) { return e == cudaSuccess ? QS_OK : cuda_fail(e); }
 
@@ -156,7 +156,7 @@ int qs_cache_attention(const qs_cache_attention_args* args, void* stream) {
     const qs_cache_attention_args& a = *args;
     const int h = a.n_heads, kv = a.cache.n_kv_heads, d = a.cache.head_dim, n = a.n_tokens;
     if (!cache_ok(a.cache, false) || !seqs_ok(a.seqs, a.cache, n) || !attention_shape_ok(h, kv, d, a.max_new)) return QS_ERR_INVALID;
-    if (!(a.scale >= -3.0e38f && a.scale <= 3.0e38f) || a.window < 0) return QS_ERR_INVALID;
+    if (!(a.scale >= -1.0e38f && a.scale <= 1.0e38f) || a.window < 0) return QS_ERR_INVALID;
     if (!heads_ok(a.q, n, h, d, false) || !heads_aligned(a.q, n, h)) return QS_ERR_INVALID;
     if (n > 0 && !a.out.data && !a.codes.q) return QS_ERR_INVALID;
     if (a.out.data && (!heads_ok(a.out, n, h, d, true) || !heads_aligned(a.out, n, h))) return QS_ERR_INVALID;

@@ -238,7 +238,7 @@ struct CacheRowsArgs {
     HeadsView k, v;
     int n_tokens;
     bool aligned;      // every row of k and v at 16-byte boundaries
-    int lanes, units;  // set by the launch: lanes of a head row, warps of a token
+    int lane_bits;     // set by the launch: 2^lane_bits lanes a head row
 };
 cudaError_t launch_cache_write(const CacheRowsArgs& p, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheRowsArgs& p, cudaStream_t st);

@@ -537,7 +537,7 @@ int qs_combine_tokens_backward(const qs_combine_backward_args *args, void *strea
  *  - Sequence i's new tokens are rows offsets[i] .. offsets[i + 1] - 1 of the call's
  *    token rows (device int32 [n_seqs + 1], ascending, offsets of one sequence may be equal; NULL: token i is sequence i's only
  *    one, n_tokens == n_seqs), at positions starts[i], starts[i] + 1, ... (device
- *    int32 [n_seqs]; NULL: 0).  n_seqs <= 2^20, n_tokens <= 2^24.  Rows of no sequence, those
+ *    int32 [n_seqs]; NULL: 0).  n_seqs <= 2^16, n_tokens <= 2^24.  Rows of no sequence, those
  *    behind the last one among them, are left alone.  Lengths are read on the
  *    device: a captured graph follows them.
  *  - Sequences may share pages, but not one that a call writes to: two tokens
@@ -613,7 +613,8 @@ typedef struct {
  * key-value head's cache is read once per 64 rows of n_heads / n_kv_heads * max_new.
  * Sums have a fixed order for given lengths (run-to-run identical); a row's bits
  * depend on the other sequences' lengths, by which the work is split.
- * Value scales below 2^-100 keep fewer bits.
+ * Value scales below 2^-100 keep fewer bits.  |scale| <= 1e38.  QS_ERR_UNSUPPORTED where pages and slots, counted in the largest
+ * power of two of bytes that divides their strides, pass 2^31 (34 GB of keys at strides of odd multiples of 16 bytes).
  * workspace: at least qs_cache_attention_workspace_bytes (0 for a bad shape),
  * 256-byte aligned, initialised with qs_workspace_init and used by this entry
  * alone.  One launch. */

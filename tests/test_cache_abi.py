@@ -33,7 +33,7 @@ BAD_CACHE = [
     dict(page=-16), dict(slot=8), dict(head=100), dict(page=1 << 41), dict(spage=-1), dict(n_pages=-1), dict(page_size=0), dict(kv=0), dict(kv=257),
     dict(d=0), dict(d=120), dict(d=272), dict(page_size=(1 << 30) + 1)]
 BAD_SEQS = [
-    dict(table=0), dict(table=FAKE + 2), dict(starts=FAKE + 1), dict(offsets=FAKE + 2), dict(table_stride=4), dict(n_seqs=-1), dict(n_seqs=(1 << 20) + 1),
+    dict(table=0), dict(table=FAKE + 2), dict(starts=FAKE + 1), dict(offsets=FAKE + 2), dict(table_stride=4), dict(n_seqs=-1), dict(n_seqs=(1 << 16) + 1),
     dict(n_seq_pages=-1), dict(n_seq_pages=1 << 27, table_stride=1 << 27), dict(offsets=0), dict(n=-1), dict(n=(1 << 24) + 1)]
 
 
@@ -62,11 +62,18 @@ def test_read_refuses_rows_that_coincide(over):
     (dict(out_head=0), INV), (dict(out_token=1000), INV), (dict(codes=0), INV), (dict(codes_scale=0), INV), (dict(codes=FAKE + 8), INV),
     (dict(codes_stride=1032), INV), (dict(codes_stride=1008), INV), (dict(codes_scale_stride=7), INV), (dict(codes_scale=FAKE + 1), INV),
     (dict(d=64, head=64, slot=256, page=4096), INV),                     # codes of rows whose heads share a scale
-    (dict(lse=FAKE + 2), INV), (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV), (dict(window=-1), INV), (dict(max_new=0), INV),
+    (dict(lse=FAKE + 2), INV), (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV), (dict(scale=2e38), INV), (dict(window=-1), INV), (dict(max_new=0), INV),
     (dict(max_new=257), INV), (dict(h=9), INV), (dict(h=0), INV), (dict(h=2), INV), (dict(ws=0), WS), (dict(ws=FAKE + 16), WS), (dict(bytes=1000), WS)], ids=str)
 def test_attention_refusals(over, code):
     assert call("qs_cache_attention", ATTN, over) == code
     assert qm.load().qs_cache_attention(None, None) == INV
+
+
+def test_attention_refuses_places_past_32_bits():
+    """Places are counted in the largest power of two that divides the pages' and slots' strides: 2^31 of them at most."""
+    odd = dict(page=16 * (1 << 21) + 16, n_pages=1 << 11)      # 16 bytes: 34 GB of them are more
+    assert call("qs_cache_attention", ATTN, odd) == qm.QS_ERR_UNSUPPORTED
+    assert call("qs_cache_attention", ATTN, dict(page=1 << 25, n_pages=1 << 11, n=0)) == qm.QS_OK
 
 
 def test_calls_without_tokens_launch_nothing():

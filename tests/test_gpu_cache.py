@@ -615,6 +615,51 @@ def test_a_decode_step_in_a_graph():
         starts += 1
 
 
+def test_prompt_prefix_decode_and_projection():
+    """As a program uses them: a prompt's rows into the cache, its prefix back as rows, one more token's row, attention over
+    all of it to codes, and the 8-bit projection of these."""
+    heads, kv, d, page, hidden = 8, 2, 128, 32, 384
+    lens, new = [75, 130], [75, 130]
+    c = Paged(lens, new, E4M3, kv=kv, d=d, page=page, seed=11, garbage=False)
+    wide = torch.randn(c.tokens, heads + 2 * kv, d, device="cuda").to(BF16)  # a projection's output: queries, keys, values
+    k, v = wide[:, heads:heads + kv], wide[:, heads + kv:]
+    qm.qs_cache_write(c.cache, c.seqs, k, v)
+    back = torch.empty(c.tokens, kv, d, device="cuda"), torch.empty(c.tokens, kv, d, device="cuda")
+    qm.qs_cache_read(c.cache, c.seqs, *back)
+    for rows, got in ((k, back[0]), (v, back[1])):
+        scale = rows.double().abs().amax(2) / 448
+        assert ((got.double() - rows.double()).abs() <= (2.0 ** -4 + 2.0 ** -20) * rows.double().abs() + 2.0 ** -9 * scale[..., None]).all()
+    # the next token overwrites the last prompt position of each sequence
+    seqs = qm.make_seqs(c.table, torch.tensor([x - 1 for x in lens], dtype=torch.int32, device="cuda"))
+    one = torch.randn(2, heads + 2 * kv, d, device="cuda").to(BF16)
+    qm.qs_cache_write(c.cache, seqs, one[:, heads:heads + kv], one[:, heads + kv:])
+    c.starts, c.offsets, c.new, c.tokens = torch.tensor([x - 1 for x in lens], dtype=torch.int32).cuda(), torch.tensor([0, 1, 2], dtype=torch.int32).cuda(), [1, 1], 2
+    codes, scale = torch.empty(2, heads * d, dtype=E4M3, device="cuda"), torch.empty(2, heads * d // 128, device="cuda")
+    qm.qs_cache_attention(c.cache, seqs, one[:, :heads], d ** -0.5, None, qm.alloc_cache_attention_workspace(heads, kv, d), codes=codes, codes_scale=scale)
+    exact, _, mass, size, most = attend64(c, one[:, :heads], d ** -0.5)
+    tol, _ = bounds(c, one[:, :heads], F32, True, exact, mass, size, most)
+    exact, tol = exact.reshape(2, -1), tol.reshape(2, -1)
+    w = (0.02 * torch.randn(hidden, heads * d, device="cuda")).to(E4M3)
+    ws = torch.rand(hidden // 128, heads * d // 128, device="cuda") + 0.5
+    out = torch.empty(2, hidden, device="cuda")
+    qm.qs_fp8_matmul(codes, scale, w, ws, out, qm.alloc_fp8_matmul_workspace(2, hidden, heads * d))
+    wide_w = w.double() * ws.double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+    # each code is off by 2^-4 of its value and half of the smallest step, the row by its tolerance; the product's sums by 2^-12 in all
+    room = (2.0 ** -4 * exact.abs() + 2.0 ** -9 * scale.double().repeat_interleave(128, 1) + 1.07 * tol + 2.0 ** -12 * exact.abs()) @ wide_w.abs().T
+    assert ((out.double() - exact @ wide_w.T).abs() <= room).all()
+
+
+def test_attention_of_many_tokens_and_heads():
+    """The largest counts of rows: 256 heads to a key-value head, 256 new tokens of a sequence."""
+    check(Paged([300], [3], BF16, kv=1, d=16, page=16), 256)
+    check(Paged([300, 256], [256, 200], E4M3, kv=1, d=64, page=32), 2, max_new=256)
+
+
+@pytest.mark.parametrize("page", [2, 127, 128, 129, 255, 1023, 65535, 65536])
+def test_attention_more_page_sizes(page):
+    check(Paged([400, 3], [2, 1], BF16, kv=1, d=16, page=page, spare_pages=1), 2)
+
+
 def test_bindings_refusals():
     c = Paged([20], [1], BF16, kv=2, d=64)
     q = torch.zeros(1, 4, 64, dtype=BF16, device="cuda")
