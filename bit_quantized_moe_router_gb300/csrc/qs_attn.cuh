@@ -352,11 +352,6 @@ __device__ __forceinline__ int key_swap(int row) { return E4 ? (NC >= 8 ? (row &
 template <bool E4, int NC>
 __device__ __forceinline__ int value_swap(int row) { return E4 ? ((row >> 1) & 3) * 2 & (NC - 1) : row & 7; }
 
-template <int N>
-struct Count {
-    static constexpr int value = N;
-};
-
 // What a part with maximum ml.x counts beside the maximum m; one of no positions (-infinity, 0) nothing.
 __device__ __forceinline__ float part_factor(float2 ml, float m) { return ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - m); }
 
@@ -1036,7 +1031,8 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     unsigned starts = __ballot_sync(0xffffffffu, my_at >= 0 && (!before || at_before != my_at));
     const int items = __popc(starts);
     if (items == 0) return;
-    const int crews = min(items, kWarps), size = kWarps / crews, crew = warp / size, crew_tid = tid - crew * size * 32;
+    // (two of 64 rows one after the other: the last of an item's CTAs has every warp for it)
+    const int crews = RT > 16 && items <= 2 ? 1 : min(items, kWarps), size = kWarps / crews, crew = warp / size, crew_tid = tid - crew * size * 32;
     if (crew >= crews) return;
     auto cta_of = [&](int64_t place) {  // the CTA whose run has it
         const int64_t split = longer * (each + 1);
@@ -1066,79 +1062,77 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             const int step = level == 1 ? 2 * P::kPart : 2 * kFan * P::kPart, shift = level == 2 || first == c0 ? P::kPart : 0;
             float* const result = (level == 0 ? p.parts + (c * 2 + (c == c0)) * P::kPart : p.merged + (first * 2 + (first == c0)) * P::kPart);
             const int parts = level == 1 ? many : subs, n_real = min(RT, q.rows - q.row0);
+            // four columns of a row a thread, of two such pieces at a time where the registers allow, seven parts of each on their way at once
+            constexpr int kPer = kWarps <= 12 ? 2 : 1, kBatch = 7;
+            const int pieces_end = (n_real * (DP / 4) + 31) / 32 * 32;
 #pragma unroll 1
-            for (int x = crew_tid; x < (n_real * (DP / 4) + 31) / 32 * 32; x += size * 32) {  // four columns of a row a thread
-                const int row = x / (DP / 4), col = x % (DP / 4) * 4;
-                float m = -INFINITY, l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                auto add = [&](const float2* ml, const float4* a, auto count) {
-                    float now = m;
+            for (int x0 = crew_tid; x0 < pieces_end; x0 += size * 32 * kPer) {
+                float m[kPer], l[kPer], v[kPer][4];
 #pragma unroll
-                    for (int y = 0; y < count.value; y++) now = fmaxf(now, ml[y].x);
-                    const float by = part_factor(make_float2(m, l), now);
-                    m = now;
-                    l *= by;
-#pragma unroll
-                    for (int e = 0; e < 4; e++) v[e] *= by;
-#pragma unroll
-                    for (int y = 0; y < count.value; y++) {
-                        const float f = part_factor(ml[y], m);
-                        l += f * ml[y].y;
-                        v[0] += f * a[y].x;
-                        v[1] += f * a[y].y;
-                        v[2] += f * a[y].z;
-                        v[3] += f * a[y].w;
-                    }
-                };
-                if (level == 0) {
+                for (int k = 0; k < kPer; k++) {
+                    m[k] = -INFINITY;
+                    l[k] = v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.0f;
+                }
+                unsigned rest = level == 0 ? of_item : (1u << parts) - 1u;
 #pragma unroll 1
-                    for (unsigned rest = of_item; rest;) {
-                        float2 ml[4];
-                        float4 a[4];
+                while (rest) {
+                    float2 ml[kPer][kBatch];
+                    float4 a[kPer][kBatch];
 #pragma unroll
-                        for (int y = 0; y < 4; y++) {
-                            ml[y] = make_float2(-INFINITY, 0.0f);
-                            a[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (!rest) continue;
-                            const int k = __ffs(rest) - 1;
-                            rest &= rest - 1u;
-                            if (k % 2) {
-                                const float* from_team = red + k / 2 * P::kPart;
-                                ml[y] = reinterpret_cast<const float2*>(from_team + RT * P::kRow)[row];
-                                a[y] = *reinterpret_cast<const float4*>(from_team + row * P::kRow + col);
-                            } else {
-                                const float* from_part = p.heads + (c * P::kTeams + k / 2) * P::kPart;
-                                ml[y] = __ldcg(reinterpret_cast<const float2*>(from_part + RT * P::kRow) + row);
-                                a[y] = __ldcg(reinterpret_cast<const float4*>(from_part + row * P::kRow + col));
-                            }
+                    for (int y = 0; y < kBatch; y++) {
+#pragma unroll
+                        for (int k = 0; k < kPer; k++) {
+                            ml[k][y] = make_float2(-INFINITY, 0.0f);
+                            a[k][y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         }
-                        add(ml, a, Count<4>());
+                        if (!rest) continue;
+                        const int i = __ffs(rest) - 1;
+                        rest &= rest - 1u;
+                        const bool shared = level == 0 && i % 2;
+                        const float* const part = shared       ? red + i / 2 * P::kPart
+                                                  : level == 0 ? p.heads + (c * P::kTeams + i / 2) * P::kPart
+                                                               : base + (int64_t)i * step + (i == 0 ? shift : 0);
+#pragma unroll
+                        for (int k = 0; k < kPer; k++) {
+                            const int x = x0 + k * size * 32, row = x / (DP / 4), col = x % (DP / 4) * 4;
+                            if (x >= pieces_end) continue;
+                            const float2* ml_at = reinterpret_cast<const float2*>(part + RT * P::kRow) + row;
+                            const float4* a_at = reinterpret_cast<const float4*>(part + row * P::kRow + col);
+                            ml[k][y] = shared ? *ml_at : __ldcg(ml_at);
+                            a[k][y] = shared ? *a_at : __ldcg(a_at);
+                        }
                     }
-                } else {  // seven parts on their way at once
-                    const float* at = base + row * P::kRow + col;
-                    const float2* ml_at = reinterpret_cast<const float2*>(base + RT * P::kRow) + row;
-                    constexpr int kBatch = 7;
-#pragma unroll 1
-                    for (int y0 = 0; y0 < parts; y0 += kBatch) {
-                        float2 ml[kBatch];
-                        float4 a[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kPer; k++) {
+                        float now = m[k];
+#pragma unroll
+                        for (int y = 0; y < kBatch; y++) now = fmaxf(now, ml[k][y].x);
+                        const float by = part_factor(make_float2(m[k], l[k]), now);
+                        m[k] = now;
+                        l[k] *= by;
+#pragma unroll
+                        for (int e = 0; e < 4; e++) v[k][e] *= by;
 #pragma unroll
                         for (int y = 0; y < kBatch; y++) {
-                            ml[y] = make_float2(-INFINITY, 0.0f);
-                            a[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (y0 + y < parts) {
-                                const int64_t off = (int64_t)(y0 + y) * step + (y0 + y == 0 ? shift : 0);
-                                ml[y] = __ldcg(ml_at + off / 2);
-                                a[y] = __ldcg(reinterpret_cast<const float4*>(at + off));
-                            }
+                            const float f = part_factor(ml[k][y], now);
+                            l[k] += f * ml[k][y].y;
+                            v[k][0] += f * a[k][y].x;
+                            v[k][1] += f * a[k][y].y;
+                            v[k][2] += f * a[k][y].z;
+                            v[k][3] += f * a[k][y].w;
                         }
-                        add(ml, a, Count<kBatch>());
                     }
                 }
-                if (done) {
-                    finish<P::WIDE>(p, row_of(p, q, q.row0 + row), col, v, m, l);
-                } else {
-                    __stcg(reinterpret_cast<float4*>(result + row * P::kRow + col), make_float4(v[0], v[1], v[2], v[3]));
-                    if (col == 0) __stcg(reinterpret_cast<float2*>(result + RT * P::kRow) + row, make_float2(m, l));
+#pragma unroll
+                for (int k = 0; k < kPer; k++) {
+                    const int x = x0 + k * size * 32, row = x / (DP / 4), col = x % (DP / 4) * 4;
+                    if (x >= pieces_end) continue;
+                    if (done) {
+                        finish<P::WIDE>(p, row_of(p, q, q.row0 + row), col, v[k], m[k], l[k]);
+                    } else {
+                        __stcg(reinterpret_cast<float4*>(result + row * P::kRow + col), make_float4(v[k][0], v[k][1], v[k][2], v[k][3]));
+                        if (col == 0) __stcg(reinterpret_cast<float2*>(result + RT * P::kRow) + row, make_float2(m[k], l[k]));
+                    }
                 }
             }
             if (done) break;
