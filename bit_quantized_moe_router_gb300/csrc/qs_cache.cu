@@ -4,12 +4,14 @@
 // v / scale rounded to nearest, ties to even (BlockCode: 448 / amax in two parts, so a code has one rounding before
 // its own).  Reading: code * scale (one fp32 product) or the bf16 value, rounded to the output's type.
 //
-// Bound: HBM, each row in once and out once.  A head row is held by the lanes that take eight elements each (2 to 32 of
-// them, a power of two), so a warp has one to 16 rows side by side and a row's maximum is at most five shuffles.  A
-// warp takes kPasses such steps of one token, all their loads before the first use and held as they came, since the
-// copies are bound by the bytes on their way: eight steps where there are many rows (16384 tokens of 8 heads of 128 into
-// e4m3: 25.1 us with eight, 26.4 with four, 31.7 with two), two where all warps have a place at once (one token of 2 heads of
-// 256: 2.5 us, 3.8 with eight).  The place of a token is looked up once a warp, while its rows are on their way.
+// Bound: HBM, each row in once and out once, and nearly as much the instructions of a row (its maximum, the codes' own
+// rounding, addresses).  A head row is held by the lanes that take eight elements each (2 to 32 of them, a power of two),
+// so a warp has one to 16 rows side by side and a row's maximum is at most five shuffles.  A warp takes kPasses such steps
+// of one token, all their loads before the first use and held as they came: eight steps where there are many rows
+// (16384 tokens of 8 heads of 128 into e4m3: 25.1 us with eight, 26.4 with four, 31.7 with two, and 23.7 with eight since
+// addresses are added up instead of multiplied), two where all warps have a place at once (one token of 2 heads of 256: 2.2
+// us, 3.8 with eight).  The place of a token is looked up once a warp, while its rows are on their way.  On one GB300, cold:
+// that write 23.7 us (4.3 TB/s), 32768 e4m3 tokens of 8 heads of 128 read into bf16 33.3 us (6.1 TB/s).
 #include "qs_cache.cuh"
 
 namespace qs {
@@ -18,18 +20,22 @@ namespace {
 
 constexpr int kWarps = 4;    // of a CTA
 
-// One of a token's 2 * n_kv head rows, keys first.
-struct HeadRow {
-    int which, head;
-    bool there;
+// A lane's head rows of a token, keys' first: r, r + rows, ... of 2 * n_kv.  Addresses go along by additions (as integers:
+// those of the half that a row is not in are never used).
+template <class T>
+struct Walk {
+    T *k, *v;
+    int64_t k_step, v_step;
+    __device__ __forceinline__ Walk(T* keys, T* values, int64_t k_stride, int64_t v_stride, int r, int n_kv, int rows)
+        : k(reinterpret_cast<T*>((uintptr_t)keys + r * k_stride * (int64_t)sizeof(T))),
+          v(reinterpret_cast<T*>((uintptr_t)values + (r - n_kv) * v_stride * (int64_t)sizeof(T))),
+          k_step(rows * k_stride * (int64_t)sizeof(T)), v_step(rows * v_stride * (int64_t)sizeof(T)) {}
+    __device__ __forceinline__ T* row(bool which) const { return which ? v : k; }
+    __device__ __forceinline__ void next() {
+        k = reinterpret_cast<T*>((uintptr_t)k + k_step);
+        v = reinterpret_cast<T*>((uintptr_t)v + v_step);
+    }
 };
-__device__ __forceinline__ HeadRow head_row(int r, int n_kv) {
-    HeadRow h;
-    h.which = r >= n_kv;
-    h.head = r - (h.which ? n_kv : 0);
-    h.there = r < 2 * n_kv;
-    return h;
-}
 
 // Eight elements of a row from column i, as they are and widened.  VEC: 16-byte aligned rows; B16: bf16, else fp32.
 template <bool VEC, bool B16>
@@ -87,25 +93,28 @@ __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheRow
     if (t >= p.n_tokens) return;
     const int lanes = 1 << p.lane_bits, rows = 32 >> p.lane_bits, col = (lane & (lanes - 1)) * 8, first = blockIdx.y * kPasses * rows + (lane >> p.lane_bits);
     const bool in = col < p.cache.head_dim;
+    const int n_kv = p.cache.n_kv;
     Eight<VEC, B16> x[kPasses];
+    Walk<uint8_t> from(p.k.data + t * p.k.token_stride, p.v.data + t * p.v.token_stride, p.k.head_stride, p.v.head_stride, first, n_kv, rows);
 #pragma unroll
     for (int k = 0; k < kPasses; k++) {
-        const HeadRow h = head_row(first + k * rows, p.cache.n_kv);
+        const int r = first + k * rows;
         x[k].clear();
-        if (h.there && in) {
-            const HeadsView& from = h.which ? p.v : p.k;
-            x[k].load(from.data + t * from.token_stride + h.head * from.head_stride, col);
-        }
+        if (in && r < 2 * n_kv) x[k].load(from.row(r >= n_kv), col);
+        from.next();
     }
     int seq;
     int64_t pos;
     if (!token_at(p.seqs, t, seq, pos)) return;
     const Place at = place_of(p.cache, p.seqs, seq, pos);
     if (at.at < 0) return;
+    Walk<uint8_t> to(p.cache.k + at.at, p.cache.v + at.at, p.cache.head_stride, p.cache.head_stride, first, n_kv, rows);
+    Walk<float> scale_to(p.cache.k_scale + at.scale_at, p.cache.v_scale + at.scale_at, p.cache.scale_head_stride, p.cache.scale_head_stride, first, n_kv, rows);
 #pragma unroll
-    for (int k = 0; k < kPasses; k++) {
-        const HeadRow h = head_row(first + k * rows, p.cache.n_kv);
-        uint8_t* row = (h.which ? p.cache.v : p.cache.k) + at.at + h.head * p.cache.head_stride;
+    for (int k = 0; k < kPasses; k++, to.next(), scale_to.next()) {
+        const int r = first + k * rows;
+        const bool there = in && r < 2 * n_kv;
+        uint8_t* row = to.row(r >= n_kv);
         float v[8];
         x[k].get(v);
         if (E4) {
@@ -113,11 +122,11 @@ __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheRow
 #pragma unroll
             for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(v[q]));
             const BlockCode code(lanes_max(a, lanes / 2), 1.0f, kMinAmax);
-            if (!h.there || !in) continue;
+            if (!there) continue;
             *reinterpret_cast<uint2*>(row + col) =
                 make_uint2(code.pair(v[0], v[1]) | (code.pair(v[2], v[3]) << 16), code.pair(v[4], v[5]) | (code.pair(v[6], v[7]) << 16));
-            if (col == 0) (h.which ? p.cache.v_scale : p.cache.k_scale)[at.scale_at + h.head * p.cache.scale_head_stride] = code.scale;
-        } else if (h.there && in) {
+            if (col == 0) *scale_to.row(r >= n_kv) = code.scale;
+        } else if (there) {
             store8_row<true>(row, QS_BF16, col, col + 8, v);
         }
     }
@@ -136,28 +145,32 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheRows
     const Place at = place_of(p.cache, p.seqs, seq, pos);
     const int lanes = 1 << p.lane_bits, rows = 32 >> p.lane_bits, col = (lane & (lanes - 1)) * 8, first = blockIdx.y * kPasses * rows + (lane >> p.lane_bits);
     if (col >= p.cache.head_dim) return;
+    const int n_kv = p.cache.n_kv;
     uint4 raw[kPasses];
     float scale[kPasses];
+    Walk<uint8_t> from(p.cache.k + at.at, p.cache.v + at.at, p.cache.head_stride, p.cache.head_stride, first, n_kv, rows);
+    Walk<float> scale_from(p.cache.k_scale + at.scale_at, p.cache.v_scale + at.scale_at, p.cache.scale_head_stride, p.cache.scale_head_stride, first, n_kv, rows);
 #pragma unroll
-    for (int k = 0; k < kPasses; k++) {
-        const HeadRow h = head_row(first + k * rows, p.cache.n_kv);
+    for (int k = 0; k < kPasses; k++, from.next(), scale_from.next()) {
+        const int r = first + k * rows;
         raw[k] = make_uint4(0, 0, 0, 0);
         scale[k] = 0.0f;
-        if (!h.there || at.at < 0) continue;
-        const uint8_t* row = (h.which ? p.cache.v : p.cache.k) + at.at + h.head * p.cache.head_stride;
+        if (r >= 2 * n_kv || at.at < 0) continue;
+        const uint8_t* row = from.row(r >= n_kv);
         if (E4) {
             const uint2 w = *reinterpret_cast<const uint2*>(row + col);
             raw[k].x = w.x;
             raw[k].y = w.y;
-            scale[k] = (h.which ? p.cache.v_scale : p.cache.k_scale)[at.scale_at + h.head * p.cache.scale_head_stride];
+            scale[k] = *scale_from.row(r >= n_kv);
         } else {
             raw[k] = *reinterpret_cast<const uint4*>(row + 2 * col);
         }
     }
+    Walk<uint8_t> to(p.k.data + t * p.k.token_stride, p.v.data + t * p.v.token_stride, p.k.head_stride, p.v.head_stride, first, n_kv, rows);
 #pragma unroll
-    for (int k = 0; k < kPasses; k++) {
-        const HeadRow h = head_row(first + k * rows, p.cache.n_kv);
-        if (!h.there) continue;
+    for (int k = 0; k < kPasses; k++, to.next()) {
+        const int r = first + k * rows;
+        if (r >= 2 * n_kv) continue;
         float v[8];
         if (E4) {
             const uint32_t w[2] = {raw[k].x, raw[k].y};
@@ -175,8 +188,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheRows
                 v[2 * q + 1] = bf16_hi(w[q]);
             }
         }
-        const HeadsView& x = h.which ? p.v : p.k;
-        store8_at<VEC>(x.data + t * x.token_stride + h.head * x.head_stride, x.dtype, col, v);
+        store8_at<VEC>(to.row(r >= n_kv), p.k.dtype, col, v);
     }
 }
 
