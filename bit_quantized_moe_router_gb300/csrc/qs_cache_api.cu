@@ -166,8 +166,8 @@ int qs_cache_attention(const qs_cache_attention_args* args, void* stream) {
         if (n > 1 && (a.codes.stride < (int64_t)h * d || a.codes.scale_stride < h * d / kScaleCols)) return QS_ERR_INVALID;
     }
     if ((uintptr_t)a.lse & 3u) return QS_ERR_INVALID;
-    // the line of all tiles is counted in 64 bits, times the number of CTAs
-    if ((double)a.seqs.n_seqs * ((double)a.seqs.n_seq_pages * a.cache.page_size / 16 + 2) * kv * ((double)(h / kv) * a.max_new / 8 + 1) > 4.5e15) return QS_ERR_INVALID;
+    // tiles of 16 positions and 8 rows, at most an eighth of the line's places: a CTA's share of these is counted in 32 bits
+    if ((double)a.seqs.n_seqs * ((double)a.seqs.n_seq_pages * a.cache.page_size / 16 + 2) * kv * ((double)(h / kv) * a.max_new / 8 + 1) > 2.0e10) return QS_ERR_UNSUPPORTED;
     if (!a.workspace || ((uintptr_t)a.workspace & 255u) || a.workspace_bytes < attn_workspace(h, kv, d, a.max_new)) return QS_ERR_WORKSPACE;
     AttnArgs p = {};
     p.cache = view(a.cache);

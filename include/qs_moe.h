@@ -614,7 +614,9 @@ typedef struct {
  * Sums have a fixed order for given lengths (run-to-run identical); a row's bits
  * depend on the other sequences' lengths, by which the work is split.
  * Value scales below 2^-100 keep fewer bits.  |scale| <= 1e38.  QS_ERR_UNSUPPORTED where pages and slots, counted in the largest
- * power of two of bytes that divides their strides, pass 2^31 (34 GB of keys at strides of odd multiples of 16 bytes).
+ * power of two of bytes that divides their strides, pass 2^31 (34 GB of keys at strides of odd multiples of 16 bytes), and
+ * where the tables have room for more than 2e10 tiles of 16 positions by 8 rows: n_seqs * (n_seq_pages * page_size / 16 + 2)
+ * * n_kv_heads * (n_heads / n_kv_heads * max_new / 8 + 1).
  * workspace: at least qs_cache_attention_workspace_bytes (0 for a bad shape),
  * 256-byte aligned, initialised with qs_workspace_init and used by this entry
  * alone.  One launch. */

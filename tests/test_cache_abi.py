@@ -76,6 +76,14 @@ def test_attention_refuses_places_past_32_bits():
     assert call("qs_cache_attention", ATTN, dict(page=1 << 25, n_pages=1 << 11, n=0)) == qm.QS_OK
 
 
+def test_attention_refuses_more_tiles_than_a_cta_counts():
+    """2e10 tiles of 16 positions and 8 rows: a CTA's share of the places that these take is a 32-bit number."""
+    room = dict(n=0, n_seqs=1 << 16, n_seq_pages=1 << 13, table_stride=1 << 13)   # 2^16 sequences of 2^17 positions: 3.2e9
+    assert call("qs_cache_attention", ATTN, room) == qm.QS_OK
+    for more in (dict(n_seq_pages=1 << 16, table_stride=1 << 16), dict(n_seq_pages=1 << 26, table_stride=1 << 26), dict(max_new=256, h=256)):
+        assert call("qs_cache_attention", ATTN, {**room, **more}) == qm.QS_ERR_UNSUPPORTED
+
+
 def test_calls_without_tokens_launch_nothing():
     for name, base in (("qs_cache_write", ROWS), ("qs_cache_read", ROWS), ("qs_cache_attention", ATTN)):
         assert call(name, base, dict(n=0)) == qm.QS_OK
