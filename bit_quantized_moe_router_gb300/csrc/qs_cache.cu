@@ -6,12 +6,13 @@
 //
 // Bound: HBM, each row in once and out once, and nearly as much the instructions of a row (its maximum, the codes' own
 // rounding, addresses).  A head row is held by the lanes that take eight elements each (2 to 32 of them, a power of two),
-// so a warp has one to 16 rows side by side and a row's maximum is at most five shuffles.  A warp takes kPasses such steps
-// of one token, all their loads before the first use and held as they came: eight steps where there are many rows
-// (16384 tokens of 8 heads of 128 into e4m3: 25.1 us with eight, 26.4 with four, 31.7 with two, and 23.7 with eight since
-// addresses are added up instead of multiplied), two where all warps have a place at once (one token of 2 heads of 256: 2.2
-// us, 3.8 with eight).  The place of a token is looked up once a warp, while its rows are on their way.  On one GB300, cold:
-// that write 23.7 us (4.3 TB/s), 32768 e4m3 tokens of 8 heads of 128 read into bf16 33.3 us (6.1 TB/s).
+// so a warp has one to 16 rows side by side.  A warp takes kPasses such steps of one token, all their loads before the first
+// use and held as they came: eight steps where there are many rows (16384 tokens of 8 heads of 128 into e4m3, with a
+// butterfly and a reciprocal a row: 25.1 us with eight, 26.4 with four, 31.7 with two), two where all warps have a place
+// at once (one token of 2 heads of 256: 2.2 us, 3.8 with eight).  Of eight steps' rows each is one group of lanes' to reduce and
+// to take the reciprocal of (23.7 -> 20.7 us; addresses added up, not multiplied, were 25.1 -> 23.7).  The place of a token is
+// looked up once a warp, while its rows are on their way.  On one GB300, cold: that write 20.7 us (4.9 TB/s), 32768 e4m3 tokens of
+// 8 heads of 128 read into bf16 33.2 us (6.1 TB/s).
 #include "qs_cache.cuh"
 
 namespace qs {
@@ -70,7 +71,44 @@ struct Eight {
             v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
         }
     }
+    // The largest |v|, a NaN left out; bf16 two at a time.
+    __device__ __forceinline__ float largest() const {
+        if (B16) {
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+            __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+            for (int q = 1; q < 4; q++) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[q])));
+            return fmaxf(__low2float(m), __high2float(m));
+        }
+        float v[8], m = 0.0f;
+        get(v);
+#pragma unroll
+        for (int q = 0; q < 8; q++) m = fmaxf(m, fabsf(v[q]));
+        return m;
+    }
 };
+
+// The maxima of eight rows over the lanes that hold them (8 or more, a power of two): a lane's a[] are its own columns' of
+// each, and it ends with that of the row returned.  Halves are swapped, so that a lane keeps half of the rows at a step: 8
+// shuffles where a butterfly a row takes 24 to 40.
+__device__ __forceinline__ int max_of_rows(float (&a)[8], int lanes, float& most) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int half = 4; half > 0; half >>= 1) {
+        lanes >>= 1;
+        const bool upper = lane & lanes;
+#pragma unroll
+        for (int k = 0; k < half; k++) {
+            const float other = __shfl_xor_sync(0xffffffffu, upper ? a[k] : a[k + half], lanes);
+            a[k] = fmaxf(upper ? a[k + half] : a[k], other);
+        }
+    }
+    const int row = lane / lanes & 7;
+    most = a[0];
+#pragma unroll 1
+    for (int o = lanes >> 1; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    return row;
+}
 template <bool VEC>
 __device__ __forceinline__ void store8_at(void* row, int dtype, int i, const float (&v)[8]) {
     if (VEC) {
@@ -109,23 +147,44 @@ __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheRow
     const Place at = place_of(p.cache, p.seqs, seq, pos);
     if (at.at < 0) return;
     Walk<uint8_t> to(p.cache.k + at.at, p.cache.v + at.at, p.cache.head_stride, p.cache.head_stride, first, n_kv, rows);
-    Walk<float> scale_to(p.cache.k_scale + at.scale_at, p.cache.v_scale + at.scale_at, p.cache.scale_head_stride, p.cache.scale_head_stride, first, n_kv, rows);
+    float* const k_scale = p.cache.k_scale + at.scale_at;
+    float* const v_scale = p.cache.v_scale + at.scale_at;
+    const auto scale_to = [&](int r) { return r < n_kv ? k_scale + r * p.cache.scale_head_stride : v_scale + (r - n_kv) * p.cache.scale_head_stride; };
+    // The rows' factors: with eight rows a group of lanes each has one of them to compute, and all get them from shared memory.
+    __shared__ float2 factor_of[E4 && kPasses == 8 ? kWarps : 1][8][4];
+    const bool dealt = E4 && kPasses == 8 && lanes >= 8;
+    if (dealt) {
+        float a[8], most;
 #pragma unroll
-    for (int k = 0; k < kPasses; k++, to.next(), scale_to.next()) {
+        for (int k = 0; k < 8; k++) a[k] = x[k % kPasses].largest();
+        const int k = max_of_rows(a, lanes, most), r = first + k * rows;
+        const BlockCode code(most, 1.0f, kMinAmax);
+        if ((lane & (lanes / 8 - 1)) == 0) {
+            factor_of[threadIdx.x >> 5][k][lane >> p.lane_bits] = make_float2(code.inv, code.rest);
+            if (r < 2 * n_kv) *scale_to(r) = code.scale;
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int k = 0; k < kPasses; k++, to.next()) {
         const int r = first + k * rows;
         const bool there = in && r < 2 * n_kv;
         uint8_t* row = to.row(r >= n_kv);
         float v[8];
         x[k].get(v);
         if (E4) {
-            float a = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 8; q++) a = fmaxf(a, fabsf(v[q]));
-            const BlockCode code(lanes_max(a, lanes / 2), 1.0f, kMinAmax);
+            BlockCode code;
+            if (dealt) {
+                const float2 f = factor_of[threadIdx.x >> 5][k][lane >> p.lane_bits];
+                code.inv = f.x;
+                code.rest = f.y;
+            } else {
+                code = BlockCode(lanes_max(x[k].largest(), lanes / 2), 1.0f, kMinAmax);
+                if (there && col == 0) *scale_to(r) = code.scale;
+            }
             if (!there) continue;
             *reinterpret_cast<uint2*>(row + col) =
                 make_uint2(code.pair(v[0], v[1]) | (code.pair(v[2], v[3]) << 16), code.pair(v[4], v[5]) | (code.pair(v[6], v[7]) << 16));
-            if (col == 0) *scale_to.row(r >= n_kv) = code.scale;
         } else if (there) {
             store8_row<true>(row, QS_BF16, col, col + 8, v);
         }

@@ -118,6 +118,7 @@ __host__ __device__ constexpr int type_size(int dtype) { return dtype == QS_F32 
 // An infinite a leaves no remainder: all codes of the block are NaNs.
 struct BlockCode {
     float inv, rest, scale;
+    BlockCode() = default;
     __device__ __forceinline__ BlockCode(float a, float factor, float least) {
         a = fmaxf(a, least);
         const float part = __frcp_rn(a);

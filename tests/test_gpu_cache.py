@@ -477,6 +477,51 @@ def test_write_then_read(kind, d, rows_type, kv):
         assert (back[name][c.tokens:] == 9.0).all()
 
 
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [16, 32, 48, 64, 80, 128, 208, 256])
+@pytest.mark.parametrize("rows_type", [BF16, F32], ids=["r16", "r32"])
+@pytest.mark.parametrize("kv,aligned", [(1, True), (3, True), (8, True), (5, False)])
+def test_many_rows_are_written_and_read_as_few(kind, d, rows_type, kv, aligned):
+    """The bytes of one call with 6001 tokens and of calls with 250 are the same, both ways."""
+    n, each, page = 6001, 250, 16
+    pages = -(-n // page) + 1
+    table = torch.randperm(pages, device="cuda", dtype=torch.int32)[None, :-1].contiguous()
+
+    def rows():
+        pad = 0 if aligned else 1
+        return torch.randn(n, kv, d + pad, device="cuda").to(rows_type)[:, :, pad:]
+
+    k, v = rows(), rows()
+    k[0] = 0.0
+    k[1, 0, 3], k[1, 0, 4], k[2, 0, d - 1] = float("nan"), 7.0, float("inf")
+    v[3] = float("nan")
+    v[4] *= 2.0 ** -110
+    v[5, kv - 1, d - 1] = -1000.0
+
+    def cache():
+        t = [torch.zeros(pages, page, kv, d, device="cuda").to(kind) for _ in range(2)]
+        return t + ([torch.zeros(pages, page, kv, device="cuda") for _ in range(2)] if kind is E4M3 else [])
+
+    def seqs(lo, m):
+        return qm.make_seqs(table, torch.tensor([lo], dtype=torch.int32, device="cuda"), torch.tensor([0, m], dtype=torch.int32, device="cuda"))
+
+    one, few = cache(), cache()
+    qm.qs_cache_write(qm.make_cache(*one), seqs(0, n), k, v)
+    for lo in range(0, n, each):
+        m = min(each, n - lo)
+        qm.qs_cache_write(qm.make_cache(*few), seqs(lo, m), k[lo:lo + m], v[lo:lo + m])
+    for x, y in zip(one, few):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    back, pieces = [rows() for _ in range(2)], [rows() for _ in range(2)]
+    qm.qs_cache_read(qm.make_cache(*one), seqs(0, n), *back)
+    for lo in range(0, n, each):
+        m = min(each, n - lo)
+        qm.qs_cache_read(qm.make_cache(*one), seqs(lo, m), *(x[lo:lo + m] for x in pieces))
+    bits = torch.int16 if rows_type is BF16 else torch.int32
+    for x, y in zip(back, pieces):
+        assert torch.equal(x.contiguous().view(bits), y.contiguous().view(bits))
+
+
 def test_codes_are_the_nearest_and_ties_go_to_even():
     c = Paged([300], [300], E4M3, kv=1, d=256, page=32, garbage=False)
     # scale 1: every code's value, the middles between neighbours, and values beside these
