@@ -42,10 +42,10 @@
 // Code that runs once an SM and call costs 3 to 6 cycles an instruction beyond 32 KB, so there is one copy of each part.
 //
 // Measured on one GB300, in a replayed graph, cold (HBM): 64 sequences of up to 8192 positions, 32 heads on 8 of 128
-// columns, bf16 174 us (6.2 TB/s), e4m3 to codes 116 us (4.8 TB/s; 4-byte scales of one head are 32-byte sectors); one
-// token over 131072 positions of 2 e4m3 heads of 256 43 us (3.2 TB/s: 23 us of it enter, add up and join); 1000 positions
-// of 2 bf16 heads of 256 15 us; 16 sequences of up to eight drafted tokens over 16384 positions 105 us; 200 windows of 301
-// positions 50 us.
+// columns, bf16 169 to 183 us (by the lengths drawn, 1.0 to 1.2 GB: 6.2 to 6.7 TB/s), e4m3 to codes 110 to 123 us (5.0 TB/s; 4-byte scales of one head are 32-byte sectors); one
+// token over 131072 positions of 2 e4m3 heads of 256 40 us (3.4 TB/s: 20 us of it enter, add up and join); 1000 positions
+// of 2 bf16 heads of 256 15 us; 16 sequences of up to eight drafted tokens over 16384 positions 101 us; 200 windows of 301
+// positions 48 us.
 #pragma once
 
 #include <algorithm>
