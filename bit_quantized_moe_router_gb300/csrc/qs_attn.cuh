@@ -8,7 +8,7 @@
 // Work.  An item is a sequence, a key-value head and a tile of RT rows (a row: a new token and one of the group's
 // heads).  Its positions are cut into tiles of TP.  All items' tiles in one line are dealt to the teams of warps in equal
 // runs, wherever an item begins or ends: lengths are known on the device alone and may be uneven, and an even share of the
-// line keeps every SM busy to the end.  Entering an item counts as kEnter places of the line (many short sequences 70 -> 44
+// line keeps every SM busy to the end.  Entering an item counts as kEnter places of the line (many short sequences 70 -> 34
 // us), and an item of few places is not split over CTAs (many short windows 65 -> 48 us).  An item inside one team's run is written from its registers.  What a CTA's teams
 // have of the same item is added up in shared memory when their runs end; what several CTAs have of one is joined by the
 // last of them to finish (a counter an item, no waits), above kFan of them in two steps, always in the order of the
@@ -42,10 +42,10 @@
 // Code that runs once an SM and call costs 3 to 6 cycles an instruction beyond 32 KB, so there is one copy of each part.
 //
 // Measured on one GB300, in a replayed graph, cold (HBM): 64 sequences of up to 8192 positions, 32 heads on 8 of 128
-// columns, bf16 169 to 183 us (by the lengths drawn, 1.0 to 1.2 GB: 6.2 to 6.7 TB/s), e4m3 to codes 110 to 123 us (5.0 TB/s; 4-byte scales of one head are 32-byte sectors); one
-// token over 131072 positions of 2 e4m3 heads of 256 40 us (3.4 TB/s: 20 us of it enter, add up and join); 1000 positions
-// of 2 bf16 heads of 256 15 us; 16 sequences of up to eight drafted tokens over 16384 positions 101 us; 200 windows of 301
-// positions 48 us.
+// columns, bf16 169 to 183 us (by the lengths drawn, 1.0 to 1.2 GB: 6.2 to 6.7 TB/s), e4m3 to codes 110 to 123 us (5.0
+// TB/s; 4-byte scales of one head are 32-byte sectors); one token over 131072 positions of 2 e4m3 heads of 256 39 us (3.4 TB/s:
+// 20 us of it enter, add up and join); 1000 positions of 2 bf16 heads of 256 15 us; 16 sequences of up to eight drafted tokens
+// over 16384 positions 101 us; 200 windows of 301 positions 47 us.
 #pragma once
 
 #include <algorithm>
@@ -92,10 +92,12 @@ struct Plan {
     static constexpr int kRing = kTeams * ST * kStage;
     static constexpr int kSmem = kQBytes + kRing > kRed ? kQBytes + kRing : kRed;
     // Places in the line.  A tile's: one, or where warps share it kTileBase and one more for each warp with rows (a tile takes
-    // nearly as long for 8 rows as for 64).  Entering an item; the least share of a team (one token over 1000 positions: 15.2
-    // us with two places, 17.1 with four); the largest item that is not split over CTAs.
-    static constexpr int kTileBase = 12, kEnter = R == 1 ? 4 : 4 * (kTileBase + R);
-    static constexpr int kLeast = R == 1 ? 2 : kEnter + kTileBase, kUnsplit = 2 * kEnter * kTeams;
+    // nearly as long for 8 rows as for 64).  Entering an item, two tiles' where queries are scaled and cut into parts (16 rows of
+    // e4m3: 46.7 us, 49.0 with one, 48.9 with four), one's where they are taken as they lie (many short sequences: 33.5 us, 34.5
+    // with two, 37.2 with four), four's where warps share them (drafted tokens: 102.4 us, 104.7 with two); the least share of a
+    // team (one token over 1000 positions: 15.2 us with two places, 17.1 with four); the largest item that is not split over CTAs.
+    static constexpr int kTileBase = 12, kEnter = R > 1 ? 4 * (kTileBase + R) : E4 || WIDE ? 2 : 1;
+    static constexpr int kLeast = R == 1 ? 2 : kEnter + kTileBase, kUnsplit = 8 * (R == 1 ? 1 : kTileBase + R) * kTeams;
     static_assert(ST >= 2 && kSmem + kStatic <= kSmemMax, "shared memory");
     static_assert(kWarps % kTeam == 0 && 32 * kTeam % kChunks == 0 && TP * kChunks % (32 * kTeam) == 0, "copies");
     static_assert(kTeams <= (RT <= 16 ? kMostTeams : 3) && kTeams <= 16 && kCols % 64 == 0 && (kTeam == 1 || kTeams <= 15), "teams");
