@@ -204,8 +204,9 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& p, int s) {
     q.first_token = s;
     q.tokens = 1;
     if (p.seqs.offsets) {
+        // both clipped before they are subtracted: the difference stays in 32 bits and the rows inside the call's
         q.first_token = min(max(p.seqs.offsets[s], 0), p.n_tokens);
-        q.tokens = min(max(min(p.seqs.offsets[s + 1], p.n_tokens) - q.first_token, 0), p.max_new);
+        q.tokens = min(max(min(max(p.seqs.offsets[s + 1], 0), p.n_tokens) - q.first_token, 0), p.max_new);
     }
     const int64_t start = p.seqs.starts ? p.seqs.starts[s] : 0;
     const int n = p.seqs.positions;
