@@ -829,10 +829,10 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     if (E4) {  // the values' scales count for the maximum, 2^-100 at least: the weight's two factors stay in fp32's range
                         by_key[b][y] = scales[16 * b + 8 * y + g];
                         vs[b][y] = scales[TP + 16 * b + 8 * y + g];
-                        // a position that some rows do not see has weights of 0 for them, which its scale must not make NaNs: it is left to
-                        // its own sums below, with the scale as it is
-                        if (mixed && (pos0 + 16 * b + 8 * y + g < all_lo || pos0 + 16 * b + 8 * y + g >= all_hi)) vs[b][y] = 1.0f;
                         lv[b][y] = fmaxf(lg2(vs[b][y]), -100.0f);
+                        // a position that some rows do not see counts for the maximum as any other, but it is left to its own sums
+                        // below, with the scale as it is: here it has no weight, which may be beyond fp16 without its scale
+                        if (mixed && (pos0 + 16 * b + 8 * y + g < all_lo || pos0 + 16 * b + 8 * y + g >= all_hi)) vs[b][y] = 0.0f;
                     }
                 }
 #pragma unroll
@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                         }
                     }
             }
-            // weights, left in sc, and their parts, transposed to the second product's operand
+            // weights, left in sc, and their parts (e4m3: with the value's scale), transposed to the second product's operand
             uint32_t pb[kB][NT][P::PP][2];
 #pragma unroll
             for (int b = 0; b < kB; b++)
@@ -901,8 +901,8 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                             const float z = sc[b][nt][2 * y + e], ref = top[nt][e] == -INFINITY ? 0.0f : top[nt][e];
                             two[e] = ex2(z - ref);
                             sum[nt][e] += two[e];
-                            if (E4) two[e] *= vs[b][y];
                             sc[b][nt][2 * y + e] = two[e];
+                            if (E4) two[e] *= vs[b][y];
                         }
 #pragma unroll
                         for (int pl = 0; pl < P::PP; pl++) pb[b][nt][pl][y] = transposed(part<E4>(two[0], two[1]));

@@ -1,13 +1,128 @@
-"""Attention over the paged cache at the ends of its ranges."""
+"""Attention over the paged cache at the ends of its ranges: value scales of any size, infinities, offsets that are none.
+
+Tolerances are a row's own (a token and head), from its own scores and scales.  A score is off by delta = (d + 8) 2^-23 scale
+sum |q k| + 2^-22 |s|, a weight by 2 delta + 2^-21 of itself, a sum over n positions by n 2^-23, and the 16-bit parts of a
+weight leave out u_p: 2^-22 with fp32 rows or codes, else 2^-16 (bf16 cache) or 2^-11 (e4m3).  Over e4m3 the argument of a weight's
+exponential has the value scale's logarithm in it, up to |log2 scale| + 16 of a rounding of 2^-24; and the smallest step of an
+fp16 weight is 2^-24 where the row's largest is 2^3 at least, so each position is off by up to 2^-28 of the largest weighted scale:
+    |out - exact| <= u |exact| + (2 delta + n 2^-23 + u_p + 2^-21 + 2^-23 (max |log2 scale| + 16)) sum w |v| + 2^-28 max(w scale) sum |code|
+"""
+import math
+
 import pytest
 import torch
 
 from bit_quantized_moe_router_gb300 import qs_moe as qm
-from test_gpu_cache import BF16, E4M3, Paged
+from test_gpu_cache import BF16, E4M3, F32, U, Paged
 
 pytestmark = pytest.mark.gpu
 
 INF, NAN = float("inf"), float("nan")
+
+
+def rows64(c, q, scale, window=0):
+    """A dict of what is exact and what the tolerances are made of, each per token and head, in 64 bits."""
+    heads, group, eight = q.shape[1], q.shape[1] // c.kv, c.kind is E4M3
+    r = {n: torch.zeros(q.shape, dtype=torch.float64, device="cuda") for n in ("out", "mass", "floor")}
+    r.update({n: torch.zeros(q.shape[:2], dtype=torch.float64, device="cuda") for n in ("size", "most", "lv")})
+    r["lse"] = torch.full(q.shape[:2], -INF, dtype=torch.float64, device="cuda")
+    for i in range(len(c.lens)):
+        k, v, there = c.rows("k", i), c.rows("v", i), c.there(i)
+        if eight:
+            pages = self_pages(c, i)
+            codes = c.v.view(torch.uint8)[pages].view(E4M3).double().flatten(0, 1)
+            scales = c.v_scale[pages].double().flatten(0, 1)
+        for j in range(c.new[i]):
+            t, p = int(c.offsets[i]) + j, int(c.starts[i]) + j
+            at = torch.arange(k.shape[0], device="cuda")
+            seen = (there & (at >= (max(0, p + 1 - window) if window else 0)) & (at <= p)).nonzero().flatten()
+            if not seen.numel():
+                continue
+            kk, vv = k[seen].repeat_interleave(group, 1), v[seen].repeat_interleave(group, 1)
+            x = q[t].double()
+            s = torch.einsum("hd,lhd->hl", x, kk) * scale
+            w = torch.softmax(s, 1)
+            r["out"][t], r["lse"][t] = torch.einsum("hl,lhd->hd", w, vv), torch.logsumexp(s, 1)
+            r["mass"][t] = torch.einsum("hl,lhd->hd", w, vv.abs())
+            r["size"][t] = (torch.einsum("hd,lhd->hl", x.abs(), kk.abs()) * abs(scale)).amax(1)
+            r["most"][t] = s.abs().amax(1)
+            if eight:
+                u = scales[seen].repeat_interleave(group, 1).T  # [heads, positions]
+                r["lv"][t] = torch.log2(u).abs().clamp_max(150.0).amax(1)
+                r["floor"][t] = (w * u).amax(1)[:, None] * codes[seen].repeat_interleave(group, 1).abs().sum(0)
+    return r
+
+
+def self_pages(c, i):
+    there = c.there_pages(i)
+    return torch.where(there, c.table[i].long(), torch.zeros_like(c.table[i].long()))
+
+
+def tolerances(c, r, out_type, wide):
+    """(of the output, of the log-sum)"""
+    eight, n = c.kind is E4M3, max(c.lens)
+    delta = (c.d + 8) * 2.0 ** -23 * r["size"] + 2.0 ** -22 * r["most"]
+    args = 2.0 ** -23 * (r["lv"] + 16) if eight else torch.zeros_like(delta)
+    each = 2 * delta + n * 2.0 ** -23 + (2.0 ** -22 if wide else 2.0 ** -11 if eight else 2.0 ** -16) + 2.0 ** -21 + args
+    out = U[out_type] * r["out"].abs() + each[..., None] * r["mass"] + 2.0 ** -28 * r["floor"] + 2.0 ** -133
+    return out, delta + n * 2.0 ** -23 + 2.0 ** -20 + args + 2.0 ** -22 * r["lse"].abs()
+
+
+def attend(c, q, scale, out_type, window=0, codes=False):
+    """(out or None, lse, codes or None, their scales) of every token of c."""
+    heads, most_new = q.shape[1], max(c.new)
+    out = None if codes else torch.full(q.shape, 7.0, dtype=out_type, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    q8 = torch.zeros(q.shape[0], heads * c.d, dtype=E4M3, device="cuda") if codes else None
+    s8 = torch.zeros(q.shape[0], heads * c.d // 128, device="cuda") if codes else None
+    qm.qs_cache_attention(c.cache, c.seqs, q, scale, out, qm.alloc_cache_attention_workspace(heads, c.kv, c.d, most_new), max_new=most_new,
+                          window=window, lse=lse, codes=q8, codes_scale=s8)
+    return out, lse, q8, s8
+
+
+def check_rows(c, q, out_type=None, window=0, scale=None, codes=False):
+    out_type = F32 if codes else out_type or q.dtype
+    scale = 1.3 / math.sqrt(c.d) if scale is None else scale
+    out, lse, q8, s8 = attend(c, q, scale, out_type, window, codes)
+    r = rows64(c, q, scale, window)
+    tol, tol_lse = tolerances(c, r, out_type, codes or q.dtype is F32 or out_type is F32)
+    if codes:  # a code's rounding, or half of the smallest step
+        n = q.shape[0]
+        scales = s8.double().repeat_interleave(128, 1).view(q.shape)
+        out = q8.double().view(q.shape) * scales
+        tol = 1.07 * tol + 2.0 ** -4 * r["out"].abs() + 2.0 ** -10 * scales
+        assert n == out.shape[0]
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    worst = ((out.double() - r["out"]).abs() / tol).max().item()
+    assert worst <= 1.0, f"out: {worst:.3g} of the tolerance"
+    worst = ((lse.double() - r["lse"]).abs() / tol_lse).max().item()
+    assert worst <= 1.0, f"lse: {worst:.3g} of the tolerance"
+
+
+FORMS = [(BF16, BF16, False), (F32, F32, False), (BF16, F32, False), (F32, BF16, False), (BF16, BF16, True)]
+IDS = ["bf16", "f32", "bf16-f32", "f32-bf16", "codes"]
+
+
+def queries(c, heads, kind=BF16, seed=1):
+    return torch.randn(c.tokens, heads, c.d, generator=torch.Generator().manual_seed(seed)).to(kind).cuda()
+
+
+# ------------------------------------------------------------------ value scales
+
+@pytest.mark.parametrize("form", FORMS, ids=IDS)
+@pytest.mark.parametrize("group", [1, 4, 16])
+@pytest.mark.parametrize("new,window", [(1, 0), (4, 0), (4, 57), (1, 57), (4, 2)])
+@pytest.mark.parametrize("power", [-100, -60, -40, -16, 0, 60, 90, "any"])
+def test_value_scales_of_any_size(power, new, window, group, form):
+    """Positions that only some of an item's rows see count for the running maximum as the others do."""
+    q_type, out_type, codes = form
+    c = Paged([200, new, 60, 33], [new, new, new, max(new - 1, 1)], E4M3, kv=2, d=128, page=16)
+    if power == "any":
+        c.v_scale *= torch.exp2(torch.randint(-40, 40, c.v_scale.shape, generator=torch.Generator().manual_seed(5)).cuda().float())
+    else:
+        c.v_scale *= 2.0 ** power * 16.0
+        c.v_scale.clamp_(2.0 ** (power - 2), 2.0 ** (power + 2))  # (a NaN of a slot that nobody has stays)
+    check_rows(c, queries(c, 2 * group, q_type), out_type, window, codes=codes)
 
 
 # ------------------------------------------------------------------ offsets from device memory
