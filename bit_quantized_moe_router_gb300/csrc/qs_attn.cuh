@@ -58,6 +58,11 @@ namespace attn {
 
 constexpr float kSlack = 8.0f;    // a row's maximum may lag behind by this much (log2) before the sums are scaled
 constexpr float kLift = 7.0f;     // fp16 weights are 2^(score - maximum + kLift), at most 2^15: small ones keep 7 more bits
+// Over e4m3 the running maximum is of a score and the logarithm of the value's scale, kLeastScale at least (values that are all zero
+// have 2^-109).  A weight may so be 2^(kLift + kSlack - kLeastScale) = 2^111, and a row has 2^30 of them at most: their sum is held in
+// units of 2^kDown, below 2^127.  The other way a scale of 2^119, the largest that fp32 rows are written with, leaves a maximum's weight 2^-112,
+// in these units fp32's smallest normal number.
+constexpr float kLeastScale = -96.0f, kDown = 14.0f, kUnit = 0x1p-14f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kFan = 12;          // parts of an item that one CTA joins at a time
@@ -247,13 +252,17 @@ __device__ __forceinline__ Row row_of(const AttnArgs& p, const X& x, int row) {
     const int at = token_of(p, row);
     return {x.first_token + at, x.kv * p.group + row - at * p.group, row < x.rows};
 }
-__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
+// From a row's sum of weights, which is held in units of 2^kDown over e4m3.
+template <bool E4>
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + (log2f(l) + (E4 ? kDown : 0.0f))) * kLn2; }
+template <bool E4>
+__device__ __forceinline__ float inverse_of(float l) { return l == 0.0f ? 0.0f : (E4 ? kUnit : 1.0f) / l; }
 
 // Four columns of a row from col, of a warp that has 128 of it side by side: v is the sum of weighted values, l the sum of
 // weights, m the maximum that they are relative to.
-template <bool WIDE>
+template <bool E4, bool WIDE>
 __device__ __forceinline__ void finish(const AttnArgs& p, const Row& r, int col, float (&v)[4], float m, float l) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = inverse_of<E4>(l);
 #pragma unroll
     for (int q = 0; q < 4; q++) v[q] = l == 0.0f ? 0.0f : v[q] * inv;
     const int d = p.cache.head_dim;
@@ -271,7 +280,7 @@ __device__ __forceinline__ void finish(const AttnArgs& p, const Row& r, int col,
         if (WIDE && p.out.dtype == QS_F32) *reinterpret_cast<float4*>(to + 4 * col) = make_float4(v[0], v[1], v[2], v[3]);
         else *reinterpret_cast<uint2*>(to + 2 * col) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     }
-    if (p.lse && col == 0) p.lse[r.token * p.n_heads + r.head] = lse_of(m, l);
+    if (p.lse && col == 0) p.lse[r.token * p.n_heads + r.head] = lse_of<E4>(m, l);
 }
 
 // A warp's output, acc[j][nt][2 h + e]: of piece j the column col_of_value(j, h) from the warp's first, of rows nt * 8 + 2 t + e.
@@ -292,9 +301,9 @@ __device__ __forceinline__ void finish_rows(const AttnArgs& p, const X& x, int w
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-            const float l = sum[nt][e], by = l == 0.0f ? 0.0f : 1.0f / l;
+            const float l = sum[nt][e], by = inverse_of<P::E4>(l);
             const Row r = row_of(p, x, w0 + nt * 8 + 2 * t + e);
-            if (p.lse && g == 0 && col0 == 0 && r.real) p.lse[r.token * p.n_heads + r.head] = lse_of(top[nt][e], l);
+            if (p.lse && g == 0 && col0 == 0 && r.real) p.lse[r.token * p.n_heads + r.head] = lse_of<P::E4>(top[nt][e], l);
             float v[kJ][2];
 #pragma unroll
             for (int j = 0; j < kJ; j++)
@@ -826,10 +835,10 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     by_key[b][y] = 1.0f;
                     vs[b][y] = 1.0f;
                     lv[b][y] = 0.0f;
-                    if (E4) {  // the values' scales count for the maximum, 2^-100 at least: the weight's two factors stay in fp32's range
+                    if (E4) {  // the values' scales count for the maximum
                         by_key[b][y] = scales[16 * b + 8 * y + g];
                         vs[b][y] = scales[TP + 16 * b + 8 * y + g];
-                        lv[b][y] = fmaxf(lg2(vs[b][y]), -100.0f);
+                        lv[b][y] = fmaxf(lg2(vs[b][y]), kLeastScale);
                         // a position that some rows do not see counts for the maximum as any other, but it is left to its own sums
                         // below, with the scale as it is: here it has no weight, which may be beyond fp16 without its scale
                         if (mixed && (pos0 + 16 * b + 8 * y + g < all_lo || pos0 + 16 * b + 8 * y + g >= all_hi)) vs[b][y] = 0.0f;
@@ -900,7 +909,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                         for (int e = 0; e < 2; e++) {
                             const float z = sc[b][nt][2 * y + e], ref = top[nt][e] == -INFINITY ? 0.0f : top[nt][e];
                             two[e] = ex2(z - ref);
-                            sum[nt][e] += two[e];
+                            sum[nt][e] = E4 ? fmaf(two[e], kUnit, sum[nt][e]) : sum[nt][e] + two[e];
                             sc[b][nt][2 * y + e] = two[e];
                             if (E4) two[e] *= vs[b][y];
                         }
@@ -1131,7 +1140,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     const int x = x0 + k * size * 32, row = x / (DP / 4), col = x % (DP / 4) * 4;
                     if (x >= pieces_end) continue;
                     if (done) {
-                        finish<P::WIDE>(p, row_of(p, q, q.row0 + row), col, v[k], m[k], l[k]);
+                        finish<E4, P::WIDE>(p, row_of(p, q, q.row0 + row), col, v[k], m[k], l[k]);
                     } else {
                         __stcg(reinterpret_cast<float4*>(result + row * P::kRow + col), make_float4(v[k][0], v[k][1], v[k][2], v[k][3]));
                         if (col == 0) __stcg(reinterpret_cast<float2*>(result + RT * P::kRow) + row, make_float2(m[k], l[k]));

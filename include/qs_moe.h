@@ -613,7 +613,7 @@ typedef struct {
  * key-value head's cache is read once per 64 rows of n_heads / n_kv_heads * max_new.
  * Sums have a fixed order for given lengths (run-to-run identical); a row's bits
  * depend on the other sequences' lengths, by which the work is split.
- * Value scales below 2^-100 keep fewer bits.  |scale| <= 1e38.  QS_ERR_UNSUPPORTED where pages and slots, counted in the largest
+ * Value scales below 2^-100 or above 2^119 (past what qs_cache_write makes of fp32) keep fewer bits.  |scale| <= 1e38.  QS_ERR_UNSUPPORTED where pages and slots, counted in the largest
  * power of two of bytes that divides their strides, pass 2^31 (34 GB of keys at strides of odd multiples of 16 bytes), and
  * where the tables have room for more than 2e10 tiles of 16 positions by 8 rows: n_seqs * (n_seq_pages * page_size / 16 + 2)
  * * n_kv_heads * (n_heads / n_kv_heads * max_new / 8 + 1).

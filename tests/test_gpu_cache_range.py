@@ -125,6 +125,27 @@ def test_value_scales_of_any_size(power, new, window, group, form):
     check_rows(c, queries(c, 2 * group, q_type), out_type, window, codes=codes)
 
 
+@pytest.mark.parametrize("new", [1, 3])
+@pytest.mark.parametrize("value", [0.0, 2.0 ** -100])
+def test_log_sums_of_many_small_values(value, new):
+    """2^22 positions whose values are all zero, or as small as scales get: 64 of them, over and over."""
+    n, d, page = 1 << 22, 16, 64
+    k, v = torch.zeros(1, page, 1, d, device="cuda"), torch.full((1, page, 1, d), value, device="cuda")
+    k8, v8 = torch.zeros(1, page, 1, d, dtype=E4M3, device="cuda"), torch.zeros(1, page, 1, d, dtype=E4M3, device="cuda")
+    ks, vs = torch.zeros(1, page, 1, device="cuda"), torch.zeros(1, page, 1, device="cuda")
+    cache = qm.make_cache(k8, v8, ks, vs)
+    qm.qs_cache_write(cache, qm.make_seqs(torch.zeros(1, 1, dtype=torch.int32, device="cuda"), None, torch.tensor([0, page], dtype=torch.int32, device="cuda")), k[0], v[0])
+    seqs = qm.make_seqs(torch.zeros(1, n // page, dtype=torch.int32, device="cuda"), torch.tensor([n - new], dtype=torch.int32, device="cuda"),
+                        torch.tensor([0, new], dtype=torch.int32, device="cuda"))
+    q = torch.ones(new, 4, d, device="cuda").to(BF16)
+    out, lse = torch.full((new, 4, d), 7.0, dtype=BF16, device="cuda"), torch.empty(new, 4, device="cuda")
+    qm.qs_cache_attention(cache, seqs, q, 0.25, out, qm.alloc_cache_attention_workspace(4, 1, d, new), max_new=new, lse=lse)
+    # every weight is the same power of two, and sums of them have few bits: what is left is the logarithm's own
+    want = torch.log(torch.arange(n - new + 1, n + 1, dtype=torch.float64, device="cuda"))
+    assert ((lse.double() - want[:, None]).abs() <= 2.0 ** -16 * want[:, None]).all(), lse
+    assert ((out.double() - value).abs() <= 2.0 ** -4 * value).all()
+
+
 # ------------------------------------------------------------------ offsets from device memory
 
 @pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
