@@ -185,6 +185,24 @@ __device__ __forceinline__ uint32_t part(float& lo, float& hi) {
     return w;
 }
 
+// The same of queries, whose parts all meet the same keys.  A bf16 key may be infinite: its products with the parts have to agree, so the
+// parts are cut toward zero, of one sign, and what is left is never zero beside a query that is not: `crumb`, 2^-30 of the query (keys
+// are infinite for queries from 2^-96 on).  Three of eight bits hold 24.  Of an infinite query every part is infinite.
+template <bool E4>
+__device__ __forceinline__ uint32_t query_part(float& lo, float& hi, float2 crumb) {
+    if (E4) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        const float2 f = __half22float2(h);
+        if (!isinf(lo)) lo -= f.x;
+        if (!isinf(hi)) hi -= f.y;
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const uint32_t w = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+    if (!isinf(lo)) lo = (lo - bf16_lo(w)) + crumb.x;
+    if (!isinf(hi)) hi = (hi - bf16_hi(w)) + crumb.y;
+    return w;
+}
+
 // What a sequence has to do.  Positions are 32-bit numbers near enough to the table's (0 .. positions): a start far outside
 // it is brought so near that its tokens see the same.
 struct Seq {
@@ -582,10 +600,11 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     y.y *= factor;
                     z.x *= factor;
                     z.y *= factor;
+                    const float2 y_crumb = make_float2(y.x * 0x1p-30f, y.y * 0x1p-30f), z_crumb = make_float2(z.x * 0x1p-30f, z.y * 0x1p-30f);
 #pragma unroll
                     for (int pl = 0; pl < P::QP; pl++) {
-                        const uint32_t lo = part<E4>(y.x, y.y);
-                        store(step, pl, lo, part<E4>(z.x, z.y));
+                        const uint32_t lo = query_part<E4>(y.x, y.y, y_crumb);
+                        store(step, pl, lo, query_part<E4>(z.x, z.y, z_crumb));
                     }
                 }
             }

@@ -146,6 +146,61 @@ def test_log_sums_of_many_small_values(value, new):
     assert ((out.double() - value).abs() <= 2.0 ** -4 * value).all()
 
 
+# ------------------------------------------------------------------ infinities
+
+def special(c, i, p, name, value):
+    """Position p of sequence i gets this value in every head."""
+    getattr(c, name)[int(c.table[i, p // c.page]), p % c.page] = value
+
+
+@pytest.mark.parametrize("form", FORMS, ids=IDS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group,new", [(1, 1), (4, 1), (12, 1), (20, 1), (3, 4), (8, 8)])
+def test_scores_of_minus_infinity(group, new, d, form):
+    """Where every score is -infinity a row is zeros, and its log-sum -infinity; one such position among others counts nothing."""
+    q_type, out_type, codes = form
+    if codes and d < 128:
+        d = 128
+    c = Paged([30, 70, 25], [new, new, new], BF16, kv=2, d=d, page=16, garbage=False)
+    c.k[c.table[0].long()[c.table[0] >= 0]] = -INF
+    special(c, 1, 5, "k", -INF)
+    special(c, 2, 25 - new, "k", -INF)   # the first new token's own
+    q = (torch.rand(c.tokens, 2 * group, d, generator=torch.Generator().manual_seed(2)) + 0.5).to(q_type)
+    q[:, :, 1] = 1.0  # held by one part
+    q = q.cuda()
+    scale = 1.0 / d
+    out, lse, q8, s8 = attend(c, q, scale, out_type, codes=codes)
+    if codes:
+        out = q8.double().view(q.shape) * s8.double().repeat_interleave(128, 1).view(q.shape)
+    assert out[:new].double().count_nonzero() == 0 and (lse[:new] == -INF).all()
+    # the others' as if the position were not there: one key that no row sees a difference of
+    finite = Paged([30, 70, 25], [new, new, new], BF16, kv=2, d=d, page=16, garbage=False)
+    special(finite, 1, 5, "k", -1.0e30)
+    special(finite, 2, 25 - new, "k", -1.0e30)
+    want, want_lse, w8, t8 = attend(finite, q, scale, out_type, codes=codes)
+    if codes:
+        want = w8.double().view(q.shape) * t8.double().repeat_interleave(128, 1).view(q.shape)
+    assert torch.equal(out[new:], want[new:]) and torch.equal(lse[new:], want_lse[new:])
+    assert torch.isfinite(out[new:]).all() and torch.isfinite(lse[new:]).all()
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("form", FORMS[:4], ids=IDS[:4])
+def test_queries_of_minus_infinity(kind, form):
+    """Queries of -infinity over positive keys: every score is -infinity."""
+    c = Paged([30, 20], [1, 1], kind, kv=2, d=64, page=16, garbage=False)
+    c.k.copy_(c.k.float().abs().clamp_min(0.25).to(kind))
+    q = queries(c, 8, form[0])
+    q[0, 3] = -INF
+    q[0, 5, 7] = -INF
+    out, lse, _, _ = attend(c, q, 0.1, form[1])
+    want, want_lse, _, _ = attend(c, queries(c, 8, form[0]), 0.1, form[1])
+    quiet = torch.zeros(2, 8, dtype=torch.bool, device="cuda")
+    quiet[0, 3] = quiet[0, 5] = True
+    assert out[quiet].count_nonzero() == 0 and (lse[quiet] == -INF).all()
+    assert torch.equal(out[~quiet], want[~quiet]) and torch.equal(lse[~quiet], want_lse[~quiet])
+
+
 # ------------------------------------------------------------------ offsets from device memory
 
 @pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
