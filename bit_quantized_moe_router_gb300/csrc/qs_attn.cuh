@@ -169,25 +169,38 @@ __device__ __forceinline__ uint32_t widen(uint32_t two) {
     return r;
 }
 
-// Two values as their 16-bit roundings, and what these leave out.
-template <bool E4>
-__device__ __forceinline__ uint32_t part(float& lo, float& hi) {
-    if (E4) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        const float2 f = __half22float2(h);
-        lo -= f.x;
-        hi -= f.y;
-        return *reinterpret_cast<const uint32_t*>(&h);
+// The N 16-bit parts of two weights, each what the ones before leave out.  bf16: a value may be infinite, and its products with the
+// parts have to agree: all but the last are cut toward zero, and none is zero beside a weight that is not (from 2^-96 on).  For
+// two parts (16 bits) the first is taken from 1 + 2^-23 of the weight, for three (24 bits) 2^-30 of it is added to what is left.
+template <bool E4, int N>
+__device__ __forceinline__ void weight_parts(uint32_t (&parts)[N], float lo, float hi) {
+    const float lo_crumb = lo * 0x1p-30f, hi_crumb = hi * 0x1p-30f;
+#pragma unroll
+    for (int pl = 0; pl < N; pl++) {
+        if (E4) {
+            const __half2 h = __floats2half2_rn(lo, hi);
+            const float2 f = __half22float2(h);
+            lo -= f.x;
+            hi -= f.y;
+            parts[pl] = *reinterpret_cast<const uint32_t*>(&h);
+        } else if (pl == N - 1) {
+            parts[pl] = pack_bf16(lo, hi);
+        } else {
+            const uint32_t w = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+            if (N == 2) {
+                lo = fmaf(lo, 1.0f + 0x1p-23f, -bf16_lo(w));
+                hi = fmaf(hi, 1.0f + 0x1p-23f, -bf16_hi(w));
+            } else {
+                lo = (lo - bf16_lo(w)) + lo_crumb;
+                hi = (hi - bf16_hi(w)) + hi_crumb;
+            }
+            parts[pl] = w;
+        }
     }
-    const uint32_t w = pack_bf16(lo, hi);
-    lo -= bf16_lo(w);
-    hi -= bf16_hi(w);
-    return w;
 }
 
-// The same of queries, whose parts all meet the same keys.  A bf16 key may be infinite: its products with the parts have to agree, so the
-// parts are cut toward zero, of one sign, and what is left is never zero beside a query that is not: `crumb`, 2^-30 of the query (keys
-// are infinite for queries from 2^-96 on).  Three of eight bits hold 24.  Of an infinite query every part is infinite.
+// The next part of two queries, and what it leaves out.  Keys may be infinite as values may: of bf16 the parts are cut toward zero and what is
+// left has `crumb`, 2^-30 of the query, added to it.  Of an infinite query every part is infinite.
 template <bool E4>
 __device__ __forceinline__ uint32_t query_part(float& lo, float& hi, float2 crumb) {
     if (E4) {
@@ -932,8 +945,10 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                             sc[b][nt][2 * y + e] = two[e];
                             if (E4) two[e] *= vs[b][y];
                         }
+                        uint32_t parts[P::PP];
+                        weight_parts<E4>(parts, two[0], two[1]);
 #pragma unroll
-                        for (int pl = 0; pl < P::PP; pl++) pb[b][nt][pl][y] = transposed(part<E4>(two[0], two[1]));
+                        for (int pl = 0; pl < P::PP; pl++) pb[b][nt][pl][y] = transposed(parts[pl]);
                     }
             if (mixed) {
                 // positions that some of the rows see: one at a time, for those rows alone

@@ -201,6 +201,27 @@ def test_queries_of_minus_infinity(kind, form):
     assert torch.equal(out[~quiet], want[~quiet]) and torch.equal(lse[~quiet], want_lse[~quiet])
 
 
+@pytest.mark.parametrize("form", FORMS[:4], ids=IDS[:4])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group,new", [(1, 1), (4, 1), (12, 1), (20, 1), (3, 4), (8, 8)])
+def test_values_that_are_infinite(group, new, d, form):
+    """An infinite value makes its column infinite for the rows that see it (a NaN where both signs are seen), and no other column."""
+    c = Paged([30, 70, 5000], [new, new, new], BF16, kv=2, d=d, page=16, garbage=False)
+    places = [(1, 5, 3, INF), (1, 69, 4, -INF), (1, 20, 8, INF), (1, 40, 8, -INF), (2, 1, d - 1, -INF), (2, 4999, 0, INF), (2, 2500, 1, INF)]
+    q = queries(c, 2 * group, form[0])
+    clean, clean_lse, _, _ = attend(c, q, 1.0 / math.sqrt(d), form[1])
+    expect = clean.double().clone()
+    for i, p, col, value in places:
+        c.v[int(c.table[i, p // 16]), p % 16, :, col] = value
+        first = max(0, p - (c.lens[i] - new))   # the first of the sequence's tokens that sees it
+        t0, t1 = int(c.offsets[i]) + first, int(c.offsets[i + 1])
+        expect[t0:t1, :, col] = torch.where(torch.isinf(expect[t0:t1, :, col]), NAN, value)
+    out, lse, _, _ = attend(c, q, 1.0 / math.sqrt(d), form[1])
+    assert torch.equal(lse, clean_lse)
+    assert torch.equal(torch.isnan(out), torch.isnan(expect))
+    assert torch.equal(out.double().nan_to_num(0.0), expect.nan_to_num(0.0))
+
+
 # ------------------------------------------------------------------ offsets from device memory
 
 @pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
