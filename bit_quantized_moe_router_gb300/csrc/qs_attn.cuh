@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                             v[step][half] = make_float2(bf16_lo(w), bf16_hi(w));
                         }
                     }
-                if (E4) {  // a power of two that brings the row's largest into fp16's upper range
+                if (E4) {  // a power of two that brings the row's largest into fp16's upper range (down from any that fp32 has)
                     float a = 0.0f;
 #pragma unroll
                     for (int step = 0; step < P::kSteps; step++)
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                         for (int half = 0; half < 2; half++) a = fmaxf(a, fmaxf(fabsf(v[step][half].x), fabsf(v[step][half].y)));
                     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
                     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-                    const int e = min(max(14 - ((int)(__float_as_uint(a) >> 23) - 127), -100), 100);
+                    const int e = min(max(14 - ((int)(__float_as_uint(a) >> 23) - 127), -113), 100);
                     factor = __uint_as_float((uint32_t)(127 + e) << 23);
                 }
 #pragma unroll

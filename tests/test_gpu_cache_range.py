@@ -222,6 +222,17 @@ def test_values_that_are_infinite(group, new, d, form):
     assert torch.equal(out.double().nan_to_num(0.0), expect.nan_to_num(0.0))
 
 
+@pytest.mark.parametrize("power", [100, 113, 116, 120, 124])
+@pytest.mark.parametrize("form", FORMS, ids=IDS)
+def test_large_queries_over_small_keys(power, form):
+    """Queries next to fp32's end over e4m3 keys next to its beginning: scores as anywhere."""
+    q_type, out_type, codes = form
+    c = Paged([60, 33], [1, 1], E4M3, kv=2, d=128, page=16)
+    c.k_scale.copy_(torch.where(torch.isnan(c.k_scale), NAN, 2.0 ** -(power - 1)))
+    q = queries(c, 8, F32)
+    check_rows(c, (q / q.abs().max() * 2.0 ** power * 7.9).to(q_type), out_type, codes=codes, scale=0.02)
+
+
 # ------------------------------------------------------------------ offsets from device memory
 
 @pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
