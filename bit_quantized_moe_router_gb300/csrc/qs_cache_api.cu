@@ -14,7 +14,7 @@ int done(cudaError_t e) { return e == cudaSuccess ? QS_OK : cuda_fail(e); }
 
 bool head_dim_ok(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
 
-// Dimensions of these strides and sizes under a contiguous inner one: whether no two places are the same.
+// Dimensions of these strides and sizes under a contiguous inner one (of one element or more): whether no two places are the same.
 struct Dim {
     int64_t stride, size;
 };
@@ -24,7 +24,7 @@ bool distinct(Dim a, Dim b, Dim c, int64_t inner) {
     for (const Dim& x : d) {
         if (x.size <= 1) continue;
         if (x.stride < inner) return false;
-        if (x.stride > (int64_t)1 << 45 || x.size > (int64_t)1 << 31 || x.stride * (x.size - 1) / 2 > (int64_t)1 << 60) return false;
+        if (x.size - 1 > ((int64_t)1 << 60) / x.stride) return false;  // (three such extents are within 64 bits; their product may not be)
         inner += x.stride * (x.size - 1);
     }
     return true;

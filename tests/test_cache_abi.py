@@ -51,6 +51,18 @@ def test_write_refuses_places_that_coincide(over):
     assert call("qs_cache_write", ROWS, over) == INV
 
 
+# extents past 2^60 elements, whose product of stride and size passes 64 bits (2^64 exactly, and beside it)
+@pytest.mark.parametrize("over", [dict(page=1 << 40, n_pages=(1 << 24) + 1), dict(page=1 << 40, n_pages=1 << 24), dict(page=1 << 40, n_pages=(1 << 31) - 1),
+                                  dict(page=3 << 38, n_pages=(1 << 24) + 1), dict(spage=1 << 40, n_pages=(1 << 24) + 1)], ids=str)
+def test_write_refuses_extents_past_64_bits(over):
+    assert call("qs_cache_write", ROWS, {**over, "n": 0}) == INV
+    assert call("qs_cache_write", ROWS, {**over, "n_pages": 1 << 20, "n": 0}) == qm.QS_OK  # 2^60
+
+
+def test_read_refuses_rows_whose_extents_pass_64_bits():
+    assert call("qs_cache_read", ROWS, dict(k_token=1 << 40, n=1 << 24)) == INV
+
+
 # rows that coincide: fine to write from, not to read into
 @pytest.mark.parametrize("over", [dict(k_head=0), dict(v_token=0), dict(v_head=64), dict(k_token=500)], ids=str)
 def test_read_refuses_rows_that_coincide(over):
