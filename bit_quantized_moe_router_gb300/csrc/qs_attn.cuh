@@ -86,7 +86,8 @@ struct Plan {
     static constexpr int kSteps = DP / 16;            // of the first product
     // The queries' fragments: in registers where they fit beside the sums and about 80 others, else in shared memory.
     static constexpr int kQEach = 2 * NT * QP;         // registers of a step
-    static constexpr bool kQInRegs = kQEach * kSteps <= 65536 / (32 * kWarps) - 80 - kCols * NT / 4;
+    static constexpr int kRegs = 65536 / (32 * kWarps) < 255 ? 65536 / (32 * kWarps) : 255;  // of a thread
+    static constexpr bool kQInRegs = kQEach * kSteps <= kRegs - 80 - kCols * NT / 4;
     static constexpr int kQBytes = kQInRegs ? 0 : kWarps * QP * NT * kSteps * 32 * 8;
     static constexpr int kPieces = kCols / 16;         // of the output: 16 columns of a warp's rows
     static constexpr int kRow = DP + 4, kPart = RT * (kRow + 2);  // floats of an item's part: rows of sums, maxima and sums of weights
