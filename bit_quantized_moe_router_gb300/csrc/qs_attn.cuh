@@ -170,12 +170,15 @@ __device__ __forceinline__ uint32_t widen(uint32_t two) {
     return r;
 }
 
-// The N 16-bit parts of two weights, each what the ones before leave out.  bf16: a value may be infinite, and its products with the
-// parts have to agree: all but the last are cut toward zero, and none is zero beside a weight that is not (from 2^-96 on).  For
-// two parts (16 bits) the first is taken from 1 + 2^-23 of the weight, for three (24 bits) 2^-30 of it is added to what is left.
+// Of bf16 keys and values one may be infinite, and its products with the parts of a query or a weight have to agree.  So all parts but the
+// last are cut toward zero, and what they leave is taken from kOver of the value: of one sign, and never zero beside a value that is
+// not (queries from 2^-80 on, weights from 2^-80 of the largest).  Two parts hold 16 bits, three 24.  kBack takes kOver back out where
+// there are three, from the scores' factor and from the rows': with two it is far below what they leave out.
+constexpr float kOver = 1.0f + 0x1p-23f, kBack = 1.0f - 0x1p-23f;
+
+// The N 16-bit parts of two weights, each what the ones before leave out.
 template <bool E4, int N>
 __device__ __forceinline__ void weight_parts(uint32_t (&parts)[N], float lo, float hi) {
-    const float lo_crumb = lo * 0x1p-30f, hi_crumb = hi * 0x1p-30f;
 #pragma unroll
     for (int pl = 0; pl < N; pl++) {
         if (E4) {
@@ -187,33 +190,27 @@ __device__ __forceinline__ void weight_parts(uint32_t (&parts)[N], float lo, flo
         } else if (pl == N - 1) {
             parts[pl] = pack_bf16(lo, hi);
         } else {
-            const uint32_t w = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
-            if (N == 2) {
-                lo = fmaf(lo, 1.0f + 0x1p-23f, -bf16_lo(w));
-                hi = fmaf(hi, 1.0f + 0x1p-23f, -bf16_hi(w));
-            } else {
-                lo = (lo - bf16_lo(w)) + lo_crumb;
-                hi = (hi - bf16_hi(w)) + hi_crumb;
-            }
-            parts[pl] = w;
+            parts[pl] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+            lo = fmaf(lo, kOver, -bf16_lo(parts[pl]));
+            hi = fmaf(hi, kOver, -bf16_hi(parts[pl]));
         }
     }
 }
 
-// The next part of two queries, and what it leaves out.  Keys may be infinite as values may: of bf16 the parts are cut toward zero and what is
-// left has `crumb`, 2^-30 of the query, added to it.  Of an infinite query every part is infinite.
+// The next part of two queries, and what it leaves out.  Of an infinite query every part is infinite: where a row has one (`finite` is false)
+// parts are not taken from one another, and what its other columns come to then does not count.
 template <bool E4>
-__device__ __forceinline__ uint32_t query_part(float& lo, float& hi, float2 crumb) {
+__device__ __forceinline__ uint32_t query_part(float& lo, float& hi, bool finite) {
     if (E4) {
         const __half2 h = __floats2half2_rn(lo, hi);
         const float2 f = __half22float2(h);
-        if (!isinf(lo)) lo -= f.x;
-        if (!isinf(hi)) hi -= f.y;
+        if (finite) lo -= f.x;
+        if (finite) hi -= f.y;
         return *reinterpret_cast<const uint32_t*>(&h);
     }
     const uint32_t w = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
-    if (!isinf(lo)) lo = (lo - bf16_lo(w)) + crumb.x;
-    if (!isinf(hi)) hi = (hi - bf16_hi(w)) + crumb.y;
+    if (finite) lo = fmaf(lo, kOver, -bf16_lo(w));
+    if (finite) hi = fmaf(hi, kOver, -bf16_hi(w));
     return w;
 }
 
@@ -287,14 +284,14 @@ __device__ __forceinline__ Row row_of(const AttnArgs& p, const X& x, int row) {
 // From a row's sum of weights, which is held in units of 2^kDown over e4m3.
 template <bool E4>
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + (log2f(l) + (E4 ? kDown : 0.0f))) * kLn2; }
-template <bool E4>
-__device__ __forceinline__ float inverse_of(float l) { return l == 0.0f ? 0.0f : (E4 ? kUnit : 1.0f) / l; }
+template <bool E4, bool WIDE>
+__device__ __forceinline__ float inverse_of(float l) { return l == 0.0f ? 0.0f : (E4 ? kUnit : WIDE ? kBack : 1.0f) / l; }
 
 // Four columns of a row from col, of a warp that has 128 of it side by side: v is the sum of weighted values, l the sum of
 // weights, m the maximum that they are relative to.
 template <bool E4, bool WIDE>
 __device__ __forceinline__ void finish(const AttnArgs& p, const Row& r, int col, float (&v)[4], float m, float l) {
-    const float inv = inverse_of<E4>(l);
+    const float inv = inverse_of<E4, WIDE>(l);
 #pragma unroll
     for (int q = 0; q < 4; q++) v[q] = l == 0.0f ? 0.0f : v[q] * inv;
     const int d = p.cache.head_dim;
@@ -333,7 +330,7 @@ __device__ __forceinline__ void finish_rows(const AttnArgs& p, const X& x, int w
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-            const float l = sum[nt][e], by = inverse_of<P::E4>(l);
+            const float l = sum[nt][e], by = inverse_of<P::E4, P::WIDE>(l);
             const Row r = row_of(p, x, w0 + nt * 8 + 2 * t + e);
             if (p.lse && g == 0 && col0 == 0 && r.real) p.lse[r.token * p.n_heads + r.head] = lse_of<P::E4>(top[nt][e], l);
             float v[kJ][2];
@@ -596,12 +593,13 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                             v[step][half] = make_float2(bf16_lo(w), bf16_hi(w));
                         }
                     }
+                float a = 0.0f;
+#pragma unroll
+                for (int step = 0; step < P::kSteps; step++)
+#pragma unroll
+                    for (int half = 0; half < 2; half++) a = fmaxf(a, fmaxf(fabsf(v[step][half].x), fabsf(v[step][half].y)));
+                const bool finite = a < INFINITY;  // of this lane's columns
                 if (E4) {  // a power of two that brings the row's largest into fp16's upper range (down from any that fp32 has)
-                    float a = 0.0f;
-#pragma unroll
-                    for (int step = 0; step < P::kSteps; step++)
-#pragma unroll
-                        for (int half = 0; half < 2; half++) a = fmaxf(a, fmaxf(fabsf(v[step][half].x), fabsf(v[step][half].y)));
                     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
                     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
                     const int e = min(max(14 - ((int)(__float_as_uint(a) >> 23) - 127), -113), 100);
@@ -614,11 +612,10 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     y.y *= factor;
                     z.x *= factor;
                     z.y *= factor;
-                    const float2 y_crumb = make_float2(y.x * 0x1p-30f, y.y * 0x1p-30f), z_crumb = make_float2(z.x * 0x1p-30f, z.y * 0x1p-30f);
 #pragma unroll
                     for (int pl = 0; pl < P::QP; pl++) {
-                        const uint32_t lo = query_part<E4>(y.x, y.y, y_crumb);
-                        store(step, pl, lo, query_part<E4>(z.x, z.y, z_crumb));
+                        const uint32_t lo = query_part<E4>(y.x, y.y, finite);
+                        store(step, pl, lo, query_part<E4>(z.x, z.y, finite));
                     }
                 }
             }
@@ -626,7 +623,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
             for (int e = 0; e < 2; e++) {
                 top[nt][e] = -INFINITY;
                 sum[nt][e] = 0.0f;
-                row_scale[nt][e] = E4 ? p.scale * (1.0f / __shfl_sync(0xffffffffu, factor, 8 * t + 4 * e)) : p.scale;
+                row_scale[nt][e] = E4 ? p.scale * (1.0f / __shfl_sync(0xffffffffu, factor, 8 * t + 4 * e)) : P::WIDE ? p.scale * kBack : p.scale;
             }
         }
 #pragma unroll
