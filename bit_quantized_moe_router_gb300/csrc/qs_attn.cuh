@@ -1197,7 +1197,7 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
     }
 }
 
-// CTAs that fit the current device, looked up once a kernel and device.
+// One CTA an SM of the current device, looked up once a kernel and device.
 template <class P>
 cudaError_t launch(AttnArgs p, cudaStream_t st) {
     static int ctas_of[64];  // 0: not known yet; written with the same value by whoever finds it
@@ -1211,7 +1211,7 @@ cudaError_t launch(AttnArgs p, cudaStream_t st) {
         if ((e = cudaFuncSetAttribute(attn_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem)) != cudaSuccess) return e;
         if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, attn_kernel<P>, 32 * P::kWarps, P::kSmem)) != cudaSuccess) return e;
         if (each < 1) return cudaErrorLaunchOutOfResources;
-        ctas = std::min(kAttnMaxCtas, sms * each);
+        ctas = std::min(kAttnMaxCtas, sms);  // equal runs: a second CTA on some SMs alone would end late
         if (dev < 64) ctas_of[dev] = ctas;
     }
     return launch_pdl(attn_kernel<P>, dim3((unsigned)ctas), 32 * P::kWarps, P::kSmem, st, p);
