@@ -630,10 +630,15 @@ class Seqs:
     __slots__ = ("tensors", "packed", "device", "n_seqs", "has_offsets")
 
 
+def _one_layout(a, b):
+    """Whether tensors of one shape lie alike: a dimension of one is never stepped over."""
+    return not a.numel() or all(n == 1 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride()))
+
+
 def make_cache(k, v, k_scale=None, v_scale=None):
     """A paged cache of k and v [pages, page size, key-value heads, head size], bf16, or e4m3 with fp32 scales
     [pages, page size, key-value heads].  Any strides (a view of another order of dimensions, or one half of a tensor that
-    holds both), the same for k and v."""
+    holds both), the same for k and v where a dimension has more than one."""
     if k.dim() != 4:
         raise ValueError(f"k: expected [pages, page size, heads, head size], got {k.dim()} dimensions")
     dev = k.get_device()
@@ -649,7 +654,7 @@ def make_cache(k, v, k_scale=None, v_scale=None):
     for t, what in ((k, "k"), (v, "v")):
         if t.stride(3) != 1 and d > 1 and t.numel():
             _refuse(t, what, t.shape, kinds, dev)
-    if k.stride() != v.stride() and k.numel():
+    if k.stride() != v.stride() and not _one_layout(k, v):
         raise ValueError(f"v: strides {v.stride()}, k has {k.stride()}")
     if k.dtype is torch.float8_e4m3fn:
         if k_scale is None or v_scale is None:
@@ -657,7 +662,7 @@ def make_cache(k, v, k_scale=None, v_scale=None):
         for t, what in ((k_scale, "k scale"), (v_scale, "v scale")):
             if t.dtype != torch.float32 or t.shape != k.shape[:3] or t.get_device() != dev:
                 _refuse(t, what, k.shape[:3], _F32, dev)
-        if k_scale.stride() != v_scale.stride() and k.numel():
+        if k_scale.stride() != v_scale.stride() and not _one_layout(k_scale, v_scale):
             raise ValueError(f"v scale: strides {v_scale.stride()}, k scale has {k_scale.stride()}")
         scales, scale_strides = (k_scale.data_ptr(), v_scale.data_ptr()), k_scale.stride()
     elif k_scale is not None or v_scale is not None:

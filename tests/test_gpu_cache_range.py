@@ -265,3 +265,36 @@ def test_offsets_that_are_no_offsets(offsets, kind):
     qm.qs_cache_write(c.cache, c.seqs, new[inside], new[inside])
     changed = (before != c.k.view(torch.uint8)).flatten(2).any(2)
     assert changed.sum() <= n and torch.isfinite(c.k.float()[changed]).all()
+
+
+# ------------------------------------------------------------------ layouts
+
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("one", [0, 1, 2])
+def test_strides_of_dimensions_of_one_do_not_count(one, kind):
+    """Keys and values, and their scales, that differ in such a stride alone are one layout: what is written comes back."""
+    shape = [3, 16, 2, 64]
+    shape[one] = 1
+
+    def odd(t):  # the same elements, with another stride where the size is one
+        strides = list(t.stride())
+        strides[one] = 7 * strides[one] + 5
+        return t.as_strided(t.shape, strides)
+
+    k, v = torch.zeros(shape, device="cuda").to(kind), odd(torch.zeros(shape, device="cuda").to(kind))
+    scales = (torch.zeros(shape[:3], device="cuda"), odd(torch.zeros(shape[:3], device="cuda"))) if kind is E4M3 else ()
+    assert k.stride() != v.stride()
+    n = shape[0] * shape[1]
+    seqs = qm.make_seqs(torch.arange(shape[0], dtype=torch.int32, device="cuda")[None], None, torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    rows = [torch.randint(-8, 9, (n, shape[2], 64), device="cuda").float() for _ in range(2)]
+    for x in rows:
+        x[:, :, 0] = 448.0 if kind is E4M3 else 1.0  # a scale of one
+    for pair in ((k, v, *scales), (v, k, *scales[::-1])):
+        cache = qm.make_cache(*pair)
+        back = [torch.empty_like(x) for x in rows]
+        qm.qs_cache_write(cache, seqs, *rows)
+        qm.qs_cache_read(cache, seqs, *back)
+        for x, y in zip(rows, back):
+            assert ((x - y).abs() <= 2.0 ** -20 * x.abs()).all()
+    with pytest.raises(ValueError, match="strides"):  # strides that count
+        qm.make_cache(k, torch.zeros([2 * x for x in shape], device="cuda").to(kind)[:shape[0], :shape[1], :shape[2], :64], *scales)
