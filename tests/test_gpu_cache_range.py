@@ -125,6 +125,20 @@ def test_value_scales_of_any_size(power, new, window, group, form):
     check_rows(c, queries(c, 2 * group, q_type), out_type, window, codes=codes)
 
 
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("form", FORMS[:4], ids=IDS[:4])
+def test_quiet_rows_beside_loud_ones(kind, form):
+    """A row of zeros and rows next to them have their own tolerance, whatever the others' scores are."""
+    c = Paged([200, 100], [1, 1], kind, kv=2, d=64, page=16)
+    q = 50.0 * torch.randn(2, 8, 64, generator=torch.Generator().manual_seed(3))
+    q[0, 0] = 0.0
+    q[0, 1] *= 2.0 ** -60
+    q[1, 1] *= 2.0 ** -120
+    q[1, 2] *= 0.01
+    check_rows(c, q.to(form[0]).cuda(), form[1])
+    check_rows(c, q.to(form[0]).cuda(), form[1], scale=-0.2)
+
+
 @pytest.mark.parametrize("new", [1, 3])
 @pytest.mark.parametrize("value", [0.0, 2.0 ** -100])
 def test_log_sums_of_many_small_values(value, new):
