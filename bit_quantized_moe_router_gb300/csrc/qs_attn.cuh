@@ -31,9 +31,10 @@
 //
 // Roundings.  Scores, maxima, sums and O are fp32.  e4m3 scales stay out of the 16-bit operands: the key's multiplies
 // the score, the value's the weight, and the running maximum is of s' + log2(value scale), so that fp16 weights stay below
-// 2^(kLift + kSlack) whatever the scales are.  A weight goes into the product as PP 16-bit parts, each the rounding of what the
-// ones before leave out: two of bf16 or one of fp16 for bf16 output (off by 2^-16, 2^-11 of the weight), three or two with fp32
-// rows or codes (2^-24, 2^-22).  fp32 queries are QP such parts; for an fp16 product a row is scaled by a power of two.
+// 2^(kLift + kSlack) whatever the scales are.  A weight goes into the product as PP 16-bit parts, each of what the ones before
+// leave out: two of bf16 or one of fp16 for bf16 output (off by 2^-16, 2^-11 of the weight), three or two with fp32
+// rows or codes (2^-24, 2^-22).  fp32 queries are QP such parts; for an fp16 product a row is scaled by a power of two.  Keys and
+// values of bf16 may be infinite, so that its parts have one sign and none is zero alone (kOver).
 //
 // A position that a row does not see never touches it, NaN and infinity included: scores are replaced, and positions that
 // some of an item's rows see and others do not (the drafted tokens' own, the first ones of a window) are added for those rows
@@ -42,10 +43,10 @@
 // Code that runs once an SM and call costs 3 to 6 cycles an instruction beyond 32 KB, so there is one copy of each part.
 //
 // Measured on one GB300, in a replayed graph, cold (HBM): 64 sequences of up to 8192 positions, 32 heads on 8 of 128
-// columns, bf16 169 to 183 us (by the lengths drawn, 1.0 to 1.2 GB: 6.2 to 6.7 TB/s), e4m3 to codes 110 to 123 us (5.0
-// TB/s; 4-byte scales of one head are 32-byte sectors); one token over 131072 positions of 2 e4m3 heads of 256 39 us (3.4 TB/s:
+// columns, bf16 169 to 183 us (by the lengths drawn, 1.0 to 1.2 GB: 6.2 to 6.7 TB/s; fp32 rows 174, to codes 181), e4m3 to codes 111
+// to 123 us (5.0 TB/s; 4-byte scales of one head are 32-byte sectors); one token over 131072 positions of 2 e4m3 heads of 256 39 us (3.4 TB/s:
 // 20 us of it enter, add up and join); 1000 positions of 2 bf16 heads of 256 15 us; 16 sequences of up to eight drafted tokens
-// over 16384 positions 101 us; 200 windows of 301 positions 47 us.
+// over 16384 positions 101 us (e4m3 107; heads of 256 195, fp32 rows 313); 200 windows of 301 positions 47 us.
 #pragma once
 
 #include <algorithm>

@@ -529,7 +529,7 @@ int qs_combine_tokens_backward(const qs_combine_backward_args *args, void *strea
  *    order and padding; k, v at 16-byte boundaries and the strides multiples of
  *    16 bytes.  QS_BF16, or QS_E4M3 with one fp32 scale per page, slot and head
  *    (k_scale, v_scale with strides of their own in floats): the value is code *
- *    scale.  Scales are >= 0.  head_dim a multiple of 16 up to 256, n_kv_heads <= 256, any page size
+ *    scale.  Scales are >= 0 and finite.  head_dim a multiple of 16 up to 256, n_kv_heads <= 256, any page size
  *    up to 2^30.
  *  - Sequence i's page of positions j * page_size .. is table[i * table_stride +
  *    j], j < n_seq_pages (n_seq_pages * page_size <= 2^30).  An id outside 0 ..
@@ -540,8 +540,9 @@ int qs_combine_tokens_backward(const qs_combine_backward_args *args, void *strea
  *    int32 [n_seqs]; NULL: 0).  n_seqs <= 2^16, n_tokens <= 2^24.  Rows of no sequence, those
  *    behind the last one among them, are left alone.  Lengths are read on the
  *    device: a captured graph follows them.
- *  - Sequences may share pages, but not one that a call writes to: two tokens
- *    of a call at the same place leave either's values there.
+ *  - Sequences may share pages, but not one that a call writes to: what two tokens
+ *    of a call leave at the same place is not defined (some columns of either, one's
+ *    codes with the other's scale).  k and v are two buffers where they are written.
  */
 typedef struct {
     void *k, *v;
@@ -602,9 +603,15 @@ typedef struct {
  * the last `window`.  Per token and head h, with key-value head h / (n_heads / n_kv_heads):
  *   s_i = scale * (q . k_i),  out = sum_i exp(s_i) v_i / sum_i exp(s_i),
  *   lse = log(sum_i exp(s_i))
- * in fp32; out rounded to its type; a token that sees no position (or whose every
+ * with scores, maxima and sums in fp32; out rounded to its type; a token that sees no position (or whose every
  * score is -infinity) has zeros, and an lse of -infinity.  Positions that a token
- * does not see do not touch it, whatever they hold.  codes (if there): the same
+ * does not see do not touch it, whatever they hold.  A score of +infinity or a NaN makes
+ * the row and its lse NaNs; an infinite value makes its column infinite for the rows that
+ * see it (a NaN where both signs are seen, or where its weight is below 2^-80 of the row's largest).
+ * What goes into products of 16-bit values: keys and values as they are stored; each weight exp(s_i) to 2^-16 of
+ * itself (QS_BF16 cache) or 2^-11 (QS_E4M3), to 2^-22 where q or out is fp32 or codes are asked for; fp32 queries to 2^-24
+ * of each (QS_BF16) or 2^-22 (QS_E4M3).  A weight over QS_E4M3 is off by another 2^-24 (|log2 of its value's scale| + 16), the
+ * rounding of its exponent.  codes (if there): the same
  * rows of n_heads * head_dim columns as e4m3 codes with a scale per 128, as
  * qs_fp8_matmul takes them; head_dim must be a multiple of 128, codes and their
  * stride at 16 bytes.  lse may be NULL, out may be left out where codes are there.
@@ -613,7 +620,8 @@ typedef struct {
  * key-value head's cache is read once per 64 rows of n_heads / n_kv_heads * max_new.
  * Sums have a fixed order for given lengths (run-to-run identical); a row's bits
  * depend on the other sequences' lengths, by which the work is split.
- * Value scales below 2^-100 or above 2^119 (past what qs_cache_write makes of fp32) keep fewer bits.  |scale| <= 1e38.  QS_ERR_UNSUPPORTED where pages and slots, counted in the largest
+ * Value scales below 2^-100 or above 2^119 (past what qs_cache_write makes of fp32) keep fewer bits, and over QS_E4M3
+ * rows of queries whose largest is below 2^-86.  |scale| <= 1e38, and over QS_E4M3 |scale| times a row's largest |q| <= 2^140.  QS_ERR_UNSUPPORTED where pages and slots, counted in the largest
  * power of two of bytes that divides their strides, pass 2^31 (34 GB of keys at strides of odd multiples of 16 bytes), and
  * where the tables have room for more than 2e10 tiles of 16 positions by 8 rows: n_seqs * (n_seq_pages * page_size / 16 + 2)
  * * n_kv_heads * (n_heads / n_kv_heads * max_new / 8 + 1).
