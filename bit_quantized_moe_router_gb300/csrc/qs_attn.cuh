@@ -199,9 +199,9 @@ __device__ __forceinline__ void weight_parts(uint32_t (&parts)[N], float lo, flo
 }
 
 // The next part of two queries, and what it leaves out.  Of an infinite query every part is infinite: where a row has one (`finite` is false)
-// parts are not taken from one another, and what its other columns come to then does not count.
+// parts are not taken from one another, and what its other columns come to then does not count.  The last is rounded.
 template <bool E4>
-__device__ __forceinline__ uint32_t query_part(float& lo, float& hi, bool finite) {
+__device__ __forceinline__ uint32_t query_part(float& lo, float& hi, bool finite, bool last) {
     if (E4) {
         const __half2 h = __floats2half2_rn(lo, hi);
         const float2 f = __half22float2(h);
@@ -209,6 +209,7 @@ __device__ __forceinline__ uint32_t query_part(float& lo, float& hi, bool finite
         if (finite) hi -= f.y;
         return *reinterpret_cast<const uint32_t*>(&h);
     }
+    if (last) return pack_bf16(lo, hi);
     const uint32_t w = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
     if (finite) lo = fmaf(lo, kOver, -bf16_lo(w));
     if (finite) hi = fmaf(hi, kOver, -bf16_hi(w));
@@ -615,8 +616,8 @@ __global__ void __launch_bounds__(32 * P::kWarps, 1) attn_kernel(const AttnArgs 
                     z.y *= factor;
 #pragma unroll
                     for (int pl = 0; pl < P::QP; pl++) {
-                        const uint32_t lo = query_part<E4>(y.x, y.y, finite);
-                        store(step, pl, lo, query_part<E4>(z.x, z.y, finite));
+                        const uint32_t lo = query_part<E4>(y.x, y.y, finite, pl == P::QP - 1);
+                        store(step, pl, lo, query_part<E4>(z.x, z.y, finite, pl == P::QP - 1));
                     }
                 }
             }
